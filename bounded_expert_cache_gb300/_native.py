@@ -1,4 +1,4 @@
-"""ctypes declarations of the libmoecache C ABI (include/moecache.h).
+"""ctypes declarations of the libmoecache C ABI (include/moecache.h, include/moekv.h).
 
 Argument marshalling only. Importing this module loads the in-tree
 ``libmoecache.so`` and raises ImportError if it is missing: there is no
@@ -61,6 +61,13 @@ class Budget(C.Structure):
                 ("slots_per_layer", C.c_int32), ("accepted", C.c_int32)]
 
 
+class KvT(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("table", C.c_void_p), ("lens", C.c_void_p),
+                ("ref", C.c_void_p), ("work", C.c_void_p), ("work_bytes", C.c_int64), ("n_layers", C.c_int32),
+                ("n_pages", C.c_int32), ("n_kv_heads", C.c_int32), ("page_tokens", C.c_int32),
+                ("head_dim", C.c_int32), ("dtype", C.c_int32), ("max_seqs", C.c_int32), ("max_pages", C.c_int32)]
+
+
 def _load():
     if not os.path.exists(_LIB_PATH):
         raise ImportError(
@@ -74,7 +81,9 @@ lib = _load()
 _vp, _i32, _i64, _u64, _sz = C.c_void_p, C.c_int32, C.c_int64, C.c_uint64, C.c_size_t
 _st = C.c_int  # moe_status_t
 
-# (name, restype, argtypes) for every symbol of include/moecache.h
+_kv = C.POINTER(KvT)
+
+# (name, restype, argtypes) for every symbol of include/moecache.h and include/moekv.h
 SIGNATURES = [
     ("moe_create", _st, [C.POINTER(Config), C.POINTER(_vp)]),
     ("moe_destroy", None, [_vp]),
@@ -116,6 +125,18 @@ SIGNATURES = [
                          C.POINTER(_i32), C.POINTER(_i32), C.POINTER(Stats)]),
     ("moe_static_budget", _st, [_i32, _i32, C.c_int64, C.c_int64, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
                                 C.c_int64, C.POINTER(Budget)]),
+    ("moe_kv_work_bytes", _st, [_kv, C.POINTER(_i64)]),
+    ("moe_kv_check_errors", _st, [_kv, _vp]),
+    ("moe_kv_fork", _st, [_kv, _vp, _vp, _i32, _vp]),
+    ("moe_kv_reserve", _st, [_kv, _vp, _vp, _i32, _vp]),
+    ("moe_kv_write", _st, [_kv, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _vp]),
+    ("moe_kv_free", _st, [_kv, _vp, _i32, _vp]),
+    ("moe_kv_compact", _st, [_kv, _vp]),
+    ("moe_kv_copy_pages", _st, [_kv, _vp, _vp, _i32, _vp]),
+    ("moe_attn_decode", _st, [_kv, _i32, _vp, _i64, _vp, _i32, _i32, _i32, C.c_float, _i32, _i32, _vp, _i64, _vp]),
+    ("moe_attn_prefill", _st, [_kv, _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, C.c_float, _i32, _i32, _vp, _i64,
+                               _vp]),
+    ("moe_quant_linear", _st, [_vp, _i32, _i32, _i32, _vp, _i32, _i64, _i32, _vp, _vp, _i32, _i64, _vp]),
 ]
 
 for _name, _res, _args in SIGNATURES:

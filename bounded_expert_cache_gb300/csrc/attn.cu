@@ -1,0 +1,924 @@
+// Attention over the paged cache on warp-level matrix instructions (bf16) and
+// on the CUDA cores (f32): the newest tokens of many sequences, split over the
+// cache's length and joined; and whole row tiles of prompt chunks.
+//
+// For a row at position p with visible tokens J:
+//   s_j = c q.k_j (c = scale log2 e),  m = max s_j,  o = sum 2^(s_j-m) v_j / sum 2^(s_j-m),
+// computed in one pass over the tokens with a running (m, l, o): a tile with a
+// larger maximum m' scales l and o by 2^(m-m') first. Two partial results of
+// disjoint token sets join by the same rule, which is what lets several warps,
+// and several CTAs, share one row's tokens.
+//
+// Rows: the group's query heads share a cache head, so a unit of work is one
+// (sequence, row tile, cache head) whose rows are (token, head of the group)
+// pairs, and K and V are read once for all of them.
+//
+// Decode work split: the token tiles of all units form one line, cut into one
+// equal run per CTA (one CTA per SM). A run covers whole units or ends inside
+// one; a unit cut by run ends leaves partial (m, l, o) rows in the scratch and
+// the CTA that arrives last joins them in run order, so results do not depend
+// on arrival order. Every CTA derives the cut from the lengths itself: no
+// planning launch and no host copy of the lengths.
+//
+// What bounds it: HBM. K and V tiles come by 16-byte asynchronous copies into
+// a ring in shared memory; one barrier per tile.
+#include <cuda_bf16.h>
+
+#include "kv.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = 8;
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;  // bytes read; the rest of the 16 is zero
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&p);
+}
+// Either half of a bf16 pair is an infinity or a NaN.
+__device__ __forceinline__ bool nonfinite2(uint32_t v) {
+  return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
+}
+
+// One sequence's share of the call.
+struct Seq {
+  int id;    // table row
+  int len;   // tokens held
+  int m;     // query tokens
+  int row0;  // first query row
+};
+
+// Query rows of chunk b; 0 (with an error recorded) if cu leaves the rows given.
+__device__ __forceinline__ int chunk_rows(const AttnArgs& a, int b) {
+  const int r0 = __ldg(a.cu + b), r1 = __ldg(a.cu + b + 1);
+  if (r0 < 0 || r1 < r0 || r1 > a.n_rows) {
+    atomicOr(a.err, MOE_DEVERR_BADIDX);
+    return 0;
+  }
+  return r1 - r0;
+}
+
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
+  Seq s;
+  s.id = a.seqs ? __ldg(a.seqs + b) : b;
+  if (a.cu) {
+    s.row0 = __ldg(a.cu + b);
+    s.m = chunk_rows(a, b);
+  } else {
+    s.row0 = b * a.n_q;
+    s.m = a.n_q;
+  }
+  s.len = 0;
+  if (s.id < 0 || s.id >= a.max_seqs) {
+    atomicOr(a.err, MOE_DEVERR_BADIDX);
+    s.id = 0;
+  } else {
+    s.len = max(0, __ldg(a.lens + s.id));
+    if (s.len > static_cast<int64_t>(a.max_pages) << a.page_shift) {
+      atomicOr(a.err, MOE_DEVERR_BADIDX);
+      s.len = 0;
+    }
+  }
+  return s;
+}
+
+// Token tiles that rows of query tokens [i0, i1) see: the n0 tiles that hold
+// the first tokens, then tiles lo .. lo + n - n0 - 1. At least one tile, so
+// that every unit is visited and writes its rows.
+struct Span {
+  int n, n0, lo;
+  int low;  // tokens in [sinks, low) are seen by no row
+  int end;  // tokens >= end are seen by no row
+  __device__ __forceinline__ int tile(int t) const { return t < n0 ? t : lo + t - n0; }
+};
+template <int KT>
+__device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& s, int i0, int i1) {
+  Span r;
+  r.end = max(0, s.len - s.m + i1);
+  r.low = 0;
+  if (a.window > 0) r.low = max(0, s.len - s.m + i0 - a.window + 1);
+  r.lo = r.low / KT;
+  r.n0 = min(r.lo, (min(a.sinks, r.low) + KT - 1) / KT);
+  r.n = max(1, (r.end + KT - 1) / KT - r.lo + r.n0);
+  return r;
+}
+
+// A unit of work, and the position of a cursor on the line of tiles.
+struct Cursor {
+  int b, rt, h;  // sequence, row tile, cache head
+  int t;         // tile of the unit
+  int per;       // tiles of each of the sequence's units
+  Seq s;
+  Span sp;
+};
+
+template <int KT>
+__device__ __forceinline__ void open_seq(const AttnArgs& a, Cursor& c) {
+  c.s = load_seq(a, c.b);
+  c.sp = span_of<KT>(a, c.s, 0, c.s.m);
+  c.per = c.sp.n;
+}
+
+// Issue one K or V tile (KT tokens of one head) into shared memory. Tokens
+// that no row of the unit sees arrive as zeros, whatever the cache holds.
+// Shared rows are swizzled: 16-byte piece c of row r lies at c ^ (r & 7).
+template <int KT, int ROWB>
+__device__ __forceinline__ void issue_tile(const AttnArgs& a, const Cursor& c, const void* base, uint32_t dst,
+                                           int row_bytes) {
+  constexpr int kPieces = ROWB / 16;              // 16-byte pieces of a padded row
+  constexpr int kPer = KT * kPieces / kThreads;   // pieces a thread
+  constexpr int kStep = kThreads / kPieces;       // rows between a thread's pieces
+  static_assert(kPer * kThreads == KT * kPieces, "pieces");
+  const int tile0 = c.sp.tile(c.t) * KT;
+  const int piece = threadIdx.x % kPieces, r0 = threadIdx.x / kPieces;
+  const int32_t* row = a.table + static_cast<int64_t>(c.s.id) * a.max_pages;
+  const bool col_ok = piece * 16 < row_bytes;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int r = r0 + i * kStep, j = tile0 + r;
+    bool ok = col_ok && j < c.sp.end && (j >= c.sp.low || j < a.sinks);
+    const char* src = static_cast<const char*>(base);
+    if (ok) {
+      const int p = __ldg(row + (j >> a.page_shift));
+      if (p < 0 || p >= a.n_pages) {
+        atomicOr(a.err, MOE_DEVERR_BADIDX);
+        ok = false;
+      } else {
+        const int64_t tok = ((static_cast<int64_t>(p) * a.Hkv + c.h) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
+        src += tok * row_bytes + piece * 16;
+      }
+    }
+    cp16(dst + r * ROWB + ((piece ^ (r & 7)) << 4), src, ok);
+  }
+}
+
+// ------------------------------------------------------------ bf16 engine
+// RG row groups of 16 rows by KG = 8 / RG token groups, one warp each. Per
+// tile a warp forms S = Q K^T for its 16 rows and KT / KG tokens (m16n8k16,
+// K rows as the columns of B), updates its own (m, l), and adds P V with P
+// straight from its accumulators. DP: head size padded to 64, 128 or 256.
+template <int DP_, int RG_, int KT_>
+struct MmaEngine {
+  using T = __nv_bfloat16;
+  static constexpr int DP = DP_, RG = RG_, KT = KT_;
+  static constexpr int KG = kWarps / RG, kRows = RG * 16, KC = KT / KG / 16;
+  static constexpr int ROWB = DP * 2;
+  static constexpr uint32_t kTileBytes = KT * ROWB;
+  static constexpr int kMergeBytes = kWarps * 16 * 64 * 4;
+  static_assert(KC >= 1 && KC * KG * 16 == KT, "token groups");
+
+  uint32_t qf[DP / 16][4];
+  float o[DP / 8][4];
+  float s[KC][2][4];
+  uint32_t p[KC][4];
+  float m[2], l[2];
+  int pos[2];     // positions of this thread's rows lane / 4 and + 8; -1: no row
+  bool active;    // the warp has a row
+  bool edge;      // the tile holds a token seen by some but not all of the warp's rows
+  uint32_t seen[KC];  // of an edge tile, per chunk: bit 4r+i of s[r][i] visible
+  int rg, kg;
+
+  __device__ __forceinline__ void begin(const AttnArgs& a, const Cursor& c) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    rg = warp / KG;
+    kg = warp % KG;
+    const int first = c.rt * kRows + rg * 16, total = c.s.m * a.g;
+    active = first < total;
+    const T* q[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = first + lane / 4 + 8 * h;
+      pos[h] = -1;
+      q[h] = nullptr;
+      if (r < total) {
+        const int i = r / a.g;
+        pos[h] = c.s.len - c.s.m + i;
+        q[h] = static_cast<const T*>(a.q) + (c.s.row0 + i) * a.ldq + (c.h * a.g + r - i * a.g) * a.D;
+      }
+      m[h] = -INFINITY;
+      l[h] = 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int d = k * 16 + (i >> 1) * 8 + (lane & 3) * 2;
+        qf[k][i] = (q[i & 1] && d < a.D) ? __ldg(reinterpret_cast<const unsigned int*>(q[i & 1] + d)) : 0u;
+      }
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+  }
+
+  __device__ __forceinline__ void scores(const AttnArgs& a, const Cursor& c, uint32_t kt) {
+    if (!active) return;
+    const int lane = threadIdx.x & 31;
+    const int tile0 = c.sp.tile(c.t) * KT;
+    // every row of the warp sees every token of the tile, or some do not
+    const int lo_pos = c.s.len - c.s.m + (c.rt * kRows + rg * 16) / a.g;
+    const int last = min(c.rt * kRows + rg * 16 + 15, c.s.m * a.g - 1);
+    const int hi_pos = c.s.len - c.s.m + last / a.g;
+    edge = tile0 + KT - 1 > lo_pos;
+    if (a.window > 0) edge |= hi_pos - tile0 >= a.window;
+#pragma unroll
+    for (int ch = 0; ch < KC; ++ch) {
+      const int key0 = (ch * KG + kg) * 16;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[ch][i >> 2][i & 3] = 0.f;
+      // matrices: tokens 0-7 (d, d+8), tokens 8-15 (d, d+8)
+      const int r = key0 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+      for (int k = 0; k < DP / 16; ++k) {
+        uint32_t b[4];
+        const int piece = 2 * k + ((lane >> 3) & 1);
+        ldsm4(b, kt + r * ROWB + ((piece ^ (r & 7)) << 4));
+        mma16816(s[ch][0], qf[k], b[0], b[1]);
+        mma16816(s[ch][1], qf[k], b[2], b[3]);
+      }
+    }
+    float mx[2] = {m[0], m[1]};
+#pragma unroll
+    for (int ch = 0; ch < KC; ++ch) {
+      seen[ch] = 0xFFu;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float v = s[ch][r][i] * a.scale_log2;
+          if (edge) {
+            const int j = tile0 + (ch * KG + kg) * 16 + r * 8 + (lane & 3) * 2 + (i & 1);
+            const int back = pos[i >> 1] - j;
+            const bool see = back >= 0 && (a.window == 0 || back < a.window || j < a.sinks);
+            if (!see) {
+              v = -INFINITY;
+              seen[ch] &= ~(1u << (4 * r + i));
+            }
+          }
+          s[ch][r][i] = v;
+          mx[i >> 1] = fmaxf(mx[i >> 1], v);
+        }
+    }
+    float f[2], mu[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      mx[h] = fmaxf(mx[h], __shfl_xor_sync(~0u, mx[h], 1));
+      mx[h] = fmaxf(mx[h], __shfl_xor_sync(~0u, mx[h], 2));
+      mu[h] = mx[h] == -INFINITY ? 0.f : mx[h];  // nothing seen yet: every numerator is 2^-inf = 0
+      f[h] = ex2(m[h] - mu[h]);
+      m[h] = mx[h];
+      l[h] *= f[h];
+    }
+#pragma unroll
+    for (int ch = 0; ch < KC; ++ch) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[ch][r][i] = ex2(s[ch][r][i] - mu[i >> 1]);
+          l[i >> 1] += s[ch][r][i];
+        }
+      // numerators round to bf16 for the matrix product (the sum l keeps fp32):
+      // relative 2^-8 each at most, as the rounding of a bf16 result
+      p[ch][0] = pack_bf16(s[ch][0][0], s[ch][0][1]);
+      p[ch][1] = pack_bf16(s[ch][0][2], s[ch][0][3]);
+      p[ch][2] = pack_bf16(s[ch][1][0], s[ch][1][1]);
+      p[ch][3] = pack_bf16(s[ch][1][2], s[ch][1][3]);
+    }
+    if (__any_sync(~0u, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+      for (int n = 0; n < DP / 8; ++n) {
+        o[n][0] *= f[0];
+        o[n][1] *= f[0];
+        o[n][2] *= f[1];
+        o[n][3] *= f[1];
+      }
+    }
+  }
+
+  __device__ __forceinline__ void values(const AttnArgs& a, const Cursor&, uint32_t vt) {
+    if (!active) return;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int ch = 0; ch < KC; ++ch) {
+      const int key0 = (ch * KG + kg) * 16;
+      if (edge && any_nonfinite(vt, key0)) {
+        // a product with a zero numerator would carry the infinity or NaN of a
+        // token into rows that do not see it
+        values_by_row(vt, key0, ch);
+        continue;
+      }
+      const int r = key0 + (lane & 7) + (((lane >> 3) & 1) << 3);
+#pragma unroll
+      for (int n = 0; n < DP / 16; ++n) {
+        uint32_t b[4];
+        const int piece = 2 * n + (lane >> 4);
+        ldsm4t(b, vt + r * ROWB + ((piece ^ (r & 7)) << 4));
+        mma16816(o[2 * n], p[ch], b[0], b[1]);
+        mma16816(o[2 * n + 1], p[ch], b[2], b[3]);
+      }
+    }
+  }
+
+  __device__ __forceinline__ bool any_nonfinite(uint32_t vt, int key0) const {
+    const int lane = threadIdx.x & 31;
+    bool bad = false;
+    for (int i = lane; i < 16 * (ROWB / 16); i += 32) {
+      uint32_t w[4];
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(vt + key0 * ROWB + i * 16));
+      bad |= nonfinite2(w[0]) || nonfinite2(w[1]) || nonfinite2(w[2]) || nonfinite2(w[3]);
+    }
+    return __any_sync(~0u, bad);
+  }
+
+  __device__ __forceinline__ void values_by_row(uint32_t vt, int key0, int ch) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int key = 0; key < 16; ++key) {
+      // the quad's thread (key % 8) / 2 holds this token's numerators
+      const int from = (lane & ~3) | ((key & 7) >> 1);
+      float pr[2];
+      uint32_t mask = 0;
+#pragma unroll
+      for (int cc = 0; cc < KC; ++cc) {
+        if (cc != ch) continue;
+        mask = __shfl_sync(~0u, seen[cc], from);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t w = __shfl_sync(~0u, key < 8 ? p[cc][h] : p[cc][2 + h], from);
+          pr[h] = __uint_as_float((key & 1) ? (w & 0xFFFF0000u) : (w << 16));
+        }
+      }
+      const int r = key0 + key;
+#pragma unroll
+      for (int n = 0; n < DP / 8; ++n) {
+        uint32_t w;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(vt + r * ROWB + ((n ^ (r & 7)) << 4) + (lane & 3) * 4));
+        const float v[2] = {__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((mask >> (4 * (key >> 3) + (i >> 1) * 2 + (key & 1))) & 1) o[n][i] += pr[i >> 1] * v[i & 1];
+      }
+    }
+  }
+
+  // Join the token groups' results in shared memory, 64 columns at a time, and
+  // hand (row, column, 4 values, m, l) to store. Called by every thread.
+  template <class F>
+  __device__ __forceinline__ void end(const AttnArgs& a, const Cursor& c, float* buf, float2* ml, F&& store) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(~0u, l[h], 1);
+      l[h] += __shfl_xor_sync(~0u, l[h], 2);
+      if ((lane & 3) == 0) ml[warp * 16 + lane / 4 + 8 * h] = make_float2(m[h], l[h]);
+    }
+    const int rows = min(kRows, c.s.m * a.g - c.rt * kRows);
+#pragma unroll
+    for (int n0 = 0; n0 < DP; n0 += 64) {
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float2*>(buf + (warp * 16 + lane / 4 + 8 * h) * 64 + ((n * 8 + (lane & 3) * 2) ^ ((lane & 12) << 1))) =
+              make_float2(o[n0 / 8 + n][2 * h], o[n0 / 8 + n][2 * h + 1]);
+      __syncthreads();
+      for (int e = threadIdx.x; e < rows * 16; e += kThreads) {
+        const int r = e >> 4, col = (e & 15) * 4;
+        if (n0 + col < a.D) {
+          const int w0 = (r >> 4) * KG, rr = r & 15;
+          float M = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < KG; ++k) M = fmaxf(M, ml[(w0 + k) * 16 + rr].x);
+          const float Mu = M == -INFINITY ? 0.f : M;
+          float L = 0.f;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < KG; ++k) {
+            const float2 t = ml[(w0 + k) * 16 + rr];
+            const float f = ex2(t.x - Mu);
+            L += f * t.y;
+            const float4 u =
+                *reinterpret_cast<const float4*>(buf + ((w0 + k) * 16 + rr) * 64 + (col ^ ((rr & 3) << 3)));
+            v.x += f * u.x;
+            v.y += f * u.y;
+            v.z += f * u.z;
+            v.w += f * u.w;
+          }
+          store(r, n0 + col, v, M, L);
+        }
+      }
+      __syncthreads();
+    }
+  }
+};
+
+// ------------------------------------------------------------- f32 engine
+// 16 rows; per tile of 32 tokens a thread forms the scores of two rows and one
+// token, the warps' softmax goes through shared memory, and a thread then owns
+// four columns of a few rows. fp32 products throughout.
+template <int DP_>
+struct FmaEngine {
+  using T = float;
+  static constexpr int DP = DP_, KT = 32, kRows = 16;
+  static constexpr int ROWB = DP * 4;
+  static constexpr uint32_t kTileBytes = KT * ROWB;
+  static constexpr int kC4 = DP / 4;                       // column quads
+  static constexpr int kRT = kRows * kC4 / kThreads;       // rows a thread in the value product
+  // q rows, numerators, row factors
+  static constexpr int kMergeBytes = kRows * ROWB + kRows * KT * 4 + kRows * 4;
+  static_assert(kRT >= 1 && kRT * kThreads == kRows * kC4, "columns");
+
+  float4 o[kRT];
+  float m[2], l[2];  // rows 2 warp and 2 warp + 1, kept by every lane
+  float* qs;
+  float* ps;
+  float* fs;
+  bool edge;
+
+  __device__ __forceinline__ void begin(const AttnArgs& a, const Cursor& c) {
+    const int total = c.s.m * a.g;
+    for (int e = threadIdx.x; e < kRows * DP; e += kThreads) {
+      const int rr = e / DP, d = e % DP, r = c.rt * kRows + rr;
+      float v = 0.f;
+      if (r < total && d < a.D) {
+        const int i = r / a.g;
+        v = __ldg(static_cast<const float*>(a.q) + (c.s.row0 + i) * a.ldq + (c.h * a.g + r - i * a.g) * a.D + d);
+      }
+      qs[e] = v;
+    }
+#pragma unroll
+    for (int i = 0; i < kRT; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      m[h] = -INFINITY;
+      l[h] = 0.f;
+    }
+    __syncthreads();
+  }
+
+  __device__ __forceinline__ static float4 lds4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+  }
+  // position of row rr of the tile, -1 past the last row
+  __device__ __forceinline__ static int pos_of(const AttnArgs& a, const Cursor& c, int rr) {
+    const int r = c.rt * kRows + rr;
+    return r < c.s.m * a.g ? c.s.len - c.s.m + r / a.g : -1;
+  }
+  __device__ __forceinline__ static bool sees(const AttnArgs& a, int pos, int j) {
+    const int back = pos - j;
+    return back >= 0 && (a.window == 0 || back < a.window || j < a.sinks);
+  }
+
+  __device__ __forceinline__ void scores(const AttnArgs& a, const Cursor& c, uint32_t kt) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tile0 = c.sp.tile(c.t) * KT;
+    const int lo_pos = pos_of(a, c, 0);
+    const int hi_pos = c.s.len - c.s.m + (min((c.rt + 1) * kRows, c.s.m * a.g) - 1) / a.g;
+    edge = tile0 + KT - 1 > lo_pos || (a.window > 0 && hi_pos - tile0 >= a.window);
+    float acc[2] = {0.f, 0.f};
+    const float* q0 = qs + 2 * warp * DP;
+#pragma unroll 8
+    for (int d4 = 0; d4 < kC4; ++d4) {
+      const float4 k = lds4(kt + lane * ROWB + ((d4 ^ (lane & 7)) << 4));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 q = *reinterpret_cast<const float4*>(q0 + h * DP + d4 * 4);
+        acc[h] += q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int rr = 2 * warp + h;
+      const bool see = sees(a, pos_of(a, c, rr), tile0 + lane);
+      const float v = see ? acc[h] * a.scale_log2 : -INFINITY;
+      float mx = v;
+#pragma unroll
+      for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, x));
+      mx = fmaxf(m[h], mx);
+      const float mu = mx == -INFINITY ? 0.f : mx, f = ex2(m[h] - mu), p = ex2(v - mu);
+      m[h] = mx;
+      l[h] = l[h] * f + p;  // this lane's tokens only, until the end
+      ps[rr * KT + lane] = p;
+      if (lane == 0) fs[rr] = f;
+    }
+    // values() starts after the barrier that publishes its tile, which also
+    // publishes ps and fs
+  }
+
+  __device__ __forceinline__ void values(const AttnArgs& a, const Cursor& c, uint32_t vt) {
+    const int c4 = threadIdx.x % kC4, r0 = threadIdx.x / kC4;
+    constexpr int kStep = kThreads / kC4;
+    const int tile0 = c.sp.tile(c.t) * KT;
+#pragma unroll
+    for (int i = 0; i < kRT; ++i) {
+      const float f = fs[r0 + i * kStep];
+      o[i].x *= f, o[i].y *= f, o[i].z *= f, o[i].w *= f;
+    }
+#pragma unroll 4
+    for (int key = 0; key < KT; ++key) {
+      const float4 v = lds4(vt + key * ROWB + ((c4 ^ (key & 7)) << 4));
+#pragma unroll
+      for (int i = 0; i < kRT; ++i) {
+        const int rr = r0 + i * kStep;
+        const float p = ps[rr * KT + key];
+        // a hidden token's infinity or NaN times its zero numerator is not added
+        if (edge && !sees(a, pos_of(a, c, rr), tile0 + key)) continue;
+        o[i].x += p * v.x;
+        o[i].y += p * v.y;
+        o[i].z += p * v.z;
+        o[i].w += p * v.w;
+      }
+    }
+  }
+
+  template <class F>
+  __device__ __forceinline__ void end(const AttnArgs& a, const Cursor& c, float*, float2* ml, F&& store) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float t = l[h];
+#pragma unroll
+      for (int x = 16; x; x >>= 1) t += __shfl_xor_sync(~0u, t, x);
+      if (lane == 0) ml[2 * warp + h] = make_float2(m[h], t);
+    }
+    __syncthreads();
+    const int c4 = threadIdx.x % kC4, r0 = threadIdx.x / kC4;
+    const int rows = min(kRows, c.s.m * a.g - c.rt * kRows);
+#pragma unroll
+    for (int i = 0; i < kRT; ++i) {
+      const int rr = r0 + i * (kThreads / kC4);
+      if (rr < rows && c4 * 4 < a.D) store(rr, c4 * 4, o[i], ml[rr].x, ml[rr].y);
+    }
+    __syncthreads();
+  }
+};
+
+template <class T>
+__device__ __forceinline__ void store4(T* dst, float4 v);
+template <>
+__device__ __forceinline__ void store4<float>(float* dst, float4 v) {
+  *reinterpret_cast<float4*>(dst) = v;
+}
+template <>
+__device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* dst, float4 v) {
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
+
+// The result of a row: o / l, 0 for a row that sees nothing.
+template <class T>
+__device__ __forceinline__ void write_out(const AttnArgs& a, const Cursor& c, int rows_per_tile, int r, int col,
+                                          float4 v, float L) {
+  const int rr = c.rt * rows_per_tile + r, i = rr / a.g;
+  const float inv = c.s.len - c.s.m + i < 0 ? 0.f : 1.f / L;
+  T* dst = static_cast<T*>(a.out) + (c.s.row0 + i) * a.ldo + (c.h * a.g + rr - i * a.g) * a.D + col;
+  if (inv == 0.f && c.s.len - c.s.m + i < 0)
+    v = make_float4(0.f, 0.f, 0.f, 0.f);
+  else
+    v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  store4<T>(dst, v);
+}
+
+// Block-wide inclusive scan of one int64 per thread; returns the thread's
+// exclusive prefix and the total.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(~0u, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) tmp[warp] = x;
+  __syncthreads();
+  int64_t base = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) base += tmp[w];
+    all += tmp[w];
+  }
+  __syncthreads();
+  *total = all;
+  return base + x - v;
+}
+
+// The ring takes what the merge buffer leaves of 220 KB, at most 8 tiles.
+template <class E>
+struct Ring {
+  static constexpr int kFit = (220 * 1024 - E::kMergeBytes) / static_cast<int>(E::kTileBytes);
+  static constexpr int kSlots = kFit > 8 ? 8 : kFit;
+  static constexpr int kSmem = kSlots * static_cast<int>(E::kTileBytes) + E::kMergeBytes;
+};
+
+// SPLIT: runs of the line of tiles (decode). Otherwise one unit a CTA (chunks).
+template <class E, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1) attn_kernel(AttnArgs a) {
+  constexpr int NS = Ring<E>::kSlots;
+  static_assert(NS >= 3, "ring");
+  constexpr int KT = E::KT, R = E::kRows;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  __shared__ int64_t s_scan[kWarps];
+  __shared__ int64_t s_found[2];
+  __shared__ float2 s_ml[kWarps * 16];
+  __shared__ int s_last;
+  const uint32_t ring = smem_u32(sm);
+  float* merge = reinterpret_cast<float*>(sm + NS * E::kTileBytes);
+  const int row_bytes = a.D * static_cast<int>(sizeof(typename E::T));
+  const int rt_n = a.row_tiles;
+
+  // ---- this CTA's run [first, last) of the line
+  Cursor ld;
+  int64_t todo = 0, run0 = 0, unit0 = 0, total = 0, G = 1;
+  if (SPLIT) {
+    auto tiles_of = [&](int b) -> int64_t {
+      Seq s = load_seq(a, b);
+      return static_cast<int64_t>(span_of<KT>(a, s, 0, s.m).n) * rt_n * a.Hkv;
+    };
+    int64_t mine = 0, all = 0;
+    for (int b0 = 0; b0 < a.n; b0 += kThreads) {
+      mine = b0 + static_cast<int>(threadIdx.x) < a.n ? tiles_of(b0 + threadIdx.x) : 0;
+      int64_t t;
+      block_scan(mine, s_scan, &t);
+      all += t;
+    }
+    total = all;
+    G = min(static_cast<int64_t>(gridDim.x), total);
+    if (blockIdx.x >= G) return;
+    run0 = total * blockIdx.x / G;
+    todo = total * (blockIdx.x + 1) / G - run0;
+    int64_t base = 0;
+    for (int b0 = 0; b0 < a.n; b0 += kThreads) {
+      if (a.n > kThreads) mine = b0 + static_cast<int>(threadIdx.x) < a.n ? tiles_of(b0 + threadIdx.x) : 0;
+      int64_t t;
+      const int64_t ex = base + block_scan(mine, s_scan, &t);
+      if (run0 >= ex && run0 < ex + mine) {
+        s_found[0] = b0 + threadIdx.x;
+        s_found[1] = ex;
+      }
+      base += t;
+      __syncthreads();
+      if (run0 < base) break;
+    }
+    ld.b = static_cast<int>(s_found[0]);
+    open_seq<KT>(a, ld);
+    const int64_t off = run0 - s_found[1];
+    const int u = static_cast<int>(off / ld.per);
+    ld.t = static_cast<int>(off % ld.per);
+    ld.rt = u / a.Hkv;
+    ld.h = u % a.Hkv;
+    unit0 = run0 - ld.t;
+  } else {
+    // row tiles of every sequence in order, cache heads innermost
+    const int want = blockIdx.x / a.Hkv;
+    ld.h = blockIdx.x % a.Hkv;
+    int64_t base = 0;
+    if (threadIdx.x == 0) s_found[0] = -1;
+    __syncthreads();
+    for (int b0 = 0; b0 < a.n && base <= want; b0 += kThreads) {
+      int64_t mine = 0, t;
+      if (b0 + static_cast<int>(threadIdx.x) < a.n) {
+        mine = (static_cast<int64_t>(chunk_rows(a, b0 + threadIdx.x)) * a.g + R - 1) / R;
+      }
+      const int64_t ex = base + block_scan(mine, s_scan, &t);
+      if (want >= ex && want < ex + mine) {
+        s_found[0] = b0 + threadIdx.x;
+        s_found[1] = want - ex;
+      }
+      base += t;
+    }
+    __syncthreads();
+    if (s_found[0] < 0) return;
+    ld.b = static_cast<int>(s_found[0]);
+    ld.rt = static_cast<int>(s_found[1]);
+    ld.s = load_seq(a, ld.b);
+    ld.sp = span_of<KT>(a, ld.s, ld.rt * R / a.g, (min((ld.rt + 1) * R, ld.s.m * a.g) - 1) / a.g + 1);
+    ld.per = ld.sp.n;
+    ld.t = 0;
+    todo = ld.per;
+  }
+
+  E eng;
+  if constexpr (sizeof(typename E::T) == 4) {
+    eng.qs = merge;
+    eng.ps = merge + R * E::DP;
+    eng.fs = eng.ps + R * KT;
+  }
+  // The load cursor runs ahead of the compute cursor, across units: element
+  // 2i of the ring's sequence is the K tile, 2i + 1 the V tile, of tile i.
+  Cursor cp = ld;
+  int64_t issued = 0;  // elements
+  const int64_t elems = 2 * todo;
+  int slot_in = 0, slot_out = 0;
+  auto advance = [&](Cursor& c) {
+    if (++c.t < c.per || !SPLIT) return;
+    c.t = 0;
+    if (++c.h < a.Hkv) return;
+    c.h = 0;
+    if (++c.rt < rt_n) return;
+    c.rt = 0;
+    if (++c.b < a.n) open_seq<KT>(a, c);
+  };
+  auto issue = [&]() {
+    if (issued < elems) {
+      issue_tile<KT, E::ROWB>(a, ld, (issued & 1) ? a.v : a.k, ring + slot_in * E::kTileBytes, row_bytes);
+      if ((issued & 1) && issued + 1 < elems) advance(ld);
+      ++issued;
+      if (++slot_in == NS) slot_in = 0;
+    }
+    cp_commit();  // empty groups keep the count
+  };
+  for (int i = 0; i < NS - 1; ++i) issue();
+  // One element: wait for it, let every thread see it (and be done with the
+  // element before), refill that slot.
+  auto next = [&]() -> uint32_t {
+    cp_wait<NS - 2>();
+    __syncthreads();
+    issue();
+    const uint32_t at = ring + slot_out * E::kTileBytes;
+    if (++slot_out == NS) slot_out = 0;
+    return at;
+  };
+
+  int64_t at = run0;
+  while (todo > 0) {
+    // ---- one unit's share of the run
+    const int t0 = cp.t;
+    const int nt = static_cast<int>(min(todo, static_cast<int64_t>(cp.per - t0)));
+    const Cursor unit = cp;
+    eng.begin(a, cp);
+    for (int i = 0; i < nt; ++i) {
+      const uint32_t kt = next();
+      eng.scores(a, cp, kt);
+      const uint32_t vt = next();
+      eng.values(a, cp, vt);
+      if (i + 1 < nt) ++cp.t;
+    }
+    todo -= nt;
+    const bool whole = t0 == 0 && nt == unit.per;
+    if (whole) {
+      eng.end(a, unit, merge, s_ml, [&](int r, int col, float4 v, float, float L) {
+        write_out<typename E::T>(a, unit, R, r, col, v, L);
+      });
+    } else {
+      // partial rows of this CTA: slot 0 if its run starts in this unit, else 1
+      constexpr int kPS = E::DP + 4;
+      const int64_t kSlot = static_cast<int64_t>(kPartRows) * kPS;
+      float* mine = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (run0 >= unit0 ? 0 : 1)) * kSlot;
+      eng.end(a, unit, merge, s_ml, [&](int r, int col, float4 v, float M, float L) {
+        *reinterpret_cast<float4*>(mine + r * kPS + 4 + col) = v;
+        if (col == 0) *reinterpret_cast<float2*>(mine + r * kPS) = make_float2(M, L);
+      });
+      // CTAs that hold a part of this unit: those whose runs meet it
+      const int64_t unit1 = unit0 + unit.per;
+      auto cta_of = [&](int64_t tile) {  // the c with total*c/G <= tile < total*(c+1)/G
+        int64_t c = tile * G / total;
+        while (total * c / G > tile) --c;
+        while (total * (c + 1) / G <= tile) ++c;
+        return c;
+      };
+      const int64_t c0 = cta_of(unit0), c1 = cta_of(unit1 - 1);
+      __threadfence();
+      __syncthreads();
+      unsigned int* ticket = a.tickets + c0;  // only one unit can start in c0's run and leave it
+      if (threadIdx.x == 0) {
+        const unsigned int done = atomicAdd(ticket, 1u);
+        s_last = done == static_cast<unsigned int>(c1 - c0);
+        if (s_last) *ticket = 0u;  // zero between launches
+      }
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        const int rows = min(R, unit.s.m * a.g - unit.rt * R), c4n = a.D / 4;
+        auto slot_of = [&](int64_t c) {
+          return a.part + (2 * c + (total * c / G >= unit0 ? 0 : 1)) * kSlot;
+        };
+        for (int e = threadIdx.x; e < rows * c4n; e += kThreads) {
+          const int r = e / c4n, col = (e - r * c4n) * 4;
+          float M = -INFINITY;
+#pragma unroll 8
+          for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(slot_of(c) + r * kPS));
+          const float Mu = M == -INFINITY ? 0.f : M;
+          float L = 0.f;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int64_t c = c0; c <= c1; ++c) {
+            const float* p = slot_of(c) + r * kPS;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p));
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(p + 4 + col));
+            const float f = ex2(ml.x - Mu);
+            L += f * ml.y;
+            v.x += f * u.x;
+            v.y += f * u.y;
+            v.z += f * u.z;
+            v.w += f * u.w;
+          }
+          write_out<typename E::T>(a, unit, R, r, col, v, L);
+        }
+      }
+    }
+    at += nt;
+    unit0 = at;
+    if (todo > 0) {
+      cp.t = cp.per - 1;
+      advance(cp);
+    }
+  }
+  cp_wait<0>();
+}
+
+template <class E, bool SPLIT>
+cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
+  constexpr int smem = Ring<E>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(attn_kernel<E, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  attn_kernel<E, SPLIT><<<grid, kThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <class E>
+cudaError_t decode_rows(AttnArgs a, int num_sms, cudaStream_t st) {
+  a.row_tiles = (a.n_q * a.g + E::kRows - 1) / E::kRows;
+  return launch<E, true>(a, num_sms, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_decode(const AttnArgs& a, int32_t dtype, int num_sms, cudaStream_t st) {
+  if (dtype == MOE_F32) {
+    if (a.D <= 64) return decode_rows<FmaEngine<64>>(a, num_sms, st);
+    if (a.D <= 128) return decode_rows<FmaEngine<128>>(a, num_sms, st);
+    return decode_rows<FmaEngine<256>>(a, num_sms, st);
+  }
+  // the fewest row groups that hold the rows: more token groups per tile
+  const int rows = a.n_q * a.g;
+  if (a.D <= 64) {
+    if (rows <= 16) return decode_rows<MmaEngine<64, 1, 128>>(a, num_sms, st);
+    if (rows <= 32) return decode_rows<MmaEngine<64, 2, 128>>(a, num_sms, st);
+    return decode_rows<MmaEngine<64, 4, 128>>(a, num_sms, st);
+  }
+  if (a.D <= 128) {
+    if (rows <= 16) return decode_rows<MmaEngine<128, 1, 128>>(a, num_sms, st);
+    if (rows <= 32) return decode_rows<MmaEngine<128, 2, 128>>(a, num_sms, st);
+    return decode_rows<MmaEngine<128, 4, 128>>(a, num_sms, st);
+  }
+  if (rows <= 32) return decode_rows<MmaEngine<256, 2, 64>>(a, num_sms, st);
+  return decode_rows<MmaEngine<256, 4, 64>>(a, num_sms, st);
+}
+
+cudaError_t launch_attn_prefill(const AttnArgs& a, int32_t dtype, int32_t n_rows, int num_sms, cudaStream_t st) {
+  (void)num_sms;
+  // every sequence has at most one partly filled row tile
+  auto grid = [&](int rows) {
+    return static_cast<int>(((static_cast<int64_t>(n_rows) * a.g + rows - 1) / rows + a.n) * a.Hkv);
+  };
+  if (dtype == MOE_F32) {
+    if (a.D <= 64) return launch<FmaEngine<64>, false>(a, grid(16), st);
+    if (a.D <= 128) return launch<FmaEngine<128>, false>(a, grid(16), st);
+    return launch<FmaEngine<256>, false>(a, grid(16), st);
+  }
+  if (a.D <= 64) return launch<MmaEngine<64, 4, 128>, false>(a, grid(64), st);
+  if (a.D <= 128) return launch<MmaEngine<128, 4, 128>, false>(a, grid(64), st);
+  return launch<MmaEngine<256, 4, 64>, false>(a, grid(64), st);
+}
+
+}  // namespace moe

@@ -1,0 +1,563 @@
+// Bookkeeping of the paged key-value cache on the device: fork, reserve with
+// copy-on-write, write, free, compact, copy.
+//
+// The integer work (page counts, lowest free pages, moves) runs in one cluster
+// of 8 CTAs: every phase reads a consistent state, a cluster barrier separates
+// it from the phase that changes that state, and nothing returns to the host,
+// so a decode step that grows its sequences stays capturable in a CUDA graph.
+// A call first checks its whole list in every CTA of the cluster (the same
+// reads, so the same verdict) and then changes either everything or nothing.
+//
+// Page ids come from prefix sums over ref, never from the order of atomics:
+// the lowest free page first, in list order.
+//
+// What bounds it: the small calls are latency (a few dependent reads and two
+// or three cluster barriers); the copies are HBM.
+#include <cooperative_groups.h>
+
+#include "kv.h"
+
+namespace cg = cooperative_groups;
+
+namespace moe {
+namespace {
+
+constexpr int kCtas = 8, kThreads = 1024;
+constexpr int kWarps = kThreads / 32, kAll = kCtas * kThreads, kAllWarps = kCtas * kWarps;
+constexpr int kBitmapWords = 65536 / 32;
+
+struct Kv {
+  int32_t* table;
+  int32_t* lens;
+  int32_t* ref;
+  KvWork* work;
+  int32_t *src, *dst, *filled, *map, *shr, *last;
+  int32_t S, W, P, page, page_shift;
+};
+
+__device__ __forceinline__ int pages_of(const Kv& kv, int64_t tokens) {
+  return static_cast<int>((tokens + kv.page - 1) >> kv.page_shift);
+}
+__device__ __forceinline__ bool pending(const Kv& kv) { return *const_cast<volatile uint32_t*>(&kv.work->err) != 0u; }
+
+// Threads that share one listed sequence: a power of two, at least a warp.
+__device__ __forceinline__ int lanes_per(int n) {
+  int t = 32;
+  while (t * 2 * n <= kAll) t *= 2;
+  return t;
+}
+
+// Mark id in the bitmap; false if it is out of range or was marked.
+__device__ __forceinline__ bool mark(uint32_t* bits, int id, int S) {
+  if (id < 0 || id >= S) return false;
+  return !(atomicOr(bits + (id >> 5), 1u << (id & 31)) & (1u << (id & 31)));
+}
+__device__ __forceinline__ bool held_ok(const Kv& kv, int len) {
+  return len >= 0 && pages_of(kv, len) <= kv.W;
+}
+
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+    fork_kernel(Kv kv, const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n) {
+  __shared__ uint32_t bits[kBitmapWords];
+  auto cluster = cg::this_cluster();
+  const int tid = threadIdx.x, rank = cluster.block_rank();
+  for (int i = tid; i < kBitmapWords; i += kThreads) bits[i] = 0u;
+  const bool stop = pending(kv);
+  __syncthreads();
+  bool ok = true;
+  for (int i = tid; i < n; i += kThreads) {
+    const int s = src[i], d = dst[i];
+    ok &= mark(bits, d, kv.S) && kv.lens[d] == 0;
+    ok &= s >= 0 && s < kv.S && held_ok(kv, kv.lens[s]);
+  }
+  ok = __syncthreads_and(ok);
+  cluster.sync();  // every CTA has its verdict before anything changes
+  if (stop) return;
+  if (!ok) {
+    if (rank == 0 && tid == 0) atomicOr(&kv.work->err, MOE_DEVERR_BADIDX);
+    return;
+  }
+  const int per = lanes_per(n), g = (rank * kThreads + tid) / per, lane = (rank * kThreads + tid) % per;
+  for (int i = g; i < n; i += kAll / per) {
+    const int s = src[i], d = dst[i];
+    // a source that is also a destination was empty before the call
+    const int len = (bits[s >> 5] >> (s & 31)) & 1u ? 0 : kv.lens[s];
+    const int np = pages_of(kv, len);
+    for (int j = lane; j < np; j += per) {
+      const int p = kv.table[static_cast<int64_t>(s) * kv.W + j];
+      kv.table[static_cast<int64_t>(d) * kv.W + j] = p;
+      if (p >= 0 && p < kv.P)
+        atomicAdd(kv.ref + p, 1);
+      else
+        atomicOr(&kv.work->err, MOE_DEVERR_BADIDX);
+    }
+    if (lane == 0 && len > 0) kv.lens[d] = len;
+  }
+}
+
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+    free_kernel(Kv kv, const int32_t* __restrict__ seqs, int n) {
+  __shared__ uint32_t bits[kBitmapWords];
+  auto cluster = cg::this_cluster();
+  const int tid = threadIdx.x, rank = cluster.block_rank();
+  for (int i = tid; i < kBitmapWords; i += kThreads) bits[i] = 0u;
+  const bool stop = pending(kv);
+  __syncthreads();
+  bool ok = true;
+  for (int i = tid; i < n; i += kThreads) {
+    const int s = seqs[i];
+    ok &= mark(bits, s, kv.S) && held_ok(kv, kv.lens[s]);
+  }
+  ok = __syncthreads_and(ok);
+  cluster.sync();
+  if (stop) return;
+  if (!ok) {
+    if (rank == 0 && tid == 0) atomicOr(&kv.work->err, MOE_DEVERR_BADIDX);
+    return;
+  }
+  const int per = lanes_per(n), g = (rank * kThreads + tid) / per, lane = (rank * kThreads + tid) % per;
+  for (int i = g; i < n; i += kAll / per) {
+    const int s = seqs[i], np = pages_of(kv, kv.lens[s]);
+    for (int j = lane; j < np; j += per) {
+      int32_t* e = kv.table + static_cast<int64_t>(s) * kv.W + j;
+      const int p = *e;
+      if (p >= 0 && p < kv.P)
+        atomicSub(kv.ref + p, 1);
+      else
+        atomicOr(&kv.work->err, MOE_DEVERR_BADIDX);
+      *e = -1;
+    }
+  }
+  cluster.sync();  // lengths were read by every thread of their group
+  for (int i = rank * kThreads + tid; i < n; i += kAll) kv.lens[seqs[i]] = 0;
+}
+
+// Pages of one warp of the cluster: [first, last), whole strips of 32.
+struct Strip {
+  int first, last;
+};
+__device__ __forceinline__ Strip strip_of(int P, int w) {
+  const int strips = (P + 31) / 32;
+  Strip s;
+  s.first = static_cast<int>(static_cast<int64_t>(strips) * w / kAllWarps) * 32;
+  s.last = min(P, static_cast<int>(static_cast<int64_t>(strips) * (w + 1) / kAllWarps) * 32);
+  return s;
+}
+// Free pages in a warp's strips (every lane gets the count).
+__device__ __forceinline__ int count_free(const Kv& kv, Strip s, int lane) {
+  int c = 0;
+#pragma unroll 8
+  for (int p0 = s.first; p0 < s.last; p0 += 32) c += p0 + lane < s.last && kv.ref[p0 + lane] == 0;
+  return __reduce_add_sync(~0u, c);
+}
+// Give every CTA of the cluster every warp's count.
+__device__ __forceinline__ void share_counts(cg::cluster_group& cluster, int* counts, int w, int lane, int c) {
+  if (lane < kCtas) *cluster.map_shared_rank(counts + w, lane) = c;
+  cluster.sync();
+}
+// Sum of the counts of warps before w, and of all.
+__device__ __forceinline__ int2 prefix_of(const int* counts, int w, int lane) {
+  int before = 0, all = 0;
+#pragma unroll
+  for (int i = lane; i < kAllWarps; i += 32) {
+    const int c = counts[i];
+    all += c;
+    before += i < w ? c : 0;
+  }
+  return make_int2(__reduce_add_sync(~0u, before), __reduce_add_sync(~0u, all));
+}
+
+// Block-wide inclusive scan.
+__device__ __forceinline__ int block_incl(int v, int* tmp, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(~0u, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) tmp[warp] = x;
+  __syncthreads();
+  const int t = tmp[lane];
+  const int below = __reduce_add_sync(~0u, lane < warp ? t : 0);
+  *total = __reduce_add_sync(~0u, t);
+  __syncthreads();
+  return x + below;
+}
+
+// first[i]: requests of the sequences before the i-th; info[i]: its pages
+// before the call, times two, plus one if it copies its last page first.
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+    reserve_kernel(Kv kv, const int32_t* __restrict__ seqs, const int32_t* __restrict__ n_new, int n) {
+  extern __shared__ int dyn[];
+  int* first = dyn;
+  int* info = dyn + n + 1;
+  __shared__ uint32_t bits[kBitmapWords];
+  __shared__ int counts[kAllWarps];
+  __shared__ int scan[kWarps];
+  auto cluster = cg::this_cluster();
+  const int tid = threadIdx.x, rank = cluster.block_rank(), lane = tid & 31;
+  const int w = rank * kWarps + (tid >> 5);
+  for (int i = tid; i < kBitmapWords; i += kThreads) bits[i] = 0u;
+  const bool stop = pending(kv);
+  __syncthreads();
+  // the list, and the sharers of every partly filled shared last page
+  bool ok = true, room = true;
+  for (int i = tid; i < n; i += kThreads) {
+    const int s = seqs[i], add = n_new[i];
+    if (!mark(bits, s, kv.S) || add < 0 || !held_ok(kv, kv.lens[s])) {
+      ok = false;
+      continue;
+    }
+    const int len = kv.lens[s];
+    if (static_cast<int64_t>(len) + add > static_cast<int64_t>(kv.W) << kv.page_shift) room = false;
+    if (add > 0 && (len & (kv.page - 1))) {
+      const int p = kv.table[static_cast<int64_t>(s) * kv.W + (len >> kv.page_shift)];
+      if (p < 0 || p >= kv.P)
+        ok = false;
+      else if (i / kThreads % kCtas == rank && kv.ref[p] > 1) {
+        atomicAdd(kv.shr + p, 1);
+        atomicMax(kv.last + p, i + 1);
+      }
+    }
+  }
+  ok = __syncthreads_and(ok);
+  room = __syncthreads_and(room);
+  const Strip st = strip_of(kv.P, w);
+  const int mine = count_free(kv, st, lane);
+  share_counts(cluster, counts, w, lane, mine);  // also publishes shr and last
+  // requests of every listed sequence
+  int total = 0;
+  if (ok && room && !stop) {
+    for (int i0 = 0; i0 < n; i0 += kThreads) {
+      const int i = i0 + tid;
+      int need = 0;
+      if (i < n) {
+        const int s = seqs[i], len = kv.lens[s], add = n_new[i];
+        const int have = pages_of(kv, len);
+        int cow = 0;
+        if (add > 0 && (len & (kv.page - 1))) {
+          const int p = kv.table[static_cast<int64_t>(s) * kv.W + have - 1];
+          const int k = __ldcg(kv.shr + p);
+          // every sharer copies; if all of them are listed, the last one stays
+          cow = kv.ref[p] > 1 && !(k == kv.ref[p] && __ldcg(kv.last + p) == i + 1);
+        }
+        need = cow + pages_of(kv, static_cast<int64_t>(len) + add) - have;
+        info[i] = have * 2 + cow;
+      }
+      int t;
+      const int incl = block_incl(need, scan, &t);
+      if (i < n) first[i] = total + incl - need;
+      // the pool bounds what can be granted; beyond it only the verdict counts
+      total = min(total + t, kv.P + 1);
+    }
+    if (tid == 0) first[n] = total;
+  }
+  const int2 pre = prefix_of(counts, w, lane);
+  if (total > pre.y) room = false;
+  __syncthreads();
+  const bool go = ok && room && !stop;
+  // the lowest free pages, in order
+  if (go) {
+    int r = pre.x;
+    for (int p0 = st.first; p0 < st.last && r < total; p0 += 32) {
+      const bool f = p0 + lane < st.last && kv.ref[p0 + lane] == 0;
+      const unsigned int b = __ballot_sync(~0u, f);
+      const int q = r + __popc(b & ((1u << lane) - 1u));
+      if (f && q < total) kv.src[q] = p0 + lane;
+      r += __popc(b);
+    }
+  }
+  cluster.sync();
+  // the sharer counts go back to zero whatever the verdict
+  for (int i = rank * kThreads + tid; i < n; i += kAll) {
+    const int s = seqs[i];
+    if (s < 0 || s >= kv.S) continue;
+    const int len = kv.lens[s];
+    if (!held_ok(kv, len) || !(len & (kv.page - 1))) continue;
+    const int p = kv.table[static_cast<int64_t>(s) * kv.W + (len >> kv.page_shift)];
+    if (p < 0 || p >= kv.P) continue;
+    kv.shr[p] = 0;
+    kv.last[p] = 0;
+  }
+  if (!go) {
+    if (rank == 0 && tid == 0) {
+      kv.work->n_copies = 0;
+      if (!stop) atomicOr(&kv.work->err, !ok ? MOE_DEVERR_BADIDX : MOE_DEVERR_CAPACITY);
+    }
+    return;
+  }
+  cluster.sync();  // lengths and table rows were read above
+  for (int q = rank * kThreads + tid; q < total; q += kAll) {
+    int lo = 0, hi = n;  // the sequence i with first[i] <= q < first[i + 1]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first[mid] <= q)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int j = q - first[lo], cow = info[lo] & 1, e = (info[lo] >> 1) + j - cow;
+    const int p = kv.src[q];
+    int32_t* at = kv.table + static_cast<int64_t>(seqs[lo]) * kv.W + e;
+    if (cow && j == 0) atomicSub(kv.ref + *at, 1);
+    if (cow && j == 0) kv.map[lo] = *at;
+    *at = p;
+    kv.ref[p] = 1;
+  }
+  for (int i = rank * kThreads + tid; i < n; i += kAll) {
+    const int s = seqs[i], len = kv.lens[s];
+    kv.lens[s] = len + n_new[i];
+    kv.filled[i] = info[i] & 1 ? len & (kv.page - 1) : 0;
+    if (info[i] & 1) kv.dst[i] = kv.src[first[i]];
+  }
+  if (rank == 0 && tid == 0) kv.work->n_copies = n;
+}
+
+// The copies of reserve: entry i copies the first filled[i] tokens of page
+// map[i] to page dst[i], in every layer and head of k and v. A warp copies
+// one (entry, layer, k or v, head) at a time.
+__global__ void __launch_bounds__(256)
+    cow_copy_kernel(Kv kv, uint4* k, uint4* v, int L, int H, int tok_vecs, int64_t page_vecs) {
+  const int n = kv.work->n_copies, lane = threadIdx.x & 31;
+  const int64_t items = static_cast<int64_t>(n) * L * 2 * H;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t it = blockIdx.x * 8ll + (threadIdx.x >> 5); it < items; it += warps) {
+    int64_t r = it;
+    const int h = static_cast<int>(r % H);
+    r /= H;
+    uint4* pool = r & 1 ? v : k;
+    r >>= 1;
+    const int l = static_cast<int>(r % L), i = static_cast<int>(r / L);
+    const int vecs = kv.filled[i] * tok_vecs;
+    if (vecs == 0) continue;
+    const int64_t head = static_cast<int64_t>(h) * kv.page * tok_vecs;
+    const uint4* from = pool + (static_cast<int64_t>(l) * kv.P + kv.map[i]) * page_vecs + head;
+    uint4* to = pool + (static_cast<int64_t>(l) * kv.P + kv.dst[i]) * page_vecs + head;
+#pragma unroll 4
+    for (int x = lane; x < vecs; x += 32) to[x] = from[x];
+  }
+}
+
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) compact_kernel(Kv kv) {
+  __shared__ int counts[kAllWarps], below[kAllWarps];
+  auto cluster = cg::this_cluster();
+  const int tid = threadIdx.x, rank = cluster.block_rank(), lane = tid & 31;
+  const int w = rank * kWarps + (tid >> 5);
+  const bool stop = pending(kv);
+  const Strip st = strip_of(kv.P, w);
+  const int free_mine = count_free(kv, st, lane);
+  share_counts(cluster, counts, w, lane, free_mine);
+  const int2 pre = prefix_of(counts, w, lane);
+  const int live = kv.P - pre.y;
+  // holes below the new end = pages in use above it
+  int c = 0;
+#pragma unroll 8
+  for (int p0 = st.first; p0 < st.last; p0 += 32) c += p0 + lane < min(st.last, live) && kv.ref[p0 + lane] == 0;
+  share_counts(cluster, below, w, lane, __reduce_add_sync(~0u, c));
+  const int holes = prefix_of(below, w, lane).y;
+  if (stop) {
+    if (rank == 0 && tid == 0) {
+      kv.work->n_copies = 0;
+      kv.work->n_live = kv.P;
+    }
+    return;
+  }
+  int f = pre.x;  // free pages before the strip
+  for (int p0 = st.first; p0 < st.last; p0 += 32) {
+    const int p = p0 + lane;
+    const bool in = p < st.last, fr = in && kv.ref[p] == 0;
+    const unsigned int b = __ballot_sync(~0u, fr);
+    const int before = f + __popc(b & ((1u << lane) - 1u));
+    if (fr && p < live) kv.dst[before] = p;
+    // pages in use before p, less those below the new end
+    if (in && !fr && p >= live) kv.src[p - before - (live - holes)] = p;
+    f += __popc(b);
+  }
+  cluster.sync();
+  for (int r = rank * kThreads + tid; r < holes; r += kAll) {
+    const int s = kv.src[r], d = kv.dst[r];
+    kv.map[s] = d;
+    kv.ref[d] = kv.ref[s];
+    kv.ref[s] = 0;
+  }
+  if (rank == 0 && tid == 0) {
+    kv.work->n_copies = holes;
+    kv.work->n_live = live;
+  }
+}
+
+// Whole pages src[i] -> dst[i] in every layer, pieces of kPiece vectors, and
+// (REMAP) the table entries of moved pages.
+constexpr int kPiece = 1024;  // 16 KB
+template <bool REMAP>
+__global__ void __launch_bounds__(256)
+    page_copy_kernel(Kv kv, uint4* k, uint4* v, const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n,
+                     int L, int64_t page_vecs) {
+  if (REMAP) n = kv.work->n_copies;
+  else if (pending(kv)) return;
+  const int pieces = static_cast<int>((page_vecs + kPiece - 1) / kPiece);
+  const int64_t items = static_cast<int64_t>(n) * L * 2 * pieces;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    int64_t r = it;
+    const int piece = static_cast<int>(r % pieces);
+    r /= pieces;
+    uint4* pool = r & 1 ? v : k;
+    r >>= 1;
+    const int l = static_cast<int>(r % L), i = static_cast<int>(r / L);
+    const int s = src[i], d = dst[i];
+    if (!REMAP && (s < 0 || s >= kv.P || d < 0 || d >= kv.P)) {
+      if (threadIdx.x == 0) atomicOr(&kv.work->err, MOE_DEVERR_BADIDX);
+      continue;
+    }
+    const uint4* from = pool + (static_cast<int64_t>(l) * kv.P + s) * page_vecs + static_cast<int64_t>(piece) * kPiece;
+    uint4* to = pool + (static_cast<int64_t>(l) * kv.P + d) * page_vecs + static_cast<int64_t>(piece) * kPiece;
+    const int vecs = static_cast<int>(min(static_cast<int64_t>(kPiece), page_vecs - static_cast<int64_t>(piece) * kPiece));
+    uint4 t[kPiece / 256];
+#pragma unroll
+    for (int x = 0; x < kPiece / 256; ++x)
+      if (static_cast<int>(threadIdx.x) + x * 256 < vecs) t[x] = __ldcs(from + threadIdx.x + x * 256);
+#pragma unroll
+    for (int x = 0; x < kPiece / 256; ++x)
+      if (static_cast<int>(threadIdx.x) + x * 256 < vecs) __stcs(to + threadIdx.x + x * 256, t[x]);
+  }
+  if (REMAP) {
+    const int live = kv.work->n_live, lane = threadIdx.x & 31;
+    const int warps = gridDim.x * 8;
+    for (int s = blockIdx.x * 8 + (threadIdx.x >> 5); s < kv.S; s += warps) {
+      const int len = kv.lens[s];
+      const int np = held_ok(kv, len) ? pages_of(kv, len) : 0;
+      for (int j = lane; j < np; j += 32) {
+        int32_t* e = kv.table + static_cast<int64_t>(s) * kv.W + j;
+        if (*e >= live && *e < kv.P) *e = kv.map[*e];
+      }
+    }
+  }
+}
+
+// One warp per new token: K and V of every head to its place in its page.
+__global__ void __launch_bounds__(256)
+    write_kernel(Kv kv, uint4* k, uint4* v, const uint4* __restrict__ nk, int64_t ldk, const uint4* __restrict__ nv,
+                 int64_t ldv, const int32_t* __restrict__ seqs, const int32_t* __restrict__ cu, int n, int n_rows,
+                 int H, int tok_vecs) {
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= n_rows || pending(kv)) return;
+  int lo = 0, hi = n;  // the last i with cu[i] <= row
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(cu + mid) <= row)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int r0 = __ldg(cu + lo), r1 = __ldg(cu + lo + 1);
+  if (row < r0 || row >= r1) return;
+  const int s = seqs ? __ldg(seqs + lo) : lo;
+  if (s < 0 || s >= kv.S) {
+    if (lane == 0) atomicOr(&kv.work->err, MOE_DEVERR_BADIDX);
+    return;
+  }
+  const int len = kv.lens[s], at = len - (r1 - row);
+  if (len - (r1 - r0) < 0 || !held_ok(kv, len)) {  // the chunk does not fit: none of it is written
+    if (lane == 0) atomicOr(&kv.work->err, KV_DEVERR_SHARED);
+    return;
+  }
+  const int p = kv.table[static_cast<int64_t>(s) * kv.W + (at >> kv.page_shift)];
+  if (p < 0 || p >= kv.P || kv.ref[p] != 1) {
+    if (lane == 0) atomicOr(&kv.work->err, p < 0 || p >= kv.P ? MOE_DEVERR_BADIDX : KV_DEVERR_SHARED);
+    return;
+  }
+  const uint4* fk = nk + row * ldk;
+  const uint4* fv = nv + row * ldv;
+  const int64_t base = ((static_cast<int64_t>(p) * H) << kv.page_shift) + (at & (kv.page - 1));
+#pragma unroll 4
+  for (int x = lane; x < H * tok_vecs; x += 32) {
+    const int h = x / tok_vecs, c = x - h * tok_vecs;
+    const int64_t to = (base + (static_cast<int64_t>(h) << kv.page_shift)) * tok_vecs + c;
+    k[to] = __ldg(fk + x);
+    v[to] = __ldg(fv + x);
+  }
+}
+
+Kv kv_of(const moe_kv_t& a, const KvLayout& l) {
+  Kv kv;
+  char* w = static_cast<char*>(a.work);
+  kv.table = a.table;
+  kv.lens = a.lens;
+  kv.ref = a.ref;
+  kv.work = reinterpret_cast<KvWork*>(w);
+  kv.src = reinterpret_cast<int32_t*>(w + l.src);
+  kv.dst = reinterpret_cast<int32_t*>(w + l.dst);
+  kv.filled = reinterpret_cast<int32_t*>(w + l.filled);
+  kv.map = reinterpret_cast<int32_t*>(w + l.map);
+  kv.shr = reinterpret_cast<int32_t*>(w + l.shr);
+  kv.last = reinterpret_cast<int32_t*>(w + l.last);
+  kv.S = a.max_seqs;
+  kv.W = a.max_pages;
+  kv.P = a.n_pages;
+  kv.page = a.page_tokens;
+  kv.page_shift = __builtin_ctz(a.page_tokens);
+  return kv;
+}
+// 16-byte vectors of one token of one head, and of a page of one layer
+int tok_vecs(const moe_kv_t& a) { return a.head_dim * (a.dtype == MOE_F32 ? 4 : 2) / 16; }
+int64_t page_vecs(const moe_kv_t& a) { return static_cast<int64_t>(a.n_kv_heads) * a.page_tokens * tok_vecs(a); }
+
+}  // namespace
+
+cudaError_t launch_kv_fork(const moe_kv_t& a, const KvLayout& l, const int32_t* src, const int32_t* dst, int32_t n,
+                           cudaStream_t st) {
+  fork_kernel<<<kCtas, kThreads, 0, st>>>(kv_of(a, l), src, dst, n);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_reserve(const moe_kv_t& a, const KvLayout& l, const int32_t* seqs, const int32_t* n_new,
+                              int32_t n, int num_sms, cudaStream_t st) {
+  const int smem = (2 * n + 1) * 4;
+  cudaError_t e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (2 * kMaxList + 1) * 4);
+  if (e != cudaSuccess) return e;
+  const Kv kv = kv_of(a, l);
+  reserve_kernel<<<kCtas, kThreads, smem, st>>>(kv, seqs, n_new, n);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int64_t items = static_cast<int64_t>(n) * a.n_layers * 2 * a.n_kv_heads;
+  const int grid = static_cast<int>(std::min<int64_t>((items + 7) / 8, 8ll * num_sms));
+  cow_copy_kernel<<<grid, 256, 0, st>>>(kv, static_cast<uint4*>(a.k), static_cast<uint4*>(a.v), a.n_layers,
+                                        a.n_kv_heads, tok_vecs(a), page_vecs(a));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_write(const moe_kv_t& a, const KvLayout& l, int32_t layer, const void* k_new, int64_t ldk,
+                            const void* v_new, int64_t ldv, const int32_t* seqs, const int32_t* cu, int32_t n,
+                            int32_t n_rows, cudaStream_t st) {
+  const int per = a.dtype == MOE_F32 ? 4 : 8;
+  const int64_t off = layer * (static_cast<int64_t>(a.n_pages) * page_vecs(a));
+  write_kernel<<<(n_rows + 7) / 8, 256, 0, st>>>(kv_of(a, l), static_cast<uint4*>(a.k) + off,
+                                                  static_cast<uint4*>(a.v) + off, static_cast<const uint4*>(k_new),
+                                                  ldk / per, static_cast<const uint4*>(v_new), ldv / per, seqs, cu, n,
+                                                  n_rows, a.n_kv_heads, tok_vecs(a));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_free(const moe_kv_t& a, const KvLayout& l, const int32_t* seqs, int32_t n, cudaStream_t st) {
+  free_kernel<<<kCtas, kThreads, 0, st>>>(kv_of(a, l), seqs, n);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_compact(const moe_kv_t& a, const KvLayout& l, int num_sms, cudaStream_t st) {
+  const Kv kv = kv_of(a, l);
+  compact_kernel<<<kCtas, kThreads, 0, st>>>(kv);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  page_copy_kernel<true><<<8 * num_sms, 256, 0, st>>>(kv, static_cast<uint4*>(a.k), static_cast<uint4*>(a.v), kv.src,
+                                                      kv.dst, 0, a.n_layers, page_vecs(a));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_copy_pages(const moe_kv_t& a, const KvLayout& l, const int32_t* src, const int32_t* dst,
+                                 int32_t n, int num_sms, cudaStream_t st) {
+  page_copy_kernel<false><<<8 * num_sms, 256, 0, st>>>(kv_of(a, l), static_cast<uint4*>(a.k), static_cast<uint4*>(a.v),
+                                                       src, dst, n, a.n_layers, page_vecs(a));
+  return cudaGetLastError();
+}
+
+}  // namespace moe

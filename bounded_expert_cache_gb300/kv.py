@@ -1,0 +1,198 @@
+"""Paged key-value cache, attention over it and the 4-bit linear layer: the
+binding of include/moekv.h. PyTorch supplies device memory and streams; every
+step runs in the library's CUDA kernels.
+"""
+from __future__ import annotations
+
+import ctypes as C
+import math
+from typing import Optional
+
+import torch
+
+from . import _native as N
+from ._native import lib
+from .api import _check, _ptr, _stream
+
+
+def _dtype_id(dtype: torch.dtype) -> int:
+    if dtype == torch.float32:
+        return N.F32
+    if dtype == torch.bfloat16:
+        return N.BF16
+    raise TypeError(f"expected float32 or bfloat16 (got {dtype})")
+
+
+def _ints(t: torch.Tensor, name: str, n: Optional[int] = None) -> torch.Tensor:
+    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 1 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous one-dimensional int32 CUDA tensor")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must hold {n} entries (got {t.numel()})")
+    return t
+
+
+def _head_rows(t: torch.Tensor, name: str, heads: Optional[int], dim: int, dtype: torch.dtype) -> int:
+    """Row stride (elements) of [rows, heads, dim] whose rows are dense but may lie apart."""
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a {dtype} CUDA tensor")
+    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [rows, {heads if heads is not None else 'heads'}, {dim}] "
+                         f"(got {tuple(t.shape)})")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim):
+        raise ValueError(f"the heads of a row of {name} must be dense")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * dim)
+
+
+class KvCache:
+    """Device arrays of a paged key-value cache (``moe_kv_t``).
+
+    Either over tensors that the caller has (k, v: [layers, pages, kv_heads,
+    page_tokens, head_dim]; table: int32 [max_seqs, max_pages]; lens: int32
+    [max_seqs]; ref: int32 [pages]) or, with :meth:`empty`, over new ones.
+    Sequence ids are rows of ``table``; every list of them is an int32 CUDA
+    tensor, so that a captured step can be replayed with other contents.
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor):
+        for t, name, dims in ((k, "k", 5), (v, "v", 5), (table, "table", 2), (lens, "lens", 1), (ref, "ref", 1)):
+            if not t.is_cuda or t.dim() != dims or not t.is_contiguous():
+                raise TypeError(f"{name} must be a contiguous CUDA tensor of {dims} dimensions")
+        _dtype_id(k.dtype)
+        if k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must have one shape and type")
+        if any(t.dtype != torch.int32 for t in (table, lens, ref)):
+            raise TypeError("table, lens and ref must be int32")
+        if lens.numel() != table.shape[0] or ref.numel() != k.shape[1]:
+            raise ValueError("lens needs one entry per table row, ref one per page")
+        if any(t.device != k.device for t in (v, table, lens, ref)):
+            raise ValueError("the cache's tensors must be on one device")
+        self.k, self.v, self.table, self.lens, self.ref = k, v, table, lens, ref
+        L, P, Hkv, page, D = k.shape
+        self.raw = N.KvT(k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), ref.data_ptr(), None, 0, L, P,
+                         Hkv, page, D, _dtype_id(k.dtype), table.shape[0], table.shape[1])
+        n = C.c_int64()
+        with torch.cuda.device(k.device):
+            _check(lib.moe_kv_work_bytes(C.byref(self.raw), C.byref(n)))
+        self.work = torch.zeros(n.value, dtype=torch.uint8, device=k.device)
+        self.raw.work, self.raw.work_bytes = self.work.data_ptr(), n.value
+
+    @classmethod
+    def empty(cls, n_layers, n_pages, n_kv_heads, page_tokens, head_dim, max_seqs, max_pages,
+              dtype=torch.bfloat16, device=None) -> "KvCache":
+        dev = device or torch.device("cuda")
+        shape = (n_layers, n_pages, n_kv_heads, page_tokens, head_dim)
+        i32 = dict(dtype=torch.int32, device=dev)
+        return cls(torch.zeros(shape, dtype=dtype, device=dev), torch.zeros(shape, dtype=dtype, device=dev),
+                   torch.full((max_seqs, max_pages), -1, **i32), torch.zeros(max_seqs, **i32),
+                   torch.zeros(n_pages, **i32))
+
+    @property
+    def token_bytes(self) -> int:
+        """Bytes of one token over all layers: kv_bytes_per_token of static_budget."""
+        L, _, Hkv, _, D = self.k.shape
+        return 2 * L * Hkv * D * self.k.element_size()
+
+    def fork(self, src, dst, stream=None):
+        """dst[i] becomes a sequence of src[i]'s tokens, sharing its pages."""
+        _ints(src, "src")
+        _ints(dst, "dst", src.numel())
+        _check(lib.moe_kv_fork(C.byref(self.raw), _ptr(src), _ptr(dst), src.numel(), _stream(stream)))
+
+    def reserve(self, seqs, n_new, stream=None):
+        """Pages for n_new[i] more tokens of seqs[i]; their lengths grow by it."""
+        _ints(seqs, "seqs")
+        _ints(n_new, "n_new", seqs.numel())
+        _check(lib.moe_kv_reserve(C.byref(self.raw), _ptr(seqs), _ptr(n_new), seqs.numel(), _stream(stream)))
+
+    def write(self, layer, k, v, seqs, cu, stream=None):
+        """Rows cu[i]..cu[i+1]-1 of k and v [rows, kv_heads, head_dim] become the newest tokens of seqs[i]."""
+        _ints(seqs, "seqs")
+        _ints(cu, "cu", seqs.numel() + 1)
+        Hkv, D = self.k.shape[2], self.k.shape[4]
+        ldk = _head_rows(k, "k", Hkv, D, self.k.dtype)
+        ldv = _head_rows(v, "v", Hkv, D, self.k.dtype)
+        if k.shape[0] != v.shape[0]:
+            raise ValueError("k and v must have as many rows")
+        _check(lib.moe_kv_write(C.byref(self.raw), layer, _ptr(k), ldk, _ptr(v), ldv, _ptr(seqs), _ptr(cu),
+                                seqs.numel(), k.shape[0], _stream(stream)))
+
+    def free(self, seqs, stream=None):
+        _ints(seqs, "seqs")
+        _check(lib.moe_kv_free(C.byref(self.raw), _ptr(seqs), seqs.numel(), _stream(stream)))
+
+    def compact(self, stream=None):
+        """Move the pages in use to the lowest ids."""
+        _check(lib.moe_kv_compact(C.byref(self.raw), _stream(stream)))
+
+    def copy_pages(self, src, dst, stream=None):
+        """Copy whole pages src[i] -> dst[i] in every layer; table and ref are untouched."""
+        _ints(src, "src")
+        _ints(dst, "dst", src.numel())
+        _check(lib.moe_kv_copy_pages(C.byref(self.raw), _ptr(src), _ptr(dst), src.numel(), _stream(stream)))
+
+    def check_errors(self, stream=None):
+        """Synchronise, raise what kernels recorded on this cache, and clear it."""
+        _check(lib.moe_kv_check_errors(C.byref(self.raw), _stream(stream)))
+
+    def _out(self, q, out):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        return out
+
+    def attn_decode(self, layer, q, seqs, n_q=1, out=None, scale=None, window=0, sinks=0, stream=None):
+        """Attention of the newest n_q tokens of each sequence: q [len(seqs) * n_q, heads, head_dim]."""
+        _ints(seqs, "seqs")
+        D = self.k.shape[4]
+        ldq = _head_rows(q, "q", None, D, self.k.dtype)
+        if q.shape[0] != seqs.numel() * n_q:
+            raise ValueError(f"q must have {seqs.numel()} x {n_q} rows (got {q.shape[0]})")
+        out = self._out(q, out)
+        ldo = _head_rows(out, "out", q.shape[1], D, self.k.dtype)
+        _check(lib.moe_attn_decode(C.byref(self.raw), layer, _ptr(q), ldq, _ptr(seqs), seqs.numel(), n_q, q.shape[1],
+                                   1.0 / math.sqrt(D) if scale is None else scale, window, sinks, _ptr(out), ldo,
+                                   _stream(stream)))
+        return out
+
+    def attn_prefill(self, layer, q, seqs, cu, out=None, scale=None, window=0, sinks=0, stream=None):
+        """Attention of chunks: rows cu[i]..cu[i+1]-1 of q are the newest tokens of seqs[i]."""
+        _ints(seqs, "seqs")
+        _ints(cu, "cu", seqs.numel() + 1)
+        D = self.k.shape[4]
+        ldq = _head_rows(q, "q", None, D, self.k.dtype)
+        out = self._out(q, out)
+        ldo = _head_rows(out, "out", q.shape[1], D, self.k.dtype)
+        _check(lib.moe_attn_prefill(C.byref(self.raw), layer, _ptr(q), ldq, _ptr(seqs), _ptr(cu), seqs.numel(),
+                                    q.shape[0], q.shape[1], 1.0 / math.sqrt(D) if scale is None else scale, window,
+                                    sinks, _ptr(out), ldo, _stream(stream)))
+        return out
+
+
+def quant_linear(x: torch.Tensor, w: torch.Tensor, quant: int, n_out: int, bias: Optional[torch.Tensor] = None,
+                 y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y = x W^T (+ bias) for a 4-bit matrix W [n_out, K] in split-plane layout.
+
+    x: [T, K] float32 or bfloat16 (rows may lie apart); w: uint8 with
+    n_out*K/2 quant bytes and n_out*K/16 scale bytes; quant: Q4_0 or I4_G64;
+    bias: float32 [n_out]; y: [T, n_out] float32 or bfloat16 (a new tensor of
+    x's type if None).
+    """
+    if x.dim() != 2 or not x.is_cuda or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be a [T, K] CUDA tensor with dense rows")
+    T, K = x.shape
+    xt = _dtype_id(x.dtype)
+    if w.dtype != torch.uint8 or not w.is_cuda or not w.is_contiguous() or w.numel() != n_out * K * 9 // 16:
+        raise ValueError(f"w must be {n_out * K * 9 // 16} contiguous uint8 CUDA bytes")
+    if bias is not None and (bias.dtype != torch.float32 or not bias.is_cuda or not bias.is_contiguous()
+                             or bias.numel() != n_out):
+        raise ValueError(f"bias must be a contiguous float32 CUDA tensor of {n_out} entries")
+    if y is None:
+        y = torch.empty((T, n_out), dtype=x.dtype, device=x.device)
+    if y.shape != (T, n_out) or not y.is_cuda or (n_out > 1 and y.stride(1) != 1):
+        raise ValueError(f"y must be a [{T}, {n_out}] CUDA tensor with dense rows")
+    ldx = x.stride(0) if T > 1 else max(x.stride(0), K)
+    ldy = y.stride(0) if T > 1 else max(y.stride(0), n_out)
+    _check(lib.moe_quant_linear(_ptr(w), quant, n_out, K, _ptr(x), xt, ldx, T, _ptr(bias), _ptr(y),
+                                _dtype_id(y.dtype), ldy, _stream(stream)))
+    return y
