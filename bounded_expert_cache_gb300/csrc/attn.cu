@@ -24,7 +24,7 @@
 // a ring in shared memory; one barrier per tile.
 #include <cuda_bf16.h>
 
-#include "kv.h"
+#include "attn.cuh"
 
 namespace moe {
 namespace {
@@ -44,11 +44,6 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -67,78 +62,6 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&p);
-}
-// Either half of a bf16 pair is an infinity or a NaN.
-__device__ __forceinline__ bool nonfinite2(uint32_t v) {
-  return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
-}
-
-// One sequence's share of the call.
-struct Seq {
-  int id;    // table row
-  int len;   // tokens held
-  int m;     // query tokens
-  int row0;  // first query row
-};
-
-// Query rows of chunk b; 0 (with an error recorded) if cu leaves the rows given.
-__device__ __forceinline__ int chunk_rows(const AttnArgs& a, int b) {
-  const int r0 = __ldg(a.cu + b), r1 = __ldg(a.cu + b + 1);
-  if (r0 < 0 || r1 < r0 || r1 > a.n_rows) {
-    atomicOr(a.err, MOE_DEVERR_BADIDX);
-    return 0;
-  }
-  return r1 - r0;
-}
-
-__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
-  Seq s;
-  s.id = a.seqs ? __ldg(a.seqs + b) : b;
-  if (a.cu) {
-    s.row0 = __ldg(a.cu + b);
-    s.m = chunk_rows(a, b);
-  } else {
-    s.row0 = b * a.n_q;
-    s.m = a.n_q;
-  }
-  s.len = 0;
-  if (s.id < 0 || s.id >= a.max_seqs) {
-    atomicOr(a.err, MOE_DEVERR_BADIDX);
-    s.id = 0;
-  } else {
-    s.len = max(0, __ldg(a.lens + s.id));
-    if (s.len > static_cast<int64_t>(a.max_pages) << a.page_shift) {
-      atomicOr(a.err, MOE_DEVERR_BADIDX);
-      s.len = 0;
-    }
-  }
-  return s;
-}
-
-// Token tiles that rows of query tokens [i0, i1) see: the n0 tiles that hold
-// the first tokens, then tiles lo .. lo + n - n0 - 1. At least one tile, so
-// that every unit is visited and writes its rows.
-struct Span {
-  int n, n0, lo;
-  int low;  // tokens in [sinks, low) are seen by no row
-  int end;  // tokens >= end are seen by no row
-  __device__ __forceinline__ int tile(int t) const { return t < n0 ? t : lo + t - n0; }
-};
-template <int KT>
-__device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& s, int i0, int i1) {
-  Span r;
-  r.end = max(0, s.len - s.m + i1);
-  r.low = 0;
-  if (a.window > 0) r.low = max(0, s.len - s.m + i0 - a.window + 1);
-  r.lo = r.low / KT;
-  r.n0 = min(r.lo, (min(a.sinks, r.low) + KT - 1) / KT);
-  r.n = max(1, (r.end + KT - 1) / KT - r.lo + r.n0);
-  return r;
-}
-
 // A unit of work, and the position of a cursor on the line of tiles.
 struct Cursor {
   int b, rt, h;  // sequence, row tile, cache head
@@ -906,7 +829,7 @@ cudaError_t launch_attn_decode(const AttnArgs& a, int32_t dtype, int num_sms, cu
 }
 
 cudaError_t launch_attn_prefill(const AttnArgs& a, int32_t dtype, int32_t n_rows, int num_sms, cudaStream_t st) {
-  (void)num_sms;
+  if (dtype == MOE_BF16 && a.D <= kTcHeadDim) return launch_attn_prefill_tc(a, num_sms, st);
   // every sequence has at most one partly filled row tile
   auto grid = [&](int rows) {
     return static_cast<int>(((static_cast<int64_t>(n_rows) * a.g + rows - 1) / rows + a.n) * a.Hkv);
@@ -916,8 +839,6 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, int32_t dtype, int32_t n_rows
     if (a.D <= 128) return launch<FmaEngine<128>, false>(a, grid(16), st);
     return launch<FmaEngine<256>, false>(a, grid(16), st);
   }
-  if (a.D <= 64) return launch<MmaEngine<64, 4, 128>, false>(a, grid(64), st);
-  if (a.D <= 128) return launch<MmaEngine<128, 4, 128>, false>(a, grid(64), st);
   return launch<MmaEngine<256, 4, 64>, false>(a, grid(64), st);
 }
 

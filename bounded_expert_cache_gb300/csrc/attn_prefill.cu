@@ -1,0 +1,775 @@
+// Attention of prompt chunks over the paged cache on the 5th-generation tensor
+// cores (bf16, head sizes up to 128).
+//
+// A unit of work is 256 rows of one sequence and cache head, a row being a
+// (token, head of the group) pair, so that K and V are read once for all the
+// heads that share them. The rows are two tiles of 128; per tile of 128 tokens
+//   S = Q K^T           128 x 128, fp32 in tensor memory
+//   P = 2^(c S - c m)   row by row, one thread a row, rounded to bf16 and
+//                       written back over S in tensor memory
+//   O = O + P V         128 x D, fp32 in tensor memory, P from tensor memory
+// with c = scale log2 e and m the row's running maximum. m is only raised (and
+// O and the row's sum scaled) when the maximum has grown by more than 2^8
+// since: numerators then stay below 2^8, which bf16 and fp32 hold as precisely
+// as those below 1, and O is hardly ever read back.
+//
+// The two row tiles take turns on the tensor cores: while one's scores are
+// exponentiated the other's products run. Order of the issuing thread:
+//   QK0(0) QK1(0) | PV0(0) QK0(1) PV1(0) QK1(1) | PV0(1) QK0(2) ...
+// These execute in order, so the barrier of a QK also says that the PV before
+// it is done, and P may share S's columns.
+//
+// Warps: 0-3 and 4-7 softmax of row tiles 0 and 1 (they also load Q and write
+// the results), 8 TMA of K and V pages, 9 MMA issue, 10 V check.
+// The V check: a token that only some rows see must not reach the others, but
+// 0 * NaN is NaN in a matrix product. In tiles with such tokens the warp zeroes
+// the tokens that no row sees, and looks for infinities and NaN among the
+// rest; if it finds one, the unit's rows are formed again one by one.
+//
+// Work split: the token tiles of all units form one line, cut into one equal
+// run per CTA (one CTA per SM), as in the decode kernel: causal units differ in
+// length, and whole units would leave SMs idle in the last wave. A unit cut by
+// run ends leaves partial rows (m, l, O), joined by the warp that arrives last,
+// in run order.
+//
+// Every wait is bounded, as in the prefill GEMMs: on a time-out all roles leave
+// their loops, copies and MMAs in flight are drained, an error is recorded.
+#include <cuda.h>
+
+#include "attn.cuh"
+#include "prefill.h"
+#include "tc.cuh"
+
+namespace moe {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 384;
+constexpr int kKT = 128;      // tokens a tile
+constexpr int kQT = 128;      // rows a row tile
+constexpr int kUnitRows = 2 * kQT;
+constexpr float kRaise = 8.f;  // log2 of the growth that raises m
+
+template <int DP>
+struct Cfg {
+  static constexpr uint32_t kHalf = kKT * 128;              // 64 columns of a tile: 128-byte rows
+  static constexpr uint32_t kTile = kHalf * (DP / 64);      // a Q, K or V tile
+  static constexpr int kKS = DP == 64 ? 4 : 2, kVS = DP == 64 ? 4 : 3;  // ring slots of K and V
+  static constexpr int kSmem = (2 + kKS + kVS) * static_cast<int>(kTile) + 1024;
+  static constexpr uint32_t kTmemS = 0, kTmemO = 256;       // columns: S0 S1 O0 O1
+  // partial rows of one row tile: (m, l) then O by column quads
+  static constexpr int64_t kPart = static_cast<int64_t>(kQT) * (DP + 4);
+};
+
+__device__ __forceinline__ void umma_ss(uint32_t dt, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(dt),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// Descriptor of an operand whose contiguous direction is its M or N direction
+// (V: tokens x columns): 128-byte swizzle, blocks of 64 columns `lbo` bytes
+// apart, groups of 8 tokens 1024 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFF) >> 4);
+  d |= static_cast<uint64_t>(lbo >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+__device__ __forceinline__ void tma3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          dst),
+      "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// 32 columns of this warp's 32 lanes, without waiting
+__device__ __forceinline__ void tmem_ld32_async(uint32_t ta, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+        "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
+        "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]),
+        "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]),
+        "=f"(r[30]), "=f"(r[31])
+      : "r"(ta));
+}
+__device__ __forceinline__ void tmem_ld16_async(uint32_t ta, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+        "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(ta));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// two fp32 lanes an instruction
+__device__ __forceinline__ unsigned long long pack2(float a, float b) {
+  unsigned long long v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ float2 unpack2(unsigned long long v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// A CTA's walk along the line: units (sequence, row tile, cache head) in order,
+// of each the tiles [t0, t0 + nt) that fall into the run.
+struct Walk {
+  int b, rt, h;
+  int t0, nt;         // this segment
+  int64_t unit0;      // line position of the unit's first tile
+  int64_t left;       // tiles of the run not yet in a segment
+  Seq s;
+  Span sp;
+  int rows;           // rows of the unit
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && nt == sp.n; }
+};
+__device__ __forceinline__ int unit_count(const AttnArgs& a, int m) {
+  return static_cast<int>((static_cast<int64_t>(m) * a.g + kUnitRows - 1) / kUnitRows);
+}
+__device__ __forceinline__ Span unit_span(const AttnArgs& a, const Seq& s, int rt) {
+  const int64_t r0 = static_cast<int64_t>(rt) * kUnitRows, total = static_cast<int64_t>(s.m) * a.g;
+  const int64_t r1 = min(r0 + kUnitRows, total) - 1;
+  return span_of<kKT>(a, s, static_cast<int>(r0 / a.g), static_cast<int>(r1 / a.g) + 1);
+}
+__device__ __forceinline__ void open_unit(const AttnArgs& a, Walk& w) {
+  w.sp = unit_span(a, w.s, w.rt);
+  w.rows = static_cast<int>(min(static_cast<int64_t>(kUnitRows),
+                                static_cast<int64_t>(w.s.m) * a.g - static_cast<int64_t>(w.rt) * kUnitRows));
+}
+__device__ __forceinline__ void open_segment(Walk& w) {
+  w.nt = static_cast<int>(min(w.left, static_cast<int64_t>(w.sp.n - w.t0)));
+  w.left -= w.nt;
+}
+// The next unit; only called while w.left > 0, so there is one.
+__device__ __forceinline__ void next_segment(const AttnArgs& a, Walk& w) {
+  w.unit0 += w.sp.n;
+  w.t0 = 0;
+  if (++w.h == a.Hkv) {
+    w.h = 0;
+    if (++w.rt >= unit_count(a, w.s.m)) {
+      w.rt = 0;
+      do {
+        ++w.b;
+        if (w.b < a.n) w.s = load_seq(a, w.b);
+      } while (w.b < a.n && w.s.m == 0);
+    }
+    open_unit(a, w);
+  }
+  open_segment(w);
+}
+
+// Scores and values of the segment formed again, token by token, for the 32
+// columns from d0: what the matrix product must not be used for.
+__device__ __noinline__ void row_by_row(const AttnArgs& a, const Walk& w, const __nv_bfloat16* q, int pos, int d0,
+                                        float* acc, float* ml) {
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+  const int32_t* row = a.table + static_cast<int64_t>(w.s.id) * a.max_pages;
+  for (int t = w.t0; t < w.t0 + w.nt; ++t) {
+    const int tile0 = w.sp.tile(t) * kKT;
+    for (int j = tile0; j < tile0 + kKT; ++j) {
+      const int back = pos - j;
+      if (!q || back < 0 || (a.window > 0 && back >= a.window && j >= a.sinks)) continue;
+      const int p = __ldg(row + (j >> a.page_shift));
+      if (p < 0 || p >= a.n_pages) continue;
+      const int64_t tok =
+          ((((static_cast<int64_t>(p) * a.Hkv + w.h) << a.page_shift) + (j & ((1 << a.page_shift) - 1)))) * a.D;
+      const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + tok;
+      const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + tok;
+      float s = 0.f;
+      for (int d = 0; d < a.D; ++d) s += __bfloat162float(q[d]) * __bfloat162float(k[d]);
+      s *= a.scale_log2;
+      const float mn = fmaxf(m, s), mu = mn == -INFINITY ? 0.f : mn;
+      const float f = ex2(m - mu), e = ex2(s - mu);
+      m = mn;
+      l = l * f + e;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (d0 + i < a.D) acc[i] = acc[i] * f + e * __bfloat162float(v[d0 + i]);
+    }
+  }
+  ml[0] = m;
+  ml[1] = l;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, AttnArgs a,
+                   long long wait_cycles) {
+  using C = Cfg<DP>;
+  extern __shared__ unsigned char smraw[];
+  const uint32_t sbase = (su32(smraw) + 1023u) & ~1023u;
+  const uint32_t sq = sbase, sk = sbase + 2 * C::kTile, sv = sk + C::kKS * C::kTile;
+  // kf/ke, vf/ve: full and empty slots of the rings; vr: V checked;
+  // qr: Q tile ready; sr: scores ready; pr: numerators ready; of: O final
+  __shared__ uint64_t b_kf[C::kKS], b_ke[C::kKS], b_vf[C::kVS], b_ve[C::kVS], b_vr[C::kVS];
+  __shared__ uint64_t b_qr[2], b_sr[2], b_pr[2], b_of[2], b_drain;
+  __shared__ uint32_t tmem_holder;
+  __shared__ int s_abort;
+  __shared__ uint32_t s_poison[8];  // ring over units: number + 1 of a unit with an infinity or NaN to hide
+  __shared__ int64_t s_scan[kThreads / 32];
+  __shared__ int s_first[kThreads];
+  __shared__ Walk s_walk;
+  volatile int* abort_flag = &s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // ---- this CTA's run. Units are counted sequence block by sequence block;
+  // a unit's length follows from its last token's position.
+  auto scan = [&](int64_t v, int64_t* total) -> int64_t {  // exclusive prefix over the block
+    int64_t x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(~0u, x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    int64_t base = 0, all = 0;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) base += s_scan[i];
+      all += s_scan[i];
+    }
+    __syncthreads();
+    *total = all;
+    return base + x - v;
+  };
+  // visit(b, rt, span length, line position) for every unit row, in parallel
+  auto visit_units = [&](auto&& f) -> int64_t {
+    int64_t line = 0;
+    for (int b0 = 0; b0 < a.n; b0 += kThreads) {
+      const int b = b0 + tid;
+      int64_t units;
+      const int64_t mine = b < a.n ? unit_count(a, chunk_rows(a, b)) : 0;
+      const int64_t first = scan(mine, &units);
+      s_first[tid] = static_cast<int>(first);
+      __syncthreads();
+      for (int64_t u0 = 0; u0 < units; u0 += kThreads) {
+        const int64_t u = u0 + tid;
+        int n = 0, sb = 0, rt = 0;
+        if (u < units) {
+          int lo = 0, hi = min(kThreads, a.n - b0);
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_first[mid] <= u)
+              lo = mid;
+            else
+              hi = mid;
+          }
+          sb = b0 + lo;
+          rt = static_cast<int>(u - s_first[lo]);
+          n = unit_span(a, load_seq(a, sb), rt).n;
+        }
+        int64_t all;
+        const int64_t at = line + scan(static_cast<int64_t>(n) * a.Hkv, &all);
+        if (n > 0) f(sb, rt, n, at);
+        line += all;
+      }
+      __syncthreads();
+    }
+    return line;
+  };
+  const int64_t total = visit_units([](int, int, int, int64_t) {});
+  const int64_t G = min(static_cast<int64_t>(gridDim.x), total);
+  if (blockIdx.x >= G) return;
+  const int64_t run0 = total * blockIdx.x / G, run1 = total * (blockIdx.x + 1) / G;
+  visit_units([&](int b, int rt, int n, int64_t at) {
+    if (run0 >= at && run0 < at + static_cast<int64_t>(n) * a.Hkv) {
+      Walk w;
+      w.b = b;
+      w.rt = rt;
+      w.h = static_cast<int>((run0 - at) / n);
+      w.t0 = static_cast<int>((run0 - at) % n);
+      w.unit0 = run0 - w.t0;
+      w.left = run1 - run0;
+      w.s = load_seq(a, b);
+      open_unit(a, w);
+      open_segment(w);
+      s_walk = w;
+    }
+  });
+
+  if (tid == 0) {
+    s_abort = 0;
+    for (int i = 0; i < C::kKS; ++i) {
+      mbar_init(su32(&b_kf[i]), 1);
+      mbar_init(su32(&b_ke[i]), 1);
+    }
+    for (int i = 0; i < C::kVS; ++i) {
+      mbar_init(su32(&b_vf[i]), 1);
+      mbar_init(su32(&b_ve[i]), 1);
+      mbar_init(su32(&b_vr[i]), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(su32(&b_qr[t]), 4);
+      mbar_init(su32(&b_sr[t]), 1);
+      mbar_init(su32(&b_pr[t]), 4);
+      mbar_init(su32(&b_of[t]), 1);
+    }
+    mbar_init(su32(&b_drain), 1);
+    for (int i = 0; i < 8; ++i) s_poison[i] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_holder)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_holder;
+  Walk w = s_walk;
+
+  if (warp == 8) {
+    // ---------------- TMA: lane i copies page i of the tile (its 64-column
+    // halves); pages that no row sees are left out
+    const int boxr = min(1 << a.page_shift, kKT), per = kKT / boxr;
+    RingPos kp, vp;
+    uint32_t nk = 0, nv = 0;  // tiles issued
+    bool ok = true;
+    while (ok) {
+      const int32_t* row = a.table + static_cast<int64_t>(w.s.id) * a.max_pages;
+      for (int i = 0; i < w.nt && ok; ++i) {
+        const int tok = w.sp.tile(w.t0 + i) * kKT + lane * boxr;
+        bool need = lane < per && tok < w.sp.end && (tok < a.sinks || tok + boxr > w.sp.low);
+        int page = 0;
+        if (need) {
+          page = __ldg(row + (tok >> a.page_shift));
+          if (page < 0 || page >= a.n_pages) {
+            atomicOr(a.err, MOE_DEVERR_BADIDX);
+            need = false;
+          }
+        }
+        const uint32_t bytes = __popc(__ballot_sync(~0u, need)) * static_cast<uint32_t>(boxr) * 128u * (DP / 64);
+        const int y = tok & ((1 << a.page_shift) - 1), z = page * a.Hkv + w.h;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          RingPos& rp = kv ? vp : kp;
+          uint32_t& n = kv ? nv : nk;
+          const uint32_t slots = kv ? C::kVS : C::kKS;
+          const uint32_t full = su32(kv ? &b_vf[rp.s] : &b_kf[rp.s]);
+          if (n >= slots && !mbar_wait(su32(kv ? &b_ve[rp.s] : &b_ke[rp.s]), rp.ph ^ 1u, abort_flag, a.err, wait_cycles))
+            ok = false;
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(full, bytes);  // without pages the barrier completes by this arrival
+          __syncwarp();
+          if (need) {
+            const uint32_t dst = (kv ? sv : sk) + rp.s * C::kTile + lane * boxr * 128u;
+#pragma unroll
+            for (int hf = 0; hf < DP / 64; ++hf) tma3d(dst + hf * C::kHalf, kv ? &map_v : &map_k, full, hf * 64, y, z);
+          }
+          __syncwarp();
+          ++n;
+          rp.next(slots);
+        }
+      }
+      if (*abort_flag) ok = false;
+      ok = __all_sync(~0u, ok) && w.left > 0;
+      if (ok) next_segment(a, w);
+    }
+    // drain: copies in flight land before the CTA ends
+    if (lane == 0) {
+      for (uint32_t j = 0; j < nk && j < C::kKS; ++j)
+        mbar_drain(su32(&b_kf[(nk - 1 - j) % C::kKS]), ((nk - 1 - j) / C::kKS) & 1u, a.err, wait_cycles);
+      for (uint32_t j = 0; j < nv && j < C::kVS; ++j)
+        mbar_drain(su32(&b_vf[(nv - 1 - j) % C::kVS]), ((nv - 1 - j) / C::kVS) & 1u, a.err, wait_cycles);
+    }
+  } else if (warp == 9) {
+    // ---------------- MMA issue
+    if (lane == 0) {
+      const uint32_t id_qk = (1u << 4) | (1u << 7) | (1u << 10) | ((kKT >> 3) << 17) | ((kQT >> 4) << 24);
+      const uint32_t id_pv = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((DP >> 3) << 17) | ((kQT >> 4) << 24);
+      RingPos kp, vp;
+      uint32_t q_ph = 0;            // units seen by row tile 0; tile 1 counts its own
+      uint32_t q_ph1 = 0;
+      uint32_t p_ph[2] = {0, 0};
+      bool ok = true;
+      auto wait = [&](uint64_t* b, uint32_t ph) { return mbar_wait(su32(b), ph, abort_flag, a.err, wait_cycles); };
+      auto qk = [&](int t) {
+        const uint64_t qa = sdesc(sq + t * C::kTile), kb = sdesc(sk + kp.s * C::kTile);
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint32_t off = (k >> 2) * (C::kHalf >> 4) + (k & 3) * 2;
+          umma_ss(tmem + C::kTmemS + t * 128u, qa + off, kb + off, id_qk, k > 0);
+        }
+        umma_commit(su32(&b_sr[t]));
+      };
+      while (ok) {
+        const int nq = w.rows > kQT ? 2 : 1;
+        if (!(ok = wait(&b_kf[kp.s], kp.ph))) break;
+        for (int t = 0; t < nq && ok; ++t) {
+          uint32_t& ph = t ? q_ph1 : q_ph;
+          if (!(ok = wait(&b_qr[t], ph))) break;
+          ph ^= 1u;
+          fence_after();
+          qk(t);
+        }
+        if (!ok) break;
+        umma_commit(su32(&b_ke[kp.s]));
+        kp.next(C::kKS);
+        for (int j = 0; j < w.nt && ok; ++j) {
+          const bool more = j + 1 < w.nt;
+          for (int t = 0; t < nq; ++t) {
+            if (!(ok = wait(&b_pr[t], p_ph[t]))) break;
+            p_ph[t] ^= 1u;
+            if (t == 0 && !(ok = wait(&b_vr[vp.s], vp.ph))) break;
+            fence_after();
+            const uint64_t vb = sdesc_mn(sv + vp.s * C::kTile, C::kHalf);
+#pragma unroll
+            for (int k = 0; k < kKT / 16; ++k)
+              umma_ts(tmem + C::kTmemO + t * static_cast<uint32_t>(DP), tmem + C::kTmemS + t * 128u + 8u * k,
+                      vb + k * (2048u >> 4), id_pv, k > 0 || j > 0);
+            if (more) {
+              if (t == 0 && !(ok = wait(&b_kf[kp.s], kp.ph))) break;
+              qk(t);
+            } else {
+              umma_commit(su32(&b_of[t]));
+            }
+          }
+          if (!ok) break;
+          umma_commit(su32(&b_ve[vp.s]));
+          vp.next(C::kVS);
+          if (more) {
+            umma_commit(su32(&b_ke[kp.s]));
+            kp.next(C::kKS);
+          }
+        }
+        if (w.left == 0 || *abort_flag) break;
+        if (ok) next_segment(a, w);
+      }
+      // drain: every MMA issued here is done before tensor memory is released
+      umma_commit(su32(&b_drain));
+      mbar_drain(su32(&b_drain), 0, a.err, wait_cycles);
+    }
+  } else if (warp == 10) {
+    // ---------------- V check
+    RingPos vp;
+    bool ok = true;
+    for (uint32_t unit = 0; ok; ++unit) {
+      const int lo_pos = w.s.len - w.s.m + static_cast<int>(static_cast<int64_t>(w.rt) * kUnitRows / a.g);
+      const int hi_pos = w.sp.end - 1;
+      for (int i = 0; i < w.nt; ++i) {
+        ok = mbar_wait(su32(&b_vf[vp.s]), vp.ph, abort_flag, a.err, wait_cycles);
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        const int tile0 = w.sp.tile(w.t0 + i) * kKT;
+        if (tile0 + kKT - 1 > lo_pos || (a.window > 0 && hi_pos - tile0 >= a.window)) {
+          const uint32_t st = sv + vp.s * C::kTile;
+          bool bad = false;
+          // rows of 128 bytes, halves one after the other: 8 pieces a row
+          for (int e = lane; e < kKT * 8 * (DP / 64); e += 32) {
+            const int j = tile0 + ((e >> 3) & (kKT - 1));
+            if (j >= w.sp.end || (j >= a.sinks && j < w.sp.low)) {
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(st + e * 16), "r"(0) : "memory");
+            } else {
+              uint32_t v[4];
+              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                           : "r"(st + e * 16)
+                           : "memory");
+              bad |= nonfinite2(v[0]) || nonfinite2(v[1]) || nonfinite2(v[2]) || nonfinite2(v[3]);
+            }
+          }
+          if (bad) *const_cast<volatile uint32_t*>(&s_poison[unit & 7]) = unit + 1;
+          fence_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(su32(&b_vr[vp.s]));
+        vp.next(C::kVS);
+      }
+      if (!ok || w.left == 0) break;
+      next_segment(a, w);
+    }
+  } else if (warp < 8) {
+    // ---------------- softmax: one thread a row
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane;  // row tile, row
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + C::kTmemS + t * 128u + lanes, to = tmem + C::kTmemO + t * static_cast<uint32_t>(DP) + lanes;
+    const float c = a.scale_log2, raise = kRaise / c;
+    uint32_t s_ph = 0, o_ph = 0;
+    bool ok = true;
+    for (uint32_t unit = 0; ok; ++unit) {
+      if (t * kQT < w.rows) {
+        // Q: this thread's row, swizzled as TMA would; rows past the end are zero
+        const int64_t rg = static_cast<int64_t>(w.rt) * kUnitRows + t * kQT + r;
+        const bool row_ok = t * kQT + r < w.rows;
+        const int i = static_cast<int>(rg / a.g), hq = static_cast<int>(rg - static_cast<int64_t>(i) * a.g);
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(w.s.row0) + i) * a.ldq +
+                                 static_cast<int64_t>(w.h * a.g + hq) * a.D;
+#pragma unroll
+        for (int p = 0; p < DP / 8; ++p) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (row_ok && p * 8 < a.D) v = __ldg(reinterpret_cast<const uint4*>(q) + p);
+          const uint32_t dst = sq + t * C::kTile + (p >> 3) * C::kHalf + r * 128u + (((p & 7) ^ (r & 7)) << 4);
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                       : "memory");
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(su32(&b_qr[t]));
+
+        const int pos = row_ok ? w.s.len - w.s.m + i : -1;
+        // positions of the warp's rows, for the tiles that need no mask
+        const int64_t r0 = static_cast<int64_t>(w.rt) * kUnitRows + t * kQT + (warp & 3) * 32;
+        const int lo_pos = w.s.len - w.s.m + static_cast<int>(r0 / a.g);
+        const int64_t r_last = min(r0 + 31, static_cast<int64_t>(w.s.m) * a.g - 1);
+        const int hi_pos = w.s.len - w.s.m + static_cast<int>(r_last / a.g);
+        float m = -INFINITY, l = 0.f;
+        for (int j = 0; j < w.nt; ++j) {
+          ok = mbar_wait(su32(&b_sr[t]), s_ph, abort_flag, a.err, wait_cycles);
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+          s_ph ^= 1u;
+          fence_after();
+          const int tile0 = w.sp.tile(w.t0 + j) * kKT;
+          const bool edge = tile0 + kKT - 1 > lo_pos || (a.window > 0 && hi_pos - tile0 >= a.window);
+          const int last = pos - tile0;                              // columns after it are hidden
+          const int from = a.window > 0 ? last - a.window + 1 : -1;  // columns before it are hidden, but for
+          const int keep = a.sinks - tile0;                          // the first `keep`
+          auto hide = [&](float* s, int x0) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (x0 + x > last || (x0 + x < from && x0 + x >= keep)) s[x] = -INFINITY;
+          };
+          // the scores are read twice, first for the maximum: holding all 128
+          // would take more registers than a thread has
+          float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < 128; x += 64) {
+            float s[64];
+            tmem_ld32_async(ts + x, s);
+            tmem_ld32_async(ts + x + 32, s + 32);
+            tmem_wait_ld();
+            if (edge) {
+              hide(s, x);
+              hide(s + 32, x + 32);
+            }
+#pragma unroll
+            for (int y = 0; y < 64; y += 4) {
+              mx0 = fmaxf(mx0, s[y]);
+              mx1 = fmaxf(mx1, s[y + 1]);
+              mx2 = fmaxf(mx2, s[y + 2]);
+              mx3 = fmaxf(mx3, s[y + 3]);
+            }
+          }
+          const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+          const bool up = mx > m + raise || (m == -INFINITY && mx > m);
+          if (__any_sync(~0u, up)) {
+            const float mn = up ? mx : m;
+            const float f = up ? ex2((m - mn) * c) : 1.f;  // 0 for the first maximum
+            m = mn;
+            l *= f;
+            if (j > 0) {
+#pragma unroll 1
+              for (int x = 0; x < DP; x += 16) {
+                float o[16];
+                tmem_ld16_async(to + x, o);
+                tmem_wait_ld();
+                uint32_t u[16];
+#pragma unroll
+                for (int y = 0; y < 16; ++y) u[y] = __float_as_uint(o[y] * f);
+                tmem_st16(to + x, u);
+              }
+              tmem_wait_st();
+            }
+          }
+          const float mc = m == -INFINITY ? 0.f : m * c;
+          const unsigned long long c2 = pack2(c, c), m2 = pack2(-mc, -mc);
+          unsigned long long l0 = 0ull, l1 = 0ull;
+          float sb[2][32];
+          tmem_ld32_async(ts, sb[0]);
+#pragma unroll
+          for (int x = 0; x < 128; x += 32) {
+            float* s = sb[(x >> 5) & 1];
+            tmem_wait_ld();
+            if (x < 96) tmem_ld32_async(ts + x + 32, sb[((x >> 5) & 1) ^ 1]);
+            if (edge) hide(s, x);
+            uint32_t p[16];
+#pragma unroll
+            for (int y = 0; y < 32; y += 4) {
+              const float2 u = unpack2(fma2(pack2(s[y], s[y + 1]), c2, m2));
+              const float2 v = unpack2(fma2(pack2(s[y + 2], s[y + 3]), c2, m2));
+              const float e0 = ex2(u.x), e1 = ex2(u.y), e2 = ex2(v.x), e3 = ex2(v.y);
+              // the sum takes the numerators before their rounding to bf16
+              l0 = add2(l0, pack2(e0, e1));
+              l1 = add2(l1, pack2(e2, e3));
+              p[y / 2] = pack_bf16(e0, e1);
+              p[y / 2 + 1] = pack_bf16(e2, e3);
+            }
+            tmem_st16(ts + x / 2, p);  // over scores already read
+          }
+          const float2 la = unpack2(add2(l0, l1));
+          l += la.x + la.y;
+          tmem_wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(su32(&b_pr[t]));
+        }
+        if (!ok) break;
+        ok = mbar_wait(su32(&b_of[t]), o_ph, abort_flag, a.err, wait_cycles);
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        o_ph ^= 1u;
+        fence_after();
+        if (*const_cast<volatile uint32_t*>(&s_poison[unit & 7]) == unit + 1) {
+          const Walk seg = w;
+          float ml[2];
+#pragma unroll 1
+          for (int x = 0; x < DP; x += 32) {
+            float o[32];
+            row_by_row(a, seg, row_ok ? q : nullptr, pos, x, o, ml);
+            __syncwarp();
+            uint32_t u[32];
+#pragma unroll
+            for (int y = 0; y < 32; ++y) u[y] = __float_as_uint(o[y]);
+            tmem_st16(to + x, u);
+            tmem_st16(to + x + 16, u + 16);
+          }
+          m = ml[0] / c;  // back to the unit of the scores
+          l = ml[1];
+          tmem_wait_st();
+        }
+        // ---- results of the segment
+        const bool seen = pos >= 0;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (static_cast<int64_t>(w.s.row0) + i) * a.ldo +
+                             static_cast<int64_t>(w.h * a.g + hq) * a.D;
+        const bool whole = w.whole();
+        float* part = nullptr;
+        if (!whole) {
+          const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (run0 >= w.unit0 ? 0 : 1)) * 2 + t;
+          part = a.part + slot * C::kPart;
+          *reinterpret_cast<float4*>(part + r * 4) = make_float4(m, l, 0.f, 0.f);
+        }
+        const float inv = 1.f / l;  // no weight at all on what is seen: 0/0
+#pragma unroll 1
+        for (int x = 0; x < DP; x += 32) {
+          float o[32];
+          tmem_ld32_async(to + x, o);
+          tmem_wait_ld();
+          if (whole) {
+#pragma unroll
+            for (int y = 0; y < 32; y += 8) {
+              if (!row_ok || x + y >= a.D) continue;
+              uint4 v;
+              v.x = pack_bf16(seen ? o[y] * inv : 0.f, seen ? o[y + 1] * inv : 0.f);
+              v.y = pack_bf16(seen ? o[y + 2] * inv : 0.f, seen ? o[y + 3] * inv : 0.f);
+              v.z = pack_bf16(seen ? o[y + 4] * inv : 0.f, seen ? o[y + 5] * inv : 0.f);
+              v.w = pack_bf16(seen ? o[y + 6] * inv : 0.f, seen ? o[y + 7] * inv : 0.f);
+              *reinterpret_cast<uint4*>(out + x + y) = v;
+            }
+          } else {
+#pragma unroll
+            for (int y = 0; y < 32; y += 4)
+              *reinterpret_cast<float4*>(part + kQT * 4 + ((x + y) / 4 * kQT + r) * 4) =
+                  make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+          }
+        }
+        if (!whole) {
+          auto cta_of = [&](int64_t tile) {  // the c with total*c/G <= tile < total*(c+1)/G
+            int64_t x = tile * G / total;
+            while (total * x / G > tile) --x;
+            while (total * (x + 1) / G <= tile) ++x;
+            return x;
+          };
+          const int64_t c0 = cta_of(w.unit0), c1 = cta_of(w.unit0 + w.sp.n - 1);
+          // one ticket a warp: its 32 rows of the unit that starts in c0's run
+          unsigned int* ticket = a.tickets + c0 * 8 + warp;
+          __threadfence();
+          __syncwarp();
+          unsigned int done = 0;
+          if (lane == 0) done = atomicAdd(ticket, 1u);
+          done = __shfl_sync(~0u, done, 0);
+          if (done == static_cast<unsigned int>(c1 - c0)) {
+            if (lane == 0) *ticket = 0u;  // zero between launches
+            __threadfence();
+            auto part_of = [&](int64_t x) {
+              return a.part + ((2 * x + (total * x / G >= w.unit0 ? 0 : 1)) * 2 + t) * C::kPart;
+            };
+            float M = -INFINITY, L = 0.f;
+            for (int64_t x = c0; x <= c1; ++x) M = fmaxf(M, __ldcg(part_of(x) + r * 4));
+            const float Mu = M == -INFINITY ? 0.f : M;
+            for (int64_t x = c0; x <= c1; ++x) {
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_of(x) + r * 4));
+              L += ex2((ml.x - Mu) * c) * ml.y;
+            }
+            const float inv_l = 1.f / L;
+#pragma unroll 1
+            for (int y = 0; y < DP; y += 8) {
+              float o[8] = {};
+              for (int64_t x = c0; x <= c1; ++x) {
+                const float* p = part_of(x);
+                const float f = ex2((__ldcg(p + r * 4) - Mu) * c);
+                const float4 u = __ldcg(reinterpret_cast<const float4*>(p + kQT * 4 + (y / 4 * kQT + r) * 4));
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(p + kQT * 4 + ((y / 4 + 1) * kQT + r) * 4));
+                o[0] += f * u.x, o[1] += f * u.y, o[2] += f * u.z, o[3] += f * u.w;
+                o[4] += f * v.x, o[5] += f * v.y, o[6] += f * v.z, o[7] += f * v.w;
+              }
+              if (!row_ok || y >= a.D) continue;
+              uint4 v;
+              v.x = pack_bf16(seen ? o[0] * inv_l : 0.f, seen ? o[1] * inv_l : 0.f);
+              v.y = pack_bf16(seen ? o[2] * inv_l : 0.f, seen ? o[3] * inv_l : 0.f);
+              v.z = pack_bf16(seen ? o[4] * inv_l : 0.f, seen ? o[5] * inv_l : 0.f);
+              v.w = pack_bf16(seen ? o[6] * inv_l : 0.f, seen ? o[7] * inv_l : 0.f);
+              *reinterpret_cast<uint4*>(out + y) = v;
+            }
+          }
+        }
+        // the next unit's products overwrite O only after this read
+        fence_before();
+      }
+      if (*abort_flag || w.left == 0) break;
+      next_segment(a, w);
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+template <int DP>
+cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  const int page = 1 << a.page_shift;
+  cudaError_t e;
+  if ((e = map_pages(&mk, a.k, a.D, page, static_cast<int64_t>(a.n_pages) * a.Hkv, std::min(page, kKT))) != cudaSuccess ||
+      (e = map_pages(&mv, a.v, a.D, page, static_cast<int64_t>(a.n_pages) * a.Hkv, std::min(page, kKT))) != cudaSuccess)
+    return e;
+  e = cudaFuncSetAttribute(prefill_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DP>::kSmem);
+  if (e != cudaSuccess) return e;
+  prefill_kernel<DP><<<num_sms, kThreads, Cfg<DP>::kSmem, st>>>(mk, mv, a, kPrefillWaitCycles);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_prefill_tc(const AttnArgs& a, int num_sms, cudaStream_t st) {
+  cudaError_t e = encoder();
+  if (e != cudaSuccess) return e;
+  return a.D <= 64 ? launch<64>(a, num_sms, st) : launch<128>(a, num_sms, st);
+}
+
+}  // namespace moe

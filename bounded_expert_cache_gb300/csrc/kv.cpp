@@ -44,8 +44,9 @@ const char* bad_geometry(const moe_kv_t& a) {
   if (a.head_dim < 8 || a.head_dim > 256 || a.head_dim % 8) return "head_dim is not a multiple of 8 in 8..256";
   if (a.n_kv_heads > 1024) return "n_kv_heads above 1024";
   if (a.max_seqs < 1 || a.max_seqs > 65536) return "max_seqs outside 1..65536";
-  if (a.max_pages < 1 || static_cast<int64_t>(a.max_pages) * a.page_tokens > 0x7FFFFFFFll - 256)
-    return "max_pages < 1 or max_pages * page_tokens too large";
+  if (a.max_pages < 1 || static_cast<int64_t>(a.max_pages) * a.page_tokens > 1ll << 30)
+    return "max_pages < 1 or max_pages * page_tokens above 2^30";
+  if (static_cast<int64_t>(a.n_pages) * a.n_kv_heads > 0x7FFFFFFFll) return "n_pages * n_kv_heads above 2^31 - 1";
   return nullptr;
 }
 
@@ -87,7 +88,7 @@ moe_status_t attention(const char* call, bool decode, const moe_kv_t* kv, int32_
   if (!seqs && n > kv->max_seqs) return fail(MOE_ERR_ARG, call, "n above max_seqs without seqs");
   if (n_heads < 1 || n_heads % kv->n_kv_heads || n_heads / kv->n_kv_heads > 64)
     return fail(MOE_ERR_ARG, call, "n_heads is not a multiple of n_kv_heads, or above 64 times as many");
-  if (!std::isfinite(scale)) return fail(MOE_ERR_ARG, call, "scale is not finite");
+  if (!std::isfinite(scale) || !(scale > 0.f)) return fail(MOE_ERR_ARG, call, "scale is not finite and positive");
   if (window < 0 || sinks < 0) return fail(MOE_ERR_ARG, call, "window or sinks < 0");
   const int32_t rows = decode ? n * n_q : n_rows;
   if (n == 0 || rows == 0) return MOE_OK;
@@ -97,6 +98,7 @@ moe_status_t attention(const char* call, bool decode, const moe_kv_t* kv, int32_
   if (!aligned16(q) || !aligned16(out) || ldq % per || ldo % per)
     return fail(MOE_ERR_ARG, call, "rows of q or out are not 16-byte aligned");
   if (ldq < width || ldo < width) return fail(MOE_ERR_ARG, call, "ldq or ldo is smaller than a row");
+  if (!decode && rows > 1 << 30) return fail(MOE_ERR_ARG, call, "n_rows above 2^30");
   // one CTA's index space of the prefill grid
   if (!decode && (static_cast<int64_t>(rows) * (n_heads / kv->n_kv_heads) / 16 + n + 1) * kv->n_kv_heads > 0x7FFFFFFFll)
     return fail(MOE_ERR_ARG, call, "too many rows for one call");
@@ -125,8 +127,10 @@ moe_status_t attention(const char* call, bool decode, const moe_kv_t* kv, int32_
   a.max_seqs = kv->max_seqs;
   a.n_pages = kv->n_pages;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.window = window;
-  a.sinks = sinks;
+  // a window that no row's past exceeds hides nothing
+  const int32_t most = kv->max_pages * kv->page_tokens;
+  a.window = window >= most ? 0 : window;
+  a.sinks = std::min(sinks, most);
   char* w = static_cast<char*>(kv->work);
   a.part = reinterpret_cast<float*>(w + l.part);
   a.tickets = reinterpret_cast<unsigned int*>(w + l.tickets);
@@ -154,10 +158,11 @@ KvLayout kv_layout(const moe_kv_t& kv, int num_sms) {
   l.filled = take(kMaxList * 4ll);
   l.shr = take(kv.n_pages * 4ll);
   l.last = take(kv.n_pages * 4ll);
-  l.tickets = take(num_sms * 4ll);
+  l.tickets = take(num_sms * kPrefillTickets * 4ll);
   // two partial results a CTA: rows of (m, l, -, -, head size padded)
   const int64_t dp = kv.head_dim <= 64 ? 64 : (kv.head_dim <= 128 ? 128 : 256);
-  l.part = take(2ll * num_sms * kPartRows * (dp + 4) * 4);
+  const bool tc = kv.dtype == MOE_BF16 && kv.head_dim <= kTcHeadDim;
+  l.part = take(2ll * num_sms * (tc ? kPrefillPartRows : kPartRows) * (dp + 4) * 4);
   l.bytes = at;
   return l;
 }
@@ -190,7 +195,12 @@ extern "C" moe_status_t moe_kv_check_errors(const moe_kv_t* kv, moe_stream_t str
     if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof(err), stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_fail(call, e);
-    if (err & MOE_DEVERR_TIMEOUT) return fail(MOE_ERR_TIMEOUT, call, "a bounded device wait ran out");
+    if (err & MOE_DEVERR_TIMEOUT) {
+      // units left unjoined have left their tickets behind
+      e = cudaMemsetAsync(static_cast<char*>(kv->work) + l.tickets, 0, sms * moe::kPrefillTickets * 4, stream);
+      if (e != cudaSuccess) return cuda_fail(call, e);
+      return fail(MOE_ERR_TIMEOUT, call, "a bounded device wait ran out");
+    }
     if (err & MOE_DEVERR_BADIDX)
       return fail(MOE_ERR_ARG, call, "a sequence or page id out of range or listed twice, or a fork into a sequence "
                                      "that holds tokens");

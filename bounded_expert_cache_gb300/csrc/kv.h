@@ -22,7 +22,10 @@ struct KvWork {
   int32_t n_live;     // pages in use, of the last compact
   int32_t pad[61];
 };
-constexpr int kPartRows = 64;        // most rows of one partial result
+constexpr int kPartRows = 64;        // most rows of one partial result (decode)
+constexpr int kPrefillTickets = 8;   // tickets a CTA (prefill; decode uses one)
+constexpr int kPrefillPartRows = 256;
+constexpr int kTcHeadDim = 128;      // largest head size of the tensor-core prefill
 
 struct KvLayout {
   // byte offsets into the scratch: page lists (src, dst, map, shr, last: one
@@ -53,6 +56,8 @@ struct AttnArgs {
 };
 cudaError_t launch_attn_decode(const AttnArgs& a, int32_t dtype, int num_sms, cudaStream_t st);
 cudaError_t launch_attn_prefill(const AttnArgs& a, int32_t dtype, int32_t n_rows, int num_sms, cudaStream_t st);
+
+cudaError_t launch_attn_prefill_tc(const AttnArgs& a, int num_sms, cudaStream_t st);
 
 cudaError_t launch_kv_fork(const moe_kv_t& kv, const KvLayout& l, const int32_t* src, const int32_t* dst, int32_t n,
                            cudaStream_t st);

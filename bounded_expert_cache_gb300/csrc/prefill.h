@@ -83,6 +83,9 @@ cudaError_t encoder();
 // 8): boxes of 64 columns x box_rows rows, 128-byte swizzle.
 cudaError_t map16(CUtensorMap* m, const void* base, CUtensorMapDataType t, int64_t rows, int64_t cols,
                   int box_rows);
+// bf16 cache pages of one layer: D x page tokens x (page, head) blocks, boxes
+// of 64 columns x box_rows tokens, 128-byte swizzle.
+cudaError_t map_pages(CUtensorMap* m, const void* base, int D, int page, int64_t blocks, int box_rows);
 
 int gemm_stages(int phase);
 size_t gemm_smem_bytes(int phase, int stages);

@@ -43,7 +43,7 @@ typedef struct {
   int32_t head_dim;    /* multiple of 8, 8..256 */
   int32_t dtype;       /* moe_dtype_t of k and v, and of q, out and new tokens */
   int32_t max_seqs;    /* 1..65536 */
-  int32_t max_pages;   /* most pages of one sequence; max_pages * page_tokens < 2^31 */
+  int32_t max_pages;   /* most pages of one sequence; max_pages * page_tokens <= 2^30 */
 } moe_kv_t;
 
 /* Scratch bytes of a cache of this geometry on the current device (the
@@ -125,7 +125,7 @@ moe_status_t moe_kv_copy_pages(const moe_kv_t* kv, const int32_t* src, const int
  * moe_attn_prefill: chunks of any length; rows cu[i] .. cu[i+1]-1 (device
  * int32 [n+1], cu[n] = n_rows) are the newest tokens of seqs[i].
  *
- * seqs may be NULL: sequences 0 .. n-1. n_heads must be a multiple of
+ * scale must be positive. seqs may be NULL: sequences 0 .. n-1. n_heads must be a multiple of
  * n_kv_heads, at most 64 times as many. */
 moe_status_t moe_attn_decode(const moe_kv_t* kv, int32_t layer, const void* q, int64_t ldq, const int32_t* seqs,
                              int32_t n, int32_t n_q, int32_t n_heads, float scale, int32_t window, int32_t sinks,
