@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(AttnArgs a) {
 
   // ---- this CTA's run [first, last) of the line
   Cursor ld;
-  int64_t todo = 0, run0 = 0, unit0 = 0, total = 0, G = 1;
+  int64_t todo = 0, run0 = 0, unit0 = 0, total = 1;
   if (SPLIT) {
     auto tiles_of = [&](int b) -> int64_t {
       Seq s = load_seq(a, b);
@@ -605,10 +605,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(AttnArgs a) {
       all += t;
     }
     total = all;
-    G = min(static_cast<int64_t>(gridDim.x), total);
-    if (blockIdx.x >= G) return;
-    run0 = total * blockIdx.x / G;
-    todo = total * (blockIdx.x + 1) / G - run0;
+    const Runs runs(total, gridDim.x);
+    if (blockIdx.x >= runs.n) return;
+    run0 = runs.start(blockIdx.x);
+    todo = runs.start(blockIdx.x + 1) - run0;
     int64_t base = 0;
     for (int b0 = 0; b0 < a.n; b0 += kThreads) {
       if (a.n > kThreads) mine = b0 + static_cast<int>(threadIdx.x) < a.n ? tiles_of(b0 + threadIdx.x) : 0;
@@ -723,23 +723,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(AttnArgs a) {
         write_out<typename E::T>(a, unit, R, r, col, v, L);
       });
     } else {
-      // partial rows of this CTA: slot 0 if its run starts in this unit, else 1
+      // partial rows of this CTA: slot 0 if its run starts inside the unit, else 1
       constexpr int kPS = E::DP + 4;
       const int64_t kSlot = static_cast<int64_t>(kPartRows) * kPS;
-      float* mine = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (run0 >= unit0 ? 0 : 1)) * kSlot;
+      float* mine = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (run0 > unit0 ? 0 : 1)) * kSlot;
       eng.end(a, unit, merge, s_ml, [&](int r, int col, float4 v, float M, float L) {
         *reinterpret_cast<float4*>(mine + r * kPS + 4 + col) = v;
         if (col == 0) *reinterpret_cast<float2*>(mine + r * kPS) = make_float2(M, L);
       });
       // CTAs that hold a part of this unit: those whose runs meet it
       const int64_t unit1 = unit0 + unit.per;
-      auto cta_of = [&](int64_t tile) {  // the c with total*c/G <= tile < total*(c+1)/G
-        int64_t c = tile * G / total;
-        while (total * c / G > tile) --c;
-        while (total * (c + 1) / G <= tile) ++c;
-        return c;
-      };
-      const int64_t c0 = cta_of(unit0), c1 = cta_of(unit1 - 1);
+      const Runs runs(total, gridDim.x);
+      const int64_t c0 = runs.of(unit0), c1 = runs.of(unit1 - 1);
       __threadfence();
       __syncthreads();
       unsigned int* ticket = a.tickets + c0;  // only one unit can start in c0's run and leave it
@@ -752,9 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(AttnArgs a) {
       if (s_last) {
         __threadfence();
         const int rows = min(R, unit.s.m * a.g - unit.rt * R), c4n = a.D / 4;
-        auto slot_of = [&](int64_t c) {
-          return a.part + (2 * c + (total * c / G >= unit0 ? 0 : 1)) * kSlot;
-        };
+        // only c0's run starts no later than the unit
+        auto slot_of = [&](int64_t c) { return a.part + (2 * c + (c == c0 ? 1 : 0)) * kSlot; };
         for (int e = threadIdx.x; e < rows * c4n; e += kThreads) {
           const int r = e / c4n, col = (e - r * c4n) * 4;
           float M = -INFINITY;

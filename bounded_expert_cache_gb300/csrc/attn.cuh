@@ -64,6 +64,18 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
   return s;
 }
 
+// A line of `total` positions cut into n runs that differ by one at most.
+struct Runs {
+  int64_t n, per, rem;
+  __device__ __forceinline__ Runs(int64_t total, int64_t most) : n(min(total, most)), per(total / n), rem(total - per * n) {}
+  __device__ __forceinline__ int64_t start(int64_t x) const { return x * per + min(x, rem); }
+  // the run that holds a position
+  __device__ __forceinline__ int64_t of(int64_t at) const {
+    const int64_t big = rem * (per + 1);
+    return at < big ? at / (per + 1) : rem + (at - big) / per;
+  }
+};
+
 // Token tiles that rows of query tokens [i0, i1) see: the n0 tiles that hold
 // the first tokens, then tiles lo .. lo + n - n0 - 1. At least one tile, so
 // that every unit is visited and writes its rows.

@@ -17,18 +17,24 @@
 // exponentiated the other's products run. Order of the issuing thread:
 //   QK0(0) QK1(0) | PV0(0) QK0(1) PV1(0) QK1(1) | PV0(1) QK0(2) ...
 // These execute in order, so the barrier of a QK also says that the PV before
-// it is done, and P may share S's columns.
+// it is done, and P may share S's columns. The time from S to the next S of a
+// row tile is its softmax and its two products; the products of the other row
+// tile fit into it. PV starts on the first 64 tokens while the numerators of
+// the others are formed.
 //
-// Warps: 0-3 and 4-7 softmax of row tiles 0 and 1 (they also load Q and write
-// the results), 8 TMA of K and V pages, 9 MMA issue, 10 V check.
+// Warps: 0-3 and 4-7 softmax of row tiles 0 and 1, one thread a row (they also
+// write the results), 8 TMA of K and V pages, 9 MMA issue, 10 and 11 load Q
+// (each a row tile, one unit ahead: Q is free once the unit's last scores are
+// formed) and check V.
 // The V check: a token that only some rows see must not reach the others, but
-// 0 * NaN is NaN in a matrix product. In tiles with such tokens the warp zeroes
-// the tokens that no row sees, and looks for infinities and NaN among the
-// rest; if it finds one, the unit's rows are formed again one by one.
+// 0 * NaN is NaN in a matrix product. In tiles with such tokens the warps zero
+// the tokens that no row sees, and look for infinities and NaN among the
+// rest; if there is one, the unit's rows are formed again one by one.
 //
 // Work split: the token tiles of all units form one line, cut into one equal
 // run per CTA (one CTA per SM), as in the decode kernel: causal units differ in
-// length, and whole units would leave SMs idle in the last wave. A unit cut by
+// length, and whole units would leave SMs idle in the last wave. A unit counts
+// kUnitCost tiles more than it has, for its Q and its results. A unit cut by
 // run ends leaves partial rows (m, l, O), joined by the warp that arrives last,
 // in run order.
 //
@@ -46,9 +52,11 @@ namespace {
 using namespace tc;
 
 constexpr int kThreads = 384;
+constexpr int kSoftWarps = 8;
 constexpr int kKT = 128;      // tokens a tile
 constexpr int kQT = 128;      // rows a row tile
 constexpr int kUnitRows = 2 * kQT;
+constexpr int kUnitCost = 3;   // tiles' worth of time of a unit's Q and results
 constexpr float kRaise = 8.f;  // log2 of the growth that raises m
 
 template <int DP>
@@ -56,9 +64,9 @@ struct Cfg {
   static constexpr uint32_t kHalf = kKT * 128;              // 64 columns of a tile: 128-byte rows
   static constexpr uint32_t kTile = kHalf * (DP / 64);      // a Q, K or V tile
   static constexpr int kKS = DP == 64 ? 4 : 2, kVS = DP == 64 ? 4 : 3;  // ring slots of K and V
-  static constexpr int kSmem = (2 + kKS + kVS) * static_cast<int>(kTile) + 1024;
+  static constexpr int kTiles = (2 + kKS + kVS) * static_cast<int>(kTile);
   static constexpr uint32_t kTmemS = 0, kTmemO = 256;       // columns: S0 S1 O0 O1
-  // partial rows of one row tile: (m, l) then O by column quads
+  // partial rows of one row tile: (m, l, -, -), then O by column quads
   static constexpr int64_t kPart = static_cast<int64_t>(kQT) * (DP + 4);
 };
 
@@ -110,6 +118,20 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// the n lowest bits; none for n <= 0, all for n >= 32
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : ~0u >> (32 - min(n, 32));
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred q; elect.sync _|q, 0xFFFFFFFF; selp.u32 %0, 1, 0, q; }" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // two fp32 lanes an instruction
 __device__ __forceinline__ unsigned long long pack2(float a, float b) {
   unsigned long long v;
@@ -133,17 +155,39 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigne
 }
 
 // A CTA's walk along the line: units (sequence, row tile, cache head) in order,
-// of each the tiles [t0, t0 + nt) that fall into the run.
+// of each the tiles [t0, t0 + nt) that fall into the run. On the line a unit is
+// kUnitCost positions and then one per tile.
 struct Walk {
   int b, rt, h;
   int t0, nt;         // this segment
-  int64_t unit0;      // line position of the unit's first tile
-  int64_t left;       // tiles of the run not yet in a segment
+  int64_t unit0;      // line position of the unit
+  int64_t end;        // end of the run
   Seq s;
   Span sp;
   int rows;           // rows of the unit
-  __device__ __forceinline__ bool whole() const { return t0 == 0 && nt == sp.n; }
+  __device__ __forceinline__ bool whole() const { return nt == sp.n; }
+  __device__ __forceinline__ int64_t tiles0() const { return unit0 + kUnitCost; }
+  __device__ __forceinline__ bool more() const { return tiles0() + sp.n + kUnitCost < end; }
 };
+// Shared memory behind the tiles.
+template <int DP>
+struct Shared {
+  using C = Cfg<DP>;
+  // kf/ke, vf/ve: full and empty slots of the rings; vr: V checked; qr, qe: Q
+  // tile ready, free; sr: scores ready; pa, pb: numerators of the first and the
+  // last 64 tokens ready; of: O final
+  uint64_t kf[C::kKS], ke[C::kKS], vf[C::kVS], ve[C::kVS], vr[C::kVS];
+  uint64_t qr[2], qe[2], sr[2], pa[2], pb[2], of[2], drain;
+  int64_t scan[kThreads / 32];
+  Walk walk;
+  uint32_t poison[8];  // ring over units: number + 1 of a unit with an infinity or NaN to hide
+  uint32_t tmem;
+  int abort;
+};
+template <int DP>
+constexpr int kSmem = Cfg<DP>::kTiles + static_cast<int>(sizeof(Shared<DP>));
+static_assert(kSmem<128> <= 227 * 1024, "shared memory");
+
 __device__ __forceinline__ int unit_count(const AttnArgs& a, int m) {
   return static_cast<int>((static_cast<int64_t>(m) * a.g + kUnitRows - 1) / kUnitRows);
 }
@@ -152,19 +196,17 @@ __device__ __forceinline__ Span unit_span(const AttnArgs& a, const Seq& s, int r
   const int64_t r1 = min(r0 + kUnitRows, total) - 1;
   return span_of<kKT>(a, s, static_cast<int>(r0 / a.g), static_cast<int>(r1 / a.g) + 1);
 }
-__device__ __forceinline__ void open_unit(const AttnArgs& a, Walk& w) {
+// The segment from line position `at` (inside the unit) on.
+__device__ __forceinline__ void open_unit(const AttnArgs& a, Walk& w, int64_t at) {
   w.sp = unit_span(a, w.s, w.rt);
   w.rows = static_cast<int>(min(static_cast<int64_t>(kUnitRows),
                                 static_cast<int64_t>(w.s.m) * a.g - static_cast<int64_t>(w.rt) * kUnitRows));
+  w.t0 = static_cast<int>(max(at - w.tiles0(), static_cast<int64_t>(0)));
+  w.nt = static_cast<int>(min(w.end - w.tiles0(), static_cast<int64_t>(w.sp.n))) - w.t0;
 }
-__device__ __forceinline__ void open_segment(Walk& w) {
-  w.nt = static_cast<int>(min(w.left, static_cast<int64_t>(w.sp.n - w.t0)));
-  w.left -= w.nt;
-}
-// The next unit; only called while w.left > 0, so there is one.
+// The next unit; only called while w.more(), so there is one with a tile.
 __device__ __forceinline__ void next_segment(const AttnArgs& a, Walk& w) {
-  w.unit0 += w.sp.n;
-  w.t0 = 0;
+  w.unit0 = w.tiles0() + w.sp.n;
   if (++w.h == a.Hkv) {
     w.h = 0;
     if (++w.rt >= unit_count(a, w.s.m)) {
@@ -174,9 +216,8 @@ __device__ __forceinline__ void next_segment(const AttnArgs& a, Walk& w) {
         if (w.b < a.n) w.s = load_seq(a, w.b);
       } while (w.b < a.n && w.s.m == 0);
     }
-    open_unit(a, w);
   }
-  open_segment(w);
+  open_unit(a, w, w.unit0);
 }
 
 // Scores and values of the segment formed again, token by token, for the 32
@@ -219,21 +260,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, AttnArgs a,
                    long long wait_cycles) {
   using C = Cfg<DP>;
-  extern __shared__ unsigned char smraw[];
-  const uint32_t sbase = (su32(smraw) + 1023u) & ~1023u;
+  extern __shared__ __align__(1024) unsigned char smraw[];
+  const uint32_t sbase = su32(smraw);
+  if (sbase & 1023u) {  // the swizzle's pattern starts at such a boundary
+    if (threadIdx.x == 0) atomicOr(a.err, MOE_DEVERR_TIMEOUT);
+    return;
+  }
   const uint32_t sq = sbase, sk = sbase + 2 * C::kTile, sv = sk + C::kKS * C::kTile;
-  // kf/ke, vf/ve: full and empty slots of the rings; vr: V checked;
-  // qr: Q tile ready; sr: scores ready; pr: numerators ready; of: O final
-  __shared__ uint64_t b_kf[C::kKS], b_ke[C::kKS], b_vf[C::kVS], b_ve[C::kVS], b_vr[C::kVS];
-  __shared__ uint64_t b_qr[2], b_sr[2], b_pr[2], b_of[2], b_drain;
-  __shared__ uint32_t tmem_holder;
-  __shared__ int s_abort;
-  __shared__ uint32_t s_poison[8];  // ring over units: number + 1 of a unit with an infinity or NaN to hide
-  __shared__ int64_t s_scan[kThreads / 32];
-  __shared__ int s_first[kThreads];
-  __shared__ Walk s_walk;
-  volatile int* abort_flag = &s_abort;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Shared<DP>& sh = *reinterpret_cast<Shared<DP>*>(smraw + C::kTiles);
+  int* const s_first = reinterpret_cast<int*>(smraw);  // before the tiles are in use
+  volatile int* abort_flag = &sh.abort;
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
 
   // ---- this CTA's run. Units are counted sequence block by sequence block;
   // a unit's length follows from its last token's position.
@@ -244,12 +281,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t y = __shfl_up_sync(~0u, x, d);
       if (lane >= d) x += y;
     }
-    if (lane == 31) s_scan[warp] = x;
+    if (lane == 31) sh.scan[warp] = x;
     __syncthreads();
     int64_t base = 0, all = 0;
     for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) base += s_scan[i];
-      all += s_scan[i];
+      if (i < warp) base += sh.scan[i];
+      all += sh.scan[i];
     }
     __syncthreads();
     *total = all;
@@ -282,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           n = unit_span(a, load_seq(a, sb), rt).n;
         }
         int64_t all;
-        const int64_t at = line + scan(static_cast<int64_t>(n) * a.Hkv, &all);
+        const int64_t at = line + scan(u < units ? static_cast<int64_t>(n + kUnitCost) * a.Hkv : 0, &all);
         if (n > 0) f(sb, rt, n, at);
         line += all;
       }
@@ -291,56 +328,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     return line;
   };
   const int64_t total = visit_units([](int, int, int, int64_t) {});
-  const int64_t G = min(static_cast<int64_t>(gridDim.x), total);
-  if (blockIdx.x >= G) return;
-  const int64_t run0 = total * blockIdx.x / G, run1 = total * (blockIdx.x + 1) / G;
+  if (total == 0) return;
+  const Runs runs(total, gridDim.x);
+  if (blockIdx.x >= runs.n) return;
+  const int64_t run0 = runs.start(blockIdx.x), run1 = runs.start(blockIdx.x + 1);
+  if (tid == 0) sh.walk.nt = 0;
+  __syncthreads();
   visit_units([&](int b, int rt, int n, int64_t at) {
-    if (run0 >= at && run0 < at + static_cast<int64_t>(n) * a.Hkv) {
+    const int64_t per = n + kUnitCost;
+    if (run0 >= at && run0 < at + per * a.Hkv) {
       Walk w;
       w.b = b;
       w.rt = rt;
-      w.h = static_cast<int>((run0 - at) / n);
-      w.t0 = static_cast<int>((run0 - at) % n);
-      w.unit0 = run0 - w.t0;
-      w.left = run1 - run0;
+      w.h = static_cast<int>((run0 - at) / per);
+      w.unit0 = at + w.h * per;
+      w.end = run1;
       w.s = load_seq(a, b);
-      open_unit(a, w);
-      open_segment(w);
-      s_walk = w;
+      open_unit(a, w, run0);
+      sh.walk = w;
     }
   });
+  if (sh.walk.nt <= 0) return;  // a run within a unit's fixed cost
 
   if (tid == 0) {
-    s_abort = 0;
+    sh.abort = 0;
     for (int i = 0; i < C::kKS; ++i) {
-      mbar_init(su32(&b_kf[i]), 1);
-      mbar_init(su32(&b_ke[i]), 1);
+      mbar_init(su32(&sh.kf[i]), 1);
+      mbar_init(su32(&sh.ke[i]), 1);
     }
     for (int i = 0; i < C::kVS; ++i) {
-      mbar_init(su32(&b_vf[i]), 1);
-      mbar_init(su32(&b_ve[i]), 1);
-      mbar_init(su32(&b_vr[i]), 1);
+      mbar_init(su32(&sh.vf[i]), 1);
+      mbar_init(su32(&sh.ve[i]), 1);
+      mbar_init(su32(&sh.vr[i]), 2);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(su32(&b_qr[t]), 4);
-      mbar_init(su32(&b_sr[t]), 1);
-      mbar_init(su32(&b_pr[t]), 4);
-      mbar_init(su32(&b_of[t]), 1);
+      mbar_init(su32(&sh.qr[t]), 1);
+      mbar_init(su32(&sh.qe[t]), 1);
+      mbar_init(su32(&sh.sr[t]), 1);
+      mbar_init(su32(&sh.pa[t]), kSoftWarps / 2);
+      mbar_init(su32(&sh.pb[t]), kSoftWarps / 2);
+      mbar_init(su32(&sh.of[t]), 1);
     }
-    mbar_init(su32(&b_drain), 1);
-    for (int i = 0; i < 8; ++i) s_poison[i] = 0;
+    mbar_init(su32(&sh.drain), 1);
+    for (int i = 0; i < 8; ++i) sh.poison[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 9) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_holder)),
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&sh.tmem)),
                  "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = tmem_holder;
-  Walk w = s_walk;
+  const uint32_t tmem = sh.tmem;
+  Walk w = sh.walk;
 
   if (warp == 8) {
     // ---------------- TMA: lane i copies page i of the tile (its 64-column
@@ -369,8 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           RingPos& rp = kv ? vp : kp;
           uint32_t& n = kv ? nv : nk;
           const uint32_t slots = kv ? C::kVS : C::kKS;
-          const uint32_t full = su32(kv ? &b_vf[rp.s] : &b_kf[rp.s]);
-          if (n >= slots && !mbar_wait(su32(kv ? &b_ve[rp.s] : &b_ke[rp.s]), rp.ph ^ 1u, abort_flag, a.err, wait_cycles))
+          const uint32_t full = su32(kv ? &sh.vf[rp.s] : &sh.kf[rp.s]);
+          if (n >= slots && !mbar_wait(su32(kv ? &sh.ve[rp.s] : &sh.ke[rp.s]), rp.ph ^ 1u, abort_flag, a.err, wait_cycles))
             ok = false;
           ok = __all_sync(~0u, ok);
           if (!ok) break;
@@ -387,19 +429,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (*abort_flag) ok = false;
-      ok = __all_sync(~0u, ok) && w.left > 0;
+      ok = __all_sync(~0u, ok) && w.more();
       if (ok) next_segment(a, w);
     }
     // drain: copies in flight land before the CTA ends
     if (lane == 0) {
       for (uint32_t j = 0; j < nk && j < C::kKS; ++j)
-        mbar_drain(su32(&b_kf[(nk - 1 - j) % C::kKS]), ((nk - 1 - j) / C::kKS) & 1u, a.err, wait_cycles);
+        mbar_drain(su32(&sh.kf[(nk - 1 - j) % C::kKS]), ((nk - 1 - j) / C::kKS) & 1u, a.err, wait_cycles);
       for (uint32_t j = 0; j < nv && j < C::kVS; ++j)
-        mbar_drain(su32(&b_vf[(nv - 1 - j) % C::kVS]), ((nv - 1 - j) / C::kVS) & 1u, a.err, wait_cycles);
+        mbar_drain(su32(&sh.vf[(nv - 1 - j) % C::kVS]), ((nv - 1 - j) / C::kVS) & 1u, a.err, wait_cycles);
     }
   } else if (warp == 9) {
-    // ---------------- MMA issue
-    if (lane == 0) {
+    // ---------------- MMA issue, by one elected thread: elect.sync under a
+    // branch that is uniform in the warp lets the compiler keep descriptors in
+    // uniform registers. (A lane comparison does not: 100 cycles an MMA. The
+    // tensor cores take 73 cycles for 128 x 128 x 16 with A in tensor memory and
+    // 105 with A in shared memory.)
+    if (elect_one()) {
       const uint32_t id_qk = (1u << 4) | (1u << 7) | (1u << 10) | ((kKT >> 3) << 17) | ((kQT >> 4) << 24);
       const uint32_t id_pv = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((DP >> 3) << 17) | ((kQT >> 4) << 24);
       RingPos kp, vp;
@@ -415,131 +461,159 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t off = (k >> 2) * (C::kHalf >> 4) + (k & 3) * 2;
           umma_ss(tmem + C::kTmemS + t * 128u, qa + off, kb + off, id_qk, k > 0);
         }
-        umma_commit(su32(&b_sr[t]));
+        umma_commit(su32(&sh.sr[t]));
       };
       while (ok) {
         const int nq = w.rows > kQT ? 2 : 1;
-        if (!(ok = wait(&b_kf[kp.s], kp.ph))) break;
+        if (!(ok = wait(&sh.kf[kp.s], kp.ph))) break;
         for (int t = 0; t < nq && ok; ++t) {
           uint32_t& ph = t ? q_ph1 : q_ph;
-          if (!(ok = wait(&b_qr[t], ph))) break;
+          if (!(ok = wait(&sh.qr[t], ph))) break;
           ph ^= 1u;
           fence_after();
           qk(t);
+          if (w.nt == 1) umma_commit(su32(&sh.qe[t]));
         }
         if (!ok) break;
-        umma_commit(su32(&b_ke[kp.s]));
+        umma_commit(su32(&sh.ke[kp.s]));
         kp.next(C::kKS);
         for (int j = 0; j < w.nt && ok; ++j) {
           const bool more = j + 1 < w.nt;
           for (int t = 0; t < nq; ++t) {
-            if (!(ok = wait(&b_pr[t], p_ph[t]))) break;
-            p_ph[t] ^= 1u;
-            if (t == 0 && !(ok = wait(&b_vr[vp.s], vp.ph))) break;
-            fence_after();
+            if (t == 0 && !(ok = wait(&sh.vr[vp.s], vp.ph))) break;
             const uint64_t vb = sdesc_mn(sv + vp.s * C::kTile, C::kHalf);
 #pragma unroll
-            for (int k = 0; k < kKT / 16; ++k)
-              umma_ts(tmem + C::kTmemO + t * static_cast<uint32_t>(DP), tmem + C::kTmemS + t * 128u + 8u * k,
-                      vb + k * (2048u >> 4), id_pv, k > 0 || j > 0);
+            for (int hf = 0; hf < 2; ++hf) {
+              if (!(ok = wait(hf ? &sh.pb[t] : &sh.pa[t], p_ph[t]))) break;
+              fence_after();
+#pragma unroll
+              for (int k = 4 * hf; k < 4 * hf + 4; ++k)
+                umma_ts(tmem + C::kTmemO + t * static_cast<uint32_t>(DP), tmem + C::kTmemS + t * 128u + 8u * k,
+                        vb + k * (2048u >> 4), id_pv, k > 0 || j > 0);
+            }
+            if (!ok) break;
+            p_ph[t] ^= 1u;
             if (more) {
-              if (t == 0 && !(ok = wait(&b_kf[kp.s], kp.ph))) break;
+              if (t == 0 && !(ok = wait(&sh.kf[kp.s], kp.ph))) break;
               qk(t);
+              if (j + 2 == w.nt) umma_commit(su32(&sh.qe[t]));
             } else {
-              umma_commit(su32(&b_of[t]));
+              umma_commit(su32(&sh.of[t]));
             }
           }
           if (!ok) break;
-          umma_commit(su32(&b_ve[vp.s]));
+          umma_commit(su32(&sh.ve[vp.s]));
           vp.next(C::kVS);
           if (more) {
-            umma_commit(su32(&b_ke[kp.s]));
+            umma_commit(su32(&sh.ke[kp.s]));
             kp.next(C::kKS);
           }
         }
-        if (w.left == 0 || *abort_flag) break;
-        if (ok) next_segment(a, w);
+        if (!ok || !w.more() || *abort_flag) break;
+        next_segment(a, w);
       }
       // drain: every MMA issued here is done before tensor memory is released
-      umma_commit(su32(&b_drain));
-      mbar_drain(su32(&b_drain), 0, a.err, wait_cycles);
+      umma_commit(su32(&sh.drain));
+      mbar_drain(su32(&sh.drain), 0, a.err, wait_cycles);
     }
-  } else if (warp == 10) {
-    // ---------------- V check
+  } else if (warp >= 10) {
+    // ---------------- Q of row tile t, and the check of half of every V tile
+    const int t = warp - 10;
     RingPos vp;
-    bool ok = true;
+    uint32_t qe_ph = 0;
+    bool ok = true, q_used = false;
     for (uint32_t unit = 0; ok; ++unit) {
+      if (t * kQT < w.rows) {
+        if (q_used) {
+          ok = mbar_wait(su32(&sh.qe[t]), qe_ph, abort_flag, a.err, wait_cycles);
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+          qe_ph ^= 1u;
+        }
+        q_used = true;
+        // 16-byte pieces, swizzled as TMA would; rows and columns past the end are zero
+        constexpr int kPieces = DP / 8, kRowsPer = 32 / kPieces;
+        const int p = lane % kPieces, rows = w.rows - t * kQT;
+        const int64_t rg = static_cast<int64_t>(w.rt) * kUnitRows + t * kQT + lane / kPieces;
+        int i = static_cast<int>(rg / a.g), hq = static_cast<int>(rg - static_cast<int64_t>(i) * a.g);
+        const __nv_bfloat16* qh = static_cast<const __nv_bfloat16*>(a.q) + static_cast<int64_t>(w.h * a.g) * a.D + p * 8;
+#pragma unroll 4
+        for (int r = lane / kPieces; r < kQT; r += kRowsPer) {
+          const bool in = r < rows && p * 8 < a.D;
+          const void* src = in ? qh + (static_cast<int64_t>(w.s.row0) + i) * a.ldq + hq * a.D : a.q;
+          const uint32_t dst = sq + t * C::kTile + (p >> 3) * C::kHalf + r * 128u + (((p & 7) ^ (r & 7)) << 4);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
+                       : "memory");
+          hq += kRowsPer;
+          while (hq >= a.g) {
+            hq -= a.g;
+            ++i;
+          }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(su32(&sh.qr[t]));
+      }
       const int lo_pos = w.s.len - w.s.m + static_cast<int>(static_cast<int64_t>(w.rt) * kUnitRows / a.g);
       const int hi_pos = w.sp.end - 1;
       for (int i = 0; i < w.nt; ++i) {
-        ok = mbar_wait(su32(&b_vf[vp.s]), vp.ph, abort_flag, a.err, wait_cycles);
+        ok = mbar_wait(su32(&sh.vf[vp.s]), vp.ph, abort_flag, a.err, wait_cycles);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
         const int tile0 = w.sp.tile(w.t0 + i) * kKT;
         if (tile0 + kKT - 1 > lo_pos || (a.window > 0 && hi_pos - tile0 >= a.window)) {
           const uint32_t st = sv + vp.s * C::kTile;
           bool bad = false;
-          // rows of 128 bytes, halves one after the other: 8 pieces a row
-          for (int e = lane; e < kKT * 8 * (DP / 64); e += 32) {
-            const int j = tile0 + ((e >> 3) & (kKT - 1));
-            if (j >= w.sp.end || (j >= a.sinks && j < w.sp.low)) {
-              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(st + e * 16), "r"(0) : "memory");
-            } else {
-              uint32_t v[4];
-              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                           : "r"(st + e * 16)
-                           : "memory");
-              bad |= nonfinite2(v[0]) || nonfinite2(v[1]) || nonfinite2(v[2]) || nonfinite2(v[3]);
+          // this warp's 64 tokens: 8 pieces a row of 128 bytes, column halves one after the other
+#pragma unroll 1
+          for (int hf = 0; hf < DP / 64; ++hf) {
+#pragma unroll 8
+            for (int e = lane; e < 64 * 8; e += 32) {
+              const int j = tile0 + t * 64 + (e >> 3);
+              const uint32_t at = st + hf * C::kHalf + t * 8192u + e * 16u;
+              if (j >= w.sp.end || (j >= a.sinks && j < w.sp.low)) {
+                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+              } else {
+                uint32_t v[4];
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                             : "r"(at));
+                bad |= nonfinite2(v[0]) || nonfinite2(v[1]) || nonfinite2(v[2]) || nonfinite2(v[3]);
+              }
             }
           }
-          if (bad) *const_cast<volatile uint32_t*>(&s_poison[unit & 7]) = unit + 1;
+          if (bad) *const_cast<volatile uint32_t*>(&sh.poison[unit & 7]) = unit + 1;
           fence_async_smem();
           __syncwarp();
         }
-        if (lane == 0) mbar_arrive(su32(&b_vr[vp.s]));
+        if (lane == 0) mbar_arrive(su32(&sh.vr[vp.s]));
         vp.next(C::kVS);
       }
-      if (!ok || w.left == 0) break;
+      if (!ok || !w.more()) break;
       next_segment(a, w);
     }
-  } else if (warp < 8) {
+  } else {
     // ---------------- softmax: one thread a row
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;  // row tile, row
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + C::kTmemS + t * 128u + lanes, to = tmem + C::kTmemO + t * static_cast<uint32_t>(DP) + lanes;
-    const float c = a.scale_log2, raise = kRaise / c;
+    const float c = a.scale_log2;
     uint32_t s_ph = 0, o_ph = 0;
     bool ok = true;
     for (uint32_t unit = 0; ok; ++unit) {
       if (t * kQT < w.rows) {
-        // Q: this thread's row, swizzled as TMA would; rows past the end are zero
-        const int64_t rg = static_cast<int64_t>(w.rt) * kUnitRows + t * kQT + r;
         const bool row_ok = t * kQT + r < w.rows;
-        const int i = static_cast<int>(rg / a.g), hq = static_cast<int>(rg - static_cast<int64_t>(i) * a.g);
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(w.s.row0) + i) * a.ldq +
-                                 static_cast<int64_t>(w.h * a.g + hq) * a.D;
-#pragma unroll
-        for (int p = 0; p < DP / 8; ++p) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (row_ok && p * 8 < a.D) v = __ldg(reinterpret_cast<const uint4*>(q) + p);
-          const uint32_t dst = sq + t * C::kTile + (p >> 3) * C::kHalf + r * 128u + (((p & 7) ^ (r & 7)) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                       : "memory");
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(su32(&b_qr[t]));
-
-        const int pos = row_ok ? w.s.len - w.s.m + i : -1;
+        const int64_t rg = static_cast<int64_t>(w.rt) * kUnitRows + t * kQT + r;
+        const int qi = static_cast<int>(rg / a.g);
+        const int pos = row_ok ? w.s.len - w.s.m + qi : -1;
         // positions of the warp's rows, for the tiles that need no mask
-        const int64_t r0 = static_cast<int64_t>(w.rt) * kUnitRows + t * kQT + (warp & 3) * 32;
-        const int lo_pos = w.s.len - w.s.m + static_cast<int>(r0 / a.g);
-        const int64_t r_last = min(r0 + 31, static_cast<int64_t>(w.s.m) * a.g - 1);
+        const int lo_pos = w.s.len - w.s.m + static_cast<int>((rg - lane) / a.g);
+        const int64_t r_last = min(rg - lane + 31, static_cast<int64_t>(w.s.m) * a.g - 1);
         const int hi_pos = w.s.len - w.s.m + static_cast<int>(r_last / a.g);
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < w.nt; ++j) {
-          ok = mbar_wait(su32(&b_sr[t]), s_ph, abort_flag, a.err, wait_cycles);
+          ok = mbar_wait(su32(&sh.sr[t]), s_ph, abort_flag, a.err, wait_cycles);
           ok = __all_sync(~0u, ok);
           if (!ok) break;
           s_ph ^= 1u;
@@ -549,34 +623,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int last = pos - tile0;                              // columns after it are hidden
           const int from = a.window > 0 ? last - a.window + 1 : -1;  // columns before it are hidden, but for
           const int keep = a.sinks - tile0;                          // the first `keep`
-          auto hide = [&](float* s, int x0) {
+          float s[128];
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (x0 + x > last || (x0 + x < from && x0 + x >= keep)) s[x] = -INFINITY;
-          };
-          // the scores are read twice, first for the maximum: holding all 128
-          // would take more registers than a thread has
-          float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+          for (int x = 0; x < 128; x += 32) tmem_ld32_async(ts + x, s + x);
+          tmem_wait_ld();
+          if (edge) {
 #pragma unroll
-          for (int x = 0; x < 128; x += 64) {
-            float s[64];
-            tmem_ld32_async(ts + x, s);
-            tmem_ld32_async(ts + x + 32, s + 32);
-            tmem_wait_ld();
-            if (edge) {
-              hide(s, x);
-              hide(s + 32, x + 32);
-            }
+            for (int x = 0; x < 128; x += 32) {
+              // bit y: column x + y is visible
+              const uint32_t see = low_bits(last + 1 - x) & (~low_bits(from - x) | low_bits(keep - x));
 #pragma unroll
-            for (int y = 0; y < 64; y += 4) {
-              mx0 = fmaxf(mx0, s[y]);
-              mx1 = fmaxf(mx1, s[y + 1]);
-              mx2 = fmaxf(mx2, s[y + 2]);
-              mx3 = fmaxf(mx3, s[y + 3]);
+              for (int y = 0; y < 32; ++y) s[x + y] = (see >> y) & 1u ? s[x + y] : -INFINITY;
             }
           }
-          const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
-          const bool up = mx > m + raise || (m == -INFINITY && mx > m);
+          float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+          for (int y = 0; y < 128; y += 8) {
+            mx0 = max3(mx0, s[y], s[y + 1]);
+            mx1 = max3(mx1, s[y + 2], s[y + 3]);
+            mx2 = max3(mx2, s[y + 4], s[y + 5]);
+            mx3 = max3(mx3, s[y + 6], s[y + 7]);
+          }
+          const float mx = max3(fmaxf(mx0, mx1), mx2, mx3);
+          const bool up = (mx - m) * c > kRaise || (m == -INFINITY && mx > m);
           if (__any_sync(~0u, up)) {
             const float mn = up ? mx : m;
             const float f = up ? ex2((m - mn) * c) : 1.f;  // 0 for the first maximum
@@ -593,25 +662,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int y = 0; y < 16; ++y) u[y] = __float_as_uint(o[y] * f);
                 tmem_st16(to + x, u);
               }
-              tmem_wait_st();
             }
           }
           const float mc = m == -INFINITY ? 0.f : m * c;
           const unsigned long long c2 = pack2(c, c), m2 = pack2(-mc, -mc);
           unsigned long long l0 = 0ull, l1 = 0ull;
-          float sb[2][32];
-          tmem_ld32_async(ts, sb[0]);
 #pragma unroll
           for (int x = 0; x < 128; x += 32) {
-            float* s = sb[(x >> 5) & 1];
-            tmem_wait_ld();
-            if (x < 96) tmem_ld32_async(ts + x + 32, sb[((x >> 5) & 1) ^ 1]);
-            if (edge) hide(s, x);
             uint32_t p[16];
 #pragma unroll
             for (int y = 0; y < 32; y += 4) {
-              const float2 u = unpack2(fma2(pack2(s[y], s[y + 1]), c2, m2));
-              const float2 v = unpack2(fma2(pack2(s[y + 2], s[y + 3]), c2, m2));
+              const float2 u = unpack2(fma2(pack2(s[x + y], s[x + y + 1]), c2, m2));
+              const float2 v = unpack2(fma2(pack2(s[x + y + 2], s[x + y + 3]), c2, m2));
               const float e0 = ex2(u.x), e1 = ex2(u.y), e2 = ex2(v.x), e3 = ex2(v.y);
               // the sum takes the numerators before their rounding to bf16
               l0 = add2(l0, pack2(e0, e1));
@@ -620,22 +682,27 @@ __global__ void __launch_bounds__(kThreads, 1)
               p[y / 2 + 1] = pack_bf16(e2, e3);
             }
             tmem_st16(ts + x / 2, p);  // over scores already read
+            if (x == 32 || x == 96) {
+              tmem_wait_st();
+              fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(su32(x == 32 ? &sh.pa[t] : &sh.pb[t]));
+            }
           }
           const float2 la = unpack2(add2(l0, l1));
           l += la.x + la.y;
-          tmem_wait_st();
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(su32(&b_pr[t]));
         }
         if (!ok) break;
-        ok = mbar_wait(su32(&b_of[t]), o_ph, abort_flag, a.err, wait_cycles);
+        ok = mbar_wait(su32(&sh.of[t]), o_ph, abort_flag, a.err, wait_cycles);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
         o_ph ^= 1u;
         fence_after();
-        if (*const_cast<volatile uint32_t*>(&s_poison[unit & 7]) == unit + 1) {
+        const int hq = w.h * a.g + static_cast<int>(rg - static_cast<int64_t>(qi) * a.g);
+        const int64_t row = static_cast<int64_t>(w.s.row0) + qi;
+        if (*const_cast<volatile uint32_t*>(&sh.poison[unit & 7]) == unit + 1) {
           const Walk seg = w;
+          const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + row * a.ldq + static_cast<int64_t>(hq) * a.D;
           float ml[2];
 #pragma unroll 1
           for (int x = 0; x < DP; x += 32) {
@@ -654,15 +721,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // ---- results of the segment
         const bool seen = pos >= 0;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (static_cast<int64_t>(w.s.row0) + i) * a.ldo +
-                             static_cast<int64_t>(w.h * a.g + hq) * a.D;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * a.ldo + static_cast<int64_t>(hq) * a.D;
+        auto store32 = [&](const float* o, float f, int x) {
+#pragma unroll
+          for (int y = 0; y < 32; y += 8) {
+            if (!row_ok || x + y >= a.D) continue;
+            uint4 v;
+            v.x = pack_bf16(seen ? o[y] * f : 0.f, seen ? o[y + 1] * f : 0.f);
+            v.y = pack_bf16(seen ? o[y + 2] * f : 0.f, seen ? o[y + 3] * f : 0.f);
+            v.z = pack_bf16(seen ? o[y + 4] * f : 0.f, seen ? o[y + 5] * f : 0.f);
+            v.w = pack_bf16(seen ? o[y + 6] * f : 0.f, seen ? o[y + 7] * f : 0.f);
+            *reinterpret_cast<uint4*>(out + x + y) = v;
+          }
+        };
         const bool whole = w.whole();
-        float* part = nullptr;
-        if (!whole) {
-          const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (run0 >= w.unit0 ? 0 : 1)) * 2 + t;
-          part = a.part + slot * C::kPart;
-          *reinterpret_cast<float4*>(part + r * 4) = make_float4(m, l, 0.f, 0.f);
-        }
+        // a partial result: slot 0 if the run starts inside the unit's tiles, else 1
+        float* part = a.part + ((2 * static_cast<int64_t>(blockIdx.x) + (run0 > w.tiles0() ? 0 : 1)) * 2 + t) * C::kPart;
+        if (!whole) *reinterpret_cast<float2*>(part + r * 4) = make_float2(m, l);
         const float inv = 1.f / l;  // no weight at all on what is seen: 0/0
 #pragma unroll 1
         for (int x = 0; x < DP; x += 32) {
@@ -670,16 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32_async(to + x, o);
           tmem_wait_ld();
           if (whole) {
-#pragma unroll
-            for (int y = 0; y < 32; y += 8) {
-              if (!row_ok || x + y >= a.D) continue;
-              uint4 v;
-              v.x = pack_bf16(seen ? o[y] * inv : 0.f, seen ? o[y + 1] * inv : 0.f);
-              v.y = pack_bf16(seen ? o[y + 2] * inv : 0.f, seen ? o[y + 3] * inv : 0.f);
-              v.z = pack_bf16(seen ? o[y + 4] * inv : 0.f, seen ? o[y + 5] * inv : 0.f);
-              v.w = pack_bf16(seen ? o[y + 6] * inv : 0.f, seen ? o[y + 7] * inv : 0.f);
-              *reinterpret_cast<uint4*>(out + x + y) = v;
-            }
+            store32(o, inv, x);
           } else {
 #pragma unroll
             for (int y = 0; y < 32; y += 4)
@@ -688,15 +754,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!whole) {
-          auto cta_of = [&](int64_t tile) {  // the c with total*c/G <= tile < total*(c+1)/G
-            int64_t x = tile * G / total;
-            while (total * x / G > tile) --x;
-            while (total * (x + 1) / G <= tile) ++x;
-            return x;
-          };
-          const int64_t c0 = cta_of(w.unit0), c1 = cta_of(w.unit0 + w.sp.n - 1);
-          // one ticket a warp: its 32 rows of the unit that starts in c0's run
-          unsigned int* ticket = a.tickets + c0 * 8 + warp;
+          const int64_t c0 = runs.of(w.tiles0()), c1 = runs.of(w.tiles0() + w.sp.n - 1);
+          // one ticket a warp: its rows of the unit whose first tile is in c0's run
+          unsigned int* ticket = a.tickets + c0 * kSoftWarps + warp;
           __threadfence();
           __syncwarp();
           unsigned int done = 0;
@@ -705,8 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (done == static_cast<unsigned int>(c1 - c0)) {
             if (lane == 0) *ticket = 0u;  // zero between launches
             __threadfence();
-            auto part_of = [&](int64_t x) {
-              return a.part + ((2 * x + (total * x / G >= w.unit0 ? 0 : 1)) * 2 + t) * C::kPart;
+            auto part_of = [&](int64_t x) {  // only c0's run starts before the unit's tiles
+              return a.part + ((2 * x + (x == c0 ? 1 : 0)) * 2 + t) * C::kPart;
             };
             float M = -INFINITY, L = 0.f;
             for (int64_t x = c0; x <= c1; ++x) M = fmaxf(M, __ldcg(part_of(x) + r * 4));
@@ -717,30 +777,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const float inv_l = 1.f / L;
 #pragma unroll 1
-            for (int y = 0; y < DP; y += 8) {
-              float o[8] = {};
-              for (int64_t x = c0; x <= c1; ++x) {
-                const float* p = part_of(x);
-                const float f = ex2((__ldcg(p + r * 4) - Mu) * c);
-                const float4 u = __ldcg(reinterpret_cast<const float4*>(p + kQT * 4 + (y / 4 * kQT + r) * 4));
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(p + kQT * 4 + ((y / 4 + 1) * kQT + r) * 4));
-                o[0] += f * u.x, o[1] += f * u.y, o[2] += f * u.z, o[3] += f * u.w;
-                o[4] += f * v.x, o[5] += f * v.y, o[6] += f * v.z, o[7] += f * v.w;
+            for (int y = 0; y < DP; y += 32) {
+              float o[32] = {};
+              for (int64_t x0 = c0; x0 <= c1; x0 += 2) {  // two parts' loads in flight
+                float4 u[2][8];
+                float f[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const float* p = part_of(min(x0 + i, c1));
+                  f[i] = x0 + i <= c1 ? ex2((__ldcg(p + r * 4) - Mu) * c) : 0.f;
+#pragma unroll
+                  for (int z = 0; z < 8; ++z)
+                    u[i][z] = __ldcg(reinterpret_cast<const float4*>(p + kQT * 4 + ((y / 4 + z) * kQT + r) * 4));
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  if (x0 + i > c1) break;
+#pragma unroll
+                  for (int z = 0; z < 8; ++z) {
+                    o[4 * z] += f[i] * u[i][z].x;
+                    o[4 * z + 1] += f[i] * u[i][z].y;
+                    o[4 * z + 2] += f[i] * u[i][z].z;
+                    o[4 * z + 3] += f[i] * u[i][z].w;
+                  }
+                }
               }
-              if (!row_ok || y >= a.D) continue;
-              uint4 v;
-              v.x = pack_bf16(seen ? o[0] * inv_l : 0.f, seen ? o[1] * inv_l : 0.f);
-              v.y = pack_bf16(seen ? o[2] * inv_l : 0.f, seen ? o[3] * inv_l : 0.f);
-              v.z = pack_bf16(seen ? o[4] * inv_l : 0.f, seen ? o[5] * inv_l : 0.f);
-              v.w = pack_bf16(seen ? o[6] * inv_l : 0.f, seen ? o[7] * inv_l : 0.f);
-              *reinterpret_cast<uint4*>(out + y) = v;
+              store32(o, inv_l, y);
             }
           }
         }
         // the next unit's products overwrite O only after this read
         fence_before();
       }
-      if (*abort_flag || w.left == 0) break;
+      if (!w.more()) break;
       next_segment(a, w);
     }
   }
@@ -758,9 +827,9 @@ cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t st) {
   if ((e = map_pages(&mk, a.k, a.D, page, static_cast<int64_t>(a.n_pages) * a.Hkv, std::min(page, kKT))) != cudaSuccess ||
       (e = map_pages(&mv, a.v, a.D, page, static_cast<int64_t>(a.n_pages) * a.Hkv, std::min(page, kKT))) != cudaSuccess)
     return e;
-  e = cudaFuncSetAttribute(prefill_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DP>::kSmem);
+  e = cudaFuncSetAttribute(prefill_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<DP>);
   if (e != cudaSuccess) return e;
-  prefill_kernel<DP><<<num_sms, kThreads, Cfg<DP>::kSmem, st>>>(mk, mv, a, kPrefillWaitCycles);
+  prefill_kernel<DP><<<num_sms, kThreads, kSmem<DP>, st>>>(mk, mv, a, kPrefillWaitCycles);
   return cudaGetLastError();
 }
 
