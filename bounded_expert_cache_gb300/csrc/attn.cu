@@ -20,29 +20,31 @@
 // on arrival order. Every CTA derives the cut from the lengths itself: no
 // planning launch and no host copy of the lengths.
 //
-// What bounds it: HBM. K and V tiles come by 16-byte asynchronous copies into
-// a ring in shared memory; one barrier per tile.
+// What bounds it: HBM. One warp walks the run and brings K and V tiles in by
+// TMA, a box per page, into a ring in shared memory; eight warps compute. The
+// copies run ahead across tiles and units, so the memory pipe stays full while
+// a unit ends. Waits are bounded; after a time-out (recorded as an error) the
+// loops run to their end on whatever is there, so no barrier is left waiting.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "attn.cuh"
+#include "prefill.h"
+#include "tc.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = 8;
+using namespace tc;
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? 16 : 0;  // bytes read; the rest of the 16 is zero
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+constexpr int kWarps = 8;  // computing warps; the first warp of a third warpgroup copies
+constexpr int kCompute = 32 * kWarps;
+constexpr int kThreads = kCompute + 128;
+
+// barrier of the computing warps
+__device__ __forceinline__ void sync_compute() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
+  tma4d(dst, m, bar, x, y, 0, z);
 }
 __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -78,38 +80,19 @@ __device__ __forceinline__ void open_seq(const AttnArgs& a, Cursor& c) {
   c.per = c.sp.n;
 }
 
-// Issue one K or V tile (KT tokens of one head) into shared memory. Tokens
-// that no row of the unit sees arrive as zeros, whatever the cache holds.
-// Shared rows are swizzled: 16-byte piece c of row r lies at c ^ (r & 7).
-template <int KT, int ROWB>
-__device__ __forceinline__ void issue_tile(const AttnArgs& a, const Cursor& c, const void* base, uint32_t dst,
-                                           int row_bytes) {
-  constexpr int kPieces = ROWB / 16;              // 16-byte pieces of a padded row
-  constexpr int kPer = KT * kPieces / kThreads;   // pieces a thread
-  constexpr int kStep = kThreads / kPieces;       // rows between a thread's pieces
-  static_assert(kPer * kThreads == KT * kPieces, "pieces");
-  const int tile0 = c.sp.tile(c.t) * KT;
-  const int piece = threadIdx.x % kPieces, r0 = threadIdx.x / kPieces;
-  const int32_t* row = a.table + static_cast<int64_t>(c.s.id) * a.max_pages;
-  const bool col_ok = piece * 16 < row_bytes;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int r = r0 + i * kStep, j = tile0 + r;
-    bool ok = col_ok && j < c.sp.end && (j >= c.sp.low || j < a.sinks);
-    const char* src = static_cast<const char*>(base);
-    if (ok) {
-      const int p = __ldg(row + (j >> a.page_shift));
-      if (p < 0 || p >= a.n_pages) {
-        atomicOr(a.err, MOE_DEVERR_BADIDX);
-        ok = false;
-      } else {
-        const int64_t tok = ((static_cast<int64_t>(p) * a.Hkv + c.h) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
-        src += tok * row_bytes + piece * 16;
-      }
-    }
-    cp16(dst + r * ROWB + ((piece ^ (r & 7)) << 4), src, ok);
+// A tile in shared memory: per page (box of `rows` = min(page, KT) tokens),
+// per column block of 128 bytes, `rows` rows of 128 bytes whose 16-byte pieces
+// the copy has swizzled: piece c of row r lies at c ^ (r & 7).
+struct Tile {
+  uint32_t base;
+  int shift;  // log2 of rows
+  // start of the 128-byte row of token r in column block 0
+  template <int NB>
+  __device__ __forceinline__ uint32_t row(int r) const {
+    return base + (((r >> shift) * NB) << (shift + 7)) + ((r & ((1 << shift) - 1)) << 7);
   }
-}
+  __device__ __forceinline__ uint32_t block() const { return 128u << shift; }
+};
 
 // ------------------------------------------------------------ bf16 engine
 // RG row groups of 16 rows by KG = 8 / RG token groups, one warp each. Per
@@ -121,12 +104,17 @@ struct MmaEngine {
   using T = __nv_bfloat16;
   static constexpr int DP = DP_, RG = RG_, KT = KT_;
   static constexpr int KG = kWarps / RG, kRows = RG * 16, KC = KT / KG / 16;
-  static constexpr int ROWB = DP * 2;
-  static constexpr uint32_t kTileBytes = KT * ROWB;
-  static constexpr int kMergeBytes = kWarps * 16 * 64 * 4;
+  static constexpr int NB = DP / 64;  // column blocks
+  static constexpr uint32_t kTileBytes = KT * DP * 2;
+  // Q of large heads stays in shared memory: its fragments would not fit
+  // beside the results' in registers
+  static constexpr bool kQInSmem = DP > 128;
+  static constexpr int kQPitch = DP * 2 + 16;
+  static constexpr int kMergeBytes = kWarps * 16 * 64 * 4 + (kQInSmem ? kRows * kQPitch : 0);
   static_assert(KC >= 1 && KC * KG * 16 == KT, "token groups");
 
-  uint32_t qf[DP / 16][4];
+  uint32_t qf[kQInSmem ? 1 : DP / 16][4];
+  uint32_t qs;        // shared copy of Q
   float o[DP / 8][4];
   float s[KC][2][4];
   uint32_t p[KC][4];
@@ -157,20 +145,37 @@ struct MmaEngine {
       m[h] = -INFINITY;
       l[h] = 0.f;
     }
-#pragma unroll
-    for (int k = 0; k < DP / 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = k * 16 + (i >> 1) * 8 + (lane & 3) * 2;
-        qf[k][i] = (q[i & 1] && d < a.D) ? __ldg(reinterpret_cast<const unsigned int*>(q[i & 1] + d)) : 0u;
+    if constexpr (kQInSmem) {
+      // this warp's rows; the KG warps of a row group write the same
+      for (int e = lane; e < 16 * (DP / 8); e += 32) {
+        const int rr = e / (DP / 8), p = e % (DP / 8), r = first + rr;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (r < total && p * 8 < a.D) {
+          const int i = r / a.g;
+          v = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (c.s.row0 + i) * a.ldq +
+                                                   (c.h * a.g + r - i * a.g) * a.D) + p);
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(qs + (rg * 16 + rr) * kQPitch + p * 16), "r"(v.x),
+                     "r"(v.y), "r"(v.z), "r"(v.w)
+                     : "memory");
       }
+      __syncwarp();
+    } else {
+#pragma unroll
+      for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int d = k * 16 + (i >> 1) * 8 + (lane & 3) * 2;
+          qf[k][i] = (q[i & 1] && d < a.D) ? __ldg(reinterpret_cast<const unsigned int*>(q[i & 1] + d)) : 0u;
+        }
+    }
 #pragma unroll
     for (int n = 0; n < DP / 8; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
   }
 
-  __device__ __forceinline__ void scores(const AttnArgs& a, const Cursor& c, uint32_t kt) {
+  __device__ __forceinline__ void scores(const AttnArgs& a, const Cursor& c, const Tile& kt) {
     if (!active) return;
     const int lane = threadIdx.x & 31;
     const int tile0 = c.sp.tile(c.t) * KT;
@@ -187,13 +192,21 @@ struct MmaEngine {
       for (int i = 0; i < 8; ++i) s[ch][i >> 2][i & 3] = 0.f;
       // matrices: tokens 0-7 (d, d+8), tokens 8-15 (d, d+8)
       const int r = key0 + (lane & 7) + ((lane >> 4) << 3);
+      const uint32_t at = kt.row<NB>(r);
 #pragma unroll
       for (int k = 0; k < DP / 16; ++k) {
         uint32_t b[4];
         const int piece = 2 * k + ((lane >> 3) & 1);
-        ldsm4(b, kt + r * ROWB + ((piece ^ (r & 7)) << 4));
-        mma16816(s[ch][0], qf[k], b[0], b[1]);
-        mma16816(s[ch][1], qf[k], b[2], b[3]);
+        ldsm4(b, at + (piece >> 3) * kt.block() + (((piece & 7) ^ (r & 7)) << 4));
+        if constexpr (kQInSmem) {
+          uint32_t qa[4];
+          ldsm4(qa, qs + (rg * 16 + (lane & 15)) * kQPitch + (2 * k + (lane >> 4)) * 16);
+          mma16816(s[ch][0], qa, b[0], b[1]);
+          mma16816(s[ch][1], qa, b[2], b[3]);
+        } else {
+          mma16816(s[ch][0], qf[k], b[0], b[1]);
+          mma16816(s[ch][1], qf[k], b[2], b[3]);
+        }
       }
     }
     float mx[2] = {m[0], m[1]};
@@ -255,44 +268,59 @@ struct MmaEngine {
     }
   }
 
-  __device__ __forceinline__ void values(const AttnArgs& a, const Cursor&, uint32_t vt) {
+  __device__ __forceinline__ void values(const AttnArgs& a, const Cursor& c, const Tile& vt) {
     if (!active) return;
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int ch = 0; ch < KC; ++ch) {
       const int key0 = (ch * KG + kg) * 16;
-      if (edge && any_nonfinite(vt, key0)) {
+      if (edge) {
         // a product with a zero numerator would carry the infinity or NaN of a
         // token into rows that do not see it
-        values_by_row(vt, key0, ch);
-        continue;
+        const bool bad = clean(a, c, vt, key0);
+        if (bad) {
+          values_by_row(vt, key0, ch);
+          continue;
+        }
       }
       const int r = key0 + (lane & 7) + (((lane >> 3) & 1) << 3);
+      const uint32_t at = vt.row<NB>(r);
 #pragma unroll
       for (int n = 0; n < DP / 16; ++n) {
         uint32_t b[4];
         const int piece = 2 * n + (lane >> 4);
-        ldsm4t(b, vt + r * ROWB + ((piece ^ (r & 7)) << 4));
+        ldsm4t(b, at + (piece >> 3) * vt.block() + (((piece & 7) ^ (r & 7)) << 4));
         mma16816(o[2 * n], p[ch], b[0], b[1]);
         mma16816(o[2 * n + 1], p[ch], b[2], b[3]);
       }
     }
+    if (edge) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the zeros, before the slot's next copy
   }
 
-  __device__ __forceinline__ bool any_nonfinite(uint32_t vt, int key0) const {
+  // Zero the chunk's tokens that no row of the unit sees (the slot may hold
+  // anything there); is there an infinity or NaN among the others?
+  __device__ __forceinline__ bool clean(const AttnArgs& a, const Cursor& c, const Tile& vt, int key0) const {
     const int lane = threadIdx.x & 31;
+    const int j0 = c.sp.tile(c.t) * KT + key0;
     bool bad = false;
-    for (int i = lane; i < 16 * (ROWB / 16); i += 32) {
-      uint32_t w[4];
-      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                   : "r"(vt + key0 * ROWB + i * 16));
-      bad |= nonfinite2(w[0]) || nonfinite2(w[1]) || nonfinite2(w[2]) || nonfinite2(w[3]);
+    for (int i = lane; i < 16 * NB * 8; i += 32) {
+      const int r = (i >> 3) & 15, j = j0 + r;
+      const uint32_t at = vt.row<NB>(key0 + r) + (i >> 7) * vt.block() + ((i & 7) << 4);
+      if (j >= c.sp.end || (j >= a.sinks && j < c.sp.low)) {
+        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+      } else {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(at)
+                     : "memory");
+        bad |= nonfinite2(w[0]) || nonfinite2(w[1]) || nonfinite2(w[2]) || nonfinite2(w[3]);
+      }
     }
     return __any_sync(~0u, bad);
   }
 
-  __device__ __forceinline__ void values_by_row(uint32_t vt, int key0, int ch) {
+  __device__ __forceinline__ void values_by_row(const Tile& vt, int key0, int ch) {
     const int lane = threadIdx.x & 31;
 #pragma unroll 1
     for (int key = 0; key < 16; ++key) {
@@ -311,10 +339,11 @@ struct MmaEngine {
         }
       }
       const int r = key0 + key;
+      const uint32_t at = vt.row<NB>(r) + (lane & 3) * 4;
 #pragma unroll
       for (int n = 0; n < DP / 8; ++n) {
         uint32_t w;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(vt + r * ROWB + ((n ^ (r & 7)) << 4) + (lane & 3) * 4));
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at + (n >> 3) * vt.block() + (((n & 7) ^ (r & 7)) << 4)));
         const float v[2] = {__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -343,8 +372,8 @@ struct MmaEngine {
         for (int h = 0; h < 2; ++h)
           *reinterpret_cast<float2*>(buf + (warp * 16 + lane / 4 + 8 * h) * 64 + ((n * 8 + (lane & 3) * 2) ^ ((lane & 12) << 1))) =
               make_float2(o[n0 / 8 + n][2 * h], o[n0 / 8 + n][2 * h + 1]);
-      __syncthreads();
-      for (int e = threadIdx.x; e < rows * 16; e += kThreads) {
+      sync_compute();
+      for (int e = threadIdx.x; e < rows * 16; e += kCompute) {
         const int r = e >> 4, col = (e & 15) * 4;
         if (n0 + col < a.D) {
           const int w0 = (r >> 4) * KG, rr = r & 15;
@@ -369,37 +398,47 @@ struct MmaEngine {
           store(r, n0 + col, v, M, L);
         }
       }
-      __syncthreads();
+      sync_compute();
     }
   }
 };
 
 // ------------------------------------------------------------- f32 engine
-// 16 rows; per tile of 32 tokens a thread forms the scores of two rows and one
-// token, the warps' softmax goes through shared memory, and a thread then owns
-// four columns of a few rows. fp32 products throughout.
-template <int DP_>
+// R rows (4 or 16) in fp32 on the CUDA cores; K and V are read from shared
+// memory once for all of them. Scores: the lanes of a warp are TPW tokens by
+// 32 / TPW parts of the head, each for every row. Softmax: a warp a row, or two.
+// Values: a thread owns four columns of every row and each TG-th token; the
+// token groups are added when the unit ends.
+template <int DP_, int R_>
 struct FmaEngine {
   using T = float;
-  static constexpr int DP = DP_, KT = 32, kRows = 16;
-  static constexpr int ROWB = DP * 4;
-  static constexpr uint32_t kTileBytes = KT * ROWB;
-  static constexpr int kC4 = DP / 4;                       // column quads
-  static constexpr int kRT = kRows * kC4 / kThreads;       // rows a thread in the value product
-  // q rows, numerators, row factors
-  static constexpr int kMergeBytes = kRows * ROWB + kRows * KT * 4 + kRows * 4;
-  static_assert(kRT >= 1 && kRT * kThreads == kRows * kC4, "columns");
+  static constexpr int DP = DP_, kRows = R_, KT = DP == 256 ? 32 : 64;
+  static constexpr int NB = DP / 32;                // column blocks
+  static constexpr uint32_t kTileBytes = KT * DP * 4;
+  static constexpr int kC4 = DP / 4;                // column quads
+  static constexpr int TPW = KT / kWarps;           // tokens a warp (scores)
+  static constexpr int kParts = 32 / TPW;
+  static constexpr int TG = kCompute / kC4;         // token groups (values)
+  static constexpr int kSum = TG * 4 * DP;          // floats of the groups' results of 4 rows
+  static constexpr int kSP = kRows + 4;             // pitch of a token's numerators
+  static constexpr int kMergeBytes = (kSum + kRows * DP + kRows * KT + KT * kSP + kRows) * 4;
+  static_assert(kC4 % kParts == 0 && KT % TG == 0, "work of a thread");
 
-  float4 o[kRT];
-  float m[2], l[2];  // rows 2 warp and 2 warp + 1, kept by every lane
-  float* qs;
-  float* ps;
-  float* fs;
+  float4 o[kRows];
+  float m[2], l[2];  // of this warp's rows: warp, and warp + 8
+  float *sum, *qs, *ss, *ps, *fs;
   bool edge;
 
+  __device__ __forceinline__ void place(float* buf) {
+    sum = buf;
+    qs = sum + kSum;
+    ss = qs + kRows * DP;
+    ps = ss + kRows * KT;
+    fs = ps + KT * kSP;
+  }
   __device__ __forceinline__ void begin(const AttnArgs& a, const Cursor& c) {
     const int total = c.s.m * a.g;
-    for (int e = threadIdx.x; e < kRows * DP; e += kThreads) {
+    for (int e = threadIdx.x; e < kRows * DP; e += kCompute) {
       const int rr = e / DP, d = e % DP, r = c.rt * kRows + rr;
       float v = 0.f;
       if (r < total && d < a.D) {
@@ -409,18 +448,21 @@ struct FmaEngine {
       qs[e] = v;
     }
 #pragma unroll
-    for (int i = 0; i < kRT; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < kRows; ++r) o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       m[h] = -INFINITY;
       l[h] = 0.f;
     }
-    __syncthreads();
+    sync_compute();
   }
 
   __device__ __forceinline__ static float4 lds4(uint32_t addr) {
     float4 v;
-    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
   }
   // position of row rr of the tile, -1 past the last row
@@ -433,65 +475,105 @@ struct FmaEngine {
     return back >= 0 && (a.window == 0 || back < a.window || j < a.sinks);
   }
 
-  __device__ __forceinline__ void scores(const AttnArgs& a, const Cursor& c, uint32_t kt) {
+  __device__ __forceinline__ void scores(const AttnArgs& a, const Cursor& c, const Tile& kt) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile0 = c.sp.tile(c.t) * KT;
+    {
+      const int tok = warp * TPW + lane % TPW, part = lane / TPW;
+      const uint32_t at = kt.row<NB>(tok);
+      float acc[kRows] = {};
+#pragma unroll 4
+      for (int i = 0; i < kC4 / kParts; ++i) {
+        const int d4 = part + i * kParts;
+        const float4 k = lds4(at + (d4 >> 3) * kt.block() + (((d4 & 7) ^ (tok & 7)) << 4));
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          const float4 q = *reinterpret_cast<const float4*>(qs + r * DP + d4 * 4);
+          acc[r] += q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+        for (int x = TPW; x < 32; x <<= 1) acc[r] += __shfl_xor_sync(~0u, acc[r], x);
+        if (r % kParts == part) ss[r * KT + tok] = acc[r];
+      }
+    }
     const int lo_pos = pos_of(a, c, 0);
     const int hi_pos = c.s.len - c.s.m + (min((c.rt + 1) * kRows, c.s.m * a.g) - 1) / a.g;
     edge = tile0 + KT - 1 > lo_pos || (a.window > 0 && hi_pos - tile0 >= a.window);
-    float acc[2] = {0.f, 0.f};
-    const float* q0 = qs + 2 * warp * DP;
-#pragma unroll 8
-    for (int d4 = 0; d4 < kC4; ++d4) {
-      const float4 k = lds4(kt + lane * ROWB + ((d4 ^ (lane & 7)) << 4));
+    sync_compute();
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float4 q = *reinterpret_cast<const float4*>(q0 + h * DP + d4 * 4);
-        acc[h] += q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+    for (int h = 0; h < (kRows + kWarps - 1) / kWarps; ++h) {
+      const int rr = warp + kWarps * h;
+      if (rr >= kRows) break;
+      const int pos = pos_of(a, c, rr);
+      float v[KT / 32], mx = m[h];
+#pragma unroll
+      for (int x = 0; x < KT / 32; ++x) {
+        const int t = lane + 32 * x;
+        v[x] = sees(a, pos, tile0 + t) ? ss[rr * KT + t] * a.scale_log2 : -INFINITY;
+        mx = fmaxf(mx, v[x]);
       }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int rr = 2 * warp + h;
-      const bool see = sees(a, pos_of(a, c, rr), tile0 + lane);
-      const float v = see ? acc[h] * a.scale_log2 : -INFINITY;
-      float mx = v;
 #pragma unroll
       for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, x));
-      mx = fmaxf(m[h], mx);
-      const float mu = mx == -INFINITY ? 0.f : mx, f = ex2(m[h] - mu), p = ex2(v - mu);
+      const float mu = mx == -INFINITY ? 0.f : mx, f = ex2(m[h] - mu);
       m[h] = mx;
-      l[h] = l[h] * f + p;  // this lane's tokens only, until the end
-      ps[rr * KT + lane] = p;
+      l[h] *= f;  // this lane's tokens only, until the end
+#pragma unroll
+      for (int x = 0; x < KT / 32; ++x) {
+        const float p = ex2(v[x] - mu);
+        l[h] += p;
+        ps[(lane + 32 * x) * kSP + rr] = p;
+      }
       if (lane == 0) fs[rr] = f;
     }
-    // values() starts after the barrier that publishes its tile, which also
-    // publishes ps and fs
+    sync_compute();
   }
 
-  __device__ __forceinline__ void values(const AttnArgs& a, const Cursor& c, uint32_t vt) {
-    const int c4 = threadIdx.x % kC4, r0 = threadIdx.x / kC4;
-    constexpr int kStep = kThreads / kC4;
+  __device__ __forceinline__ void values(const AttnArgs& a, const Cursor& c, const Tile& vt) {
+    const int c4 = threadIdx.x % kC4, tg = threadIdx.x / kC4;
     const int tile0 = c.sp.tile(c.t) * KT;
 #pragma unroll
-    for (int i = 0; i < kRT; ++i) {
-      const float f = fs[r0 + i * kStep];
-      o[i].x *= f, o[i].y *= f, o[i].z *= f, o[i].w *= f;
+    for (int r = 0; r < kRows; ++r) {
+      const float f = fs[r];
+      o[r].x *= f, o[r].y *= f, o[r].z *= f, o[r].w *= f;
     }
-#pragma unroll 4
-    for (int key = 0; key < KT; ++key) {
-      const float4 v = lds4(vt + key * ROWB + ((c4 ^ (key & 7)) << 4));
-#pragma unroll
-      for (int i = 0; i < kRT; ++i) {
-        const int rr = r0 + i * kStep;
-        const float p = ps[rr * KT + key];
+#pragma unroll 2
+    for (int key = tg; key < KT; key += TG) {
+      const float4 v = lds4(vt.row<NB>(key) + (c4 >> 3) * vt.block() + (((c4 & 7) ^ (key & 7)) << 4));
+      const float4* p4 = reinterpret_cast<const float4*>(ps + key * kSP);
+      if (edge && !(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w))) {
         // a hidden token's infinity or NaN times its zero numerator is not added
-        if (edge && !sees(a, pos_of(a, c, rr), tile0 + key)) continue;
-        o[i].x += p * v.x;
-        o[i].y += p * v.y;
-        o[i].z += p * v.z;
-        o[i].w += p * v.w;
+        for (int r = 0; r < kRows; ++r) {
+          const bool see = sees(a, pos_of(a, c, r), tile0 + key);
+          const float p = ps[key * kSP + r];
+          add_row(r, see, p, v);
+        }
+        continue;
       }
+#pragma unroll
+      for (int q = 0; q < kRows / 4; ++q) {
+        const float4 p = p4[q];
+        const float pr[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[4 * q + i].x += pr[i] * v.x;
+          o[4 * q + i].y += pr[i] * v.y;
+          o[4 * q + i].z += pr[i] * v.z;
+          o[4 * q + i].w += pr[i] * v.w;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void add_row(int row, bool see, float p, const float4& v) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (r != row || !see) continue;
+      o[r].x += p * v.x;
+      o[r].y += p * v.y;
+      o[r].z += p * v.z;
+      o[r].w += p * v.w;
     }
   }
 
@@ -499,21 +581,34 @@ struct FmaEngine {
   __device__ __forceinline__ void end(const AttnArgs& a, const Cursor& c, float*, float2* ml, F&& store) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < (kRows + kWarps - 1) / kWarps; ++h) {
       float t = l[h];
 #pragma unroll
       for (int x = 16; x; x >>= 1) t += __shfl_xor_sync(~0u, t, x);
-      if (lane == 0) ml[2 * warp + h] = make_float2(m[h], t);
+      if (lane == 0 && warp + kWarps * h < kRows) ml[warp + kWarps * h] = make_float2(m[h], t);
     }
-    __syncthreads();
-    const int c4 = threadIdx.x % kC4, r0 = threadIdx.x / kC4;
+    const int c4 = threadIdx.x % kC4, tg = threadIdx.x / kC4;
     const int rows = min(kRows, c.s.m * a.g - c.rt * kRows);
 #pragma unroll
-    for (int i = 0; i < kRT; ++i) {
-      const int rr = r0 + i * (kThreads / kC4);
-      if (rr < rows && c4 * 4 < a.D) store(rr, c4 * 4, o[i], ml[rr].x, ml[rr].y);
+    for (int r0 = 0; r0 < kRows; r0 += 4) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<float4*>(sum + (tg * 4 + r) * DP + c4 * 4) = o[r0 + r];
+      sync_compute();
+      for (int e = threadIdx.x; e < 4 * kC4; e += kCompute) {
+        const int r = e / kC4, col = e % kC4 * 4;
+        if (r0 + r < rows && col < a.D) {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int g = 0; g < TG; ++g) {
+            const float4 u = *reinterpret_cast<const float4*>(sum + (g * 4 + r) * DP + col);
+            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+          }
+          store(r0 + r, col, v, ml[r0 + r].x, ml[r0 + r].y);
+        }
+      }
+      sync_compute();
     }
-    __syncthreads();
   }
 };
 
@@ -556,7 +651,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t* 
   __syncthreads();
   int64_t base = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) base += tmp[w];
     all += tmp[w];
   }
@@ -575,22 +670,40 @@ struct Ring {
 
 // SPLIT: runs of the line of tiles (decode). Otherwise one unit a CTA (chunks).
 template <class E, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1) attn_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, AttnArgs a,
+                int boxes, long long wait_cycles) {
   constexpr int NS = Ring<E>::kSlots;
   static_assert(NS >= 3, "ring");
   constexpr int KT = E::KT, R = E::kRows;
   extern __shared__ __align__(1024) unsigned char sm[];
-  __shared__ int64_t s_scan[kWarps];
+  __shared__ uint64_t b_full[NS], b_empty[NS];
+  __shared__ int64_t s_scan[kThreads / 32];
   __shared__ int64_t s_found[2];
   __shared__ float2 s_ml[kWarps * 16];
-  __shared__ int s_last;
-  const uint32_t ring = smem_u32(sm);
+  __shared__ int s_last, s_abort;
+  const uint32_t ring = su32(sm);
+  if (ring & 1023u) {  // the swizzle's pattern starts at such a boundary
+    if (threadIdx.x == 0) atomicOr(a.err, MOE_DEVERR_TIMEOUT);
+    return;
+  }
   float* merge = reinterpret_cast<float*>(sm + NS * E::kTileBytes);
-  const int row_bytes = a.D * static_cast<int>(sizeof(typename E::T));
   const int rt_n = a.row_tiles;
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
-  // ---- this CTA's run [first, last) of the line
-  Cursor ld;
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    s_found[0] = -1;
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(su32(&b_full[i]), 1);
+      mbar_init(su32(&b_empty[i]), kWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+
+  // ---- this CTA's run [run0, run0 + todo) of the line
+  Cursor cp;
   int64_t todo = 0, run0 = 0, unit0 = 0, total = 1;
   if (SPLIT) {
     auto tiles_of = [&](int b) -> int64_t {
@@ -622,26 +735,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(AttnArgs a) {
       __syncthreads();
       if (run0 < base) break;
     }
-    ld.b = static_cast<int>(s_found[0]);
-    open_seq<KT>(a, ld);
+    cp.b = static_cast<int>(s_found[0]);
+    open_seq<KT>(a, cp);
     const int64_t off = run0 - s_found[1];
-    const int u = static_cast<int>(off / ld.per);
-    ld.t = static_cast<int>(off % ld.per);
-    ld.rt = u / a.Hkv;
-    ld.h = u % a.Hkv;
-    unit0 = run0 - ld.t;
+    const int u = static_cast<int>(off / cp.per);
+    cp.t = static_cast<int>(off % cp.per);
+    cp.rt = u / a.Hkv;
+    cp.h = u % a.Hkv;
+    unit0 = run0 - cp.t;
   } else {
     // row tiles of every sequence in order, cache heads innermost
     const int want = blockIdx.x / a.Hkv;
-    ld.h = blockIdx.x % a.Hkv;
+    cp.h = blockIdx.x % a.Hkv;
     int64_t base = 0;
-    if (threadIdx.x == 0) s_found[0] = -1;
-    __syncthreads();
     for (int b0 = 0; b0 < a.n && base <= want; b0 += kThreads) {
       int64_t mine = 0, t;
-      if (b0 + static_cast<int>(threadIdx.x) < a.n) {
+      if (b0 + static_cast<int>(threadIdx.x) < a.n)
         mine = (static_cast<int64_t>(chunk_rows(a, b0 + threadIdx.x)) * a.g + R - 1) / R;
-      }
       const int64_t ex = base + block_scan(mine, s_scan, &t);
       if (want >= ex && want < ex + mine) {
         s_found[0] = b0 + threadIdx.x;
@@ -651,27 +761,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(AttnArgs a) {
     }
     __syncthreads();
     if (s_found[0] < 0) return;
-    ld.b = static_cast<int>(s_found[0]);
-    ld.rt = static_cast<int>(s_found[1]);
-    ld.s = load_seq(a, ld.b);
-    ld.sp = span_of<KT>(a, ld.s, ld.rt * R / a.g, (min((ld.rt + 1) * R, ld.s.m * a.g) - 1) / a.g + 1);
-    ld.per = ld.sp.n;
-    ld.t = 0;
-    todo = ld.per;
+    cp.b = static_cast<int>(s_found[0]);
+    cp.rt = static_cast<int>(s_found[1]);
+    cp.s = load_seq(a, cp.b);
+    cp.sp = span_of<KT>(a, cp.s, cp.rt * R / a.g, (min((cp.rt + 1) * R, cp.s.m * a.g) - 1) / a.g + 1);
+    cp.per = cp.sp.n;
+    cp.t = 0;
+    todo = cp.per;
   }
-
-  E eng;
-  if constexpr (sizeof(typename E::T) == 4) {
-    eng.qs = merge;
-    eng.ps = merge + R * E::DP;
-    eng.fs = eng.ps + R * KT;
-  }
-  // The load cursor runs ahead of the compute cursor, across units: element
-  // 2i of the ring's sequence is the K tile, 2i + 1 the V tile, of tile i.
-  Cursor cp = ld;
-  int64_t issued = 0;  // elements
-  const int64_t elems = 2 * todo;
-  int slot_in = 0, slot_out = 0;
   auto advance = [&](Cursor& c) {
     if (++c.t < c.per || !SPLIT) return;
     c.t = 0;
@@ -681,84 +778,135 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(AttnArgs a) {
     c.rt = 0;
     if (++c.b < a.n) open_seq<KT>(a, c);
   };
-  auto issue = [&]() {
-    if (issued < elems) {
-      issue_tile<KT, E::ROWB>(a, ld, (issued & 1) ? a.v : a.k, ring + slot_in * E::kTileBytes, row_bytes);
-      if ((issued & 1) && issued + 1 < elems) advance(ld);
-      ++issued;
-      if (++slot_in == NS) slot_in = 0;
-    }
-    cp_commit();  // empty groups keep the count
-  };
-  for (int i = 0; i < NS - 1; ++i) issue();
-  // One element: wait for it, let every thread see it (and be done with the
-  // element before), refill that slot.
-  auto next = [&]() -> uint32_t {
-    cp_wait<NS - 2>();
-    __syncthreads();
-    issue();
-    const uint32_t at = ring + slot_out * E::kTileBytes;
-    if (++slot_out == NS) slot_out = 0;
-    return at;
-  };
+  const int shift = min(a.page_shift, 31 - __clz(KT));  // log2 of a box's tokens
 
+  // Registers: the block is launched with 384 x 168; the computing warpgroups
+  // take 216 a thread, the third keeps 72 (256 x 216 + 128 x 72 = 384 x 168).
+  if (warp >= kWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp > kWarps) return;
+    // ---------------- copies: lane i brings page i of the tile; pages that no
+    // row sees are left out
+    const int per = KT >> shift;
+    RingPos rp;
+    uint32_t n = 0;  // tiles issued
+    bool ok = true;
+    for (int64_t left = todo; left > 0 && ok; --left) {
+      const int tok = cp.sp.tile(cp.t) * KT + (lane << shift);
+      bool need = lane < per && tok < cp.sp.end && (tok < a.sinks || tok + (1 << shift) > cp.sp.low);
+      int page = 0;
+      if (need) {
+        page = __ldg(a.table + static_cast<int64_t>(cp.s.id) * a.max_pages + (tok >> a.page_shift));
+        if (page < 0 || page >= a.n_pages) {
+          atomicOr(a.err, MOE_DEVERR_BADIDX);
+          need = false;
+        }
+      }
+      const uint32_t box_bytes = (128u * E::NB) << shift;
+      const uint32_t bytes = __popc(__ballot_sync(~0u, need)) * box_bytes;
+      const int y = tok & ((1 << a.page_shift) - 1), z = page * a.Hkv + cp.h;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t full = su32(&b_full[rp.s]);
+        if (n >= NS && !mbar_wait(su32(&b_empty[rp.s]), rp.ph ^ 1u, &s_abort, a.err, wait_cycles)) ok = false;
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_expect_tx(full, bytes);  // without pages the barrier completes by this arrival
+        __syncwarp();
+        if (need) {
+          const uint32_t dst = ring + rp.s * E::kTileBytes + lane * box_bytes;
+          for (int x = 0; x < boxes; ++x)
+            tma_page(dst + x * (128u << shift), kv ? &map_v : &map_k, full, x * (128 / static_cast<int>(sizeof(typename E::T))),
+                     y, z);
+        }
+        __syncwarp();
+        ++n;
+        rp.next(NS);
+      }
+      if (left > 1) advance(cp);
+    }
+    // drain: copies in flight land before the CTA ends
+    if (lane == 0)
+      for (uint32_t j = 0; j < n && j < NS; ++j)
+        mbar_drain(su32(&b_full[(n - 1 - j) % NS]), ((n - 1 - j) / NS) & 1u, a.err, wait_cycles);
+    return;
+  }
+
+  // ---------------- computing warps
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+  E eng;
+  if constexpr (sizeof(typename E::T) == 4)
+    eng.place(merge);
+  else
+    eng.qs = su32(merge) + kWarps * 16 * 64 * 4;
+  RingPos rp;
+  Tile tile;
+  tile.shift = shift;
+  auto wait_tile = [&]() {
+    mbar_wait(su32(&b_full[rp.s]), rp.ph, &s_abort, a.err, wait_cycles);
+    tile.base = ring + rp.s * E::kTileBytes;
+  };
+  auto free_tile = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(su32(&b_empty[rp.s]));
+    rp.next(NS);
+  };
   int64_t at = run0;
   while (todo > 0) {
     // ---- one unit's share of the run
     const int t0 = cp.t;
     const int nt = static_cast<int>(min(todo, static_cast<int64_t>(cp.per - t0)));
-    const Cursor unit = cp;
     eng.begin(a, cp);
     for (int i = 0; i < nt; ++i) {
-      const uint32_t kt = next();
-      eng.scores(a, cp, kt);
-      const uint32_t vt = next();
-      eng.values(a, cp, vt);
+      wait_tile();
+      eng.scores(a, cp, tile);
+      free_tile();
+      wait_tile();
+      eng.values(a, cp, tile);
+      free_tile();
       if (i + 1 < nt) ++cp.t;
     }
     todo -= nt;
-    const bool whole = t0 == 0 && nt == unit.per;
-    if (whole) {
-      eng.end(a, unit, merge, s_ml, [&](int r, int col, float4 v, float, float L) {
-        write_out<typename E::T>(a, unit, R, r, col, v, L);
+    if (t0 == 0 && nt == cp.per) {
+      eng.end(a, cp, merge, s_ml, [&](int r, int col, float4 v, float, float L) {
+        write_out<typename E::T>(a, cp, R, r, col, v, L);
       });
     } else {
       // partial rows of this CTA: slot 0 if its run starts inside the unit, else 1
       constexpr int kPS = E::DP + 4;
       const int64_t kSlot = static_cast<int64_t>(kPartRows) * kPS;
       float* mine = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (run0 > unit0 ? 0 : 1)) * kSlot;
-      eng.end(a, unit, merge, s_ml, [&](int r, int col, float4 v, float M, float L) {
+      eng.end(a, cp, merge, s_ml, [&](int r, int col, float4 v, float M, float L) {
         *reinterpret_cast<float4*>(mine + r * kPS + 4 + col) = v;
         if (col == 0) *reinterpret_cast<float2*>(mine + r * kPS) = make_float2(M, L);
       });
       // CTAs that hold a part of this unit: those whose runs meet it
-      const int64_t unit1 = unit0 + unit.per;
       const Runs runs(total, gridDim.x);
-      const int64_t c0 = runs.of(unit0), c1 = runs.of(unit1 - 1);
+      const int c0 = static_cast<int>(runs.of(unit0)), c1 = static_cast<int>(runs.of(unit0 + cp.per - 1));
       __threadfence();
-      __syncthreads();
+      sync_compute();
       unsigned int* ticket = a.tickets + c0;  // only one unit can start in c0's run and leave it
       if (threadIdx.x == 0) {
         const unsigned int done = atomicAdd(ticket, 1u);
         s_last = done == static_cast<unsigned int>(c1 - c0);
         if (s_last) *ticket = 0u;  // zero between launches
       }
-      __syncthreads();
+      sync_compute();
       if (s_last) {
         __threadfence();
-        const int rows = min(R, unit.s.m * a.g - unit.rt * R), c4n = a.D / 4;
+        const int rows = min(R, cp.s.m * a.g - cp.rt * R), c4n = a.D / 4;
         // only c0's run starts no later than the unit
-        auto slot_of = [&](int64_t c) { return a.part + (2 * c + (c == c0 ? 1 : 0)) * kSlot; };
-        for (int e = threadIdx.x; e < rows * c4n; e += kThreads) {
+        auto slot_of = [&](int c) { return a.part + (2 * c + (c == c0 ? 1 : 0)) * kSlot; };
+        for (int e = threadIdx.x; e < rows * c4n; e += kCompute) {
           const int r = e / c4n, col = (e - r * c4n) * 4;
           float M = -INFINITY;
 #pragma unroll 8
-          for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(slot_of(c) + r * kPS));
+          for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(slot_of(c) + r * kPS));
           const float Mu = M == -INFINITY ? 0.f : M;
           float L = 0.f;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-          for (int64_t c = c0; c <= c1; ++c) {
+          for (int c = c0; c <= c1; ++c) {
             const float* p = slot_of(c) + r * kPS;
             const float2 ml = __ldcg(reinterpret_cast<const float2*>(p));
             const float4 u = __ldcg(reinterpret_cast<const float4*>(p + 4 + col));
@@ -769,7 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(AttnArgs a) {
             v.z += f * u.z;
             v.w += f * u.w;
           }
-          write_out<typename E::T>(a, unit, R, r, col, v, L);
+          write_out<typename E::T>(a, cp, R, r, col, v, L);
         }
       }
     }
@@ -780,15 +928,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(AttnArgs a) {
       advance(cp);
     }
   }
-  cp_wait<0>();
 }
 
 template <class E, bool SPLIT>
 cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
-  constexpr int smem = Ring<E>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(attn_kernel<E, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int es = static_cast<int>(sizeof(typename E::T));
+  cudaError_t e = encoder();
   if (e != cudaSuccess) return e;
-  attn_kernel<E, SPLIT><<<grid, kThreads, smem, st>>>(a);
+  CUtensorMap mk, mv;
+  const int page = 1 << a.page_shift;
+  const int64_t blocks = static_cast<int64_t>(a.n_pages) * a.Hkv;
+  int boxes = 0;
+  if ((e = map_page_cols(&mk, a.k, es, a.D, page, blocks, std::min(page, E::KT), E::NB, &boxes)) != cudaSuccess ||
+      (e = map_page_cols(&mv, a.v, es, a.D, page, blocks, std::min(page, E::KT), E::NB, &boxes)) != cudaSuccess)
+    return e;
+  constexpr int smem = Ring<E>::kSmem;
+  e = cudaFuncSetAttribute(attn_kernel<E, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  attn_kernel<E, SPLIT><<<grid, kThreads, smem, st>>>(mk, mv, a, boxes, kPrefillWaitCycles);
   return cudaGetLastError();
 }
 
@@ -798,13 +955,20 @@ cudaError_t decode_rows(AttnArgs a, int num_sms, cudaStream_t st) {
   return launch<E, true>(a, num_sms, st);
 }
 
+// f32: four rows a unit if that holds them all, else sixteen
+template <int DP>
+cudaError_t decode_f32(const AttnArgs& a, int num_sms, cudaStream_t st) {
+  return a.n_q * a.g <= 4 ? decode_rows<FmaEngine<DP, 4>>(a, num_sms, st)
+                          : decode_rows<FmaEngine<DP, 16>>(a, num_sms, st);
+}
+
 }  // namespace
 
 cudaError_t launch_attn_decode(const AttnArgs& a, int32_t dtype, int num_sms, cudaStream_t st) {
   if (dtype == MOE_F32) {
-    if (a.D <= 64) return decode_rows<FmaEngine<64>>(a, num_sms, st);
-    if (a.D <= 128) return decode_rows<FmaEngine<128>>(a, num_sms, st);
-    return decode_rows<FmaEngine<256>>(a, num_sms, st);
+    if (a.D <= 64) return decode_f32<64>(a, num_sms, st);
+    if (a.D <= 128) return decode_f32<128>(a, num_sms, st);
+    return decode_f32<256>(a, num_sms, st);
   }
   // the fewest row groups that hold the rows: more token groups per tile
   const int rows = a.n_q * a.g;
@@ -829,9 +993,9 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, int32_t dtype, int32_t n_rows
     return static_cast<int>(((static_cast<int64_t>(n_rows) * a.g + rows - 1) / rows + a.n) * a.Hkv);
   };
   if (dtype == MOE_F32) {
-    if (a.D <= 64) return launch<FmaEngine<64>, false>(a, grid(16), st);
-    if (a.D <= 128) return launch<FmaEngine<128>, false>(a, grid(16), st);
-    return launch<FmaEngine<256>, false>(a, grid(16), st);
+    if (a.D <= 64) return launch<FmaEngine<64, 16>, false>(a, grid(16), st);
+    if (a.D <= 128) return launch<FmaEngine<128, 16>, false>(a, grid(16), st);
+    return launch<FmaEngine<256, 16>, false>(a, grid(16), st);
   }
   return launch<MmaEngine<256, 4, 64>, false>(a, grid(64), st);
 }

@@ -191,6 +191,24 @@ cudaError_t map_pages(CUtensorMap* m, const void* base, int D, int page, int64_t
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t map_page_cols(CUtensorMap* m, const void* base, int es, int D, int page, int64_t blocks, int box_rows,
+                          int cols, int* boxes) {
+  const cuuint32_t e = static_cast<cuuint32_t>(128 / es);  // elements of a column block
+  const cuuint64_t row = static_cast<cuuint64_t>(D) * es;
+  const bool whole = D % e == 0;
+  cuuint64_t dims[4] = {whole ? e : static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(page),
+                        whole ? static_cast<cuuint64_t>(D / e) : 1, static_cast<cuuint64_t>(blocks)};
+  cuuint64_t strides[3] = {row, whole ? 128 : row * page, row * page};
+  cuuint32_t box[4] = {e, static_cast<cuuint32_t>(box_rows), whole ? static_cast<cuuint32_t>(cols) : 1, 1};
+  cuuint32_t step[4] = {1, 1, 1, 1};
+  *boxes = whole ? 1 : cols;
+  CUresult r = g_encode(m, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                        const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 namespace {
 
 // Q8_0 quant planes in every slot: bytes x rows x matrix x slot. The box is

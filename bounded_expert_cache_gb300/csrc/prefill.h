@@ -86,6 +86,12 @@ cudaError_t map16(CUtensorMap* m, const void* base, CUtensorMapDataType t, int64
 // bf16 cache pages of one layer: D x page tokens x (page, head) blocks, boxes
 // of 64 columns x box_rows tokens, 128-byte swizzle.
 cudaError_t map_pages(CUtensorMap* m, const void* base, int D, int page, int64_t blocks, int box_rows);
+// The same pages (es bytes an element) with one box per page: column blocks of
+// 128 bytes x box_rows tokens, `cols` of them one after the other. A head that
+// is no multiple of 128 bytes takes one box per column block (*boxes), so that
+// the columns past its end are filled with zeros.
+cudaError_t map_page_cols(CUtensorMap* m, const void* base, int es, int D, int page, int64_t blocks, int box_rows,
+                          int cols, int* boxes);
 
 int gemm_stages(int phase);
 size_t gemm_smem_bytes(int phase, int stages);
