@@ -13,8 +13,8 @@
 // (sequence, row tile, cache head) whose rows are (token, head of the group)
 // pairs, and K and V are read once for all of them.
 //
-// Decode work split: the token tiles of all units form one line, cut into one
-// equal run per CTA (one CTA per SM). A run covers whole units or ends inside
+// Decode work split: the token tiles of all units (and a unit's fixed cost)
+// form one line, cut into one equal run per CTA (one CTA per SM). A run covers whole units or ends inside
 // one; a unit cut by run ends leaves partial (m, l, o) rows in the scratch and
 // the CTA that arrives last joins them in run order, so results do not depend
 // on arrival order. Every CTA derives the cut from the lengths itself: no
@@ -64,13 +64,25 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// A unit of work, and the position of a cursor on the line of tiles.
+// A CTA's walk along the line: units in order, of each the tiles [t0, t1) that
+// fall into the run. On the line a unit is kUnitCost positions, for its Q and
+// its results, and then one per tile.
+constexpr int kUnitCost = 2;
+constexpr int kJoinGroup = 8;  // CTAs whose parts of a unit are joined first, where many hold one
 struct Cursor {
-  int b, rt, h;  // sequence, row tile, cache head
-  int t;         // tile of the unit
-  int per;       // tiles of each of the sequence's units
+  int b, rt, h;   // sequence, row tile, cache head
+  int t, t0, t1;  // tile of the unit, and this run's
+  int per;        // tiles of the unit
+  int64_t tiles0; // line position of the unit's first tile
+  int64_t end;    // end of the run
   Seq s;
   Span sp;
+  __device__ __forceinline__ void open(int64_t at) {
+    t0 = static_cast<int>(max(at - tiles0, static_cast<int64_t>(0)));
+    t1 = static_cast<int>(min(end - tiles0, static_cast<int64_t>(per)));
+    t = t0;
+  }
+  __device__ __forceinline__ bool more() const { return tiles0 + per + kUnitCost < end; }
 };
 
 template <int KT>
@@ -78,6 +90,20 @@ __device__ __forceinline__ void open_seq(const AttnArgs& a, Cursor& c) {
   c.s = load_seq(a, c.b);
   c.sp = span_of<KT>(a, c.s, 0, c.s.m);
   c.per = c.sp.n;
+}
+// The next unit (decode); only called while c.more(), so there is one with a tile.
+template <int KT>
+__device__ __forceinline__ void next_unit(const AttnArgs& a, Cursor& c) {
+  c.tiles0 += c.per + kUnitCost;
+  if (++c.h == a.Hkv) {
+    c.h = 0;
+    if (++c.rt == a.row_tiles) {
+      c.rt = 0;
+      ++c.b;
+      open_seq<KT>(a, c);
+    }
+  }
+  c.open(c.tiles0);
 }
 
 // A tile in shared memory: per page (box of `rows` = min(page, KT) tokens),
@@ -146,16 +172,19 @@ struct MmaEngine {
       l[h] = 0.f;
     }
     if constexpr (kQInSmem) {
-      // this warp's rows; the KG warps of a row group write the same
-      for (int e = lane; e < 16 * (DP / 8); e += 32) {
-        const int rr = e / (DP / 8), p = e % (DP / 8), r = first + rr;
+      // this warp's rows, a lane a 16-byte piece; the KG warps of a row group
+      // write the same
+      static_assert(DP / 8 == 32, "a lane a piece");
+#pragma unroll 8
+      for (int rr = 0; rr < 16; ++rr) {
+        const int r = first + rr;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (r < total && p * 8 < a.D) {
+        if (r < total && lane * 8 < a.D) {
           const int i = r / a.g;
           v = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (c.s.row0 + i) * a.ldq +
-                                                   (c.h * a.g + r - i * a.g) * a.D) + p);
+                                                   (c.h * a.g + r - i * a.g) * a.D) + lane);
         }
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(qs + (rg * 16 + rr) * kQPitch + p * 16), "r"(v.x),
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(qs + (rg * 16 + rr) * kQPitch + lane * 16), "r"(v.x),
                      "r"(v.y), "r"(v.z), "r"(v.w)
                      : "memory");
       }
@@ -702,17 +731,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
 
-  // ---- this CTA's run [run0, run0 + todo) of the line
+  // ---- this CTA's run of the line
   Cursor cp;
-  int64_t todo = 0, run0 = 0, unit0 = 0, total = 1;
+  int64_t run0 = 0, total = 1;
   if (SPLIT) {
-    auto tiles_of = [&](int b) -> int64_t {
+    auto line_of = [&](int b) -> int64_t {  // positions of a sequence
+      if (b >= a.n) return 0;
       Seq s = load_seq(a, b);
-      return static_cast<int64_t>(span_of<KT>(a, s, 0, s.m).n) * rt_n * a.Hkv;
+      return static_cast<int64_t>(span_of<KT>(a, s, 0, s.m).n + kUnitCost) * rt_n * a.Hkv;
     };
     int64_t mine = 0, all = 0;
     for (int b0 = 0; b0 < a.n; b0 += kThreads) {
-      mine = b0 + static_cast<int>(threadIdx.x) < a.n ? tiles_of(b0 + threadIdx.x) : 0;
+      mine = line_of(b0 + threadIdx.x);
       int64_t t;
       block_scan(mine, s_scan, &t);
       all += t;
@@ -721,10 +751,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Runs runs(total, gridDim.x);
     if (blockIdx.x >= runs.n) return;
     run0 = runs.start(blockIdx.x);
-    todo = runs.start(blockIdx.x + 1) - run0;
     int64_t base = 0;
     for (int b0 = 0; b0 < a.n; b0 += kThreads) {
-      if (a.n > kThreads) mine = b0 + static_cast<int>(threadIdx.x) < a.n ? tiles_of(b0 + threadIdx.x) : 0;
+      if (a.n > kThreads) mine = line_of(b0 + threadIdx.x);
       int64_t t;
       const int64_t ex = base + block_scan(mine, s_scan, &t);
       if (run0 >= ex && run0 < ex + mine) {
@@ -737,12 +766,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     cp.b = static_cast<int>(s_found[0]);
     open_seq<KT>(a, cp);
-    const int64_t off = run0 - s_found[1];
-    const int u = static_cast<int>(off / cp.per);
-    cp.t = static_cast<int>(off % cp.per);
+    const int u = static_cast<int>((run0 - s_found[1]) / (cp.per + kUnitCost));
     cp.rt = u / a.Hkv;
     cp.h = u % a.Hkv;
-    unit0 = run0 - cp.t;
+    cp.tiles0 = s_found[1] + static_cast<int64_t>(u) * (cp.per + kUnitCost) + kUnitCost;
+    cp.end = runs.start(blockIdx.x + 1);
+    cp.open(run0);
+    if (cp.t1 <= cp.t0) return;  // a run within a unit's fixed cost
   } else {
     // row tiles of every sequence in order, cache heads innermost
     const int want = blockIdx.x / a.Hkv;
@@ -766,18 +796,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     cp.s = load_seq(a, cp.b);
     cp.sp = span_of<KT>(a, cp.s, cp.rt * R / a.g, (min((cp.rt + 1) * R, cp.s.m * a.g) - 1) / a.g + 1);
     cp.per = cp.sp.n;
-    cp.t = 0;
-    todo = cp.per;
+    cp.tiles0 = 0;
+    cp.end = cp.per;
+    cp.open(0);
   }
-  auto advance = [&](Cursor& c) {
-    if (++c.t < c.per || !SPLIT) return;
-    c.t = 0;
-    if (++c.h < a.Hkv) return;
-    c.h = 0;
-    if (++c.rt < rt_n) return;
-    c.rt = 0;
-    if (++c.b < a.n) open_seq<KT>(a, c);
-  };
   const int shift = min(a.page_shift, 31 - __clz(KT));  // log2 of a box's tokens
 
   // Registers: the block is launched with 384 x 168; the computing warpgroups
@@ -791,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     RingPos rp;
     uint32_t n = 0;  // tiles issued
     bool ok = true;
-    for (int64_t left = todo; left > 0 && ok; --left) {
+    while (ok) {
       const int tok = cp.sp.tile(cp.t) * KT + (lane << shift);
       bool need = lane < per && tok < cp.sp.end && (tok < a.sinks || tok + (1 << shift) > cp.sp.low);
       int page = 0;
@@ -823,7 +845,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n;
         rp.next(NS);
       }
-      if (left > 1) advance(cp);
+      if (++cp.t < cp.t1) continue;
+      if (!cp.more()) break;
+      next_unit<KT>(a, cp);
     }
     // drain: copies in flight land before the CTA ends
     if (lane == 0)
@@ -851,82 +875,118 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(su32(&b_empty[rp.s]));
     rp.next(NS);
   };
-  int64_t at = run0;
-  while (todo > 0) {
+  while (true) {
     // ---- one unit's share of the run
-    const int t0 = cp.t;
-    const int nt = static_cast<int>(min(todo, static_cast<int64_t>(cp.per - t0)));
     eng.begin(a, cp);
-    for (int i = 0; i < nt; ++i) {
+    for (; cp.t < cp.t1; ++cp.t) {
       wait_tile();
       eng.scores(a, cp, tile);
       free_tile();
       wait_tile();
       eng.values(a, cp, tile);
       free_tile();
-      if (i + 1 < nt) ++cp.t;
     }
-    todo -= nt;
-    if (t0 == 0 && nt == cp.per) {
+    if (cp.t1 - cp.t0 == cp.per) {
       eng.end(a, cp, merge, s_ml, [&](int r, int col, float4 v, float, float L) {
         write_out<typename E::T>(a, cp, R, r, col, v, L);
       });
     } else {
-      // partial rows of this CTA: slot 0 if its run starts inside the unit, else 1
+      // partial rows of this CTA, (m, l, -, -) and the row: slot 0 if its run
+      // starts inside the unit's tiles, else 1
       constexpr int kPS = E::DP + 4;
-      const int64_t kSlot = static_cast<int64_t>(kPartRows) * kPS;
-      float* mine = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (run0 > unit0 ? 0 : 1)) * kSlot;
+      constexpr int64_t kSlot = static_cast<int64_t>(kPartRows) * kPS;
+      float* mine = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (run0 > cp.tiles0 ? 0 : 1)) * kSlot;
       eng.end(a, cp, merge, s_ml, [&](int r, int col, float4 v, float M, float L) {
         *reinterpret_cast<float4*>(mine + r * kPS + 4 + col) = v;
         if (col == 0) *reinterpret_cast<float2*>(mine + r * kPS) = make_float2(M, L);
       });
-      // CTAs that hold a part of this unit: those whose runs meet it
+      // CTAs that hold a part of this unit: those whose runs meet its tiles;
+      // only c0's run starts no later than they do
       const Runs runs(total, gridDim.x);
-      const int c0 = static_cast<int>(runs.of(unit0)), c1 = static_cast<int>(runs.of(unit0 + cp.per - 1));
-      __threadfence();
-      sync_compute();
-      unsigned int* ticket = a.tickets + c0;  // only one unit can start in c0's run and leave it
-      if (threadIdx.x == 0) {
-        const unsigned int done = atomicAdd(ticket, 1u);
-        s_last = done == static_cast<unsigned int>(c1 - c0);
-        if (s_last) *ticket = 0u;  // zero between launches
-      }
-      sync_compute();
-      if (s_last) {
+      const int c0 = static_cast<int>(runs.of(cp.tiles0)), c1 = static_cast<int>(runs.of(cp.tiles0 + cp.per - 1));
+      const int me = blockIdx.x;
+      const int rows = min(R, cp.s.m * a.g - cp.rt * R), c4n = a.D / 4;
+      auto slot_of = [&](int c) { return a.part + (2 * c + (c == c0 ? 1 : 0)) * kSlot; };
+      // arrive at a ticket; true for the last of `count`
+      auto last_of = [&](unsigned int* ticket, int count) {
         __threadfence();
-        const int rows = min(R, cp.s.m * a.g - cp.rt * R), c4n = a.D / 4;
-        // only c0's run starts no later than the unit
-        auto slot_of = [&](int c) { return a.part + (2 * c + (c == c0 ? 1 : 0)) * kSlot; };
+        sync_compute();
+        if (threadIdx.x == 0) {
+          s_last = atomicAdd(ticket, 1u) == static_cast<unsigned int>(count - 1);
+          if (s_last) *ticket = 0u;  // zero between launches
+        }
+        sync_compute();
+        if (s_last) __threadfence();
+        return s_last != 0;
+      };
+      // Join `count` (at most 32) partial results: row r of the i-th at
+      // part(i) + r * kPS, its (m, l) at offset hdr. A warp first forms a row's
+      // weights, a lane a part; the sums' loads then depend on nothing.
+      auto join = [&](auto&& part, int count, int hdr, auto&& emit) {
+        float* const wts = merge;                                  // [rows][32]
+        float2* const tot = reinterpret_cast<float2*>(merge + kPartRows * 32);  // (M, L) of a row
+        for (int r = warp; r < rows; r += kWarps) {
+          float2 ml = make_float2(-INFINITY, 0.f);
+          if (lane < count) ml = __ldcg(reinterpret_cast<const float2*>(part(lane) + r * kPS + hdr));
+          float M = ml.x;
+#pragma unroll
+          for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
+          const float f = ex2(ml.x - (M == -INFINITY ? 0.f : M));
+          float L = f * ml.y;
+#pragma unroll
+          for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
+          wts[r * 32 + lane] = lane < count ? f : 0.f;
+          if (lane == 0) tot[r] = make_float2(M, L);
+        }
+        sync_compute();
         for (int e = threadIdx.x; e < rows * c4n; e += kCompute) {
           const int r = e / c4n, col = (e - r * c4n) * 4;
-          float M = -INFINITY;
-#pragma unroll 8
-          for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(slot_of(c) + r * kPS));
-          const float Mu = M == -INFINITY ? 0.f : M;
-          float L = 0.f;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int c = c0; c <= c1; ++c) {
-            const float* p = slot_of(c) + r * kPS;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p));
-            const float4 u = __ldcg(reinterpret_cast<const float4*>(p + 4 + col));
-            const float f = ex2(ml.x - Mu);
-            L += f * ml.y;
-            v.x += f * u.x;
-            v.y += f * u.y;
-            v.z += f * u.z;
-            v.w += f * u.w;
+          for (int i0 = 0; i0 < count; i0 += 16) {
+            float4 u[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              u[i] = i0 + i < count ? __ldcg(reinterpret_cast<const float4*>(part(i0 + i) + r * kPS + 4 + col))
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float f = wts[r * 32 + i0 + i];
+              v.x += f * u[i].x;
+              v.y += f * u[i].y;
+              v.z += f * u[i].z;
+              v.w += f * u[i].w;
+            }
           }
-          write_out<typename E::T>(a, cp, R, r, col, v, L);
+          emit(r, col, v, tot[r].x, tot[r].y);
+        }
+        sync_compute();
+      };
+      auto finish = [&](int r, int col, float4 v, float, float L) {
+        write_out<typename E::T>(a, cp, R, r, col, v, L);
+      };
+      unsigned int* const t_unit = a.tickets + c0;  // only one unit can start in c0's run and leave it
+      if (c1 - c0 < kJoinGroup * 2) {
+        if (last_of(t_unit, c1 - c0 + 1)) join([&](int i) { return slot_of(c0 + i); }, c1 - c0 + 1, 0, finish);
+      } else {
+        // many parts: groups of kJoinGroup CTAs first (their result goes to the
+        // first one's slot, its (m, l) behind that part's own), then the groups
+        const int g = me / kJoinGroup, g0 = c0 / kJoinGroup, g1 = c1 / kJoinGroup;
+        auto first_of = [&](int k) { return max(c0, k * kJoinGroup); };
+        const int f = first_of(g), n = min(c1, g * kJoinGroup + kJoinGroup - 1) - f + 1;
+        unsigned int* const t_group = a.tickets + (f == c0 ? 1 : 2) * static_cast<int>(gridDim.x) + f;
+        if (last_of(t_group, n)) {
+          join([&](int i) { return slot_of(f + i); }, n, 0, [&](int r, int col, float4 v, float M, float L) {
+            float* p = slot_of(f) + r * kPS;
+            *reinterpret_cast<float4*>(p + 4 + col) = v;
+            if (col == 0) *reinterpret_cast<float2*>(p + 2) = make_float2(M, L);
+          });
+          if (last_of(t_unit, g1 - g0 + 1))
+            join([&](int i) { return slot_of(first_of(g0 + i)); }, g1 - g0 + 1, 2, finish);
         }
       }
     }
-    at += nt;
-    unit0 = at;
-    if (todo > 0) {
-      cp.t = cp.per - 1;
-      advance(cp);
-    }
+    if (!cp.more()) break;
+    next_unit<KT>(a, cp);
   }
 }
 

@@ -12,7 +12,16 @@ import torch
 
 from . import _native as N
 from ._native import lib
-from .api import _check, _ptr, _stream
+from .api import MoeError
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+# These calls take microseconds on the device, so the binding keeps its own
+# share small: plain integers for pointers, no temporary ctypes objects.
+def _ok(st: int):
+    if st != N.MOE_OK:
+        raise MoeError(st, (lib.moe_last_error(None) or b"").decode(errors="replace"))
 
 
 def _dtype_id(dtype: torch.dtype) -> int:
@@ -23,24 +32,28 @@ def _dtype_id(dtype: torch.dtype) -> int:
     raise TypeError(f"expected float32 or bfloat16 (got {dtype})")
 
 
-def _ints(t: torch.Tensor, name: str, n: Optional[int] = None) -> torch.Tensor:
+def _ints(t: torch.Tensor, name: str, n: Optional[int] = None) -> int:
+    """Entries of an index list."""
     if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 1 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous one-dimensional int32 CUDA tensor")
-    if n is not None and t.numel() != n:
-        raise ValueError(f"{name} must hold {n} entries (got {t.numel()})")
-    return t
+    have = t.shape[0]
+    if n is not None and have != n:
+        raise ValueError(f"{name} must hold {n} entries (got {have})")
+    return have
 
 
 def _head_rows(t: torch.Tensor, name: str, heads: Optional[int], dim: int, dtype: torch.dtype) -> int:
     """Row stride (elements) of [rows, heads, dim] whose rows are dense but may lie apart."""
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a {dtype} CUDA tensor")
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must be [rows, {heads if heads is not None else 'heads'}, {dim}] "
-                         f"(got {tuple(t.shape)})")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim):
+                         f"(got {tuple(shape)})")
+    rows, head, one = t.stride()
+    if one != 1 or (shape[1] > 1 and head != dim):
         raise ValueError(f"the heads of a row of {name} must be dense")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * dim)
+    return rows if shape[0] > 1 else max(rows, shape[1] * dim)
 
 
 class KvCache:
@@ -70,11 +83,17 @@ class KvCache:
         L, P, Hkv, page, D = k.shape
         self.raw = N.KvT(k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), ref.data_ptr(), None, 0, L, P,
                          Hkv, page, D, _dtype_id(k.dtype), table.shape[0], table.shape[1])
+        self._ref = C.byref(self.raw)
+        self._device = k.device.index
+        self._kv_heads, self._dim, self._dtype = Hkv, D, k.dtype
         n = C.c_int64()
         with torch.cuda.device(k.device):
-            _check(lib.moe_kv_work_bytes(C.byref(self.raw), C.byref(n)))
+            _ok(lib.moe_kv_work_bytes(self._ref, C.byref(n)))
         self.work = torch.zeros(n.value, dtype=torch.uint8, device=k.device)
         self.raw.work, self.raw.work_bytes = self.work.data_ptr(), n.value
+
+    def _st(self, stream) -> int:
+        return _raw_stream(self._device) if stream is None else stream.cuda_stream
 
     @classmethod
     def empty(cls, n_layers, n_pages, n_kv_heads, page_tokens, head_dim, max_seqs, max_pages,
@@ -94,78 +113,77 @@ class KvCache:
 
     def fork(self, src, dst, stream=None):
         """dst[i] becomes a sequence of src[i]'s tokens, sharing its pages."""
-        _ints(src, "src")
-        _ints(dst, "dst", src.numel())
-        _check(lib.moe_kv_fork(C.byref(self.raw), _ptr(src), _ptr(dst), src.numel(), _stream(stream)))
+        n = _ints(src, "src")
+        _ints(dst, "dst", n)
+        _ok(lib.moe_kv_fork(self._ref, src.data_ptr(), dst.data_ptr(), n, self._st(stream)))
 
     def reserve(self, seqs, n_new, stream=None):
         """Pages for n_new[i] more tokens of seqs[i]; their lengths grow by it."""
-        _ints(seqs, "seqs")
-        _ints(n_new, "n_new", seqs.numel())
-        _check(lib.moe_kv_reserve(C.byref(self.raw), _ptr(seqs), _ptr(n_new), seqs.numel(), _stream(stream)))
+        n = _ints(seqs, "seqs")
+        _ints(n_new, "n_new", n)
+        _ok(lib.moe_kv_reserve(self._ref, seqs.data_ptr(), n_new.data_ptr(), n, self._st(stream)))
 
     def write(self, layer, k, v, seqs, cu, stream=None):
         """Rows cu[i]..cu[i+1]-1 of k and v [rows, kv_heads, head_dim] become the newest tokens of seqs[i]."""
-        _ints(seqs, "seqs")
-        _ints(cu, "cu", seqs.numel() + 1)
-        Hkv, D = self.k.shape[2], self.k.shape[4]
-        ldk = _head_rows(k, "k", Hkv, D, self.k.dtype)
-        ldv = _head_rows(v, "v", Hkv, D, self.k.dtype)
-        if k.shape[0] != v.shape[0]:
+        n = _ints(seqs, "seqs")
+        _ints(cu, "cu", n + 1)
+        ldk = _head_rows(k, "k", self._kv_heads, self._dim, self._dtype)
+        ldv = _head_rows(v, "v", self._kv_heads, self._dim, self._dtype)
+        rows = k.shape[0]
+        if rows != v.shape[0]:
             raise ValueError("k and v must have as many rows")
-        _check(lib.moe_kv_write(C.byref(self.raw), layer, _ptr(k), ldk, _ptr(v), ldv, _ptr(seqs), _ptr(cu),
-                                seqs.numel(), k.shape[0], _stream(stream)))
+        _ok(lib.moe_kv_write(self._ref, layer, k.data_ptr(), ldk, v.data_ptr(), ldv, seqs.data_ptr(), cu.data_ptr(), n,
+                             rows, self._st(stream)))
 
     def free(self, seqs, stream=None):
-        _ints(seqs, "seqs")
-        _check(lib.moe_kv_free(C.byref(self.raw), _ptr(seqs), seqs.numel(), _stream(stream)))
+        """Drop sequences; pages that no other sequence names become free."""
+        n = _ints(seqs, "seqs")
+        _ok(lib.moe_kv_free(self._ref, seqs.data_ptr(), n, self._st(stream)))
 
     def compact(self, stream=None):
         """Move the pages in use to the lowest ids."""
-        _check(lib.moe_kv_compact(C.byref(self.raw), _stream(stream)))
+        _ok(lib.moe_kv_compact(self._ref, self._st(stream)))
 
     def copy_pages(self, src, dst, stream=None):
         """Copy whole pages src[i] -> dst[i] in every layer; table and ref are untouched."""
-        _ints(src, "src")
-        _ints(dst, "dst", src.numel())
-        _check(lib.moe_kv_copy_pages(C.byref(self.raw), _ptr(src), _ptr(dst), src.numel(), _stream(stream)))
+        n = _ints(src, "src")
+        _ints(dst, "dst", n)
+        _ok(lib.moe_kv_copy_pages(self._ref, src.data_ptr(), dst.data_ptr(), n, self._st(stream)))
 
     def check_errors(self, stream=None):
         """Synchronise, raise what kernels recorded on this cache, and clear it."""
-        _check(lib.moe_kv_check_errors(C.byref(self.raw), _stream(stream)))
+        _ok(lib.moe_kv_check_errors(self._ref, self._st(stream)))
 
-    def _out(self, q, out):
+    def _q_out(self, q, out):
+        """out (new if None) and the row strides of q and out."""
+        ldq = _head_rows(q, "q", None, self._dim, self._dtype)
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if out.shape != q.shape:
+        elif out.shape != q.shape:
             raise ValueError("out must have q's shape")
-        return out
+        return out, ldq, _head_rows(out, "out", None, self._dim, self._dtype)
 
     def attn_decode(self, layer, q, seqs, n_q=1, out=None, scale=None, window=0, sinks=0, stream=None):
         """Attention of the newest n_q tokens of each sequence: q [len(seqs) * n_q, heads, head_dim]."""
-        _ints(seqs, "seqs")
-        D = self.k.shape[4]
-        ldq = _head_rows(q, "q", None, D, self.k.dtype)
-        if q.shape[0] != seqs.numel() * n_q:
-            raise ValueError(f"q must have {seqs.numel()} x {n_q} rows (got {q.shape[0]})")
-        out = self._out(q, out)
-        ldo = _head_rows(out, "out", q.shape[1], D, self.k.dtype)
-        _check(lib.moe_attn_decode(C.byref(self.raw), layer, _ptr(q), ldq, _ptr(seqs), seqs.numel(), n_q, q.shape[1],
-                                   1.0 / math.sqrt(D) if scale is None else scale, window, sinks, _ptr(out), ldo,
-                                   _stream(stream)))
+        n = _ints(seqs, "seqs")
+        out, ldq, ldo = self._q_out(q, out)
+        rows, heads, dim = q.shape
+        if rows != n * n_q:
+            raise ValueError(f"q must have {n} x {n_q} rows (got {rows})")
+        _ok(lib.moe_attn_decode(self._ref, layer, q.data_ptr(), ldq, seqs.data_ptr(), n, n_q, heads,
+                                1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(), ldo,
+                                self._st(stream)))
         return out
 
     def attn_prefill(self, layer, q, seqs, cu, out=None, scale=None, window=0, sinks=0, stream=None):
         """Attention of chunks: rows cu[i]..cu[i+1]-1 of q are the newest tokens of seqs[i]."""
-        _ints(seqs, "seqs")
-        _ints(cu, "cu", seqs.numel() + 1)
-        D = self.k.shape[4]
-        ldq = _head_rows(q, "q", None, D, self.k.dtype)
-        out = self._out(q, out)
-        ldo = _head_rows(out, "out", q.shape[1], D, self.k.dtype)
-        _check(lib.moe_attn_prefill(C.byref(self.raw), layer, _ptr(q), ldq, _ptr(seqs), _ptr(cu), seqs.numel(),
-                                    q.shape[0], q.shape[1], 1.0 / math.sqrt(D) if scale is None else scale, window,
-                                    sinks, _ptr(out), ldo, _stream(stream)))
+        n = _ints(seqs, "seqs")
+        _ints(cu, "cu", n + 1)
+        out, ldq, ldo = self._q_out(q, out)
+        rows, heads, dim = q.shape
+        _ok(lib.moe_attn_prefill(self._ref, layer, q.data_ptr(), ldq, seqs.data_ptr(), cu.data_ptr(), n, rows, heads,
+                                 1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(), ldo,
+                                 self._st(stream)))
         return out
 
 
@@ -189,10 +207,11 @@ def quant_linear(x: torch.Tensor, w: torch.Tensor, quant: int, n_out: int, bias:
         raise ValueError(f"bias must be a contiguous float32 CUDA tensor of {n_out} entries")
     if y is None:
         y = torch.empty((T, n_out), dtype=x.dtype, device=x.device)
-    if y.shape != (T, n_out) or not y.is_cuda or (n_out > 1 and y.stride(1) != 1):
+    elif y.shape != (T, n_out) or not y.is_cuda or (n_out > 1 and y.stride(1) != 1):
         raise ValueError(f"y must be a [{T}, {n_out}] CUDA tensor with dense rows")
     ldx = x.stride(0) if T > 1 else max(x.stride(0), K)
     ldy = y.stride(0) if T > 1 else max(y.stride(0), n_out)
-    _check(lib.moe_quant_linear(_ptr(w), quant, n_out, K, _ptr(x), xt, ldx, T, _ptr(bias), _ptr(y),
-                                _dtype_id(y.dtype), ldy, _stream(stream)))
+    _ok(lib.moe_quant_linear(w.data_ptr(), quant, n_out, K, x.data_ptr(), xt, ldx, T,
+                             None if bias is None else bias.data_ptr(), y.data_ptr(), _dtype_id(y.dtype), ldy,
+                             _raw_stream(x.device.index) if stream is None else stream.cuda_stream))
     return y
