@@ -15,10 +15,12 @@
 //
 // Decode work split: the token tiles of all units (and a unit's fixed cost)
 // form one line, cut into one equal run per CTA (one CTA per SM). A run covers whole units or ends inside
-// one; a unit cut by run ends leaves partial (m, l, o) rows in the scratch and
-// the CTA that arrives last joins them in run order, so results do not depend
-// on arrival order. Every CTA derives the cut from the lengths itself: no
-// planning launch and no host copy of the lengths.
+// one; a unit cut by run ends leaves partial (m, l, o) rows in the scratch, and
+// a second small launch (a block per row, scheduled while the first drains)
+// joins them in run order, so results do not depend on timing. One CTA joining
+// a unit's parts after the last had arrived took up to 20 us of the 96 that
+// 4 x 32,768 tokens at D 256 took, against 3 for the launch. Every CTA derives
+// the cut from the lengths itself: no planning launch, no host copy of lengths.
 //
 // What bounds it: HBM. One warp walks the run and brings K and V tiles in by
 // TMA, a box per page, into a ring in shared memory; eight warps compute. The
@@ -29,6 +31,7 @@
 #include <cuda_bf16.h>
 
 #include "attn.cuh"
+#include "pdl.cuh"
 #include "prefill.h"
 #include "tc.cuh"
 
@@ -65,14 +68,13 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // A CTA's walk along the line: units in order, of each the tiles [t0, t1) that
-// fall into the run. On the line a unit is kUnitCost positions, for its Q and
-// its results, and then one per tile.
-constexpr int kUnitCost = 2;
-constexpr int kJoinGroup = 8;  // CTAs whose parts of a unit are joined first, where many hold one
+// fall into the run. On the line a unit is `cost` positions, for its Q and its
+// results, and then one per tile.
 struct Cursor {
   int b, rt, h;   // sequence, row tile, cache head
   int t, t0, t1;  // tile of the unit, and this run's
   int per;        // tiles of the unit
+  int cost;
   int64_t tiles0; // line position of the unit's first tile
   int64_t end;    // end of the run
   Seq s;
@@ -82,7 +84,7 @@ struct Cursor {
     t1 = static_cast<int>(min(end - tiles0, static_cast<int64_t>(per)));
     t = t0;
   }
-  __device__ __forceinline__ bool more() const { return tiles0 + per + kUnitCost < end; }
+  __device__ __forceinline__ bool more() const { return tiles0 + per + cost < end; }
 };
 
 template <int KT>
@@ -94,7 +96,7 @@ __device__ __forceinline__ void open_seq(const AttnArgs& a, Cursor& c) {
 // The next unit (decode); only called while c.more(), so there is one with a tile.
 template <int KT>
 __device__ __forceinline__ void next_unit(const AttnArgs& a, Cursor& c) {
-  c.tiles0 += c.per + kUnitCost;
+  c.tiles0 += c.per + c.cost;
   if (++c.h == a.Hkv) {
     c.h = 0;
     if (++c.rt == a.row_tiles) {
@@ -131,6 +133,9 @@ struct MmaEngine {
   static constexpr int DP = DP_, RG = RG_, KT = KT_;
   static constexpr int KG = kWarps / RG, kRows = RG * 16, KC = KT / KG / 16;
   static constexpr int NB = DP / 64;  // column blocks
+  // A unit's Q, edge tile and results take 12,000 cycles at DP 256 and 6,000
+  // below, a tile of 64 KB of K and V 2,800 at the HBM rate.
+  static constexpr int kUnitCost = DP > 128 ? 4 : 2;
   static constexpr uint32_t kTileBytes = KT * DP * 2;
   // Q of large heads stays in shared memory: its fragments would not fit
   // beside the results' in registers
@@ -175,18 +180,26 @@ struct MmaEngine {
       // this warp's rows, a lane a 16-byte piece; the KG warps of a row group
       // write the same
       static_assert(DP / 8 == 32, "a lane a piece");
-#pragma unroll 8
-      for (int rr = 0; rr < 16; ++rr) {
-        const int r = first + rr;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (r < total && lane * 8 < a.D) {
-          const int i = r / a.g;
-          v = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (c.s.row0 + i) * a.ldq +
-                                                   (c.h * a.g + r - i * a.g) * a.D) + lane);
+      int i = first / a.g, hq = first - i * a.g;
+      const T* src = static_cast<const T*>(a.q) + c.h * a.g * a.D + lane * 8;
+#pragma unroll 1
+      for (int r0 = 0; r0 < 16; r0 += 8) {
+        uint4 v[8];  // eight loads in flight
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          v[x] = make_uint4(0u, 0u, 0u, 0u);
+          if (first + r0 + x < total && lane * 8 < a.D)
+            v[x] = __ldg(reinterpret_cast<const uint4*>(src + (c.s.row0 + i) * a.ldq + hq * a.D));
+          if (++hq == a.g) {
+            hq = 0;
+            ++i;
+          }
         }
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(qs + (rg * 16 + rr) * kQPitch + lane * 16), "r"(v.x),
-                     "r"(v.y), "r"(v.z), "r"(v.w)
-                     : "memory");
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(qs + (rg * 16 + r0 + x) * kQPitch + lane * 16),
+                       "r"(v[x].x), "r"(v[x].y), "r"(v[x].z), "r"(v[x].w)
+                       : "memory");
       }
       __syncwarp();
     } else {
@@ -332,6 +345,7 @@ struct MmaEngine {
     const int lane = threadIdx.x & 31;
     const int j0 = c.sp.tile(c.t) * KT + key0;
     bool bad = false;
+#pragma unroll 4
     for (int i = lane; i < 16 * NB * 8; i += 32) {
       const int r = (i >> 3) & 15, j = j0 + r;
       const uint32_t at = vt.row<NB>(key0 + r) + (i >> 7) * vt.block() + ((i & 7) << 4);
@@ -341,8 +355,7 @@ struct MmaEngine {
         uint32_t w[4];
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(at)
-                     : "memory");
+                     : "r"(at));
         bad |= nonfinite2(w[0]) || nonfinite2(w[1]) || nonfinite2(w[2]) || nonfinite2(w[3]);
       }
     }
@@ -443,6 +456,7 @@ struct FmaEngine {
   using T = float;
   static constexpr int DP = DP_, kRows = R_, KT = DP == 256 ? 32 : 64;
   static constexpr int NB = DP / 32;                // column blocks
+  static constexpr int kUnitCost = 3;               // as the bf16 engine's
   static constexpr uint32_t kTileBytes = KT * DP * 4;
   static constexpr int kC4 = DP / 4;                // column quads
   static constexpr int TPW = KT / kWarps;           // tokens a warp (scores)
@@ -710,11 +724,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int64_t s_scan[kThreads / 32];
   __shared__ int64_t s_found[2];
   __shared__ float2 s_ml[kWarps * 16];
-  __shared__ int s_last, s_abort;
+  __shared__ int s_abort;
   const uint32_t ring = su32(sm);
   if (ring & 1023u) {  // the swizzle's pattern starts at such a boundary
     if (threadIdx.x == 0) atomicOr(a.err, MOE_DEVERR_TIMEOUT);
     return;
+  }
+  if (SPLIT) {
+    pdl_trigger();  // the joining launch may be scheduled; it waits for this one's end
+    if (threadIdx.x == 0) a.cuts[blockIdx.x].count = 0;
   }
   float* merge = reinterpret_cast<float*>(sm + NS * E::kTileBytes);
   const int rt_n = a.row_tiles;
@@ -733,18 +751,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- this CTA's run of the line
   Cursor cp;
+  cp.cost = SPLIT ? E::kUnitCost : 0;
   int64_t run0 = 0, total = 1;
   if (SPLIT) {
     auto line_of = [&](int b) -> int64_t {  // positions of a sequence
       if (b >= a.n) return 0;
       Seq s = load_seq(a, b);
-      return static_cast<int64_t>(span_of<KT>(a, s, 0, s.m).n + kUnitCost) * rt_n * a.Hkv;
+      return static_cast<int64_t>(span_of<KT>(a, s, 0, s.m).n + E::kUnitCost) * rt_n * a.Hkv;
     };
-    int64_t mine = 0, all = 0;
+    int64_t mine = 0, ex = 0, all = 0;
     for (int b0 = 0; b0 < a.n; b0 += kThreads) {
       mine = line_of(b0 + threadIdx.x);
       int64_t t;
-      block_scan(mine, s_scan, &t);
+      ex = block_scan(mine, s_scan, &t);
       all += t;
     }
     total = all;
@@ -753,9 +772,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     run0 = runs.start(blockIdx.x);
     int64_t base = 0;
     for (int b0 = 0; b0 < a.n; b0 += kThreads) {
-      if (a.n > kThreads) mine = line_of(b0 + threadIdx.x);
-      int64_t t;
-      const int64_t ex = base + block_scan(mine, s_scan, &t);
+      int64_t t = total;
+      if (a.n > kThreads) {
+        mine = line_of(b0 + threadIdx.x);
+        ex = base + block_scan(mine, s_scan, &t);
+      }
       if (run0 >= ex && run0 < ex + mine) {
         s_found[0] = b0 + threadIdx.x;
         s_found[1] = ex;
@@ -766,10 +787,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     cp.b = static_cast<int>(s_found[0]);
     open_seq<KT>(a, cp);
-    const int u = static_cast<int>((run0 - s_found[1]) / (cp.per + kUnitCost));
+    const int u = static_cast<int>(quotient(run0 - s_found[1], cp.per + E::kUnitCost));
     cp.rt = u / a.Hkv;
     cp.h = u % a.Hkv;
-    cp.tiles0 = s_found[1] + static_cast<int64_t>(u) * (cp.per + kUnitCost) + kUnitCost;
+    cp.tiles0 = s_found[1] + static_cast<int64_t>(u) * (cp.per + E::kUnitCost) + E::kUnitCost;
     cp.end = runs.start(blockIdx.x + 1);
     cp.open(run0);
     if (cp.t1 <= cp.t0) return;  // a run within a unit's fixed cost
@@ -900,94 +921,91 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<float4*>(mine + r * kPS + 4 + col) = v;
         if (col == 0) *reinterpret_cast<float2*>(mine + r * kPS) = make_float2(M, L);
       });
-      // CTAs that hold a part of this unit: those whose runs meet its tiles;
-      // only c0's run starts no later than they do
-      const Runs runs(total, gridDim.x);
-      const int c0 = static_cast<int>(runs.of(cp.tiles0)), c1 = static_cast<int>(runs.of(cp.tiles0 + cp.per - 1));
-      const int me = blockIdx.x;
-      const int rows = min(R, cp.s.m * a.g - cp.rt * R), c4n = a.D / 4;
-      auto slot_of = [&](int c) { return a.part + (2 * c + (c == c0 ? 1 : 0)) * kSlot; };
-      // arrive at a ticket; true for the last of `count`
-      auto last_of = [&](unsigned int* ticket, int count) {
-        __threadfence();
-        sync_compute();
-        if (threadIdx.x == 0) {
-          s_last = atomicAdd(ticket, 1u) == static_cast<unsigned int>(count - 1);
-          if (s_last) *ticket = 0u;  // zero between launches
-        }
-        sync_compute();
-        if (s_last) __threadfence();
-        return s_last != 0;
-      };
-      // Join `count` (at most 32) partial results: row r of the i-th at
-      // part(i) + r * kPS, its (m, l) at offset hdr. A warp first forms a row's
-      // weights, a lane a part; the sums' loads then depend on nothing.
-      auto join = [&](auto&& part, int count, int hdr, auto&& emit) {
-        float* const wts = merge;                                  // [rows][32]
-        float2* const tot = reinterpret_cast<float2*>(merge + kPartRows * 32);  // (M, L) of a row
-        for (int r = warp; r < rows; r += kWarps) {
-          float2 ml = make_float2(-INFINITY, 0.f);
-          if (lane < count) ml = __ldcg(reinterpret_cast<const float2*>(part(lane) + r * kPS + hdr));
-          float M = ml.x;
-#pragma unroll
-          for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
-          const float f = ex2(ml.x - (M == -INFINITY ? 0.f : M));
-          float L = f * ml.y;
-#pragma unroll
-          for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
-          wts[r * 32 + lane] = lane < count ? f : 0.f;
-          if (lane == 0) tot[r] = make_float2(M, L);
-        }
-        sync_compute();
-        for (int e = threadIdx.x; e < rows * c4n; e += kCompute) {
-          const int r = e / c4n, col = (e - r * c4n) * 4;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int i0 = 0; i0 < count; i0 += 16) {
-            float4 u[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              u[i] = i0 + i < count ? __ldcg(reinterpret_cast<const float4*>(part(i0 + i) + r * kPS + 4 + col))
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float f = wts[r * 32 + i0 + i];
-              v.x += f * u[i].x;
-              v.y += f * u[i].y;
-              v.z += f * u[i].z;
-              v.w += f * u[i].w;
-            }
-          }
-          emit(r, col, v, tot[r].x, tot[r].y);
-        }
-        sync_compute();
-      };
-      auto finish = [&](int r, int col, float4 v, float, float L) {
-        write_out<typename E::T>(a, cp, R, r, col, v, L);
-      };
-      unsigned int* const t_unit = a.tickets + c0;  // only one unit can start in c0's run and leave it
-      if (c1 - c0 < kJoinGroup * 2) {
-        if (last_of(t_unit, c1 - c0 + 1)) join([&](int i) { return slot_of(c0 + i); }, c1 - c0 + 1, 0, finish);
-      } else {
-        // many parts: groups of kJoinGroup CTAs first (their result goes to the
-        // first one's slot, its (m, l) behind that part's own), then the groups
-        const int g = me / kJoinGroup, g0 = c0 / kJoinGroup, g1 = c1 / kJoinGroup;
-        auto first_of = [&](int k) { return max(c0, k * kJoinGroup); };
-        const int f = first_of(g), n = min(c1, g * kJoinGroup + kJoinGroup - 1) - f + 1;
-        unsigned int* const t_group = a.tickets + (f == c0 ? 1 : 2) * static_cast<int>(gridDim.x) + f;
-        if (last_of(t_group, n)) {
-          join([&](int i) { return slot_of(f + i); }, n, 0, [&](int r, int col, float4 v, float M, float L) {
-            float* p = slot_of(f) + r * kPS;
-            *reinterpret_cast<float4*>(p + 4 + col) = v;
-            if (col == 0) *reinterpret_cast<float2*>(p + 2) = make_float2(M, L);
-          });
-          if (last_of(t_unit, g1 - g0 + 1))
-            join([&](int i) { return slot_of(first_of(g0 + i)); }, g1 - g0 + 1, 2, finish);
-        }
+      if (threadIdx.x == 0 && run0 <= cp.tiles0) {  // the unit's first part: the record for the join
+        const Runs runs(total, gridDim.x);
+        Cut cut;
+        cut.count = static_cast<int>(runs.of(cp.tiles0 + cp.per - 1)) - static_cast<int>(blockIdx.x) + 1;
+        cut.rt = cp.rt;
+        cut.h = cp.h;
+        cut.row0 = cp.s.row0;
+        cut.m = cp.s.m;
+        cut.len = cp.s.len;
+        a.cuts[blockIdx.x] = cut;
       }
     }
     if (!cp.more()) break;
     next_unit<KT>(a, cp);
   }
+}
+
+// Join of one row of the unit whose first part is CTA c0's (blockIdx.x): the
+// threads are DP / 4 column quads by part groups; the groups are added in order.
+// Only c0's run starts no later than the unit's tiles, so its part is in its
+// slot 1 and the others' in slot 0.
+constexpr int kJoinThreads = 256;
+constexpr int kMostParts = 256;  // CTAs of a launch
+template <class T, int DP>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int rows_per_tile) {
+  constexpr int kC4 = DP / 4, kPG = kJoinThreads / kC4, kPS = DP + 4;
+  constexpr int64_t kSlot = static_cast<int64_t>(kPartRows) * kPS;
+  __shared__ float s_w[kMostParts];
+  __shared__ float s_red[kJoinThreads / 32];
+  __shared__ float4 s_sum[kJoinThreads];
+  pdl_wait();
+  const Cut cut = a.cuts[blockIdx.x];
+  const int r = blockIdx.y;
+  if (cut.count == 0 || r >= min(rows_per_tile, cut.m * a.g - cut.rt * rows_per_tile)) return;
+  const int c0 = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  auto part = [&](int i) { return a.part + (2 * (c0 + i) + (i == 0 ? 1 : 0)) * kSlot + r * kPS; };
+  const int c4 = tid % kC4, pg = tid / kC4;
+  // a part's weight is 2^(m_i - M); parts are at most as many as threads
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (tid < cut.count) ml = __ldcg(reinterpret_cast<const float2*>(part(tid)));
+  float M = ml.x;
+#pragma unroll
+  for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
+  if (lane == 0) s_red[tid >> 5] = M;
+  __syncthreads();
+  M = s_red[lane & 7];
+#pragma unroll
+  for (int x = 4; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
+  const float w = ex2(ml.x - (M == -INFINITY ? 0.f : M));
+  s_w[tid] = tid < cut.count ? w : 0.f;
+  float L = tid < cut.count ? w * ml.y : 0.f;
+#pragma unroll
+  for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
+  __syncthreads();
+  if (lane == 0) s_red[tid >> 5] = L;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c4 * 4 < a.D) {
+#pragma unroll 8
+    for (int i = pg; i < cut.count; i += kPG) {
+      const float4 u = __ldcg(reinterpret_cast<const float4*>(part(i) + 4 + c4 * 4));
+      const float f = s_w[i];
+      v.x += f * u.x;
+      v.y += f * u.y;
+      v.z += f * u.z;
+      v.w += f * u.w;
+    }
+  }
+  s_sum[tid] = v;
+  __syncthreads();
+  if (pg > 0 || c4 * 4 >= a.D) return;
+  L = 0.f;
+#pragma unroll
+  for (int i = 0; i < kJoinThreads / 32; ++i) L += s_red[i];
+#pragma unroll
+  for (int i = 1; i < kPG; ++i) {
+    const float4 u = s_sum[i * kC4 + c4];
+    v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+  }
+  Cursor c;
+  c.rt = cut.rt;
+  c.h = cut.h;
+  c.s.row0 = cut.row0;
+  c.s.m = cut.m;
+  c.s.len = cut.len;
+  write_out<T>(a, c, rows_per_tile, r, c4 * 4, v, L);
 }
 
 template <class E, bool SPLIT>
@@ -1012,7 +1030,11 @@ cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
 template <class E>
 cudaError_t decode_rows(AttnArgs a, int num_sms, cudaStream_t st) {
   a.row_tiles = (a.n_q * a.g + E::kRows - 1) / E::kRows;
-  return launch<E, true>(a, num_sms, st);
+  const int ctas = std::min(num_sms, kMostParts);
+  cudaError_t e = launch<E, true>(a, ctas, st);
+  if (e != cudaSuccess) return e;
+  return pdl_launch(join_kernel<typename E::T, E::DP>, dim3(ctas, std::min(E::kRows, a.n_q * a.g)), dim3(kJoinThreads), 0,
+                    st, a, E::kRows);
 }
 
 // f32: four rows a unit if that holds them all, else sixteen

@@ -194,7 +194,7 @@ __device__ __forceinline__ int unit_count(const AttnArgs& a, int m) {
 __device__ __forceinline__ Span unit_span(const AttnArgs& a, const Seq& s, int rt) {
   const int64_t r0 = static_cast<int64_t>(rt) * kUnitRows, total = static_cast<int64_t>(s.m) * a.g;
   const int64_t r1 = min(r0 + kUnitRows, total) - 1;
-  return span_of<kKT>(a, s, static_cast<int>(r0 / a.g), static_cast<int>(r1 / a.g) + 1);
+  return span_of<kKT>(a, s, static_cast<int>(quotient(r0, a.g)), static_cast<int>(quotient(r1, a.g)) + 1);
 }
 // The segment from line position `at` (inside the unit) on.
 __device__ __forceinline__ void open_unit(const AttnArgs& a, Walk& w, int64_t at) {
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Walk w;
       w.b = b;
       w.rt = rt;
-      w.h = static_cast<int>((run0 - at) / per);
+      w.h = static_cast<int>(quotient(run0 - at, per));
       w.unit0 = at + w.h * per;
       w.end = run1;
       w.s = load_seq(a, b);
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kPieces = DP / 8, kRowsPer = 32 / kPieces;
         const int p = lane % kPieces, rows = w.rows - t * kQT;
         const int64_t rg = static_cast<int64_t>(w.rt) * kUnitRows + t * kQT + lane / kPieces;
-        int i = static_cast<int>(rg / a.g), hq = static_cast<int>(rg - static_cast<int64_t>(i) * a.g);
+        int i = static_cast<int>(quotient(rg, a.g)), hq = static_cast<int>(rg - static_cast<int64_t>(i) * a.g);
         const __nv_bfloat16* qh = static_cast<const __nv_bfloat16*>(a.q) + static_cast<int64_t>(w.h * a.g) * a.D + p * 8;
 #pragma unroll 4
         for (int r = lane / kPieces; r < kQT; r += kRowsPer) {
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(su32(&sh.qr[t]));
       }
-      const int lo_pos = w.s.len - w.s.m + static_cast<int>(static_cast<int64_t>(w.rt) * kUnitRows / a.g);
+      const int lo_pos = w.s.len - w.s.m + static_cast<int>(quotient(static_cast<int64_t>(w.rt) * kUnitRows, a.g));
       const int hi_pos = w.sp.end - 1;
       for (int i = 0; i < w.nt; ++i) {
         ok = mbar_wait(su32(&sh.vf[vp.s]), vp.ph, abort_flag, a.err, wait_cycles);
@@ -605,12 +605,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t * kQT < w.rows) {
         const bool row_ok = t * kQT + r < w.rows;
         const int64_t rg = static_cast<int64_t>(w.rt) * kUnitRows + t * kQT + r;
-        const int qi = static_cast<int>(rg / a.g);
+        const int qi = static_cast<int>(quotient(rg, a.g));
         const int pos = row_ok ? w.s.len - w.s.m + qi : -1;
         // positions of the warp's rows, for the tiles that need no mask
-        const int lo_pos = w.s.len - w.s.m + static_cast<int>((rg - lane) / a.g);
+        const int lo_pos = w.s.len - w.s.m + static_cast<int>(quotient(rg - lane, a.g));
         const int64_t r_last = min(rg - lane + 31, static_cast<int64_t>(w.s.m) * a.g - 1);
-        const int hi_pos = w.s.len - w.s.m + static_cast<int>(r_last / a.g);
+        const int hi_pos = w.s.len - w.s.m + static_cast<int>(quotient(r_last, a.g));
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < w.nt; ++j) {
           ok = mbar_wait(su32(&sh.sr[t]), s_ph, abort_flag, a.err, wait_cycles);

@@ -134,6 +134,7 @@ moe_status_t attention(const char* call, bool decode, const moe_kv_t* kv, int32_
   char* w = static_cast<char*>(kv->work);
   a.part = reinterpret_cast<float*>(w + l.part);
   a.tickets = reinterpret_cast<unsigned int*>(w + l.tickets);
+  a.cuts = reinterpret_cast<moe::Cut*>(w + l.cuts);
   a.err = &reinterpret_cast<moe::KvWork*>(w)->err;
   return launched(call, decode ? moe::launch_attn_decode(a, kv->dtype, sms, stream)
                                : moe::launch_attn_prefill(a, kv->dtype, rows, sms, stream));
@@ -159,6 +160,7 @@ KvLayout kv_layout(const moe_kv_t& kv, int num_sms) {
   l.shr = take(kv.n_pages * 4ll);
   l.last = take(kv.n_pages * 4ll);
   l.tickets = take(num_sms * kPrefillTickets * 4ll);
+  l.cuts = take(num_sms * static_cast<int64_t>(sizeof(Cut)));
   // two partial results a CTA: rows of (m, l, -, -, head size padded)
   const int64_t dp = kv.head_dim <= 64 ? 64 : (kv.head_dim <= 128 ? 128 : 256);
   const bool tc = kv.dtype == MOE_BF16 && kv.head_dim <= kTcHeadDim;

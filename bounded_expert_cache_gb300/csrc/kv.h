@@ -23,17 +23,23 @@ struct KvWork {
   int32_t pad[61];
 };
 constexpr int kPartRows = 64;        // most rows of one partial result (decode)
-constexpr int kPrefillTickets = 8;   // tickets a CTA (prefill; decode uses one)
+constexpr int kPrefillTickets = 8;   // tickets a CTA (prefill)
 constexpr int kPrefillPartRows = 256;
 constexpr int kTcHeadDim = 128;      // largest head size of the tensor-core prefill
 
 struct KvLayout {
   // byte offsets into the scratch: page lists (src, dst, map, shr, last: one
-  // int per page; filled: one per listed sequence), tickets, partial results
-  int64_t src, dst, filled, map, shr, last, tickets, part, bytes;
+  // int per page; filled: one per listed sequence), tickets, records of cut units, partial results
+  int64_t src, dst, filled, map, shr, last, tickets, cuts, part, bytes;
 };
 constexpr int kMaxList = 8192;  // most sequences of one page call
 KvLayout kv_layout(const moe_kv_t& kv, int num_sms);
+
+// A unit that several CTAs of moe_attn_decode hold parts of, recorded by the
+// first of them: the parts are in CTAs c .. c + count - 1.
+struct Cut {
+  int32_t count, rt, h, row0, m, len;
+};
 
 struct AttnArgs {
   const void* q;
@@ -50,7 +56,8 @@ struct AttnArgs {
   float scale_log2;     // scale * log2(e)
   int32_t window, sinks;
   float* part;          // partial results
-  unsigned int* tickets;
+  unsigned int* tickets;  // prefill: arrivals at a cut unit
+  Cut* cuts;              // decode: [CTAs]
   uint32_t* err;
   int32_t row_tiles;    // row tiles a sequence and cache head (decode)
 };
