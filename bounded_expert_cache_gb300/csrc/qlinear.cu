@@ -3,8 +3,23 @@
 //   Q4_0 (groups of 32):    y[t,n] = sum_g d_g sum_{k in g} (q_k - 8) x_k
 //   I4_G64 (groups of 64):  y[t,n] = sum_g (s_g sum_{k in g} q_k x_k + b_g sum_{k in g} x_k)
 //
-// What bounds it: HBM, the 4.5 bits a weight. A warp takes one row; its lanes
-// take 16 weight bytes (32 weights) each, four tokens at a time.
+// What bounds it: HBM, the 4.5 bits a weight, as long as a weight costs less
+// than about three instructions of a thread. The inner sums therefore run on
+// warp-level matrix instructions (m16n8k16, weights as A, tokens as B): codes
+// become bf16 integers by two byte permutes and a subtraction for eight of them,
+// products of a 4-bit integer and a bf16 are exact, sums are fp32, and the
+// group's factor is applied in fp32 to the 16 x 8 sums. An fp32 x is the exact
+// sum of three bf16 (8 + 8 + 8 significand bits), one instruction each.
+//
+// The order of k within an instruction is free as long as A and B agree, so x
+// is stored in the order in which a lane's 4-byte word yields its eight codes:
+// a lane's eight x of a group are 16 contiguous bytes.
+//
+// A CTA holds the tokens' x in shared memory (in slices of K if they do not
+// fit) and walks row tiles. Its eight warps are 8 / WK groups of 16 rows by WK
+// slices of K, so that a matrix of few rows still fills the GPU; the slices are
+// added in shared memory. A stage is 16 rows x 256 k a warp: 16 KB of codes, 2 KB
+// of scales, by 16-byte asynchronous copies into a ring.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -13,103 +28,407 @@
 namespace moe {
 namespace {
 
-constexpr int kTok = 4;
+constexpr int kThreads = 256, kWarps = 8;
+constexpr int kWK = 256;                      // k of a warp's stage
+constexpr int kCodeBytes = kWarps * 16 * 128; // codes of a stage
+constexpr int kMetaBytes = kWarps * 16 * 16;  // scales of a stage
+constexpr int kStageBytes = kCodeBytes + kMetaBytes;
+constexpr int kMaxTok = 24;                   // tokens of a launch's y block
 
-template <class X>
-__device__ __forceinline__ void load8(const X* p, float* v);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float* v) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+struct Plan {
+  int tok;         // tokens of a block
+  int kx;          // k of a slice of x, a multiple of 256 * WK
+  int x_pitch;     // bytes of a token's slice: 64 modulo 128
+  int x_bytes;     // all tokens and parts
+  int slots;       // ring
+  int tiles;       // row tiles
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* v) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Codes of a 4-byte word as bf16 integers less `bias` - 128: the nibble becomes
+// the low mantissa bits of 128 (exact), bias is subtracted (exact).
+// o[0], o[1]: low nibbles of bytes 0,1 and 2,3; o[2], o[3]: high nibbles.
+__device__ __forceinline__ void codes(uint32_t w, uint32_t bias2, uint32_t* o) {
+  const uint32_t v01 = __byte_perm(w, 0, 0x4140), v23 = __byte_perm(w, 0, 0x4342);
+  o[0] = (v01 & 0x000F000Fu) | 0x43004300u;
+  o[1] = (v23 & 0x000F000Fu) | 0x43004300u;
+  o[2] = ((v01 >> 4) & 0x000F000Fu) | 0x43004300u;
+  o[3] = ((v23 >> 4) & 0x000F000Fu) | 0x43004300u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  for (int i = 0; i < 4; ++i) asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(o[i]) : "r"(bias2));
+}
+
+// The three bf16 of an fp32: each the leading 8 significand bits of what is
+// left, so their sum is exact. Infinities and NaN stay in the first.
+__device__ __forceinline__ void split3(float x, uint32_t* p) {
+  const uint32_t u = __float_as_uint(x);
+  const bool odd = (u & 0x7F800000u) == 0x7F800000u;
+  p[0] = odd && (u & 0x007FFFFFu) ? 0x7FC0u : u >> 16;
+  const float r1 = odd ? 0.f : x - __uint_as_float(u & 0xFFFF0000u);
+  const uint32_t u1 = __float_as_uint(r1);
+  p[1] = u1 >> 16;
+  p[2] = __float_as_uint(r1 - __uint_as_float(u1 & 0xFFFF0000u)) >> 16;
+}
+
+// x of tokens [t0, t0 + tok) and k [k0, k0 + kx) to shared memory, zeros past K;
+// for I4_G64 also each token's sum over every group of 64.
+template <int QUANT, bool XF32>
+__device__ __forceinline__ void load_x(const LinearArgs& a, const Plan& p, int t0, int tok, int k0, uint32_t xs,
+                                       float* sums) {
+  constexpr int kParts = XF32 ? 3 : 1;
+  const int chunks = p.kx / 8;  // of 8 x: (group of 32, lane of a quad)
+  const int part_bytes = p.tok * p.x_pitch;
+  const int total = tok * chunks;  // kx is a multiple of 256: a warp has 32 chunks of one token
+#pragma unroll 2
+  for (int e = threadIdx.x; e < total; e += kThreads) {
+    const int t = e / chunks, c = e - t * chunks;
+    // element offsets of the two runs of four
+    const int ka = QUANT == MOE_Q4_0 ? k0 + (c >> 2) * 32 + (c & 3) * 4 : k0 + c * 8;
+    const int kb = QUANT == MOE_Q4_0 ? ka + 16 : ka + 4;
+    const bool in = ka < a.K;  // K is a multiple of 32: both runs are in or out
+    const uint32_t at = xs + t * p.x_pitch + c * 16;
+    float sum = 0.f;
+    if constexpr (XF32) {
+      const float* x = static_cast<const float*>(a.x) + (t0 + t) * a.ldx;
+      float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+      if (in) {
+        u = __ldg(reinterpret_cast<const float4*>(x + ka));
+        v = __ldg(reinterpret_cast<const float4*>(x + kb));
+      }
+      float f[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+      if (QUANT != MOE_Q4_0) {
+        sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+        const float g[8] = {f[0], f[2], f[4], f[6], f[1], f[3], f[5], f[7]};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = g[i];
+      }
+      uint32_t s[8][3];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) split3(f[i], s[i]);
+#pragma unroll
+      for (int q = 0; q < kParts; ++q)
+        sts128(at + q * part_bytes, make_uint4(s[0][q] | s[1][q] << 16, s[2][q] | s[3][q] << 16,
+                                               s[4][q] | s[5][q] << 16, s[6][q] | s[7][q] << 16));
+    } else {
+      const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + (t0 + t) * a.ldx;
+      uint2 u = make_uint2(0u, 0u), v = u;
+      if (in) {
+        u = __ldg(reinterpret_cast<const uint2*>(x + ka));
+        v = __ldg(reinterpret_cast<const uint2*>(x + kb));
+      }
+      if (QUANT == MOE_Q4_0) {
+        sts128(at, make_uint4(u.x, u.y, v.x, v.y));
+      } else {
+        const uint32_t w[4] = {u.x, u.y, v.x, v.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += __uint_as_float(w[i] << 16) + __uint_as_float(w[i] & 0xFFFF0000u);
+        sts128(at, make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(v.x, v.y, 0x5410),
+                              __byte_perm(u.x, u.y, 0x7632), __byte_perm(v.x, v.y, 0x7632)));
+      }
+    }
+    if (QUANT != MOE_Q4_0) {
+      // eight lanes hold a group of 64
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
+      if ((c & 7) == 0) sums[(c >> 3) * kMaxTok + t] = sum;
+    }
   }
 }
 
-template <class X, class Y, int QUANT>
-__global__ void __launch_bounds__(256) linear_kernel(LinearArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int n = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (n >= a.N) return;
-  const int t0 = blockIdx.y * kTok, nt = min(kTok, a.T - t0);
-  const uint8_t* row = a.w + static_cast<int64_t>(n) * (a.K / 2);
-  const uint8_t* meta = a.meta + static_cast<int64_t>(n) * (a.K / 16);
-  float acc[kTok] = {};
-  for (int b = lane; b < a.K / 32; b += 32) {
-    const uint4 w4 = __ldg(reinterpret_cast<const uint4*>(row) + b);
-    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-    float s, bias = 0.f;
-    if (QUANT == MOE_Q4_0) {
-      s = __half2float(__ldg(reinterpret_cast<const __half*>(meta) + b));
-    } else {
-      const uint32_t sb = __ldg(reinterpret_cast<const uint32_t*>(meta) + b / 2);
-      s = __uint_as_float(sb << 16);
-      bias = __uint_as_float(sb & 0xFFFF0000u);
-    }
+template <int QUANT, bool XF32, int NT, int WK>
+__global__ void __launch_bounds__(kThreads, 2) linear_kernel(LinearArgs a, Plan p) {
+  constexpr int kParts = XF32 ? 3 : 1, R = 16 * kWarps / WK;  // rows of a tile
+  extern __shared__ __align__(128) unsigned char sm[];
+  const uint32_t ring = smem_u32(sm), xs = ring + p.slots * kStageBytes;
+  float* const sums = reinterpret_cast<float*>(sm + p.slots * kStageBytes + p.x_bytes);
+  float* const red = sums + (QUANT == MOE_Q4_0 ? 0 : p.kx / 64 * kMaxTok);  // [8 warps][16 rows][8 NT]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int wr = warp / WK, wk = warp % WK;  // row group, slice of K
+  const int t0 = blockIdx.y * p.tok, tok = min(p.tok, a.T - t0);
+  const int stage_k = kWK * WK;
+  const int n_slices = (a.K + p.kx - 1) / p.kx;
+  const int my_tiles = (p.tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  const int stages_tile = (a.K + stage_k - 1) / stage_k;  // slices hold whole stages
+  const int total = my_tiles * stages_tile;
+
+  // One stage: codes [wk][row][128 bytes], 16-byte pieces (32 codes) swizzled by
+  // the row; scales [wk][row][16 bytes]. Zeros past N and K.
+  int ld_tile = blockIdx.x, ld_stage = 0, ld_slot = 0, issued = 0;
+  auto issue = [&]() {
+    if (issued < total) {
+      const uint32_t st = ring + ld_slot * kStageBytes;
+      const int n0 = ld_tile * R, k0 = ld_stage * stage_k;
 #pragma unroll
-    for (int t = 0; t < kTok; ++t) {
-      if (t >= nt) break;
-      const X* x = static_cast<const X*>(a.x) + (t0 + t) * a.ldx + b * 32;
-      float dot = 0.f, sum = 0.f;
+      for (int i = 0; i < kCodeBytes / 16 / kThreads; ++i) {
+        const int e = tid + i * kThreads, piece = e & 7, row = (e >> 3) % R, w = (e >> 3) / R;
+        const int n = n0 + row, k = k0 + w * kWK + piece * 32;
+        const bool in = n < a.N && k < a.K;
+        cp16(st + (e >> 3) * 128 + ((piece ^ (row & 7)) << 4),
+             in ? a.w + static_cast<int64_t>(n) * (a.K / 2) + k / 2 : a.w, in);
+      }
+      if (tid < kWarps * 16) {
+        const int row = tid % R, w = tid / R, n = n0 + row, k = k0 + w * kWK;
+        const uint32_t dst = st + kCodeBytes + tid * 16;
+        const uint8_t* src = a.meta + static_cast<int64_t>(n) * (a.K / 16) + k / 16;
+        if ((a.K & 255) == 0) {
+          const bool in = n < a.N && k < a.K;
+          cp16(dst, in ? src : a.meta, in);
+        } else if ((a.K & 63) == 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float v[8];
-        load8<X>(x + 8 * i, v);
+          for (int i = 0; i < 4; ++i) {
+            const bool in = n < a.N && k + i * 64 < a.K;
+            cp4(dst + i * 4, in ? src + i * 4 : a.meta, in);
+          }
+        } else {  // an odd number of groups a row: scales are 2-byte aligned
+          uint32_t v[4] = {};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          // Q4_0: elements 0-15 are the low nibbles of bytes 0-15, 16-31 the high ones
-          const int e = 8 * i + j;
-          const int byte = QUANT == MOE_Q4_0 ? e & 15 : e / 2, high = QUANT == MOE_Q4_0 ? e >> 4 : e & 1;
-          const int q = (w[byte >> 2] >> ((byte & 3) * 8 + high * 4)) & 15;
-          dot += static_cast<float>(QUANT == MOE_Q4_0 ? q - 8 : q) * v[j];
-          sum += v[j];
+          for (int i = 0; i < 8; ++i)
+            if (n < a.N && k + i * 32 < a.K)
+              v[i >> 1] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(src) + i)) << (16 * (i & 1));
+          sts128(dst, make_uint4(v[0], v[1], v[2], v[3]));
         }
       }
-      acc[t] += s * dot;
-      if (QUANT != MOE_Q4_0) acc[t] += bias * sum;
+      ++issued;
+      if (++ld_slot == p.slots) ld_slot = 0;
+      if (++ld_stage == stages_tile) {
+        ld_stage = 0;
+        ld_tile += gridDim.x;
+      }
     }
-  }
+    asm volatile("cp.async.commit_group;" ::: "memory");  // empty groups keep the count
+  };
+  for (int i = 0; i < p.slots - 1; ++i) issue();
+  load_x<QUANT, XF32>(a, p, t0, tok, 0, xs, sums);
+  int have = 0;  // slice of x in shared memory
+
+  float acc[NT][4];
 #pragma unroll
-  for (int t = 0; t < kTok; ++t) {
-    float v = acc[t];
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
-    if (t < nt && lane == 0) {
+    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+  const int r = lane >> 2, c = lane & 3;  // rows r and r + 8, quad lane
+  const int part_bytes = p.tok * p.x_pitch;
+  constexpr uint32_t kBias = QUANT == MOE_Q4_0 ? 0x43084308u : 0x43004300u;  // 136, 128
+
+  int slot = 0, stage = 0;
+  for (int tile = blockIdx.x; tile < p.tiles;) {
+    if (p.slots == 4)
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (p.slots == 3)
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+      asm volatile("cp.async.wait_group 4;" ::: "memory");  // six slots
+    __syncthreads();
+    issue();
+    if (n_slices > 1) {
+      const int slice = stage * stage_k / p.kx;
+      if (slice != have) {  // x does not fit: the next slice (every thread is past the last one)
+        load_x<QUANT, XF32>(a, p, t0, tok, slice * p.kx, xs, sums);
+        have = slice;
+        __syncthreads();
+      }
+    }
+    const int k0 = stage * stage_k - have * p.kx + wk * kWK;  // within the slice
+    const uint32_t st = ring + slot * kStageBytes;
+    const int row0 = wk * R + wr * 16 + r;
+    const uint32_t q0 = st + row0 * 128 + c * 4, q1 = q0 + 8 * 128;
+    const uint4 m0 = lds128(st + kCodeBytes + row0 * 16), m1 = lds128(st + kCodeBytes + (row0 + 8) * 16);
+    const uint32_t ma[4] = {m0.x, m0.y, m0.z, m0.w}, mb[4] = {m1.x, m1.y, m1.z, m1.w};
+    const uint32_t xa = xs + r * p.x_pitch + k0 * 2 + c * 16;  // token r of a block of eight
+    const int groups = min(8, (a.K - (stage * stage_k + wk * kWK) + 31) / 32);  // may be negative
+#pragma unroll
+    for (int g2 = 0; g2 < 4; ++g2) {  // 64 k: two groups of Q4_0, one of I4_G64
+      if (2 * g2 >= groups) break;
+      float s[2][NT][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int g = 2 * g2 + h;
+        const uint32_t swz = static_cast<uint32_t>(g ^ (r & 7)) << 4;  // rows r and r + 8 have one phase
+        uint32_t wa[4], wb[4];
+        codes(lds32(q0 + swz), kBias, wa);
+        codes(lds32(q1 + swz), kBias, wb);
+        const uint32_t f0[4] = {wa[0], wb[0], wa[1], wb[1]}, f1[4] = {wa[2], wb[2], wa[3], wb[3]};
+        float(*d)[4] = s[QUANT == MOE_Q4_0 ? h : 0];
+        if (QUANT == MOE_Q4_0 || h == 0) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[n][i] = 0.f;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int q = 0; q < kParts; ++q) {
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (n * 8 + r < tok) x = lds128(xa + n * 8 * p.x_pitch + q * part_bytes + g * 64);
+            mma(d[n], f0, x.x, x.y);
+            mma(d[n], f1, x.z, x.w);
+          }
+        }
+      }
+      if (QUANT == MOE_Q4_0) {
+        const float2 da = __half22float2(*reinterpret_cast<const __half2*>(&ma[g2]));
+        const float2 db = __half22float2(*reinterpret_cast<const __half2*>(&mb[g2]));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          acc[n][0] += da.x * s[0][n][0];
+          acc[n][1] += da.x * s[0][n][1];
+          acc[n][2] += db.x * s[0][n][2];
+          acc[n][3] += db.x * s[0][n][3];
+          acc[n][0] += da.y * s[1][n][0];
+          acc[n][1] += da.y * s[1][n][1];
+          acc[n][2] += db.y * s[1][n][2];
+          acc[n][3] += db.y * s[1][n][3];
+        }
+      } else {
+        const float sa = __uint_as_float(ma[g2] << 16), ba = __uint_as_float(ma[g2] & 0xFFFF0000u);
+        const float sb = __uint_as_float(mb[g2] << 16), bb = __uint_as_float(mb[g2] & 0xFFFF0000u);
+        const float* su = sums + (k0 / 64 + g2) * kMaxTok + c * 2;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float2 xsum = *reinterpret_cast<const float2*>(su + n * 8);
+          acc[n][0] += sa * s[0][n][0] + ba * xsum.x;
+          acc[n][1] += sa * s[0][n][1] + ba * xsum.y;
+          acc[n][2] += sb * s[0][n][2] + bb * xsum.x;
+          acc[n][3] += sb * s[0][n][3] + bb * xsum.y;
+        }
+      }
+    }
+    if (++slot == p.slots) slot = 0;
+    if (++stage < stages_tile) continue;
+    // ---- the tile's rows: slices of K added in order, bias, one rounding
+    stage = 0;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        *reinterpret_cast<float2*>(red + (warp * 16 + r + 8 * h) * (8 * NT) + n * 8 + c * 2) =
+            make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
+        acc[n][2 * h] = acc[n][2 * h + 1] = 0.f;
+      }
+    __syncthreads();
+    for (int e = tid; e < R * tok; e += kThreads) {
+      const int row = e % R, t = e / R, n = tile * R + row;
+      if (n >= a.N) continue;
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < WK; ++k) v += red[(((row >> 4) * WK + k) * 16 + (row & 15)) * (8 * NT) + t];
       if (a.bias) v += __ldg(a.bias + n);
-      Y* y = static_cast<Y*>(a.y) + (t0 + t) * a.ldy + n;
-      if constexpr (sizeof(Y) == 4)
-        *y = v;
+      const int64_t at = (t0 + t) * a.ldy + n;
+      if (a.yt == MOE_F32)
+        static_cast<float*>(a.y)[at] = v;
       else
-        *y = __float2bfloat16_rn(v);
+        static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
     }
+    tile += gridDim.x;  // red is written again only after the next stage's barrier
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Two CTAs an SM share its 227 KB with rings of four or three slots; with much
+// x, one CTA with six.
+constexpr int kHalf = 113 * 1024, kFull = 226 * 1024;
+
+// Shared bytes beside the ring: x of a slice and its sums, the slices' results.
+inline int64_t x_bytes(int quant, int parts, int tok, int64_t kx) {
+  return static_cast<int64_t>(tok) * parts * (kx * 2 + 64) + (quant == MOE_Q4_0 ? 0 : kx / 64 * kMaxTok * 4);
+}
+inline int red_bytes(int tok) { return kWarps * 16 * 8 * ((tok + 7) / 8) * 4; }
+
+template <int QUANT, bool XF32, int NT, int WK>
+cudaError_t launch(const LinearArgs& a, int blocks_t, int num_sms, cudaStream_t st) {
+  constexpr int R = 16 * kWarps / WK, kParts = XF32 ? 3 : 1, stage_k = kWK * WK;
+  Plan p;
+  p.tok = (a.T + blocks_t - 1) / blocks_t;
+  p.tiles = (a.N + R - 1) / R;
+  p.kx = (a.K + stage_k - 1) / stage_k * stage_k;
+  const int red = red_bytes(8 * NT);
+  const int64_t whole = x_bytes(QUANT, kParts, p.tok, p.kx) + red;
+  if (whole + 4 * kStageBytes <= kHalf) {
+    p.slots = 4;
+  } else if (whole + 3 * kStageBytes <= kHalf) {
+    p.slots = 3;
+  } else {
+    p.slots = 6;
+    // x in slices of whole stages where all of it does not fit
+    int n = 1;
+    auto slice = [&] { return ((p.kx / stage_k + n - 1) / n) * stage_k; };
+    while (x_bytes(QUANT, kParts, p.tok, slice()) + red + 6 * kStageBytes > kFull) {
+      if (slice() == stage_k) return cudaErrorInvalidValue;
+      ++n;
+    }
+    p.kx = slice();
+  }
+  p.x_pitch = p.kx * 2 + 64;
+  p.x_bytes = p.tok * kParts * p.x_pitch;
+  const int smem = p.slots * kStageBytes + static_cast<int>(x_bytes(QUANT, kParts, p.tok, p.kx)) + red;
+  cudaError_t e = cudaFuncSetAttribute(linear_kernel<QUANT, XF32, NT, WK>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFull);
+  if (e != cudaSuccess) return e;
+  const int per_sm = smem <= kHalf ? 2 : 1;
+  const dim3 grid(std::min(p.tiles, std::max(1, per_sm * num_sms / blocks_t)), blocks_t);
+  linear_kernel<QUANT, XF32, NT, WK><<<grid, kThreads, smem, st>>>(a, p);
+  return cudaGetLastError();
+}
+
+// Rows of a tile: the largest of 128, 64, 32 and 16 that leaves each SM four
+// tiles (they end unevenly), 16 where none does. A stage of small tiles is long
+// in K: not longer than K, and one stage of x has to fit.
+template <int QUANT, bool XF32, int NT>
+cudaError_t by_rows(const LinearArgs& a, int blocks_t, int num_sms, cudaStream_t st) {
+  constexpr int kParts = XF32 ? 3 : 1;
+  const int tok = (a.T + blocks_t - 1) / blocks_t;
+  int wk = 1;
+  while (wk < 8 && a.N < 128 / wk * 4 * num_sms && a.K > wk * kWK &&
+         x_bytes(QUANT, kParts, tok, 2 * wk * kWK) + red_bytes(8 * NT) + 6 * kStageBytes <= kFull)
+    wk *= 2;
+  switch (wk) {
+    case 1: return launch<QUANT, XF32, NT, 1>(a, blocks_t, num_sms, st);
+    case 2: return launch<QUANT, XF32, NT, 2>(a, blocks_t, num_sms, st);
+    case 4: return launch<QUANT, XF32, NT, 4>(a, blocks_t, num_sms, st);
+    default: return launch<QUANT, XF32, NT, 8>(a, blocks_t, num_sms, st);
   }
 }
 
-template <class X, class Y>
-cudaError_t by_quant(const LinearArgs& a, int32_t quant, cudaStream_t st) {
-  const dim3 grid((a.N + 7) / 8, (a.T + kTok - 1) / kTok);
-  if (quant == MOE_Q4_0)
-    linear_kernel<X, Y, MOE_Q4_0><<<grid, 256, 0, st>>>(a);
-  else
-    linear_kernel<X, Y, MOE_I4_G64><<<grid, 256, 0, st>>>(a);
-  return cudaGetLastError();
+template <int QUANT, bool XF32>
+cudaError_t by_tokens(const LinearArgs& a, int num_sms, cudaStream_t st) {
+  const int blocks_t = (a.T + kMaxTok - 1) / kMaxTok, tok = (a.T + blocks_t - 1) / blocks_t;
+  if (tok <= 8) return by_rows<QUANT, XF32, 1>(a, blocks_t, num_sms, st);
+  if (tok <= 16) return by_rows<QUANT, XF32, 2>(a, blocks_t, num_sms, st);
+  return by_rows<QUANT, XF32, 3>(a, blocks_t, num_sms, st);
 }
 
 }  // namespace
 
 cudaError_t launch_quant_linear(const LinearArgs& a, int32_t quant, int num_sms, cudaStream_t st) {
-  (void)num_sms;
-  if (a.xt == MOE_F32)
-    return a.yt == MOE_F32 ? by_quant<float, float>(a, quant, st) : by_quant<float, __nv_bfloat16>(a, quant, st);
-  return a.yt == MOE_F32 ? by_quant<__nv_bfloat16, float>(a, quant, st)
-                         : by_quant<__nv_bfloat16, __nv_bfloat16>(a, quant, st);
+  if (quant == MOE_Q4_0)
+    return a.xt == MOE_F32 ? by_tokens<MOE_Q4_0, true>(a, num_sms, st) : by_tokens<MOE_Q4_0, false>(a, num_sms, st);
+  return a.xt == MOE_F32 ? by_tokens<MOE_I4_G64, true>(a, num_sms, st) : by_tokens<MOE_I4_G64, false>(a, num_sms, st);
 }
 
 }  // namespace moe
