@@ -6,8 +6,7 @@
 // What bounds it: HBM, the 4.5 bits a weight, as long as a weight costs less
 // than about three instructions of a thread. The inner sums therefore run on
 // warp-level matrix instructions (m16n8k16, weights as A, tokens as B): codes
-// become bf16 integers by two byte permutes and a subtraction for eight of them,
-// products of a 4-bit integer and a bf16 are exact, sums are fp32, and the
+// become bf16 integers by a mask and a subtraction for two of them, products of a 4-bit integer and a bf16 are exact, sums are fp32, and the
 // group's factor is applied in fp32 to the 16 x 8 sums. An fp32 x is the exact
 // sum of three bf16 (8 + 8 + 8 significand bits), one instruction each.
 //
@@ -15,11 +14,11 @@
 // is stored in the order in which a lane's 4-byte word yields its eight codes:
 // a lane's eight x of a group are 16 contiguous bytes.
 //
-// A CTA holds the tokens' x in shared memory (in slices of K if they do not
-// fit) and walks row tiles. Its eight warps are 8 / WK groups of 16 rows by WK
-// slices of K, so that a matrix of few rows still fills the GPU; the slices are
-// added in shared memory. A stage is 16 rows x 256 k a warp: 16 KB of codes, 2 KB
-// of scales, by 16-byte asynchronous copies into a ring.
+// A CTA (one per SM) holds the tokens' x in shared memory, in slices of K if
+// they do not fit, and walks row tiles. Its sixteen warps are 16 / WK groups of
+// 16 rows by WK slices of K, so that a matrix of few rows still fills the GPU;
+// the slices are added in shared memory. A stage is 16 rows x 256 k a warp:
+// 32 KB of codes, 4 KB of scales, by asynchronous copies into a ring.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -28,12 +27,14 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256, kWarps = 8;
+constexpr int kThreads = 512, kWarps = 16;
 constexpr int kWK = 256;                      // k of a warp's stage
 constexpr int kCodeBytes = kWarps * 16 * 128; // codes of a stage
 constexpr int kMetaBytes = kWarps * 16 * 16;  // scales of a stage
 constexpr int kStageBytes = kCodeBytes + kMetaBytes;
 constexpr int kMaxTok = 24;                   // tokens of a launch's y block
+
+constexpr int kPieces = kCodeBytes / 16 / kThreads;  // 16-byte pieces a thread and stage
 
 struct Plan {
   int tok;         // tokens of a block
@@ -71,15 +72,28 @@ __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, ui
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Codes of a 4-byte word as bf16 integers less `bias` - 128: the nibble becomes
-// the low mantissa bits of 128 (exact), bias is subtracted (exact).
-// o[0], o[1]: low nibbles of bytes 0,1 and 2,3; o[2], o[3]: high nibbles.
+__device__ __forceinline__ void mma0(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {  // onto zero
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// d[0..1] += s * v[0..1], one instruction
+__device__ __forceinline__ void fma2(float* d, float s, const float* v) {
+  unsigned long long dd, vv, ss;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(dd) : "f"(d[0]), "f"(d[1]));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(vv) : "f"(v[0]), "f"(v[1]));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(dd) : "l"(ss), "l"(vv));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d[0]), "=f"(d[1]) : "l"(dd));
+}
+// The eight codes of a 4-byte word as bf16 integers less `bias` - 128: the
+// nibble becomes the low mantissa bits of 128 (exact), bias is subtracted
+// (exact). o[0], o[1]: low nibbles of bytes 0,2 and 1,3; o[2], o[3]: high ones.
 __device__ __forceinline__ void codes(uint32_t w, uint32_t bias2, uint32_t* o) {
-  const uint32_t v01 = __byte_perm(w, 0, 0x4140), v23 = __byte_perm(w, 0, 0x4342);
-  o[0] = (v01 & 0x000F000Fu) | 0x43004300u;
-  o[1] = (v23 & 0x000F000Fu) | 0x43004300u;
-  o[2] = ((v01 >> 4) & 0x000F000Fu) | 0x43004300u;
-  o[3] = ((v23 >> 4) & 0x000F000Fu) | 0x43004300u;
+  o[0] = (w & 0x000F000Fu) | 0x43004300u;
+  o[1] = ((w >> 8) & 0x000F000Fu) | 0x43004300u;
+  o[2] = ((w >> 4) & 0x000F000Fu) | 0x43004300u;
+  o[3] = ((w >> 12) & 0x000F000Fu) | 0x43004300u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(o[i]) : "r"(bias2));
 }
@@ -122,15 +136,12 @@ __device__ __forceinline__ void load_x(const LinearArgs& a, const Plan& p, int t
         v = __ldg(reinterpret_cast<const float4*>(x + kb));
       }
       float f[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-      if (QUANT != MOE_Q4_0) {
-        sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-        const float g[8] = {f[0], f[2], f[4], f[6], f[1], f[3], f[5], f[7]};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = g[i];
-      }
+      if (QUANT != MOE_Q4_0) sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+      // the order of a word's codes
+      constexpr int kQ4[8] = {0, 2, 1, 3, 4, 6, 5, 7}, kI4[8] = {0, 4, 2, 6, 1, 5, 3, 7};
       uint32_t s[8][3];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) split3(f[i], s[i]);
+      for (int i = 0; i < 8; ++i) split3(f[QUANT == MOE_Q4_0 ? kQ4[i] : kI4[i]], s[i]);
 #pragma unroll
       for (int q = 0; q < kParts; ++q)
         sts128(at + q * part_bytes, make_uint4(s[0][q] | s[1][q] << 16, s[2][q] | s[3][q] << 16,
@@ -143,13 +154,14 @@ __device__ __forceinline__ void load_x(const LinearArgs& a, const Plan& p, int t
         v = __ldg(reinterpret_cast<const uint2*>(x + kb));
       }
       if (QUANT == MOE_Q4_0) {
-        sts128(at, make_uint4(u.x, u.y, v.x, v.y));
+        sts128(at, make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.x, u.y, 0x7632),
+                              __byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632)));
       } else {
         const uint32_t w[4] = {u.x, u.y, v.x, v.y};
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum += __uint_as_float(w[i] << 16) + __uint_as_float(w[i] & 0xFFFF0000u);
-        sts128(at, make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(v.x, v.y, 0x5410),
-                              __byte_perm(u.x, u.y, 0x7632), __byte_perm(v.x, v.y, 0x7632)));
+        sts128(at, make_uint4(__byte_perm(u.x, v.x, 0x5410), __byte_perm(u.y, v.y, 0x5410),
+                              __byte_perm(u.x, v.x, 0x7632), __byte_perm(u.y, v.y, 0x7632)));
       }
     }
     if (QUANT != MOE_Q4_0) {
@@ -162,48 +174,54 @@ __device__ __forceinline__ void load_x(const LinearArgs& a, const Plan& p, int t
 }
 
 template <int QUANT, bool XF32, int NT, int WK>
-__global__ void __launch_bounds__(kThreads, 2) linear_kernel(LinearArgs a, Plan p) {
+__global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan p) {
   constexpr int kParts = XF32 ? 3 : 1, R = 16 * kWarps / WK;  // rows of a tile
   extern __shared__ __align__(128) unsigned char sm[];
   const uint32_t ring = smem_u32(sm), xs = ring + p.slots * kStageBytes;
   float* const sums = reinterpret_cast<float*>(sm + p.slots * kStageBytes + p.x_bytes);
-  float* const red = sums + (QUANT == MOE_Q4_0 ? 0 : p.kx / 64 * kMaxTok);  // [8 warps][16 rows][8 NT]
+  float* const red = sums + (QUANT == MOE_Q4_0 ? 0 : p.kx / 64 * kMaxTok);  // [16 warps][16 rows][8], WK > 1
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wr = warp / WK, wk = warp % WK;  // row group, slice of K
   const int t0 = blockIdx.y * p.tok, tok = min(p.tok, a.T - t0);
-  const int stage_k = kWK * WK;
+  constexpr int stage_k = kWK * WK;
   const int n_slices = (a.K + p.kx - 1) / p.kx;
-  const int my_tiles = (p.tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
   const int stages_tile = (a.K + stage_k - 1) / stage_k;  // slices hold whole stages
-  const int total = my_tiles * stages_tile;
 
   // One stage: codes [wk][row][128 bytes], 16-byte pieces (32 codes) swizzled by
-  // the row; scales [wk][row][16 bytes]. Zeros past N and K.
-  int ld_tile = blockIdx.x, ld_stage = 0, ld_slot = 0, issued = 0;
+  // the row; scales [wk][row][16 bytes]. Zeros past N and K. A thread copies
+  // piece tid % 8 of rows tid / 8 + 64 i of the stage's [wk][row].
+  int ld_tile = blockIdx.x, ld_stage = 0, ld_slot = 0;
+  const int piece = tid & 7;
+  uint32_t dst[kPieces];  // within a slot
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int e = (tid >> 3) + i * (kThreads / 8);
+    dst[i] = e * 128 + ((piece ^ (e & 7)) << 4);
+  }
+  const int mrow = tid % R, mw = tid / R;  // scales: threads below 256
   auto issue = [&]() {
-    if (issued < total) {
+    if (ld_tile < p.tiles) {
       const uint32_t st = ring + ld_slot * kStageBytes;
       const int n0 = ld_tile * R, k0 = ld_stage * stage_k;
+      const uint8_t* const w0 = a.w + static_cast<int64_t>(n0) * (a.K / 2) + k0 / 2 + piece * 16;
 #pragma unroll
-      for (int i = 0; i < kCodeBytes / 16 / kThreads; ++i) {
-        const int e = tid + i * kThreads, piece = e & 7, row = (e >> 3) % R, w = (e >> 3) / R;
-        const int n = n0 + row, k = k0 + w * kWK + piece * 32;
-        const bool in = n < a.N && k < a.K;
-        cp16(st + (e >> 3) * 128 + ((piece ^ (row & 7)) << 4),
-             in ? a.w + static_cast<int64_t>(n) * (a.K / 2) + k / 2 : a.w, in);
+      for (int i = 0; i < kPieces; ++i) {
+        const int e = (tid >> 3) + i * (kThreads / 8), row = e % R, w = e / R;
+        const bool in = n0 + row < a.N && k0 + w * kWK + piece * 32 < a.K;
+        cp16(st + dst[i], in ? w0 + row * (a.K / 2) + w * (kWK / 2) : a.w, in);
       }
       if (tid < kWarps * 16) {
-        const int row = tid % R, w = tid / R, n = n0 + row, k = k0 + w * kWK;
-        const uint32_t dst = st + kCodeBytes + tid * 16;
+        const int n = n0 + mrow, k = k0 + mw * kWK;
+        const uint32_t md = st + kCodeBytes + tid * 16;
         const uint8_t* src = a.meta + static_cast<int64_t>(n) * (a.K / 16) + k / 16;
         if ((a.K & 255) == 0) {
           const bool in = n < a.N && k < a.K;
-          cp16(dst, in ? src : a.meta, in);
+          cp16(md, in ? src : a.meta, in);
         } else if ((a.K & 63) == 0) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const bool in = n < a.N && k + i * 64 < a.K;
-            cp4(dst + i * 4, in ? src + i * 4 : a.meta, in);
+            cp4(md + i * 4, in ? src + i * 4 : a.meta, in);
           }
         } else {  // an odd number of groups a row: scales are 2-byte aligned
           uint32_t v[4] = {};
@@ -211,10 +229,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(LinearArgs a, Plan 
           for (int i = 0; i < 8; ++i)
             if (n < a.N && k + i * 32 < a.K)
               v[i >> 1] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(src) + i)) << (16 * (i & 1));
-          sts128(dst, make_uint4(v[0], v[1], v[2], v[3]));
+          sts128(md, make_uint4(v[0], v[1], v[2], v[3]));
         }
       }
-      ++issued;
       if (++ld_slot == p.slots) ld_slot = 0;
       if (++ld_stage == stages_tile) {
         ld_stage = 0;
@@ -233,17 +250,35 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(LinearArgs a, Plan 
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
   const int r = lane >> 2, c = lane & 3;  // rows r and r + 8, quad lane
-  const int part_bytes = p.tok * p.x_pitch;
+  const uint32_t part_bytes = p.tok * p.x_pitch;
+  // this lane's x: token r of each block of eight (a token past the last reads
+  // the last one's: its sums are not stored)
+  uint32_t xt[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) xt[n] = xs + min(n * 8 + r, tok - 1) * p.x_pitch + c * 16;
   constexpr uint32_t kBias = QUANT == MOE_Q4_0 ? 0x43084308u : 0x43004300u;  // 136, 128
+  const uint32_t row0 = wk * R + wr * 16 + r;
+  const uint32_t q_off = row0 * 128 + c * 4, m_off = kCodeBytes + row0 * 16;
+  uint32_t swz[8];  // piece of group g; rows r and r + 8 have one phase
+#pragma unroll
+  for (int g = 0; g < 8; ++g) swz[g] = q_off + (static_cast<uint32_t>(g ^ (r & 7)) << 4);
+
+  auto store = [&](int n, int t, float v) {
+    if (a.bias) v += __ldg(a.bias + n);
+    const int64_t at = (t0 + t) * a.ldy + n;
+    if (a.yt == MOE_F32)
+      static_cast<float*>(a.y)[at] = v;
+    else
+      static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+  };
 
   int slot = 0, stage = 0;
   for (int tile = blockIdx.x; tile < p.tiles;) {
-    if (p.slots == 4)
-      asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (p.slots == 3)
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else
-      asm volatile("cp.async.wait_group 4;" ::: "memory");  // six slots
+    switch (p.slots) {
+      case 3: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+      case 4: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+      default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;  // five
+    }
     __syncthreads();
     issue();
     if (n_slices > 1) {
@@ -255,56 +290,43 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(LinearArgs a, Plan 
       }
     }
     const int k0 = stage * stage_k - have * p.kx + wk * kWK;  // within the slice
-    const uint32_t st = ring + slot * kStageBytes;
-    const int row0 = wk * R + wr * 16 + r;
-    const uint32_t q0 = st + row0 * 128 + c * 4, q1 = q0 + 8 * 128;
-    const uint4 m0 = lds128(st + kCodeBytes + row0 * 16), m1 = lds128(st + kCodeBytes + (row0 + 8) * 16);
+    const uint32_t st = ring + slot * kStageBytes, xk = k0 * 2;
+    const uint4 m0 = lds128(st + m_off), m1 = lds128(st + m_off + 128);
     const uint32_t ma[4] = {m0.x, m0.y, m0.z, m0.w}, mb[4] = {m1.x, m1.y, m1.z, m1.w};
-    const uint32_t xa = xs + r * p.x_pitch + k0 * 2 + c * 16;  // token r of a block of eight
-    const int groups = min(8, (a.K - (stage * stage_k + wk * kWK) + 31) / 32);  // may be negative
+    const int left = a.K - (stage * stage_k + wk * kWK);  // k of this warp's stage; may be negative
 #pragma unroll
     for (int g2 = 0; g2 < 4; ++g2) {  // 64 k: two groups of Q4_0, one of I4_G64
-      if (2 * g2 >= groups) break;
+      if (g2 * 64 >= left) break;
       float s[2][NT][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int g = 2 * g2 + h;
-        const uint32_t swz = static_cast<uint32_t>(g ^ (r & 7)) << 4;  // rows r and r + 8 have one phase
         uint32_t wa[4], wb[4];
-        codes(lds32(q0 + swz), kBias, wa);
-        codes(lds32(q1 + swz), kBias, wb);
+        codes(lds32(st + swz[g]), kBias, wa);
+        codes(lds32(st + swz[g] + 8 * 128), kBias, wb);
         const uint32_t f0[4] = {wa[0], wb[0], wa[1], wb[1]}, f1[4] = {wa[2], wb[2], wa[3], wb[3]};
         float(*d)[4] = s[QUANT == MOE_Q4_0 ? h : 0];
-        if (QUANT == MOE_Q4_0 || h == 0) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+        for (int q = 0; q < kParts; ++q)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) d[n][i] = 0.f;
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-          for (int q = 0; q < kParts; ++q) {
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (n * 8 + r < tok) x = lds128(xa + n * 8 * p.x_pitch + q * part_bytes + g * 64);
-            mma(d[n], f0, x.x, x.y);
+          for (int n = 0; n < NT; ++n) {
+            const uint4 x = lds128(xt[n] + xk + q * part_bytes + g * 64);
+            if (q == 0 && (QUANT == MOE_Q4_0 || h == 0))
+              mma0(d[n], f0, x.x, x.y);
+            else
+              mma(d[n], f0, x.x, x.y);
             mma(d[n], f1, x.z, x.w);
           }
-        }
       }
       if (QUANT == MOE_Q4_0) {
         const float2 da = __half22float2(*reinterpret_cast<const __half2*>(&ma[g2]));
         const float2 db = __half22float2(*reinterpret_cast<const __half2*>(&mb[g2]));
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          acc[n][0] += da.x * s[0][n][0];
-          acc[n][1] += da.x * s[0][n][1];
-          acc[n][2] += db.x * s[0][n][2];
-          acc[n][3] += db.x * s[0][n][3];
-          acc[n][0] += da.y * s[1][n][0];
-          acc[n][1] += da.y * s[1][n][1];
-          acc[n][2] += db.y * s[1][n][2];
-          acc[n][3] += db.y * s[1][n][3];
+          fma2(acc[n], da.x, s[0][n]);
+          fma2(acc[n] + 2, db.x, s[0][n] + 2);
+          fma2(acc[n], da.y, s[1][n]);
+          fma2(acc[n] + 2, db.y, s[1][n] + 2);
         }
       } else {
         const float sa = __uint_as_float(ma[g2] << 16), ba = __uint_as_float(ma[g2] & 0xFFFF0000u);
@@ -312,11 +334,12 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(LinearArgs a, Plan 
         const float* su = sums + (k0 / 64 + g2) * kMaxTok + c * 2;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float2 xsum = *reinterpret_cast<const float2*>(su + n * 8);
-          acc[n][0] += sa * s[0][n][0] + ba * xsum.x;
-          acc[n][1] += sa * s[0][n][1] + ba * xsum.y;
-          acc[n][2] += sb * s[0][n][2] + bb * xsum.x;
-          acc[n][3] += sb * s[0][n][3] + bb * xsum.y;
+          const float2 u = *reinterpret_cast<const float2*>(su + n * 8);
+          const float xsum[2] = {u.x, u.y};
+          fma2(acc[n], sa, s[0][n]);
+          fma2(acc[n] + 2, sb, s[0][n] + 2);
+          fma2(acc[n], ba, xsum);
+          fma2(acc[n] + 2, bb, xsum);
         }
       }
     }
@@ -324,42 +347,48 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(LinearArgs a, Plan 
     if (++stage < stages_tile) continue;
     // ---- the tile's rows: slices of K added in order, bias, one rounding
     stage = 0;
+    if constexpr (WK == 1) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        *reinterpret_cast<float2*>(red + (warp * 16 + r + 8 * h) * (8 * NT) + n * 8 + c * 2) =
-            make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
-        acc[n][2 * h] = acc[n][2 * h + 1] = 0.f;
+        for (int i = 0; i < 4; ++i) {
+          const int row = tile * R + wr * 16 + r + 8 * (i >> 1), t = n * 8 + c * 2 + (i & 1);
+          if (row < a.N && t < tok) store(row, t, acc[n][i]);
+          acc[n][i] = 0.f;
+        }
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n > 0) __syncthreads();  // (the first write follows a stage's barrier)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          *reinterpret_cast<float2*>(red + (warp * 16 + r + 8 * h) * 8 + c * 2) =
+              make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
+          acc[n][2 * h] = acc[n][2 * h + 1] = 0.f;
+        }
+        __syncthreads();
+        for (int e = tid; e < R * 8; e += kThreads) {
+          const int row = e % R, t = e / R, nn = tile * R + row;
+          if (nn >= a.N || n * 8 + t >= tok) continue;
+          float v = 0.f;
+#pragma unroll
+          for (int k = 0; k < WK; ++k) v += red[(((row >> 4) * WK + k) * 16 + (row & 15)) * 8 + t];
+          store(nn, n * 8 + t, v);
+        }
       }
-    __syncthreads();
-    for (int e = tid; e < R * tok; e += kThreads) {
-      const int row = e % R, t = e / R, n = tile * R + row;
-      if (n >= a.N) continue;
-      float v = 0.f;
-#pragma unroll
-      for (int k = 0; k < WK; ++k) v += red[(((row >> 4) * WK + k) * 16 + (row & 15)) * (8 * NT) + t];
-      if (a.bias) v += __ldg(a.bias + n);
-      const int64_t at = (t0 + t) * a.ldy + n;
-      if (a.yt == MOE_F32)
-        static_cast<float*>(a.y)[at] = v;
-      else
-        static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
     }
-    tile += gridDim.x;  // red is written again only after the next stage's barrier
+    tile += gridDim.x;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Two CTAs an SM share its 227 KB with rings of four or three slots; with much
-// x, one CTA with six.
-constexpr int kHalf = 113 * 1024, kFull = 226 * 1024;
+constexpr int kFull = 226 * 1024;              // shared memory of a CTA
+constexpr int kRedBytes = kWarps * 16 * 8 * 4;
 
-// Shared bytes beside the ring: x of a slice and its sums, the slices' results.
+// Shared bytes of x of a slice and its sums.
 inline int64_t x_bytes(int quant, int parts, int tok, int64_t kx) {
   return static_cast<int64_t>(tok) * parts * (kx * 2 + 64) + (quant == MOE_Q4_0 ? 0 : kx / 64 * kMaxTok * 4);
 }
-inline int red_bytes(int tok) { return kWarps * 16 * 8 * ((tok + 7) / 8) * 4; }
 
 template <int QUANT, bool XF32, int NT, int WK>
 cudaError_t launch(const LinearArgs& a, int blocks_t, int num_sms, cudaStream_t st) {
@@ -367,45 +396,37 @@ cudaError_t launch(const LinearArgs& a, int blocks_t, int num_sms, cudaStream_t 
   Plan p;
   p.tok = (a.T + blocks_t - 1) / blocks_t;
   p.tiles = (a.N + R - 1) / R;
-  p.kx = (a.K + stage_k - 1) / stage_k * stage_k;
-  const int red = red_bytes(8 * NT);
-  const int64_t whole = x_bytes(QUANT, kParts, p.tok, p.kx) + red;
-  if (whole + 4 * kStageBytes <= kHalf) {
-    p.slots = 4;
-  } else if (whole + 3 * kStageBytes <= kHalf) {
-    p.slots = 3;
-  } else {
-    p.slots = 6;
-    // x in slices of whole stages where all of it does not fit
-    int n = 1;
-    auto slice = [&] { return ((p.kx / stage_k + n - 1) / n) * stage_k; };
-    while (x_bytes(QUANT, kParts, p.tok, slice()) + red + 6 * kStageBytes > kFull) {
-      if (slice() == stage_k) return cudaErrorInvalidValue;
-      ++n;
-    }
-    p.kx = slice();
+  // a ring of five to three slots beside all of x, else x in slices of whole stages
+  const int stages = (a.K + stage_k - 1) / stage_k;
+  int n = 1;
+  auto slice = [&] { return (stages + n - 1) / n * stage_k; };
+  auto need = [&](int slots) { return x_bytes(QUANT, kParts, p.tok, slice()) + kRedBytes + slots * kStageBytes; };
+  p.slots = 5;
+  while (p.slots > 3 && need(p.slots) > kFull) --p.slots;
+  while (need(p.slots) > kFull) {
+    if (slice() == stage_k) return cudaErrorInvalidValue;
+    ++n;
   }
+  p.kx = slice();
   p.x_pitch = p.kx * 2 + 64;
   p.x_bytes = p.tok * kParts * p.x_pitch;
-  const int smem = p.slots * kStageBytes + static_cast<int>(x_bytes(QUANT, kParts, p.tok, p.kx)) + red;
   cudaError_t e = cudaFuncSetAttribute(linear_kernel<QUANT, XF32, NT, WK>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFull);
   if (e != cudaSuccess) return e;
-  const int per_sm = smem <= kHalf ? 2 : 1;
-  const dim3 grid(std::min(p.tiles, std::max(1, per_sm * num_sms / blocks_t)), blocks_t);
-  linear_kernel<QUANT, XF32, NT, WK><<<grid, kThreads, smem, st>>>(a, p);
+  const dim3 grid(std::min(p.tiles, std::max(1, num_sms / blocks_t)), blocks_t);
+  linear_kernel<QUANT, XF32, NT, WK><<<grid, kThreads, static_cast<int>(need(p.slots)), st>>>(a, p);
   return cudaGetLastError();
 }
 
-// Rows of a tile: the largest of 128, 64, 32 and 16 that leaves each SM four
-// tiles (they end unevenly), 16 where none does. A stage of small tiles is long
+// Rows of a tile: the largest of 256, 128, 64 and 32 that leaves each SM six
+// tiles (they end unevenly), 32 where none does. A stage of small tiles is long
 // in K: not longer than K, and one stage of x has to fit.
 template <int QUANT, bool XF32, int NT>
 cudaError_t by_rows(const LinearArgs& a, int blocks_t, int num_sms, cudaStream_t st) {
   constexpr int kParts = XF32 ? 3 : 1;
   const int tok = (a.T + blocks_t - 1) / blocks_t;
   int wk = 1;
-  while (wk < 8 && a.N < 128 / wk * 4 * num_sms && a.K > wk * kWK &&
-         x_bytes(QUANT, kParts, tok, 2 * wk * kWK) + red_bytes(8 * NT) + 6 * kStageBytes <= kFull)
+  while (wk < 8 && a.N < 256 / wk * 6 * num_sms && a.K > wk * kWK &&
+         x_bytes(QUANT, kParts, tok, 2 * wk * kWK) + kRedBytes + 3 * kStageBytes <= kFull)
     wk *= 2;
   switch (wk) {
     case 1: return launch<QUANT, XF32, NT, 1>(a, blocks_t, num_sms, st);
