@@ -17,8 +17,11 @@
 // A CTA (one per SM) holds the tokens' x in shared memory, in slices of K if
 // they do not fit, and walks row tiles. Its sixteen warps are 16 / WK groups of
 // 16 rows by WK slices of K, so that a matrix of few rows still fills the GPU;
-// the slices are added in shared memory. A stage is 16 rows x 256 k a warp:
-// 32 KB of codes, 4 KB of scales, by asynchronous copies into a ring.
+// the slices are added in shared memory. Each warp copies its own stages (16
+// rows x 256 k: 2 KB of codes, 256 B of scales) into a ring of its own by
+// asynchronous copies and meets no other warp within a tile: with one ring for
+// the block and a barrier a stage, all warps unpacked and multiplied in step,
+// and issued in half of the cycles.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -29,12 +32,13 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = 16;
 constexpr int kWK = 256;                      // k of a warp's stage
-constexpr int kCodeBytes = kWarps * 16 * 128; // codes of a stage
-constexpr int kMetaBytes = kWarps * 16 * 16;  // scales of a stage
-constexpr int kStageBytes = kCodeBytes + kMetaBytes;
+constexpr int kCodeBytes = 16 * 128;          // codes of a warp's stage
+constexpr int kMetaBytes = 16 * 16;           // scales
+constexpr int kWarpStage = kCodeBytes + kMetaBytes;
+constexpr int kStageBytes = kWarps * kWarpStage;
 constexpr int kMaxTok = 24;                   // tokens of a launch's y block
 
-constexpr int kPieces = kCodeBytes / 16 / kThreads;  // 16-byte pieces a thread and stage
+constexpr int kPieces = kCodeBytes / 16 / 32;  // 16-byte pieces a lane and stage
 
 struct Plan {
   int tok;         // tokens of a block
@@ -177,57 +181,59 @@ template <int QUANT, bool XF32, int NT, int WK>
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan p) {
   constexpr int kParts = XF32 ? 3 : 1, R = 16 * kWarps / WK;  // rows of a tile
   extern __shared__ __align__(128) unsigned char sm[];
-  const uint32_t ring = smem_u32(sm), xs = ring + p.slots * kStageBytes;
-  float* const sums = reinterpret_cast<float*>(sm + p.slots * kStageBytes + p.x_bytes);
-  float* const red = sums + (QUANT == MOE_Q4_0 ? 0 : p.kx / 64 * kMaxTok);  // [16 warps][16 rows][8], WK > 1
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t xs = smem_u32(sm) + p.slots * kStageBytes;
+  const uint32_t ring = smem_u32(sm) + warp * (p.slots * kWarpStage);
+  float* const sums = reinterpret_cast<float*>(sm + p.slots * kStageBytes + p.x_bytes);
+  // [2][16 warps][16 rows][8], WK > 1
+  float* const red = sums + (QUANT == MOE_Q4_0 ? 0 : p.kx / 64 * kMaxTok);
   const int wr = warp / WK, wk = warp % WK;  // row group, slice of K
   const int t0 = blockIdx.y * p.tok, tok = min(p.tok, a.T - t0);
   constexpr int stage_k = kWK * WK;
   const int n_slices = (a.K + p.kx - 1) / p.kx;
   const int stages_tile = (a.K + stage_k - 1) / stage_k;  // slices hold whole stages
 
-  // One stage: codes [wk][row][128 bytes], 16-byte pieces (32 codes) swizzled by
-  // the row; scales [wk][row][16 bytes]. Zeros past N and K. A thread copies
-  // piece tid % 8 of rows tid / 8 + 64 i of the stage's [wk][row].
+  // One stage of the warp: codes [16 rows][128 bytes], 16-byte pieces (32 codes)
+  // swizzled by the row; scales [16 rows][16 bytes]. Zeros past N and K. A lane
+  // copies piece lane % 8 of rows lane / 8 + 4 i, and the scales of row lane.
   int ld_tile = blockIdx.x, ld_stage = 0, ld_slot = 0;
-  const int piece = tid & 7;
+  const int piece = lane & 7;
   uint32_t dst[kPieces];  // within a slot
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
-    const int e = (tid >> 3) + i * (kThreads / 8);
-    dst[i] = e * 128 + ((piece ^ (e & 7)) << 4);
+    const int row = (lane >> 3) + 4 * i;
+    dst[i] = row * 128 + ((piece ^ (row & 7)) << 4);
   }
-  const int mrow = tid % R, mw = tid / R;  // scales: threads below 256
   auto issue = [&]() {
     if (ld_tile < p.tiles) {
-      const uint32_t st = ring + ld_slot * kStageBytes;
-      const int n0 = ld_tile * R, k0 = ld_stage * stage_k;
-      const uint8_t* const w0 = a.w + static_cast<int64_t>(n0) * (a.K / 2) + k0 / 2 + piece * 16;
+      const uint32_t st = ring + ld_slot * kWarpStage;
+      const int n0 = ld_tile * R + wr * 16, k0 = ld_stage * stage_k + wk * kWK;
+      const uint8_t* const w0 =
+          a.w + static_cast<int64_t>(n0 + (lane >> 3)) * (a.K / 2) + k0 / 2 + piece * 16;
+      const bool k_in = k0 + piece * 32 < a.K;
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        const int e = (tid >> 3) + i * (kThreads / 8), row = e % R, w = e / R;
-        const bool in = n0 + row < a.N && k0 + w * kWK + piece * 32 < a.K;
-        cp16(st + dst[i], in ? w0 + row * (a.K / 2) + w * (kWK / 2) : a.w, in);
+        const bool in = k_in && n0 + (lane >> 3) + 4 * i < a.N;
+        cp16(st + dst[i], in ? w0 + 4 * i * (a.K / 2) : a.w, in);
       }
-      if (tid < kWarps * 16) {
-        const int n = n0 + mrow, k = k0 + mw * kWK;
-        const uint32_t md = st + kCodeBytes + tid * 16;
-        const uint8_t* src = a.meta + static_cast<int64_t>(n) * (a.K / 16) + k / 16;
+      if (lane < 16) {
+        const int n = n0 + lane;
+        const uint32_t md = st + kCodeBytes + lane * 16;
+        const uint8_t* src = a.meta + static_cast<int64_t>(n) * (a.K / 16) + k0 / 16;
         if ((a.K & 255) == 0) {
-          const bool in = n < a.N && k < a.K;
+          const bool in = n < a.N && k0 < a.K;
           cp16(md, in ? src : a.meta, in);
         } else if ((a.K & 63) == 0) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const bool in = n < a.N && k + i * 64 < a.K;
+            const bool in = n < a.N && k0 + i * 64 < a.K;
             cp4(md + i * 4, in ? src + i * 4 : a.meta, in);
           }
         } else {  // an odd number of groups a row: scales are 2-byte aligned
           uint32_t v[4] = {};
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (n < a.N && k + i * 32 < a.K)
+            if (n < a.N && k0 + i * 32 < a.K)
               v[i >> 1] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(src) + i)) << (16 * (i & 1));
           sts128(md, make_uint4(v[0], v[1], v[2], v[3]));
         }
@@ -242,6 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
   };
   for (int i = 0; i < p.slots - 1; ++i) issue();
   load_x<QUANT, XF32>(a, p, t0, tok, 0, xs, sums);
+  __syncthreads();
   int have = 0;  // slice of x in shared memory
 
   float acc[NT][4];
@@ -257,8 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
 #pragma unroll
   for (int n = 0; n < NT; ++n) xt[n] = xs + min(n * 8 + r, tok - 1) * p.x_pitch + c * 16;
   constexpr uint32_t kBias = QUANT == MOE_Q4_0 ? 0x43084308u : 0x43004300u;  // 136, 128
-  const uint32_t row0 = wk * R + wr * 16 + r;
-  const uint32_t q_off = row0 * 128 + c * 4, m_off = kCodeBytes + row0 * 16;
+  const uint32_t q_off = r * 128 + c * 4, m_off = kCodeBytes + r * 16;
   uint32_t swz[8];  // piece of group g; rows r and r + 8 have one phase
 #pragma unroll
   for (int g = 0; g < 8; ++g) swz[g] = q_off + (static_cast<uint32_t>(g ^ (r & 7)) << 4);
@@ -272,25 +278,26 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
       static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
   };
 
-  int slot = 0, stage = 0;
+  int slot = 0, stage = 0, round = 0;
   for (int tile = blockIdx.x; tile < p.tiles;) {
     switch (p.slots) {
       case 3: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
       case 4: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
       default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;  // five
     }
-    __syncthreads();
+    __syncwarp();  // the warp's stage is there, and the one before it used up
     issue();
     if (n_slices > 1) {
       const int slice = stage * stage_k / p.kx;
-      if (slice != have) {  // x does not fit: the next slice (every thread is past the last one)
+      if (slice != have) {  // x does not fit: the next slice
+        __syncthreads();
         load_x<QUANT, XF32>(a, p, t0, tok, slice * p.kx, xs, sums);
         have = slice;
         __syncthreads();
       }
     }
     const int k0 = stage * stage_k - have * p.kx + wk * kWK;  // within the slice
-    const uint32_t st = ring + slot * kStageBytes, xk = k0 * 2;
+    const uint32_t st = ring + slot * kWarpStage, xk = k0 * 2;
     const uint4 m0 = lds128(st + m_off), m1 = lds128(st + m_off + 128);
     const uint32_t ma[4] = {m0.x, m0.y, m0.z, m0.w}, mb[4] = {m1.x, m1.y, m1.z, m1.w};
     const int left = a.K - (stage * stage_k + wk * kWK);  // k of this warp's stage; may be negative
@@ -359,20 +366,24 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
     } else {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if (n > 0) __syncthreads();  // (the first write follows a stage's barrier)
+        // the WK warps of the rows meet; two buffers, so that one barrier a
+        // round also keeps a write behind the reads of the round before last
+        float* const buf = red + (round & 1) * (kWarps * 16 * 8);
+        ++round;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          *reinterpret_cast<float2*>(red + (warp * 16 + r + 8 * h) * 8 + c * 2) =
+          *reinterpret_cast<float2*>(buf + (warp * 16 + r + 8 * h) * 8 + c * 2) =
               make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
           acc[n][2 * h] = acc[n][2 * h + 1] = 0.f;
         }
-        __syncthreads();
-        for (int e = tid; e < R * 8; e += kThreads) {
-          const int row = e % R, t = e / R, nn = tile * R + row;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + wr), "r"(32 * WK) : "memory");
+#pragma unroll
+        for (int e = wk * 32 + lane; e < 16 * 8; e += 32 * WK) {
+          const int row = e & 15, t = e >> 4, nn = tile * R + wr * 16 + row;
           if (nn >= a.N || n * 8 + t >= tok) continue;
           float v = 0.f;
 #pragma unroll
-          for (int k = 0; k < WK; ++k) v += red[(((row >> 4) * WK + k) * 16 + (row & 15)) * 8 + t];
+          for (int k = 0; k < WK; ++k) v += buf[((wr * WK + k) * 16 + row) * 8 + t];
           store(nn, n * 8 + t, v);
         }
       }
@@ -383,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
 }
 
 constexpr int kFull = 226 * 1024;              // shared memory of a CTA
-constexpr int kRedBytes = kWarps * 16 * 8 * 4;
+constexpr int kRedBytes = 2 * kWarps * 16 * 8 * 4;
 
 // Shared bytes of x of a slice and its sums.
 inline int64_t x_bytes(int quant, int parts, int tok, int64_t kx) {
