@@ -47,6 +47,7 @@ struct Plan {
   int x_bytes;     // all tokens and parts
   int slots;       // ring
   int tiles;       // row tiles
+  uint32_t one;    // 128 in both halves, as bf16
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -54,6 +55,9 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
@@ -81,8 +85,14 @@ __device__ __forceinline__ void mma0(float* d, const uint32_t* a, uint32_t b0, u
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
-// d[0..1] += s * v[0..1], one instruction
+// d[0..1] += s * v[0..1]; as one instruction where the pair (s, s) serves several
+template <bool PACKED>
 __device__ __forceinline__ void fma2(float* d, float s, const float* v) {
+  if (!PACKED) {
+    d[0] += s * v[0];
+    d[1] += s * v[1];
+    return;
+  }
   unsigned long long dd, vv, ss;
   asm("mov.b64 %0, {%1, %2};" : "=l"(dd) : "f"(d[0]), "f"(d[1]));
   asm("mov.b64 %0, {%1, %2};" : "=l"(vv) : "f"(v[0]), "f"(v[1]));
@@ -93,11 +103,19 @@ __device__ __forceinline__ void fma2(float* d, float s, const float* v) {
 // The eight codes of a 4-byte word as bf16 integers less `bias` - 128: the
 // nibble becomes the low mantissa bits of 128 (exact), bias is subtracted
 // (exact). o[0], o[1]: low nibbles of bytes 0,2 and 1,3; o[2], o[3]: high ones.
-__device__ __forceinline__ void codes(uint32_t w, uint32_t bias2, uint32_t* o) {
-  o[0] = (w & 0x000F000Fu) | 0x43004300u;
-  o[1] = ((w >> 8) & 0x000F000Fu) | 0x43004300u;
-  o[2] = ((w >> 4) & 0x000F000Fu) | 0x43004300u;
-  o[3] = ((w >> 12) & 0x000F000Fu) | 0x43004300u;
+// (w & mask) | one is one instruction only if `one` (128 in both halves) sits in
+// a register, which the compiler grants a value it does not know: it comes with
+// the launch's parameters.
+__device__ __forceinline__ uint32_t code2(uint32_t w, uint32_t one) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(r) : "r"(w), "r"(one));
+  return r;
+}
+__device__ __forceinline__ void codes(uint32_t w, uint32_t one, uint32_t bias2, uint32_t* o) {
+  o[0] = code2(w, one);
+  o[1] = code2(w >> 8, one);
+  o[2] = code2(w >> 4, one);
+  o[3] = code2(w >> 12, one);
 #pragma unroll
   for (int i = 0; i < 4; ++i) asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(o[i]) : "r"(bias2));
 }
@@ -204,36 +222,50 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
     const int row = (lane >> 3) + 4 * i;
     dst[i] = row * 128 + ((piece ^ (row & 7)) << 4);
   }
+  // Of the tile being copied: its codes and scales, this lane's offsets into
+  // them (the same in every tile), and whether the warp's rows are all rows.
+  const uint8_t *code0, *meta0;
+  bool full_rows;
+  uint32_t off[kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+    off[i] = static_cast<uint32_t>(wr * 16 + (lane >> 3) + 4 * i) * (a.K / 2) + wk * (kWK / 2) + piece * 16;
+  const uint32_t moff = static_cast<uint32_t>(wr * 16 + (lane & 15)) * (a.K / 16) + wk * (kWK / 16);
+  auto open_tile = [&]() {
+    code0 = a.w + static_cast<int64_t>(ld_tile) * R * (a.K / 2);
+    meta0 = a.meta + static_cast<int64_t>(ld_tile) * R * (a.K / 16);
+    full_rows = ld_tile * R + wr * 16 + 16 <= a.N;
+  };
+  open_tile();
   auto issue = [&]() {
     if (ld_tile < p.tiles) {
       const uint32_t st = ring + ld_slot * kWarpStage;
-      const int n0 = ld_tile * R + wr * 16, k0 = ld_stage * stage_k + wk * kWK;
-      const uint8_t* const w0 =
-          a.w + static_cast<int64_t>(n0 + (lane >> 3)) * (a.K / 2) + k0 / 2 + piece * 16;
-      const bool k_in = k0 + piece * 32 < a.K;
+      const int k0 = ld_stage * stage_k, left = a.K - k0 - wk * kWK;  // k of this warp's stage
+      const uint32_t md = st + kCodeBytes + (lane & 15) * 16;
+      if (full_rows && left >= kWK) {
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const bool in = k_in && n0 + (lane >> 3) + 4 * i < a.N;
-        cp16(st + dst[i], in ? w0 + 4 * i * (a.K / 2) : a.w, in);
+        for (int i = 0; i < kPieces; ++i) cp16(st + dst[i], code0 + (off[i] + k0 / 2));
+      } else {
+        const int n0 = ld_tile * R + wr * 16 + (lane >> 3);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const bool in = n0 + 4 * i < a.N && piece * 32 < left;
+          cp16(st + dst[i], in ? code0 + (off[i] + k0 / 2) : a.w, in);
+        }
       }
       if (lane < 16) {
-        const int n = n0 + lane;
-        const uint32_t md = st + kCodeBytes + lane * 16;
-        const uint8_t* src = a.meta + static_cast<int64_t>(n) * (a.K / 16) + k0 / 16;
+        const bool in = full_rows || ld_tile * R + wr * 16 + lane < a.N;
+        const uint8_t* src = meta0 + (moff + k0 / 16);
         if ((a.K & 255) == 0) {
-          const bool in = n < a.N && k0 < a.K;
-          cp16(md, in ? src : a.meta, in);
+          cp16(md, in && left > 0 ? src : a.w, in && left > 0);
         } else if ((a.K & 63) == 0) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool in = n < a.N && k0 + i * 64 < a.K;
-            cp4(md + i * 4, in ? src + i * 4 : a.meta, in);
-          }
+          for (int i = 0; i < 4; ++i) cp4(md + i * 4, in && i * 64 < left ? src + i * 4 : a.w, in && i * 64 < left);
         } else {  // an odd number of groups a row: scales are 2-byte aligned
           uint32_t v[4] = {};
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (n < a.N && k0 + i * 32 < a.K)
+            if (in && i * 32 < left)
               v[i >> 1] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(src) + i)) << (16 * (i & 1));
           sts128(md, make_uint4(v[0], v[1], v[2], v[3]));
         }
@@ -242,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
       if (++ld_stage == stages_tile) {
         ld_stage = 0;
         ld_tile += gridDim.x;
+        if (ld_tile < p.tiles) open_tile();
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");  // empty groups keep the count
@@ -265,9 +298,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
   for (int n = 0; n < NT; ++n) xt[n] = xs + min(n * 8 + r, tok - 1) * p.x_pitch + c * 16;
   constexpr uint32_t kBias = QUANT == MOE_Q4_0 ? 0x43084308u : 0x43004300u;  // 136, 128
   const uint32_t q_off = r * 128 + c * 4, m_off = kCodeBytes + r * 16;
-  uint32_t swz[8];  // piece of group g; rows r and r + 8 have one phase
-#pragma unroll
-  for (int g = 0; g < 8; ++g) swz[g] = q_off + (static_cast<uint32_t>(g ^ (r & 7)) << 4);
 
   auto store = [&](int n, int t, float v) {
     if (a.bias) v += __ldg(a.bias + n);
@@ -298,6 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
     }
     const int k0 = stage * stage_k - have * p.kx + wk * kWK;  // within the slice
     const uint32_t st = ring + slot * kWarpStage, xk = k0 * 2;
+    static_assert(kWarpStage % 128 == 0, "a slot's rows start at multiples of 128, so a piece's offset can be XORed in");
+    const uint32_t q0 = (st + q_off) ^ (static_cast<uint32_t>(r & 7) << 4);
     const uint4 m0 = lds128(st + m_off), m1 = lds128(st + m_off + 128);
     const uint32_t ma[4] = {m0.x, m0.y, m0.z, m0.w}, mb[4] = {m1.x, m1.y, m1.z, m1.w};
     const int left = a.K - (stage * stage_k + wk * kWK);  // k of this warp's stage; may be negative
@@ -309,8 +341,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
       for (int h = 0; h < 2; ++h) {
         const int g = 2 * g2 + h;
         uint32_t wa[4], wb[4];
-        codes(lds32(st + swz[g]), kBias, wa);
-        codes(lds32(st + swz[g] + 8 * 128), kBias, wb);
+        // the piece of group g; rows r and r + 8 have one phase
+        const uint32_t at = q0 ^ (static_cast<uint32_t>(g) << 4);
+        codes(lds32(at), p.one, kBias, wa);
+        codes(lds32(at + 8 * 128), p.one, kBias, wb);
         const uint32_t f0[4] = {wa[0], wb[0], wa[1], wb[1]}, f1[4] = {wa[2], wb[2], wa[3], wb[3]};
         float(*d)[4] = s[QUANT == MOE_Q4_0 ? h : 0];
 #pragma unroll
@@ -330,10 +364,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
         const float2 db = __half22float2(*reinterpret_cast<const __half2*>(&mb[g2]));
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          fma2(acc[n], da.x, s[0][n]);
-          fma2(acc[n] + 2, db.x, s[0][n] + 2);
-          fma2(acc[n], da.y, s[1][n]);
-          fma2(acc[n] + 2, db.y, s[1][n] + 2);
+          fma2<(NT > 1)>(acc[n], da.x, s[0][n]);
+          fma2<(NT > 1)>(acc[n] + 2, db.x, s[0][n] + 2);
+          fma2<(NT > 1)>(acc[n], da.y, s[1][n]);
+          fma2<(NT > 1)>(acc[n] + 2, db.y, s[1][n] + 2);
         }
       } else {
         const float sa = __uint_as_float(ma[g2] << 16), ba = __uint_as_float(ma[g2] & 0xFFFF0000u);
@@ -343,10 +377,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
         for (int n = 0; n < NT; ++n) {
           const float2 u = *reinterpret_cast<const float2*>(su + n * 8);
           const float xsum[2] = {u.x, u.y};
-          fma2(acc[n], sa, s[0][n]);
-          fma2(acc[n] + 2, sb, s[0][n] + 2);
-          fma2(acc[n], ba, xsum);
-          fma2(acc[n] + 2, bb, xsum);
+          fma2<(NT > 1)>(acc[n], sa, s[0][n]);
+          fma2<(NT > 1)>(acc[n] + 2, sb, s[0][n] + 2);
+          fma2<(NT > 1)>(acc[n], ba, xsum);
+          fma2<(NT > 1)>(acc[n] + 2, bb, xsum);
         }
       }
     }
@@ -407,6 +441,7 @@ cudaError_t launch(const LinearArgs& a, int blocks_t, int num_sms, cudaStream_t 
   Plan p;
   p.tok = (a.T + blocks_t - 1) / blocks_t;
   p.tiles = (a.N + R - 1) / R;
+  p.one = 0x43004300u;
   // a ring of five to three slots beside all of x, else x in slices of whole stages
   const int stages = (a.K + stage_k - 1) / stage_k;
   int n = 1;
@@ -430,15 +465,17 @@ cudaError_t launch(const LinearArgs& a, int blocks_t, int num_sms, cudaStream_t 
 
 // Rows of a tile: the largest of 256, 128, 64 and 32 that leaves each SM six
 // tiles (they end unevenly), 32 where none does. A stage of small tiles is long
-// in K: not longer than K, and one stage of x has to fit.
+// in K: not longer than K, and one stage of x has to fit. Where x goes in slices
+// every tile loads all of it again, so tiles are large: one for two SMs is
+// enough (32,768 x 8,192 at 24 tokens: 64 rows 154 us).
 template <int QUANT, bool XF32, int NT>
 cudaError_t by_rows(const LinearArgs& a, int blocks_t, int num_sms, cudaStream_t st) {
   constexpr int kParts = XF32 ? 3 : 1;
   const int tok = (a.T + blocks_t - 1) / blocks_t;
+  auto fits = [&](int64_t k) { return x_bytes(QUANT, kParts, tok, k) + kRedBytes + 3 * kStageBytes <= kFull; };
+  const int64_t want = fits((a.K + kWK - 1) / kWK * kWK) ? 6 * num_sms : num_sms / 2;
   int wk = 1;
-  while (wk < 8 && a.N < 256 / wk * 6 * num_sms && a.K > wk * kWK &&
-         x_bytes(QUANT, kParts, tok, 2 * wk * kWK) + kRedBytes + 3 * kStageBytes <= kFull)
-    wk *= 2;
+  while (wk < 8 && a.N < 256 / wk * want && a.K > wk * kWK && fits(2 * wk * kWK)) wk *= 2;
   switch (wk) {
     case 1: return launch<QUANT, XF32, NT, 1>(a, blocks_t, num_sms, st);
     case 2: return launch<QUANT, XF32, NT, 2>(a, blocks_t, num_sms, st);
