@@ -2,7 +2,8 @@
 // copy-on-write, write, free, compact, copy.
 //
 // The integer work (page counts, lowest free pages, moves) runs in one cluster
-// of 8 CTAs: every phase reads a consistent state, a cluster barrier separates
+// of 8 CTAs (one CTA is slower even for a pool of 260 pages and 36 sequences:
+// fork 6.1 against 5.5 us, reserve 11.6 against 10.7, cold): every phase reads a consistent state, a cluster barrier separates
 // it from the phase that changes that state, and nothing returns to the host,
 // so a decode step that grows its sequences stays capturable in a CUDA graph.
 // A call first checks its whole list in every CTA of the cluster (the same
@@ -137,10 +138,10 @@ struct Strip {
   int first, last;
 };
 __device__ __forceinline__ Strip strip_of(int P, int w) {
-  const int strips = (P + 31) / 32;
+  const int per = ((P + 31) / 32 + kAllWarps - 1) / kAllWarps;  // strips of 32 a warp
   Strip s;
-  s.first = static_cast<int>(static_cast<int64_t>(strips) * w / kAllWarps) * 32;
-  s.last = min(P, static_cast<int>(static_cast<int64_t>(strips) * (w + 1) / kAllWarps) * 32);
+  s.first = min(P, w * per * 32);
+  s.last = min(P, (w + 1) * per * 32);
   return s;
 }
 // Free pages in a warp's strips (every lane gets the count).
@@ -158,7 +159,7 @@ __device__ __forceinline__ void share_counts(cg::cluster_group& cluster, int* co
 // Sum of the counts of warps before w, and of all.
 __device__ __forceinline__ int2 prefix_of(const int* counts, int w, int lane) {
   int before = 0, all = 0;
-#pragma unroll
+  #pragma unroll
   for (int i = lane; i < kAllWarps; i += 32) {
     const int c = counts[i];
     all += c;
@@ -186,12 +187,14 @@ __device__ __forceinline__ int block_incl(int v, int* tmp, int* total) {
 }
 
 // first[i]: requests of the sequences before the i-th; info[i]: its pages
-// before the call, times two, plus one if it copies its last page first.
+// before the call, times two, plus one if it copies its last page first;
+// copies[i]: such sequences before it.
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     reserve_kernel(Kv kv, const int32_t* __restrict__ seqs, const int32_t* __restrict__ n_new, int n) {
   extern __shared__ int dyn[];
   int* first = dyn;
   int* info = dyn + n + 1;
+  int* copies = info + n;
   __shared__ uint32_t bits[kBitmapWords];
   __shared__ int counts[kAllWarps];
   __shared__ int scan[kWarps];
@@ -227,15 +230,14 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
   const int mine = count_free(kv, st, lane);
   share_counts(cluster, counts, w, lane, mine);  // also publishes shr and last
   // requests of every listed sequence
-  int total = 0;
+  int total = 0, n_copies = 0;
   if (ok && room && !stop) {
     for (int i0 = 0; i0 < n; i0 += kThreads) {
       const int i = i0 + tid;
-      int need = 0;
+      int need = 0, cow = 0;
       if (i < n) {
         const int s = seqs[i], len = kv.lens[s], add = n_new[i];
         const int have = pages_of(kv, len);
-        int cow = 0;
         if (add > 0 && (len & (kv.page - 1))) {
           const int p = kv.table[static_cast<int64_t>(s) * kv.W + have - 1];
           const int k = __ldcg(kv.shr + p);
@@ -248,6 +250,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
       int t;
       const int incl = block_incl(need, scan, &t);
       if (i < n) first[i] = total + incl - need;
+      int c;
+      const int before = block_incl(cow, scan, &c) - cow;
+      if (i < n) copies[i] = n_copies + before;
+      n_copies += c;
       // the pool bounds what can be granted; beyond it only the verdict counts
       total = min(total + t, kv.P + 1);
     }
@@ -300,42 +306,61 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     const int j = q - first[lo], cow = info[lo] & 1, e = (info[lo] >> 1) + j - cow;
     const int p = kv.src[q];
     int32_t* at = kv.table + static_cast<int64_t>(seqs[lo]) * kv.W + e;
-    if (cow && j == 0) atomicSub(kv.ref + *at, 1);
-    if (cow && j == 0) kv.map[lo] = *at;
+    if (cow && j == 0) {
+      atomicSub(kv.ref + *at, 1);
+      kv.map[copies[lo]] = *at;
+      kv.dst[copies[lo]] = p;
+    }
     *at = p;
     kv.ref[p] = 1;
   }
   for (int i = rank * kThreads + tid; i < n; i += kAll) {
     const int s = seqs[i], len = kv.lens[s];
     kv.lens[s] = len + n_new[i];
-    kv.filled[i] = info[i] & 1 ? len & (kv.page - 1) : 0;
-    if (info[i] & 1) kv.dst[i] = kv.src[first[i]];
+    if (info[i] & 1) kv.filled[copies[i]] = len & (kv.page - 1);
   }
-  if (rank == 0 && tid == 0) kv.work->n_copies = n;
+  if (rank == 0 && tid == 0) kv.work->n_copies = n_copies;
 }
 
-// The copies of reserve: entry i copies the first filled[i] tokens of page
-// map[i] to page dst[i], in every layer and head of k and v. A warp copies
-// one (entry, layer, k or v, head) at a time.
+// x / d and x % d, in 32 bits where x fits (a 64-bit division takes several hundred cycles)
+__device__ __forceinline__ uint32_t take_mod(uint64_t& x, uint32_t d) {
+  if (x >> 32) {
+    const uint64_t q = x / d;
+    const uint32_t r = static_cast<uint32_t>(x - q * d);
+    x = q;
+    return r;
+  }
+  const uint32_t y = static_cast<uint32_t>(x), q = y / d;
+  x = q;
+  return y - q * d;
+}
+
+// The copies of reserve: copy i takes the first filled[i] tokens of page map[i]
+// to page dst[i], in every layer and head of k and v. A warp copies 128 vectors
+// (2 KB) at a time, four loads a lane in flight.
+constexpr int kCowPiece = 128;
 __global__ void __launch_bounds__(256)
     cow_copy_kernel(Kv kv, uint4* k, uint4* v, int L, int H, int tok_vecs, int64_t page_vecs) {
   const int n = kv.work->n_copies, lane = threadIdx.x & 31;
-  const int64_t items = static_cast<int64_t>(n) * L * 2 * H;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t it = blockIdx.x * 8ll + (threadIdx.x >> 5); it < items; it += warps) {
-    int64_t r = it;
-    const int h = static_cast<int>(r % H);
-    r /= H;
-    uint4* pool = r & 1 ? v : k;
-    r >>= 1;
-    const int l = static_cast<int>(r % L), i = static_cast<int>(r / L);
-    const int vecs = kv.filled[i] * tok_vecs;
-    if (vecs == 0) continue;
-    const int64_t head = static_cast<int64_t>(h) * kv.page * tok_vecs;
+  const int pieces = (kv.page * tok_vecs + kCowPiece - 1) / kCowPiece;
+  const uint64_t items = static_cast<uint64_t>(n) * L * 2 * H * pieces;
+  for (uint64_t it = blockIdx.x * 8ull + (threadIdx.x >> 5); it < items; it += gridDim.x * 8ull) {
+    uint64_t r = it;
+    const int p = take_mod(r, pieces), h = take_mod(r, H);
+    uint4* pool = take_mod(r, 2) ? v : k;
+    const int l = take_mod(r, L), i = static_cast<int>(r);
+    const int vecs = kv.filled[i] * tok_vecs - p * kCowPiece;  // of this piece on
+    if (vecs <= 0) continue;
+    const int64_t head = static_cast<int64_t>(h) * kv.page * tok_vecs + p * kCowPiece;
     const uint4* from = pool + (static_cast<int64_t>(l) * kv.P + kv.map[i]) * page_vecs + head;
     uint4* to = pool + (static_cast<int64_t>(l) * kv.P + kv.dst[i]) * page_vecs + head;
-#pragma unroll 4
-    for (int x = lane; x < vecs; x += 32) to[x] = from[x];
+    uint4 t[kCowPiece / 32];
+#pragma unroll
+    for (int x = 0; x < kCowPiece / 32; ++x)
+      if (lane + 32 * x < vecs) t[x] = from[lane + 32 * x];
+#pragma unroll
+    for (int x = 0; x < kCowPiece / 32; ++x)
+      if (lane + 32 * x < vecs) to[lane + 32 * x] = t[x];
   }
 }
 
@@ -397,14 +422,12 @@ __global__ void __launch_bounds__(256)
   if (REMAP) n = kv.work->n_copies;
   else if (pending(kv)) return;
   const int pieces = static_cast<int>((page_vecs + kPiece - 1) / kPiece);
-  const int64_t items = static_cast<int64_t>(n) * L * 2 * pieces;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    int64_t r = it;
-    const int piece = static_cast<int>(r % pieces);
-    r /= pieces;
-    uint4* pool = r & 1 ? v : k;
-    r >>= 1;
-    const int l = static_cast<int>(r % L), i = static_cast<int>(r / L);
+  const uint64_t items = static_cast<uint64_t>(n) * L * 2 * pieces;
+  for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    uint64_t r = it;
+    const int piece = take_mod(r, pieces);
+    uint4* pool = take_mod(r, 2) ? v : k;
+    const int l = take_mod(r, L), i = static_cast<int>(r);
     const int s = src[i], d = dst[i];
     if (!REMAP && (s < 0 || s >= kv.P || d < 0 || d >= kv.P)) {
       if (threadIdx.x == 0) atomicOr(&kv.work->err, MOE_DEVERR_BADIDX);
@@ -441,15 +464,27 @@ __global__ void __launch_bounds__(256)
                  int64_t ldv, const int32_t* __restrict__ seqs, const int32_t* __restrict__ cu, int n, int n_rows,
                  int H, int tok_vecs) {
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= n_rows || pending(kv)) return;
-  int lo = 0, hi = n;  // the last i with cu[i] <= row
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(cu + mid) <= row)
-      lo = mid;
-    else
-      hi = mid;
+  if (row >= n_rows) return;
+  const uint4* fk = nk + row * ldk;
+  const uint4* fv = nv + row * ldv;
+  const int vecs = H * tok_vecs;
+  uint4 k0, v0;  // the row's first pieces, while its place is looked up
+  if (lane < vecs) {
+    k0 = __ldg(fk + lane);
+    v0 = __ldg(fv + lane);
   }
+  const bool stop = pending(kv);
+  // the last i with cu[i] <= row: 32 probes a step
+  int lo = 0, span = n;  // it is in [lo, lo + span)
+  while (span > 1) {
+    const int step = (span + 31) / 32, at = lo + lane * step;
+    const unsigned int b = __ballot_sync(~0u, at < lo + span && __ldg(cu + at) <= row);
+    const int hit = b ? 31 - __clz(b) : 0;
+    const int next = lo + hit * step;
+    span = min(step, lo + span - next);
+    lo = next;
+  }
+  if (stop) return;
   const int r0 = __ldg(cu + lo), r1 = __ldg(cu + lo + 1);
   if (row < r0 || row >= r1) return;
   const int s = seqs ? __ldg(seqs + lo) : lo;
@@ -467,15 +502,12 @@ __global__ void __launch_bounds__(256)
     if (lane == 0) atomicOr(&kv.work->err, p < 0 || p >= kv.P ? MOE_DEVERR_BADIDX : KV_DEVERR_SHARED);
     return;
   }
-  const uint4* fk = nk + row * ldk;
-  const uint4* fv = nv + row * ldv;
   const int64_t base = ((static_cast<int64_t>(p) * H) << kv.page_shift) + (at & (kv.page - 1));
-#pragma unroll 4
-  for (int x = lane; x < H * tok_vecs; x += 32) {
+  for (int x = lane; x < vecs; x += 32) {
     const int h = x / tok_vecs, c = x - h * tok_vecs;
     const int64_t to = (base + (static_cast<int64_t>(h) << kv.page_shift)) * tok_vecs + c;
-    k[to] = __ldg(fk + x);
-    v[to] = __ldg(fv + x);
+    k[to] = x < 32 ? k0 : __ldg(fk + x);
+    v[to] = x < 32 ? v0 : __ldg(fv + x);
   }
 }
 
@@ -513,13 +545,14 @@ cudaError_t launch_kv_fork(const moe_kv_t& a, const KvLayout& l, const int32_t* 
 
 cudaError_t launch_kv_reserve(const moe_kv_t& a, const KvLayout& l, const int32_t* seqs, const int32_t* n_new,
                               int32_t n, int num_sms, cudaStream_t st) {
-  const int smem = (2 * n + 1) * 4;
-  cudaError_t e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (2 * kMaxList + 1) * 4);
+  const int smem = (3 * n + 1) * 4;
+  cudaError_t e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (3 * kMaxList + 1) * 4);
   if (e != cudaSuccess) return e;
   const Kv kv = kv_of(a, l);
   reserve_kernel<<<kCtas, kThreads, smem, st>>>(kv, seqs, n_new, n);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int64_t items = static_cast<int64_t>(n) * a.n_layers * 2 * a.n_kv_heads;
+  const int pieces = (a.page_tokens * tok_vecs(a) + kCowPiece - 1) / kCowPiece;
+  const int64_t items = static_cast<int64_t>(n) * a.n_layers * 2 * a.n_kv_heads * pieces;
   const int grid = static_cast<int>(std::min<int64_t>((items + 7) / 8, 8ll * num_sms));
   cow_copy_kernel<<<grid, 256, 0, st>>>(kv, static_cast<uint4*>(a.k), static_cast<uint4*>(a.v), a.n_layers,
                                         a.n_kv_heads, tok_vecs(a), page_vecs(a));
