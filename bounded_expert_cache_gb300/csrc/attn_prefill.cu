@@ -21,6 +21,10 @@
 // row tile is its softmax and its two products; the products of the other row
 // tile fit into it. PV starts on the first 64 tokens while the numerators of
 // the others are formed.
+// Heads of at most 64 leave tensor memory for P beside S: the scores of the next
+// tile are formed as soon as those of this one are in registers, in the order
+//   QK0(j+1) PV0(j) QK1(j+1) PV1(j),
+// and a row tile's time is that of its softmax alone.
 //
 // Warps: 0-3 and 4-7 softmax of row tiles 0 and 1, one thread a row (they also
 // write the results), 8 TMA of K and V pages, 9 MMA issue, 10 and 11 load Q
@@ -59,13 +63,17 @@ constexpr int kUnitRows = 2 * kQT;
 constexpr int kUnitCost = 3;   // tiles' worth of time of a unit's Q and results
 constexpr float kRaise = 8.f;  // log2 of the growth that raises m
 
-template <int DP>
+template <int DP, bool APART>
 struct Cfg {
   static constexpr uint32_t kHalf = kKT * 128;              // 64 columns of a tile: 128-byte rows
   static constexpr uint32_t kTile = kHalf * (DP / 64);      // a Q, K or V tile
   static constexpr int kKS = DP == 64 ? 4 : 2, kVS = DP == 64 ? 4 : 3;  // ring slots of K and V
   static constexpr int kTiles = (2 + kKS + kVS) * static_cast<int>(kTile);
-  static constexpr uint32_t kTmemS = 0, kTmemO = 256;       // columns: S0 S1 O0 O1
+  // tensor memory columns: S0 S1 O0 O1, and where O leaves room for them, P0 P1
+  static constexpr bool kApart = APART;
+  static_assert(!APART || DP == 64, "columns");
+  static constexpr uint32_t kTmemS = 0, kTmemO = 256;
+  static constexpr uint32_t kTmemP = kApart ? 384 : kTmemS, kStrideP = kApart ? 64 : 128;
   // partial rows of one row tile: (m, l, -, -), then O by column quads
   static constexpr int64_t kPart = static_cast<int64_t>(kQT) * (DP + 4);
 };
@@ -170,23 +178,24 @@ struct Walk {
   __device__ __forceinline__ bool more() const { return tiles0() + sp.n + kUnitCost < end; }
 };
 // Shared memory behind the tiles.
-template <int DP>
+template <int DP, bool APART>
 struct Shared {
-  using C = Cfg<DP>;
+  using C = Cfg<DP, APART>;
   // kf/ke, vf/ve: full and empty slots of the rings; vr: V checked; qr, qe: Q
-  // tile ready, free; sr: scores ready; pa, pb: numerators of the first and the
-  // last 64 tokens ready; of: O final
+  // tile ready, free; sr: scores ready; sc: scores read (kApart); pa, pb:
+  // numerators of the first and the last 64 tokens ready; pv: P read, O current
+  // (kApart); of: O final
   uint64_t kf[C::kKS], ke[C::kKS], vf[C::kVS], ve[C::kVS], vr[C::kVS];
-  uint64_t qr[2], qe[2], sr[2], pa[2], pb[2], of[2], drain;
+  uint64_t qr[2], qe[2], sr[2], sc[2], pa[2], pb[2], pv[2], of[2], drain;
   int64_t scan[kThreads / 32];
   Walk walk;
   uint32_t poison[8];  // ring over units: number + 1 of a unit with an infinity or NaN to hide
   uint32_t tmem;
   int abort;
 };
-template <int DP>
-constexpr int kSmem = Cfg<DP>::kTiles + static_cast<int>(sizeof(Shared<DP>));
-static_assert(kSmem<128> <= 227 * 1024, "shared memory");
+template <int DP, bool APART>
+constexpr int kSmem = Cfg<DP, APART>::kTiles + static_cast<int>(sizeof(Shared<DP, APART>));
+static_assert(kSmem<128, false> <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ int unit_count(const AttnArgs& a, int m) {
   return static_cast<int>((static_cast<int64_t>(m) * a.g + kUnitRows - 1) / kUnitRows);
@@ -255,11 +264,11 @@ __device__ __noinline__ void row_by_row(const AttnArgs& a, const Walk& w, const 
   ml[1] = l;
 }
 
-template <int DP>
+template <int DP, bool APART>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, AttnArgs a,
                    long long wait_cycles) {
-  using C = Cfg<DP>;
+  using C = Cfg<DP, APART>;
   extern __shared__ __align__(1024) unsigned char smraw[];
   const uint32_t sbase = su32(smraw);
   if (sbase & 1023u) {  // the swizzle's pattern starts at such a boundary
@@ -267,7 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const uint32_t sq = sbase, sk = sbase + 2 * C::kTile, sv = sk + C::kKS * C::kTile;
-  Shared<DP>& sh = *reinterpret_cast<Shared<DP>*>(smraw + C::kTiles);
+  using Sh = Shared<DP, APART>;
+  Sh& sh = *reinterpret_cast<Sh*>(smraw + C::kTiles);
   int* const s_first = reinterpret_cast<int*>(smraw);  // before the tiles are in use
   volatile int* abort_flag = &sh.abort;
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
@@ -365,6 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(su32(&sh.qr[t]), 1);
       mbar_init(su32(&sh.qe[t]), 1);
       mbar_init(su32(&sh.sr[t]), 1);
+      mbar_init(su32(&sh.sc[t]), kSoftWarps / 2);
+      mbar_init(su32(&sh.pv[t]), 1);
       mbar_init(su32(&sh.pa[t]), kSoftWarps / 2);
       mbar_init(su32(&sh.pb[t]), kSoftWarps / 2);
       mbar_init(su32(&sh.of[t]), 1);
@@ -463,12 +475,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         umma_commit(su32(&sh.sr[t]));
       };
+      // O += P V of tile j of the unit
+      auto pv = [&](int t, int j) -> bool {
+        const uint64_t vb = sdesc_mn(sv + vp.s * C::kTile, C::kHalf);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!wait(hf ? &sh.pb[t] : &sh.pa[t], p_ph[t])) return false;
+          fence_after();
+#pragma unroll
+          for (int k = 4 * hf; k < 4 * hf + 4; ++k)
+            umma_ts(tmem + C::kTmemO + t * static_cast<uint32_t>(DP), tmem + C::kTmemP + t * C::kStrideP + 8u * k,
+                    vb + k * (2048u >> 4), id_pv, k > 0 || j > 0);
+        }
+        p_ph[t] ^= 1u;
+        if (C::kApart) umma_commit(su32(&sh.pv[t]));
+        return true;
+      };
+      uint32_t s_n[2] = {0, 0};  // scores formed (kApart)
+      auto scores_read = [&](int t) -> bool {
+        if (!C::kApart) return true;
+        const uint32_t n = s_n[t]++;
+        return n == 0 || wait(&sh.sc[t], (n - 1) & 1u);
+      };
       while (ok) {
         const int nq = w.rows > kQT ? 2 : 1;
         if (!(ok = wait(&sh.kf[kp.s], kp.ph))) break;
         for (int t = 0; t < nq && ok; ++t) {
           uint32_t& ph = t ? q_ph1 : q_ph;
-          if (!(ok = wait(&sh.qr[t], ph))) break;
+          if (!(ok = wait(&sh.qr[t], ph) && scores_read(t))) break;
           ph ^= 1u;
           fence_after();
           qk(t);
@@ -480,25 +514,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < w.nt && ok; ++j) {
           const bool more = j + 1 < w.nt;
           for (int t = 0; t < nq; ++t) {
-            if (t == 0 && !(ok = wait(&sh.vr[vp.s], vp.ph))) break;
-            const uint64_t vb = sdesc_mn(sv + vp.s * C::kTile, C::kHalf);
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              if (!(ok = wait(hf ? &sh.pb[t] : &sh.pa[t], p_ph[t]))) break;
+            // (kApart: first the scores of the next tile, which need only this one's to be in registers)
+            if (C::kApart && more) {
+              if (t == 0 && !(ok = wait(&sh.kf[kp.s], kp.ph))) break;
+              if (!(ok = scores_read(t))) break;
               fence_after();
-#pragma unroll
-              for (int k = 4 * hf; k < 4 * hf + 4; ++k)
-                umma_ts(tmem + C::kTmemO + t * static_cast<uint32_t>(DP), tmem + C::kTmemS + t * 128u + 8u * k,
-                        vb + k * (2048u >> 4), id_pv, k > 0 || j > 0);
+              qk(t);
+              if (j + 2 == w.nt) umma_commit(su32(&sh.qe[t]));
             }
-            if (!ok) break;
-            p_ph[t] ^= 1u;
-            if (more) {
+            if (t == 0 && !(ok = wait(&sh.vr[vp.s], vp.ph))) break;
+            if (!(ok = pv(t, j))) break;
+            if (!more) {
+              umma_commit(su32(&sh.of[t]));
+            } else if (!C::kApart) {
               if (t == 0 && !(ok = wait(&sh.kf[kp.s], kp.ph))) break;
               qk(t);
               if (j + 2 == w.nt) umma_commit(su32(&sh.qe[t]));
-            } else {
-              umma_commit(su32(&sh.of[t]));
             }
           }
           if (!ok) break;
@@ -597,9 +628,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- softmax: one thread a row
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;  // row tile, row
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + C::kTmemS + t * 128u + lanes, to = tmem + C::kTmemO + t * static_cast<uint32_t>(DP) + lanes;
-    const float c = a.scale_log2;
-    uint32_t s_ph = 0, o_ph = 0;
+    const uint32_t ts = tmem + C::kTmemS + t * 128u + lanes, tp = tmem + C::kTmemP + t * C::kStrideP + lanes;
+    const uint32_t to = tmem + C::kTmemO + t * static_cast<uint32_t>(DP) + lanes;
+    const float c = a.scale_log2, raise = kRaise / c;
+    uint32_t s_ph = 0, o_ph = 0, p_n = 0;  // p_n: numerators written (kApart)
     bool ok = true;
     for (uint32_t unit = 0; ok; ++unit) {
       if (t * kQT < w.rows) {
@@ -611,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lo_pos = w.s.len - w.s.m + static_cast<int>(quotient(rg - lane, a.g));
         const int64_t r_last = min(rg - lane + 31, static_cast<int64_t>(w.s.m) * a.g - 1);
         const int hi_pos = w.s.len - w.s.m + static_cast<int>(quotient(r_last, a.g));
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, thr = -INFINITY, l = 0.f;  // thr: a maximum above it raises m
         for (int j = 0; j < w.nt; ++j) {
           ok = mbar_wait(su32(&sh.sr[t]), s_ph, abort_flag, a.err, wait_cycles);
           ok = __all_sync(~0u, ok);
@@ -624,32 +656,51 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int from = a.window > 0 ? last - a.window + 1 : -1;  // columns before it are hidden, but for
           const int keep = a.sinks - tile0;                          // the first `keep`
           float s[128];
+          auto hide = [&](int x) {  // bit y of see: column x + y is visible
+            const uint32_t see = low_bits(last + 1 - x) & (~low_bits(from - x) | low_bits(keep - x));
+            if (__all_sync(~0u, see == ~0u)) return;
+#pragma unroll
+            for (int y = 0; y < 32; ++y) s[x + y] = (see >> y) & 1u ? s[x + y] : -INFINITY;
+          };
+          float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+          auto top = [&](int x) {
+#pragma unroll
+            for (int y = x; y < x + 64; y += 8) {
+              mx0 = max3(mx0, s[y], s[y + 1]);
+              mx1 = max3(mx1, s[y + 2], s[y + 3]);
+              mx2 = max3(mx2, s[y + 4], s[y + 5]);
+              mx3 = max3(mx3, s[y + 6], s[y + 7]);
+            }
+          };
 #pragma unroll
           for (int x = 0; x < 128; x += 32) tmem_ld32_async(ts + x, s + x);
           tmem_wait_ld();
+          if (C::kApart) {
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(su32(&sh.sc[t]));
+          }
           if (edge) {
-#pragma unroll
-            for (int x = 0; x < 128; x += 32) {
-              // bit y: column x + y is visible
-              const uint32_t see = low_bits(last + 1 - x) & (~low_bits(from - x) | low_bits(keep - x));
-#pragma unroll
-              for (int y = 0; y < 32; ++y) s[x + y] = (see >> y) & 1u ? s[x + y] : -INFINITY;
-            }
+            hide(0);
+            hide(32);
+            hide(64);
+            hide(96);
           }
-          float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
-#pragma unroll
-          for (int y = 0; y < 128; y += 8) {
-            mx0 = max3(mx0, s[y], s[y + 1]);
-            mx1 = max3(mx1, s[y + 2], s[y + 3]);
-            mx2 = max3(mx2, s[y + 4], s[y + 5]);
-            mx3 = max3(mx3, s[y + 6], s[y + 7]);
-          }
+          top(0);
+          top(64);
           const float mx = max3(fmaxf(mx0, mx1), mx2, mx3);
-          const bool up = (mx - m) * c > kRaise || (m == -INFINITY && mx > m);
+          if (C::kApart && p_n++ > 0) {  // the product of the tile before has read P and brought O up to date
+            ok = mbar_wait(su32(&sh.pv[t]), p_n & 1u, abort_flag, a.err, wait_cycles);
+            ok = __all_sync(~0u, ok);
+            if (!ok) break;
+            fence_after();
+          }
+          const bool up = mx > thr;
           if (__any_sync(~0u, up)) {
             const float mn = up ? mx : m;
             const float f = up ? ex2((m - mn) * c) : 1.f;  // 0 for the first maximum
             m = mn;
+            thr = up ? m + raise : thr;
             l *= f;
             if (j > 0) {
 #pragma unroll 1
@@ -681,14 +732,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               p[y / 2] = pack_bf16(e0, e1);
               p[y / 2 + 1] = pack_bf16(e2, e3);
             }
-            tmem_st16(ts + x / 2, p);  // over scores already read
-            if (x == 32 || x == 96) {
+            if (x == 64) {  // the first half is in place by now
               tmem_wait_st();
               fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(su32(x == 32 ? &sh.pa[t] : &sh.pb[t]));
+              if (lane == 0) mbar_arrive(su32(&sh.pa[t]));
             }
+            tmem_st16(tp + x / 2, p);  // (over scores that have been read, where P has no columns of its own)
           }
+          tmem_wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(su32(&sh.pb[t]));
           const float2 la = unpack2(add2(l0, l1));
           l += la.x + la.y;
         }
@@ -819,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
-template <int DP>
+template <int DP, bool APART>
 cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t st) {
   CUtensorMap mk, mv;
   const int page = 1 << a.page_shift;
@@ -827,9 +882,9 @@ cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t st) {
   if ((e = map_pages(&mk, a.k, a.D, page, static_cast<int64_t>(a.n_pages) * a.Hkv, std::min(page, kKT))) != cudaSuccess ||
       (e = map_pages(&mv, a.v, a.D, page, static_cast<int64_t>(a.n_pages) * a.Hkv, std::min(page, kKT))) != cudaSuccess)
     return e;
-  e = cudaFuncSetAttribute(prefill_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<DP>);
+  e = cudaFuncSetAttribute(prefill_kernel<DP, APART>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<DP, APART>);
   if (e != cudaSuccess) return e;
-  prefill_kernel<DP><<<num_sms, kThreads, kSmem<DP>, st>>>(mk, mv, a, kPrefillWaitCycles);
+  prefill_kernel<DP, APART><<<num_sms, kThreads, kSmem<DP, APART>, st>>>(mk, mv, a, kPrefillWaitCycles);
   return cudaGetLastError();
 }
 
@@ -838,7 +893,11 @@ cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t st) {
 cudaError_t launch_attn_prefill_tc(const AttnArgs& a, int num_sms, cudaStream_t st) {
   cudaError_t e = encoder();
   if (e != cudaSuccess) return e;
-  return a.D <= 64 ? launch<64>(a, num_sms, st) : launch<128>(a, num_sms, st);
+  if (a.D > 64) return launch<128, false>(a, num_sms, st);
+  // P beside S pays where most tiles need no mask (4,096 tokens at 32K, 16 heads
+  // of 64: 554 -> 500 us), not in a window's few tiles (ragged prompts, window
+  // 1,024: 92 -> 100 us)
+  return a.window > 0 ? launch<64, false>(a, num_sms, st) : launch<64, true>(a, num_sms, st);
 }
 
 }  // namespace moe
