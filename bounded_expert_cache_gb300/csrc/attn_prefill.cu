@@ -39,14 +39,18 @@
 // run per CTA (one CTA per SM), as in the decode kernel: causal units differ in
 // length, and whole units would leave SMs idle in the last wave. A unit counts
 // kUnitCost tiles more than it has, for its Q and its results. A unit cut by
-// run ends leaves partial rows (m, l, O), joined by the warp that arrives last,
-// in run order.
+// run ends leaves partial rows (m, l, O), joined in run order: up to four parts
+// by the warp that arrives last, which hides behind the other CTAs' tiles (a
+// launch for it costs 7 us of 94 on the windowed ragged prompts), more by a
+// second small launch (a short chunk over a long cache has dozens: 64 tokens at
+// 20,000, 4 cache heads, take 33 us so, 52 with the last warp).
 //
 // Every wait is bounded, as in the prefill GEMMs: on a time-out all roles leave
 // their loops, copies and MMAs in flight are drained, an error is recorded.
 #include <cuda.h>
 
 #include "attn.cuh"
+#include "pdl.cuh"
 #include "prefill.h"
 #include "tc.cuh"
 
@@ -61,6 +65,7 @@ constexpr int kKT = 128;      // tokens a tile
 constexpr int kQT = 128;      // rows a row tile
 constexpr int kUnitRows = 2 * kQT;
 constexpr int kUnitCost = 3;   // tiles' worth of time of a unit's Q and results
+constexpr int kInlineParts = 4;  // parts of a unit joined without a launch
 constexpr float kRaise = 8.f;  // log2 of the growth that raises m
 
 template <int DP, bool APART>
@@ -281,6 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* const s_first = reinterpret_cast<int*>(smraw);  // before the tiles are in use
   volatile int* abort_flag = &sh.abort;
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
+
+  pdl_trigger();  // the joining launch may be scheduled; it waits for this one's end
+  if (tid == 0) a.cuts[blockIdx.x].count = 0;
 
   // ---- this CTA's run. Units are counted sequence block by sequence block;
   // a unit's length follows from its last token's position.
@@ -790,7 +798,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         const bool whole = w.whole();
-        // a partial result: slot 0 if the run starts inside the unit's tiles, else 1
+        // a partial result: slot 0 if the run starts inside the unit's tiles, else
+        // 1; (m, l, -, -) of every row, then O by column quads
         float* part = a.part + ((2 * static_cast<int64_t>(blockIdx.x) + (run0 > w.tiles0() ? 0 : 1)) * 2 + t) * C::kPart;
         if (!whole) *reinterpret_cast<float2*>(part + r * 4) = make_float2(m, l);
         const float inv = 1.f / l;  // no weight at all on what is seen: 0/0
@@ -808,8 +817,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                   make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
           }
         }
-        if (!whole) {
-          const int64_t c0 = runs.of(w.tiles0()), c1 = runs.of(w.tiles0() + w.sp.n - 1);
+        const int64_t c0 = whole ? 0 : runs.of(w.tiles0()), c1 = whole ? 0 : runs.of(w.tiles0() + w.sp.n - 1);
+        if (!whole && c1 - c0 >= kInlineParts) {
+          if (tid == 0 && run0 <= w.tiles0()) {  // the unit's first part: the record for the joining launch
+            Cut cut;
+            cut.count = static_cast<int>(c1 - c0) + 1;
+            cut.rt = w.rt;
+            cut.h = w.h;
+            cut.row0 = w.s.row0;
+            cut.m = w.s.m;
+            cut.len = w.s.len;
+            a.cuts[blockIdx.x] = cut;
+          }
+        } else if (!whole) {
           // one ticket a warp: its rows of the unit whose first tile is in c0's run
           unsigned int* ticket = a.tickets + c0 * kSoftWarps + warp;
           __threadfence();
@@ -874,6 +894,89 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
+// Join of 16 columns of one row tile of the unit whose first part is CTA
+// blockIdx.x's: the threads are 128 rows by two groups of parts (even, odd),
+// added in order. Only the first part's run starts no later than the unit's
+// tiles, so that part is in its CTA's slot 1 and the others in slot 0. Most
+// blocks find no unit to join: they are small (with four groups an empty launch
+// takes 6 us, with two 3).
+constexpr int kJoinCols = 16, kJoinGroups = 2;
+template <int DP>
+__global__ void __launch_bounds__(kQT * kJoinGroups) prefill_join_kernel(AttnArgs a) {
+  constexpr int64_t kPart = static_cast<int64_t>(kQT) * (DP + 4);
+  __shared__ float s_m[kJoinGroups][kQT];
+  __shared__ float s_o[kJoinCols + 1][kQT];  // the odd parts' columns, and their sum of weights
+  pdl_wait();
+  const Cut cut = a.cuts[blockIdx.x];
+  const int t = blockIdx.y & 1, col0 = (blockIdx.y >> 1) * kJoinCols;
+  const int r = threadIdx.x % kQT, grp = threadIdx.x / kQT;
+  const int64_t total = static_cast<int64_t>(cut.m) * a.g, rg = static_cast<int64_t>(cut.rt) * kUnitRows + t * kQT + r;
+  if (cut.count == 0 || rg - r >= total || col0 >= a.D) return;
+  const float c = a.scale_log2;
+  auto part = [&](int i) {
+    return a.part + ((2 * static_cast<int64_t>(blockIdx.x + i) + (i == 0 ? 1 : 0)) * 2 + t) * kPart;
+  };
+  float M = -INFINITY;
+#pragma unroll 8
+  for (int i = grp; i < cut.count; i += kJoinGroups) M = fmaxf(M, __ldcg(part(i) + r * 4));
+  s_m[grp][r] = M;
+  __syncthreads();
+  M = fmaxf(s_m[0][r], s_m[1][r]);
+  const float Mu = M == -INFINITY ? 0.f : M;
+  float o[kJoinCols] = {}, L = 0.f;
+#pragma unroll 6
+  for (int i = grp; i < cut.count; i += kJoinGroups) {
+    const float* p = part(i);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + r * 4));
+    const float f = ex2((ml.x - Mu) * c);
+    L += f * ml.y;
+#pragma unroll
+    for (int z = 0; z < kJoinCols / 4; ++z) {
+      const float4 u = __ldcg(reinterpret_cast<const float4*>(p + kQT * 4 + ((col0 / 4 + z) * kQT + r) * 4));
+      o[4 * z] += f * u.x;
+      o[4 * z + 1] += f * u.y;
+      o[4 * z + 2] += f * u.z;
+      o[4 * z + 3] += f * u.w;
+    }
+  }
+  if (grp == 1) {
+#pragma unroll
+    for (int x = 0; x < kJoinCols; ++x) s_o[x][r] = o[x];
+    s_o[kJoinCols][r] = L;
+  }
+  __syncthreads();
+  if (grp == 1 || rg >= total) return;
+#pragma unroll
+  for (int x = 0; x < kJoinCols; ++x) o[x] += s_o[x][r];
+  L += s_o[kJoinCols][r];
+  const int i = static_cast<int>(quotient(rg, a.g)), hq = cut.h * a.g + static_cast<int>(rg - static_cast<int64_t>(i) * a.g);
+  const bool seen = cut.len - cut.m + i >= 0;
+  const float inv = 1.f / L;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (static_cast<int64_t>(cut.row0) + i) * a.ldo +
+                       static_cast<int64_t>(hq) * a.D + col0;
+#pragma unroll
+  for (int x = 0; x < kJoinCols; x += 8) {
+    if (col0 + x >= a.D) continue;
+    uint32_t v[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      v[y] = pack_bf16(seen ? o[x + 2 * y] * inv : 0.f, seen ? o[x + 2 * y + 1] * inv : 0.f);
+    *reinterpret_cast<uint4*>(out + x) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// Whether a unit could have more than kInlineParts parts, from what the host
+// knows: a unit's most tiles, against the least length of a run (every unit is
+// a tile and its fixed cost at least).
+bool may_need_join(const AttnArgs& a, int num_sms) {
+  int64_t tokens = static_cast<int64_t>(a.max_pages) << a.page_shift;
+  if (a.window > 0) tokens = std::min<int64_t>(tokens, static_cast<int64_t>(a.window) + kUnitRows / a.g + 1 + kKT + a.sinks + kKT);
+  const int64_t tiles = tokens / kKT + 1;
+  const int64_t units = (static_cast<int64_t>(a.n_rows) * a.g + kUnitRows - 1) / kUnitRows * a.Hkv;
+  const int64_t run = std::max<int64_t>(1, units * (1 + kUnitCost) / num_sms);
+  return std::min(tiles, (tiles + run - 1) / run + 1) > kInlineParts;
+}
+
 template <int DP, bool APART>
 cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t st) {
   CUtensorMap mk, mv;
@@ -885,7 +988,9 @@ cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t st) {
   e = cudaFuncSetAttribute(prefill_kernel<DP, APART>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<DP, APART>);
   if (e != cudaSuccess) return e;
   prefill_kernel<DP, APART><<<num_sms, kThreads, kSmem<DP, APART>, st>>>(mk, mv, a, kPrefillWaitCycles);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (!may_need_join(a, num_sms)) return cudaSuccess;
+  return pdl_launch(prefill_join_kernel<DP>, dim3(num_sms, 2 * DP / kJoinCols), dim3(kQT * kJoinGroups), 0, st, a);
 }
 
 }  // namespace

@@ -15,7 +15,7 @@ enum : uint32_t {
   KV_DEVERR_SHARED = 32u,  // write to a shared page or past the length
 };
 
-// Head of a cache's scratch, before its page lists, tickets and partials.
+// Head of a cache's scratch, before its page lists and partial results.
 struct KvWork {
   uint32_t err;       // error word
   int32_t n_copies;   // page copies planned by reserve or compact
@@ -35,8 +35,8 @@ struct KvLayout {
 constexpr int kMaxList = 8192;  // most sequences of one page call
 KvLayout kv_layout(const moe_kv_t& kv, int num_sms);
 
-// A unit that several CTAs of moe_attn_decode hold parts of, recorded by the
-// first of them: the parts are in CTAs c .. c + count - 1.
+// A unit that several CTAs of an attention launch hold parts of, recorded by
+// the first of them: the parts are in CTAs c .. c + count - 1.
 struct Cut {
   int32_t count, rt, h, row0, m, len;
 };
@@ -56,8 +56,8 @@ struct AttnArgs {
   float scale_log2;     // scale * log2(e)
   int32_t window, sinks;
   float* part;          // partial results
-  unsigned int* tickets;  // prefill: arrivals at a cut unit
-  Cut* cuts;              // decode: [CTAs]
+  unsigned int* tickets;  // prefill: arrivals at a cut unit, zero between launches
+  Cut* cuts;              // [CTAs]
   uint32_t* err;
   int32_t row_tiles;    // row tiles a sequence and cache head (decode)
 };
