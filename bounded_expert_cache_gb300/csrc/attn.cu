@@ -49,20 +49,20 @@ __device__ __forceinline__ void sync_compute() { asm volatile("bar.sync 1, 256;"
 __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
   tma4d(dst, m, bar, x, y, 0, z);
 }
+// Reads of shared memory: volatile keeps them behind the waits for the data;
+// without a memory clobber other work may move across them.
 __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
+               : "r"(a));
 }
 __device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
+               : "r"(a));
 }
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -345,18 +345,24 @@ struct MmaEngine {
     const int lane = threadIdx.x & 31;
     const int j0 = c.sp.tile(c.t) * KT + key0;
     bool bad = false;
-#pragma unroll 4
-    for (int i = lane; i < 16 * NB * 8; i += 32) {
-      const int r = (i >> 3) & 15, j = j0 + r;
-      const uint32_t at = vt.row<NB>(key0 + r) + (i >> 7) * vt.block() + ((i & 7) << 4);
-      if (j >= c.sp.end || (j >= a.sinks && j < c.sp.low)) {
-        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
-      } else {
-        uint32_t w[4];
+#pragma unroll
+    for (int x = 0; x < NB; ++x) {  // a column block: four pieces a lane
+      uint32_t at[4], w[4][4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int r = y * 4 + (lane >> 3);
+        at[y] = vt.row<NB>(key0 + r) + x * vt.block() + ((lane & 7) << 4);
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(at));
-        bad |= nonfinite2(w[0]) || nonfinite2(w[1]) || nonfinite2(w[2]) || nonfinite2(w[3]);
+                     : "=r"(w[y][0]), "=r"(w[y][1]), "=r"(w[y][2]), "=r"(w[y][3])
+                     : "r"(at[y]));
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int j = j0 + y * 4 + (lane >> 3);
+        if (j >= c.sp.end || (j >= a.sinks && j < c.sp.low))
+          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at[y]), "r"(0) : "memory");
+        else
+          bad |= nonfinite2(w[y][0]) || nonfinite2(w[y][1]) || nonfinite2(w[y][2]) || nonfinite2(w[y][3]);
       }
     }
     return __any_sync(~0u, bad);
@@ -504,8 +510,7 @@ struct FmaEngine {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
     return v;
   }
   // position of row rr of the tile, -1 past the last row
@@ -525,8 +530,9 @@ struct FmaEngine {
       const int tok = warp * TPW + lane % TPW, part = lane / TPW;
       const uint32_t at = kt.row<NB>(tok);
       float acc[kRows] = {};
-#pragma unroll 4
-      for (int i = 0; i < kC4 / kParts; ++i) {
+      const int steps = (a.D + 4 * kParts - 1) / (4 * kParts);  // columns past the head are zeros
+#pragma unroll 2
+      for (int i = 0; i < steps; ++i) {
         const int d4 = part + i * kParts;
         const float4 k = lds4(at + (d4 >> 3) * kt.block() + (((d4 & 7) ^ (tok & 7)) << 4));
 #pragma unroll
