@@ -465,13 +465,13 @@ struct FmaEngine {
   static constexpr int kUnitCost = 3;               // as the bf16 engine's
   static constexpr uint32_t kTileBytes = KT * DP * 4;
   static constexpr int kC4 = DP / 4;                // column quads
-  static constexpr int TPW = KT / kWarps;           // tokens a warp (scores)
-  static constexpr int kParts = 32 / TPW;
+  static constexpr int kTok4 = KT / 4;              // threads along the tokens (scores)
+  static constexpr int P = kCompute / (kTok4 * (kRows / 4));  // parts of the head
   static constexpr int TG = kCompute / kC4;         // token groups (values)
   static constexpr int kSum = TG * 4 * DP;          // floats of the groups' results of 4 rows
   static constexpr int kSP = kRows + 4;             // pitch of a token's numerators
   static constexpr int kMergeBytes = (kSum + kRows * DP + kRows * KT + KT * kSP + kRows) * 4;
-  static_assert(kC4 % kParts == 0 && KT % TG == 0, "work of a thread");
+  static_assert(P >= 4 && P <= 32 && KT % TG == 0, "work of a thread");
 
   float4 o[kRows];
   float m[2], l[2];  // of this warp's rows: warp, and warp + 8
@@ -527,25 +527,49 @@ struct FmaEngine {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile0 = c.sp.tile(c.t) * KT;
     {
-      const int tok = warp * TPW + lane % TPW, part = lane / TPW;
-      const uint32_t at = kt.row<NB>(tok);
-      float acc[kRows] = {};
-      const int steps = (a.D + 4 * kParts - 1) / (4 * kParts);  // columns past the head are zeros
-#pragma unroll 2
-      for (int i = 0; i < steps; ++i) {
-        const int d4 = part + i * kParts;
-        const float4 k = lds4(at + (d4 >> 3) * kt.block() + (((d4 & 7) ^ (tok & 7)) << 4));
+      const int part = threadIdx.x % P, rest = threadIdx.x / P, rg = rest / kTok4, tg = rest % kTok4;
+      // neighbouring token threads four rows apart: eight lanes of a read then
+      // meet eight different banks (P = 4), whatever the swizzle
+      const int t0 = kTok4 >= 8 ? (tg & ~7) | ((tg & 1) << 2) | ((tg & 7) >> 1) : tg;
+      uint32_t at[4];
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          const float4 q = *reinterpret_cast<const float4*>(qs + r * DP + d4 * 4);
-          acc[r] += q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+      for (int i = 0; i < 4; ++i) at[i] = kt.row<NB>(t0 + kTok4 * i);
+      const float* q0 = qs + rg * 4 * DP;
+      float acc[16] = {};
+      for (int d4 = part; d4 * 4 < a.D; d4 += P) {  // columns past the head are zeros
+        float4 k[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          k[i] = lds4(at[i] + (d4 >> 3) * kt.block() + (((d4 & 7) ^ ((t0 + kTok4 * i) & 7)) << 4));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float4 q = *reinterpret_cast<const float4*>(q0 + r * DP + d4 * 4);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[r * 4 + i] += q.x * k[i].x + q.y * k[i].y + q.z * k[i].z + q.w * k[i].w;
+        }
+      }
+      int first = 0, n = 16;  // of the 16 sums, this lane keeps [first, first + n)
+#pragma unroll
+      for (int x = 1; x < P; x <<= 1) {
+        const bool up = part & x;
+        if (n > 1) {
+          n /= 2;
+          if (up) first += n;
+#pragma unroll
+          for (int v = 0; v < 8; ++v) {
+            if (v >= n) break;
+            const float keep = up ? acc[v + n] : acc[v], give = up ? acc[v] : acc[v + n];
+            acc[v] = keep + __shfl_xor_sync(~0u, give, x);
+          }
+        } else {
+          acc[0] += __shfl_xor_sync(~0u, acc[0], x);
         }
       }
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-#pragma unroll
-        for (int x = TPW; x < 32; x <<= 1) acc[r] += __shfl_xor_sync(~0u, acc[r], x);
-        if (r % kParts == part) ss[r * KT + tok] = acc[r];
+      for (int v = 0; v < 16 / (P < 16 ? P : 16); ++v) {
+        const int e = first + v;
+        ss[(rg * 4 + (e >> 2)) * KT + t0 + kTok4 * (e & 3)] = acc[v];
       }
     }
     const int lo_pos = pos_of(a, c, 0);
