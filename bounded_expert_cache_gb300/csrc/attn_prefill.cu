@@ -41,9 +41,9 @@
 // kUnitCost tiles more than it has, for its Q and its results. A unit cut by
 // run ends leaves partial rows (m, l, O), joined in run order: up to four parts
 // by the warp that arrives last, which hides behind the other CTAs' tiles (a
-// launch for it costs 7 us of 94 on the windowed ragged prompts), more by a
+// launch for it costs 7 us of 88 on the windowed ragged prompts), more by a
 // second small launch (a short chunk over a long cache has dozens: 64 tokens at
-// 20,000, 4 cache heads, take 33 us so, 52 with the last warp).
+// 20,000, 4 cache heads, take 31 us so, 52 with the last warp).
 //
 // Every wait is bounded, as in the prefill GEMMs: on a time-out all roles leave
 // their loops, copies and MMAs in flight are drained, an error is recorded.
@@ -310,9 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     *total = all;
     return base + x - v;
   };
-  // visit(b, rt, span length, line position) for every unit row, in parallel
+  // visit(b, rt, span length, line position) for every unit row, in parallel;
+  // strips: rounds it took
+  int strips = 0;
   auto visit_units = [&](auto&& f) -> int64_t {
     int64_t line = 0;
+    strips = 0;
     for (int b0 = 0; b0 < a.n; b0 += kThreads) {
       const int b = b0 + tid;
       int64_t units;
@@ -340,19 +343,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t at = line + scan(u < units ? static_cast<int64_t>(n + kUnitCost) * a.Hkv : 0, &all);
         if (n > 0) f(sb, rt, n, at);
         line += all;
+        ++strips;
       }
       __syncthreads();
     }
     return line;
   };
-  const int64_t total = visit_units([](int, int, int, int64_t) {});
+  int my_b = 0, my_rt = 0, my_n = 0;  // this thread's unit row of the last round
+  int64_t my_at = 0;
+  const int64_t total = visit_units([&](int b, int rt, int n, int64_t at) {
+    my_b = b;
+    my_rt = rt;
+    my_n = n;
+    my_at = at;
+  });
   if (total == 0) return;
   const Runs runs(total, gridDim.x);
   if (blockIdx.x >= runs.n) return;
   const int64_t run0 = runs.start(blockIdx.x), run1 = runs.start(blockIdx.x + 1);
   if (tid == 0) sh.walk.nt = 0;
   __syncthreads();
-  visit_units([&](int b, int rt, int n, int64_t at) {
+  auto start_in = [&](int b, int rt, int n, int64_t at) {  // if the run starts in this unit row
     const int64_t per = n + kUnitCost;
     if (run0 >= at && run0 < at + per * a.Hkv) {
       Walk w;
@@ -365,7 +376,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       open_unit(a, w, run0);
       sh.walk = w;
     }
-  });
+  };
+  if (strips > 1) {
+    visit_units(start_in);
+  } else {  // every unit row is still some thread's
+    if (my_n > 0) start_in(my_b, my_rt, my_n, my_at);
+    __syncthreads();
+  }
   if (sh.walk.nt <= 0) return;  // a run within a unit's fixed cost
 
   if (tid == 0) {
@@ -574,19 +591,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kPieces = DP / 8, kRowsPer = 32 / kPieces;
         const int p = lane % kPieces, rows = w.rows - t * kQT;
         const int64_t rg = static_cast<int64_t>(w.rt) * kUnitRows + t * kQT + lane / kPieces;
-        int i = static_cast<int>(quotient(rg, a.g)), hq = static_cast<int>(rg - static_cast<int64_t>(i) * a.g);
-        const __nv_bfloat16* qh = static_cast<const __nv_bfloat16*>(a.q) + static_cast<int64_t>(w.h * a.g) * a.D + p * 8;
+        const int i = static_cast<int>(quotient(rg, a.g));
+        int hq = static_cast<int>(rg - static_cast<int64_t>(i) * a.g);
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(w.s.row0) + i) * a.ldq +
+                                   static_cast<int64_t>(w.h * a.g + hq) * a.D + p * 8;
+        const int64_t step = kRowsPer * a.D, wrap = a.ldq - static_cast<int64_t>(a.g) * a.D;
+        const bool col_in = p * 8 < a.D;
+        uint32_t dst = sq + t * C::kTile + (p >> 3) * C::kHalf;
 #pragma unroll 4
         for (int r = lane / kPieces; r < kQT; r += kRowsPer) {
-          const bool in = r < rows && p * 8 < a.D;
-          const void* src = in ? qh + (static_cast<int64_t>(w.s.row0) + i) * a.ldq + hq * a.D : a.q;
-          const uint32_t dst = sq + t * C::kTile + (p >> 3) * C::kHalf + r * 128u + (((p & 7) ^ (r & 7)) << 4);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
+          const bool in = col_in && r < rows;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + r * 128u + (((p & 7) ^ (r & 7)) << 4)),
+                       "l"(in ? src : a.q), "r"(in ? 16 : 0)
                        : "memory");
+          src += step;  // the next row's head, or the next token's first ones
           hq += kRowsPer;
           while (hq >= a.g) {
             hq -= a.g;
-            ++i;
+            src += wrap;
           }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -786,15 +808,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool seen = pos >= 0;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * a.ldo + static_cast<int64_t>(hq) * a.D;
         auto store32 = [&](const float* o, float f, int x) {
+          if (!row_ok) return;
+          uint32_t v[16];
 #pragma unroll
-          for (int y = 0; y < 32; y += 8) {
-            if (!row_ok || x + y >= a.D) continue;
-            uint4 v;
-            v.x = pack_bf16(seen ? o[y] * f : 0.f, seen ? o[y + 1] * f : 0.f);
-            v.y = pack_bf16(seen ? o[y + 2] * f : 0.f, seen ? o[y + 3] * f : 0.f);
-            v.z = pack_bf16(seen ? o[y + 4] * f : 0.f, seen ? o[y + 5] * f : 0.f);
-            v.w = pack_bf16(seen ? o[y + 6] * f : 0.f, seen ? o[y + 7] * f : 0.f);
-            *reinterpret_cast<uint4*>(out + x + y) = v;
+          for (int y = 0; y < 16; ++y) v[y] = pack_bf16(seen ? o[2 * y] * f : 0.f, seen ? o[2 * y + 1] * f : 0.f);
+#pragma unroll
+          for (int y = 0; y < 16; y += 8) {
+            if (x + 2 * y >= a.D) break;
+            if (a.wide_out) {  // a sector a thread
+              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + x + 2 * y), "r"(v[y]),
+                           "r"(v[y + 1]), "r"(v[y + 2]), "r"(v[y + 3]), "r"(v[y + 4]), "r"(v[y + 5]), "r"(v[y + 6]),
+                           "r"(v[y + 7])
+                           : "memory");
+            } else {
+              *reinterpret_cast<uint4*>(out + x + 2 * y) = make_uint4(v[y], v[y + 1], v[y + 2], v[y + 3]);
+              if (x + 2 * y + 8 < a.D)
+                *reinterpret_cast<uint4*>(out + x + 2 * y + 8) = make_uint4(v[y + 4], v[y + 5], v[y + 6], v[y + 7]);
+            }
           }
         };
         const bool whole = w.whole();
@@ -843,37 +873,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto part_of = [&](int64_t x) {  // only c0's run starts before the unit's tiles
               return a.part + ((2 * x + (x == c0 ? 1 : 0)) * 2 + t) * C::kPart;
             };
-            float M = -INFINITY, L = 0.f;
-            for (int64_t x = c0; x <= c1; ++x) M = fmaxf(M, __ldcg(part_of(x) + r * 4));
-            const float Mu = M == -INFINITY ? 0.f : M;
-            for (int64_t x = c0; x <= c1; ++x) {
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_of(x) + r * 4));
-              L += ex2((ml.x - Mu) * c) * ml.y;
+            float2 ml[kInlineParts];
+#pragma unroll
+            for (int x = 0; x < kInlineParts; ++x)
+              ml[x] = c0 + x <= c1 ? __ldcg(reinterpret_cast<const float2*>(part_of(c0 + x) + r * 4)) : make_float2(-INFINITY, 0.f);
+            float M = ml[0].x, L = 0.f, wt[kInlineParts];
+#pragma unroll
+            for (int x = 1; x < kInlineParts; ++x) M = fmaxf(M, ml[x].x);
+#pragma unroll
+            for (int x = 0; x < kInlineParts; ++x) {
+              wt[x] = ex2((ml[x].x - (M == -INFINITY ? 0.f : M)) * c);
+              L += wt[x] * ml[x].y;
             }
             const float inv_l = 1.f / L;
 #pragma unroll 1
             for (int y = 0; y < DP; y += 32) {
               float o[32] = {};
-              for (int64_t x0 = c0; x0 <= c1; x0 += 2) {  // two parts' loads in flight
+#pragma unroll
+              for (int x0 = 0; x0 < kInlineParts; x0 += 2) {  // two parts' loads in flight
+                if (c0 + x0 > c1) break;
                 float4 u[2][8];
-                float f[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  const float* p = part_of(min(x0 + i, c1));
-                  f[i] = x0 + i <= c1 ? ex2((__ldcg(p + r * 4) - Mu) * c) : 0.f;
+                  const float* p = part_of(min(c0 + x0 + i, c1));  // (a part past the last weighs nothing)
 #pragma unroll
                   for (int z = 0; z < 8; ++z)
                     u[i][z] = __ldcg(reinterpret_cast<const float4*>(p + kQT * 4 + ((y / 4 + z) * kQT + r) * 4));
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  if (x0 + i > c1) break;
+                  if (c0 + x0 + i > c1) break;
 #pragma unroll
                   for (int z = 0; z < 8; ++z) {
-                    o[4 * z] += f[i] * u[i][z].x;
-                    o[4 * z + 1] += f[i] * u[i][z].y;
-                    o[4 * z + 2] += f[i] * u[i][z].z;
-                    o[4 * z + 3] += f[i] * u[i][z].w;
+                    o[4 * z] += wt[x0 + i] * u[i][z].x;
+                    o[4 * z + 1] += wt[x0 + i] * u[i][z].y;
+                    o[4 * z + 2] += wt[x0 + i] * u[i][z].z;
+                    o[4 * z + 3] += wt[x0 + i] * u[i][z].w;
                   }
                 }
               }

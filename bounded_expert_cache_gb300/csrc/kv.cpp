@@ -115,6 +115,8 @@ moe_status_t attention(const char* call, bool decode, const moe_kv_t* kv, int32_
   a.cu = decode ? nullptr : cu;
   a.ldq = ldq;
   a.ldo = ldo;
+  a.wide_out = reinterpret_cast<uintptr_t>(out) % 32 == 0 && (ldo * elem_bytes(kv->dtype)) % 32 == 0 &&
+               (kv->head_dim * elem_bytes(kv->dtype)) % 32 == 0;
   a.n = n;
   a.n_q = n_q;
   a.n_rows = rows;

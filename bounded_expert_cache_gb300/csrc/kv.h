@@ -60,6 +60,7 @@ struct AttnArgs {
   Cut* cuts;              // [CTAs]
   uint32_t* err;
   int32_t row_tiles;    // row tiles a sequence and cache head (decode)
+  bool wide_out;        // rows of out are multiples of 32 bytes, 32-byte aligned
 };
 cudaError_t launch_attn_decode(const AttnArgs& a, int32_t dtype, int num_sms, cudaStream_t st);
 cudaError_t launch_attn_prefill(const AttnArgs& a, int32_t dtype, int32_t n_rows, int num_sms, cudaStream_t st);
