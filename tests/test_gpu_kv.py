@@ -322,6 +322,26 @@ def test_attn_prefill_matches_64_bit(bec, dtype, case):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [8, 40, 120])
+@pytest.mark.parametrize("tokens", [0, 1024])
+def test_attn_prefill_many_chunks(bec, dtype, D, tokens):
+    """More chunks than a block's threads, rows of 16 but not 32 bytes; with a long one, run ends fall into it."""
+    rng = random.Random(D)
+    lens = [rng.choice([0, 0, 1, 3, 20]) for _ in range(500)]
+    ms = [min(n, rng.choice([0, 1, 20])) for n in lens]
+    lens[411], ms[411] = 1000 + tokens, 100
+    pool = Pool(bec, lens, 16, 1, D, dtype, 5)
+    q = randn((sum(ms), 3, D), dtype, gen(6))
+    cu = [0]
+    for m in ms:
+        cu.append(cu[-1] + m)
+    out = pool.kv.attn_prefill(1, q, pool.seqs, i32(cu))
+    pool.kv.check_errors()
+    check_attn(pool, q, out, lens, ms, 0, 0, D ** -0.5)
+    assert torch.equal(out, pool.kv.attn_prefill(1, q, pool.seqs, i32(cu)))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_hidden_tokens_do_not_reach_a_row(bec, dtype, D, bad):
