@@ -38,7 +38,7 @@
 // Work split: the token tiles of all units form one line, cut into one equal
 // run per CTA (one CTA per SM), as in the decode kernel: causal units differ in
 // length, and whole units would leave SMs idle in the last wave. A unit counts
-// kUnitCost tiles more than it has, for its Q and its results. A unit cut by
+// unit_cost tiles more than it has, for its Q and its results. A unit cut by
 // run ends leaves partial rows (m, l, O), joined in run order: up to four parts
 // by the warp that arrives last, which hides behind the other CTAs' tiles (a
 // launch for it costs 7 us of 88 on the windowed ragged prompts), more by a
@@ -64,7 +64,6 @@ constexpr int kSoftWarps = 8;
 constexpr int kKT = 128;      // tokens a tile
 constexpr int kQT = 128;      // rows a row tile
 constexpr int kUnitRows = 2 * kQT;
-constexpr int kUnitCost = 3;   // tiles' worth of time of a unit's Q and results
 constexpr int kInlineParts = 4;  // parts of a unit joined without a launch
 constexpr float kRaise = 8.f;  // log2 of the growth that raises m
 
@@ -82,6 +81,12 @@ struct Cfg {
   // partial rows of one row tile: (m, l, -, -), then O by column quads
   static constexpr int64_t kPart = static_cast<int64_t>(kQT) * (DP + 4);
 };
+
+// Tiles' worth of time of a unit's Q and results. Without a window units run long
+// and are cut more often, which counts as theirs (ragged prompts of up to 4,000
+// tokens, heads of 64 and 128: 167 and 230 us with 3, 154 and 214 with 5, 157 and
+// 220 with 7; in a window of 1,024 86 and 115 with 3, 90 and 119 with 5).
+__host__ __device__ __forceinline__ int unit_cost(const AttnArgs& a) { return a.window > 0 ? 3 : 5; }
 
 __device__ __forceinline__ void umma_ss(uint32_t dt, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -169,18 +174,19 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigne
 
 // A CTA's walk along the line: units (sequence, row tile, cache head) in order,
 // of each the tiles [t0, t0 + nt) that fall into the run. On the line a unit is
-// kUnitCost positions and then one per tile.
+// `cost` positions and then one per tile.
 struct Walk {
   int b, rt, h;
   int t0, nt;         // this segment
+  int cost;
   int64_t unit0;      // line position of the unit
   int64_t end;        // end of the run
   Seq s;
   Span sp;
   int rows;           // rows of the unit
   __device__ __forceinline__ bool whole() const { return nt == sp.n; }
-  __device__ __forceinline__ int64_t tiles0() const { return unit0 + kUnitCost; }
-  __device__ __forceinline__ bool more() const { return tiles0() + sp.n + kUnitCost < end; }
+  __device__ __forceinline__ int64_t tiles0() const { return unit0 + cost; }
+  __device__ __forceinline__ bool more() const { return tiles0() + sp.n + cost < end; }
 };
 // Shared memory behind the tiles.
 template <int DP, bool APART>
@@ -313,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // visit(b, rt, span length, line position) for every unit row, in parallel;
   // strips: rounds it took
   int strips = 0;
+  const int cost = unit_cost(a);
   auto visit_units = [&](auto&& f) -> int64_t {
     int64_t line = 0;
     strips = 0;
@@ -340,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           n = unit_span(a, load_seq(a, sb), rt).n;
         }
         int64_t all;
-        const int64_t at = line + scan(u < units ? static_cast<int64_t>(n + kUnitCost) * a.Hkv : 0, &all);
+        const int64_t at = line + scan(u < units ? static_cast<int64_t>(n + cost) * a.Hkv : 0, &all);
         if (n > 0) f(sb, rt, n, at);
         line += all;
         ++strips;
@@ -364,9 +371,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) sh.walk.nt = 0;
   __syncthreads();
   auto start_in = [&](int b, int rt, int n, int64_t at) {  // if the run starts in this unit row
-    const int64_t per = n + kUnitCost;
+    const int64_t per = n + cost;
     if (run0 >= at && run0 < at + per * a.Hkv) {
       Walk w;
+      w.cost = cost;
       w.b = b;
       w.rt = rt;
       w.h = static_cast<int>(quotient(run0 - at, per));
@@ -1008,7 +1016,7 @@ bool may_need_join(const AttnArgs& a, int num_sms) {
   if (a.window > 0) tokens = std::min<int64_t>(tokens, static_cast<int64_t>(a.window) + kUnitRows / a.g + 1 + kKT + a.sinks + kKT);
   const int64_t tiles = tokens / kKT + 1;
   const int64_t units = (static_cast<int64_t>(a.n_rows) * a.g + kUnitRows - 1) / kUnitRows * a.Hkv;
-  const int64_t run = std::max<int64_t>(1, units * (1 + kUnitCost) / num_sms);
+  const int64_t run = std::max<int64_t>(1, units * (1 + unit_cost(a)) / num_sms);
   return std::min(tiles, (tiles + run - 1) / run + 1) > kInlineParts;
 }
 
