@@ -3,9 +3,10 @@
 //
 // The integer work (page counts, lowest free pages, moves) runs in one cluster
 // of 8 CTAs (one CTA is slower even for a pool of 260 pages and 36 sequences:
-// fork 6.1 against 5.5 us, reserve 11.6 against 10.7, cold): every phase reads a consistent state, a cluster barrier separates
-// it from the phase that changes that state, and nothing returns to the host,
-// so a decode step that grows its sequences stays capturable in a CUDA graph.
+// fork 6.1 against 5.5 us, reserve 11.6 against 10.7, cold): every phase reads a
+// consistent state, a cluster barrier separates it from the phase that changes
+// that state, and nothing returns to the host, so a decode step that grows its
+// sequences stays capturable in a CUDA graph.
 // A call first checks its whole list in every CTA of the cluster (the same
 // reads, so the same verdict) and then changes either everything or nothing.
 //
@@ -13,7 +14,9 @@
 // the lowest free page first, in list order.
 //
 // What bounds it: the small calls are latency (a few dependent reads and two
-// or three cluster barriers); the copies are HBM.
+// or three cluster barriers); the copies are HBM: a fragmented pool of 3,000
+// pages (64 tokens, 2 heads of 128, 10 layers, 48 sequences) is brought together
+// in 162 us, 973 MB read and written at 6.0 TB/s.
 #include <cooperative_groups.h>
 
 #include "kv.h"

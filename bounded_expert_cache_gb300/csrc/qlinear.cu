@@ -6,9 +6,14 @@
 // What bounds it: HBM, the 4.5 bits a weight, as long as a weight costs less
 // than about three instructions of a thread. The inner sums therefore run on
 // warp-level matrix instructions (m16n8k16, weights as A, tokens as B): codes
-// become bf16 integers by a mask and a subtraction for two of them, products of a 4-bit integer and a bf16 are exact, sums are fp32, and the
-// group's factor is applied in fp32 to the 16 x 8 sums. An fp32 x is the exact
-// sum of three bf16 (8 + 8 + 8 significand bits), one instruction each.
+// become bf16 integers by a mask and a subtraction for two of them, products of
+// a 4-bit integer and a bf16 are exact, sums are fp32, and the group's factor is
+// applied in fp32 to the 16 x 8 sums. An fp32 x is the exact sum of three bf16
+// (8 + 8 + 8 significand bits), one instruction each. Measured, 131,072 x 2,048
+// Q4_0 (151 MB, 22 us of HBM): 38 us for one token, 61 for 24, where the warps
+// issue in 55% of cycles, the tensor pipe works in 38% and shared memory in 52%;
+// 2,560 x 2,048 for one token: 3.6 us, the latency of a launch and of a few
+// dependent loads.
 //
 // The order of k within an instruction is free as long as A and B agree, so x
 // is stored in the order in which a lane's 4-byte word yields its eight codes:
