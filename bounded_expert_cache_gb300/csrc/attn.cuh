@@ -31,12 +31,15 @@ struct Seq {
 };
 
 // Query rows of chunk b; 0 (with an error recorded) if cu leaves the rows given.
+// Chunks that do not cover all rows are an error too: the host counts on every
+// row's work when it decides how partial results meet.
 __device__ __forceinline__ int chunk_rows(const AttnArgs& a, int b) {
   const int r0 = __ldg(a.cu + b), r1 = __ldg(a.cu + b + 1);
   if (r0 < 0 || r1 < r0 || r1 > a.n_rows) {
     atomicOr(a.err, MOE_DEVERR_BADIDX);
     return 0;
   }
+  if ((b == 0 && r0 != 0) || (b == a.n - 1 && r1 != a.n_rows)) atomicOr(a.err, MOE_DEVERR_BADIDX);
   return r1 - r0;
 }
 

@@ -84,9 +84,9 @@ moe_status_t moe_kv_reserve(const moe_kv_t* kv, const int32_t* seqs, const int32
  * rows cu[i] .. cu[i+1]-1 of k_new and v_new as its last cu[i+1]-cu[i] tokens.
  * k_new, v_new: device [n_rows][n_kv_heads][head_dim] of the cache's dtype,
  * rows ldk and ldv elements apart (a slice of a fused projection), rows
- * 16-byte aligned; cu: device int32 [n+1], cu[n] = n_rows. A chunk longer than
- * its sequence and a token whose page is shared are not written (an error is
- * recorded). */
+ * 16-byte aligned; cu: device int32 [n+1]; rows outside cu[0] .. cu[n]-1 belong
+ * to no sequence and are ignored. A chunk longer than its sequence and a token
+ * whose page is shared are not written (an error is recorded). */
 moe_status_t moe_kv_write(const moe_kv_t* kv, int32_t layer, const void* k_new, int64_t ldk, const void* v_new,
                           int64_t ldv, const int32_t* seqs, const int32_t* cu, int32_t n, int32_t n_rows,
                           moe_stream_t stream);
@@ -123,10 +123,12 @@ moe_status_t moe_kv_copy_pages(const moe_kv_t* kv, const int32_t* src, const int
  * joined, so a few long sequences use the whole GPU.
  *
  * moe_attn_prefill: chunks of any length; rows cu[i] .. cu[i+1]-1 (device
- * int32 [n+1], cu[n] = n_rows) are the newest tokens of seqs[i].
+ * int32 [n+1], cu[0] = 0, cu[n] = n_rows; anything else is recorded as an
+ * error) are the newest tokens of seqs[i]. Rows without a sequence belong to an
+ * empty one, and are 0.
  *
- * scale must be positive. seqs may be NULL: sequences 0 .. n-1. n_heads must be a multiple of
- * n_kv_heads, at most 64 times as many. */
+ * scale must be positive. seqs may be NULL: sequences 0 .. n-1. n_heads must
+ * be a multiple of n_kv_heads, at most 64 times as many. */
 moe_status_t moe_attn_decode(const moe_kv_t* kv, int32_t layer, const void* q, int64_t ldq, const int32_t* seqs,
                              int32_t n, int32_t n_q, int32_t n_heads, float scale, int32_t window, int32_t sinks,
                              void* out, int64_t ldo, moe_stream_t stream);

@@ -341,6 +341,22 @@ def test_attn_prefill_many_chunks(bec, dtype, D, tokens):
     assert torch.equal(out, pool.kv.attn_prefill(1, q, pool.seqs, i32(cu)))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_prefill_long_context_beside_rows_before_their_sequence(bec, D):
+    """Rows without a token take no part in the work: the others' units are cut into many parts all the same."""
+    lens, ms = [20000, 0], [64, 20000]
+    pool = Pool(bec, lens, 64, 2, D, BF16, 12)
+    q = randn((sum(ms), 32, D), BF16, gen(13))
+    out = torch.full_like(q, 7.0)
+    pool.kv.attn_prefill(1, q, pool.seqs, i32([0, 64, 20064]), out=out)
+    pool.kv.check_errors()
+    check_attn(pool, q[:64], out[:64], lens[:1], ms[:1], 0, 0, D ** -0.5)
+    assert (out[64:] == 0).all()
+    # the scratch is as it was: the next call's parts meet as well
+    again = pool.kv.attn_prefill(1, q[:64].contiguous(), pool.seqs[:1].contiguous(), i32([0, 64]))
+    check_attn(pool, q[:64], again, lens[:1], ms[:1], 0, 0, D ** -0.5)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
@@ -450,6 +466,19 @@ def test_attention_refusals(bec):
     assert kv.attn_prefill(1, q[:0], pool.seqs, i32([0, 0, 0])).shape == (0, 4, 64)
     assert kv.attn_decode(1, q[:0], i32([])).shape == (0, 4, 64)
     kv.check_errors()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cu", [[0, 2, 5], [1, 3, 6], [0, 6, 6]])
+def test_attn_prefill_chunks_cover_all_rows(bec, dtype, cu):
+    pool = Pool(bec, [40, 9], 16, 2, 64, dtype, 6)
+    q = randn((6, 4, 64), dtype, gen(2))
+    pool.kv.attn_prefill(1, q, pool.seqs, i32(cu))
+    if cu == [0, 6, 6]:
+        pool.kv.check_errors()
+    else:
+        with pytest.raises(bec.MoeError, match="MOE_ERR_ARG"):
+            pool.kv.check_errors()
 
 
 # ---------------------------------------------------------------- pages
