@@ -10,9 +10,9 @@
 // a 4-bit integer and a bf16 are exact, sums are fp32, and the group's factor is
 // applied in fp32 to the 16 x 8 sums. An fp32 x is the exact sum of three bf16
 // (8 + 8 + 8 significand bits), one instruction each. Measured, 131,072 x 2,048
-// Q4_0 (151 MB, 22 us of HBM): 38 us for one token, 61 for 24, where the warps
-// issue in 55% of cycles, the tensor pipe works in 38% and shared memory in 52%;
-// 2,560 x 2,048 for one token: 3.6 us, the latency of a launch and of a few
+// Q4_0 (151 MB, 22 us of HBM): 37 us for one token, 57 for 24, where the warps
+// issue in 55% of cycles, the tensor pipe works in 40% and shared memory in 52%;
+// 2,560 x 2,048 for one token: 3.5 us, the latency of a launch and of a few
 // dependent loads.
 //
 // The order of k within an instruction is free as long as A and B agree, so x
@@ -72,10 +72,12 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
+// Four blocks of 8 rows x 16 bytes, one row address a lane: a lane gets word
+// lane % 4 of row lane / 4 of each.
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -302,7 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
 #pragma unroll
   for (int n = 0; n < NT; ++n) xt[n] = xs + min(n * 8 + r, tok - 1) * p.x_pitch + c * 16;
   constexpr uint32_t kBias = QUANT == MOE_Q4_0 ? 0x43084308u : 0x43004300u;  // 136, 128
-  const uint32_t q_off = r * 128 + c * 4, m_off = kCodeBytes + r * 16;
+  // ldmatrix: lanes 0-7 and 8-15 address rows 0-7 and 8-15 of a group's piece, lanes 16-31 the next group's
+  const uint32_t q_off = (lane & 15) * 128, q_phase = ((lane & 7) ^ (lane >> 4)) << 4, m_off = kCodeBytes + r * 16;
 
   auto store = [&](int n, int t, float v) {
     if (a.bias) v += __ldg(a.bias + n);
@@ -334,22 +337,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
     const int k0 = stage * stage_k - have * p.kx + wk * kWK;  // within the slice
     const uint32_t st = ring + slot * kWarpStage, xk = k0 * 2;
     static_assert(kWarpStage % 128 == 0, "a slot's rows start at multiples of 128, so a piece's offset can be XORed in");
-    const uint32_t q0 = (st + q_off) ^ (static_cast<uint32_t>(r & 7) << 4);
+    const uint32_t q0 = (st + q_off) ^ q_phase;
     const uint4 m0 = lds128(st + m_off), m1 = lds128(st + m_off + 128);
     const uint32_t ma[4] = {m0.x, m0.y, m0.z, m0.w}, mb[4] = {m1.x, m1.y, m1.z, m1.w};
     const int left = a.K - (stage * stage_k + wk * kWK);  // k of this warp's stage; may be negative
 #pragma unroll
     for (int g2 = 0; g2 < 4; ++g2) {  // 64 k: two groups of Q4_0, one of I4_G64
       if (g2 * 64 >= left) break;
+      uint32_t w[4];  // rows r and r + 8 of group 2 g2, then of the next
+      ldsm4(w, q0 ^ (static_cast<uint32_t>(g2) << 5));
       float s[2][NT][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int g = 2 * g2 + h;
         uint32_t wa[4], wb[4];
-        // the piece of group g; rows r and r + 8 have one phase
-        const uint32_t at = q0 ^ (static_cast<uint32_t>(g) << 4);
-        codes(lds32(at), p.one, kBias, wa);
-        codes(lds32(at + 8 * 128), p.one, kBias, wb);
+        codes(w[2 * h], p.one, kBias, wa);
+        codes(w[2 * h + 1], p.one, kBias, wb);
         const uint32_t f0[4] = {wa[0], wb[0], wa[1], wb[1]}, f1[4] = {wa[2], wb[2], wa[3], wb[3]};
         float(*d)[4] = s[QUANT == MOE_Q4_0 ? h : 0];
 #pragma unroll
