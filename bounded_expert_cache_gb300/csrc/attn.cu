@@ -768,6 +768,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (SPLIT) {
     pdl_trigger();  // the joining launch may be scheduled; it waits for this one's end
     if (threadIdx.x == 0) a.cuts[blockIdx.x].count = 0;
+  } else if (blockIdx.x == 0 && threadIdx.x == kThreads - 1) {
+    check_chunks(a);
   }
   float* merge = reinterpret_cast<float*>(sm + NS * E::kTileBytes);
   const int rt_n = a.row_tiles;

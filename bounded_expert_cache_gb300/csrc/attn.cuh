@@ -31,16 +31,18 @@ struct Seq {
 };
 
 // Query rows of chunk b; 0 (with an error recorded) if cu leaves the rows given.
-// Chunks that do not cover all rows are an error too: the host counts on every
-// row's work when it decides how partial results meet.
 __device__ __forceinline__ int chunk_rows(const AttnArgs& a, int b) {
   const int r0 = __ldg(a.cu + b), r1 = __ldg(a.cu + b + 1);
   if (r0 < 0 || r1 < r0 || r1 > a.n_rows) {
     atomicOr(a.err, MOE_DEVERR_BADIDX);
     return 0;
   }
-  if ((b == 0 && r0 != 0) || (b == a.n - 1 && r1 != a.n_rows)) atomicOr(a.err, MOE_DEVERR_BADIDX);
   return r1 - r0;
+}
+// Chunks that do not cover all rows are an error: the host counts on every
+// row's work when it decides how partial results meet. One thread of the grid.
+__device__ __forceinline__ void check_chunks(const AttnArgs& a) {
+  if (__ldg(a.cu) != 0 || __ldg(a.cu + a.n) != a.n_rows) atomicOr(a.err, MOE_DEVERR_BADIDX);
 }
 
 __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {

@@ -295,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   pdl_trigger();  // the joining launch may be scheduled; it waits for this one's end
   if (tid == 0) a.cuts[blockIdx.x].count = 0;
+  if (blockIdx.x == 0 && tid == kThreads - 1) check_chunks(a);
 
   // ---- this CTA's run. Units are counted sequence block by sequence block;
   // a unit's length follows from its last token's position.

@@ -11,7 +11,7 @@
 // applied in fp32 to the 16 x 8 sums. An fp32 x is the exact sum of three bf16
 // (8 + 8 + 8 significand bits), one instruction each. Measured, 131,072 x 2,048
 // Q4_0 (151 MB, 22 us of HBM): 37 us for one token, 57 for 24, where the warps
-// issue in 55% of cycles, the tensor pipe works in 40% and shared memory in 52%;
+// issue in 56% of cycles, the tensor pipe works in 40% and shared memory in 56%;
 // 2,560 x 2,048 for one token: 3.5 us, the latency of a launch and of a few
 // dependent loads.
 //
