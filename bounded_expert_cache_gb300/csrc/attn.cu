@@ -138,9 +138,10 @@ struct MmaEngine {
   static constexpr int DP = DP_, RG = RG_, KT = KT_;
   static constexpr int KG = kWarps / RG, kRows = RG * 16, KC = KT / KG / 16;
   static constexpr int NB = DP / 64;  // column blocks
-  // A unit's Q, edge tile and results take 12,000 cycles at DP 256 and 6,000
-  // below, a tile of 64 KB of K and V 2,800 at the HBM rate.
-  static constexpr int kUnitCost = DP > 128 ? 4 : 2;
+  // Tiles' worth of time of a unit's Q, edge tile, merge of the warps and results
+  // (40 contexts of 0 to 32,768 tokens, 4 new ones, heads of 256: 75 us with 4,
+  // 68 with 5, 62.6 with 6, 63.4 with 8; of 128: 47.7 with 2, 42 with 3 and 4).
+  static constexpr int kUnitCost = DP > 128 ? 6 : 3;
   static constexpr uint32_t kTileBytes = KT * DP * 2;
   // Q of large heads stays in shared memory: its fragments would not fit
   // beside the results' in registers
