@@ -30,7 +30,7 @@
 // loops run to their end on whatever is there, so no barrier is left waiting.
 // Measured, bf16: three contexts of 131,072 to 262,143 tokens, 8 heads of 128:
 // 353 us, 6.9 TB/s; 40 contexts of 40 to 32,768 tokens, 4 new tokens, 2 heads of
-// 256: 77 us, 3.8 TB/s (the fixed costs of 80 units); one of 777: 9 us, the
+// 256: 63 us, 4.6 TB/s (the fixed costs of 78 units); one of 777: 9 us, the
 // latency of the dependent loads and of the second launch.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -468,7 +468,10 @@ struct FmaEngine {
   using T = float;
   static constexpr int DP = DP_, kRows = R_, KT = DP == 256 ? 32 : 64;
   static constexpr int NB = DP / 32;                // column blocks
-  static constexpr int kUnitCost = 3;               // as the bf16 engine's
+  // as the bf16 engine's (9 contexts in a window of 1,024, heads of 96: 13.2 us
+  // with 1, 12.9 with 2, 14.4 with 3; 16 to 29,004 tokens, 4 new ones, heads of
+  // 256: 261 with 2, 238 with 3 and 4)
+  static constexpr int kUnitCost = DP > 128 ? 3 : 2;
   static constexpr uint32_t kTileBytes = KT * DP * 4;
   static constexpr int kC4 = DP / 4;                // column quads
   static constexpr int kTok4 = KT / 4;              // threads along the tokens (scores)
