@@ -32,8 +32,8 @@
 // formed) and check V.
 // The V check: a token that only some rows see must not reach the others, but
 // 0 * NaN is NaN in a matrix product. In tiles with such tokens the warps zero
-// the tokens that no row sees, and look for infinities and NaN among the
-// rest; if there is one, the unit's rows are formed again one by one.
+// the tokens that no row sees, and infinities and NaN among the rest; if there
+// was one, the rows that see it add numerator times value when the unit ends.
 //
 // Work split: the token tiles of all units form one line, cut into one equal
 // run per CTA (one CTA per SM), as in the decode kernel: causal units differ in
@@ -200,7 +200,7 @@ struct Shared {
   uint64_t qr[2], qe[2], sr[2], sc[2], pa[2], pb[2], pv[2], of[2], drain;
   int64_t scan[kThreads / 32];
   Walk walk;
-  uint32_t poison[8];  // ring over units: number + 1 of a unit with an infinity or NaN to hide
+  uint32_t poison[8];  // ring over units: number + 1 of a unit with infinities or NaN taken out of V
   uint32_t tmem;
   int abort;
 };
@@ -240,39 +240,83 @@ __device__ __forceinline__ void next_segment(const AttnArgs& a, Walk& w) {
   open_unit(a, w, w.unit0);
 }
 
-// Scores and values of the segment formed again, token by token, for the 32
-// columns from d0: what the matrix product must not be used for.
-__device__ __noinline__ void row_by_row(const AttnArgs& a, const Walk& w, const __nv_bfloat16* q, int pos, int d0,
-                                        float* acc, float* ml) {
-  float m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+// Some rows of the unit see all or part of this tile's tokens and others do not.
+// (Tiles of first tokens only are seen by every row after them.)
+__device__ __forceinline__ bool mixed_tile(const AttnArgs& a, int tile0, int lo_pos, int hi_pos) {
+  return tile0 + kKT - 1 > lo_pos || (a.window > 0 && hi_pos - tile0 >= a.window && tile0 + kKT > a.sinks);
+}
+// Position of the unit's first row; the last one's is sp.end - 1.
+__device__ __forceinline__ int first_pos(const AttnArgs& a, const Walk& w) {
+  return w.s.len - w.s.m + static_cast<int>(quotient(static_cast<int64_t>(w.rt) * kUnitRows, a.g));
+}
+
+// The infinities and NaN among the values of mixed tiles, which the matrix
+// product has taken as zeros: numerator times value, added for the 32 columns
+// from d0 of a row that sees them. m: the maximum that the row's numerators were
+// formed with. A unit has about ten mixed tiles at most, whatever the context
+// (1,024 tokens of 200,000, 16 heads of 128: 1.03 ms, with one NaN among the last
+// 500 values 1.65, with NaN in all of the chunk's 7.6).
+__device__ __noinline__ void add_nonfinite(const AttnArgs& a, const Walk& w, const __nv_bfloat16* q, int pos, float m,
+                                           int d0, float* acc) {
+  const float mc = m == -INFINITY ? 0.f : m * a.scale_log2;
+  const int lo_pos = first_pos(a, w);
   const int32_t* row = a.table + static_cast<int64_t>(w.s.id) * a.max_pages;
   for (int t = w.t0; t < w.t0 + w.nt; ++t) {
     const int tile0 = w.sp.tile(t) * kKT;
+    if (!mixed_tile(a, tile0, lo_pos, w.sp.end - 1)) continue;
     for (int j = tile0; j < tile0 + kKT; ++j) {
       const int back = pos - j;
-      if (!q || back < 0 || (a.window > 0 && back >= a.window && j >= a.sinks)) continue;
+      if (back < 0 || (a.window > 0 && back >= a.window && j >= a.sinks)) continue;
       const int p = __ldg(row + (j >> a.page_shift));
       if (p < 0 || p >= a.n_pages) continue;
       const int64_t tok =
           ((((static_cast<int64_t>(p) * a.Hkv + w.h) << a.page_shift) + (j & ((1 << a.page_shift) - 1)))) * a.D;
-      const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + tok;
       const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + tok;
-      float s = 0.f;
-      for (int d = 0; d < a.D; ++d) s += __bfloat162float(q[d]) * __bfloat162float(k[d]);
-      s *= a.scale_log2;
-      const float mn = fmaxf(m, s), mu = mn == -INFINITY ? 0.f : mn;
-      const float f = ex2(m - mu), e = ex2(s - mu);
-      m = mn;
-      l = l * f + e;
+      bool bad = false;
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (d0 + i < a.D) acc[i] = acc[i] * f + e * __bfloat162float(v[d0 + i]);
+      for (int i = 0; i < 32; i += 8) {
+        if (d0 + i >= a.D) break;
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(v + d0 + i));
+        bad |= nonfinite2(u.x) || nonfinite2(u.y) || nonfinite2(u.z) || nonfinite2(u.w);
+      }
+      if (!bad) continue;
+      const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + tok;
+      float s = 0.f;
+      for (int d = 0; d < a.D; d += 8) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(q + d)), y = __ldg(reinterpret_cast<const uint4*>(k + d));
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          s += __uint_as_float(xs[i] << 16) * __uint_as_float(ys[i] << 16) +
+               __uint_as_float(xs[i] & 0xFFFF0000u) * __uint_as_float(ys[i] & 0xFFFF0000u);
+      }
+      const float e = ex2(s * a.scale_log2 - mc);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (d0 + i >= a.D) break;
+        const float x = __bfloat162float(v[d0 + i]);
+        if (!isfinite(x)) acc[i] += e * x;
+      }
     }
   }
-  ml[0] = m;
-  ml[1] = l;
+}
+
+// A warp's 64 rows of 128 bytes: zeros in place of infinities and NaN.
+__device__ __noinline__ void zero_nonfinite(uint32_t rows) {
+#pragma unroll 1
+  for (uint32_t at = rows + (threadIdx.x & 31) * 16u; at < rows + 8192u; at += 512u) {
+    uint32_t v[4];
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(at)
+                 : "memory");
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      if ((v[y] & 0x7F80u) == 0x7F80u) v[y] &= 0xFFFF0000u;
+      if ((v[y] & 0x7F800000u) == 0x7F800000u) v[y] &= 0xFFFFu;
+    }
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+  }
 }
 
 template <int DP, bool APART>
@@ -625,14 +669,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(su32(&sh.qr[t]));
       }
-      const int lo_pos = w.s.len - w.s.m + static_cast<int>(quotient(static_cast<int64_t>(w.rt) * kUnitRows, a.g));
-      const int hi_pos = w.sp.end - 1;
+      const int lo_pos = first_pos(a, w), hi_pos = w.sp.end - 1;
       for (int i = 0; i < w.nt; ++i) {
         ok = mbar_wait(su32(&sh.vf[vp.s]), vp.ph, abort_flag, a.err, wait_cycles);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
         const int tile0 = w.sp.tile(w.t0 + i) * kKT;
-        if (tile0 + kKT - 1 > lo_pos || (a.window > 0 && hi_pos - tile0 >= a.window)) {
+        if (mixed_tile(a, tile0, lo_pos, hi_pos)) {
           const uint32_t st = sv + vp.s * C::kTile;
           bool bad = false;
           // this warp's 64 tokens: 8 pieces a row of 128 bytes, column halves one after the other
@@ -653,7 +696,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (bad) *const_cast<volatile uint32_t*>(&sh.poison[unit & 7]) = unit + 1;
+          if (__any_sync(~0u, bad)) {
+            // zeros in their place; the rows that see them add them at the end of the unit
+            for (int hf = 0; hf < DP / 64; ++hf) zero_nonfinite(st + hf * C::kHalf + t * 8192u);
+            if (lane == 0) *const_cast<volatile uint32_t*>(&sh.poison[unit & 7]) = unit + 1;
+          }
           fence_async_smem();
           __syncwarp();
         }
@@ -797,11 +844,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (*const_cast<volatile uint32_t*>(&sh.poison[unit & 7]) == unit + 1) {
           const Walk seg = w;
           const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + row * a.ldq + static_cast<int64_t>(hq) * a.D;
-          float ml[2];
 #pragma unroll 1
           for (int x = 0; x < DP; x += 32) {
             float o[32];
-            row_by_row(a, seg, row_ok ? q : nullptr, pos, x, o, ml);
+            tmem_ld32_async(to + x, o);
+            tmem_wait_ld();
+            if (pos >= 0) add_nonfinite(a, seg, q, pos, m, x, o);
             __syncwarp();
             uint32_t u[32];
 #pragma unroll
@@ -809,8 +857,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16(to + x, u);
             tmem_st16(to + x + 16, u + 16);
           }
-          m = ml[0] / c;  // back to the unit of the scores
-          l = ml[1];
           tmem_wait_st();
         }
         // ---- results of the segment

@@ -391,6 +391,28 @@ def check_attn_one(pool, b, q, out, n, m, window, sinks, scale):
     assert worst(out, ref, tol) <= 1.0
 
 
+@pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 128), (BF16, 256), (F32, 64)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150000, 300)])
+def test_hidden_values_of_a_long_context(bec, dtype, D, window, sinks):
+    """Infinities and NaN among the values that only some rows see, 200,000 tokens in: their cost is that of the
+    tiles they lie in, the other rows and the sequence behind are as ever."""
+    lens, ms = [200000, 90], [140, 90]
+    pool = Pool(bec, lens, 64, 1, D, dtype, 41)
+    # near the rows' own positions, a whole token and single columns; at the window's far end; the second sequence
+    for b, j, bad in ((0, 199900, float("nan")), (0, 49920, float("inf")), (1, 60, -float("inf"))):
+        pool.set_token(b, j, v=torch.full((1, D), bad))
+    for j, col, bad in ((199990, 3, float("inf")), (199870, 3, -float("inf")), (199995, D - 1, -float("inf")),
+                        (50010, 9, float("nan"))):
+        one = pool.tok_v[0][j].clone()
+        one[0, col] = bad
+        pool.set_token(0, j, v=one)
+    q = randn((230, 2, D), dtype, gen(42))
+    # the rows that see a bad value give it its weight: weights that fp32 holds
+    out = pool.kv.attn_prefill(1, q, pool.seqs, i32([0, 140, 230]), window=window, sinks=sinks, scale=0.02)
+    pool.kv.check_errors()
+    check_attn(pool, q, out, lens, ms, window, sinks, 0.02)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_attn_large_and_tiny_scores(bec, dtype):
     """Scores far apart, and a running maximum that grows along the cache."""
