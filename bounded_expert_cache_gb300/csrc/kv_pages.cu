@@ -171,20 +171,22 @@ __device__ __forceinline__ int2 prefix_of(const int* counts, int w, int lane) {
   return make_int2(__reduce_add_sync(~0u, before), __reduce_add_sync(~0u, all));
 }
 
-// Block-wide inclusive scan.
-__device__ __forceinline__ int block_incl(int v, int* tmp, int* total) {
+// Block-wide inclusive scan; the total in 64 bits: 1,024 values of up to 2^26
+// pages do not fit in 32 (a warp's 32 do). The scan itself wraps where the total does.
+__device__ __forceinline__ uint32_t block_incl(uint32_t v, uint32_t* tmp, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  uint32_t x = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(~0u, x, d);
+    const uint32_t y = __shfl_up_sync(~0u, x, d);
     if (lane >= d) x += y;
   }
   if (lane == 31) tmp[warp] = x;
   __syncthreads();
-  const int t = tmp[lane];
-  const int below = __reduce_add_sync(~0u, lane < warp ? t : 0);
-  *total = __reduce_add_sync(~0u, t);
+  const uint32_t t = tmp[lane];
+  const uint32_t below = __reduce_add_sync(~0u, lane < warp ? t : 0u);
+  const uint32_t low = __reduce_add_sync(~0u, t & 0xFFFFu), high = __reduce_add_sync(~0u, t >> 16);
+  *total = (static_cast<int64_t>(high) << 16) + low;
   __syncthreads();
   return x + below;
 }
@@ -200,7 +202,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
   int* copies = info + n;
   __shared__ uint32_t bits[kBitmapWords];
   __shared__ int counts[kAllWarps];
-  __shared__ int scan[kWarps];
+  __shared__ uint32_t scan[kWarps];
   auto cluster = cg::this_cluster();
   const int tid = threadIdx.x, rank = cluster.block_rank(), lane = tid & 31;
   const int w = rank * kWarps + (tid >> 5);
@@ -233,7 +235,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
   const int mine = count_free(kv, st, lane);
   share_counts(cluster, counts, w, lane, mine);  // also publishes shr and last
   // requests of every listed sequence
-  int total = 0, n_copies = 0;
+  int64_t wanted = 0;  // pages
+  int n_copies = 0;
   if (ok && room && !stop) {
     for (int i0 = 0; i0 < n; i0 += kThreads) {
       const int i = i0 + tid;
@@ -250,20 +253,20 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
         need = cow + pages_of(kv, static_cast<int64_t>(len) + add) - have;
         info[i] = have * 2 + cow;
       }
-      int t;
-      const int incl = block_incl(need, scan, &t);
-      if (i < n) first[i] = total + incl - need;
-      int c;
-      const int before = block_incl(cow, scan, &c) - cow;
+      int64_t t, c;
+      const uint32_t incl = block_incl(need, scan, &t);
+      // (used only if all is granted: then it is below the pages there are)
+      if (i < n) first[i] = static_cast<int>(static_cast<uint32_t>(wanted) + incl - need);
+      const uint32_t before = block_incl(cow, scan, &c) - cow;
       if (i < n) copies[i] = n_copies + before;
-      n_copies += c;
-      // the pool bounds what can be granted; beyond it only the verdict counts
-      total = min(total + t, kv.P + 1);
+      n_copies += static_cast<int>(c);
+      wanted += t;
     }
-    if (tid == 0) first[n] = total;
+    if (tid == 0) first[n] = static_cast<int>(wanted);
   }
   const int2 pre = prefix_of(counts, w, lane);
-  if (total > pre.y) room = false;
+  if (wanted > pre.y) room = false;
+  const int total = room ? static_cast<int>(wanted) : 0;
   __syncthreads();
   const bool go = ok && room && !stop;
   // the lowest free pages, in order

@@ -674,6 +674,24 @@ def test_page_calls_refuse_and_change_nothing(bec):
     m.check()
 
 
+@pytest.mark.parametrize("n,each", [(32, 2 ** 30), (64, 2 ** 30), (64, 2 ** 30 - 15)])
+def test_reserve_of_more_pages_than_32_bits_count(bec, n, each):
+    """Requests that each fit their table row, 2^31 and 2^32 pages together (or a few less than a whole page's)."""
+    W = 2 ** 26
+    k = torch.zeros((1, 8, 1, 16, 8), dtype=BF16, device="cuda")
+    table = torch.empty((n, W), dtype=torch.int32, device="cuda")
+    kv = bec.KvCache(k, k.clone(), table, i32([0] * n), i32([0] * 8))
+    kv.reserve(i32(range(n)), i32([each] * n))
+    with pytest.raises(bec.MoeError, match="CAPACITY"):
+        kv.check_errors()
+    assert kv.lens.tolist() == [0] * n and kv.ref.tolist() == [0] * 8
+    # a request behind them that fits is granted alone
+    table[1, :2] = -1
+    kv.reserve(i32([1]), i32([20]))
+    kv.check_errors()
+    assert kv.lens.tolist() == [0, 20] + [0] * (n - 2) and table[1, :2].tolist() == [0, 1]
+
+
 def test_decode_step_in_a_graph_on_another_stream(bec):
     """reserve, write and attention captured once and replayed as the sequences grow."""
     dtype, hkv, hq, D, page = BF16, 2, 8, 64, 16
