@@ -91,7 +91,8 @@ moe_status_t attention(const char* call, bool decode, const moe_kv_t* kv, int32_
   if (!std::isfinite(scale) || !(scale > 0.f)) return fail(MOE_ERR_ARG, call, "scale is not finite and positive");
   if (window < 0 || sinks < 0) return fail(MOE_ERR_ARG, call, "window or sinks < 0");
   const int32_t rows = decode ? n * n_q : n_rows;
-  if (n == 0 || rows == 0) return MOE_OK;
+  if (!decode && n == 0 && n_rows > 0) return fail(MOE_ERR_ARG, call, "rows without a sequence (n is 0)");
+  if (rows == 0) return MOE_OK;
   if (!q || !out || (!decode && !cu)) return fail(MOE_ERR_ARG, call, "q, out or cu is NULL");
   const int64_t width = static_cast<int64_t>(n_heads) * kv->head_dim;
   const int per = 16 / elem_bytes(kv->dtype);

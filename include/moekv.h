@@ -124,8 +124,8 @@ moe_status_t moe_kv_copy_pages(const moe_kv_t* kv, const int32_t* src, const int
  *
  * moe_attn_prefill: chunks of any length; rows cu[i] .. cu[i+1]-1 (device
  * int32 [n+1], cu[0] = 0, cu[n] = n_rows; anything else is recorded as an
- * error) are the newest tokens of seqs[i]. Rows without a sequence belong to an
- * empty one, and are 0.
+ * error, or refused where n is 0) are the newest tokens of seqs[i]. Rows that have
+ * no sequence can be given to an empty one, and are 0. Without rows cu is not read.
  *
  * scale must be positive. seqs may be NULL: sequences 0 .. n-1. n_heads must
  * be a multiple of n_kv_heads, at most 64 times as many. */

@@ -503,6 +503,16 @@ def test_attn_prefill_chunks_cover_all_rows(bec, dtype, cu):
             pool.kv.check_errors()
 
 
+@pytest.mark.parametrize("D", [64, 256])
+def test_attn_prefill_rows_without_any_sequence_are_refused(bec, D):
+    kv = Pool(bec, [5], 16, 2, D, BF16, 1).kv
+    q = randn((6, 4, D), BF16, gen(2))
+    with pytest.raises(bec.MoeError, match="without a sequence"):
+        kv.attn_prefill(1, q, i32([]), i32([0]))
+    assert kv.attn_prefill(1, q[:0], i32([]), i32([0])).shape == (0, 4, D)
+    kv.check_errors()
+
+
 # ---------------------------------------------------------------- pages
 class Model:
     """The cache's bookkeeping on the host, page by page, with the tokens each page holds."""
