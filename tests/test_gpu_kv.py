@@ -453,6 +453,24 @@ def test_attention_past_32_bit_offsets(bec):
     assert torch.equal(k[0, 3], k[0, P - 1])
 
 
+def test_attn_prefill_more_rows_than_31_bits(bec):
+    """A chunk of more than 2^31 (token, head) rows: its last tokens are the sequence's, those before see nothing."""
+    m, n, heads, D = 2 ** 31 // 64 + 3, 40, 64, 8
+    if torch.cuda.mem_get_info()[0] < 2 * m * heads * D * 4 + 2 ** 33:
+        pytest.skip("needs 146 GB of device memory")
+    pool = Pool(bec, [n], 16, 1, D, F32, 61)
+    q = torch.empty((m, heads, D), dtype=F32, device="cuda")
+    q[-n:] = randn((n, heads, D), F32, gen(62))
+    out = torch.full((m, heads, D), 7.0, dtype=F32, device="cuda")
+    pool.kv.attn_prefill(1, q, pool.seqs, i32([0, m]), out=out)
+    pool.kv.check_errors()
+    for part in out[:-n].split(2 ** 21):
+        assert part.abs().max().item() == 0.0
+    check_attn(pool, q[-n:], out[-n:], [n], [n], 0, 0, D ** -0.5)
+    del q, out
+    torch.cuda.empty_cache()
+
+
 def test_attention_refusals(bec):
     pool = Pool(bec, [50, 20], 16, 2, 64, BF16, 1)
     kv, q = pool.kv, randn((2, 4, 64), BF16, gen(1))
