@@ -394,7 +394,9 @@ struct MmaEngine {
           bad |= nonfinite2(w[y][0]) || nonfinite2(w[y][1]) || nonfinite2(w[y][2]) || nonfinite2(w[y][3]);
       }
     }
-    return __any_sync(~0u, bad);
+    bad = __any_sync(~0u, bad);
+    __syncwarp();  // (a vote orders no memory) other lanes read these zeros
+    return bad;
   }
 
   __device__ __forceinline__ void values_by_row(const Tile& vt, int key0, int ch) {
