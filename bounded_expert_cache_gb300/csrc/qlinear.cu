@@ -202,8 +202,59 @@ __device__ __forceinline__ void load_x(const LinearArgs& a, const Plan& p, int t
   }
 }
 
+// Outputs that came out infinite or NaN, formed again weight by weight. A group's
+// sum of codes times x can overflow where the sum of weights times x does not
+// (|x| above 1e35), and an infinite x makes s sum(q x) + b sum(x) a NaN where
+// (s q + b) x is an infinity. Once not finite a sum stays so, hence this finds
+// every such output. A warp a row of the CTA's tiles, lanes along K.
+template <int QUANT, bool XF32>
+__device__ __noinline__ void form_again(const LinearArgs& a, int t0, int tok, int tiles, int R) {
+  const int lane = threadIdx.x & 31;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    for (int r = threadIdx.x >> 5; r < R && tile * R + r < a.N; r += kWarps) {
+      const int n = tile * R + r;
+      bool bad = false;
+      if (lane < tok) {
+        const int64_t at = (t0 + lane) * a.ldy + n;
+        bad = !isfinite(a.yt == MOE_F32 ? static_cast<const float*>(a.y)[at]
+                                        : __bfloat162float(static_cast<const __nv_bfloat16*>(a.y)[at]));
+      }
+      const uint8_t* row = a.w + static_cast<int64_t>(n) * (a.K / 2);
+      const uint16_t* meta = reinterpret_cast<const uint16_t*>(a.meta + static_cast<int64_t>(n) * (a.K / 16));
+      for (uint32_t left = __ballot_sync(~0u, bad); left; left &= left - 1) {
+        const int t = __ffs(left) - 1;
+        float v = 0.f;
+        for (int k = lane; k < a.K; k += 32) {
+          float w;
+          if (QUANT == MOE_Q4_0) {
+            const int c = __ldg(row + (k >> 5) * 16 + (lane & 15)) >> (lane & 16 ? 4 : 0) & 15;
+            w = __half2float(__ushort_as_half(__ldg(meta + (k >> 5)))) * static_cast<float>(c - 8);  // exact
+          } else {
+            const int c = __ldg(row + (k >> 1)) >> (k & 1 ? 4 : 0) & 15;
+            const uint32_t sb = __ldg(reinterpret_cast<const uint32_t*>(meta) + (k >> 6));
+            w = fmaf(__uint_as_float(sb << 16), static_cast<float>(c), __uint_as_float(sb & 0xFFFF0000u));
+          }
+          const int64_t at = (t0 + t) * a.ldx + k;
+          v += w * (XF32 ? __ldg(static_cast<const float*>(a.x) + at)
+                         : __bfloat162float(static_cast<const __nv_bfloat16*>(a.x)[at]));
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+        if (lane == 0) {
+          if (a.bias) v += __ldg(a.bias + n);
+          const int64_t at = (t0 + t) * a.ldy + n;
+          if (a.yt == MOE_F32)
+            static_cast<float*>(a.y)[at] = v;
+          else
+            static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+        }
+      }
+    }
+  }
+}
+
 template <int QUANT, bool XF32, int NT, int WK>
-__global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan p) {
+__global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearArgs a, Plan p) {
   constexpr int kParts = XF32 ? 3 : 1, R = 16 * kWarps / WK;  // rows of a tile
   extern __shared__ __align__(128) unsigned char sm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -307,7 +358,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
   // ldmatrix: lanes 0-7 and 8-15 address rows 0-7 and 8-15 of a group's piece, lanes 16-31 the next group's
   const uint32_t q_off = (lane & 15) * 128, q_phase = ((lane & 7) ^ (lane >> 4)) << 4, m_off = kCodeBytes + r * 16;
 
+  float probe = 0.f;  // NaN once an output is not finite
   auto store = [&](int n, int t, float v) {
+    probe = fmaf(v, 0.f, probe);
     if (a.bias) v += __ldg(a.bias + n);
     const int64_t at = (t0 + t) * a.ldy + n;
     if (a.yt == MOE_F32)
@@ -433,9 +486,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
     tile += gridDim.x;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (__syncthreads_or(probe != 0.f)) form_again<QUANT, XF32>(a, t0, tok, p.tiles, R);
 }
 
-constexpr int kFull = 226 * 1024;              // shared memory of a CTA
+constexpr int kFull = 226 * 1024;              // dynamic shared memory of a CTA
 constexpr int kRedBytes = 2 * kWarps * 16 * 8 * 4;
 
 // Shared bytes of x of a slice and its sums.

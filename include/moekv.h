@@ -142,8 +142,10 @@ moe_status_t moe_attn_prefill(const moe_kv_t* kv, int32_t layer, const void* q, 
  * by N*K/16 scale bytes; x: device [T, K], rows ldx elements apart (xt MOE_F32
  * or MOE_BF16); y: device [T, N], rows ldy apart (yt likewise); bias: device
  * fp32 [N] or NULL. w and x rows 16-byte aligned. Products are exact and sums
- * fp32 for both types of x. Meant for few tokens; T is not bounded, T = 0 does
- * nothing. */
+ * fp32 for both types of x, over a group before its scale is applied. An output
+ * that is not finite is formed again weight by weight, so infinities and NaN in x
+ * give what weight times x gives, and only the outputs' own sums can overflow.
+ * Meant for few tokens; T is not bounded, T = 0 does nothing. */
 moe_status_t moe_quant_linear(const void* w, int32_t quant, int32_t N, int32_t K, const void* x, int32_t xt,
                               int64_t ldx, int32_t T, const float* bias, void* y, int32_t yt, int64_t ldy,
                               moe_stream_t stream);

@@ -119,6 +119,37 @@ def test_quant_linear_edges(bec, group):
                             4).shape == (0, 4)
 
 
+@pytest.mark.parametrize("quant", [Q4_0, I4_G64])
+@pytest.mark.parametrize("xt", [BF16, F32])
+@pytest.mark.parametrize("T,N,K", [(1, 40, 256), (3, 515, 1088), (24, 300, 2048), (24, 70, 8192), (50, 33, 192)])
+def test_quant_linear_infinite_and_large_activations(bec, quant, xt, T, N, K):
+    """Infinities and NaN in x give what weight times x gives; sums of codes times x that pass fp32's range do not
+    reach outputs that stay within it."""
+    g = gen(T + K)
+    w, (s, q, b) = pack(N, K, quant, g)
+    W = s * q + b
+    bias = randn((N,), F32, g)
+    x = randn((T, K), xt, g).abs()
+    for t in range(T):  # every kind of token beside each other
+        kind = t % 5
+        if kind == 0:  # group sums of codes overflow, outputs do not
+            x[t, :64] *= 1.2e37 if quant == Q4_0 else 1.5e36
+        elif kind == 1:
+            x[t, K // 2] = float("inf")
+        elif kind == 2:
+            x[t, 5], x[t, K - 1] = float("inf"), -float("inf")
+        elif kind == 3:
+            x[t, 70 % K] = float("nan")
+    for yt in (F32, BF16):
+        y = bec.quant_linear(x, w, quant, N, bias=bias, y=torch.empty((T, N), dtype=yt, device="cuda"))
+        # an infinity times a weight of zero is a NaN: products one by one, not a library's sums
+        ref = torch.stack([(W * r[None]).sum(1) for r in x.double()]) + bias.double()
+        mag = x.double().abs() @ (s.abs() * q.abs() + b.abs()).t() + bias.double().abs()
+        tol = 2 * (K / 32 + 80) * U24 * mag + (U8 * ref.abs() if yt == BF16 else 0) * 1.01 + 1e-30
+        assert torch.isfinite(ref[::5]).all() and ref[0].abs().max() > 1e35
+        assert worst(y, ref, tol) <= 1.0
+
+
 def test_quant_linear_refusals(bec):
     g = gen(1)
     w, _ = pack(16, 64, Q4_0, g)
