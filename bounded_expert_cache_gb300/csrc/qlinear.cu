@@ -556,10 +556,22 @@ cudaError_t by_tokens(const LinearArgs& a, int num_sms, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_quant_linear(const LinearArgs& a, int32_t quant, int num_sms, cudaStream_t st) {
-  if (quant == MOE_Q4_0)
-    return a.xt == MOE_F32 ? by_tokens<MOE_Q4_0, true>(a, num_sms, st) : by_tokens<MOE_Q4_0, false>(a, num_sms, st);
-  return a.xt == MOE_F32 ? by_tokens<MOE_I4_G64, true>(a, num_sms, st) : by_tokens<MOE_I4_G64, false>(a, num_sms, st);
+cudaError_t launch_quant_linear(const LinearArgs& args, int32_t quant, int num_sms, cudaStream_t st) {
+  // a grid has at most 65,535 blocks of tokens
+  constexpr int kMost = 65535 * kMaxTok;
+  LinearArgs a = args;
+  for (int64_t t0 = 0; t0 < args.T; t0 += kMost) {
+    a.T = static_cast<int32_t>(std::min<int64_t>(kMost, args.T - t0));
+    a.x = static_cast<const char*>(args.x) + t0 * args.ldx * (args.xt == MOE_F32 ? 4 : 2);
+    a.y = static_cast<char*>(args.y) + t0 * args.ldy * (args.yt == MOE_F32 ? 4 : 2);
+    cudaError_t e;
+    if (quant == MOE_Q4_0)
+      e = a.xt == MOE_F32 ? by_tokens<MOE_Q4_0, true>(a, num_sms, st) : by_tokens<MOE_Q4_0, false>(a, num_sms, st);
+    else
+      e = a.xt == MOE_F32 ? by_tokens<MOE_I4_G64, true>(a, num_sms, st) : by_tokens<MOE_I4_G64, false>(a, num_sms, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace moe

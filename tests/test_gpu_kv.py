@@ -150,6 +150,23 @@ def test_quant_linear_infinite_and_large_activations(bec, quant, xt, T, N, K):
         assert worst(y, ref, tol) <= 1.0
 
 
+@pytest.mark.parametrize("quant,xt", [(Q4_0, BF16), (I4_G64, F32)])
+def test_quant_linear_more_tokens_than_a_grid_has_blocks(bec, quant, xt):
+    T, N, K = 65535 * 24 + 50, 17, 64
+    g = gen(6)
+    w, (s, q, b) = pack(N, K, quant, g)
+    x = randn((T, K + 8), xt, g)[:, :K]
+    frame = torch.full((T, N + 1), 7.0, dtype=xt, device="cuda")
+    y = bec.quant_linear(x, w, quant, N, y=frame[:, :N])
+    W = s * q + b
+    for t0 in range(0, T, 2 ** 18):
+        r = x[t0:t0 + 2 ** 18].double()
+        ref, mag = r @ W.t(), r.abs() @ (s.abs() * q.abs() + b.abs()).t()
+        tol = 2 * (K / 32 + 80) * U24 * mag + (U8 * ref.abs() if xt == BF16 else 0) * 1.01 + 1e-30
+        assert worst(y[t0:t0 + 2 ** 18], ref, tol) <= 1.0, t0
+    assert (frame[:, N] == 7.0).all()
+
+
 def test_quant_linear_refusals(bec):
     g = gen(1)
     w, _ = pack(16, 64, Q4_0, g)
