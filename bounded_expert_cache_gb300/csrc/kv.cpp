@@ -333,6 +333,8 @@ extern "C" moe_status_t moe_quant_linear(const void* w, int32_t quant, int32_t N
     if (quant != MOE_Q4_0 && quant != MOE_I4_G64) return fail(MOE_ERR_ARG, call, "quant is neither MOE_Q4_0 nor MOE_I4_G64");
     const int group = quant == MOE_Q4_0 ? 32 : 64;
     if (N < 1 || K < group || K % group) return fail(MOE_ERR_ARG, call, "N < 1, or K not a positive multiple of the group");
+    // offsets within a tile of rows are 32 bits, row numbers 31
+    if (K >= 1 << 25 || N > 0x7FFFFFFF - 512) return fail(MOE_ERR_ARG, call, "K above 2^25 - 1 or N above 2^31 - 513");
     if ((xt != MOE_F32 && xt != MOE_BF16) || (yt != MOE_F32 && yt != MOE_BF16))
       return fail(MOE_ERR_ARG, call, "x or y is neither MOE_F32 nor MOE_BF16");
     if (T < 0) return fail(MOE_ERR_ARG, call, "T < 0");

@@ -138,10 +138,11 @@ moe_status_t moe_attn_prefill(const moe_kv_t* kv, int32_t layer, const void* q, 
 
 /* y[t, n] = sum_k W[n, k] x[t, k] (+ bias[n]) for a 4-bit matrix W [N, K] in
  * the split-plane layout of one expert matrix: quant MOE_Q4_0 (K a multiple of
- * 32) or MOE_I4_G64 (K a multiple of 64). w: device, N*K/2 quant bytes followed
- * by N*K/16 scale bytes; x: device [T, K], rows ldx elements apart (xt MOE_F32
- * or MOE_BF16); y: device [T, N], rows ldy apart (yt likewise); bias: device
- * fp32 [N] or NULL. w and x rows 16-byte aligned. Products are exact and sums
+ * 32) or MOE_I4_G64 (K a multiple of 64), K below 2^25 and N below 2^31 - 512.
+ * w: device, N*K/2 quant bytes followed by N*K/16 scale bytes; x: device [T, K],
+ * rows ldx elements apart (xt MOE_F32 or MOE_BF16); y: device [T, N], rows ldy
+ * apart (yt likewise); bias: device fp32 [N] or NULL. w and x rows 16-byte
+ * aligned. Products are exact and sums
  * fp32 for both types of x, over a group before its scale is applied. An output
  * that is not finite is formed again weight by weight, so infinities and NaN in x
  * give what weight times x gives, and only the outputs' own sums can overflow.

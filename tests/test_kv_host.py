@@ -85,3 +85,13 @@ def test_quant_linear_arguments(native, args, why):
 
 def test_quant_linear_no_tokens_is_no_work(native):
     assert native.lib.moe_quant_linear(None, 1, 16, 64, None, 1, 64, 0, None, None, 0, 16, None) == 0
+
+
+@pytest.mark.parametrize("N,K,refused", [(16, 2 ** 25, True), (128, 2 ** 26, True), (1, 2 ** 31 - 64, True),
+                                         (2 ** 31 - 512, 64, True), (2 ** 31 - 1, 64, True), (16, 2 ** 25 - 64, False),
+                                         (2 ** 31 - 513, 64, False)])
+def test_quant_linear_sizes_that_offsets_hold(native, N, K, refused):
+    """Sizes that pass stop at the NULL pointers instead."""
+    st = native.lib.moe_quant_linear(None, 2, N, K, None, 1, K, 1, None, None, 0, N, None)
+    why = native.lib.moe_last_error(None)
+    assert st == 1 and (b"above" if refused else b"NULL") in why
