@@ -418,6 +418,21 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) compac
   }
 }
 
+// The list of a page copy: all of it is checked before anything is copied, so
+// that no block copies while another finds an error. Every block checks a short
+// list itself, which saves a launch (one page: 4 us instead of 5.3); a longer one
+// is checked once, before the copies' launch.
+constexpr int kShortList = 2048;
+__device__ __forceinline__ bool copy_ok(const Kv& kv, int s, int d) { return s >= 0 && s < kv.P && d >= 0 && d < kv.P; }
+__global__ void __launch_bounds__(kThreads)
+    check_pages_kernel(Kv kv, const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n) {
+  if (pending(kv)) return;  // (by now perhaps this launch's own error, of which one record is enough)
+  bool ok = true;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * kThreads)
+    ok &= copy_ok(kv, src[i], dst[i]);
+  if (!ok) atomicOr(&kv.work->err, MOE_DEVERR_BADIDX);
+}
+
 // Whole pages src[i] -> dst[i] in every layer, pieces of kPiece vectors, and
 // (REMAP) the table entries of moved pages.
 constexpr int kPiece = 1024;  // 16 KB
@@ -425,8 +440,17 @@ template <bool REMAP>
 __global__ void __launch_bounds__(256)
     page_copy_kernel(Kv kv, uint4* k, uint4* v, const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n,
                      int L, int64_t page_vecs) {
-  if (REMAP) n = kv.work->n_copies;
-  else if (pending(kv)) return;
+  if (REMAP) {
+    n = kv.work->n_copies;
+  } else {
+    const bool stop = pending(kv);
+    bool ok = true;
+    if (n <= kShortList)
+      for (int i = threadIdx.x; i < n; i += 256) ok &= copy_ok(kv, src[i], dst[i]);
+    ok = __syncthreads_and(ok);
+    if (!ok && !stop && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&kv.work->err, MOE_DEVERR_BADIDX);
+    if (__syncthreads_or(stop) || !ok) return;  // (of a good list's launch no block sets the word)
+  }
   const int pieces = static_cast<int>((page_vecs + kPiece - 1) / kPiece);
   const uint64_t items = static_cast<uint64_t>(n) * L * 2 * pieces;
   for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
@@ -435,10 +459,6 @@ __global__ void __launch_bounds__(256)
     uint4* pool = take_mod(r, 2) ? v : k;
     const int l = take_mod(r, L), i = static_cast<int>(r);
     const int s = src[i], d = dst[i];
-    if (!REMAP && (s < 0 || s >= kv.P || d < 0 || d >= kv.P)) {
-      if (threadIdx.x == 0) atomicOr(&kv.work->err, MOE_DEVERR_BADIDX);
-      continue;
-    }
     const uint4* from = pool + (static_cast<int64_t>(l) * kv.P + s) * page_vecs + static_cast<int64_t>(piece) * kPiece;
     uint4* to = pool + (static_cast<int64_t>(l) * kv.P + d) * page_vecs + static_cast<int64_t>(piece) * kPiece;
     const int vecs = static_cast<int>(min(static_cast<int64_t>(kPiece), page_vecs - static_cast<int64_t>(piece) * kPiece));
@@ -594,8 +614,14 @@ cudaError_t launch_kv_compact(const moe_kv_t& a, const KvLayout& l, int num_sms,
 
 cudaError_t launch_kv_copy_pages(const moe_kv_t& a, const KvLayout& l, const int32_t* src, const int32_t* dst,
                                  int32_t n, int num_sms, cudaStream_t st) {
-  page_copy_kernel<false><<<8 * num_sms, 256, 0, st>>>(kv_of(a, l), static_cast<uint4*>(a.k), static_cast<uint4*>(a.v),
-                                                       src, dst, n, a.n_layers, page_vecs(a));
+  const Kv kv = kv_of(a, l);
+  if (n > kShortList) {
+    check_pages_kernel<<<std::min((n - 1) / kThreads + 1, num_sms), kThreads, 0, st>>>(kv, src, dst, n);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  page_copy_kernel<false><<<8 * num_sms, 256, 0, st>>>(kv, static_cast<uint4*>(a.k), static_cast<uint4*>(a.v), src, dst,
+                                                       n, a.n_layers, page_vecs(a));
   return cudaGetLastError();
 }
 

@@ -102,7 +102,8 @@ moe_status_t moe_kv_free(const moe_kv_t* kv, const int32_t* seqs, int32_t n, moe
 moe_status_t moe_kv_compact(const moe_kv_t* kv, moe_stream_t stream);
 
 /* Copy whole pages src[i] -> dst[i] in every layer (device int32 [n]; no dst
- * may be listed twice or be a src). Table and ref are the caller's business. */
+ * may be listed twice or be a src). Table and ref are the caller's business.
+ * With a page id out of range nothing is copied. */
 moe_status_t moe_kv_copy_pages(const moe_kv_t* kv, const int32_t* src, const int32_t* dst, int32_t n,
                                moe_stream_t stream);
 

@@ -768,6 +768,30 @@ def test_reserve_of_more_pages_than_32_bits_count(bec, n, each):
     assert kv.lens.tolist() == [0, 20] + [0] * (n - 2) and table[1, :2].tolist() == [0, 1]
 
 
+@pytest.mark.parametrize("n,bad", [(3, 1), (600, 599), (2200, 0), (2200, 700), (2200, 2199)])
+@pytest.mark.parametrize("which", ["src", "dst"])
+def test_copy_pages_with_one_bad_id_copies_nothing(bec, n, bad, which):
+    """Lists good but for one entry, short ones and more work than the GPU holds blocks at once."""
+    kv = bec.KvCache.empty(2, 4500, 2, 16, 64, 1, 4)
+    kv.k.copy_(randn(kv.k.shape, BF16, gen(1)))
+    kv.v.copy_(randn(kv.v.shape, BF16, gen(2)))
+    k, v = kv.k.clone(), kv.v.clone()
+    lists = dict(src=torch.arange(n, dtype=torch.int32, device="cuda"),
+                 dst=torch.arange(2250, 2250 + n, dtype=torch.int32, device="cuda"))
+    good = lists[which][bad].item()
+    for wrong in (-1, 4500, 2 ** 31 - 1):
+        lists[which][bad] = wrong
+        kv.copy_pages(lists["src"], lists["dst"])
+        with pytest.raises(bec.MoeError, match="MOE_ERR_ARG"):
+            kv.check_errors()
+        assert torch.equal(kv.k, k) and torch.equal(kv.v, v)
+    lists[which][bad] = good
+    kv.copy_pages(lists["src"], lists["dst"])
+    kv.check_errors()
+    k[:, 2250:2250 + n], v[:, 2250:2250 + n] = k[:, :n], v[:, :n]
+    assert torch.equal(kv.k, k) and torch.equal(kv.v, v)
+
+
 def test_decode_step_in_a_graph_on_another_stream(bec):
     """reserve, write and attention captured once and replayed as the sequences grow."""
     dtype, hkv, hq, D, page = BF16, 2, 8, 64, 16
