@@ -1,6 +1,7 @@
 // C ABI entry points of the KV cache, attention and the 4-bit linear layer:
 // argument checks, scratch layout, launches.
 #include <cmath>
+#include <cstddef>
 #include <string>
 
 #include "kv.h"
@@ -194,12 +195,14 @@ extern "C" moe_status_t moe_kv_check_errors(const moe_kv_t* kv, moe_stream_t str
     int sms = 0;
     moe_status_t st = open_kv(call, kv, &l, &sms);
     if (st != MOE_OK) return st;
-    uint32_t* word = &static_cast<moe::KvWork*>(kv->work)->err;
-    uint32_t err = 0;
-    cudaError_t e = cudaMemcpyAsync(&err, word, sizeof(err), cudaMemcpyDeviceToHost, stream);
-    if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof(err), stream);
+    // both error words, with the count of planned copies between them
+    constexpr size_t kHead = offsetof(moe::KvWork, late) + sizeof(uint64_t);
+    moe::KvWork head{};
+    cudaError_t e = cudaMemcpyAsync(&head, kv->work, kHead, cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess) e = cudaMemsetAsync(kv->work, 0, kHead, stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_fail(call, e);
+    const uint32_t err = head.err | static_cast<uint32_t>(head.late);
     if (err & MOE_DEVERR_TIMEOUT) {
       // units left unjoined have left their tickets behind
       e = cudaMemsetAsync(static_cast<char*>(kv->work) + l.tickets, 0, sms * moe::kPrefillTickets * 4, stream);

@@ -19,8 +19,9 @@ enum : uint32_t {
 struct KvWork {
   uint32_t err;       // error word
   int32_t n_copies;   // page copies planned by reserve or compact
+  uint64_t late;      // errors of a write (low half) and that write's number
   int32_t n_live;     // pages in use, of the last compact
-  int32_t pad[61];
+  int32_t pad[59];
 };
 constexpr int kPartRows = 64;        // most rows of one partial result (decode)
 constexpr int kPrefillTickets = 8;   // tickets a CTA (prefill)

@@ -19,6 +19,9 @@
 // in 162 us, 973 MB read and written at 6.0 TB/s.
 #include <cooperative_groups.h>
 
+#include <atomic>
+#include <cstddef>
+
 #include "kv.h"
 
 namespace cg = cooperative_groups;
@@ -42,7 +45,18 @@ struct Kv {
 __device__ __forceinline__ int pages_of(const Kv& kv, int64_t tokens) {
   return static_cast<int>((tokens + kv.page - 1) >> kv.page_shift);
 }
-__device__ __forceinline__ bool pending(const Kv& kv) { return *const_cast<volatile uint32_t*>(&kv.work->err) != 0u; }
+// Is a failure of an earlier call pending? A write records its own errors under
+// its number beside the error word, because its other blocks may still have to
+// read that: so a write stops for earlier calls' errors and never for its own, and
+// what it writes does not depend on timing. The next call moves them to the word.
+__device__ __forceinline__ bool pending(const Kv& kv, bool a_write = false, uint32_t number = 0) {
+  static_assert(offsetof(KvWork, err) == 0 && offsetof(KvWork, late) == 8, "one load of both");
+  uint64_t head, late;  // (32,768 rows: 14 us with one load a warp, 23 with two, all of one line)
+  asm volatile("ld.volatile.global.v2.u64 {%0, %1}, [%2];" : "=l"(head), "=l"(late) : "l"(kv.work) : "memory");
+  if (late == 0 || (a_write && static_cast<uint32_t>(late >> 32) == number)) return static_cast<uint32_t>(head) != 0u;
+  if (threadIdx.x == 0) atomicOr(&kv.work->err, static_cast<uint32_t>(late));
+  return true;
+}
 
 // Threads that share one listed sequence: a power of two, at least a warp.
 __device__ __forceinline__ int lanes_per(int n) {
@@ -488,7 +502,7 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(256)
     write_kernel(Kv kv, uint4* k, uint4* v, const uint4* __restrict__ nk, int64_t ldk, const uint4* __restrict__ nv,
                  int64_t ldv, const int32_t* __restrict__ seqs, const int32_t* __restrict__ cu, int n, int n_rows,
-                 int H, int tok_vecs) {
+                 int H, int tok_vecs, uint32_t number) {
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= n_rows) return;
   const uint4* fk = nk + row * ldk;
@@ -499,7 +513,10 @@ __global__ void __launch_bounds__(256)
     k0 = __ldg(fk + lane);
     v0 = __ldg(fv + lane);
   }
-  const bool stop = pending(kv);
+  const bool stop = pending(kv, true, number);
+  auto record = [&](uint32_t why) {
+    if (lane == 0) atomicOr(reinterpret_cast<unsigned long long*>(&kv.work->late), static_cast<unsigned long long>(number) << 32 | why);
+  };
   // the last i with cu[i] <= row: 32 probes a step
   int lo = 0, span = n;  // it is in [lo, lo + span)
   while (span > 1) {
@@ -515,17 +532,17 @@ __global__ void __launch_bounds__(256)
   if (row < r0 || row >= r1) return;
   const int s = seqs ? __ldg(seqs + lo) : lo;
   if (s < 0 || s >= kv.S) {
-    if (lane == 0) atomicOr(&kv.work->err, MOE_DEVERR_BADIDX);
+    record(MOE_DEVERR_BADIDX);
     return;
   }
   const int len = kv.lens[s], at = len - (r1 - row);
   if (len - (r1 - r0) < 0 || !held_ok(kv, len)) {  // the chunk does not fit: none of it is written
-    if (lane == 0) atomicOr(&kv.work->err, KV_DEVERR_SHARED);
+    record(KV_DEVERR_SHARED);
     return;
   }
   const int p = kv.table[static_cast<int64_t>(s) * kv.W + (at >> kv.page_shift)];
   if (p < 0 || p >= kv.P || kv.ref[p] != 1) {
-    if (lane == 0) atomicOr(&kv.work->err, p < 0 || p >= kv.P ? MOE_DEVERR_BADIDX : KV_DEVERR_SHARED);
+    record(p < 0 || p >= kv.P ? MOE_DEVERR_BADIDX : KV_DEVERR_SHARED);
     return;
   }
   const int64_t base = ((static_cast<int64_t>(p) * H) << kv.page_shift) + (at & (kv.page - 1));
@@ -590,10 +607,11 @@ cudaError_t launch_kv_write(const moe_kv_t& a, const KvLayout& l, int32_t layer,
                             int32_t n_rows, cudaStream_t st) {
   const int per = a.dtype == MOE_F32 ? 4 : 8;
   const int64_t off = layer * (static_cast<int64_t>(a.n_pages) * page_vecs(a));
+  static std::atomic<uint32_t> number{0};
   write_kernel<<<(n_rows + 7) / 8, 256, 0, st>>>(kv_of(a, l), static_cast<uint4*>(a.k) + off,
                                                   static_cast<uint4*>(a.v) + off, static_cast<const uint4*>(k_new),
                                                   ldk / per, static_cast<const uint4*>(v_new), ldv / per, seqs, cu, n,
-                                                  n_rows, a.n_kv_heads, tok_vecs(a));
+                                                  n_rows, a.n_kv_heads, tok_vecs(a), ++number);
   return cudaGetLastError();
 }
 

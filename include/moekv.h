@@ -59,7 +59,9 @@ moe_status_t moe_kv_work_bytes(const moe_kv_t* kv, int64_t* bytes);
  * MOE_ERR_STATE: a write to a page that other sequences share, or past the
  * sequence's length. MOE_ERR_TIMEOUT: a bounded device wait ran out.
  * While a failure is pending, the calls that change the cache (fork,
- * reserve, write, free, compact, copy_pages) do nothing. */
+ * reserve, write, free, compact, copy_pages) do nothing. (A captured write that
+ * failed and is replayed with no other call on the cache between does again
+ * what it did.) */
 moe_status_t moe_kv_check_errors(const moe_kv_t* kv, moe_stream_t stream);
 
 /* dst[i] becomes a sequence with src[i]'s tokens, sharing its pages (their
@@ -86,7 +88,8 @@ moe_status_t moe_kv_reserve(const moe_kv_t* kv, const int32_t* seqs, const int32
  * rows ldk and ldv elements apart (a slice of a fused projection), rows
  * 16-byte aligned; cu: device int32 [n+1]; rows outside cu[0] .. cu[n]-1 belong
  * to no sequence and are ignored. A chunk longer than its sequence and a token
- * whose page is shared are not written (an error is recorded). */
+ * whose page is shared are not written (an error is recorded); the others of
+ * the call are. */
 moe_status_t moe_kv_write(const moe_kv_t* kv, int32_t layer, const void* k_new, int64_t ldk, const void* v_new,
                           int64_t ldv, const int32_t* seqs, const int32_t* cu, int32_t n, int32_t n_rows,
                           moe_stream_t stream);

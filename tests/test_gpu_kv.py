@@ -792,6 +792,42 @@ def test_copy_pages_with_one_bad_id_copies_nothing(bec, n, bad, which):
     assert torch.equal(kv.k, k) and torch.equal(kv.v, v)
 
 
+@pytest.mark.parametrize("n", [5, 8, 9, 100, 255, 20000])
+@pytest.mark.parametrize("where", [0.0, 0.5, 1.0])
+@pytest.mark.parametrize("kind", ["shared", "long", "id"])
+def test_write_leaves_out_what_is_wrong_and_writes_the_rest(bec, n, where, kind):
+    """One token a sequence, up to more blocks than the GPU holds at once; one entry of the list is bad."""
+    kv = bec.KvCache.empty(1, n + 5, 1, 16, 8, n + 2, 1)
+    for at in range(0, n, 8192):
+        seqs = torch.arange(at, min(n, at + 8192), dtype=torch.int32, device="cuda")
+        kv.reserve(seqs, torch.ones_like(seqs))
+    bad = int(where * (n - 1))
+    seqs = torch.arange(n, dtype=torch.int32, device="cuda")
+    rows = torch.arange(n + 1, dtype=torch.int32, device="cuda")  # cu
+    if kind == "shared":
+        kv.fork(seqs[bad:bad + 1].clone(), i32([n]))
+    elif kind == "long":
+        rows[bad + 1:] += 1
+    else:
+        seqs[bad] = n + 2
+    pages = kv.table[:n, 0].long()
+    for step in range(3):
+        k, v = randn((n + 1, 1, 8), BF16, gen(step)), randn((n + 1, 1, 8), BF16, gen(9 + step))
+        m = n + (kind == "long")
+        old_k, old_v = kv.k.clone(), kv.v.clone()
+        kv.write(0, k[:m], v[:m], seqs, rows)
+        first_k, first_v = kv.k.clone(), kv.v.clone()
+        kv.write(0, v[:m], k[:m], seqs, rows)  # does nothing while the failure is pending
+        with pytest.raises(bec.MoeError, match="MOE_ERR_ARG" if kind == "id" else "MOE_ERR_STATE"):
+            kv.check_errors()
+        kv.check_errors()
+        good = torch.arange(n, device="cuda") != bad
+        src = rows[:n].long()[good]
+        old_k[0, pages[good], :, 0], old_v[0, pages[good], :, 0] = k[src], v[src]
+        assert torch.equal(first_k, old_k) and torch.equal(first_v, old_v)
+        assert torch.equal(kv.k, old_k) and torch.equal(kv.v, old_v)
+
+
 def test_decode_step_in_a_graph_on_another_stream(bec):
     """reserve, write and attention captured once and replayed as the sequences grow."""
     dtype, hkv, hq, D, page = BF16, 2, 8, 64, 16
