@@ -528,8 +528,14 @@ __global__ void __launch_bounds__(256)
     lo = next;
   }
   if (stop) return;
+  // tokens that the rows do not reach (of a chunk that no row is in, too)
+  if (row == 0 && __ldg(cu + n) > n_rows) record(MOE_DEVERR_BADIDX);
   const int r0 = __ldg(cu + lo), r1 = __ldg(cu + lo + 1);
   if (row < r0 || row >= r1) return;
+  if (r0 < 0 || r1 > n_rows) {  // none of such a chunk is written
+    record(MOE_DEVERR_BADIDX);
+    return;
+  }
   const int s = seqs ? __ldg(seqs + lo) : lo;
   if (s < 0 || s >= kv.S) {
     record(MOE_DEVERR_BADIDX);

@@ -87,9 +87,9 @@ moe_status_t moe_kv_reserve(const moe_kv_t* kv, const int32_t* seqs, const int32
  * k_new, v_new: device [n_rows][n_kv_heads][head_dim] of the cache's dtype,
  * rows ldk and ldv elements apart (a slice of a fused projection), rows
  * 16-byte aligned; cu: device int32 [n+1]; rows outside cu[0] .. cu[n]-1 belong
- * to no sequence and are ignored. A chunk longer than its sequence and a token
- * whose page is shared are not written (an error is recorded); the others of
- * the call are. */
+ * to no sequence and are ignored. A chunk longer than its sequence or not wholly
+ * within the n_rows rows and a token whose page is shared are not written (an
+ * error is recorded); the others of the call are. Without rows cu is not read. */
 moe_status_t moe_kv_write(const moe_kv_t* kv, int32_t layer, const void* k_new, int64_t ldk, const void* v_new,
                           int64_t ldv, const int32_t* seqs, const int32_t* cu, int32_t n, int32_t n_rows,
                           moe_stream_t stream);

@@ -828,6 +828,30 @@ def test_write_leaves_out_what_is_wrong_and_writes_the_rest(bec, n, where, kind)
         assert torch.equal(kv.k, old_k) and torch.equal(kv.v, old_v)
 
 
+@pytest.mark.parametrize("cu", [[0, 20, 41], [0, 20, 30, 50], [0, 20, 40, 45], [-1, 20, 40],
+                                [0, 40, 2 ** 31 - 1]])
+def test_write_of_chunks_that_pass_the_rows(bec, cu):
+    """40 rows; chunks that need more are left as they were and recorded, the others are written."""
+    n = len(cu) - 1
+    kv = bec.KvCache.empty(1, 40, 1, 16, 8, n, 8)
+    seqs = i32(range(n))
+    kv.reserve(seqs, i32([60] * n))
+    kv.check_errors()
+    k, v = randn((40, 1, 8), BF16, gen(1)), randn((40, 1, 8), BF16, gen(2))
+    ref_k, ref_v = kv.k.clone(), kv.v.clone()
+    kv.write(0, k, v, seqs, i32(cu))
+    with pytest.raises(bec.MoeError, match="MOE_ERR_ARG"):
+        kv.check_errors()
+    for b in range(n):
+        if cu[b] < 0 or cu[b + 1] > 40:
+            continue
+        for r in range(cu[b], cu[b + 1]):
+            t = 60 - (cu[b + 1] - r)
+            p = kv.table[b, t // 16].item()
+            ref_k[0, p, :, t % 16], ref_v[0, p, :, t % 16] = k[r], v[r]
+    assert torch.equal(kv.k, ref_k) and torch.equal(kv.v, ref_v)
+
+
 def test_decode_step_in_a_graph_on_another_stream(bec):
     """reserve, write and attention captured once and replayed as the sequences grow."""
     dtype, hkv, hq, D, page = BF16, 2, 8, 64, 16
