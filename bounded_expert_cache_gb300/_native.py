@@ -136,6 +136,7 @@ SIGNATURES = [
     ("moe_attn_decode", _st, [_kv, _i32, _vp, _i64, _vp, _i32, _i32, _i32, C.c_float, _i32, _i32, _vp, _i64, _vp]),
     ("moe_attn_prefill", _st, [_kv, _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, C.c_float, _i32, _i32, _vp, _i64,
                                _vp]),
+    ("moe_debug_attn_wait_timeout", _st, [_i64, _i32]),
     ("moe_quant_linear", _st, [_vp, _i32, _i32, _i32, _vp, _i32, _i64, _i32, _vp, _vp, _i32, _i64, _vp]),
 ]
 

@@ -774,7 +774,7 @@ struct Ring {
 template <class E, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, AttnArgs a,
-                int boxes, long long wait_cycles) {
+                int boxes) {
   constexpr int NS = Ring<E>::kSlots;
   static_assert(NS >= 3, "ring");
   constexpr int KT = E::KT, R = E::kRows;
@@ -894,8 +894,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = KT >> shift;
     RingPos rp;
     uint32_t n = 0;  // tiles issued
+    const uint32_t most = a.copies;
     bool ok = true;
-    while (ok) {
+    while (ok && n < most) {
       const int tok = cp.sp.tile(cp.t) * KT + (lane << shift);
       bool need = lane < per && tok < cp.sp.end && (tok < a.sinks || tok + (1 << shift) > cp.sp.low);
       int page = 0;
@@ -912,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const uint32_t full = su32(&b_full[rp.s]);
-        if (n >= NS && !mbar_wait(su32(&b_empty[rp.s]), rp.ph ^ 1u, &s_abort, a.err, wait_cycles)) ok = false;
+        if (n >= NS && !mbar_wait(su32(&b_empty[rp.s]), rp.ph ^ 1u, &s_abort, a.err, a.wait_cycles)) ok = false;
         ok = __all_sync(~0u, ok);
         if (!ok) break;
         if (lane == 0) mbar_expect_tx(full, bytes);  // without pages the barrier completes by this arrival
@@ -934,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // drain: copies in flight land before the CTA ends
     if (lane == 0)
       for (uint32_t j = 0; j < n && j < NS; ++j)
-        mbar_drain(su32(&b_full[(n - 1 - j) % NS]), ((n - 1 - j) / NS) & 1u, a.err, wait_cycles);
+        mbar_drain(su32(&b_full[(n - 1 - j) % NS]), ((n - 1 - j) / NS) & 1u, a.err, kPrefillWaitCycles);
     return;
   }
 
@@ -949,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Tile tile;
   tile.shift = shift;
   auto wait_tile = [&]() {
-    mbar_wait(su32(&b_full[rp.s]), rp.ph, &s_abort, a.err, wait_cycles);
+    mbar_wait(su32(&b_full[rp.s]), rp.ph, &s_abort, a.err, a.wait_cycles);
     tile.base = ring + rp.s * E::kTileBytes;
   };
   auto free_tile = [&]() {
@@ -1084,7 +1085,7 @@ cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
   constexpr int smem = Ring<E>::kSmem;
   e = cudaFuncSetAttribute(attn_kernel<E, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attn_kernel<E, SPLIT><<<grid, kThreads, smem, st>>>(mk, mv, a, boxes, kPrefillWaitCycles);
+  attn_kernel<E, SPLIT><<<grid, kThreads, smem, st>>>(mk, mv, a, boxes);
   return cudaGetLastError();
 }
 

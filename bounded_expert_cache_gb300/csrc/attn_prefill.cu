@@ -321,8 +321,8 @@ __device__ __noinline__ void zero_nonfinite(uint32_t rows) {
 
 template <int DP, bool APART>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, AttnArgs a,
-                   long long wait_cycles) {
+    prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, AttnArgs a) {
+  const long long wait_cycles = a.wait_cycles;
   using C = Cfg<DP, APART>;
   extern __shared__ __align__(1024) unsigned char smraw[];
   const uint32_t sbase = su32(smraw);
@@ -480,10 +480,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int boxr = min(1 << a.page_shift, kKT), per = kKT / boxr;
     RingPos kp, vp;
     uint32_t nk = 0, nv = 0;  // tiles issued
+    const uint32_t most = a.copies;
     bool ok = true;
     while (ok) {
       const int32_t* row = a.table + static_cast<int64_t>(w.s.id) * a.max_pages;
-      for (int i = 0; i < w.nt && ok; ++i) {
+      for (int i = 0; i < w.nt && ok && nk < most; ++i) {
         const int tok = w.sp.tile(w.t0 + i) * kKT + lane * boxr;
         bool need = lane < per && tok < w.sp.end && (tok < a.sinks || tok + boxr > w.sp.low);
         int page = 0;
@@ -518,16 +519,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           rp.next(slots);
         }
       }
-      if (*abort_flag) ok = false;
+      if (*abort_flag || nk >= most) ok = false;
       ok = __all_sync(~0u, ok) && w.more();
       if (ok) next_segment(a, w);
     }
     // drain: copies in flight land before the CTA ends
     if (lane == 0) {
       for (uint32_t j = 0; j < nk && j < C::kKS; ++j)
-        mbar_drain(su32(&sh.kf[(nk - 1 - j) % C::kKS]), ((nk - 1 - j) / C::kKS) & 1u, a.err, wait_cycles);
+        mbar_drain(su32(&sh.kf[(nk - 1 - j) % C::kKS]), ((nk - 1 - j) / C::kKS) & 1u, a.err, kPrefillWaitCycles);
       for (uint32_t j = 0; j < nv && j < C::kVS; ++j)
-        mbar_drain(su32(&sh.vf[(nv - 1 - j) % C::kVS]), ((nv - 1 - j) / C::kVS) & 1u, a.err, wait_cycles);
+        mbar_drain(su32(&sh.vf[(nv - 1 - j) % C::kVS]), ((nv - 1 - j) / C::kVS) & 1u, a.err, kPrefillWaitCycles);
     }
   } else if (warp == 9) {
     // ---------------- MMA issue, by one elected thread: elect.sync under a
@@ -623,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // drain: every MMA issued here is done before tensor memory is released
       umma_commit(su32(&sh.drain));
-      mbar_drain(su32(&sh.drain), 0, a.err, wait_cycles);
+      mbar_drain(su32(&sh.drain), 0, a.err, kPrefillWaitCycles);
     }
   } else if (warp >= 10) {
     // ---------------- Q of row tile t, and the check of half of every V tile
@@ -1077,7 +1078,7 @@ cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t st) {
     return e;
   e = cudaFuncSetAttribute(prefill_kernel<DP, APART>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<DP, APART>);
   if (e != cudaSuccess) return e;
-  prefill_kernel<DP, APART><<<num_sms, kThreads, kSmem<DP, APART>, st>>>(mk, mv, a, kPrefillWaitCycles);
+  prefill_kernel<DP, APART><<<num_sms, kThreads, kSmem<DP, APART>, st>>>(mk, mv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (!may_need_join(a, num_sms)) return cudaSuccess;
   return pdl_launch(prefill_join_kernel<DP>, dim3(num_sms, 2 * DP / kJoinCols), dim3(kQT * kJoinGroups), 0, st, a);

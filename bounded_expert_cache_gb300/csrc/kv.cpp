@@ -5,8 +5,16 @@
 #include <string>
 
 #include "kv.h"
+#include "prefill.h"
 
 namespace {
+
+// Test hook of the attention kernels' bounded waits, for this thread's next call.
+struct WaitHook {
+  int64_t wait_cycles = 0;
+  int32_t copies = -1;
+};
+thread_local WaitHook t_hook;
 
 moe_status_t fail(moe_status_t st, const char* call, const std::string& why) {
   moe::set_thread_error(std::string(call) + ": " + why);
@@ -140,6 +148,9 @@ moe_status_t attention(const char* call, bool decode, const moe_kv_t* kv, int32_
   a.tickets = reinterpret_cast<unsigned int*>(w + l.tickets);
   a.cuts = reinterpret_cast<moe::Cut*>(w + l.cuts);
   a.err = &reinterpret_cast<moe::KvWork*>(w)->err;
+  a.copies = static_cast<uint32_t>(t_hook.copies);
+  a.wait_cycles = t_hook.wait_cycles > 0 ? t_hook.wait_cycles : moe::kPrefillWaitCycles;
+  t_hook = WaitHook{};
   return launched(call, decode ? moe::launch_attn_decode(a, kv->dtype, sms, stream)
                                : moe::launch_attn_prefill(a, kv->dtype, rows, sms, stream));
 }
@@ -204,8 +215,9 @@ extern "C" moe_status_t moe_kv_check_errors(const moe_kv_t* kv, moe_stream_t str
     if (e != cudaSuccess) return cuda_fail(call, e);
     const uint32_t err = head.err | static_cast<uint32_t>(head.late);
     if (err & MOE_DEVERR_TIMEOUT) {
-      // units left unjoined have left their tickets behind
+      // units left unjoined have left their tickets behind; gone before the return, for whichever stream is next
       e = cudaMemsetAsync(static_cast<char*>(kv->work) + l.tickets, 0, sms * moe::kPrefillTickets * 4, stream);
+      if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
       if (e != cudaSuccess) return cuda_fail(call, e);
       return fail(MOE_ERR_TIMEOUT, call, "a bounded device wait ran out");
     }
@@ -215,6 +227,15 @@ extern "C" moe_status_t moe_kv_check_errors(const moe_kv_t* kv, moe_stream_t str
     if (err & MOE_DEVERR_CAPACITY) return fail(MOE_ERR_CAPACITY, call, "too few free pages, or a table row too short");
     if (err & moe::KV_DEVERR_SHARED)
       return fail(MOE_ERR_STATE, call, "a write to a shared page or past a sequence's length");
+    return MOE_OK;
+  });
+}
+
+extern "C" moe_status_t moe_debug_attn_wait_timeout(int64_t wait_cycles, int32_t copies) {
+  return guarded([&] {
+    if (wait_cycles < 0 || copies < -1)
+      return fail(MOE_ERR_ARG, "moe_debug_attn_wait_timeout", "wait_cycles < 0 or copies < -1");
+    t_hook = WaitHook{copies >= 0 ? wait_cycles : 0, copies};
     return MOE_OK;
   });
 }

@@ -62,6 +62,8 @@ struct AttnArgs {
   uint32_t* err;
   int32_t row_tiles;    // row tiles a sequence and cache head (decode)
   bool wide_out;        // rows of out are multiples of 32 bytes, 32-byte aligned
+  int64_t wait_cycles;  // limit of a wait on a barrier
+  uint32_t copies;      // test hook: K and V tiles that a CTA copies before it stops; ~0: all
 };
 cudaError_t launch_attn_decode(const AttnArgs& a, int32_t dtype, int num_sms, cudaStream_t st);
 cudaError_t launch_attn_prefill(const AttnArgs& a, int32_t dtype, int32_t n_rows, int num_sms, cudaStream_t st);

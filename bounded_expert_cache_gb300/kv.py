@@ -154,6 +154,11 @@ class KvCache:
         """Synchronise, raise what kernels recorded on this cache, and clear it."""
         _ok(lib.moe_kv_check_errors(self._ref, self._st(stream)))
 
+    @staticmethod
+    def debug_attn_wait_timeout(wait_cycles: int, copies: int):
+        """The next attention call of this thread runs into its bounded waits (a test hook)."""
+        _ok(lib.moe_debug_attn_wait_timeout(wait_cycles, copies))
+
     def _q_out(self, q, out):
         """out (new if None) and the row strides of q and out."""
         ldq = _head_rows(q, "q", None, self._dim, self._dtype)

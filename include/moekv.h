@@ -140,6 +140,15 @@ moe_status_t moe_attn_prefill(const moe_kv_t* kv, int32_t layer, const void* q, 
                               const int32_t* cu, int32_t n, int32_t n_rows, int32_t n_heads, float scale,
                               int32_t window, int32_t sinks, void* out, int64_t ldo, moe_stream_t stream);
 
+/* Test hook of the attention kernels' bounded waits: the next moe_attn_decode
+ * or moe_attn_prefill of this thread (one launch; the hook then clears itself)
+ * limits its waits to wait_cycles SM clock cycles (0: the default, about 2 s),
+ * and every CTA stops copying after `copies` tiles of K and V (-1: off), so that
+ * the wait for a next one runs out. The kernel then drains what it did issue and
+ * ends, moe_kv_check_errors reports MOE_ERR_TIMEOUT, and the cache stays usable.
+ * No wait is removed and nothing faults. */
+moe_status_t moe_debug_attn_wait_timeout(int64_t wait_cycles, int32_t copies);
+
 /* y[t, n] = sum_k W[n, k] x[t, k] (+ bias[n]) for a 4-bit matrix W [N, K] in
  * the split-plane layout of one expert matrix: quant MOE_Q4_0 (K a multiple of
  * 32) or MOE_I4_G64 (K a multiple of 64), K below 2^25 and N below 2^31 - 512.

@@ -579,6 +579,43 @@ def test_attn_prefill_rows_without_any_sequence_are_refused(bec, D):
     kv.check_errors()
 
 
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+@pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 128), (BF16, 256), (F32, 96)])
+@pytest.mark.parametrize("copies,window", [(0, 0), (1, 200), (7, 0)])
+def test_attention_whose_wait_times_out_leaves_the_cache_usable(bec, kind, dtype, D, copies, window):
+    """Copies stop after 0, 1 or 7 tiles of a CTA, waits are limited to about 1 ms: an error, no fault; the same call then
+    succeeds, twice, so nothing of the first is left in the scratch."""
+    lens, ms = ([60000, 3, 700], [8, 8, 8]) if kind == "decode" else ([6000, 3, 700], [6000, 3, 500])
+    pool = Pool(bec, lens, 64, 2, D, dtype, 71)
+    q = randn((sum(ms), 8, D), dtype, gen(72))
+    cu = i32([0, ms[0], ms[0] + ms[1], sum(ms)])
+
+    def call():
+        if kind == "decode":
+            return pool.kv.attn_decode(1, q, pool.seqs, 8, window=window, sinks=4)
+        return pool.kv.attn_prefill(1, q, pool.seqs, cu, window=window, sinks=4)
+
+    good = call()
+    pool.kv.check_errors()
+    pool.kv.debug_attn_wait_timeout(2_000_000, copies)
+    call()
+    with pytest.raises(bec.MoeError) as e:
+        pool.kv.check_errors()
+    assert e.value.status == 5  # MOE_ERR_TIMEOUT
+    for _ in range(2):
+        assert torch.equal(call(), good)
+        pool.kv.check_errors()
+    at = sum(ms[:2])
+    ref, tol = attn_ref(q[at:], pool.tok_k[2], pool.tok_v[2], lens[2], window, 4, D ** -0.5, dtype)
+    assert worst(good[at:], ref, tol) <= 1.0
+
+
+def test_attention_wait_hook_refusals(bec):
+    for args in ((-1, 0), (5, -2)):
+        with pytest.raises(bec.MoeError, match="copies"):
+            bec.KvCache.debug_attn_wait_timeout(*args)
+
+
 # ---------------------------------------------------------------- pages
 class Model:
     """The cache's bookkeeping on the host, page by page, with the tokens each page holds."""
