@@ -581,7 +581,7 @@ def test_attn_prefill_rows_without_any_sequence_are_refused(bec, D):
 
 @pytest.mark.parametrize("kind", ["decode", "prefill"])
 @pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 128), (BF16, 256), (F32, 96)])
-@pytest.mark.parametrize("copies,window", [(0, 0), (1, 200), (7, 0)])
+@pytest.mark.parametrize("copies,window", [(0, 0), (0, 200), (1, 0), (7, 0)])
 def test_attention_whose_wait_times_out_leaves_the_cache_usable(bec, kind, dtype, D, copies, window):
     """Copies stop after 0, 1 or 7 tiles of a CTA, waits are limited to about 1 ms: an error, no fault; the same call then
     succeeds, twice, so nothing of the first is left in the scratch."""
