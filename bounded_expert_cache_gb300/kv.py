@@ -15,6 +15,7 @@ from ._native import lib
 from .api import MoeError
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 # These calls take microseconds on the device, so the binding keeps its own
@@ -32,20 +33,42 @@ def _dtype_id(dtype: torch.dtype) -> int:
     raise TypeError(f"expected float32 or bfloat16 (got {dtype})")
 
 
-def _ints(t: torch.Tensor, name: str, n: Optional[int] = None) -> int:
+def _elsewhere(t: torch.Tensor, name: str, device: int):
+    """The error for a tensor that is not on the call's device."""
+    if not t.is_cuda:
+        return TypeError(f"{name} must be a CUDA tensor")
+    return ValueError(f"{name} must be on cuda:{device} (is on cuda:{t.get_device()})")
+
+
+def _run(device: int, fn, *args):
+    """The library launches on the current device: make it the tensors' one for the call."""
+    if _current_device() == device:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st != N.MOE_OK:
+        _ok(st)
+
+
+def _ints(t: torch.Tensor, name: str, device: int, n: Optional[int] = None) -> int:
     """Entries of an index list."""
-    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 1 or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous one-dimensional int32 CUDA tensor")
+    if t.get_device() != device:
+        raise _elsewhere(t, name, device)
     have = t.shape[0]
     if n is not None and have != n:
         raise ValueError(f"{name} must hold {n} entries (got {have})")
     return have
 
 
-def _head_rows(t: torch.Tensor, name: str, heads: Optional[int], dim: int, dtype: torch.dtype) -> int:
+def _head_rows(t: torch.Tensor, name: str, heads: Optional[int], dim: int, dtype: torch.dtype, device: int) -> int:
     """Row stride (elements) of [rows, heads, dim] whose rows are dense but may lie apart."""
-    if t.dtype != dtype or not t.is_cuda:
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be a {dtype} CUDA tensor")
+    if t.get_device() != device:
+        raise _elsewhere(t, name, device)
     shape = t.shape
     if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must be [rows, {heads if heads is not None else 'heads'}, {dim}] "
@@ -87,8 +110,7 @@ class KvCache:
         self._device = k.device.index
         self._kv_heads, self._dim, self._dtype = Hkv, D, k.dtype
         n = C.c_int64()
-        with torch.cuda.device(k.device):
-            _ok(lib.moe_kv_work_bytes(self._ref, C.byref(n)))
+        _run(self._device, lib.moe_kv_work_bytes, self._ref, C.byref(n))
         self.work = torch.zeros(n.value, dtype=torch.uint8, device=k.device)
         self.raw.work, self.raw.work_bytes = self.work.data_ptr(), n.value
 
@@ -113,46 +135,46 @@ class KvCache:
 
     def fork(self, src, dst, stream=None):
         """dst[i] becomes a sequence of src[i]'s tokens, sharing its pages."""
-        n = _ints(src, "src")
-        _ints(dst, "dst", n)
-        _ok(lib.moe_kv_fork(self._ref, src.data_ptr(), dst.data_ptr(), n, self._st(stream)))
+        n = _ints(src, "src", self._device)
+        _ints(dst, "dst", self._device, n)
+        _run(self._device, lib.moe_kv_fork, self._ref, src.data_ptr(), dst.data_ptr(), n, self._st(stream))
 
     def reserve(self, seqs, n_new, stream=None):
         """Pages for n_new[i] more tokens of seqs[i]; their lengths grow by it."""
-        n = _ints(seqs, "seqs")
-        _ints(n_new, "n_new", n)
-        _ok(lib.moe_kv_reserve(self._ref, seqs.data_ptr(), n_new.data_ptr(), n, self._st(stream)))
+        n = _ints(seqs, "seqs", self._device)
+        _ints(n_new, "n_new", self._device, n)
+        _run(self._device, lib.moe_kv_reserve, self._ref, seqs.data_ptr(), n_new.data_ptr(), n, self._st(stream))
 
     def write(self, layer, k, v, seqs, cu, stream=None):
         """Rows cu[i]..cu[i+1]-1 of k and v [rows, kv_heads, head_dim] become the newest tokens of seqs[i]."""
-        n = _ints(seqs, "seqs")
-        _ints(cu, "cu", n + 1)
-        ldk = _head_rows(k, "k", self._kv_heads, self._dim, self._dtype)
-        ldv = _head_rows(v, "v", self._kv_heads, self._dim, self._dtype)
+        n = _ints(seqs, "seqs", self._device)
+        _ints(cu, "cu", self._device, n + 1)
+        ldk = _head_rows(k, "k", self._kv_heads, self._dim, self._dtype, self._device)
+        ldv = _head_rows(v, "v", self._kv_heads, self._dim, self._dtype, self._device)
         rows = k.shape[0]
         if rows != v.shape[0]:
             raise ValueError("k and v must have as many rows")
-        _ok(lib.moe_kv_write(self._ref, layer, k.data_ptr(), ldk, v.data_ptr(), ldv, seqs.data_ptr(), cu.data_ptr(), n,
-                             rows, self._st(stream)))
+        _run(self._device, lib.moe_kv_write, self._ref, layer, k.data_ptr(), ldk, v.data_ptr(), ldv, seqs.data_ptr(),
+             cu.data_ptr(), n, rows, self._st(stream))
 
     def free(self, seqs, stream=None):
         """Drop sequences; pages that no other sequence names become free."""
-        n = _ints(seqs, "seqs")
-        _ok(lib.moe_kv_free(self._ref, seqs.data_ptr(), n, self._st(stream)))
+        n = _ints(seqs, "seqs", self._device)
+        _run(self._device, lib.moe_kv_free, self._ref, seqs.data_ptr(), n, self._st(stream))
 
     def compact(self, stream=None):
         """Move the pages in use to the lowest ids."""
-        _ok(lib.moe_kv_compact(self._ref, self._st(stream)))
+        _run(self._device, lib.moe_kv_compact, self._ref, self._st(stream))
 
     def copy_pages(self, src, dst, stream=None):
         """Copy whole pages src[i] -> dst[i] in every layer; table and ref are untouched."""
-        n = _ints(src, "src")
-        _ints(dst, "dst", n)
-        _ok(lib.moe_kv_copy_pages(self._ref, src.data_ptr(), dst.data_ptr(), n, self._st(stream)))
+        n = _ints(src, "src", self._device)
+        _ints(dst, "dst", self._device, n)
+        _run(self._device, lib.moe_kv_copy_pages, self._ref, src.data_ptr(), dst.data_ptr(), n, self._st(stream))
 
     def check_errors(self, stream=None):
         """Synchronise, raise what kernels recorded on this cache, and clear it."""
-        _ok(lib.moe_kv_check_errors(self._ref, self._st(stream)))
+        _run(self._device, lib.moe_kv_check_errors, self._ref, self._st(stream))
 
     @staticmethod
     def debug_attn_wait_timeout(wait_cycles: int, copies: int):
@@ -161,34 +183,33 @@ class KvCache:
 
     def _q_out(self, q, out):
         """out (new if None) and the row strides of q and out."""
-        ldq = _head_rows(q, "q", None, self._dim, self._dtype)
+        ldq = _head_rows(q, "q", None, self._dim, self._dtype, self._device)
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         elif out.shape != q.shape:
             raise ValueError("out must have q's shape")
-        return out, ldq, _head_rows(out, "out", None, self._dim, self._dtype)
+        return out, ldq, _head_rows(out, "out", None, self._dim, self._dtype, self._device)
 
     def attn_decode(self, layer, q, seqs, n_q=1, out=None, scale=None, window=0, sinks=0, stream=None):
         """Attention of the newest n_q tokens of each sequence: q [len(seqs) * n_q, heads, head_dim]."""
-        n = _ints(seqs, "seqs")
+        n = _ints(seqs, "seqs", self._device)
         out, ldq, ldo = self._q_out(q, out)
         rows, heads, dim = q.shape
         if rows != n * n_q:
             raise ValueError(f"q must have {n} x {n_q} rows (got {rows})")
-        _ok(lib.moe_attn_decode(self._ref, layer, q.data_ptr(), ldq, seqs.data_ptr(), n, n_q, heads,
-                                1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(), ldo,
-                                self._st(stream)))
+        _run(self._device, lib.moe_attn_decode, self._ref, layer, q.data_ptr(), ldq, seqs.data_ptr(), n, n_q, heads,
+             1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(), ldo, self._st(stream))
         return out
 
     def attn_prefill(self, layer, q, seqs, cu, out=None, scale=None, window=0, sinks=0, stream=None):
         """Attention of chunks: rows cu[i]..cu[i+1]-1 of q are the newest tokens of seqs[i]."""
-        n = _ints(seqs, "seqs")
-        _ints(cu, "cu", n + 1)
+        n = _ints(seqs, "seqs", self._device)
+        _ints(cu, "cu", self._device, n + 1)
         out, ldq, ldo = self._q_out(q, out)
         rows, heads, dim = q.shape
-        _ok(lib.moe_attn_prefill(self._ref, layer, q.data_ptr(), ldq, seqs.data_ptr(), cu.data_ptr(), n, rows, heads,
-                                 1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(), ldo,
-                                 self._st(stream)))
+        _run(self._device, lib.moe_attn_prefill, self._ref, layer, q.data_ptr(), ldq, seqs.data_ptr(), cu.data_ptr(), n,
+             rows, heads, 1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(), ldo,
+             self._st(stream))
         return out
 
 
@@ -205,18 +226,19 @@ def quant_linear(x: torch.Tensor, w: torch.Tensor, quant: int, n_out: int, bias:
         raise ValueError("x must be a [T, K] CUDA tensor with dense rows")
     T, K = x.shape
     xt = _dtype_id(x.dtype)
-    if w.dtype != torch.uint8 or not w.is_cuda or not w.is_contiguous() or w.numel() != n_out * K * 9 // 16:
-        raise ValueError(f"w must be {n_out * K * 9 // 16} contiguous uint8 CUDA bytes")
-    if bias is not None and (bias.dtype != torch.float32 or not bias.is_cuda or not bias.is_contiguous()
+    device = x.get_device()
+    if w.dtype != torch.uint8 or w.get_device() != device or not w.is_contiguous() or w.numel() != n_out * K * 9 // 16:
+        raise ValueError(f"w must be {n_out * K * 9 // 16} contiguous uint8 CUDA bytes on x's device")
+    if bias is not None and (bias.dtype != torch.float32 or bias.get_device() != device or not bias.is_contiguous()
                              or bias.numel() != n_out):
-        raise ValueError(f"bias must be a contiguous float32 CUDA tensor of {n_out} entries")
+        raise ValueError(f"bias must be a contiguous float32 CUDA tensor of {n_out} entries on x's device")
     if y is None:
         y = torch.empty((T, n_out), dtype=x.dtype, device=x.device)
-    elif y.shape != (T, n_out) or not y.is_cuda or (n_out > 1 and y.stride(1) != 1):
-        raise ValueError(f"y must be a [{T}, {n_out}] CUDA tensor with dense rows")
+    elif y.shape != (T, n_out) or y.get_device() != device or (n_out > 1 and y.stride(1) != 1):
+        raise ValueError(f"y must be a [{T}, {n_out}] CUDA tensor with dense rows on x's device")
     ldx = x.stride(0) if T > 1 else max(x.stride(0), K)
     ldy = y.stride(0) if T > 1 else max(y.stride(0), n_out)
-    _ok(lib.moe_quant_linear(w.data_ptr(), quant, n_out, K, x.data_ptr(), xt, ldx, T,
-                             None if bias is None else bias.data_ptr(), y.data_ptr(), _dtype_id(y.dtype), ldy,
-                             _raw_stream(x.device.index) if stream is None else stream.cuda_stream))
+    _run(device, lib.moe_quant_linear, w.data_ptr(), quant, n_out, K, x.data_ptr(), xt, ldx, T,
+         None if bias is None else bias.data_ptr(), y.data_ptr(), _dtype_id(y.dtype), ldy,
+         _raw_stream(device) if stream is None else stream.cuda_stream)
     return y
