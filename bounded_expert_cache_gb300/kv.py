@@ -51,6 +51,15 @@ def _run(device: int, fn, *args):
         _ok(st)
 
 
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A result of a call on `stream`, from that stream's memory: a block that other streams' work may still use
+    must not be written by this one."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _ints(t: torch.Tensor, name: str, device: int, n: Optional[int] = None) -> int:
     """Entries of an index list."""
     if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
@@ -87,6 +96,10 @@ class KvCache:
     [max_seqs]; ref: int32 [pages]) or, with :meth:`empty`, over new ones.
     Sequence ids are rows of ``table``; every list of them is an int32 CUDA
     tensor, so that a captured step can be replayed with other contents.
+
+    Calls run on the current stream, or on ``stream``; a result that a call
+    makes itself is then that stream's. Inputs have to be ready there, and they
+    and the cache have to live until the call has run.
     """
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor):
@@ -113,6 +126,10 @@ class KvCache:
         _run(self._device, lib.moe_kv_work_bytes, self._ref, C.byref(n))
         self.work = torch.zeros(n.value, dtype=torch.uint8, device=k.device)
         self.raw.work, self.raw.work_bytes = self.work.data_ptr(), n.value
+        # the scratch is the cache's own: zero before a first call on whichever stream
+        with torch.cuda.device(k.device):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
 
     def _st(self, stream) -> int:
         return _raw_stream(self._device) if stream is None else stream.cuda_stream
@@ -181,11 +198,11 @@ class KvCache:
         """The next attention call of this thread runs into its bounded waits (a test hook)."""
         _ok(lib.moe_debug_attn_wait_timeout(wait_cycles, copies))
 
-    def _q_out(self, q, out):
+    def _q_out(self, q, out, stream):
         """out (new if None) and the row strides of q and out."""
         ldq = _head_rows(q, "q", None, self._dim, self._dtype, self._device)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = _new(q.shape, q.dtype, q.device, stream)
         elif out.shape != q.shape:
             raise ValueError("out must have q's shape")
         return out, ldq, _head_rows(out, "out", None, self._dim, self._dtype, self._device)
@@ -193,7 +210,7 @@ class KvCache:
     def attn_decode(self, layer, q, seqs, n_q=1, out=None, scale=None, window=0, sinks=0, stream=None):
         """Attention of the newest n_q tokens of each sequence: q [len(seqs) * n_q, heads, head_dim]."""
         n = _ints(seqs, "seqs", self._device)
-        out, ldq, ldo = self._q_out(q, out)
+        out, ldq, ldo = self._q_out(q, out, stream)
         rows, heads, dim = q.shape
         if rows != n * n_q:
             raise ValueError(f"q must have {n} x {n_q} rows (got {rows})")
@@ -205,7 +222,7 @@ class KvCache:
         """Attention of chunks: rows cu[i]..cu[i+1]-1 of q are the newest tokens of seqs[i]."""
         n = _ints(seqs, "seqs", self._device)
         _ints(cu, "cu", self._device, n + 1)
-        out, ldq, ldo = self._q_out(q, out)
+        out, ldq, ldo = self._q_out(q, out, stream)
         rows, heads, dim = q.shape
         _run(self._device, lib.moe_attn_prefill, self._ref, layer, q.data_ptr(), ldq, seqs.data_ptr(), cu.data_ptr(), n,
              rows, heads, 1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(), ldo,
@@ -233,7 +250,7 @@ def quant_linear(x: torch.Tensor, w: torch.Tensor, quant: int, n_out: int, bias:
                              or bias.numel() != n_out):
         raise ValueError(f"bias must be a contiguous float32 CUDA tensor of {n_out} entries on x's device")
     if y is None:
-        y = torch.empty((T, n_out), dtype=x.dtype, device=x.device)
+        y = _new((T, n_out), x.dtype, x.device, stream)
     elif y.shape != (T, n_out) or y.get_device() != device or (n_out > 1 and y.stride(1) != 1):
         raise ValueError(f"y must be a [{T}, {n_out}] CUDA tensor with dense rows on x's device")
     ldx = x.stride(0) if T > 1 else max(x.stride(0), K)

@@ -889,6 +889,63 @@ def test_write_of_chunks_that_pass_the_rows(bec, cu):
     assert torch.equal(kv.k, ref_k) and torch.equal(kv.v, ref_v)
 
 
+@pytest.mark.parametrize("call", ["decode", "prefill", "linear"])
+def test_new_results_are_of_the_calls_stream(bec, call):
+    """Memory that the current stream has yet to read is not written by a call on another one."""
+    pool = Pool(bec, [50] * 256, 16, 8, 128, BF16, 1)
+    q = randn((256, 64, 128), BF16, gen(1))
+    w, _ = pack(8192, 64, Q4_0, gen(2))
+    x = randn((256, 64), BF16, gen(3))
+    cu, side = i32(range(257)), torch.cuda.Stream()
+
+    def run():
+        if call == "decode":
+            return pool.kv.attn_decode(1, q, pool.seqs, stream=side)
+        if call == "prefill":
+            return pool.kv.attn_prefill(1, q, pool.seqs, cu, stream=side)
+        return bec.quant_linear(x, w, Q4_0, 8192, stream=side)
+
+    torch.cuda.synchronize()
+    run()  # a first launch loads the kernel, which waits for the device
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    # two blocks of the results' size; the second is free again at once as far as the current stream goes
+    was = torch.randn((256, 8192)).bfloat16()
+    copy = torch.empty(was.shape, dtype=BF16, device="cuda")
+    mine = torch.empty(was.shape, dtype=BF16, device="cuda")
+    mine.copy_(was)
+    torch.cuda._sleep(200_000_000)  # about 0.1 s
+    copy.copy_(mine)
+    del mine
+    out = run()
+    torch.cuda.synchronize()
+    assert torch.equal(copy.cpu(), was)
+    assert torch.isfinite(out).all()
+
+
+def test_scratch_is_zero_on_whichever_stream_comes_first(bec):
+    k = torch.zeros((1, 8, 1, 16, 64), dtype=BF16, device="cuda")
+    v, table = torch.zeros_like(k), torch.full((2, 4), -1, dtype=torch.int32, device="cuda")
+    lens, ref, seqs, new = i32([0, 0]), i32([0] * 8), i32([1]), i32([40])
+    side = torch.cuda.Stream()
+    kv = bec.KvCache(k, v, table, lens, ref)
+    n = kv.work.numel()
+    torch.cuda.synchronize()
+    kv.reserve(seqs, i32([0]), stream=side)  # a first launch loads the kernels, which waits for the device
+    torch.cuda.synchronize()
+    del kv
+    torch.cuda.empty_cache()
+    junk = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    del junk
+    torch.cuda._sleep(200_000_000)
+    kv = bec.KvCache(k, v, table, lens, ref)
+    kv.reserve(seqs, new, stream=side)
+    side.synchronize()
+    assert lens.tolist() == [0, 40] and table[1].tolist() == [0, 1, 2, -1]
+    kv.check_errors()
+
+
 def test_decode_step_in_a_graph_on_another_stream(bec):
     """reserve, write and attention captured once and replayed as the sequences grow."""
     dtype, hkv, hq, D, page = BF16, 2, 8, 64, 16
