@@ -85,7 +85,7 @@ def _head_rows(t: torch.Tensor, name: str, heads: Optional[int], dim: int, dtype
     rows, head, one = t.stride()
     if one != 1 or (shape[1] > 1 and head != dim):
         raise ValueError(f"the heads of a row of {name} must be dense")
-    return rows if shape[0] > 1 else max(rows, shape[1] * dim)
+    return rows if shape[0] > 1 else shape[1] * dim  # (a single row's stride leads nowhere)
 
 
 class KvCache:
@@ -253,8 +253,8 @@ def quant_linear(x: torch.Tensor, w: torch.Tensor, quant: int, n_out: int, bias:
         y = _new((T, n_out), x.dtype, x.device, stream)
     elif y.shape != (T, n_out) or y.get_device() != device or (n_out > 1 and y.stride(1) != 1):
         raise ValueError(f"y must be a [{T}, {n_out}] CUDA tensor with dense rows on x's device")
-    ldx = x.stride(0) if T > 1 else max(x.stride(0), K)
-    ldy = y.stride(0) if T > 1 else max(y.stride(0), n_out)
+    ldx = x.stride(0) if T > 1 else K
+    ldy = y.stride(0) if T > 1 else n_out
     _run(device, lib.moe_quant_linear, w.data_ptr(), quant, n_out, K, x.data_ptr(), xt, ldx, T,
          None if bias is None else bias.data_ptr(), y.data_ptr(), _dtype_id(y.dtype), ldy,
          _raw_stream(device) if stream is None else stream.cuda_stream)

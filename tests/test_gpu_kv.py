@@ -616,6 +616,28 @@ def test_attention_wait_hook_refusals(bec):
             bec.KvCache.debug_attn_wait_timeout(*args)
 
 
+def test_a_single_row_of_an_odd_stride(bec):
+    """The stride of a row that has no next one does not matter."""
+    pool = Pool(bec, [50], 16, 2, 64, BF16, 1)
+    wide = randn((3, 4 * 64 + 1), BF16, gen(1))
+    q = wide[:1, :256].unflatten(1, (4, 64))
+    out = torch.zeros((3, 259), dtype=BF16, device="cuda")[:1, :256].unflatten(1, (4, 64))
+    want = pool.kv.attn_decode(1, q.contiguous(), pool.seqs)
+    assert torch.equal(pool.kv.attn_decode(1, q, pool.seqs, out=out), want) and torch.equal(out, want)
+    assert torch.equal(pool.kv.attn_prefill(1, q, pool.seqs, i32([0, 1]), out=out), out)
+    check_attn(pool, q, out, [50], [1], 0, 0, 0.125)
+    rows = wide[:1, :128].unflatten(1, (2, 64))
+    pool.kv.write(1, rows, rows, pool.seqs, i32([0, 1]))
+    pool.kv.check_errors()
+    page = pool.table[pool.seqs[0], 3].item()
+    assert torch.equal(pool.kv.k[1, page, :, 1], rows[0]) and torch.equal(pool.kv.v[1, page, :, 1], rows[0])
+    w, (s, c, b) = pack(16, 64, Q4_0, gen(1))
+    x = randn((2, 67), BF16, gen(2))[:1, :64]
+    ref = x.double() @ (s * c).t()
+    assert worst(bec.quant_linear(x, w, Q4_0, 16), ref,
+                 U8 * ref.abs() * 1.01 + 200 * U24 * (x.double().abs() @ (s * c).abs().t())) <= 1
+
+
 # ---------------------------------------------------------------- pages
 class Model:
     """The cache's bookkeeping on the host, page by page, with the tokens each page holds."""
