@@ -40,6 +40,9 @@ def _elsewhere(t: torch.Tensor, name: str, device: int):
     return ValueError(f"{name} must be on cuda:{device} (is on cuda:{t.get_device()})")
 
 
+_MOST = 2 ** 31 - 1  # a window or a count of first tokens beyond it hides no more, and keeps no more, than this
+
+
 def _run(device: int, fn, *args):
     """The library launches on the current device: make it the tensors' one for the call."""
     if _current_device() == device:
@@ -215,7 +218,8 @@ class KvCache:
         if rows != n * n_q:
             raise ValueError(f"q must have {n} x {n_q} rows (got {rows})")
         _run(self._device, lib.moe_attn_decode, self._ref, layer, q.data_ptr(), ldq, seqs.data_ptr(), n, n_q, heads,
-             1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(), ldo, self._st(stream))
+             1.0 / math.sqrt(dim) if scale is None else scale, min(window, _MOST), min(sinks, _MOST), out.data_ptr(),
+             ldo, self._st(stream))
         return out
 
     def attn_prefill(self, layer, q, seqs, cu, out=None, scale=None, window=0, sinks=0, stream=None):
@@ -225,8 +229,8 @@ class KvCache:
         out, ldq, ldo = self._q_out(q, out, stream)
         rows, heads, dim = q.shape
         _run(self._device, lib.moe_attn_prefill, self._ref, layer, q.data_ptr(), ldq, seqs.data_ptr(), cu.data_ptr(), n,
-             rows, heads, 1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(), ldo,
-             self._st(stream))
+             rows, heads, 1.0 / math.sqrt(dim) if scale is None else scale, min(window, _MOST), min(sinks, _MOST),
+             out.data_ptr(), ldo, self._st(stream))
         return out
 
 

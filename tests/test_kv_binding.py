@@ -147,3 +147,13 @@ def test_linear_is_made_on_its_tensors_device(kvmod, world):
         with pytest.raises(ValueError, match=f"^{bad} must be"):
             kvmod.quant_linear(x, t["w"], 1, 16, bias=t["bias"], y=t["y"])
     assert len(world["lib"].calls) == 1
+
+
+@pytest.mark.parametrize("size", [2 ** 31, 2 ** 32 + 8, 2 ** 40])
+def test_windows_past_32_bits_are_not_cut_to_their_low_half(kvmod, world, size):
+    c = cache(kvmod, 0)
+    q, seqs, cu = Fake((3, 4, 64), torch.bfloat16), Fake((3,), torch.int32), Fake((4,), torch.int32)
+    c.attn_decode(0, q, seqs, out=q, window=size, sinks=size)
+    c.attn_prefill(0, q, seqs, cu, out=q, window=size, sinks=size)
+    for _, _, args in world["lib"].calls:
+        assert args.count(2 ** 31 - 1) == 2 and size not in args
