@@ -29,9 +29,12 @@
 // a unit ends. Waits are bounded; after a time-out (recorded as an error) the
 // loops run to their end on whatever is there, so no barrier is left waiting.
 // Measured, bf16: three contexts of 131,072 to 262,143 tokens, 8 heads of 128:
-// 353 us, 6.9 TB/s; 40 contexts of 40 to 32,768 tokens, 4 new tokens, 2 heads of
-// 256: 63 us, 4.6 TB/s (the fixed costs of 78 units); one of 777: 9 us, the
-// latency of the dependent loads and of the second launch.
+// 354 us, 6.9 TB/s; 40 contexts of 0 to 32,768 tokens, 4 new tokens, 2 heads of
+// 256: 65 us, 4.4 TB/s (the fixed costs of 78 units; 63 in a captured graph); one
+// of 777: 10 us (9 in a graph), the latency of the dependent loads and of the
+// second launch. Prompts here are not split, and run at the rate of warp-level
+// instructions or of the CUDA cores: 4,096 tokens at 32K, 16 heads of 256: 7.6 ms;
+// f32, 2,048 rows of 8,192 tokens, 8 heads of 80: 2.35 ms.
 #include <cuda.h>
 #include <cuda_bf16.h>
 

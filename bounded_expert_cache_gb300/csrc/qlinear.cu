@@ -10,10 +10,11 @@
 // a 4-bit integer and a bf16 are exact, sums are fp32, and the group's factor is
 // applied in fp32 to the 16 x 8 sums. An fp32 x is the exact sum of three bf16
 // (8 + 8 + 8 significand bits), one instruction each. Measured, 131,072 x 2,048
-// Q4_0 (151 MB, 22 us of HBM): 37 us for one token, 57 for 24, where the warps
-// issue in 56% of cycles, the tensor pipe works in 40% and shared memory in 56%;
-// 2,560 x 2,048 for one token: 3.5 us, the latency of a launch and of a few
-// dependent loads.
+// Q4_0 (151 MB, 22 us of HBM): 39 us for one token, 59 for 24 (57 in a captured
+// graph), where the warps issue in 55% of cycles, the tensor pipe works in 40% and
+// shared memory in 53%; 2,560 x 2,048 for one token: 3.6 us in a graph, the latency
+// of a launch and of a few dependent loads. Tokens past 24 go in blocks of 24 that
+// each unpack the matrix again: 4,096 tokens of the same take 370 us.
 //
 // The order of k within an instruction is free as long as A and B agree, so x
 // is stored in the order in which a lane's 4-byte word yields its eight codes:

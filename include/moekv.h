@@ -17,6 +17,10 @@
  * sequence s holds ceil(lens[s] / page_tokens) pages, named in order by the
  * leading entries of table[s]; its other entries are -1. ref[p] counts the
  * table entries that name page p; 0 means free. One table serves all layers.
+ * Only these calls change table, lens and ref of a cache in use: a length that
+ * the caller lowers leaves pages behind that the next reserve does not return.
+ *
+ * The cache's arrays and a call's tensors are on the current device.
  */
 #ifndef MOEKV_H
 #define MOEKV_H
@@ -155,10 +159,11 @@ moe_status_t moe_debug_attn_wait_timeout(int64_t wait_cycles, int32_t copies);
  * w: device, N*K/2 quant bytes followed by N*K/16 scale bytes; x: device [T, K],
  * rows ldx elements apart (xt MOE_F32 or MOE_BF16); y: device [T, N], rows ldy
  * apart (yt likewise); bias: device fp32 [N] or NULL. w and x rows 16-byte
- * aligned. Products are exact and sums
- * fp32 for both types of x, over a group before its scale is applied. An output
- * that is not finite is formed again weight by weight, so infinities and NaN in x
- * give what weight times x gives, and only the outputs' own sums can overflow.
+ * aligned. Products are exact and sums those of the matrix units in fp32 for both
+ * types of x, codes times x over a group and then its scale; where an affine
+ * group's codes and offset nearly cancel, the error is that of the parts. An
+ * output that is not finite is formed again weight by weight, so infinities and
+ * NaN in x give what weight times x gives, and only the outputs' own sums overflow.
  * Meant for few tokens; T is not bounded, T = 0 does nothing. */
 moe_status_t moe_quant_linear(const void* w, int32_t quant, int32_t N, int32_t K, const void* x, int32_t xt,
                               int64_t ldx, int32_t T, const float* bias, void* y, int32_t yt, int64_t ldy,
