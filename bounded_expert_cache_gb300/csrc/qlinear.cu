@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   // ldmatrix: lanes 0-7 and 8-15 address rows 0-7 and 8-15 of a group's piece, lanes 16-31 the next group's
   const uint32_t q_off = (lane & 15) * 128, q_phase = ((lane & 7) ^ (lane >> 4)) << 4, m_off = kCodeBytes + r * 16;
 
-  float probe = 0.f;  // NaN once an output is not finite
+  float probe = 0.f;  // NaN once a sum is not finite (a bias of -inf is no reason to form one again)
   auto store = [&](int n, int t, float v) {
     probe = fmaf(v, 0.f, probe);
     if (a.bias) v += __ldg(a.bias + n);
