@@ -18,6 +18,7 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_ARG", 2: "MOE_ERR_CUDA", 3: "MOE_ERR_CA
 Q8_0, Q4_0, I4_G64 = 0, 1, 2
 LRU, RANDOM, FARTHEST_NEXT_USE, STATIC_SET = 0, 1, 2, 3
 F32, BF16 = 0, 1
+KV_I4 = 16
 MODE_AUTO, MODE_DECODE, MODE_PREFILL = 0, 1, 2
 PREFETCH_OFF, PREFETCH_REFRESH, PREFETCH_PRESERVE = 0, 1, 2
 PREFETCH_ACTIONS = ("probe", "refresh", "load")
@@ -68,6 +69,10 @@ class KvT(C.Structure):
                 ("head_dim", C.c_int32), ("dtype", C.c_int32), ("max_seqs", C.c_int32), ("max_pages", C.c_int32)]
 
 
+class RotaryT(C.Structure):
+    _fields_ = [("turns", C.c_void_p), ("dim", C.c_int32), ("interleaved", C.c_int32), ("magnitude", C.c_float)]
+
+
 def _load():
     if not os.path.exists(_LIB_PATH):
         raise ImportError(
@@ -82,6 +87,8 @@ _vp, _i32, _i64, _u64, _sz = C.c_void_p, C.c_int32, C.c_int64, C.c_uint64, C.c_s
 _st = C.c_int  # moe_status_t
 
 _kv = C.POINTER(KvT)
+_rot = C.POINTER(RotaryT)
+_f64 = C.c_double
 
 # (name, restype, argtypes) for every symbol of include/moecache.h and include/moekv.h
 SIGNATURES = [
@@ -130,6 +137,12 @@ SIGNATURES = [
     ("moe_kv_fork", _st, [_kv, _vp, _vp, _i32, _vp]),
     ("moe_kv_reserve", _st, [_kv, _vp, _vp, _i32, _vp]),
     ("moe_kv_write", _st, [_kv, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _vp]),
+    ("moe_kv_write_rotary", _st, [_kv, _i32, _rot, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32,
+                                  _vp]),
+    ("moe_kv_read", _st, [_kv, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _vp]),
+    ("moe_rotary_angles", _st, [_i32, _f64, _f64, _i32, _f64, _f64, C.POINTER(_f64)]),
+    ("moe_rotary_turns", _st, [C.POINTER(_f64), _i32, C.POINTER(_u64)]),
+    ("moe_rotary", _st, [_rot, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _vp, _i64, _vp]),
     ("moe_kv_free", _st, [_kv, _vp, _i32, _vp]),
     ("moe_kv_compact", _st, [_kv, _vp]),
     ("moe_kv_copy_pages", _st, [_kv, _vp, _vp, _i32, _vp]),

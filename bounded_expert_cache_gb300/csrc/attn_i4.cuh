@@ -1,0 +1,434 @@
+// The engine of attention over pages of 4-bit codes, on warp-level matrix
+// instructions.
+//
+// A head of a page is an affine matrix of groups of 64 along the head: the value
+// of code q (0 to 15) of token t and group g is s_tg q + b_tg = s_tg (q - 8) +
+// b'_tg with b' = b + 8 s, so that for a query x and numerators p
+//   x.k_t   = sum_g s_tg (sum_d x_d (q_td - 8)) + b'_tg sum_d x_d
+//   sum_t p_t v_td = sum_t (p_t s_tg) (q_td - 8) + sum_t p_t b'_tg.
+// The matrix instructions multiply codes: q - 8 is exact in bf16, and so are its
+// products with a bf16 x. Scales and offsets are applied in fp32 to the scores of
+// a group, and to the numerators before they become an operand; the offsets' sums
+// stay in fp32. An f32 x, and an f32 call's p s, are multiplied as three bf16 that
+// add up to it. For bf16 calls p s is rounded to bf16 once, as p is over bf16
+// pages. Codes are centred because that rounding is multiplied by them: of q
+// itself it would carry 2.5 times the noise.
+//
+// The scores are formed transposed, S^T = K Q^T, so that a warp's 16 tokens are
+// the rows of the instruction and eight query rows its columns: eight heads that
+// share a cache head leave no row of the instruction empty. The values follow as
+// O^T = V^T P^T with P^T turned from one fragment layout to the other by
+// movmatrix. Which of a group's dimensions takes which place of a fragment is
+// free as long as both operands agree: a thread takes whole words of eight codes,
+// and nibbles i and i + 4 (K), or nibble i of two tokens (V), become a pair of
+// bf16 by one and-or into the mantissa of 128 and one subtraction.
+//
+// What a row does not see cannot reach it: hidden scores are -inf by selection,
+// and a hidden token's scale and offset, which may be anything, are left out of
+// its numerator's products by selection.
+#pragma once
+
+#include "attn_split.cuh"
+
+namespace moe {
+namespace {
+
+__device__ __forceinline__ void mma_codes(float* d, const uint32_t* a, const uint32_t* b) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// q - 8 of nibbles i and i + 4 as a pair of bf16: 128 + q has q as its last bits
+__device__ __forceinline__ uint32_t centred(uint32_t w, int i) {
+  const uint32_t m = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+  __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m), __floats2bfloat162_rn(136.f, 136.f));
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t m) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(m));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+  return r;
+}
+// scale and offset (for centred codes) of a metadata word
+__device__ __forceinline__ float scale_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float offset_of(uint32_t w) { return fmaf(8.f, scale_of(w), __uint_as_float(w & 0xFFFF0000u)); }
+// the bf16 parts of a pair: what is left after each is the next one's
+template <int N>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t* part) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    part[i] = pack_bf16(x, y);
+    if (i + 1 < N) {
+      x -= __uint_as_float(part[i] << 16);
+      y -= __uint_as_float(part[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+// G groups of 64 a head, 8 NR query rows, tiles of KT tokens of which each warp
+// takes every eighth 16.
+template <class T_, int G_, int NR_, int KT_>
+struct CodesEngine {
+  using T = T_;
+  static constexpr int G = G_, NR = NR_, KT = KT_;
+  static constexpr int DP = G == 1 ? 64 : (G == 2 ? 128 : 256);
+  static constexpr int kRows = 8 * NR, CH = KT / (16 * kWarps), NB = 1;
+  static constexpr int kParts = sizeof(T) == 4 ? 3 : 1;  // bf16 parts of an operand
+  static constexpr bool kCodes = true;
+  static constexpr int kRowBytes = 32 * G, kMetaBytes = 4 * G, kMostSlots = 12;
+  static constexpr uint32_t kTileBytes = KT * (kRowBytes + kMetaBytes);
+  static constexpr int kUnitCost = 3;
+  static constexpr int kSteps = 4 * G;  // products of 16 dimensions
+  // Q as fragments in registers, or in shared memory where there are too many
+  static constexpr bool kQInSmem = kSteps * NR * kParts > 32;
+  static constexpr int kQBytes = kQInSmem ? kSteps * NR * kParts * 256 : 0;
+  static constexpr int kMl = kWarps * kRows;
+  static constexpr int kMergeBytes = kWarps * kRows * 64 * 4 + kQBytes;
+  static_assert(CH >= 1 && CH * 16 * kWarps == KT, "token groups");
+
+  uint32_t qf[kQInSmem ? 1 : kParts * NR * kSteps][2];
+  uint32_t qs;           // shared copy of the fragments
+  float qsum[G][NR][2];  // sums of a group's x, of this thread's columns (query rows 8 nt + 2 c and + 1)
+  float o[4 * G][NR][4];
+  float bias[G][NR][2];  // this thread's share of the offsets' sums
+  float x[CH][NR][4];    // scores, then numerators: tokens r and r + 8, two columns each
+  uint32_t seen[CH];     // of an edge tile: bit 4 nt + i of x visible
+  float m[NR][2], thr[NR][2], l[NR][2];
+  int pos[NR][2];        // -1: no row
+  int lo_pos, hi_pos;    // of the unit's rows
+  bool edge;             // the tile holds a token seen by some but not all of the rows
+
+  __device__ __forceinline__ void place(float* buf) { qs = su32(buf) + kWarps * kRows * 64 * 4; }
+  __device__ __forceinline__ const uint32_t* fragment(int part, int nt, int step, uint32_t* tmp) const {
+    const int at = (part * NR + nt) * kSteps + step;
+    if constexpr (kQInSmem) {
+      const uint2 v = lds64(qs + at * 256 + (threadIdx.x & 31) * 8);
+      tmp[0] = v.x;
+      tmp[1] = v.y;
+      return tmp;
+    } else {
+      return qf[at];
+    }
+  }
+
+  __device__ __forceinline__ void begin(const AttnArgs& a, const Cursor& c) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, cc = lane & 3;
+    lo_pos = c.s.len - c.s.m + c.token(a, 0);
+    hi_pos = c.s.len - c.s.m + c.token(a, c.rows - 1);
+#pragma unroll
+    for (int nt = 0; nt < NR; ++nt) {
+      const int row = 8 * nt + r;
+      const T* q = nullptr;
+      if (row < c.rows)
+        q = static_cast<const T*>(a.q) + static_cast<int64_t>(c.s.row0 + c.token(a, row)) * a.ldq + c.head(a, row) * a.D;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          // eight dimensions; a product takes pairs (i, i + 4)
+          float v[8] = {};
+          if (q) {
+            const T* at = q + 64 * g + 16 * cc + 8 * w;
+            if constexpr (sizeof(T) == 4) {
+              const float4 u0 = __ldg(reinterpret_cast<const float4*>(at)), u1 = __ldg(reinterpret_cast<const float4*>(at) + 1);
+              v[0] = u0.x, v[1] = u0.y, v[2] = u0.z, v[3] = u0.w, v[4] = u1.x, v[5] = u1.y, v[6] = u1.z, v[7] = u1.w;
+            } else {
+              const uint4 u = __ldg(reinterpret_cast<const uint4*>(at));
+              const uint32_t us[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(us[i] << 16);
+                v[2 * i + 1] = __uint_as_float(us[i] & 0xFFFF0000u);
+              }
+            }
+          }
+          sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+          uint32_t pair[4][kParts];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) split_pair<kParts>(v[i], v[i + 4], pair[i]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int part = 0; part < kParts; ++part) {
+              const int at = (part * NR + nt) * kSteps + (g * 2 + w) * 2 + h;
+              if constexpr (kQInSmem) {
+                if (at % kWarps == warp)
+                  asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(qs + at * 256 + lane * 8), "r"(pair[2 * h][part]),
+                               "r"(pair[2 * h + 1][part])
+                               : "memory");
+              } else {
+                qf[at][0] = pair[2 * h][part];
+                qf[at][1] = pair[2 * h + 1][part];
+              }
+            }
+        }
+        sum += __shfl_xor_sync(~0u, sum, 1);
+        sum += __shfl_xor_sync(~0u, sum, 2);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          qsum[g][nt][e] = __shfl_sync(~0u, sum, 8 * cc + 4 * e);
+          bias[g][nt][e] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int col = 8 * nt + 2 * cc + e;
+        pos[nt][e] = col < c.rows ? c.s.len - c.s.m + c.token(a, col) : -1;
+        m[nt][e] = thr[nt][e] = -INFINITY;
+        l[nt][e] = 0.f;
+      }
+#pragma unroll
+      for (int t = 0; t < 4 * G; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[t][nt][i] = 0.f;
+    }
+    if constexpr (kQInSmem) sync_compute();
+  }
+
+  __device__ __forceinline__ void scores(const AttnArgs& a, const Cursor& c, const Tile& kt) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, cc = lane & 3;
+    const int tile0 = c.sp.tile(c.t) * KT;
+    edge = tile0 + KT - 1 > lo_pos || (a.window > 0 && hi_pos - tile0 >= a.window);
+#pragma unroll
+    for (int ch = 0; ch < CH; ++ch) {
+      const int key = (ch * kWarps + warp) * 16 + r;
+      const uint32_t at = kt.base + key * kRowBytes + 8 * cc, meta = kt.base + KT * kRowBytes + key * kMetaBytes;
+#pragma unroll
+      for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[ch][nt][i] = 0.f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const uint2 w0 = lds64(at + 32 * g), w1 = lds64(at + 8 * kRowBytes + 32 * g);
+        const uint32_t m0 = lds32(meta + 4 * g), m1 = lds32(meta + 8 * kMetaBytes + 4 * g);
+        float acc[NR][4] = {};
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t c0 = w ? w0.y : w0.x, c1 = w ? w1.y : w1.x;
+            const uint32_t k[4] = {centred(c0, 2 * h), centred(c1, 2 * h), centred(c0, 2 * h + 1), centred(c1, 2 * h + 1)};
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+              for (int part = 0; part < kParts; ++part) {
+                uint32_t tmp[2];
+                mma_codes(acc[nt], k, fragment(part, nt, (g * 2 + w) * 2 + h, tmp));
+              }
+          }
+        const float s0 = scale_of(m0), b0 = offset_of(m0), s1 = scale_of(m1), b1 = offset_of(m1);
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            x[ch][nt][e] += s0 * acc[nt][e] + b0 * qsum[g][nt][e];
+            x[ch][nt][2 + e] += s1 * acc[nt][2 + e] + b1 * qsum[g][nt][e];
+          }
+      }
+    }
+    if (edge) {
+#pragma unroll
+      for (int ch = 0; ch < CH; ++ch) {
+        seen[ch] = 0u;
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = tile0 + (ch * kWarps + warp) * 16 + r + 8 * (i >> 1);
+            const int back = pos[nt][i & 1] - j;
+            const bool see = back >= 0 && (a.window == 0 || back < a.window || j < a.sinks);
+            if (see)
+              seen[ch] |= 1u << (4 * nt + i);
+            else
+              x[ch][nt][i] = -INFINITY;
+          }
+      }
+    }
+    // m is raised only when a score passes it by 2^8: numerators up to there lose nothing
+    float mx[NR][2];
+    bool up = false;
+#pragma unroll
+    for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float v = fmaxf(x[0][nt][e], x[0][nt][2 + e]);
+#pragma unroll
+        for (int ch = 1; ch < CH; ++ch) v = fmaxf(v, fmaxf(x[ch][nt][e], x[ch][nt][2 + e]));
+        mx[nt][e] = v;
+        up |= v > thr[nt][e];
+      }
+    if (__any_sync(~0u, up)) {
+#pragma unroll
+      for (int nt = 0; nt < NR; ++nt) {
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float v = mx[nt][e];
+          v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
+          f[e] = 1.f;
+          if (v > thr[nt][e]) {
+            f[e] = ex2((m[nt][e] - v) * a.scale_log2);  // 0 for the first maximum
+            m[nt][e] = v;
+            thr[nt][e] = v + 8.f / a.scale_log2;
+          }
+          l[nt][e] *= f[e];
+#pragma unroll
+          for (int g = 0; g < G; ++g) bias[g][nt][e] *= f[e];
+        }
+#pragma unroll
+        for (int t = 0; t < 4 * G; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[t][nt][i] *= f[i & 1];
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float mc = m[nt][e] == -INFINITY ? 0.f : m[nt][e] * a.scale_log2;
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+          for (int i = e; i < 4; i += 2) {
+            x[ch][nt][i] = ex2(fmaf(x[ch][nt][i], a.scale_log2, -mc));
+            l[nt][e] += x[ch][nt][i];
+          }
+      }
+  }
+
+  __device__ __forceinline__ void values(const AttnArgs&, const Cursor&, const Tile& vt) {
+    if (edge)
+      add_values<true>(vt);
+    else
+      add_values<false>(vt);
+  }
+  template <bool EDGE>
+  __device__ __forceinline__ void add_values(const Tile& vt) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, cc = lane & 3;
+#pragma unroll
+    for (int ch = 0; ch < CH; ++ch) {
+      const int key0 = (ch * kWarps + warp) * 16;
+      const uint32_t meta = vt.base + KT * kRowBytes + (key0 + r) * kMetaBytes;
+      const uint32_t at = vt.base + (key0 + 2 * cc) * kRowBytes + 4 * r;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const uint32_t m0 = lds32(meta + 4 * g), m1 = lds32(meta + 8 * kMetaBytes + 4 * g);
+        const uint32_t w0 = lds32(at + 32 * g), w1 = lds32(at + kRowBytes + 32 * g);
+        const uint32_t w2 = lds32(at + 8 * kRowBytes + 32 * g), w3 = lds32(at + 9 * kRowBytes + 32 * g);
+        const float s[2] = {scale_of(m0), scale_of(m1)}, b[2] = {offset_of(m0), offset_of(m1)};
+        uint32_t p[NR][kParts][2];
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float n = x[ch][nt][2 * h + e];
+              const bool see = !EDGE || ((seen[ch] >> (4 * nt + 2 * h + e)) & 1u);
+              v[e] = see ? n * s[h] : 0.f;
+              if (see) bias[g][nt][e] += n * b[h];
+            }
+            uint32_t part[kParts];
+            split_pair<kParts>(v[0], v[1], part);
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) p[nt][i][h] = transposed(part[i]);
+          }
+        // a pair's halves are nibble i of two tokens
+        const uint32_t lo[2] = {__byte_perm(w0, w1, 0x5410), __byte_perm(w2, w3, 0x5410)};
+        const uint32_t hi[2] = {__byte_perm(w0, w1, 0x7632), __byte_perm(w2, w3, 0x7632)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t v[4] = {centred(lo[0], j), centred(hi[0], j), centred(lo[1], j), centred(hi[1], j)};
+#pragma unroll
+          for (int nt = 0; nt < NR; ++nt) {
+            if constexpr (kParts == 1) {
+              mma_codes(o[4 * g + j][nt], v, p[nt][0]);
+            } else {
+              // f32: a chunk's products are added up on their own and then to the sum in one rounding
+              float t[4] = {};
+#pragma unroll
+              for (int i = 0; i < kParts; ++i) mma_codes(t, v, p[nt][kParts - 1 - i]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[4 * g + j][nt][i] += t[i];
+            }
+          }
+        }
+      }
+    }
+  }
+
+  // Join the warps' results in shared memory, a group's 64 columns at a time, and
+  // hand (row, column, 4 values, m, l) to store. Called by every thread.
+  template <class F>
+  __device__ __forceinline__ void end(const AttnArgs& a, const Cursor& c, float* buf, float2* ml, F&& store) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, cc = lane & 3;
+    auto over_tokens = [](float v) {
+      v += __shfl_xor_sync(~0u, v, 4);
+      v += __shfl_xor_sync(~0u, v, 8);
+      return v + __shfl_xor_sync(~0u, v, 16);
+    };
+#pragma unroll
+    for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float sum = over_tokens(l[nt][e]);
+        if (r == 0) ml[warp * kRows + 8 * nt + 2 * cc + e] = make_float2(m[nt][e] * a.scale_log2, sum);
+      }
+    const int rows = c.rows;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+      for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float b = over_tokens(bias[g][nt][e]);
+          float* at = buf + (warp * kRows + 8 * nt + 2 * cc + e) * 64;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float4*>(at + ((8 * r + 4 * h) ^ (cc << 3))) =
+                make_float4(o[4 * g][nt][2 * h + e] + b, o[4 * g + 1][nt][2 * h + e] + b, o[4 * g + 2][nt][2 * h + e] + b,
+                            o[4 * g + 3][nt][2 * h + e] + b);
+        }
+      sync_compute();
+      for (int e = threadIdx.x; e < rows * 16; e += kCompute) {
+        const int row = e >> 4, col = (e & 15) * 4;
+        float M = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) M = fmaxf(M, ml[k * kRows + row].x);
+        const float Mu = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+          const float2 t = ml[k * kRows + row];
+          const float f = ex2(t.x - Mu);
+          L += f * t.y;
+          const float4 u = *reinterpret_cast<const float4*>(buf + (k * kRows + row) * 64 + (col ^ (((row >> 1) & 3) << 3)));
+          v.x += f * u.x;
+          v.y += f * u.y;
+          v.z += f * u.z;
+          v.w += f * u.w;
+        }
+        store(row, 64 * g + col, v, M, L);
+      }
+      sync_compute();
+    }
+  }
+};
+
+}  // namespace
+}  // namespace moe

@@ -1,5 +1,6 @@
 // C ABI entry points of the KV cache, attention and the 4-bit linear layer:
 // argument checks, scratch layout, launches.
+#include <atomic>
 #include <cmath>
 #include <cstddef>
 #include <string>
@@ -43,14 +44,17 @@ cudaError_t sm_count(int* n) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 int elem_bytes(int32_t dtype) { return dtype == MOE_F32 ? 4 : 2; }
+int token_elem_bytes(const moe_kv_t& a) { return elem_bytes(moe::token_type(a)); }
 
 // Geometry of a cache; nullptr if it is fine.
 const char* bad_geometry(const moe_kv_t& a) {
-  if (a.dtype != MOE_F32 && a.dtype != MOE_BF16) return "dtype is neither MOE_F32 nor MOE_BF16";
+  const int32_t type = moe::token_type(a);
+  if (type != MOE_F32 && type != MOE_BF16) return "dtype is neither MOE_F32 nor MOE_BF16, with or without MOE_KV_I4";
   if (a.n_layers < 1 || a.n_pages < 1 || a.n_kv_heads < 1) return "n_layers, n_pages or n_kv_heads < 1";
   if (a.page_tokens < 16 || a.page_tokens > 256 || (a.page_tokens & (a.page_tokens - 1)))
     return "page_tokens is not 16, 32, 64, 128 or 256";
   if (a.head_dim < 8 || a.head_dim > 256 || a.head_dim % 8) return "head_dim is not a multiple of 8 in 8..256";
+  if ((a.dtype & MOE_KV_I4) && a.head_dim % 64) return "head_dim is not a multiple of 64 in a cache of 4-bit codes";
   if (a.n_kv_heads > 1024) return "n_kv_heads above 1024";
   if (a.max_seqs < 1 || a.max_seqs > 65536) return "max_seqs outside 1..65536";
   if (a.max_pages < 1 || static_cast<int64_t>(a.max_pages) * a.page_tokens > 1ll << 30)
@@ -82,6 +86,46 @@ moe_status_t check_list(const char* call, const void* p, int32_t n) {
   return MOE_OK;
 }
 
+// Checks shared by the calls that take rows of keys and values; *none: there are none.
+moe_status_t open_rows(const char* call, const moe_kv_t* kv, int32_t layer, const void* k, int64_t ldk, const void* v,
+                       int64_t ldv, const int32_t* seqs, const int32_t* cu, int32_t n, int32_t n_rows, moe::KvLayout* l,
+                       int* sms, bool* none) {
+  moe_status_t st = open_kv(call, kv, l, sms);
+  if (st != MOE_OK) return st;
+  if (layer < 0 || layer >= kv->n_layers) return fail(MOE_ERR_ARG, call, "layer out of range");
+  if (n < 0 || n > 65536 || n_rows < 0) return fail(MOE_ERR_ARG, call, "n outside 0..65536 or n_rows < 0");
+  if (!seqs && n > kv->max_seqs) return fail(MOE_ERR_ARG, call, "n above max_seqs without seqs");
+  *none = n == 0 || n_rows == 0;
+  if (*none) return MOE_OK;
+  if (!k || !v || !cu) return fail(MOE_ERR_ARG, call, "k, v or cu is NULL");
+  const int64_t width = static_cast<int64_t>(kv->n_kv_heads) * kv->head_dim;
+  const int per = 16 / token_elem_bytes(*kv);
+  if (!aligned16(k) || !aligned16(v) || ldk % per || ldv % per)
+    return fail(MOE_ERR_ARG, call, "rows of k or v are not 16-byte aligned");
+  if (ldk < width || ldv < width) return fail(MOE_ERR_ARG, call, "ldk or ldv is smaller than a row");
+  return MOE_OK;
+}
+
+// A rotation of heads of D values as the kernels see it.
+moe_status_t open_rotary(const char* call, const moe_rotary_t* rot, int32_t D, moe::Rotary* r) {
+  if (!rot || !rot->turns) return fail(MOE_ERR_ARG, call, "the rotation or its turns are NULL");
+  if (reinterpret_cast<uintptr_t>(rot->turns) % 8) return fail(MOE_ERR_ARG, call, "turns is not 8-byte aligned");
+  if (rot->dim < 2 || rot->dim % 2 || rot->dim > D) return fail(MOE_ERR_ARG, call, "the rotation's dim is not an even number in 2..head_dim");
+  if (rot->interleaved != 0 && rot->interleaved != 1) return fail(MOE_ERR_ARG, call, "interleaved is neither 0 nor 1");
+  if (!std::isfinite(rot->magnitude)) return fail(MOE_ERR_ARG, call, "magnitude is not finite");
+  *r = moe::Rotary{rot->turns, rot->dim, rot->interleaved, rot->magnitude};
+  return MOE_OK;
+}
+// Rows of heads that go from x to y.
+moe_status_t check_heads(const char* call, const void* x, int64_t ldx, const void* y, int64_t ldy, int32_t heads, int32_t D,
+                         int32_t type) {
+  const int per = 16 / elem_bytes(type);
+  if (!aligned16(x) || !aligned16(y) || ldx % per || ldy % per) return fail(MOE_ERR_ARG, call, "rows of heads are not 16-byte aligned");
+  const int64_t width = static_cast<int64_t>(heads) * D;
+  if (ldx < width || ldy < width) return fail(MOE_ERR_ARG, call, "a row stride is smaller than a row");
+  return MOE_OK;
+}
+
 moe_status_t attention(const char* call, bool decode, const moe_kv_t* kv, int32_t layer, const void* q, int64_t ldq,
                        const int32_t* seqs, const int32_t* cu, int32_t n, int32_t n_q, int32_t n_rows,
                        int32_t n_heads, float scale, int32_t window, int32_t sinks, void* out, int64_t ldo,
@@ -104,7 +148,7 @@ moe_status_t attention(const char* call, bool decode, const moe_kv_t* kv, int32_
   if (rows == 0) return MOE_OK;
   if (!q || !out || (!decode && !cu)) return fail(MOE_ERR_ARG, call, "q, out or cu is NULL");
   const int64_t width = static_cast<int64_t>(n_heads) * kv->head_dim;
-  const int per = 16 / elem_bytes(kv->dtype);
+  const int per = 16 / token_elem_bytes(*kv);
   if (!aligned16(q) || !aligned16(out) || ldq % per || ldo % per)
     return fail(MOE_ERR_ARG, call, "rows of q or out are not 16-byte aligned");
   if (ldq < width || ldo < width) return fail(MOE_ERR_ARG, call, "ldq or ldo is smaller than a row");
@@ -113,20 +157,18 @@ moe_status_t attention(const char* call, bool decode, const moe_kv_t* kv, int32_
   if (!decode && (static_cast<int64_t>(rows) * (n_heads / kv->n_kv_heads) / 16 + n + 1) * kv->n_kv_heads > 0x7FFFFFFFll)
     return fail(MOE_ERR_ARG, call, "too many rows for one call");
   moe::AttnArgs a{};
-  const int64_t layer_bytes = static_cast<int64_t>(kv->n_pages) * kv->n_kv_heads * kv->page_tokens * kv->head_dim *
-                              elem_bytes(kv->dtype);
   a.q = q;
   a.out = out;
-  a.k = static_cast<const char*>(kv->k) + layer * layer_bytes;
-  a.v = static_cast<const char*>(kv->v) + layer * layer_bytes;
+  a.k = static_cast<const char*>(kv->k) + layer * moe::layer_bytes(*kv);
+  a.v = static_cast<const char*>(kv->v) + layer * moe::layer_bytes(*kv);
   a.table = kv->table;
   a.lens = kv->lens;
   a.seqs = seqs;
   a.cu = decode ? nullptr : cu;
   a.ldq = ldq;
   a.ldo = ldo;
-  a.wide_out = reinterpret_cast<uintptr_t>(out) % 32 == 0 && (ldo * elem_bytes(kv->dtype)) % 32 == 0 &&
-               (kv->head_dim * elem_bytes(kv->dtype)) % 32 == 0;
+  a.wide_out = reinterpret_cast<uintptr_t>(out) % 32 == 0 && (ldo * token_elem_bytes(*kv)) % 32 == 0 &&
+               (kv->head_dim * token_elem_bytes(*kv)) % 32 == 0;
   a.n = n;
   a.n_q = n_q;
   a.n_rows = rows;
@@ -151,6 +193,9 @@ moe_status_t attention(const char* call, bool decode, const moe_kv_t* kv, int32_
   a.copies = static_cast<uint32_t>(t_hook.copies);
   a.wait_cycles = t_hook.wait_cycles > 0 ? t_hook.wait_cycles : moe::kPrefillWaitCycles;
   t_hook = WaitHook{};
+  if (kv->dtype & MOE_KV_I4)
+    return launched(call, decode ? moe::launch_attn_decode_codes(a, moe::token_type(*kv), sms, stream)
+                                 : moe::launch_attn_prefill_codes(a, moe::token_type(*kv), stream));
   return launched(call, decode ? moe::launch_attn_decode(a, kv->dtype, sms, stream)
                                : moe::launch_attn_prefill(a, kv->dtype, rows, sms, stream));
 }
@@ -158,6 +203,11 @@ moe_status_t attention(const char* call, bool decode, const moe_kv_t* kv, int32_
 }  // namespace
 
 namespace moe {
+
+uint32_t next_write() {
+  static std::atomic<uint32_t> number{0};
+  return ++number;
+}
 
 KvLayout kv_layout(const moe_kv_t& kv, int num_sms) {
   KvLayout l;
@@ -178,7 +228,7 @@ KvLayout kv_layout(const moe_kv_t& kv, int num_sms) {
   l.cuts = take(num_sms * static_cast<int64_t>(sizeof(Cut)));
   // two partial results a CTA: rows of (m, l, -, -, head size padded)
   const int64_t dp = kv.head_dim <= 64 ? 64 : (kv.head_dim <= 128 ? 128 : 256);
-  const bool tc = kv.dtype == MOE_BF16 && kv.head_dim <= kTcHeadDim;
+  const bool tc = token_type(kv) == MOE_BF16 && kv.head_dim <= kTcHeadDim;
   l.part = take(2ll * num_sms * (tc ? kPrefillPartRows : kPartRows) * (dp + 4) * 4);
   l.bytes = at;
   return l;
@@ -275,19 +325,109 @@ extern "C" moe_status_t moe_kv_write(const moe_kv_t* kv, int32_t layer, const vo
     const char* call = "moe_kv_write";
     moe::KvLayout l;
     int sms = 0;
-    moe_status_t st = open_kv(call, kv, &l, &sms);
-    if (st != MOE_OK) return st;
-    if (layer < 0 || layer >= kv->n_layers) return fail(MOE_ERR_ARG, call, "layer out of range");
-    if (n < 0 || n > 65536 || n_rows < 0) return fail(MOE_ERR_ARG, call, "n outside 0..65536 or n_rows < 0");
-    if (!seqs && n > kv->max_seqs) return fail(MOE_ERR_ARG, call, "n above max_seqs without seqs");
-    if (n == 0 || n_rows == 0) return MOE_OK;
-    if (!k_new || !v_new || !cu) return fail(MOE_ERR_ARG, call, "k_new, v_new or cu is NULL");
-    const int64_t width = static_cast<int64_t>(kv->n_kv_heads) * kv->head_dim;
-    const int per = 16 / elem_bytes(kv->dtype);
-    if (!aligned16(k_new) || !aligned16(v_new) || ldk % per || ldv % per)
-      return fail(MOE_ERR_ARG, call, "rows of k_new or v_new are not 16-byte aligned");
-    if (ldk < width || ldv < width) return fail(MOE_ERR_ARG, call, "ldk or ldv is smaller than a row");
+    bool none = false;
+    moe_status_t st = open_rows(call, kv, layer, k_new, ldk, v_new, ldv, seqs, cu, n, n_rows, &l, &sms, &none);
+    if (st != MOE_OK || none) return st;
+    if (kv->dtype & MOE_KV_I4)
+      return launched(call, moe::launch_kv_write_rotary(*kv, l, layer, moe::Rotary{}, nullptr, 0, 0, nullptr, 0, k_new, ldk, v_new,
+                                                        ldv, seqs, cu, n, n_rows, sms, stream));
     return launched(call, moe::launch_kv_write(*kv, l, layer, k_new, ldk, v_new, ldv, seqs, cu, n, n_rows, stream));
+  });
+}
+
+extern "C" moe_status_t moe_kv_write_rotary(const moe_kv_t* kv, int32_t layer, const moe_rotary_t* rot, const void* q,
+                                            int64_t ldq, int32_t n_heads, void* q_out, int64_t ldqo, const void* k_new,
+                                            int64_t ldk, const void* v_new, int64_t ldv, const int32_t* seqs,
+                                            const int32_t* cu, int32_t n, int32_t n_rows, moe_stream_t stream) {
+  return guarded([&] {
+    const char* call = "moe_kv_write_rotary";
+    moe::KvLayout l;
+    int sms = 0;
+    bool none = false;
+    moe_status_t st = open_rows(call, kv, layer, k_new, ldk, v_new, ldv, seqs, cu, n, n_rows, &l, &sms, &none);
+    if (st != MOE_OK) return st;
+    moe::Rotary r{};
+    if ((st = open_rotary(call, rot, kv->head_dim, &r)) != MOE_OK) return st;
+    if (n_heads < 1 || n_heads > 65536) return fail(MOE_ERR_ARG, call, "n_heads outside 1..65536");
+    if (none) return MOE_OK;
+    if (!q || !q_out) return fail(MOE_ERR_ARG, call, "q or q_out is NULL");
+    if ((st = check_heads(call, q, ldq, q_out, ldqo, n_heads, kv->head_dim, moe::token_type(*kv))) != MOE_OK) return st;
+    return launched(call, moe::launch_kv_write_rotary(*kv, l, layer, r, q, ldq, n_heads, q_out, ldqo, k_new, ldk, v_new, ldv,
+                                                      seqs, cu, n, n_rows, sms, stream));
+  });
+}
+
+extern "C" moe_status_t moe_kv_read(const moe_kv_t* kv, int32_t layer, void* k, int64_t ldk, void* v, int64_t ldv,
+                                    const int32_t* seqs, const int32_t* cu, int32_t n, int32_t n_rows,
+                                    moe_stream_t stream) {
+  return guarded([&] {
+    const char* call = "moe_kv_read";
+    moe::KvLayout l;
+    int sms = 0;
+    bool none = false;
+    moe_status_t st = open_rows(call, kv, layer, k, ldk, v, ldv, seqs, cu, n, n_rows, &l, &sms, &none);
+    if (st != MOE_OK || none) return st;
+    return launched(call, moe::launch_kv_read(*kv, l, layer, k, ldk, v, ldv, seqs, cu, n, n_rows, sms, stream));
+  });
+}
+
+extern "C" moe_status_t moe_rotary_angles(int32_t dim, double base, double factor, int32_t context, double turns_low,
+                                          double turns_high, double* angles) {
+  return guarded([&] {
+    const char* call = "moe_rotary_angles";
+    if (dim < 2 || dim % 2 || dim > 65536) return fail(MOE_ERR_ARG, call, "dim is not an even number in 2..65536");
+    if (!(base > 0.0) || !std::isfinite(base)) return fail(MOE_ERR_ARG, call, "base is not finite and positive");
+    if (!(factor > 0.0) || !std::isfinite(factor)) return fail(MOE_ERR_ARG, call, "factor is not finite and positive");
+    if (context < 0) return fail(MOE_ERR_ARG, call, "context < 0");
+    if (context > 0 && !(turns_high > turns_low && std::isfinite(turns_low) && std::isfinite(turns_high)))
+      return fail(MOE_ERR_ARG, call, "turns_high is not above turns_low, or not finite");
+    if (!angles) return fail(MOE_ERR_ARG, call, "angles is NULL");
+    constexpr double kTurn = 6.283185307179586476925;
+    for (int32_t i = 0; i < dim / 2; ++i) {
+      const double f = std::pow(base, -2.0 * i / dim);
+      double keep = 0.0;  // the share of the frequency that is not stretched
+      if (context > 0) keep = std::min(1.0, std::max(0.0, (f * context / kTurn - turns_low) / (turns_high - turns_low)));
+      angles[i] = f * (keep + (1.0 - keep) / factor);
+    }
+    return MOE_OK;
+  });
+}
+
+extern "C" moe_status_t moe_rotary_turns(const double* angles, int32_t n, uint64_t* turns) {
+  return guarded([&] {
+    const char* call = "moe_rotary_turns";
+    if (n < 0 || (n > 0 && (!angles || !turns))) return fail(MOE_ERR_ARG, call, "n < 0, or angles or turns is NULL");
+    constexpr double kTurn = 6.283185307179586476925;
+    for (int32_t i = 0; i < n; ++i)
+      if (!std::isfinite(angles[i])) return fail(MOE_ERR_ARG, call, "an angle is not finite");
+    for (int32_t i = 0; i < n; ++i) {
+      double t = angles[i] / kTurn;
+      t -= std::floor(t);  // whole turns are none
+      turns[i] = t >= 1.0 ? 0 : static_cast<uint64_t>(t * 18446744073709551616.0);
+    }
+    return MOE_OK;
+  });
+}
+
+extern "C" moe_status_t moe_rotary(const moe_rotary_t* rot, const int32_t* pos, const void* x, int32_t xt, int64_t ldx,
+                                   int32_t n_rows, int32_t n_heads, int32_t head_dim, void* y, int64_t ldy,
+                                   moe_stream_t stream) {
+  return guarded([&] {
+    const char* call = "moe_rotary";
+    if (xt != MOE_F32 && xt != MOE_BF16) return fail(MOE_ERR_ARG, call, "x is neither MOE_F32 nor MOE_BF16");
+    if (head_dim < 8 || head_dim > 256 || head_dim % 8) return fail(MOE_ERR_ARG, call, "head_dim is not a multiple of 8 in 8..256");
+    moe::Rotary r{};
+    moe_status_t st = open_rotary(call, rot, head_dim, &r);
+    if (st != MOE_OK) return st;
+    if (n_rows < 0 || n_rows > 1 << 30) return fail(MOE_ERR_ARG, call, "n_rows outside 0..2^30");
+    if (n_heads < 1 || n_heads > 65536) return fail(MOE_ERR_ARG, call, "n_heads outside 1..65536");
+    if (n_rows == 0) return MOE_OK;
+    if (!pos || !x || !y) return fail(MOE_ERR_ARG, call, "pos, x or y is NULL");
+    if ((st = check_heads(call, x, ldx, y, ldy, n_heads, head_dim, xt)) != MOE_OK) return st;
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return cuda_fail(call, e);
+    return launched(call, moe::launch_rotary(r, pos, x, xt, ldx, y, ldy, n_rows, n_heads, head_dim, sms, stream));
   });
 }
 

@@ -33,6 +33,16 @@ struct KvLayout {
   // int per page; filled: one per listed sequence), tickets, records of cut units, partial results
   int64_t src, dst, filled, map, shr, last, tickets, cuts, part, bytes;
 };
+// type of a cache's tokens, queries and results
+inline int32_t token_type(const moe_kv_t& a) { return a.dtype & ~MOE_KV_I4; }
+// bytes of one head of one page, and of a layer's pages
+inline int64_t head_bytes(const moe_kv_t& a) {
+  const int64_t values = static_cast<int64_t>(a.page_tokens) * a.head_dim;
+  return a.dtype & MOE_KV_I4 ? values * 9 / 16 : values * (a.dtype == MOE_F32 ? 4 : 2);
+}
+inline int64_t layer_bytes(const moe_kv_t& a) { return static_cast<int64_t>(a.n_pages) * a.n_kv_heads * head_bytes(a); }
+uint32_t next_write();  // a write's number
+
 constexpr int kMaxList = 8192;  // most sequences of one page call
 KvLayout kv_layout(const moe_kv_t& kv, int num_sms);
 
@@ -69,6 +79,9 @@ cudaError_t launch_attn_decode(const AttnArgs& a, int32_t dtype, int num_sms, cu
 cudaError_t launch_attn_prefill(const AttnArgs& a, int32_t dtype, int32_t n_rows, int num_sms, cudaStream_t st);
 
 cudaError_t launch_attn_prefill_tc(const AttnArgs& a, int num_sms, cudaStream_t st);
+// over pages of 4-bit codes; dtype: the type of q and out
+cudaError_t launch_attn_decode_codes(const AttnArgs& a, int32_t dtype, int num_sms, cudaStream_t st);
+cudaError_t launch_attn_prefill_codes(const AttnArgs& a, int32_t dtype, cudaStream_t st);
 
 cudaError_t launch_kv_fork(const moe_kv_t& kv, const KvLayout& l, const int32_t* src, const int32_t* dst, int32_t n,
                            cudaStream_t st);
@@ -77,6 +90,21 @@ cudaError_t launch_kv_reserve(const moe_kv_t& kv, const KvLayout& l, const int32
 cudaError_t launch_kv_write(const moe_kv_t& kv, const KvLayout& l, int32_t layer, const void* k_new, int64_t ldk,
                             const void* v_new, int64_t ldv, const int32_t* seqs, const int32_t* cu, int32_t n,
                             int32_t n_rows, cudaStream_t st);
+// A rotation as the kernels see it (dim 0: none).
+struct Rotary {
+  const uint64_t* turns;  // [dim / 2] turns a position, times 2^64
+  int32_t dim, interleaved;
+  float magnitude;
+};
+cudaError_t launch_rotary(const Rotary& rot, const int32_t* pos, const void* x, int32_t xt, int64_t ldx, void* y, int64_t ldy,
+                          int32_t rows, int32_t heads, int32_t D, int num_sms, cudaStream_t st);
+// q NULL: keys and values only
+cudaError_t launch_kv_write_rotary(const moe_kv_t& kv, const KvLayout& l, int32_t layer, const Rotary& rot, const void* q,
+                                   int64_t ldq, int32_t n_heads, void* q_out, int64_t ldqo, const void* k, int64_t ldk,
+                                   const void* v, int64_t ldv, const int32_t* seqs, const int32_t* cu, int32_t n, int32_t n_rows,
+                                   int num_sms, cudaStream_t st);
+cudaError_t launch_kv_read(const moe_kv_t& kv, const KvLayout& l, int32_t layer, void* k, int64_t ldk, void* v, int64_t ldv,
+                           const int32_t* seqs, const int32_t* cu, int32_t n, int32_t n_rows, int num_sms, cudaStream_t st);
 cudaError_t launch_kv_free(const moe_kv_t& kv, const KvLayout& l, const int32_t* seqs, int32_t n, cudaStream_t st);
 cudaError_t launch_kv_compact(const moe_kv_t& kv, const KvLayout& l, int num_sms, cudaStream_t st);
 cudaError_t launch_kv_copy_pages(const moe_kv_t& kv, const KvLayout& l, const int32_t* src, const int32_t* dst,

@@ -21,10 +21,7 @@
 // written at 6.2 TB/s.
 #include <cooperative_groups.h>
 
-#include <atomic>
-#include <cstddef>
-
-#include "kv.h"
+#include "kv_device.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -34,31 +31,6 @@ namespace {
 constexpr int kCtas = 8, kThreads = 1024;
 constexpr int kWarps = kThreads / 32, kAll = kCtas * kThreads, kAllWarps = kCtas * kWarps;
 constexpr int kBitmapWords = 65536 / 32;
-
-struct Kv {
-  int32_t* table;
-  int32_t* lens;
-  int32_t* ref;
-  KvWork* work;
-  int32_t *src, *dst, *filled, *map, *shr, *last;
-  int32_t S, W, P, page, page_shift;
-};
-
-__device__ __forceinline__ int pages_of(const Kv& kv, int64_t tokens) {
-  return static_cast<int>((tokens + kv.page - 1) >> kv.page_shift);
-}
-// Is a failure of an earlier call pending? A write records its own errors under
-// its number beside the error word, because its other blocks may still have to
-// read that: so a write stops for earlier calls' errors and never for its own, and
-// what it writes does not depend on timing. The next call moves them to the word.
-__device__ __forceinline__ bool pending(const Kv& kv, bool a_write = false, uint32_t number = 0) {
-  static_assert(offsetof(KvWork, err) == 0 && offsetof(KvWork, late) == 8, "one load of both");
-  uint64_t head, late;  // (32,768 rows: 14 us with one load a warp, 23 with two, all of one line)
-  asm volatile("ld.volatile.global.v2.u64 {%0, %1}, [%2];" : "=l"(head), "=l"(late) : "l"(kv.work) : "memory");
-  if (late == 0 || (a_write && static_cast<uint32_t>(late >> 32) == number)) return static_cast<uint32_t>(head) != 0u;
-  if (threadIdx.x == 0) atomicOr(&kv.work->err, static_cast<uint32_t>(late));
-  return true;
-}
 
 // Threads that share one listed sequence: a power of two, at least a warp.
 __device__ __forceinline__ int lanes_per(int n) {
@@ -71,9 +43,6 @@ __device__ __forceinline__ int lanes_per(int n) {
 __device__ __forceinline__ bool mark(uint32_t* bits, int id, int S) {
   if (id < 0 || id >= S) return false;
   return !(atomicOr(bits + (id >> 5), 1u << (id & 31)) & (1u << (id & 31)));
-}
-__device__ __forceinline__ bool held_ok(const Kv& kv, int len) {
-  return len >= 0 && pages_of(kv, len) <= kv.W;
 }
 
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
@@ -358,22 +327,23 @@ __device__ __forceinline__ uint32_t take_mod(uint64_t& x, uint32_t d) {
 }
 
 // The copies of reserve: copy i takes the first filled[i] tokens of page map[i]
-// to page dst[i], in every layer and head of k and v. A warp copies 128 vectors
-// (2 KB) at a time, four loads a lane in flight.
+// to page dst[i], in every layer and head of k and v; of pages of codes, where a
+// token's codes and scales lie apart, the whole head. A warp copies 128 vectors (2
+// KB) at a time, four loads a lane in flight.
 constexpr int kCowPiece = 128;
 __global__ void __launch_bounds__(256)
-    cow_copy_kernel(Kv kv, uint4* k, uint4* v, int L, int H, int tok_vecs, int64_t page_vecs) {
+    cow_copy_kernel(Kv kv, uint4* k, uint4* v, int L, int H, int tok_vecs, int head_vecs, int64_t page_vecs) {
   const int n = kv.work->n_copies, lane = threadIdx.x & 31;
-  const int pieces = (kv.page * tok_vecs + kCowPiece - 1) / kCowPiece;
+  const int pieces = (head_vecs + kCowPiece - 1) / kCowPiece;
   const uint64_t items = static_cast<uint64_t>(n) * L * 2 * H * pieces;
   for (uint64_t it = blockIdx.x * 8ull + (threadIdx.x >> 5); it < items; it += gridDim.x * 8ull) {
     uint64_t r = it;
     const int p = take_mod(r, pieces), h = take_mod(r, H);
     uint4* pool = take_mod(r, 2) ? v : k;
     const int l = take_mod(r, L), i = static_cast<int>(r);
-    const int vecs = kv.filled[i] * tok_vecs - p * kCowPiece;  // of this piece on
+    const int vecs = (tok_vecs ? kv.filled[i] * tok_vecs : head_vecs) - p * kCowPiece;  // of this piece on
     if (vecs <= 0) continue;
-    const int64_t head = static_cast<int64_t>(h) * kv.page * tok_vecs + p * kCowPiece;
+    const int64_t head = static_cast<int64_t>(h) * head_vecs + p * kCowPiece;
     const uint4* from = pool + (static_cast<int64_t>(l) * kv.P + kv.map[i]) * page_vecs + head;
     uint4* to = pool + (static_cast<int64_t>(l) * kv.P + kv.dst[i]) * page_vecs + head;
     uint4 t[kCowPiece / 32];
@@ -516,43 +486,14 @@ __global__ void __launch_bounds__(256)
     v0 = __ldg(fv + lane);
   }
   const bool stop = pending(kv, true, number);
-  auto record = [&](uint32_t why) {
-    if (lane == 0) atomicOr(reinterpret_cast<unsigned long long*>(&kv.work->late), static_cast<unsigned long long>(number) << 32 | why);
-  };
-  // the last i with cu[i] <= row: 32 probes a step
-  int lo = 0, span = n;  // it is in [lo, lo + span)
-  while (span > 1) {
-    const int step = (span + 31) / 32, at = lo + lane * step;
-    const unsigned int b = __ballot_sync(~0u, at < lo + span && __ldg(cu + at) <= row);
-    const int hit = b ? 31 - __clz(b) : 0;
-    const int next = lo + hit * step;
-    span = min(step, lo + span - next);
-    lo = next;
-  }
+  const int lo = chunk_of(cu, n, row, lane);
   if (stop) return;
   // tokens that the rows do not reach (of a chunk that no row is in, too)
-  if (row == 0 && __ldg(cu + n) > n_rows) record(MOE_DEVERR_BADIDX);
-  const int r0 = __ldg(cu + lo), r1 = __ldg(cu + lo + 1);
-  if (row < r0 || row >= r1) return;
-  if (r0 < 0 || r1 > n_rows) {  // none of such a chunk is written
-    record(MOE_DEVERR_BADIDX);
-    return;
-  }
-  const int s = seqs ? __ldg(seqs + lo) : lo;
-  if (s < 0 || s >= kv.S) {
-    record(MOE_DEVERR_BADIDX);
-    return;
-  }
-  const int len = kv.lens[s], at = len - (r1 - row);
-  if (len - (r1 - r0) < 0 || !held_ok(kv, len)) {  // the chunk does not fit: none of it is written
-    record(KV_DEVERR_SHARED);
-    return;
-  }
-  const int p = kv.table[static_cast<int64_t>(s) * kv.W + (at >> kv.page_shift)];
-  if (p < 0 || p >= kv.P || kv.ref[p] != 1) {
-    record(p < 0 || p >= kv.P ? MOE_DEVERR_BADIDX : KV_DEVERR_SHARED);
-    return;
-  }
+  if (row == 0 && __ldg(cu + n) > n_rows) record_late(kv, number, MOE_DEVERR_BADIDX, lane);
+  const Place pl = place_of<true>(kv, seqs, cu, lo, n_rows, row);
+  if (pl.why) record_late(kv, number, pl.why, lane);
+  if (pl.page < 0) return;
+  const int p = pl.page, at = pl.pos;
   const int64_t base = ((static_cast<int64_t>(p) * H) << kv.page_shift) + (at & (kv.page - 1));
   for (int x = lane; x < vecs; x += 32) {
     const int h = x / tok_vecs, c = x - h * tok_vecs;
@@ -562,29 +503,10 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-Kv kv_of(const moe_kv_t& a, const KvLayout& l) {
-  Kv kv;
-  char* w = static_cast<char*>(a.work);
-  kv.table = a.table;
-  kv.lens = a.lens;
-  kv.ref = a.ref;
-  kv.work = reinterpret_cast<KvWork*>(w);
-  kv.src = reinterpret_cast<int32_t*>(w + l.src);
-  kv.dst = reinterpret_cast<int32_t*>(w + l.dst);
-  kv.filled = reinterpret_cast<int32_t*>(w + l.filled);
-  kv.map = reinterpret_cast<int32_t*>(w + l.map);
-  kv.shr = reinterpret_cast<int32_t*>(w + l.shr);
-  kv.last = reinterpret_cast<int32_t*>(w + l.last);
-  kv.S = a.max_seqs;
-  kv.W = a.max_pages;
-  kv.P = a.n_pages;
-  kv.page = a.page_tokens;
-  kv.page_shift = __builtin_ctz(a.page_tokens);
-  return kv;
-}
-// 16-byte vectors of one token of one head, and of a page of one layer
-int tok_vecs(const moe_kv_t& a) { return a.head_dim * (a.dtype == MOE_F32 ? 4 : 2) / 16; }
-int64_t page_vecs(const moe_kv_t& a) { return static_cast<int64_t>(a.n_kv_heads) * a.page_tokens * tok_vecs(a); }
+// 16-byte vectors of one token of one head (0 in pages of codes), of a head of a page, of a page of one layer
+int tok_vecs(const moe_kv_t& a) { return a.dtype & MOE_KV_I4 ? 0 : a.head_dim * (a.dtype == MOE_F32 ? 4 : 2) / 16; }
+int head_vecs(const moe_kv_t& a) { return static_cast<int>(head_bytes(a) / 16); }
+int64_t page_vecs(const moe_kv_t& a) { return static_cast<int64_t>(a.n_kv_heads) * head_vecs(a); }
 
 }  // namespace
 
@@ -602,11 +524,11 @@ cudaError_t launch_kv_reserve(const moe_kv_t& a, const KvLayout& l, const int32_
   const Kv kv = kv_of(a, l);
   reserve_kernel<<<kCtas, kThreads, smem, st>>>(kv, seqs, n_new, n);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int pieces = (a.page_tokens * tok_vecs(a) + kCowPiece - 1) / kCowPiece;
+  const int pieces = (head_vecs(a) + kCowPiece - 1) / kCowPiece;
   const int64_t items = static_cast<int64_t>(n) * a.n_layers * 2 * a.n_kv_heads * pieces;
   const int grid = static_cast<int>(std::min<int64_t>((items + 7) / 8, 8ll * num_sms));
   cow_copy_kernel<<<grid, 256, 0, st>>>(kv, static_cast<uint4*>(a.k), static_cast<uint4*>(a.v), a.n_layers,
-                                        a.n_kv_heads, tok_vecs(a), page_vecs(a));
+                                        a.n_kv_heads, tok_vecs(a), head_vecs(a), page_vecs(a));
   return cudaGetLastError();
 }
 
@@ -615,11 +537,10 @@ cudaError_t launch_kv_write(const moe_kv_t& a, const KvLayout& l, int32_t layer,
                             int32_t n_rows, cudaStream_t st) {
   const int per = a.dtype == MOE_F32 ? 4 : 8;
   const int64_t off = layer * (static_cast<int64_t>(a.n_pages) * page_vecs(a));
-  static std::atomic<uint32_t> number{0};
   write_kernel<<<(n_rows + 7) / 8, 256, 0, st>>>(kv_of(a, l), static_cast<uint4*>(a.k) + off,
                                                   static_cast<uint4*>(a.v) + off, static_cast<const uint4*>(k_new),
                                                   ldk / per, static_cast<const uint4*>(v_new), ldv / per, seqs, cu, n,
-                                                  n_rows, a.n_kv_heads, tok_vecs(a), ++number);
+                                                  n_rows, a.n_kv_heads, tok_vecs(a), next_write());
   return cudaGetLastError();
 }
 

@@ -1,4 +1,4 @@
-"""Paged key-value cache, attention over it and the 4-bit linear layer: the
+"""Paged key-value cache, attention over it, rotary positions and the 4-bit linear layer: the
 binding of include/moekv.h. PyTorch supplies device memory and streams; every
 step runs in the library's CUDA kernels.
 """
@@ -91,12 +91,79 @@ def _head_rows(t: torch.Tensor, name: str, heads: Optional[int], dim: int, dtype
     return rows if shape[0] > 1 else shape[1] * dim  # (a single row's stride leads nowhere)
 
 
+class Rotary:
+    """Rotary positions of the leading ``dim`` columns of a head (``moe_rotary_t``).
+
+    Pairs are halves of those columns, or with ``interleaved`` neighbours. Frequency i
+    is base^(-2i/dim) radians a position; for long contexts it is divided by ``factor``:
+    every one with context 0, else those of at most turns[0] turns within ``context``
+    tokens, less and less up to those of turns[1] turns, which stay. ``angles``
+    gives the dim / 2 frequencies themselves instead. Results are scaled by ``magnitude``.
+    """
+
+    def __init__(self, dim: int, base: float = 10000.0, interleaved: bool = False, factor: float = 1.0, context: int = 0,
+                 turns=(1.0, 32.0), magnitude: float = 1.0, angles=None, device=None):
+        if dim < 2 or dim % 2:
+            raise ValueError("dim must be an even number of at least 2")
+        n = dim // 2
+        radians, fractions = (C.c_double * n)(), (C.c_uint64 * n)()
+        if angles is None:
+            _ok(lib.moe_rotary_angles(dim, base, factor, context, turns[0], turns[1], radians))
+        else:
+            if len(angles) != n:
+                raise ValueError(f"angles must hold {n} entries (got {len(angles)})")
+            radians[:] = [float(a) for a in angles]
+        _ok(lib.moe_rotary_turns(radians, n, fractions))
+        self.dim, self.interleaved, self.magnitude = dim, bool(interleaved), float(magnitude)
+        self.angles = list(radians)
+        # (a copy from pageable memory has been taken when the call returns, and is there before later work on any stream)
+        self.turns = torch.frombuffer(fractions, dtype=torch.int64).to(device or torch.device("cuda"))
+        if not self.turns.is_cuda:
+            raise TypeError("a rotation's device must be a CUDA device")
+        self.raw = N.RotaryT(self.turns.data_ptr(), dim, int(self.interleaved), self.magnitude)
+        self._ref = C.byref(self.raw)
+        self._device = self.turns.device.index
+
+
+def _rotation(rot, device: int):
+    if not isinstance(rot, Rotary):
+        raise TypeError("the rotation must be a Rotary")
+    if rot._device != device:
+        raise ValueError(f"the rotation must be on cuda:{device} (is on cuda:{rot._device})")
+    return rot._ref
+
+
+def rotary(x: torch.Tensor, pos: torch.Tensor, rot: Rotary, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """x [rows, heads, head_dim] (float32 or bfloat16, rows may lie apart) turned to pos (int32 [rows]).
+
+    ``out`` may be x itself. Runs on the current stream, or on ``stream``.
+    """
+    if x.dim() != 3 or not x.is_cuda:
+        raise ValueError("x must be a [rows, heads, head_dim] CUDA tensor")
+    xt = _dtype_id(x.dtype)
+    device = x.get_device()
+    rows, heads, dim = x.shape
+    _ints(pos, "pos", device, rows)
+    ldx = _head_rows(x, "x", heads, dim, x.dtype, device)
+    if out is None:
+        out = _new(x.shape, x.dtype, x.device, stream)
+    elif out.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    _run(device, lib.moe_rotary, _rotation(rot, device), pos.data_ptr(), x.data_ptr(), xt, ldx, rows, heads, dim, out.data_ptr(),
+         _head_rows(out, "out", heads, dim, x.dtype, device), _raw_stream(device) if stream is None else stream.cuda_stream)
+    return out
+
+
 class KvCache:
     """Device arrays of a paged key-value cache (``moe_kv_t``).
 
     Either over tensors that the caller has (k, v: [layers, pages, kv_heads,
     page_tokens, head_dim]; table: int32 [max_seqs, max_pages]; lens: int32
     [max_seqs]; ref: int32 [pages]) or, with :meth:`empty`, over new ones.
+    Pages of 4-bit codes are uint8 [layers, pages, kv_heads, page_tokens,
+    head_dim * 9 / 16], where the last two dimensions together are a head's codes
+    and behind them its scales and offsets; ``dtype`` is then the type of queries,
+    results and new tokens.
     Sequence ids are rows of ``table``; every list of them is an int32 CUDA
     tensor, so that a captured step can be replayed with other contents.
 
@@ -105,11 +172,18 @@ class KvCache:
     and the cache have to live until the call has run.
     """
 
-    def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor):
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor,
+                 dtype: Optional[torch.dtype] = None):
         for t, name, dims in ((k, "k", 5), (v, "v", 5), (table, "table", 2), (lens, "lens", 1), (ref, "ref", 1)):
             if not t.is_cuda or t.dim() != dims or not t.is_contiguous():
                 raise TypeError(f"{name} must be a contiguous CUDA tensor of {dims} dimensions")
-        _dtype_id(k.dtype)
+        codes = k.dtype == torch.uint8
+        if dtype is None and codes:
+            raise TypeError("pages of codes need the dtype of queries and new tokens")
+        if dtype is not None and not codes and dtype != k.dtype:
+            raise TypeError("dtype must be that of k and v")
+        dtype = dtype or k.dtype
+        kind = _dtype_id(dtype) | (N.KV_I4 if codes else 0)
         if k.shape != v.shape or k.dtype != v.dtype:
             raise ValueError("k and v must have one shape and type")
         if any(t.dtype != torch.int32 for t in (table, lens, ref)):
@@ -120,11 +194,15 @@ class KvCache:
             raise ValueError("the cache's tensors must be on one device")
         self.k, self.v, self.table, self.lens, self.ref = k, v, table, lens, ref
         L, P, Hkv, page, D = k.shape
+        if codes:
+            if D % 36:
+                raise ValueError("the last dimension of pages of codes must be head_dim * 9 / 16, head_dim a multiple of 64")
+            D = D * 16 // 9
         self.raw = N.KvT(k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), ref.data_ptr(), None, 0, L, P,
-                         Hkv, page, D, _dtype_id(k.dtype), table.shape[0], table.shape[1])
+                         Hkv, page, D, kind, table.shape[0], table.shape[1])
         self._ref = C.byref(self.raw)
         self._device = k.device.index
-        self._kv_heads, self._dim, self._dtype = Hkv, D, k.dtype
+        self._kv_heads, self._dim, self._dtype = Hkv, D, dtype
         n = C.c_int64()
         _run(self._device, lib.moe_kv_work_bytes, self._ref, C.byref(n))
         self.work = torch.zeros(n.value, dtype=torch.uint8, device=k.device)
@@ -139,13 +217,19 @@ class KvCache:
 
     @classmethod
     def empty(cls, n_layers, n_pages, n_kv_heads, page_tokens, head_dim, max_seqs, max_pages,
-              dtype=torch.bfloat16, device=None) -> "KvCache":
+              dtype=torch.bfloat16, device=None, bits: int = 0) -> "KvCache":
+        """bits: 4 for pages of 4-bit codes; 0 for pages of ``dtype``."""
+        if bits not in (0, 4):
+            raise ValueError("bits must be 0 (pages of dtype) or 4")
+        if bits and head_dim % 64:
+            raise ValueError("head_dim must be a multiple of 64 in a cache of 4-bit codes")
         dev = device or torch.device("cuda")
-        shape = (n_layers, n_pages, n_kv_heads, page_tokens, head_dim)
+        shape = (n_layers, n_pages, n_kv_heads, page_tokens, head_dim * 9 // 16 if bits else head_dim)
+        held = dict(dtype=torch.uint8 if bits else dtype, device=dev)
         i32 = dict(dtype=torch.int32, device=dev)
-        return cls(torch.zeros(shape, dtype=dtype, device=dev), torch.zeros(shape, dtype=dtype, device=dev),
+        return cls(torch.zeros(shape, **held), torch.zeros(shape, **held),
                    torch.full((max_seqs, max_pages), -1, **i32), torch.zeros(max_seqs, **i32),
-                   torch.zeros(n_pages, **i32))
+                   torch.zeros(n_pages, **i32), dtype)
 
     @property
     def token_bytes(self) -> int:
@@ -177,6 +261,42 @@ class KvCache:
         _run(self._device, lib.moe_kv_write, self._ref, layer, k.data_ptr(), ldk, v.data_ptr(), ldv, seqs.data_ptr(),
              cu.data_ptr(), n, rows, self._st(stream))
 
+    def write_rotary(self, layer, q, k, v, seqs, cu, rot, q_out=None, stream=None):
+        """write with k turned to its tokens' positions on the way, and q [rows, heads, head_dim] into q_out.
+
+        Returns q_out (new if None; it may be q itself). Rows of no sequence are left as they are in it.
+        """
+        n = _ints(seqs, "seqs", self._device)
+        _ints(cu, "cu", self._device, n + 1)
+        ldk = _head_rows(k, "k", self._kv_heads, self._dim, self._dtype, self._device)
+        ldv = _head_rows(v, "v", self._kv_heads, self._dim, self._dtype, self._device)
+        q_out, ldq, ldqo = self._q_out(q, q_out, stream, "q_out")
+        rows, heads = q.shape[:2]
+        if rows != v.shape[0] or rows != k.shape[0]:
+            raise ValueError("q, k and v must have as many rows")
+        _run(self._device, lib.moe_kv_write_rotary, self._ref, layer, _rotation(rot, self._device), q.data_ptr(), ldq, heads,
+             q_out.data_ptr(), ldqo, k.data_ptr(), ldk, v.data_ptr(), ldv, seqs.data_ptr(), cu.data_ptr(), n, rows,
+             self._st(stream))
+        return q_out
+
+    def read(self, layer, seqs, cu, rows, k=None, v=None, stream=None):
+        """The newest cu[i+1]-cu[i] tokens of seqs[i] as rows cu[i].. of k and v [rows, kv_heads, head_dim].
+
+        Returns k and v (new ones of ``rows`` rows if None). Rows of no sequence are left as they are.
+        """
+        n = _ints(seqs, "seqs", self._device)
+        _ints(cu, "cu", self._device, n + 1)
+        shape = (rows, self._kv_heads, self._dim)
+        k = _new(shape, self._dtype, self.k.device, stream) if k is None else k
+        v = _new(shape, self._dtype, self.k.device, stream) if v is None else v
+        if k.shape != shape or v.shape != shape:
+            raise ValueError(f"k and v must be {list(shape)}")
+        ldk = _head_rows(k, "k", self._kv_heads, self._dim, self._dtype, self._device)
+        ldv = _head_rows(v, "v", self._kv_heads, self._dim, self._dtype, self._device)
+        _run(self._device, lib.moe_kv_read, self._ref, layer, k.data_ptr(), ldk, v.data_ptr(), ldv, seqs.data_ptr(),
+             cu.data_ptr(), n, rows, self._st(stream))
+        return k, v
+
     def free(self, seqs, stream=None):
         """Drop sequences; pages that no other sequence names become free."""
         n = _ints(seqs, "seqs", self._device)
@@ -201,14 +321,14 @@ class KvCache:
         """The next attention call of this thread runs into its bounded waits (a test hook)."""
         _ok(lib.moe_debug_attn_wait_timeout(wait_cycles, copies))
 
-    def _q_out(self, q, out, stream):
+    def _q_out(self, q, out, stream, name="out"):
         """out (new if None) and the row strides of q and out."""
         ldq = _head_rows(q, "q", None, self._dim, self._dtype, self._device)
         if out is None:
             out = _new(q.shape, q.dtype, q.device, stream)
         elif out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-        return out, ldq, _head_rows(out, "out", None, self._dim, self._dtype, self._device)
+            raise ValueError(f"{name} must have q's shape")
+        return out, ldq, _head_rows(out, name, None, self._dim, self._dtype, self._device)
 
     def attn_decode(self, layer, q, seqs, n_q=1, out=None, scale=None, window=0, sinks=0, stream=None):
         """Attention of the newest n_q tokens of each sequence: q [len(seqs) * n_q, heads, head_dim]."""

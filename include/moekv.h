@@ -1,8 +1,9 @@
 /*
  * moekv.h — the operators a decoder layer needs beside the routed FFN of
- * moecache.h: a paged key-value cache with its page bookkeeping, attention
- * over it (of the newest tokens of many sequences, and of prompt chunks), and
- * a linear layer with 4-bit weights and group scales for the projections.
+ * moecache.h: a paged key-value cache with its page bookkeeping, in values or in
+ * 4-bit codes, attention over it (of the newest tokens of many sequences, and of
+ * prompt chunks), rotary positions, and a linear layer with 4-bit weights and
+ * group scales for the projections.
  *
  * Conventions are those of moecache.h: every call returns moe_status_t and
  * nothing throws across the ABI; moe_last_error(NULL) describes the last
@@ -20,6 +21,17 @@
  * Only these calls change table, lens and ref of a cache in use: a length that
  * the caller lowers leaves pages behind that the next reserve does not return.
  *
+ * With MOE_KV_I4 in dtype the pages hold 4-bit codes, 0.5625 bytes a value, for
+ * queries, results and new tokens of the other part of dtype: each head of a page
+ * is an affine INT4 matrix [page_tokens][head_dim] in groups of 64 along the head,
+ * in the split-plane layout of one expert matrix (MOE_I4_G64 of moecache.h): the
+ * codes, then the bf16 pairs (s, b). k and v are then bytes,
+ * [n_layers][n_pages][n_kv_heads][page_tokens * head_dim * 9 / 16], and a value is
+ * s*q + b. Storing a group takes b = its least value and s = (its largest - b) / 15,
+ * both rounded to bf16, and q = (x - b) / s rounded to the nearest integer, ties to
+ * even, within 0..15 (0 where s is 0), in fp32. A group with an infinity, a NaN or a
+ * magnitude above 2^126 becomes NaN as a whole.
+ *
  * The cache's arrays and a call's tensors are on the current device.
  */
 #ifndef MOEKV_H
@@ -30,6 +42,9 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+/* Added to a cache's dtype: pages of 4-bit codes. */
+enum { MOE_KV_I4 = 16 };
 
 /* Device arrays of a cache, owned by the caller. */
 typedef struct {
@@ -44,8 +59,8 @@ typedef struct {
   int32_t n_pages;
   int32_t n_kv_heads;
   int32_t page_tokens; /* 16, 32, 64, 128 or 256 */
-  int32_t head_dim;    /* multiple of 8, 8..256 */
-  int32_t dtype;       /* moe_dtype_t of k and v, and of q, out and new tokens */
+  int32_t head_dim;    /* multiple of 8, 8..256; with MOE_KV_I4 of 64 */
+  int32_t dtype;       /* moe_dtype_t of k and v, and of q, out and new tokens; or that | MOE_KV_I4 */
   int32_t max_seqs;    /* 1..65536 */
   int32_t max_pages;   /* most pages of one sequence; max_pages * page_tokens <= 2^30 */
 } moe_kv_t;
@@ -98,6 +113,53 @@ moe_status_t moe_kv_write(const moe_kv_t* kv, int32_t layer, const void* k_new, 
                           int64_t ldv, const int32_t* seqs, const int32_t* cu, int32_t n, int32_t n_rows,
                           moe_stream_t stream);
 
+/* Rotary positions. The leading dim columns of a head are pairs, (x[i], x[i + dim/2])
+ * or with interleaved = 1 (x[2i], x[2i+1]), and a pair (a, b) of a token at position
+ * p becomes magnitude * (a cos t - b sin t, b cos t + a sin t), t = p * angles[i]. The
+ * columns from dim on stay. turns: device, [dim / 2], the angles in turns a position
+ * modulo 1, times 2^64 (moe_rotary_turns), so that far positions lose nothing. */
+typedef struct {
+  const uint64_t* turns;
+  int32_t dim;         /* even, 2..head size */
+  int32_t interleaved; /* 0: halves, 1: neighbours */
+  float magnitude;     /* 1 for a plain rotation */
+} moe_rotary_t;
+
+/* Angles a position, in radians: angles[i] = base^(-2i/dim) (host, [dim / 2]), for
+ * long contexts divided by factor: all of them with context = 0; else those that
+ * make at most turns_low turns within `context` tokens, while those of at least
+ * turns_high turns stay and the ones between are interpolated by their turns.
+ * moe_rotary_turns: angles (host, any finite ones) as fractions of a turn times
+ * 2^64 (host, [n]). Host only, no CUDA call. */
+moe_status_t moe_rotary_angles(int32_t dim, double base, double factor, int32_t context, double turns_low,
+                               double turns_high, double* angles);
+moe_status_t moe_rotary_turns(const double* angles, int32_t n, uint64_t* turns);
+
+/* y = x turned to pos (device int32 [n_rows], any value): x and y device
+ * [n_rows][n_heads][head_dim] (xt MOE_F32 or MOE_BF16), rows ldx and ldy elements
+ * apart and 16-byte aligned; head_dim a multiple of 8, 8..256. Arithmetic is fp32,
+ * rounded once. y may be x (with ldy = ldx), and must not overlap it otherwise. */
+moe_status_t moe_rotary(const moe_rotary_t* rot, const int32_t* pos, const void* x, int32_t xt, int64_t ldx,
+                        int32_t n_rows, int32_t n_heads, int32_t head_dim, void* y, int64_t ldy, moe_stream_t stream);
+
+/* moe_kv_write with the rotation on the way: row r of a chunk is turned to its
+ * position in its sequence, k_new into the pages (from fp32 if they hold codes) and
+ * q [n_rows][n_heads][head_dim] into q_out, which may be q (with ldqo = ldq) and
+ * must not overlap q, k_new or v_new otherwise. v_new is stored as it is. Rows that
+ * moe_kv_write would ignore or leave out are left as they are in q_out. */
+moe_status_t moe_kv_write_rotary(const moe_kv_t* kv, int32_t layer, const moe_rotary_t* rot, const void* q, int64_t ldq,
+                                 int32_t n_heads, void* q_out, int64_t ldqo, const void* k_new, int64_t ldk,
+                                 const void* v_new, int64_t ldv, const int32_t* seqs, const int32_t* cu, int32_t n,
+                                 int32_t n_rows, moe_stream_t stream);
+
+/* The newest tokens of n sequences out of their pages, shared ones too: rows cu[i] ..
+ * cu[i+1]-1 of k and v (as k_new and v_new of moe_kv_write) become the last
+ * cu[i+1]-cu[i] tokens of seqs[i]. Rows outside of cu[0] .. cu[n]-1 are left as they
+ * are, and so, with an error recorded, are those of a chunk that moe_kv_write would
+ * not store. */
+moe_status_t moe_kv_read(const moe_kv_t* kv, int32_t layer, void* k, int64_t ldk, void* v, int64_t ldv,
+                         const int32_t* seqs, const int32_t* cu, int32_t n, int32_t n_rows, moe_stream_t stream);
+
 /* Drop n sequences (device int32 [n], each once): their pages lose one
  * reference, their table rows become -1 and their lengths 0. The bytes of
  * freed pages are left as they are. All or nothing. */
@@ -121,9 +183,10 @@ moe_status_t moe_kv_copy_pages(const moe_kv_t* kv, const int32_t* src, const int
  * with the keys and values of cache head h / (n_heads / n_kv_heads). A row
  * whose position is negative sees nothing and is 0. What a row does not see
  * does not reach it, infinities and NaN included. q and out: device
- * [rows][n_heads][head_dim] of the cache's dtype, rows ldq and ldo elements
- * apart and 16-byte aligned. Scores, softmax statistics and sums are fp32;
- * for bf16 the softmax's numerators enter the value product as bf16.
+ * [rows][n_heads][head_dim] of the cache's dtype (without MOE_KV_I4), rows ldq and
+ * ldo elements apart and 16-byte aligned. Scores, softmax statistics and sums are
+ * fp32; for bf16 the softmax's numerators (over pages of codes: times a scale)
+ * enter the value product as bf16.
  *
  * moe_attn_decode: the newest n_q (1..8) tokens of each of n sequences; rows
  * i*n_q .. i*n_q+n_q-1 belong to seqs[i] (device int32 [n], n <= 65536), at
