@@ -73,6 +73,11 @@ class RotaryT(C.Structure):
     _fields_ = [("turns", C.c_void_p), ("dim", C.c_int32), ("interleaved", C.c_int32), ("magnitude", C.c_float)]
 
 
+class SamplingT(C.Structure):
+    _fields_ = [("temperature", C.c_float), ("top_p", C.c_float), ("min_p", C.c_float), ("top_k", C.c_int32),
+                ("temperatures", C.c_void_p), ("top_ps", C.c_void_p), ("min_ps", C.c_void_p), ("top_ks", C.c_void_p)]
+
+
 def _load():
     if not os.path.exists(_LIB_PATH):
         raise ImportError(
@@ -149,6 +154,7 @@ SIGNATURES = [
     ("moe_attn_decode", _st, [_kv, _i32, _vp, _i64, _vp, _i32, _i32, _i32, C.c_float, _i32, _i32, _vp, _i64, _vp]),
     ("moe_attn_prefill", _st, [_kv, _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, C.c_float, _i32, _i32, _vp, _i64,
                                _vp]),
+    ("moe_sample", _st, [_vp, _i32, _i64, _i32, _i32, _vp, C.POINTER(SamplingT), _vp, _vp, _vp]),
     ("moe_debug_attn_wait_timeout", _st, [_i64, _i32]),
     ("moe_quant_linear", _st, [_vp, _i32, _i32, _i32, _vp, _i32, _i64, _i32, _vp, _vp, _i32, _i64, _vp]),
 ]

@@ -528,3 +528,25 @@ extern "C" moe_status_t moe_quant_linear(const void* w, int32_t quant, int32_t N
     return launched(call, moe::launch_quant_linear(a, quant, sms, stream));
   });
 }
+
+extern "C" moe_status_t moe_sample(const void* logits, int32_t zt, int64_t ld, int32_t rows, int32_t V, const float* u,
+                                   const moe_sampling_t* by, int32_t* token, float* prob, moe_stream_t stream) {
+  return guarded([&] {
+    const char* call = "moe_sample";
+    if (zt != MOE_F32 && zt != MOE_BF16) return fail(MOE_ERR_ARG, call, "logits are neither MOE_F32 nor MOE_BF16");
+    if (V < 1 || V > 1 << 20) return fail(MOE_ERR_ARG, call, "V outside 1..2^20");
+    if (rows < 0 || rows > 1 << 24) return fail(MOE_ERR_ARG, call, "rows outside 0..2^24");
+    if (!by) return fail(MOE_ERR_ARG, call, "by is NULL");
+    if (rows == 0) return MOE_OK;
+    if (!logits || !u || !token) return fail(MOE_ERR_ARG, call, "logits, u or token is NULL");
+    if (ld < V) return fail(MOE_ERR_ARG, call, "ld is smaller than a row");
+    auto unaligned = [](const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) % bytes) != 0; };
+    if (unaligned(logits, elem_bytes(zt)) || unaligned(u, 4) || unaligned(token, 4) || unaligned(prob, 4) ||
+        unaligned(by->temperatures, 4) || unaligned(by->top_ks, 4) || unaligned(by->top_ps, 4) || unaligned(by->min_ps, 4))
+      return fail(MOE_ERR_ARG, call, "a pointer is not aligned to its type");
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return cuda_fail(call, e);
+    return launched(call, moe::launch_sample(logits, zt, ld, rows, V, u, *by, token, prob, sms, stream));
+  });
+}

@@ -110,6 +110,9 @@ cudaError_t launch_kv_compact(const moe_kv_t& kv, const KvLayout& l, int num_sms
 cudaError_t launch_kv_copy_pages(const moe_kv_t& kv, const KvLayout& l, const int32_t* src, const int32_t* dst,
                                  int32_t n, int num_sms, cudaStream_t st);
 
+cudaError_t launch_sample(const void* z, int32_t zt, int64_t ld, int32_t rows, int32_t V, const float* u, const moe_sampling_t& by,
+                          int32_t* token, float* prob, int num_sms, cudaStream_t st);
+
 struct LinearArgs {
   const uint8_t* w;
   const uint8_t* meta;  // scale plane

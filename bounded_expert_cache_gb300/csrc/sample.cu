@@ -1,0 +1,553 @@
+// The next token of each row of logits: temperature, top-k, top-p and min-p, drawn
+// with a given random number.
+//
+// With M the row's largest logit, token i weighs w_i = 2^-d_i, d_i = (M - z_i) log2(e) / T.
+// In the order of falling logits, ties by index, what is kept is a prefix: the first
+// k; of these the shortest with top_p of their weight; of these those with w >= min_p.
+// The token is the first, by index, up to which the kept weights exceed u times
+// their sum.
+//
+// Which token u falls on is decided by sums over the whole vocabulary, so they must
+// not depend on the order of adding, nor be off by what fp32 sums are. Weights are
+// whole numbers of 2^-43: sums of them in 64 bits are exact in any order. A weight's
+// own error is about 2^-31 of it: d is formed as a pair of fp32 (2^-34), cut into a
+// whole n, a multiple a of 2^-8 and a rest r, and 2^-d = 2^-n 2^-a (1 + (2^-r - 1))
+// takes 2^-a from a table and the rest from its power series.
+//
+// One cluster of CTAs a row. Each holds a slice of the row in shared memory, so the
+// logits are read once. The end of the prefix is found by histograms (tokens, weight)
+// over 1,024 bins: first of d; then, within the bin that holds the end, of the place
+// in the order, (logit, index) as one number, ten bits a round, until the end is
+// decided: mostly one round. Bins that cannot hold it are left out: with top-k those
+// behind the k-th largest of the threads' own maxima; with top-p tokens of less than
+// (1 - top_p) / V of the weight, which all together are no more than what is cut off.
+//
+// What bounds it: few rows the passes' and cluster barriers' latency; many the issue
+// of the weights' arithmetic (some 40 instructions a token where all weights count).
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "kv.h"
+
+namespace cg = cooperative_groups;
+
+namespace moe {
+namespace {
+
+constexpr int kSampleThreads = 512, kSampleWarps = kSampleThreads / 32;
+constexpr int kBins = 1024, kMostCtas = 8;
+constexpr int kFraction = 43;  // weights are whole numbers of 2^-43
+constexpr float kReach = 44.f;  // weights from here on are none
+constexpr float kBinsPer = kBins / kReach;
+constexpr int kIndexBits = 20;
+
+// 2^-(i - 128) / 256 times 2^31
+struct PowerTable {
+  uint32_t p[257];
+};
+
+struct Hist {
+  uint32_t count[kBins];
+  unsigned long long weight[kBins];
+};
+// What a search round starts from, or its result.
+struct Search {
+  int bin;               // the end's bin of d
+  int shift;             // of the round's digits
+  unsigned long long lo, hi;  // the end's place is in [lo, hi]
+  unsigned long long before, bin_before;  // weight of the tokens before lo, and before the bin
+  unsigned int n_before, bin_n;           // and their number
+  int done;              // 1: the end is decided: bin and hi; 2: there is none, all are kept
+  unsigned long long sum;     // then: the weight kept
+  unsigned int kept;          // and the number
+};
+struct SampleShared {
+  Hist first, next;
+  uint32_t maxima[kBins];
+  unsigned long long chunk[kMostCtas * kSampleWarps];
+  unsigned long long best[kMostCtas], sum[kMostCtas];
+  unsigned long long warp64[kSampleWarps];
+  unsigned int warp32[kSampleWarps];
+  unsigned long long found64;
+  int found;
+  Search search;
+  float c_hi, c_lo;
+  uint32_t power[257];
+};
+
+__device__ __forceinline__ uint32_t order_key(float z) {
+  const uint32_t u = __float_as_uint(z);
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
+// place in the order: falling logits, ties by index
+__device__ __forceinline__ unsigned long long place(float z, int i) {
+  return static_cast<unsigned long long>(~order_key(z)) << kIndexBits | static_cast<unsigned int>(i);
+}
+
+struct Row {
+  float top, c_hi, c_lo;
+  const uint32_t* power;
+  // bin of d; kBins: no weight. Does not fall as z falls.
+  __device__ __forceinline__ int bin(float z) const {
+    if (z == top) return 0;
+    const float d = (top - z) * c_hi;
+    return d < kReach ? min(static_cast<int>(d * kBinsPer), kBins - 1) : kBins;
+  }
+  // weight of a token with bin(z) < kBins
+  __device__ __forceinline__ unsigned long long weight(float z) const {
+    if (z == top) return 1ull << kFraction;
+    // top - z, and the rest of its rounding
+    const float d0 = top - z, zz = top - d0, rest = (top - (d0 + zz)) + (zz - z);
+    const float p = d0 * c_hi;
+    const float e = fmaf(d0, c_hi, -p) + (d0 * c_lo + rest * c_hi);
+    constexpr float kWhole = 12582912.f;        // 1.5 * 2^23: adding it rounds to a whole number
+    constexpr float kPart = 49152.f;            // 1.5 * 2^15: to a multiple of 2^-8
+    const float n = p + kWhole, f = p - (n - kWhole);
+    const float a = f + kPart, r = (f - (a - kPart)) + e;
+    const uint32_t t = power[__float_as_int(a) - 0x47400000 + 128];  // (0x47400000: kPart)
+    constexpr float kLn2 = 0.693147181f;
+    const float x = r * -kLn2;  // 2^-r = e^x, |x| < 2^-9
+    const float q = x * fmaf(x, fmaf(x, 1.f / 6.f, 0.5f), 1.f);
+    const float add = static_cast<float>(t) * q + kWhole;  // below 2^22
+    const uint32_t w = t + (__float_as_uint(add) - 0x4B400000u);
+    const int by = __float_as_int(n) - 0x4B400000;
+    return (static_cast<unsigned long long>(w) << (kFraction - 31)) >> by;
+  }
+};
+
+__device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
+#pragma unroll
+  for (int x = 16; x; x >>= 1) v += __shfl_xor_sync(~0u, v, x);
+  return v;
+}
+// inclusive over the block's threads, in order
+template <class T>
+__device__ __forceinline__ T block_scan_incl(T v, T* tmp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const T y = __shfl_up_sync(~0u, v, d);
+    if (lane >= d) v += y;
+  }
+  if (lane == 31) tmp[warp] = v;
+  __syncthreads();
+  T below = 0;
+  for (int w = 0; w < warp; ++w) below += tmp[w];
+  __syncthreads();
+  return v + below;
+}
+
+struct SampleArgs {
+  const void* z;
+  int64_t ld;
+  int V;
+  const float* u;
+  moe_sampling_t by;
+  int32_t* token;
+  float* prob;
+  int slice;   // tokens a CTA, a multiple of 512
+  int staged;  // of them in shared memory
+};
+
+__device__ __forceinline__ float clean(float z) { return z != z ? -INFINITY : z + 0.f; }  // NaN: never; -0 is 0
+template <class T>
+__device__ __forceinline__ float logit(const SampleArgs& a, int row, int i) {
+  return clean(static_cast<float>(__ldg(static_cast<const T*>(a.z) + row * a.ld + i)));
+}
+
+// u times s, rounded down; u in [0, 1)
+__device__ __forceinline__ unsigned long long share_of(float u, unsigned long long s, bool up) {
+  const unsigned long long f = u <= 0.f ? 0ull : static_cast<unsigned long long>(static_cast<double>(u) * 18446744073709551616.0);
+  return __umul64hi(f, s) + (up && f * s != 0ull);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kSampleThreads)
+    sample_kernel(const __grid_constant__ SampleArgs a, const __grid_constant__ PowerTable table) {
+  extern __shared__ __align__(16) unsigned char sm_raw[];
+  SampleShared& sh = *reinterpret_cast<SampleShared*>(sm_raw);
+  float* const held = reinterpret_cast<float*>(sm_raw + sizeof(SampleShared));
+  auto cluster = cg::this_cluster();
+  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int row = blockIdx.x / C;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // this warp's tokens: [w0, w0 + per) of the slice
+  const int slice0 = rank * a.slice, per = a.slice / kSampleWarps, w0 = warp * per;
+  const int n_mine = max(0, min(per, a.V - slice0 - w0));
+  const float temperature = a.by.temperatures ? a.by.temperatures[row] : a.by.temperature;
+  const int top_k = a.by.top_ks ? a.by.top_ks[row] : a.by.top_k;
+  const float top_p = a.by.top_ps ? a.by.top_ps[row] : a.by.top_p;
+  const float min_p = a.by.min_ps ? a.by.min_ps[row] : a.by.min_p;
+  const float u = a.u[row];
+  const bool k_on = top_k > 0 && top_k < a.V, p_on = top_p < 1.f;
+
+  for (int i = tid; i < kBins; i += kSampleThreads) {
+    sh.first.count[i] = sh.next.count[i] = sh.maxima[i] = 0u;
+    sh.first.weight[i] = sh.next.weight[i] = 0ull;
+  }
+  for (int i = tid; i < 257; i += kSampleThreads) sh.power[i] = table.p[i];
+  if (tid == 0) {
+    const double c = 1.4426950408889634074 / static_cast<double>(temperature);
+    sh.c_hi = static_cast<float>(c);
+    sh.c_lo = isfinite(sh.c_hi) ? static_cast<float>(c - static_cast<double>(sh.c_hi)) : 0.f;
+  }
+
+  // ---- the slice, and the first in the order
+  float mine = -INFINITY;
+  int mine_i = 0;
+#pragma unroll 8
+  for (int j = lane; j < n_mine; j += 32) {
+    const int i = slice0 + w0 + j;
+    const float z = logit<T>(a, row, i);
+    if (w0 + j < a.staged) held[w0 + j] = z;
+    if (z > mine) {
+      mine = z;
+      mine_i = i;
+    }
+  }
+  {
+    unsigned long long b = place(mine, mine == -INFINITY ? (1 << kIndexBits) - 1 : mine_i);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) b = min(b, __shfl_xor_sync(~0u, b, x));
+    if (lane == 0) sh.warp64[warp] = b;
+    __syncthreads();
+    if (warp == 0) {
+      b = sh.warp64[lane & (kSampleWarps - 1)];
+#pragma unroll
+      for (int x = 8; x; x >>= 1) b = min(b, __shfl_xor_sync(~0u, b, x));
+      if (lane < C) *cluster.map_shared_rank(&sh.best[rank], lane) = b;
+    }
+  }
+  cluster.sync();
+  unsigned long long best = sh.best[0];
+  for (int i = 1; i < C; ++i) best = min(best, sh.best[i]);
+  Row r;
+  r.top = of_key(~static_cast<uint32_t>(best >> kIndexBits));
+  r.c_hi = sh.c_hi;
+  r.c_lo = sh.c_lo;
+  r.power = sh.power;
+  // nothing to choose from, or nothing to choose
+  if (r.top == -INFINITY || !(temperature > 0.f) || top_k == 1) {
+    if (rank == 0 && tid == 0) {
+      const bool none = r.top == -INFINITY;
+      a.token[row] = none ? -1 : static_cast<int32_t>(best & ((1u << kIndexBits) - 1));
+      if (a.prob) a.prob[row] = none ? 0.f : 1.f;
+    }
+    return;  // (every CTA's stores to the others were before the barrier)
+  }
+  auto each = [&](auto&& f) {  // f(logit, index) of this warp's tokens, a lane every 32nd
+#pragma unroll 4
+    for (int j = lane; j < n_mine; j += 32) {
+      const int i = slice0 + w0 + j;
+      f(w0 + j < a.staged ? held[w0 + j] : logit<T>(a, row, i), i);
+    }
+  };
+  auto share_sum = [&](unsigned long long v) {  // over the cluster
+    v = warp_sum(v);
+    if (lane == 0) sh.warp64[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+      v = warp_sum(lane < kSampleWarps ? sh.warp64[lane] : 0ull);
+      if (lane < C) *cluster.map_shared_rank(&sh.sum[rank], lane) = v;
+    }
+    cluster.sync();
+    v = 0;
+    for (int i = 0; i < C; ++i) v += sh.sum[i];
+    return v;
+  };
+  SampleShared& lead = *cluster.map_shared_rank(&sh, 0);
+  auto tell = [&](auto* field, auto v) {  // every CTA, by the first one's first threads
+    if (tid < C) *cluster.map_shared_rank(field, tid) = v;
+  };
+
+  int end_bin = kBins - 1;                   // kept: bin <= end_bin and place <= end
+  unsigned long long end = ~0ull;
+  if (k_on || p_on) {
+    // ---- bins that can hold the end
+    int most = kBins - 1;
+    unsigned long long sum = 0;  // all weight, where top-p needs it
+    if (k_on) {
+      const int b = mine == -INFINITY ? kBins : r.bin(mine);
+      if (b < kBins) atomicAdd(&lead.maxima[b], 1u);
+      cluster.sync();
+      if (rank == 0) {
+        const uint32_t n0 = sh.maxima[2 * tid], n1 = sh.maxima[2 * tid + 1];
+        const uint32_t upto = block_scan_incl(n0 + n1, sh.warp32);
+        if (tid == 0) sh.found = kBins - 1;
+        __syncthreads();
+        const uint32_t k = static_cast<uint32_t>(top_k);
+        if (upto >= k && upto - n0 - n1 < k) sh.found = upto - n1 >= k ? 2 * tid : 2 * tid + 1;
+        __syncthreads();
+        const int f = sh.found;
+        __syncthreads();
+        tell(&sh.found, f);
+      }
+      cluster.sync();
+      most = sh.found;
+    } else {
+      unsigned long long v = 0;
+      each([&](float z, int) {
+        if (r.bin(z) < kBins) v += r.weight(z);
+      });
+      sum = share_sum(v);
+      const float d = log2f(static_cast<float>(a.V)) + static_cast<float>(kFraction) - log2f((1.f - fmaxf(top_p, 0.f)) * static_cast<float>(sum));
+      most = static_cast<int>(fminf(fmaxf(d * kBinsPer, 0.f) + 2.f, kBins - 1.f));
+    }
+    // ---- tokens and weight by bins of d
+    each([&](float z, int) {
+      const int b = r.bin(z);
+      if (b <= most) {
+        atomicAdd(&sh.first.count[b], 1u);
+        atomicAdd(&sh.first.weight[b], r.weight(z));
+      }
+    });
+    auto merge = [&](Hist& h, Hist& to) {  // into the first CTA's
+      __syncthreads();
+      if (rank > 0)
+        for (int i = tid; i < kBins; i += kSampleThreads)
+          if (h.count[i]) {
+            atomicAdd(&to.count[i], h.count[i]);
+            atomicAdd(&to.weight[i], h.weight[i]);
+          }
+      cluster.sync();
+    };
+    merge(sh.first, lead.first);
+    // ---- one search after the other: by number, then by weight
+    bool cut_k = false;
+#pragma unroll 1
+    for (int by_weight = 0; by_weight < 2; ++by_weight) {
+      if (by_weight ? !p_on : !k_on) continue;
+      // round 0 is over bins of d, later ones over places
+      unsigned long long goal = 0;  // the end is where the number or weight reaches it
+#pragma unroll 1
+      for (int round = 0;; ++round) {
+        if (rank == 0) {
+          Hist& h = round == 0 ? sh.first : sh.next;
+          if (round == 0 && by_weight) {
+            if (cut_k) {  // what top-k has left of its last bin
+              __syncthreads();
+              if (tid == 0) {
+                sh.first.weight[end_bin] = sh.search.sum - sh.search.bin_before;
+                sh.first.count[end_bin] = sh.search.kept - sh.search.bin_n;
+              }
+            }
+          }
+          if (round == 0) goal = by_weight ? max(share_of(top_p, sum, true), 1ull) : static_cast<unsigned long long>(top_k);
+          __syncthreads();
+          uint32_t n0 = h.count[2 * tid], n1 = h.count[2 * tid + 1];
+          unsigned long long s0 = h.weight[2 * tid], s1 = h.weight[2 * tid + 1];
+          if (round == 0 && cut_k) {
+            if (2 * tid > end_bin) n0 = 0, s0 = 0;
+            if (2 * tid + 1 > end_bin) n1 = 0, s1 = 0;
+          }
+          const uint32_t nb = round == 0 ? 0u : sh.search.n_before;
+          const unsigned long long sb = round == 0 ? 0ull : sh.search.before;
+          const uint32_t n = nb + block_scan_incl(n0 + n1, sh.warp32);
+          const unsigned long long s = sb + block_scan_incl(s0 + s1, sh.warp64);
+          if (tid == 0) sh.found = 0;
+          __syncthreads();
+          // the bin in which the goal is reached
+          const unsigned long long after = by_weight ? s : n, m0 = by_weight ? s0 : n0, m1 = by_weight ? s1 : n1;
+          const bool here = after >= goal && after - m0 - m1 < goal && m0 + m1 > 0;
+          if (here) {
+            const bool second = after - m1 < goal;
+            const int b = 2 * tid + second;
+            Search q = sh.search;
+            q.n_before = second ? n - n1 : n - n0 - n1;
+            q.before = second ? s - s1 : s - s0 - s1;
+            const uint32_t in = second ? n1 : n0;
+            const unsigned long long weight_in = second ? s1 : s0;
+            if (round == 0) {
+              q.bin_n = q.n_before;
+              q.bin_before = q.before;
+              // the bin's logits, with room for rounding
+              q.bin = b;
+              const float per_bin = 1.f / (kBinsPer * r.c_hi), room = fabsf(r.top) * 0x1p-20f + per_bin * 0.01f;
+              q.lo = b == 0 ? 0ull : place(r.top - per_bin * b + room, 0);
+              q.hi = place(fmaxf(r.top - per_bin * (b + 1) - room, -3.402823466e38f), (1 << kIndexBits) - 1);
+            } else {
+              const unsigned long long lo = q.lo + (static_cast<unsigned long long>(b) << q.shift);
+              q.hi = min(q.hi, lo + (1ull << q.shift) - 1);
+              q.lo = lo;
+            }
+            // one token, or all of the bin's: no need to look closer
+            q.done = in == 1 || (!by_weight && q.n_before + in == goal) || (round > 0 && q.shift == 0);
+            q.sum = q.before + weight_in;
+            q.kept = q.n_before + in;
+            if (q.lo >> kIndexBits == q.hi >> kIndexBits)
+              q.hi = min(q.hi, (q.hi >> kIndexBits << kIndexBits) + static_cast<unsigned int>(a.V - 1));
+            q.shift = max(0, 54 - __clzll(static_cast<long long>(q.hi - q.lo) | 1));
+            sh.search = q;
+            sh.found = 1;
+          }
+          __syncthreads();
+          if (tid == 0 && !sh.found) {  // fewer tokens than k have weight
+            Search q = sh.search;
+            q.bin = kBins - 1;
+            q.lo = 0;
+            q.hi = ~0ull;
+            q.done = 2;
+            sh.search = q;
+          }
+          if (tid == kSampleThreads - 1) sh.found64 = s;  // all weight (round 0)
+          __syncthreads();
+          if (sh.search.done == 2 && tid == 0) sh.search.sum = sh.found64;
+          for (int i = tid; i < kBins; i += kSampleThreads) {
+            sh.next.count[i] = 0u;
+            sh.next.weight[i] = 0ull;
+          }
+          __syncthreads();
+          const Search q = sh.search;
+          if (tid > 0 && tid < C) *cluster.map_shared_rank(&sh.search, tid) = q;
+        } else {
+          for (int i = tid; i < kBins; i += kSampleThreads) {
+            sh.next.count[i] = 0u;
+            sh.next.weight[i] = 0ull;
+          }
+        }
+        cluster.sync();
+        const Search q = sh.search;
+        if (q.done) break;
+        each([&](float z, int i) {
+          if (r.bin(z) != q.bin) return;
+          const unsigned long long at = place(z, i);
+          if (at < q.lo || at > q.hi || (q.bin == end_bin && at > end)) return;
+          const int d = static_cast<int>((at - q.lo) >> q.shift);
+          atomicAdd(&sh.next.count[d], 1u);
+          atomicAdd(&sh.next.weight[d], r.weight(z));
+        });
+        merge(sh.next, lead.next);
+      }
+      const Search q = sh.search;
+      if (q.done == 1) {
+        end = q.bin == end_bin ? min(end, q.hi) : q.hi;
+        end_bin = q.bin;
+      }
+      cut_k = q.done == 1;
+      if (!by_weight) sum = q.sum;
+      cluster.sync();  // the search is read before the next one's is written
+    }
+  }
+
+  // ---- weights kept, by the cluster's warps in the order of the vocabulary
+  const unsigned long long least =
+      min_p > 0.f ? static_cast<unsigned long long>(ceil(fmin(static_cast<double>(min_p), 1.0) * static_cast<double>(1ull << kFraction))) : 0ull;
+  auto kept = [&](float z, int i) -> unsigned long long {
+    const int b = r.bin(z);
+    if (b > end_bin || (b == end_bin && place(z, i) > end)) return 0ull;
+    const unsigned long long w = r.weight(z);
+    return w >= least ? w : 0ull;
+  };
+  unsigned long long v = 0;
+  each([&](float z, int i) { v += kept(z, i); });
+  v = warp_sum(v);
+  if (lane < C) *cluster.map_shared_rank(&sh.chunk[rank * kSampleWarps + warp], lane) = v;
+  cluster.sync();
+  // (no CTA stores to another's shared memory from here on)
+  unsigned long long total = 0, to_cta = 0;
+  for (int i = lane; i < C * kSampleWarps; i += 32) {
+    total += sh.chunk[i];
+    if (i < rank * kSampleWarps) to_cta += sh.chunk[i];
+  }
+  total = warp_sum(total);
+  to_cta = warp_sum(to_cta);
+  const unsigned long long goal = min(u < 1.f ? share_of(u, total, false) : ~0ull, total - 1);  // the first sum above it
+  unsigned long long at = to_cta;  // before chunk c of this CTA
+  int c = 0;
+  for (; c < kSampleWarps; ++c) {
+    const unsigned long long x = sh.chunk[rank * kSampleWarps + c];
+    if (goal < at + x) break;
+    at += x;
+  }
+  if (goal < to_cta || c == kSampleWarps) return;
+  // ---- the token's warp chunk, cut between the CTA's warps
+  const int part = ((per + kSampleWarps - 1) / kSampleWarps + 31) / 32 * 32, p0 = c * per + warp * part;
+  const int p1 = min(c * per + per, p0 + part);
+  auto weight_at = [&](int j) -> unsigned long long {
+    const int i = slice0 + j;
+    if (j >= p1 || i >= a.V) return 0ull;
+    return kept(j < a.staged ? held[j] : logit<T>(a, row, i), i);
+  };
+  v = 0;
+  for (int j = p0 + lane; j < p1; j += 32) v += weight_at(j);
+  v = warp_sum(v);
+  __syncthreads();
+  if (lane == 0) sh.warp64[warp] = v;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) at += sh.warp64[w];
+  if (goal < at || goal >= at + v) return;
+  for (int j0 = p0; j0 < p1; j0 += 32) {
+    const unsigned long long w = weight_at(j0 + lane);
+    unsigned long long x = w;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const unsigned long long y = __shfl_up_sync(~0u, x, d);
+      if (lane >= d) x += y;
+    }
+    const unsigned int above = __ballot_sync(~0u, at + x > goal);
+    if (above) {
+      if (lane == __ffs(above) - 1) {
+        a.token[row] = slice0 + j0 + lane;
+        if (a.prob) a.prob[row] = static_cast<float>(static_cast<double>(w) / static_cast<double>(total));
+      }
+      return;
+    }
+    at += __shfl_sync(~0u, x, 31);
+  }
+}
+
+const PowerTable& powers() {
+  static const PowerTable t = [] {
+    PowerTable p;
+    for (int i = 0; i < 257; ++i) p.p[i] = static_cast<uint32_t>(std::llround(std::ldexp(std::exp2(-(i - 128) / 256.0), 31)));
+    return p;
+  }();
+  return t;
+}
+
+template <class T>
+cudaError_t sample(SampleArgs a, int rows, int num_sms, cudaStream_t st) {
+  // CTAs a row: slices of 16,384 tokens at most, and smaller ones, down to 2,048,
+  // while there are SMs without a CTA
+  int ctas = 1;
+  while (ctas < kMostCtas && (a.V > 16384 * ctas || (static_cast<int64_t>(rows) * ctas < num_sms && a.V >= 4096 * ctas))) ctas *= 2;
+  const int each = (a.V + ctas - 1) / ctas;
+  a.slice = (each + kSampleThreads - 1) / kSampleThreads * kSampleThreads;
+  constexpr int kMostSmem = 227 * 1024;
+  a.staged = std::min(a.slice, (kMostSmem - static_cast<int>(sizeof(SampleShared))) / 4);
+  const int smem = static_cast<int>(sizeof(SampleShared)) + a.staged * 4;
+  cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows) * ctas);
+  cfg.blockDim = dim3(kSampleThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a, powers());
+}
+
+}  // namespace
+
+cudaError_t launch_sample(const void* z, int32_t zt, int64_t ld, int32_t rows, int32_t V, const float* u, const moe_sampling_t& by,
+                          int32_t* token, float* prob, int num_sms, cudaStream_t st) {
+  SampleArgs a{};
+  a.z = z;
+  a.ld = ld;
+  a.V = V;
+  a.u = u;
+  a.by = by;
+  a.token = token;
+  a.prob = prob;
+  return zt == MOE_F32 ? sample<float>(a, rows, num_sms, st) : sample<__nv_bfloat16>(a, rows, num_sms, st);
+}
+
+}  // namespace moe

@@ -1,4 +1,4 @@
-"""Paged key-value cache, attention over it, rotary positions and the 4-bit linear layer: the
+"""Paged key-value cache, attention over it, rotary positions, the 4-bit linear layer and sampling: the
 binding of include/moekv.h. PyTorch supplies device memory and streams; every
 step runs in the library's CUDA kernels.
 """
@@ -383,3 +383,41 @@ def quant_linear(x: torch.Tensor, w: torch.Tensor, quant: int, n_out: int, bias:
          None if bias is None else bias.data_ptr(), y.data_ptr(), _dtype_id(y.dtype), ldy,
          _raw_stream(device) if stream is None else stream.cuda_stream)
     return y
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=None, prob=None,
+           stream=None):
+    """Draw one token of each row of logits [rows, V] (float32 or bfloat16, rows may lie apart) with u [rows] in [0, 1).
+
+    temperature, top_p and min_p are numbers or float32 CUDA tensors [rows], top_k an
+    integer or an int32 one. Kept are the top_k largest logits, of these the fewest
+    with top_p of their weight, of these those of at least min_p times the largest's.
+    The token is the first, by index, up to which their weights exceed u times the sum.
+    Returns (token int32 [rows], prob float32 [rows]), new ones if None.
+    """
+    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a [rows, V] CUDA tensor with dense rows")
+    zt = _dtype_id(logits.dtype)
+    device = logits.get_device()
+    rows, V = logits.shape
+
+    def column(t, name, dtype):
+        if t.dtype != dtype or t.dim() != 1 or t.shape[0] != rows or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {rows} entries")
+        if t.get_device() != device:
+            raise _elsewhere(t, name, device)
+        return t.data_ptr()
+
+    by = N.SamplingT()
+    for value, name, dtype in ((temperature, "temperature", torch.float32), (top_p, "top_p", torch.float32),
+                               (min_p, "min_p", torch.float32), (top_k, "top_k", torch.int32)):
+        if isinstance(value, torch.Tensor):
+            setattr(by, name + "s", column(value, name, dtype))
+        else:
+            setattr(by, name, min(max(int(value), 0), _MOST) if name == "top_k" else float(value))
+    token = _new((rows,), torch.int32, logits.device, stream) if token is None else token
+    prob = _new((rows,), torch.float32, logits.device, stream) if prob is None else prob
+    _run(device, lib.moe_sample, logits.data_ptr(), zt, logits.stride(0) if rows > 1 else V, rows, V,
+         column(u, "u", torch.float32), C.byref(by), column(token, "token", torch.int32), column(prob, "prob", torch.float32),
+         _raw_stream(device) if stream is None else stream.cuda_stream)
+    return token, prob

@@ -2,8 +2,8 @@
  * moekv.h — the operators a decoder layer needs beside the routed FFN of
  * moecache.h: a paged key-value cache with its page bookkeeping, in values or in
  * 4-bit codes, attention over it (of the newest tokens of many sequences, and of
- * prompt chunks), rotary positions, and a linear layer with 4-bit weights and
- * group scales for the projections.
+ * prompt chunks), rotary positions, a linear layer with 4-bit weights and group
+ * scales for the projections, and the draw of the next token from its logits.
  *
  * Conventions are those of moecache.h: every call returns moe_status_t and
  * nothing throws across the ABI; moe_last_error(NULL) describes the last
@@ -231,6 +231,36 @@ moe_status_t moe_debug_attn_wait_timeout(int64_t wait_cycles, int32_t copies);
 moe_status_t moe_quant_linear(const void* w, int32_t quant, int32_t N, int32_t K, const void* x, int32_t xt,
                               int64_t ldx, int32_t T, const float* bias, void* y, int32_t yt, int64_t ldy,
                               moe_stream_t stream);
+
+/* How moe_sample draws: one value for all rows, or device arrays [rows] (NULL: the
+ * value). Of a row's tokens in the order of falling logits, ties by index, a prefix
+ * is kept:
+ *   temperature T: token i weighs exp((z_i - max z) / T). 0, less or NaN: the first
+ *     token of the order is the row's.
+ *   top_k: the first k tokens; off if 0 or less, or the number of tokens or more.
+ *   top_p: of those the shortest prefix with at least top_p of their weight; at least
+ *     one token; off if 1 or more (or NaN).
+ *   min_p: of those the ones that weigh at least min_p times the first; off if 0 or
+ *     less, 1 if more. */
+typedef struct {
+  float temperature, top_p, min_p;
+  int32_t top_k;
+  const float* temperatures;
+  const float* top_ps;
+  const float* min_ps;
+  const int32_t* top_ks;
+} moe_sampling_t;
+
+/* Draw one token of each row: the first, by index, up to which the kept weights
+ * exceed u[row] times their sum. logits: device [rows][V] (zt MOE_F32 or MOE_BF16),
+ * rows ld elements apart, aligned to their type; 1 <= V <= 2^20. u: device [rows], in
+ * [0, 1). token: device int32 [rows]; prob: device [rows], the token's share of the
+ * kept weight, or NULL. A NaN counts as -inf. Infinite logits share all the weight. A
+ * row without a logit above -inf gets token -1 and probability 0. Weights are formed
+ * to about 2^-31 of themselves, down to 2^-43 of the first, and added without
+ * rounding, so a result does not depend on how the work is split. */
+moe_status_t moe_sample(const void* logits, int32_t zt, int64_t ld, int32_t rows, int32_t V, const float* u,
+                        const moe_sampling_t* by, int32_t* token, float* prob, moe_stream_t stream);
 
 #ifdef __cplusplus
 }
