@@ -539,7 +539,7 @@ extern "C" moe_status_t moe_sample(const void* logits, int32_t zt, int64_t ld, i
     if (!by) return fail(MOE_ERR_ARG, call, "by is NULL");
     if (rows == 0) return MOE_OK;
     if (!logits || !u || !token) return fail(MOE_ERR_ARG, call, "logits, u or token is NULL");
-    if (ld < V) return fail(MOE_ERR_ARG, call, "ld is smaller than a row");
+    if (ld < V && ld != 0) return fail(MOE_ERR_ARG, call, "ld is smaller than a row, and not 0");
     auto unaligned = [](const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) % bytes) != 0; };
     if (unaligned(logits, elem_bytes(zt)) || unaligned(u, 4) || unaligned(token, 4) || unaligned(prob, 4) ||
         unaligned(by->temperatures, 4) || unaligned(by->top_ks, 4) || unaligned(by->top_ps, 4) || unaligned(by->min_ps, 4))

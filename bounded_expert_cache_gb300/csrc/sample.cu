@@ -87,20 +87,21 @@ __device__ __forceinline__ unsigned long long place(float z, int i) {
   return static_cast<unsigned long long>(~order_key(z)) << kIndexBits | static_cast<unsigned int>(i);
 }
 
+// Differences of logits are halved, which loses nothing and does not overflow; c is 2 log2(e) / T.
 struct Row {
-  float top, c_hi, c_lo;
+  float top, half, c_hi, c_lo;
   const uint32_t* power;
   // bin of d; kBins: no weight. Does not fall as z falls.
   __device__ __forceinline__ int bin(float z) const {
     if (z == top) return 0;
-    const float d = (top - z) * c_hi;
+    const float d = fmaf(z, -0.5f, half) * c_hi;
     return d < kReach ? min(static_cast<int>(d * kBinsPer), kBins - 1) : kBins;
   }
   // weight of a token with bin(z) < kBins
   __device__ __forceinline__ unsigned long long weight(float z) const {
     if (z == top) return 1ull << kFraction;
-    // top - z, and the rest of its rounding
-    const float d0 = top - z, zz = top - d0, rest = (top - (d0 + zz)) + (zz - z);
+    // (top - z) / 2, and the rest of its rounding
+    const float y = 0.5f * z, d0 = half - y, yy = half - d0, rest = (half - (d0 + yy)) + (yy - y);
     const float p = d0 * c_hi;
     const float e = fmaf(d0, c_hi, -p) + (d0 * c_lo + rest * c_hi);
     constexpr float kWhole = 12582912.f;        // 1.5 * 2^23: adding it rounds to a whole number
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kSampleThreads)
   }
   for (int i = tid; i < 257; i += kSampleThreads) sh.power[i] = table.p[i];
   if (tid == 0) {
-    const double c = 1.4426950408889634074 / static_cast<double>(temperature);
+    const double c = 2.8853900817779268148 / static_cast<double>(temperature);
     sh.c_hi = static_cast<float>(c);
     sh.c_lo = isfinite(sh.c_hi) ? static_cast<float>(c - static_cast<double>(sh.c_hi)) : 0.f;
   }
@@ -226,6 +227,7 @@ __global__ void __launch_bounds__(kSampleThreads)
   for (int i = 1; i < C; ++i) best = min(best, sh.best[i]);
   Row r;
   r.top = of_key(~static_cast<uint32_t>(best >> kIndexBits));
+  r.half = 0.5f * r.top;
   r.c_hi = sh.c_hi;
   r.c_lo = sh.c_lo;
   r.power = sh.power;
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(kSampleThreads)
               q.bin_before = q.before;
               // the bin's logits, with room for rounding
               q.bin = b;
-              const float per_bin = 1.f / (kBinsPer * r.c_hi), room = fabsf(r.top) * 0x1p-20f + per_bin * 0.01f;
+              const float per_bin = 2.f / (kBinsPer * r.c_hi), room = fabsf(r.top) * 0x1p-20f + per_bin * 0.01f;
               q.lo = b == 0 ? 0ull : place(r.top - per_bin * b + room, 0);
               q.hi = place(fmaxf(r.top - per_bin * (b + 1) - room, -3.402823466e38f), (1 << kIndexBits) - 1);
             } else {

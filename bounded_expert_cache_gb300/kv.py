@@ -411,7 +411,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     by = N.SamplingT()
     for value, name, dtype in ((temperature, "temperature", torch.float32), (top_p, "top_p", torch.float32),
                                (min_p, "min_p", torch.float32), (top_k, "top_k", torch.int32)):
-        if isinstance(value, torch.Tensor):
+        if hasattr(value, "data_ptr"):
             setattr(by, name + "s", column(value, name, dtype))
         else:
             setattr(by, name, min(max(int(value), 0), _MOST) if name == "top_k" else float(value))

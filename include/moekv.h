@@ -253,7 +253,7 @@ typedef struct {
 
 /* Draw one token of each row: the first, by index, up to which the kept weights
  * exceed u[row] times their sum. logits: device [rows][V] (zt MOE_F32 or MOE_BF16),
- * rows ld elements apart, aligned to their type; 1 <= V <= 2^20. u: device [rows], in
+ * rows ld elements apart (0: one row for all), aligned to their type; 1 <= V <= 2^20. u: device [rows], in
  * [0, 1). token: device int32 [rows]; prob: device [rows], the token's share of the
  * kept weight, or NULL. A NaN counts as -inf. Infinite logits share all the weight. A
  * row without a logit above -inf gets token -1 and probability 0. Weights are formed
