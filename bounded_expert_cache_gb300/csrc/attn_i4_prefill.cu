@@ -1,5 +1,6 @@
-// Attention of prompt chunks over pages of 4-bit codes: row tiles of the engine of
-// attn_i4.cuh, one a CTA.
+// Attention of prompt chunks over pages of 4-bit codes in f32 and of heads above 128:
+// row tiles of the engine of attn_i4.cuh, one a CTA. (bf16 heads of 64 and 128 run on
+// the 5th-generation tensor cores, attn_prefill.cu.)
 #include "attn_i4.cuh"
 
 namespace moe {
@@ -13,10 +14,11 @@ cudaError_t chunks(const AttnArgs& a, cudaStream_t st) {
 }
 template <class T>
 cudaError_t prefill_of(const AttnArgs& a, cudaStream_t st) {
-  constexpr int kNR = sizeof(T) == 4 ? 2 : 4;
+  if constexpr (sizeof(T) == 4) {
+    if (a.D == 64) return chunks<CodesEngine<T, 1, 2, 256>>(a, st);
+    if (a.D == 128) return chunks<CodesEngine<T, 2, 2, 256>>(a, st);
+  }
   switch (a.D / 64) {
-    case 1: return chunks<CodesEngine<T, 1, kNR, 256>>(a, st);
-    case 2: return chunks<CodesEngine<T, 2, kNR, 256>>(a, st);
     case 3: return chunks<CodesEngine<T, 3, 2, 128>>(a, st);
     default: return chunks<CodesEngine<T, 4, 2, 128>>(a, st);
   }
@@ -24,7 +26,8 @@ cudaError_t prefill_of(const AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_attn_prefill_codes(const AttnArgs& a, int32_t dtype, cudaStream_t st) {
+cudaError_t launch_attn_prefill_codes(const AttnArgs& a, int32_t dtype, int num_sms, cudaStream_t st) {
+  if (dtype == MOE_BF16 && a.D <= kTcHeadDim) return launch_attn_prefill_codes_tc(a, num_sms, st);
   return dtype == MOE_F32 ? prefill_of<float>(a, st) : prefill_of<__nv_bfloat16>(a, st);
 }
 

@@ -48,6 +48,7 @@
 // Every wait is bounded, as in the prefill GEMMs: on a time-out all roles leave
 // their loops, copies and MMAs in flight are drained, an error is recorded.
 #include <cuda.h>
+#include <cuda_fp16.h>
 
 #include "attn.cuh"
 #include "pdl.cuh"
@@ -59,7 +60,6 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;
 constexpr int kKT = 128;      // tokens a tile
 constexpr int kQT = 128;      // rows a row tile
@@ -67,8 +67,12 @@ constexpr int kUnitRows = 2 * kQT;
 constexpr int kInlineParts = 4;  // parts of a unit joined without a launch
 constexpr float kRaise = 8.f;  // log2 of the growth that raises m
 
-template <int DP, bool APART>
+template <int DP, bool APART, bool CODES>
 struct Cfg {
+  // warps: after the softmax's, TMA, MMA and two of Q; or four of codes, MMA and two of Q
+  static constexpr int kThreads = CODES ? 512 : 384;
+  static constexpr int kMmaWarp = CODES ? 12 : 9, kQWarp = CODES ? 13 : 10;
+  static constexpr int kFillers = CODES ? 4 : 1;  // arrivals that fill a slot
   static constexpr uint32_t kHalf = kKT * 128;              // 64 columns of a tile: 128-byte rows
   static constexpr uint32_t kTile = kHalf * (DP / 64);      // a Q, K or V tile
   static constexpr int kKS = DP == 64 ? 4 : 2, kVS = DP == 64 ? 4 : 3;  // ring slots of K and V
@@ -189,24 +193,27 @@ struct Walk {
   __device__ __forceinline__ bool more() const { return tiles0() + sp.n + cost < end; }
 };
 // Shared memory behind the tiles.
-template <int DP, bool APART>
+template <int DP, bool APART, bool CODES>
 struct Shared {
-  using C = Cfg<DP, APART>;
+  using C = Cfg<DP, APART, CODES>;
   // kf/ke, vf/ve: full and empty slots of the rings; vr: V checked; qr, qe: Q
   // tile ready, free; sr: scores ready; sc: scores read (kApart); pa, pb:
   // numerators of the first and the last 64 tokens ready; pv: P read, O current
   // (kApart); of: O final
   uint64_t kf[C::kKS], ke[C::kKS], vf[C::kVS], ve[C::kVS], vr[C::kVS];
   uint64_t qr[2], qe[2], sr[2], sc[2], pa[2], pb[2], pv[2], of[2], drain;
-  int64_t scan[kThreads / 32];
+  int64_t scan[C::kThreads / 32];
   Walk walk;
   uint32_t poison[8];  // ring over units: number + 1 of a unit with infinities or NaN taken out of V
   uint32_t tmem;
   int abort;
+  // codes: powers of two taken out of the last tiles of K and V and of the last units' Q, by their number
+  int k_exp[8], v_exp[8], q_exp[2][8];
+  uint32_t fill_top[4];
 };
-template <int DP, bool APART>
-constexpr int kSmem = Cfg<DP, APART>::kTiles + static_cast<int>(sizeof(Shared<DP, APART>));
-static_assert(kSmem<128, false> <= 227 * 1024, "shared memory");
+template <int DP, bool APART, bool CODES>
+constexpr int kSmem = Cfg<DP, APART, CODES>::kTiles + static_cast<int>(sizeof(Shared<DP, APART, CODES>));
+static_assert(kSmem<128, false, true> <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ int unit_count(const AttnArgs& a, int m) {
   return static_cast<int>((static_cast<int64_t>(m) * a.g + kUnitRows - 1) / kUnitRows);
@@ -319,11 +326,300 @@ __device__ __noinline__ void zero_nonfinite(uint32_t rows) {
   }
 }
 
-template <int DP, bool APART>
-__global__ void __launch_bounds__(kThreads, 1)
+// ---- pages of 4-bit codes. A tile's values s q + b become f16, whose 11 bits keep
+// what 8 of bf16 would not (keys rounded to bf16 put 0.25% of noise on every
+// numerator: 3.4e-3 of the results' norm instead of 2.0e-3); Q and the numerators are
+// f16 with them. f16's range is made up for by powers of two: a tile whose largest
+// value is above 2^14 or below 2^-8, and a row tile of Q likewise, is divided by one,
+// and scores, numerators and O are kept in units that make up for it. In a tile
+// divided so, values 2^-24 of the largest and below are lost. Of the eight values of
+// a word, nibbles i and i + 4 come out as a pair, so that columns lie in the order 0 4
+// 1 5 2 6 3 7: Q is laid out the same, and results are put back as they are read.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void in_order(float* o, float f) {
+#pragma unroll
+  for (int x = 0; x < 32; x += 8) {
+    float t[8];
+#pragma unroll
+    for (int y = 0; y < 8; ++y) t[y] = o[x + (y < 4 ? 2 * y : 2 * y - 7)] * f;
+#pragma unroll
+    for (int y = 0; y < 8; ++y) o[x + y] = t[y];
+  }
+}
+constexpr float kHalfMost = 16384.f, kHalfLeast = 0x1p-8f;
+// the power of two that a tile with this largest value is divided by
+__device__ __forceinline__ int half_exponent(float top) {
+  if (top == 0.f || (top <= kHalfMost && top >= kHalfLeast)) return 0;
+  return max(-120, static_cast<int>(__float_as_uint(top) >> 23) - 127 - 10);  // (a denormal's is -137)
+}
+__device__ __forceinline__ bool finite_words(uint32_t m) { return !nonfinite2(m); }
+__device__ __forceinline__ bool any_of_fillers(bool x) {
+  uint32_t r;
+  asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.or.pred q, 2, 128, p; selp.u32 %0, 1, 0, q; }"
+               : "=r"(r)
+               : "r"(static_cast<uint32_t>(x))
+               : "memory");
+  return r != 0;
+}
+
+// Four warps turn the codes of every tile into K and V in shared memory, loads a
+// tile ahead. A thread takes 16 bytes, 32 values, of every 128 / kPieces-th token.
+template <int DP, class Sh>
+__device__ __forceinline__ void fill_tiles(const AttnArgs& a, Walk w, Sh& sh, uint32_t sk, uint32_t sv) {
+  using C = typename Sh::C;
+  constexpr int kPieces = DP / 32, kStep = 128 / kPieces, kRowBytes = DP / 2, kMetaBytes = DP / 16;
+  const int t = threadIdx.x - 256, lane = t & 31, piece = t % kPieces, row0 = t / kPieces;
+  const int page_tokens = 1 << a.page_shift;
+  volatile int* abort_flag = &sh.abort;
+  struct Tile {
+    uint4 codes[kPieces];
+    uint32_t meta[kPieces];
+  };
+  Tile k, v;
+  int64_t at[kPieces];  // of the thread's tokens: bytes to the head's block of their page; -1: hidden
+  auto find = [&](int j) {  // tile j of the segment
+    const int tile0 = w.sp.tile(w.t0 + j) * kKT;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int tok = tile0 + row0 + i * kStep;
+      at[i] = -1;
+      if (tok < w.sp.end && (tok < a.sinks || tok >= w.sp.low)) {
+        const int page = __ldg(a.table + static_cast<int64_t>(w.s.id) * a.max_pages + (tok >> a.page_shift));
+        if (page >= 0 && page < a.n_pages)
+          at[i] = ((static_cast<int64_t>(page) * a.Hkv + w.h) * (kRowBytes + kMetaBytes)) << a.page_shift;
+        else
+          atomicOr(a.err, MOE_DEVERR_BADIDX);
+      }
+    }
+  };
+  auto load = [&](Tile& x, const void* pool, int j) {
+    const int tile0 = w.sp.tile(w.t0 + j) * kKT;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      x.codes[i] = make_uint4(0u, 0u, 0u, 0u);
+      x.meta[i] = 0u;
+      if (at[i] >= 0) {
+        const int y = (tile0 + row0 + i * kStep) & (page_tokens - 1);
+        const char* b = static_cast<const char*>(pool) + at[i];
+        x.codes[i] = __ldg(reinterpret_cast<const uint4*>(b + y * kRowBytes + piece * 16));
+        x.meta[i] = __ldg(reinterpret_cast<const uint32_t*>(b + (static_cast<int64_t>(kRowBytes) << a.page_shift) + y * kMetaBytes + (piece >> 1) * 4));
+      }
+    }
+  };
+  // the power of two of a tile, the same in every thread
+  auto exponent = [&](const Tile& x) -> int {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const float s = __uint_as_float(x.meta[i] << 16), b = __uint_as_float(x.meta[i] & 0xFFFF0000u);
+      if (finite_words(x.meta[i])) top = fmaxf(top, fmaxf(fabsf(b), fabsf(fmaf(15.f, s, b))));
+    }
+    const bool large = any_of_fillers(top > kHalfMost), enough = any_of_fillers(top >= kHalfLeast);
+    if (!large && enough) return 0;
+    top = fminf(top, 3.3e38f);
+    const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(top));
+    if (lane == 0) sh.fill_top[t >> 5] = most;
+    asm volatile("bar.sync 2, 128;" ::: "memory");
+    const volatile uint32_t* all = sh.fill_top;
+    const uint32_t m = max(max(all[0], all[1]), max(all[2], all[3]));
+    asm volatile("bar.sync 2, 128;" ::: "memory");
+    return half_exponent(__uint_as_float(m));
+  };
+  auto store = [&](const Tile& x, uint32_t slot, int e) {
+    const float f = exp2f(static_cast<float>(-e));
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int r = row0 + i * kStep;
+      const uint32_t dst = slot + (piece >> 1) * C::kHalf + r * 128u;
+      const __half2 s = __float2half2_rn(__uint_as_float(x.meta[i] << 16) * f);
+      const __half2 b = __float2half2_rn(__uint_as_float(x.meta[i] & 0xFFFF0000u) * f);
+      const uint32_t words[4] = {x.codes[i].x, x.codes[i].y, x.codes[i].z, x.codes[i].w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        uint32_t o[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          // 1024 + q has q as its last bits
+          const uint32_t m = ((words[y] >> (4 * z)) & 0x000F000Fu) | 0x64006400u;
+          const __half2 q = __hsub2(*reinterpret_cast<const __half2*>(&m), __float2half2_rn(1024.f));
+          const __half2 val = __hfma2(q, s, b);
+          o[z] = *reinterpret_cast<const uint32_t*>(&val);
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + ((((piece & 1) * 4 + y) ^ (r & 7)) << 4)), "r"(o[0]),
+                     "r"(o[1]), "r"(o[2]), "r"(o[3])
+                     : "memory");
+      }
+    }
+  };
+  RingPos kp, vp;
+  uint32_t n = 0;  // tiles filled
+  bool ok = true;
+  auto room = [&](uint64_t* empty, uint32_t slots, const RingPos& rp) {
+    if (n >= slots) ok = mbar_wait(su32(empty), rp.ph ^ 1u, abort_flag, a.err, a.wait_cycles);
+    ok = __all_sync(~0u, ok);
+    return ok;
+  };
+  auto filled = [&](uint64_t* full) {
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(su32(full));
+  };
+  for (uint32_t unit = 0; n < a.copies; ++unit) {
+    const int lo_pos = first_pos(a, w), hi_pos = w.sp.end - 1;
+    find(0);
+    load(k, a.k, 0);
+    load(v, a.v, 0);
+    for (int j = 0; j < w.nt && n < a.copies; ++j) {
+      // A value that is infinite or NaN, in a tile with tokens that only some rows
+      // see: a zero in the product, and the rows that see it learn at the unit's end.
+      if (mixed_tile(a, w.sp.tile(w.t0 + j) * kKT, lo_pos, hi_pos)) {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          if (!finite_words(v.meta[i])) {
+            v.meta[i] = 0u;
+            bad = true;
+          }
+        if (bad) *const_cast<volatile uint32_t*>(&sh.poison[unit & 7]) = unit + 1;
+      }
+      const int ke = exponent(k), ve = exponent(v);
+      if (t == 0) {
+        sh.k_exp[n & 7] = ke;
+        sh.v_exp[n & 7] = ve;
+      }
+      const bool more = j + 1 < w.nt;
+      if (!room(&sh.ke[kp.s], C::kKS, kp)) return;
+      store(k, sk + kp.s * C::kTile, ke);
+      filled(&sh.kf[kp.s]);
+      kp.next(C::kKS);
+      if (more) {
+        find(j + 1);
+        load(k, a.k, j + 1);
+      }
+      if (!room(&sh.ve[vp.s], C::kVS, vp)) return;
+      store(v, sv + vp.s * C::kTile, ve);
+      filled(&sh.vf[vp.s]);
+      vp.next(C::kVS);
+      if (more) load(v, a.v, j + 1);
+      ++n;
+    }
+    if (*abort_flag || !w.more()) return;
+    next_segment(a, w);
+  }
+}
+
+// A warp brings in Q of row tile t of every unit, as f16 in the columns' order.
+template <int DP, class Sh>
+__device__ __forceinline__ void convert_q(const AttnArgs& a, Walk w, Sh& sh, uint32_t sq, int t) {
+  using C = typename Sh::C;
+  constexpr int kPieces = DP / 8, kRowsPer = 32 / kPieces, kBatch = 4;
+  const int lane = threadIdx.x & 31, p = lane % kPieces;
+  volatile int* abort_flag = &sh.abort;
+  uint32_t qe_ph = 0;
+  bool ok = true, q_used = false;
+  for (uint32_t unit = 0; ok; ++unit) {
+    if (t * kQT < w.rows) {
+      if (q_used) {
+        ok = mbar_wait(su32(&sh.qe[t]), qe_ph, abort_flag, a.err, a.wait_cycles);
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        qe_ph ^= 1u;
+      }
+      q_used = true;
+      const int rows = w.rows - t * kQT;
+      int e = 0;
+      float top;
+      auto pass = [&]() {
+        const float f = exp2f(static_cast<float>(-e));
+        const int64_t rg = static_cast<int64_t>(w.rt) * kUnitRows + t * kQT + lane / kPieces;
+        const int i = static_cast<int>(quotient(rg, a.g));
+        int hq = static_cast<int>(rg - static_cast<int64_t>(i) * a.g);
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(w.s.row0) + i) * a.ldq +
+                                   static_cast<int64_t>(w.h * a.g + hq) * a.D + p * 8;
+        const int64_t step = kRowsPer * a.D, wrap = a.ldq - static_cast<int64_t>(a.g) * a.D;
+        const uint32_t dst = sq + (p >> 3) * C::kHalf;
+        top = 0.f;
+#pragma unroll 1
+        for (int r0 = lane / kPieces; r0 < kQT; r0 += kRowsPer * kBatch) {
+          uint4 u[kBatch];
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x) {
+            u[x] = make_uint4(0u, 0u, 0u, 0u);
+            if (r0 + x * kRowsPer < rows) u[x] = __ldg(reinterpret_cast<const uint4*>(src));
+            src += step;  // the next row's head, or the next token's first ones
+            hq += kRowsPer;
+            while (hq >= a.g) {
+              hq -= a.g;
+              src += wrap;
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x) {
+            const int r = r0 + x * kRowsPer;
+            const uint32_t ws[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
+            float v[8];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              v[2 * y] = __uint_as_float(ws[y] << 16) * f;
+              v[2 * y + 1] = __uint_as_float(ws[y] & 0xFFFF0000u) * f;
+            }
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              if (fabsf(v[y]) < INFINITY) top = fmaxf(top, fabsf(v[y]));
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + r * 128u + (((p & 7) ^ (r & 7)) << 4)),
+                         "r"(pack_f16(v[0], v[4])), "r"(pack_f16(v[1], v[5])), "r"(pack_f16(v[2], v[6])), "r"(pack_f16(v[3], v[7]))
+                         : "memory");
+          }
+        }
+      };
+      pass();
+      top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
+      e = half_exponent(top);
+      if (e != 0) pass();
+      if (lane == 0) sh.q_exp[t][unit & 7] = e;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(su32(&sh.qr[t]));
+    }
+    if (!w.more()) break;
+    next_segment(a, w);
+  }
+}
+
+// The column groups of a row that the tokens it sees, in tiles with tokens that only
+// some rows see, make NaN.
+template <int DP>
+__device__ __noinline__ uint32_t lost_groups(const AttnArgs& a, const Walk& w, int pos) {
+  uint32_t lost = 0;
+  const int lo_pos = first_pos(a, w);
+  const int32_t* row = a.table + static_cast<int64_t>(w.s.id) * a.max_pages;
+  for (int t = w.t0; t < w.t0 + w.nt; ++t) {
+    const int tile0 = w.sp.tile(t) * kKT;
+    if (!mixed_tile(a, tile0, lo_pos, w.sp.end - 1)) continue;
+    for (int j = tile0; j < tile0 + kKT; ++j) {
+      const int back = pos - j;
+      if (back < 0 || (a.window > 0 && back >= a.window && j >= a.sinks)) continue;
+      const int p = __ldg(row + (j >> a.page_shift));
+      if (p < 0 || p >= a.n_pages) continue;
+      const char* block = static_cast<const char*>(a.v) + (((static_cast<int64_t>(p) * a.Hkv + w.h) * (DP / 2 + DP / 16)) << a.page_shift);
+      const char* meta = block + (static_cast<int64_t>(DP / 2) << a.page_shift) + (j & ((1 << a.page_shift) - 1)) * (DP / 16);
+#pragma unroll
+      for (int g = 0; g < DP / 64; ++g)
+        if (!finite_words(__ldg(reinterpret_cast<const uint32_t*>(meta + 4 * g)))) lost |= 1u << g;
+    }
+  }
+  return lost;
+}
+
+template <int DP, bool APART, bool CODES>
+__global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, AttnArgs a) {
   const long long wait_cycles = a.wait_cycles;
-  using C = Cfg<DP, APART>;
+  using C = Cfg<DP, APART, CODES>;
+  constexpr int kThreads = C::kThreads;
   extern __shared__ __align__(1024) unsigned char smraw[];
   const uint32_t sbase = su32(smraw);
   if (sbase & 1023u) {  // the swizzle's pattern starts at such a boundary
@@ -331,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const uint32_t sq = sbase, sk = sbase + 2 * C::kTile, sv = sk + C::kKS * C::kTile;
-  using Sh = Shared<DP, APART>;
+  using Sh = Shared<DP, APART, CODES>;
   Sh& sh = *reinterpret_cast<Sh*>(smraw + C::kTiles);
   int* const s_first = reinterpret_cast<int*>(smraw);  // before the tiles are in use
   volatile int* abort_flag = &sh.abort;
@@ -441,11 +737,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     sh.abort = 0;
     for (int i = 0; i < C::kKS; ++i) {
-      mbar_init(su32(&sh.kf[i]), 1);
+      mbar_init(su32(&sh.kf[i]), C::kFillers);
       mbar_init(su32(&sh.ke[i]), 1);
     }
     for (int i = 0; i < C::kVS; ++i) {
-      mbar_init(su32(&sh.vf[i]), 1);
+      mbar_init(su32(&sh.vf[i]), C::kFillers);
       mbar_init(su32(&sh.ve[i]), 1);
       mbar_init(su32(&sh.vr[i]), 2);
     }
@@ -463,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 8; ++i) sh.poison[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 9) {
+  if (warp == C::kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&sh.tmem)),
                  "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -474,7 +770,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sh.tmem;
   Walk w = sh.walk;
 
-  if (warp == 8) {
+  // Codes: the block is launched with 512 x 128 registers; the softmax's warpgroups
+  // take 168 a thread, that of the codes keeps 96 and the last 80 (256 x 168 + 128 x
+  // 96 + 128 x 80 = 512 x 128).
+  if (CODES && warp >= 8 && warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    fill_tiles<DP>(a, w, sh, sk, sv);
+  } else if (!CODES && warp == 8) {
     // ---------------- TMA: lane i copies page i of the tile (its 64-column
     // halves); pages that no row sees are left out
     const int boxr = min(1 << a.page_shift, kKT), per = kKT / boxr;
@@ -530,15 +832,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t j = 0; j < nv && j < C::kVS; ++j)
         mbar_drain(su32(&sh.vf[(nv - 1 - j) % C::kVS]), ((nv - 1 - j) / C::kVS) & 1u, a.err, kPrefillWaitCycles);
     }
-  } else if (warp == 9) {
+  } else if (CODES ? warp >= C::kMmaWarp : warp == C::kMmaWarp) {
     // ---------------- MMA issue, by one elected thread: elect.sync under a
     // branch that is uniform in the warp lets the compiler keep descriptors in
     // uniform registers. (A lane comparison does not: 100 cycles an MMA. The
     // tensor cores take 73 cycles for 128 x 128 x 16 with A in tensor memory and
     // 105 with A in shared memory.)
-    if (elect_one()) {
-      const uint32_t id_qk = (1u << 4) | (1u << 7) | (1u << 10) | ((kKT >> 3) << 17) | ((kQT >> 4) << 24);
-      const uint32_t id_pv = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((DP >> 3) << 17) | ((kQT >> 4) << 24);
+    // (With codes the warpgroup's other warps are here too, as it lowers its registers in one instruction.)
+    if (CODES) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (CODES && warp >= C::kQWarp) {
+      if (warp < C::kQWarp + 2) convert_q<DP>(a, w, sh, sq + (warp - C::kQWarp) * C::kTile, warp - C::kQWarp);
+    } else if (elect_one()) {
+      constexpr uint32_t kOperands = CODES ? 0u : (1u << 7) | (1u << 10);  // f16 or bf16
+      const uint32_t id_qk = (1u << 4) | kOperands | ((kKT >> 3) << 17) | ((kQT >> 4) << 24);
+      const uint32_t id_pv = (1u << 4) | kOperands | (1u << 16) | ((DP >> 3) << 17) | ((kQT >> 4) << 24);
       RingPos kp, vp;
       uint32_t q_ph = 0;            // units seen by row tile 0; tile 1 counts its own
       uint32_t q_ph1 = 0;
@@ -601,7 +908,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               qk(t);
               if (j + 2 == w.nt) umma_commit(su32(&sh.qe[t]));
             }
-            if (t == 0 && !(ok = wait(&sh.vr[vp.s], vp.ph))) break;
+            if (t == 0 && !(ok = wait(CODES ? &sh.vf[vp.s] : &sh.vr[vp.s], vp.ph))) break;
+            if (CODES) fence_after();
             if (!(ok = pv(t, j))) break;
             if (!more) {
               umma_commit(su32(&sh.of[t]));
@@ -626,9 +934,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit(su32(&sh.drain));
       mbar_drain(su32(&sh.drain), 0, a.err, kPrefillWaitCycles);
     }
-  } else if (warp >= 10) {
+  } else if (!CODES && warp >= C::kQWarp) {
     // ---------------- Q of row tile t, and the check of half of every V tile
-    const int t = warp - 10;
+    const int t = warp - C::kQWarp;
     RingPos vp;
     uint32_t qe_ph = 0;
     bool ok = true, q_used = false;
@@ -713,12 +1021,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------- softmax: one thread a row
+    if (CODES) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;  // row tile, row
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + C::kTmemS + t * 128u + lanes, tp = tmem + C::kTmemP + t * C::kStrideP + lanes;
     const uint32_t to = tmem + C::kTmemO + t * static_cast<uint32_t>(DP) + lanes;
-    const float c = a.scale_log2, raise = kRaise / c;
+    // (codes: maxima are in units of log2, as a score's unit differs from tile to tile)
+    const float c = CODES ? 1.f : a.scale_log2, raise = kRaise / c;
     uint32_t s_ph = 0, o_ph = 0, p_n = 0;  // p_n: numerators written (kApart)
+    uint32_t tile_n = 0;                   // tiles before this unit's
     bool ok = true;
     for (uint32_t unit = 0; ok; ++unit) {
       if (t * kQT < w.rows) {
@@ -731,6 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t r_last = min(rg - lane + 31, static_cast<int64_t>(w.s.m) * a.g - 1);
         const int hi_pos = w.s.len - w.s.m + static_cast<int>(quotient(r_last, a.g));
         float m = -INFINITY, thr = -INFINITY, l = 0.f;  // thr: a maximum above it raises m
+        int o_exp = 0;                                  // codes: O is kept divided by 2^o_exp
         for (int j = 0; j < w.nt; ++j) {
           ok = mbar_wait(su32(&sh.sr[t]), s_ph, abort_flag, a.err, wait_cycles);
           ok = __all_sync(~0u, ok);
@@ -775,7 +1087,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           top(0);
           top(64);
-          const float mx = max3(fmaxf(mx0, mx1), mx2, mx3);
+          float mx = max3(fmaxf(mx0, mx1), mx2, mx3), cj = c, grown = 1.f, shift = 0.f;
+          bool wider = false;
+          if constexpr (CODES) {
+            const volatile Sh& vs = sh;
+            const uint32_t n = (tile_n + j) & 7;
+            cj = a.scale_log2 * exp2f(static_cast<float>(vs.k_exp[n] + vs.q_exp[t][unit & 7]));
+            mx *= cj;
+            const int ve = vs.v_exp[n];
+            wider = j == 0 || ve > o_exp;
+            if (wider) {
+              grown = j == 0 ? 1.f : exp2f(static_cast<float>(o_exp - ve));
+              o_exp = ve;
+            }
+            shift = static_cast<float>(ve - o_exp);
+          }
           if (C::kApart && p_n++ > 0) {  // the product of the tile before has read P and brought O up to date
             ok = mbar_wait(su32(&sh.pv[t]), p_n & 1u, abort_flag, a.err, wait_cycles);
             ok = __all_sync(~0u, ok);
@@ -783,12 +1109,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_after();
           }
           const bool up = mx > thr;
-          if (__any_sync(~0u, up)) {
+          if (wider || __any_sync(~0u, up)) {
             const float mn = up ? mx : m;
-            const float f = up ? ex2((m - mn) * c) : 1.f;  // 0 for the first maximum
+            float f = up ? ex2((m - mn) * c) : 1.f;  // 0 for the first maximum
             m = mn;
             thr = up ? m + raise : thr;
             l *= f;
+            if (CODES) f *= grown;
             if (j > 0) {
 #pragma unroll 1
               for (int x = 0; x < DP; x += 16) {
@@ -802,8 +1129,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          const float mc = m == -INFINITY ? 0.f : m * c;
-          const unsigned long long c2 = pack2(c, c), m2 = pack2(-mc, -mc);
+          const float mc = (m == -INFINITY ? 0.f : m * c) - shift;
+          const unsigned long long c2 = pack2(cj, cj), m2 = pack2(-mc, -mc);
           unsigned long long l0 = 0ull, l1 = 0ull;
 #pragma unroll
           for (int x = 0; x < 128; x += 32) {
@@ -816,8 +1143,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               // the sum takes the numerators before their rounding to bf16
               l0 = add2(l0, pack2(e0, e1));
               l1 = add2(l1, pack2(e2, e3));
-              p[y / 2] = pack_bf16(e0, e1);
-              p[y / 2 + 1] = pack_bf16(e2, e3);
+              p[y / 2] = CODES ? pack_f16(e0, e1) : pack_bf16(e0, e1);
+              p[y / 2 + 1] = CODES ? pack_f16(e2, e3) : pack_bf16(e2, e3);
             }
             if (x == 64) {  // the first half is in place by now
               tmem_wait_st();
@@ -832,7 +1159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(su32(&sh.pb[t]));
           const float2 la = unpack2(add2(l0, l1));
-          l += la.x + la.y;
+          l += CODES ? (la.x + la.y) * exp2f(-shift) : la.x + la.y;
         }
         if (!ok) break;
         ok = mbar_wait(su32(&sh.of[t]), o_ph, abort_flag, a.err, wait_cycles);
@@ -842,7 +1169,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_after();
         const int hq = w.h * a.g + static_cast<int>(rg - static_cast<int64_t>(qi) * a.g);
         const int64_t row = static_cast<int64_t>(w.s.row0) + qi;
-        if (*const_cast<volatile uint32_t*>(&sh.poison[unit & 7]) == unit + 1) {
+        const bool poisoned = *const_cast<volatile uint32_t*>(&sh.poison[unit & 7]) == unit + 1;
+        // codes: the groups of 64 columns that a visible token's scale or offset makes NaN
+        const uint32_t lost = CODES && poisoned ? lost_groups<DP>(a, w, pos) : 0u;
+        if (!CODES && poisoned) {
           const Walk seg = w;
           const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + row * a.ldq + static_cast<int64_t>(hq) * a.D;
 #pragma unroll 1
@@ -889,11 +1219,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* part = a.part + ((2 * static_cast<int64_t>(blockIdx.x) + (run0 > w.tiles0() ? 0 : 1)) * 2 + t) * C::kPart;
         if (!whole) *reinterpret_cast<float2*>(part + r * 4) = make_float2(m, l);
         const float inv = 1.f / l;  // no weight at all on what is seen: 0/0
+        const float unit_of_o = CODES ? exp2f(static_cast<float>(o_exp)) : 1.f;
 #pragma unroll 1
         for (int x = 0; x < DP; x += 32) {
           float o[32];
           tmem_ld32_async(to + x, o);
           tmem_wait_ld();
+          if constexpr (CODES) in_order(o, (lost >> (x / 64)) & 1u ? NAN : unit_of_o);
           if (whole) {
             store32(o, inv, x);
           } else {
@@ -975,6 +1307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the next unit's products overwrite O only after this read
         fence_before();
       }
+      tile_n += w.nt;
       if (!w.more()) break;
       next_segment(a, w);
     }
@@ -982,7 +1315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  if (warp == C::kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
 // Join of 16 columns of one row tile of the unit whose first part is CTA
@@ -1068,20 +1401,24 @@ bool may_need_join(const AttnArgs& a, int num_sms) {
   return std::min(tiles, (tiles + run - 1) / run + 1) > kInlineParts;
 }
 
-template <int DP, bool APART>
+template <int DP, bool APART, bool CODES>
 cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t st) {
-  CUtensorMap mk, mv;
+  CUtensorMap mk{}, mv{};  // (codes are loaded without)
   const int page = 1 << a.page_shift;
   cudaError_t e;
-  if ((e = map_pages(&mk, a.k, a.D, page, static_cast<int64_t>(a.n_pages) * a.Hkv, std::min(page, kKT))) != cudaSuccess ||
+  if (CODES) {
+  } else if ((e = map_pages(&mk, a.k, a.D, page, static_cast<int64_t>(a.n_pages) * a.Hkv, std::min(page, kKT))) != cudaSuccess ||
       (e = map_pages(&mv, a.v, a.D, page, static_cast<int64_t>(a.n_pages) * a.Hkv, std::min(page, kKT))) != cudaSuccess)
     return e;
-  e = cudaFuncSetAttribute(prefill_kernel<DP, APART>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<DP, APART>);
+  constexpr int smem = kSmem<DP, APART, CODES>;
+  e = cudaFuncSetAttribute(prefill_kernel<DP, APART, CODES>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  prefill_kernel<DP, APART><<<num_sms, kThreads, kSmem<DP, APART>, st>>>(mk, mv, a);
+  prefill_kernel<DP, APART, CODES><<<num_sms, Cfg<DP, APART, CODES>::kThreads, smem, st>>>(mk, mv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (!may_need_join(a, num_sms)) return cudaSuccess;
-  return pdl_launch(prefill_join_kernel<DP>, dim3(num_sms, 2 * DP / kJoinCols), dim3(kQT * kJoinGroups), 0, st, a);
+  AttnArgs j = a;
+  if (CODES) j.scale_log2 = 1.f;  // the parts' maxima are in units of log2
+  return pdl_launch(prefill_join_kernel<DP>, dim3(num_sms, 2 * DP / kJoinCols), dim3(kQT * kJoinGroups), 0, st, j);
 }
 
 }  // namespace
@@ -1089,11 +1426,15 @@ cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t st) {
 cudaError_t launch_attn_prefill_tc(const AttnArgs& a, int num_sms, cudaStream_t st) {
   cudaError_t e = encoder();
   if (e != cudaSuccess) return e;
-  if (a.D > 64) return launch<128, false>(a, num_sms, st);
+  if (a.D > 64) return launch<128, false, false>(a, num_sms, st);
   // P beside S pays where most tiles need no mask (4,096 tokens at 32K, 16 heads
   // of 64: 554 -> 500 us), not in a window's few tiles (ragged prompts, window
   // 1,024: 92 -> 100 us)
-  return a.window > 0 ? launch<64, false>(a, num_sms, st) : launch<64, true>(a, num_sms, st);
+  return a.window > 0 ? launch<64, false, false>(a, num_sms, st) : launch<64, true, false>(a, num_sms, st);
+}
+cudaError_t launch_attn_prefill_codes_tc(const AttnArgs& a, int num_sms, cudaStream_t st) {
+  if (a.D > 64) return launch<128, false, true>(a, num_sms, st);
+  return a.window > 0 ? launch<64, false, true>(a, num_sms, st) : launch<64, true, true>(a, num_sms, st);
 }
 
 }  // namespace moe

@@ -195,7 +195,7 @@ moe_status_t attention(const char* call, bool decode, const moe_kv_t* kv, int32_
   t_hook = WaitHook{};
   if (kv->dtype & MOE_KV_I4)
     return launched(call, decode ? moe::launch_attn_decode_codes(a, moe::token_type(*kv), sms, stream)
-                                 : moe::launch_attn_prefill_codes(a, moe::token_type(*kv), stream));
+                                 : moe::launch_attn_prefill_codes(a, moe::token_type(*kv), sms, stream));
   return launched(call, decode ? moe::launch_attn_decode(a, kv->dtype, sms, stream)
                                : moe::launch_attn_prefill(a, kv->dtype, rows, sms, stream));
 }

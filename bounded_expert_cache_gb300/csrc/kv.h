@@ -81,7 +81,8 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, int32_t dtype, int32_t n_rows
 cudaError_t launch_attn_prefill_tc(const AttnArgs& a, int num_sms, cudaStream_t st);
 // over pages of 4-bit codes; dtype: the type of q and out
 cudaError_t launch_attn_decode_codes(const AttnArgs& a, int32_t dtype, int num_sms, cudaStream_t st);
-cudaError_t launch_attn_prefill_codes(const AttnArgs& a, int32_t dtype, cudaStream_t st);
+cudaError_t launch_attn_prefill_codes(const AttnArgs& a, int32_t dtype, int num_sms, cudaStream_t st);
+cudaError_t launch_attn_prefill_codes_tc(const AttnArgs& a, int num_sms, cudaStream_t st);
 
 cudaError_t launch_kv_fork(const moe_kv_t& kv, const KvLayout& l, const int32_t* src, const int32_t* dst, int32_t n,
                            cudaStream_t st);
