@@ -69,14 +69,17 @@ constexpr float kRaise = 8.f;  // log2 of the growth that raises m
 
 template <int DP, bool APART, bool CODES>
 struct Cfg {
-  // warps: after the softmax's, TMA, MMA and two of Q; or four of codes, MMA and two of Q
+  // warps: after the softmax's, TMA, MMA and two of Q; or four of codes, MMA, two of Q and one that copies codes
   static constexpr int kThreads = CODES ? 512 : 384;
   static constexpr int kMmaWarp = CODES ? 12 : 9, kQWarp = CODES ? 13 : 10;
   static constexpr int kFillers = CODES ? 4 : 1;  // arrivals that fill a slot
   static constexpr uint32_t kHalf = kKT * 128;              // 64 columns of a tile: 128-byte rows
   static constexpr uint32_t kTile = kHalf * (DP / 64);      // a Q, K or V tile
-  static constexpr int kKS = DP == 64 ? 4 : 2, kVS = DP == 64 ? 4 : 3;  // ring slots of K and V
-  static constexpr int kTiles = (2 + kKS + kVS) * static_cast<int>(kTile);
+  static constexpr int kKS = DP == 64 ? 4 : 2, kVS = DP == 64 ? 4 : (CODES ? 2 : 3);  // ring slots of K and V
+  // codes: a tile's rows of codes, then its scales and offsets, and the ring of them
+  static constexpr int kCodeRow = DP / 2, kMetaRow = DP / 16, kRaw = kKT * (kCodeRow + kMetaRow);
+  static constexpr int kRS = !CODES ? 0 : (DP == 64 ? 6 : 3);
+  static constexpr int kTiles = (2 + kKS + kVS) * static_cast<int>(kTile) + kRS * kRaw;
   // tensor memory columns: S0 S1 O0 O1, and where O leaves room for them, P0 P1
   static constexpr bool kApart = APART;
   static_assert(!APART || DP == 64, "columns");
@@ -107,6 +110,11 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t lbo) {
   d |= static_cast<uint64_t>(1) << 46;
   d |= static_cast<uint64_t>(2) << 61;
   return d;
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void tma3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
   asm volatile(
@@ -201,15 +209,21 @@ struct Shared {
   // numerators of the first and the last 64 tokens ready; pv: P read, O current
   // (kApart); of: O final
   uint64_t kf[C::kKS], ke[C::kKS], vf[C::kVS], ve[C::kVS], vr[C::kVS];
+  uint64_t rf[6], re[6];  // codes: full and empty slots of their ring
   uint64_t qr[2], qe[2], sr[2], sc[2], pa[2], pb[2], pv[2], of[2], drain;
   int64_t scan[C::kThreads / 32];
   Walk walk;
   uint32_t poison[8];  // ring over units: number + 1 of a unit with infinities or NaN taken out of V
   uint32_t tmem;
   int abort;
-  // codes: powers of two taken out of the last tiles of K and V and of the last units' Q, by their number
-  int k_exp[8], v_exp[8], q_exp[2][8];
-  uint32_t fill_top[4];
+  // codes: powers of two taken out of the last tiles of K (as the factor that makes
+  // up for it) and V (as exponent) and of the last units' Q, by their number
+  struct Powers {
+    float k;
+    int v;
+  } powers[8];
+  float q_power[2][8];
+  uint32_t fill_top[2][4];
 };
 template <int DP, bool APART, bool CODES>
 constexpr int kSmem = Cfg<DP, APART, CODES>::kTiles + static_cast<int>(sizeof(Shared<DP, APART, CODES>));
@@ -329,10 +343,11 @@ __device__ __noinline__ void zero_nonfinite(uint32_t rows) {
 // ---- pages of 4-bit codes. A tile's values s q + b become f16, whose 11 bits keep
 // what 8 of bf16 would not (keys rounded to bf16 put 0.25% of noise on every
 // numerator: 3.4e-3 of the results' norm instead of 2.0e-3); Q and the numerators are
-// f16 with them. f16's range is made up for by powers of two: a tile whose largest
-// value is above 2^14 or below 2^-8, and a row tile of Q likewise, is divided by one,
-// and scores, numerators and O are kept in units that make up for it. In a tile
-// divided so, values 2^-24 of the largest and below are lost. Of the eight values of
+// f16 with them. f16's range is made up for by powers of two: a tile of K whose
+// largest value is above 2^14 or below 2^-8, and a row tile of Q likewise, is divided by
+// one that makes it about 2^10, and its scores multiplied by it; V by the largest power
+// that its unit has come across, and O is kept in that unit. (Values that are then below
+// 2^-24, or 2^-34 of the largest, are lost.) Of the eight values of
 // a word, nibbles i and i + 4 come out as a pair, so that columns lie in the order 0 4
 // 1 5 2 6 3 7: Q is laid out the same, and results are put back as they are read.
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -365,148 +380,205 @@ __device__ __forceinline__ bool any_of_fillers(bool x) {
   return r != 0;
 }
 
-// Four warps turn the codes of every tile into K and V in shared memory, loads a
-// tile ahead. A thread takes 16 bytes, 32 values, of every 128 / kPieces-th token.
+// One warp copies the codes of every tile of K and V, with their scales and offsets, into
+// a ring: lane i those of page i of the tile.
 template <int DP, class Sh>
-__device__ __forceinline__ void fill_tiles(const AttnArgs& a, Walk w, Sh& sh, uint32_t sk, uint32_t sv) {
+__device__ __forceinline__ void copy_codes(const AttnArgs& a, Walk w, Sh& sh, uint32_t raw) {
   using C = typename Sh::C;
-  constexpr int kPieces = DP / 32, kStep = 128 / kPieces, kRowBytes = DP / 2, kMetaBytes = DP / 16;
-  const int t = threadIdx.x - 256, lane = t & 31, piece = t % kPieces, row0 = t / kPieces;
-  const int page_tokens = 1 << a.page_shift;
+  const int lane = threadIdx.x & 31;
+  const int boxr = min(1 << a.page_shift, kKT), per = kKT / boxr;
   volatile int* abort_flag = &sh.abort;
-  struct Tile {
-    uint4 codes[kPieces];
-    uint32_t meta[kPieces];
-  };
-  Tile k, v;
-  int64_t at[kPieces];  // of the thread's tokens: bytes to the head's block of their page; -1: hidden
-  auto find = [&](int j) {  // tile j of the segment
-    const int tile0 = w.sp.tile(w.t0 + j) * kKT;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int tok = tile0 + row0 + i * kStep;
-      at[i] = -1;
-      if (tok < w.sp.end && (tok < a.sinks || tok >= w.sp.low)) {
-        const int page = __ldg(a.table + static_cast<int64_t>(w.s.id) * a.max_pages + (tok >> a.page_shift));
-        if (page >= 0 && page < a.n_pages)
-          at[i] = ((static_cast<int64_t>(page) * a.Hkv + w.h) * (kRowBytes + kMetaBytes)) << a.page_shift;
-        else
+  RingPos rp;
+  uint32_t n = 0;  // tiles of K and V copied
+  bool ok = true;
+  while (ok) {
+    const int32_t* row = a.table + static_cast<int64_t>(w.s.id) * a.max_pages;
+    for (int i = 0; i < w.nt && ok && n / 2 < a.copies; ++i) {
+      const int tok = w.sp.tile(w.t0 + i) * kKT + lane * boxr;
+      bool need = lane < per && tok < w.sp.end && (tok < a.sinks || tok + boxr > w.sp.low);
+      int page = 0;
+      if (need) {
+        page = __ldg(row + (tok >> a.page_shift));
+        if (page < 0 || page >= a.n_pages) {
           atomicOr(a.err, MOE_DEVERR_BADIDX);
+          need = false;
+        }
+      }
+      const uint32_t bytes = __popc(__ballot_sync(~0u, need)) * static_cast<uint32_t>(boxr * (C::kCodeRow + C::kMetaRow));
+      const int y = tok & ((1 << a.page_shift) - 1);
+      const int64_t block = ((static_cast<int64_t>(page) * a.Hkv + w.h) * (C::kCodeRow + C::kMetaRow)) << a.page_shift;
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t full = su32(&sh.rf[rp.s]);
+        if (n >= C::kRS && !mbar_wait(su32(&sh.re[rp.s]), rp.ph ^ 1u, abort_flag, a.err, a.wait_cycles)) ok = false;
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_expect_tx(full, bytes);  // without pages the barrier completes by this arrival
+        __syncwarp();
+        if (need) {
+          const char* src = static_cast<const char*>(kv ? a.v : a.k) + block;
+          const uint32_t dst = raw + rp.s * C::kRaw;
+          bulk_copy(dst + lane * boxr * C::kCodeRow, src + y * C::kCodeRow, boxr * C::kCodeRow, full);
+          bulk_copy(dst + kKT * C::kCodeRow + lane * boxr * C::kMetaRow,
+                    src + (static_cast<int64_t>(C::kCodeRow) << a.page_shift) + y * C::kMetaRow, boxr * C::kMetaRow, full);
+        }
+        __syncwarp();
+        ++n;
+        rp.next(C::kRS);
       }
     }
-  };
-  auto load = [&](Tile& x, const void* pool, int j) {
-    const int tile0 = w.sp.tile(w.t0 + j) * kKT;
-#pragma unroll
+    if (*abort_flag || n / 2 >= a.copies) ok = false;
+    ok = __all_sync(~0u, ok) && w.more();
+    if (ok) next_segment(a, w);
+  }
+  // drain: copies in flight land before the CTA ends
+  if (lane == 0)
+    for (uint32_t j = 0; j < n && j < C::kRS; ++j)
+      mbar_drain(su32(&sh.rf[(n - 1 - j) % C::kRS]), ((n - 1 - j) / C::kRS) & 1u, a.err, kPrefillWaitCycles);
+}
+
+// Four warps turn the codes of every tile into K and V. The loops are kept short: all
+// roles' code runs at once, and unrolled (loads to registers a tile ahead, 16 kB of
+// instructions) the warps waited for instructions most of the time (2,048 tokens at 32K, 16
+// heads of 128: 810 us; one piece of 16 bytes a turn 468, two 449; of 64: 370 and 418; a
+// word of 4 bytes a turn 570; eight warps, which take issue slots of the softmax's: 539).
+template <int DP, class Sh>
+__device__ __forceinline__ void fill_tiles(const AttnArgs& a, Walk w, Sh& sh, uint32_t sk, uint32_t sv, uint32_t raw) {
+  using C = typename Sh::C;
+  constexpr int kPieces = DP / 32, kStep = 128 / kPieces, G = DP / 64;
+  const int t = threadIdx.x - 256, lane = t & 31, piece = t % kPieces, row0 = t / kPieces;
+  volatile int* abort_flag = &sh.abort;
+  // Values of the raw tile at `src`, times f, into the slot at `dst`: a thread takes 16
+  // bytes, 32 values, of every kStep-th token. Their four pieces of eight go out in an
+  // order that differs between the halves of a head of 128, for the banks' sake.
+  auto convert = [&](uint32_t src, uint32_t dst, float f) {
+    uint32_t from = src + row0 * C::kCodeRow + piece * 16, meta = src + kKT * C::kCodeRow + row0 * C::kMetaRow + (piece >> 1) * 4;
+    dst += (piece >> 1) * C::kHalf + row0 * 128u;
+    const uint32_t turn = piece & 2;
+    uint32_t c[4], m;
+    auto read = [&]() {
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(from));
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(m) : "r"(meta));
+    };
+    read();
+#pragma unroll kPieces / 2
     for (int i = 0; i < kPieces; ++i) {
-      x.codes[i] = make_uint4(0u, 0u, 0u, 0u);
-      x.meta[i] = 0u;
-      if (at[i] >= 0) {
-        const int y = (tile0 + row0 + i * kStep) & (page_tokens - 1);
-        const char* b = static_cast<const char*>(pool) + at[i];
-        x.codes[i] = __ldg(reinterpret_cast<const uint4*>(b + y * kRowBytes + piece * 16));
-        x.meta[i] = __ldg(reinterpret_cast<const uint32_t*>(b + (static_cast<int64_t>(kRowBytes) << a.page_shift) + y * kMetaBytes + (piece >> 1) * 4));
-      }
-    }
-  };
-  // the power of two of a tile, the same in every thread
-  auto exponent = [&](const Tile& x) -> int {
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const float s = __uint_as_float(x.meta[i] << 16), b = __uint_as_float(x.meta[i] & 0xFFFF0000u);
-      if (finite_words(x.meta[i])) top = fmaxf(top, fmaxf(fabsf(b), fabsf(fmaf(15.f, s, b))));
-    }
-    const bool large = any_of_fillers(top > kHalfMost), enough = any_of_fillers(top >= kHalfLeast);
-    if (!large && enough) return 0;
-    top = fminf(top, 3.3e38f);
-    const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(top));
-    if (lane == 0) sh.fill_top[t >> 5] = most;
-    asm volatile("bar.sync 2, 128;" ::: "memory");
-    const volatile uint32_t* all = sh.fill_top;
-    const uint32_t m = max(max(all[0], all[1]), max(all[2], all[3]));
-    asm volatile("bar.sync 2, 128;" ::: "memory");
-    return half_exponent(__uint_as_float(m));
-  };
-  auto store = [&](const Tile& x, uint32_t slot, int e) {
-    const float f = exp2f(static_cast<float>(-e));
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int r = row0 + i * kStep;
-      const uint32_t dst = slot + (piece >> 1) * C::kHalf + r * 128u;
-      const __half2 s = __float2half2_rn(__uint_as_float(x.meta[i] << 16) * f);
-      const __half2 b = __float2half2_rn(__uint_as_float(x.meta[i] & 0xFFFF0000u) * f);
-      const uint32_t words[4] = {x.codes[i].x, x.codes[i].y, x.codes[i].z, x.codes[i].w};
+      const uint32_t word[4] = {turn ? c[2] : c[0], turn ? c[3] : c[1], turn ? c[0] : c[2], turn ? c[1] : c[3]};
+      const __half2 s = __float2half2_rn(__uint_as_float(m << 16) * f);
+      const __half2 b = __float2half2_rn(__uint_as_float(m & 0xFFFF0000u) * f);
+      from += kStep * C::kCodeRow;
+      meta += kStep * C::kMetaRow;
+      if (i + 1 < kPieces) read();
+      const uint32_t swz = (row0 + i * kStep) & 7;
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         uint32_t o[4];
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
-          // 1024 + q has q as its last bits
-          const uint32_t m = ((words[y] >> (4 * z)) & 0x000F000Fu) | 0x64006400u;
-          const __half2 q = __hsub2(*reinterpret_cast<const __half2*>(&m), __float2half2_rn(1024.f));
+          // 1024 + q has q as its last bits, 1024 + 16 q as the four before: one shift a word
+          const uint32_t at = z < 2 ? word[y] : word[y] >> 8;
+          const uint32_t n = (at & (z & 1 ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+          const __half2 h = *reinterpret_cast<const __half2*>(&n);
+          const __half2 q = z & 1 ? __hfma2(h, __float2half2_rn(0.0625f), __float2half2_rn(-64.f)) : __hsub2(h, __float2half2_rn(1024.f));
           const __half2 val = __hfma2(q, s, b);
           o[z] = *reinterpret_cast<const uint32_t*>(&val);
         }
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + ((((piece & 1) * 4 + y) ^ (r & 7)) << 4)), "r"(o[0]),
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + ((((piece & 1) * 4 + (y ^ turn)) ^ swz) << 4)), "r"(o[0]),
                      "r"(o[1]), "r"(o[2]), "r"(o[3])
                      : "memory");
       }
+      dst += kStep * 128;
     }
   };
-  RingPos kp, vp;
+  RingPos kp, vp, rp;
   uint32_t n = 0;  // tiles filled
   bool ok = true;
-  auto room = [&](uint64_t* empty, uint32_t slots, const RingPos& rp) {
-    if (n >= slots) ok = mbar_wait(su32(empty), rp.ph ^ 1u, abort_flag, a.err, a.wait_cycles);
+  auto wait = [&](uint64_t* b, uint32_t ph) {
+    ok = ok && mbar_wait(su32(b), ph, abort_flag, a.err, a.wait_cycles);
     ok = __all_sync(~0u, ok);
     return ok;
   };
-  auto filled = [&](uint64_t* full) {
-    fence_async_smem();
+  auto tell = [&](uint64_t* b) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(su32(full));
+    if (lane == 0) mbar_arrive(su32(b));
   };
-  for (uint32_t unit = 0; n < a.copies; ++unit) {
+  for (uint32_t unit = 0;; ++unit) {
     const int lo_pos = first_pos(a, w), hi_pos = w.sp.end - 1;
-    find(0);
-    load(k, a.k, 0);
-    load(v, a.v, 0);
-    for (int j = 0; j < w.nt && n < a.copies; ++j) {
-      // A value that is infinite or NaN, in a tile with tokens that only some rows
-      // see: a zero in the product, and the rows that see it learn at the unit's end.
-      if (mixed_tile(a, w.sp.tile(w.t0 + j) * kKT, lo_pos, hi_pos)) {
-        bool bad = false;
+    int ve = -1000;  // V's power of two so far
+    for (int j = 0; j < w.nt; ++j) {
+      RingPos next = rp;
+      next.next(C::kRS);
+      if (!wait(&sh.rf[rp.s], rp.ph) || !wait(&sh.rf[next.s], next.ph)) return;
+      const uint32_t rk = raw + rp.s * C::kRaw, rv = raw + next.s * C::kRaw;
+      const int tile0 = w.sp.tile(w.t0 + j) * kKT;
+      // One thread a token looks at its scales and offsets.
+      const int tok = tile0 + t;
+      const bool seen = tok < w.sp.end && (tok < a.sinks || tok >= w.sp.low), mixed = mixed_tile(a, tile0, lo_pos, hi_pos);
+      float top[2] = {0.f, 0.f};
+      bool changed = false;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-          if (!finite_words(v.meta[i])) {
-            v.meta[i] = 0u;
-            bad = true;
+      for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const uint32_t at = (kv ? rv : rk) + kKT * C::kCodeRow + t * C::kMetaRow + 4 * g;
+          uint32_t m;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(m) : "r"(at));
+          const float s = __uint_as_float(m << 16), b = __uint_as_float(m & 0xFFFF0000u);
+          const bool fine = finite_words(m);
+          // Tokens that no row sees become zeros. So do values that are infinite or NaN
+          // in a tile with tokens that only some rows see; the rows that see them learn
+          // of it at the unit's end.
+          if (!seen || (kv && mixed && !fine)) {
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(0) : "memory");
+            changed = true;
+            if (seen) *const_cast<volatile uint32_t*>(&sh.poison[unit & 7]) = unit + 1;
+          } else if (fine) {
+            top[kv] = fmaxf(top[kv], fminf(fmaxf(fabsf(b), fabsf(fmaf(15.f, s, b))), 3.3e38f));
           }
-        if (bad) *const_cast<volatile uint32_t*>(&sh.poison[unit & 7]) = unit + 1;
+        }
       }
-      const int ke = exponent(k), ve = exponent(v);
+      if (changed) fence_async_smem();  // these writes, before the slot's next copy
+      // the tile's powers of two, the same in every thread; a look at each thread's own token settles most
+      int ke = 0, v_now = 0;
+      if (any_of_fillers(top[0] > kHalfMost || top[0] < kHalfLeast || top[1] > kHalfMost || top[1] < kHalfLeast)) {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(top[kv]));
+          if (lane == 0) sh.fill_top[kv][t >> 5] = most;
+        }
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+        const volatile Sh& all = sh;
+        auto most = [&](int x) {
+          return __uint_as_float(max(max(all.fill_top[x][0], all.fill_top[x][1]), max(all.fill_top[x][2], all.fill_top[x][3])));
+        };
+        ke = half_exponent(most(0));
+        v_now = half_exponent(most(1));
+        if (most(1) == 0.f) v_now = ve;  // (nothing to hold)
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+      }
+      ve = max(ve, v_now);
+      const int v_exp = ve == -1000 ? 0 : ve;
       if (t == 0) {
-        sh.k_exp[n & 7] = ke;
-        sh.v_exp[n & 7] = ve;
+        sh.powers[n & 7].k = exp2f(static_cast<float>(ke));
+        sh.powers[n & 7].v = v_exp;
       }
-      const bool more = j + 1 < w.nt;
-      if (!room(&sh.ke[kp.s], C::kKS, kp)) return;
-      store(k, sk + kp.s * C::kTile, ke);
-      filled(&sh.kf[kp.s]);
+      if (n >= C::kKS && !wait(&sh.ke[kp.s], kp.ph ^ 1u)) return;
+      convert(rk, sk + kp.s * C::kTile, exp2f(static_cast<float>(-ke)));
+      fence_async_smem();
+      tell(&sh.kf[kp.s]);
+      tell(&sh.re[rp.s]);
       kp.next(C::kKS);
-      if (more) {
-        find(j + 1);
-        load(k, a.k, j + 1);
-      }
-      if (!room(&sh.ve[vp.s], C::kVS, vp)) return;
-      store(v, sv + vp.s * C::kTile, ve);
-      filled(&sh.vf[vp.s]);
+      if (n >= C::kVS && !wait(&sh.ve[vp.s], vp.ph ^ 1u)) return;
+      convert(rv, sv + vp.s * C::kTile, exp2f(static_cast<float>(-v_exp)));
+      fence_async_smem();
+      tell(&sh.vf[vp.s]);
+      tell(&sh.re[next.s]);
       vp.next(C::kVS);
-      if (more) load(v, a.v, j + 1);
+      rp = next;
+      rp.next(C::kRS);
       ++n;
     }
-    if (*abort_flag || !w.more()) return;
+    if (!w.more()) return;
     next_segment(a, w);
   }
 }
@@ -579,7 +651,7 @@ __device__ __forceinline__ void convert_q(const AttnArgs& a, Walk w, Sh& sh, uin
       top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
       e = half_exponent(top);
       if (e != 0) pass();
-      if (lane == 0) sh.q_exp[t][unit & 7] = e;
+      if (lane == 0) sh.q_power[t][unit & 7] = exp2f(static_cast<float>(e));
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(su32(&sh.qr[t]));
@@ -756,6 +828,10 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
       mbar_init(su32(&sh.of[t]), 1);
     }
     mbar_init(su32(&sh.drain), 1);
+    for (int i = 0; i < C::kRS; ++i) {
+      mbar_init(su32(&sh.rf[i]), 1);
+      mbar_init(su32(&sh.re[i]), C::kFillers);
+    }
     for (int i = 0; i < 8; ++i) sh.poison[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -771,11 +847,10 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
   Walk w = sh.walk;
 
   // Codes: the block is launched with 512 x 128 registers; the softmax's warpgroups
-  // take 168 a thread, that of the codes keeps 96 and the last 80 (256 x 168 + 128 x
-  // 96 + 128 x 80 = 512 x 128).
+  // take 168 a thread, the others keep 88 (256 x 168 + 256 x 88 = 512 x 128).
   if (CODES && warp >= 8 && warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    fill_tiles<DP>(a, w, sh, sk, sv);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    fill_tiles<DP>(a, w, sh, sk, sv, sv + C::kVS * C::kTile);
   } else if (!CODES && warp == 8) {
     // ---------------- TMA: lane i copies page i of the tile (its 64-column
     // halves); pages that no row sees are left out
@@ -839,9 +914,12 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
     // tensor cores take 73 cycles for 128 x 128 x 16 with A in tensor memory and
     // 105 with A in shared memory.)
     // (With codes the warpgroup's other warps are here too, as it lowers its registers in one instruction.)
-    if (CODES) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (CODES) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (CODES && warp >= C::kQWarp) {
-      if (warp < C::kQWarp + 2) convert_q<DP>(a, w, sh, sq + (warp - C::kQWarp) * C::kTile, warp - C::kQWarp);
+      if (warp < C::kQWarp + 2)
+        convert_q<DP>(a, w, sh, sq + (warp - C::kQWarp) * C::kTile, warp - C::kQWarp);
+      else
+        copy_codes<DP>(a, w, sh, sv + C::kVS * C::kTile);
     } else if (elect_one()) {
       constexpr uint32_t kOperands = CODES ? 0u : (1u << 7) | (1u << 10);  // f16 or bf16
       const uint32_t id_qk = (1u << 4) | kOperands | ((kKT >> 3) << 17) | ((kQT >> 4) << 24);
@@ -1073,6 +1151,13 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
           };
 #pragma unroll
           for (int x = 0; x < 128; x += 32) tmem_ld32_async(ts + x, s + x);
+          float cj = c;  // codes: a score's factor, from the powers of two of its tile of K and of Q
+          int v_exp = 0;
+          if constexpr (CODES) {
+            const volatile Sh& vs = sh;
+            cj = a.scale_log2 * vs.q_power[t][unit & 7] * vs.powers[(tile_n + j) & 7].k;
+            v_exp = vs.powers[(tile_n + j) & 7].v;
+          }
           tmem_wait_ld();
           if (C::kApart) {
             fence_before();
@@ -1087,21 +1172,8 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
           }
           top(0);
           top(64);
-          float mx = max3(fmaxf(mx0, mx1), mx2, mx3), cj = c, grown = 1.f, shift = 0.f;
-          bool wider = false;
-          if constexpr (CODES) {
-            const volatile Sh& vs = sh;
-            const uint32_t n = (tile_n + j) & 7;
-            cj = a.scale_log2 * exp2f(static_cast<float>(vs.k_exp[n] + vs.q_exp[t][unit & 7]));
-            mx *= cj;
-            const int ve = vs.v_exp[n];
-            wider = j == 0 || ve > o_exp;
-            if (wider) {
-              grown = j == 0 ? 1.f : exp2f(static_cast<float>(o_exp - ve));
-              o_exp = ve;
-            }
-            shift = static_cast<float>(ve - o_exp);
-          }
+          float mx = max3(fmaxf(mx0, mx1), mx2, mx3);
+          if constexpr (CODES) mx *= cj;
           if (C::kApart && p_n++ > 0) {  // the product of the tile before has read P and brought O up to date
             ok = mbar_wait(su32(&sh.pv[t]), p_n & 1u, abort_flag, a.err, wait_cycles);
             ok = __all_sync(~0u, ok);
@@ -1109,13 +1181,16 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
             fence_after();
           }
           const bool up = mx > thr;
-          if (wider || __any_sync(~0u, up)) {
+          if (__any_sync(~0u, up) || (CODES && v_exp != o_exp)) {
             const float mn = up ? mx : m;
             float f = up ? ex2((m - mn) * c) : 1.f;  // 0 for the first maximum
             m = mn;
             thr = up ? m + raise : thr;
             l *= f;
-            if (CODES) f *= grown;
+            if (CODES && v_exp != o_exp) {  // O's unit grows with its values'
+              f *= exp2f(static_cast<float>(o_exp - v_exp));
+              o_exp = v_exp;
+            }
             if (j > 0) {
 #pragma unroll 1
               for (int x = 0; x < DP; x += 16) {
@@ -1129,7 +1204,7 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
               }
             }
           }
-          const float mc = (m == -INFINITY ? 0.f : m * c) - shift;
+          const float mc = m == -INFINITY ? 0.f : m * c;
           const unsigned long long c2 = pack2(cj, cj), m2 = pack2(-mc, -mc);
           unsigned long long l0 = 0ull, l1 = 0ull;
 #pragma unroll
@@ -1159,7 +1234,7 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(su32(&sh.pb[t]));
           const float2 la = unpack2(add2(l0, l1));
-          l += CODES ? (la.x + la.y) * exp2f(-shift) : la.x + la.y;
+          l += la.x + la.y;
         }
         if (!ok) break;
         ok = mbar_wait(su32(&sh.of[t]), o_ph, abort_flag, a.err, wait_cycles);
