@@ -17,6 +17,19 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&p);
 }
+// (w & MASK) | magic in one instruction: of two constants the compiler makes two
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(magic));
+  return r;
+}
+// a constant that stays in a register
+__device__ __forceinline__ uint32_t in_register(uint32_t c) {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %1;" : "=r"(r) : "r"(c));
+  return r;
+}
 // Either half of a bf16 pair is an infinity or a NaN.
 __device__ __forceinline__ bool nonfinite2(uint32_t v) {
   return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;

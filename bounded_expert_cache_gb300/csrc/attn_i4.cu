@@ -11,9 +11,9 @@ namespace {
 template <class T, int G, int KT>
 cudaError_t decode_codes(const AttnArgs& a, int num_sms, cudaStream_t st) {
   const int rows = a.n_q * a.g;
-  if (rows <= 8) return decode_rows<CodesEngine<T, G, 1, KT>>(a, num_sms, st);
-  if (rows <= 16 || G > 2 || sizeof(T) == 4) return decode_rows<CodesEngine<T, G, 2, KT>>(a, num_sms, st);
-  if constexpr (G <= 2 && sizeof(T) == 2) return decode_rows<CodesEngine<T, G, 4, KT>>(a, num_sms, st);
+  if (rows <= 8) return decode_rows<CodesEngine<T, G, 1, (G <= 2 && sizeof(T) == 2) ? 512 : KT, (G <= 2 && sizeof(T) == 2) ? 16 : 8>>(a, num_sms, st);
+  if (rows <= 16 || G > 2 || sizeof(T) == 4) return decode_rows<CodesEngine<T, G, 2, KT, 8>>(a, num_sms, st);
+  if constexpr (G <= 2 && sizeof(T) == 2) return decode_rows<CodesEngine<T, G, 4, KT, 8>>(a, num_sms, st);
   return cudaErrorInvalidValue;
 }
 template <class T>

@@ -6,13 +6,17 @@
 // b'_tg with b' = b + 8 s, so that for a query x and numerators p
 //   x.k_t   = sum_g s_tg (sum_d x_d (q_td - 8)) + b'_tg sum_d x_d
 //   sum_t p_t v_td = sum_t (p_t s_tg) (q_td - 8) + sum_t p_t b'_tg.
-// The matrix instructions multiply codes: q - 8 is exact in bf16, and so are its
-// products with a bf16 x. Scales and offsets are applied in fp32 to the scores of
-// a group, and to the numerators before they become an operand; the offsets' sums
-// stay in fp32. An f32 x, and an f32 call's p s, are multiplied as three bf16 that
-// add up to it. For bf16 calls p s is rounded to bf16 once, as p is over bf16
-// pages. Codes are centred because that rounding is multiplied by them: of q
-// itself it would carry 2.5 times the noise.
+// The matrix instructions multiply codes, q - 8, which are exact in f16 and in bf16.
+// Scales and offsets are applied in fp32 to the scores of a group, and to the numerators
+// before they become an operand; the offsets' sums stay in fp32. bf16 calls multiply f16:
+// x exactly, p s rounded to f16 once (error against 64 bits 1.7e-3 of the norm, nearly all
+// of it the result's own rounding to bf16; with p s in bf16 2.4e-3). f16's range is made
+// up for by powers of two: a row's x is divided by one if its largest is above 2^14 or
+// below 2^-8, and p s by that of the largest scale come across. (What is then below 2^-24
+// is lost: a 2^-30th of the row's largest x, and of a value with the largest scale.) f32
+// calls multiply x and p s as three bf16 that add up to them.
+// Codes are centred because the rounding of p s is multiplied by them: of q itself it
+// would carry 2.5 times the noise.
 //
 // The scores are formed transposed, S^T = K Q^T, so that a warp's 16 tokens are
 // the rows of the instruction and eight query rows its columns: eight heads that
@@ -21,28 +25,52 @@
 // movmatrix. Which of a group's dimensions takes which place of a fragment is
 // free as long as both operands agree: a thread takes whole words of eight codes,
 // and nibbles i and i + 4 (K), or nibble i of two tokens (V), become a pair of
-// bf16 by one and-or into the mantissa of 128 and one subtraction.
+// f16 by one and-or into the mantissa of 1024 and one subtraction. The integer pipe,
+// at half the rate of the others, is what bounds few rows: f16's ten bits take a
+// nibble at either end of a byte, so a word needs one shift, bf16's seven three.
 //
 // What a row does not see cannot reach it: hidden scores are -inf by selection,
 // and a hidden token's scale and offset, which may be anything, are left out of
 // its numerator's products by selection.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "attn_split.cuh"
 
 namespace moe {
 namespace {
 
-__device__ __forceinline__ void mma_codes(float* d, const uint32_t* a, const uint32_t* b) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+// d (+)= a b; HALF: f16 operands, else bf16
+template <bool HALF>
+__device__ __forceinline__ void mma_codes(float* d, const uint32_t* a, const uint32_t* b, bool first = false) {
+#define MOE_MMA(T, C0, C1, C2, C3)                                                                                          \
+  asm("mma.sync.aligned.m16n8k16.row.col.f32." T "." T ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"      \
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                                                       \
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(C0), "f"(C1), "f"(C2), "f"(C3))
+  const float c[4] = {first ? 0.f : d[0], first ? 0.f : d[1], first ? 0.f : d[2], first ? 0.f : d[3]};
+  if constexpr (HALF)
+    MOE_MMA("f16", c[0], c[1], c[2], c[3]);
+  else
+    MOE_MMA("bf16", c[0], c[1], c[2], c[3]);
+#undef MOE_MMA
 }
-// q - 8 of nibbles i and i + 4 as a pair of bf16: 128 + q has q as its last bits
-__device__ __forceinline__ uint32_t centred(uint32_t w, int i) {
-  const uint32_t m = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-  __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m), __floats2bfloat162_rn(136.f, 136.f));
-  return *reinterpret_cast<uint32_t*>(&v);
+// q - 8 of nibbles i and i + 4 of a word as a pair: the magnitude that a nibble is the last bits of goes off again
+template <bool HALF>
+constexpr uint32_t kMagic = HALF ? 0x64006400u : 0x43004300u;
+template <bool HALF>
+__device__ __forceinline__ uint32_t centred(uint32_t w, int i, uint32_t magic) {
+  if constexpr (HALF) {
+    const uint32_t at = i < 2 ? w : w >> 8;
+    const uint32_t m = i & 1 ? and_or<0x00F000F0u>(at, magic) : and_or<0x000F000Fu>(at, magic);  // 1024 + q, or 1024 + 16 q
+    const __half2 h = *reinterpret_cast<const __half2*>(&m);
+    const __half2 v = i & 1 ? __hfma2(h, __float2half2_rn(0.0625f), __float2half2_rn(-72.f)) : __hsub2(h, __float2half2_rn(1032.f));
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const uint32_t m = and_or<0x000F000Fu>(w >> (4 * i), magic);  // 128 + q
+    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m), __floats2bfloat162_rn(136.f, 136.f));
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
 }
 __device__ __forceinline__ uint32_t transposed(uint32_t m) {
   uint32_t r;
@@ -62,9 +90,28 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 // scale and offset (for centred codes) of a metadata word
 __device__ __forceinline__ float scale_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float offset_of(uint32_t w) { return fmaf(8.f, scale_of(w), __uint_as_float(w & 0xFFFF0000u)); }
-// the bf16 parts of a pair: what is left after each is the next one's
+// a token's metadata words
+template <int G>
+__device__ __forceinline__ void load_meta(uint32_t at, uint32_t* m) {
+  if constexpr (G == 4) {
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(m[0]), "=r"(m[1]), "=r"(m[2]), "=r"(m[3]) : "r"(at));
+  } else if constexpr (G == 2) {
+    const uint2 v = lds64(at);
+    m[0] = v.x;
+    m[1] = v.y;
+  } else {
+#pragma unroll
+    for (int g = 0; g < G; ++g) m[g] = lds32(at + 4 * g);
+  }
+}
+// a pair as f16 (N = 1), or its bf16 parts: what is left after each is the next one's
 template <int N>
 __device__ __forceinline__ void split_pair(float x, float y, uint32_t* part) {
+  if constexpr (N == 1) {
+    const __half2 h = __floats2half2_rn(x, y);
+    part[0] = *reinterpret_cast<const uint32_t*>(&h);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     part[i] = pack_bf16(x, y);
@@ -75,15 +122,16 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t* part) {
   }
 }
 
-// G groups of 64 a head, 8 NR query rows, tiles of KT tokens of which each warp
-// takes every eighth 16.
-template <class T_, int G_, int NR_, int KT_>
+// G groups of 64 a head, 8 NR query rows, tiles of KT tokens of which each of W warps
+// takes every W-th 16.
+template <class T_, int G_, int NR_, int KT_, int W_>
 struct CodesEngine {
   using T = T_;
-  static constexpr int G = G_, NR = NR_, KT = KT_;
+  static constexpr int G = G_, NR = NR_, KT = KT_, kW = W_;
   static constexpr int DP = G == 1 ? 64 : (G == 2 ? 128 : 256);
-  static constexpr int kRows = 8 * NR, CH = KT / (16 * kWarps), NB = 1;
-  static constexpr int kParts = sizeof(T) == 4 ? 3 : 1;  // bf16 parts of an operand
+  static constexpr int kRows = 8 * NR, CH = KT / (16 * kW), NB = 1;
+  static constexpr bool kHalf = sizeof(T) == 2;
+  static constexpr int kParts = kHalf ? 1 : 3;  // parts of an operand
   static constexpr bool kCodes = true;
   static constexpr int kRowBytes = 32 * G, kMetaBytes = 4 * G, kMostSlots = 12;
   static constexpr uint32_t kTileBytes = KT * (kRowBytes + kMetaBytes);
@@ -92,9 +140,9 @@ struct CodesEngine {
   // Q as fragments in registers, or in shared memory where there are too many
   static constexpr bool kQInSmem = kSteps * NR * kParts > 32;
   static constexpr int kQBytes = kQInSmem ? kSteps * NR * kParts * 256 : 0;
-  static constexpr int kMl = kWarps * kRows;
-  static constexpr int kMergeBytes = kWarps * kRows * 64 * 4 + kQBytes;
-  static_assert(CH >= 1 && CH * 16 * kWarps == KT, "token groups");
+  static constexpr int kMl = kW * kRows;
+  static constexpr int kMergeBytes = kW * kRows * 64 * 4 + kQBytes;
+  static_assert(CH >= 1 && CH * 16 * kW == KT, "token groups");
 
   uint32_t qf[kQInSmem ? 1 : kParts * NR * kSteps][2];
   uint32_t qs;           // shared copy of the fragments
@@ -104,11 +152,19 @@ struct CodesEngine {
   float x[CH][NR][4];    // scores, then numerators: tokens r and r + 8, two columns each
   uint32_t seen[CH];     // of an edge tile: bit 4 nt + i of x visible
   float m[NR][2], thr[NR][2], l[NR][2];
+  float cs[NR][2];       // scale log2(e), times the power of two that the row's x was divided by
+  // f16: the numerators' products are kept divided by a power of two: 1 / it, and the
+  // scale from which on it has to grow (below 0: any)
+  float v_inv, v_most;
+  uint32_t magic;        // kMagic
   int pos[NR][2];        // -1: no row
   int lo_pos, hi_pos;    // of the unit's rows
   bool edge;             // the tile holds a token seen by some but not all of the rows
 
-  __device__ __forceinline__ void place(float* buf) { qs = su32(buf) + kWarps * kRows * 64 * 4; }
+  __device__ __forceinline__ void place(float* buf) {
+    qs = su32(buf) + kW * kRows * 64 * 4;
+    magic = in_register(kMagic<kHalf>);
+  }
   __device__ __forceinline__ const uint32_t* fragment(int part, int nt, int step, uint32_t* tmp) const {
     const int at = (part * NR + nt) * kSteps + step;
     if constexpr (kQInSmem) {
@@ -121,6 +177,22 @@ struct CodesEngine {
     }
   }
 
+  // eight values in fp32; zeros without an address
+  __device__ __forceinline__ static void load8(const T* at, float* v) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 u0 = at ? __ldg(reinterpret_cast<const float4*>(at)) : z, u1 = at ? __ldg(reinterpret_cast<const float4*>(at) + 1) : z;
+      v[0] = u0.x, v[1] = u0.y, v[2] = u0.z, v[3] = u0.w, v[4] = u1.x, v[5] = u1.y, v[6] = u1.z, v[7] = u1.w;
+    } else {
+      const uint4 u = at ? __ldg(reinterpret_cast<const uint4*>(at)) : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t us[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(us[i] << 16);
+        v[2 * i + 1] = __uint_as_float(us[i] & 0xFFFF0000u);
+      }
+    }
+  }
   __device__ __forceinline__ void begin(const AttnArgs& a, const Cursor& c) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, cc = lane & 3;
     lo_pos = c.s.len - c.s.m + c.token(a, 0);
@@ -131,39 +203,47 @@ struct CodesEngine {
       const T* q = nullptr;
       if (row < c.rows)
         q = static_cast<const T*>(a.q) + static_cast<int64_t>(c.s.row0 + c.token(a, row)) * a.ldq + c.head(a, row) * a.D;
+      float v[G][2][8];
+      float top = 0.f;
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          load8(q ? q + 64 * g + 16 * cc + 8 * w : nullptr, v[g][w]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (fabsf(v[g][w][i]) < INFINITY) top = fmaxf(top, fabsf(v[g][w][i]));
+        }
+      float f = 1.f, c_row = a.scale_log2;
+      if constexpr (kHalf) {
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        if (top > 16384.f || (top < 0x1p-8f && top > 0.f)) {
+          const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 137, -120);  // about 2^10 is left
+          f = exp2f(static_cast<float>(-e));
+          c_row *= exp2f(static_cast<float>(e));
+        }
+      }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          // eight dimensions; a product takes pairs (i, i + 4)
-          float v[8] = {};
-          if (q) {
-            const T* at = q + 64 * g + 16 * cc + 8 * w;
-            if constexpr (sizeof(T) == 4) {
-              const float4 u0 = __ldg(reinterpret_cast<const float4*>(at)), u1 = __ldg(reinterpret_cast<const float4*>(at) + 1);
-              v[0] = u0.x, v[1] = u0.y, v[2] = u0.z, v[3] = u0.w, v[4] = u1.x, v[5] = u1.y, v[6] = u1.z, v[7] = u1.w;
-            } else {
-              const uint4 u = __ldg(reinterpret_cast<const uint4*>(at));
-              const uint32_t us[4] = {u.x, u.y, u.z, u.w};
+          // a product takes pairs (i, i + 4) of eight dimensions
+          float (&u)[8] = v[g][w];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(us[i] << 16);
-                v[2 * i + 1] = __uint_as_float(us[i] & 0xFFFF0000u);
-              }
-            }
-          }
-          sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+          for (int i = 0; i < 8; ++i) u[i] *= f;
+          sum += ((u[0] + u[1]) + (u[2] + u[3])) + ((u[4] + u[5]) + (u[6] + u[7]));
           uint32_t pair[4][kParts];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) split_pair<kParts>(v[i], v[i + 4], pair[i]);
+          for (int i = 0; i < 4; ++i) split_pair<kParts>(u[i], u[i + 4], pair[i]);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int part = 0; part < kParts; ++part) {
               const int at = (part * NR + nt) * kSteps + (g * 2 + w) * 2 + h;
               if constexpr (kQInSmem) {
-                if (at % kWarps == warp)
+                if (at % kW == warp)
                   asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(qs + at * 256 + lane * 8), "r"(pair[2 * h][part]),
                                "r"(pair[2 * h + 1][part])
                                : "memory");
@@ -186,6 +266,7 @@ struct CodesEngine {
         const int col = 8 * nt + 2 * cc + e;
         pos[nt][e] = col < c.rows ? c.s.len - c.s.m + c.token(a, col) : -1;
         m[nt][e] = thr[nt][e] = -INFINITY;
+        cs[nt][e] = __shfl_sync(~0u, c_row, 8 * cc + 4 * e);
         l[nt][e] = 0.f;
       }
 #pragma unroll
@@ -193,7 +274,9 @@ struct CodesEngine {
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[t][nt][i] = 0.f;
     }
-    if constexpr (kQInSmem) sync_compute();
+    v_inv = 1.f;
+    v_most = -1.f;
+    if constexpr (kQInSmem) sync_compute<kW>();
   }
 
   __device__ __forceinline__ void scores(const AttnArgs& a, const Cursor& c, const Tile& kt) {
@@ -202,32 +285,39 @@ struct CodesEngine {
     edge = tile0 + KT - 1 > lo_pos || (a.window > 0 && hi_pos - tile0 >= a.window);
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
-      const int key = (ch * kWarps + warp) * 16 + r;
+      const int key = (ch * kW + warp) * 16 + r;
       const uint32_t at = kt.base + key * kRowBytes + 8 * cc, meta = kt.base + KT * kRowBytes + key * kMetaBytes;
 #pragma unroll
       for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[ch][nt][i] = 0.f;
+      uint32_t m0[G], m1[G];
+      load_meta<G>(meta, m0);
+      load_meta<G>(meta + 8 * kMetaBytes, m1);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const uint2 w0 = lds64(at + 32 * g), w1 = lds64(at + 8 * kRowBytes + 32 * g);
-        const uint32_t m0 = lds32(meta + 4 * g), m1 = lds32(meta + 8 * kMetaBytes + 4 * g);
-        float acc[NR][4] = {};
+        float acc[NR][4];
 #pragma unroll
         for (int w = 0; w < 2; ++w)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t c0 = w ? w0.y : w0.x, c1 = w ? w1.y : w1.x;
-            const uint32_t k[4] = {centred(c0, 2 * h), centred(c1, 2 * h), centred(c0, 2 * h + 1), centred(c1, 2 * h + 1)};
+            uint32_t k[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t c = i & 1 ? c1 : c0;
+              k[i] = centred<kHalf>(c, 2 * h + (i >> 1), magic);
+            }
 #pragma unroll
             for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
               for (int part = 0; part < kParts; ++part) {
                 uint32_t tmp[2];
-                mma_codes(acc[nt], k, fragment(part, nt, (g * 2 + w) * 2 + h, tmp));
+                mma_codes<kHalf>(acc[nt], k, fragment(part, nt, (g * 2 + w) * 2 + h, tmp), w == 0 && h == 0 && part == 0);
               }
           }
-        const float s0 = scale_of(m0), b0 = offset_of(m0), s1 = scale_of(m1), b1 = offset_of(m1);
+        const float s0 = scale_of(m0[g]), b0 = offset_of(m0[g]), s1 = scale_of(m1[g]), b1 = offset_of(m1[g]);
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
@@ -245,7 +335,7 @@ struct CodesEngine {
         for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int j = tile0 + (ch * kWarps + warp) * 16 + r + 8 * (i >> 1);
+            const int j = tile0 + (ch * kW + warp) * 16 + r + 8 * (i >> 1);
             const int back = pos[nt][i & 1] - j;
             const bool see = back >= 0 && (a.window == 0 || back < a.window || j < a.sinks);
             if (see)
@@ -280,9 +370,9 @@ struct CodesEngine {
           v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
           f[e] = 1.f;
           if (v > thr[nt][e]) {
-            f[e] = ex2((m[nt][e] - v) * a.scale_log2);  // 0 for the first maximum
+            f[e] = ex2((m[nt][e] - v) * cs[nt][e]);  // 0 for the first maximum
             m[nt][e] = v;
-            thr[nt][e] = v + 8.f / a.scale_log2;
+            thr[nt][e] = v + 8.f / cs[nt][e];
           }
           l[nt][e] *= f[e];
 #pragma unroll
@@ -298,12 +388,12 @@ struct CodesEngine {
     for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float mc = m[nt][e] == -INFINITY ? 0.f : m[nt][e] * a.scale_log2;
+        const float mc = m[nt][e] == -INFINITY ? 0.f : m[nt][e] * cs[nt][e];
 #pragma unroll
         for (int ch = 0; ch < CH; ++ch)
 #pragma unroll
           for (int i = e; i < 4; i += 2) {
-            x[ch][nt][i] = ex2(fmaf(x[ch][nt][i], a.scale_log2, -mc));
+            x[ch][nt][i] = ex2(fmaf(x[ch][nt][i], cs[nt][e], -mc));
             l[nt][e] += x[ch][nt][i];
           }
       }
@@ -320,15 +410,32 @@ struct CodesEngine {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, cc = lane & 3;
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
-      const int key0 = (ch * kWarps + warp) * 16;
+      const int key0 = (ch * kW + warp) * 16;
       const uint32_t meta = vt.base + KT * kRowBytes + (key0 + r) * kMetaBytes;
       const uint32_t at = vt.base + (key0 + 2 * cc) * kRowBytes + 4 * r;
+      uint32_t m0[G], m1[G];
+      load_meta<G>(meta, m0);
+      load_meta<G>(meta + 8 * kMetaBytes, m1);
+      if constexpr (kHalf) {
+        float top = -1.f;  // largest scale of this thread's tokens that a row sees
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          bool see = true;
+          if (EDGE) see = seen[ch] & (h ? 0xCCCCCCCCu : 0x33333333u);
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const float s = fabsf(scale_of(h ? m1[g] : m0[g]));
+            if (see && s < INFINITY) top = fmaxf(top, s);
+          }
+        }
+        if (__any_sync(~0u, top > v_most)) widen(top);
+      }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const uint32_t m0 = lds32(meta + 4 * g), m1 = lds32(meta + 8 * kMetaBytes + 4 * g);
         const uint32_t w0 = lds32(at + 32 * g), w1 = lds32(at + kRowBytes + 32 * g);
         const uint32_t w2 = lds32(at + 8 * kRowBytes + 32 * g), w3 = lds32(at + 9 * kRowBytes + 32 * g);
-        const float s[2] = {scale_of(m0), scale_of(m1)}, b[2] = {offset_of(m0), offset_of(m1)};
+        const float s[2] = {kHalf ? scale_of(m0[g]) * v_inv : scale_of(m0[g]), kHalf ? scale_of(m1[g]) * v_inv : scale_of(m1[g])};
+        const float b[2] = {offset_of(m0[g]), offset_of(m1[g])};
         uint32_t p[NR][kParts][2];
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt)
@@ -352,16 +459,17 @@ struct CodesEngine {
         const uint32_t hi[2] = {__byte_perm(w0, w1, 0x7632), __byte_perm(w2, w3, 0x7632)};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t v[4] = {centred(lo[0], j), centred(hi[0], j), centred(lo[1], j), centred(hi[1], j)};
+          const uint32_t v[4] = {centred<kHalf>(lo[0], j, magic), centred<kHalf>(hi[0], j, magic), centred<kHalf>(lo[1], j, magic),
+                                 centred<kHalf>(hi[1], j, magic)};
 #pragma unroll
           for (int nt = 0; nt < NR; ++nt) {
             if constexpr (kParts == 1) {
-              mma_codes(o[4 * g + j][nt], v, p[nt][0]);
+              mma_codes<kHalf>(o[4 * g + j][nt], v, p[nt][0]);
             } else {
               // f32: a chunk's products are added up on their own and then to the sum in one rounding
-              float t[4] = {};
+              float t[4];
 #pragma unroll
-              for (int i = 0; i < kParts; ++i) mma_codes(t, v, p[nt][kParts - 1 - i]);
+              for (int i = 0; i < kParts; ++i) mma_codes<kHalf>(t, v, p[nt][kParts - 1 - i], i == 0);
 #pragma unroll
               for (int i = 0; i < 4; ++i) o[4 * g + j][nt][i] += t[i];
             }
@@ -369,6 +477,21 @@ struct CodesEngine {
         }
       }
     }
+  }
+
+  // A larger scale than before: products are kept divided by its power of two, until one is 64 times as large.
+  __device__ __forceinline__ void widen(float top) {
+    const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(fmaxf(top, 0.f)));
+    const int e = max(static_cast<int>(most >> 23) - 127, -100);
+    const float inv = exp2f(static_cast<float>(-e)), f = inv / v_inv;
+    v_inv = inv;
+    v_most = exp2f(static_cast<float>(min(e + 6, 127)));
+#pragma unroll
+    for (int t = 0; t < 4 * G; ++t)
+#pragma unroll
+      for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[t][nt][i] *= f;
   }
 
   // Join the warps' results in shared memory, a group's 64 columns at a time, and
@@ -386,9 +509,10 @@ struct CodesEngine {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float sum = over_tokens(l[nt][e]);
-        if (r == 0) ml[warp * kRows + 8 * nt + 2 * cc + e] = make_float2(m[nt][e] * a.scale_log2, sum);
+        if (r == 0) ml[warp * kRows + 8 * nt + 2 * cc + e] = make_float2(m[nt][e] * cs[nt][e], sum);
       }
     const int rows = c.rows;
+    const float unit = kHalf ? 1.f / v_inv : 1.f;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
 #pragma unroll
@@ -400,20 +524,20 @@ struct CodesEngine {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             *reinterpret_cast<float4*>(at + ((8 * r + 4 * h) ^ (cc << 3))) =
-                make_float4(o[4 * g][nt][2 * h + e] + b, o[4 * g + 1][nt][2 * h + e] + b, o[4 * g + 2][nt][2 * h + e] + b,
-                            o[4 * g + 3][nt][2 * h + e] + b);
+                make_float4(fmaf(o[4 * g][nt][2 * h + e], unit, b), fmaf(o[4 * g + 1][nt][2 * h + e], unit, b),
+                            fmaf(o[4 * g + 2][nt][2 * h + e], unit, b), fmaf(o[4 * g + 3][nt][2 * h + e], unit, b));
         }
-      sync_compute();
-      for (int e = threadIdx.x; e < rows * 16; e += kCompute) {
+      sync_compute<kW>();
+      for (int e = threadIdx.x; e < rows * 16; e += 32 * kW) {
         const int row = e >> 4, col = (e & 15) * 4;
         float M = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) M = fmaxf(M, ml[k * kRows + row].x);
+        for (int k = 0; k < kW; ++k) M = fmaxf(M, ml[k * kRows + row].x);
         const float Mu = M == -INFINITY ? 0.f : M;
         float L = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
+        for (int k = 0; k < kW; ++k) {
           const float2 t = ml[k * kRows + row];
           const float f = ex2(t.x - Mu);
           L += f * t.y;
@@ -425,7 +549,7 @@ struct CodesEngine {
         }
         store(row, 64 * g + col, v, M, L);
       }
-      sync_compute();
+      sync_compute<kW>();
     }
   }
 };

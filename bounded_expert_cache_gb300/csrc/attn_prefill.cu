@@ -454,7 +454,7 @@ __device__ __forceinline__ void fill_tiles(const AttnArgs& a, Walk w, Sh& sh, ui
   auto convert = [&](uint32_t src, uint32_t dst, float f) {
     uint32_t from = src + row0 * C::kCodeRow + piece * 16, meta = src + kKT * C::kCodeRow + row0 * C::kMetaRow + (piece >> 1) * 4;
     dst += (piece >> 1) * C::kHalf + row0 * 128u;
-    const uint32_t turn = piece & 2;
+    const uint32_t turn = piece & 2, magic = in_register(0x64006400u);
     uint32_t c[4], m;
     auto read = [&]() {
       asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(from));
@@ -477,7 +477,7 @@ __device__ __forceinline__ void fill_tiles(const AttnArgs& a, Walk w, Sh& sh, ui
         for (int z = 0; z < 4; ++z) {
           // 1024 + q has q as its last bits, 1024 + 16 q as the four before: one shift a word
           const uint32_t at = z < 2 ? word[y] : word[y] >> 8;
-          const uint32_t n = (at & (z & 1 ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+          const uint32_t n = z & 1 ? and_or<0x00F000F0u>(at, magic) : and_or<0x000F000Fu>(at, magic);
           const __half2 h = *reinterpret_cast<const __half2*>(&n);
           const __half2 q = z & 1 ? __hfma2(h, __float2half2_rn(0.0625f), __float2half2_rn(-64.f)) : __hsub2(h, __float2half2_rn(1024.f));
           const __half2 val = __hfma2(q, s, b);

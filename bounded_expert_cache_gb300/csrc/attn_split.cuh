@@ -17,12 +17,14 @@ namespace {
 
 using namespace tc;
 
-constexpr int kWarps = 8;  // computing warps; the first warp of a third warpgroup copies
+constexpr int kWarps = 8;  // computing warps of the engines of values (E::kW); the first warp of a further warpgroup copies
 constexpr int kCompute = 32 * kWarps;
-constexpr int kThreads = kCompute + 128;
 
 // barrier of the computing warps
-__device__ __forceinline__ void sync_compute() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+template <int W = kWarps>
+__device__ __forceinline__ void sync_compute() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");
+}
 __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
   tma4d(dst, m, bar, x, y, 0, z);
 }
@@ -136,6 +138,7 @@ __device__ __forceinline__ void write_out(const AttnArgs& a, const Cursor& c, in
 
 // Block-wide inclusive scan of one int64 per thread; returns the thread's
 // exclusive prefix and the total.
+template <int THREADS>
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t x = v;
@@ -148,7 +151,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t* 
   __syncthreads();
   int64_t base = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) base += tmp[w];
     all += tmp[w];
   }
@@ -166,13 +169,15 @@ struct Ring {
 };
 
 // SPLIT: runs of the line of tiles (decode). Otherwise one unit a CTA (chunks).
+template <class E>
+constexpr int kThreadsOf = 32 * E::kW + 128;
 template <class E, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsOf<E>, 1)
     attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, AttnArgs a,
                 int boxes) {
   constexpr int NS = Ring<E>::kSlots;
   static_assert(NS >= 3, "ring");
-  constexpr int KT = E::KT, R = E::kRows;
+  constexpr int KT = E::KT, R = E::kRows, W = E::kW, kThreads = kThreadsOf<E>;
   extern __shared__ __align__(1024) unsigned char sm[];
   __shared__ uint64_t b_full[NS], b_empty[NS];
   __shared__ int64_t s_scan[kThreads / 32];
@@ -199,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_found[0] = -1;
     for (int i = 0; i < NS; ++i) {
       mbar_init(su32(&b_full[i]), 1);
-      mbar_init(su32(&b_empty[i]), kWarps);
+      mbar_init(su32(&b_empty[i]), W);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -219,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b0 = 0; b0 < a.n; b0 += kThreads) {
       mine = line_of(b0 + threadIdx.x);
       int64_t t;
-      ex = block_scan(mine, s_scan, &t);
+      ex = block_scan<kThreads>(mine, s_scan, &t);
       all += t;
     }
     total = all;
@@ -231,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t t = total;
       if (a.n > kThreads) {
         mine = line_of(b0 + threadIdx.x);
-        ex = base + block_scan(mine, s_scan, &t);
+        ex = base + block_scan<kThreads>(mine, s_scan, &t);
       }
       if (run0 >= ex && run0 < ex + mine) {
         s_found[0] = b0 + threadIdx.x;
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t mine = 0, t;
       if (b0 + static_cast<int>(threadIdx.x) < a.n)
         mine = (static_cast<int64_t>(chunk_rows(a, b0 + threadIdx.x)) * a.g + R - 1) / R;
-      const int64_t ex = base + block_scan(mine, s_scan, &t);
+      const int64_t ex = base + block_scan<kThreads>(mine, s_scan, &t);
       if (want >= ex && want < ex + mine) {
         s_found[0] = b0 + threadIdx.x;
         s_found[1] = want - ex;
@@ -280,10 +285,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int shift = min(a.page_shift, 31 - __clz(KT));  // log2 of a box's tokens
 
   // Registers: the block is launched with 384 x 168; the computing warpgroups
-  // take 216 a thread, the third keeps 72 (256 x 216 + 128 x 72 = 384 x 168).
-  if (warp >= kWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp > kWarps) return;
+  // take 216 a thread, the third keeps 72 (256 x 216 + 128 x 72 = 384 x 168). With
+  // sixteen computing warps: 640 x 96 become 512 x 112 and 128 x 32.
+  static_assert(W == 8 || W == 16, "registers");
+  if (warp >= W) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W == 8 ? 72 : 32));
+    if (warp > W) return;
     // ---------------- copies: lane i brings page i of the tile; pages that no
     // row sees are left out
     const int per = KT >> shift;
@@ -343,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---------------- computing warps
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(W == 8 ? 216 : 112));
   E eng;
   eng.place(merge);
   RingPos rp;
@@ -486,7 +493,7 @@ cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
   constexpr int smem = Ring<E>::kSmem;
   e = cudaFuncSetAttribute(attn_kernel<E, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attn_kernel<E, SPLIT><<<grid, kThreads, smem, st>>>(mk, mv, a, boxes);
+  attn_kernel<E, SPLIT><<<grid, kThreadsOf<E>, smem, st>>>(mk, mv, a, boxes);
   return cudaGetLastError();
 }
 

@@ -313,7 +313,7 @@ def test_codes_past_32_bit_offsets(bec):
 @pytest.mark.parametrize("copies,window", [(0, 0), (0, 200), (1, 0), (5, 0)])
 def test_attention_over_codes_whose_wait_times_out_leaves_the_cache_usable(bec, kind, dtype, D, copies, window):
     # several tiles a CTA: the hook stops it between them
-    lens = [70000, 35000, 70]
+    lens = [160000, 80000, 70]
     pool = Codes(bec, lens, 16, 2, D, dtype, 21)
     ms = [1] * 3 if kind == "decode" else [300, 129, 70]
     q = randn((sum(ms), 4, D), dtype, gen(5))
