@@ -81,8 +81,7 @@ struct MmaEngine {
   static constexpr int kMergeBytes = kWarps * 16 * 64 * 4 + (kQInSmem ? kRows * kQPitch : 0);
   static constexpr int kMl = kWarps * 16;
   static constexpr bool kCodes = false;
-  static constexpr int kW = kWarps;
-  static constexpr int kRowBytes = 0, kMostSlots = 8;
+  static constexpr int kRowBytes = 0, kMostSlots = 8, kGroup = 1;
   static_assert(KC >= 1 && KC * KG * 16 == KT, "token groups");
 
   uint32_t qf[kQInSmem ? 1 : DP / 16][4];
@@ -363,7 +362,7 @@ struct MmaEngine {
         for (int h = 0; h < 2; ++h)
           *reinterpret_cast<float2*>(buf + (warp * 16 + lane / 4 + 8 * h) * 64 + ((n * 8 + (lane & 3) * 2) ^ ((lane & 12) << 1))) =
               make_float2(o[n0 / 8 + n][2 * h], o[n0 / 8 + n][2 * h + 1]);
-      sync_compute<>();
+      sync_compute();
       for (int e = threadIdx.x; e < rows * 16; e += kCompute) {
         const int r = e >> 4, col = (e & 15) * 4;
         if (n0 + col < a.D) {
@@ -389,7 +388,7 @@ struct MmaEngine {
           store(r, n0 + col, v, M, L);
         }
       }
-      sync_compute<>();
+      sync_compute();
     }
   }
 };
@@ -419,8 +418,7 @@ struct FmaEngine {
   static constexpr int kMergeBytes = (kSum + kRows * DP + kRows * KT + KT * kSP + kRows) * 4;
   static constexpr int kMl = kWarps * 16;
   static constexpr bool kCodes = false;
-  static constexpr int kW = kWarps;
-  static constexpr int kRowBytes = 0, kMostSlots = 8;
+  static constexpr int kRowBytes = 0, kMostSlots = 8, kGroup = 1;
   static_assert(P >= 4 && P <= 32 && KT % TG == 0, "work of a thread");
 
   float4 o[kRows];
@@ -450,7 +448,7 @@ struct FmaEngine {
       m[h] = -INFINITY;
       l[h] = 0.f;
     }
-    sync_compute<>();
+    sync_compute();
   }
 
   __device__ __forceinline__ static float4 lds4(uint32_t addr) {
@@ -521,7 +519,7 @@ struct FmaEngine {
     const int lo_pos = pos_of(a, c, 0);
     const int hi_pos = c.s.len - c.s.m + c.token(a, c.rows - 1);
     edge = tile0 + KT - 1 > lo_pos || (a.window > 0 && hi_pos - tile0 >= a.window);
-    sync_compute<>();
+    sync_compute();
 #pragma unroll
     for (int h = 0; h < (kRows + kWarps - 1) / kWarps; ++h) {
       const int rr = warp + kWarps * h;
@@ -547,7 +545,7 @@ struct FmaEngine {
       }
       if (lane == 0) fs[rr] = f;
     }
-    sync_compute<>();
+    sync_compute();
   }
 
   __device__ __forceinline__ void values(const AttnArgs& a, const Cursor& c, const Tile& vt) {
@@ -613,7 +611,7 @@ struct FmaEngine {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         *reinterpret_cast<float4*>(sum + (tg * 4 + r) * DP + c4 * 4) = o[r0 + r];
-      sync_compute<>();
+      sync_compute();
       for (int e = threadIdx.x; e < 4 * kC4; e += kCompute) {
         const int r = e / kC4, col = e % kC4 * 4;
         if (r0 + r < rows && col < a.D) {
@@ -626,7 +624,7 @@ struct FmaEngine {
           store(r0 + r, col, v, ml[r0 + r].x, ml[r0 + r].y);
         }
       }
-      sync_compute<>();
+      sync_compute();
     }
   }
 };

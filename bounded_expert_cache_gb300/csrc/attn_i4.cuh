@@ -15,8 +15,11 @@
 // below 2^-8, and p s by that of the largest scale come across. (What is then below 2^-24
 // is lost: a 2^-30th of the row's largest x, and of a value with the largest scale.) f32
 // calls multiply x and p s as three bf16 that add up to them.
-// Codes are centred because the rounding of p s is multiplied by them: of q itself it
-// would carry 2.5 times the noise.
+// V's codes are centred because the rounding of p s is multiplied by them: of q itself
+// it would carry 2.5 times the noise. K's are not, for f16: their operand keeps the
+// magnitude of 1024 that unpacking gives them (and the factor of 16 of every other
+// pair, which x is divided by), and the sum starts at what that adds up to, negative.
+// Sums of some thousand times x then keep 2^-24 of that, a score's 2^-15 or so.
 //
 // The scores are formed transposed, S^T = K Q^T, so that a warp's 16 tokens are
 // the rows of the instruction and eight query rows its columns: eight heads that
@@ -41,14 +44,13 @@
 namespace moe {
 namespace {
 
-// d (+)= a b; HALF: f16 operands, else bf16
+// d = a b + c; HALF: f16 operands, else bf16
 template <bool HALF>
-__device__ __forceinline__ void mma_codes(float* d, const uint32_t* a, const uint32_t* b, bool first = false) {
+__device__ __forceinline__ void mma_codes(float* d, const uint32_t* a, const uint32_t* b, const float* c) {
 #define MOE_MMA(T, C0, C1, C2, C3)                                                                                          \
   asm("mma.sync.aligned.m16n8k16.row.col.f32." T "." T ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"      \
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                                                       \
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(C0), "f"(C1), "f"(C2), "f"(C3))
-  const float c[4] = {first ? 0.f : d[0], first ? 0.f : d[1], first ? 0.f : d[2], first ? 0.f : d[3]};
   if constexpr (HALF)
     MOE_MMA("f16", c[0], c[1], c[2], c[3]);
   else
@@ -58,11 +60,15 @@ __device__ __forceinline__ void mma_codes(float* d, const uint32_t* a, const uin
 // q - 8 of nibbles i and i + 4 of a word as a pair: the magnitude that a nibble is the last bits of goes off again
 template <bool HALF>
 constexpr uint32_t kMagic = HALF ? 0x64006400u : 0x43004300u;
+// 1024 + q of nibbles 0 and 4 or 2 and 6, 1024 + 16 q of the others
+__device__ __forceinline__ uint32_t raised(uint32_t w, int i, uint32_t magic) {
+  const uint32_t at = i < 2 ? w : w >> 8;
+  return i & 1 ? and_or<0x00F000F0u>(at, magic) : and_or<0x000F000Fu>(at, magic);
+}
 template <bool HALF>
 __device__ __forceinline__ uint32_t centred(uint32_t w, int i, uint32_t magic) {
   if constexpr (HALF) {
-    const uint32_t at = i < 2 ? w : w >> 8;
-    const uint32_t m = i & 1 ? and_or<0x00F000F0u>(at, magic) : and_or<0x000F000Fu>(at, magic);  // 1024 + q, or 1024 + 16 q
+    const uint32_t m = raised(w, i, magic);
     const __half2 h = *reinterpret_cast<const __half2*>(&m);
     const __half2 v = i & 1 ? __hfma2(h, __float2half2_rn(0.0625f), __float2half2_rn(-72.f)) : __hsub2(h, __float2half2_rn(1032.f));
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -110,59 +116,68 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t* part) {
   if constexpr (N == 1) {
     const __half2 h = __floats2half2_rn(x, y);
     part[0] = *reinterpret_cast<const uint32_t*>(&h);
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    part[i] = pack_bf16(x, y);
-    if (i + 1 < N) {
-      x -= __uint_as_float(part[i] << 16);
-      y -= __uint_as_float(part[i] & 0xFFFF0000u);
+    for (int i = 0; i < N; ++i) {
+      part[i] = pack_bf16(x, y);
+      if (i + 1 < N) {
+        x -= __uint_as_float(part[i] << 16);
+        y -= __uint_as_float(part[i] & 0xFFFF0000u);
+      }
     }
   }
 }
 
-// G groups of 64 a head, 8 NR query rows, tiles of KT tokens of which each of W warps
-// takes every W-th 16.
-template <class T_, int G_, int NR_, int KT_, int W_>
+// G groups of 64 a head, 8 NR query rows, tiles of 128 tokens of which each warp takes
+// 16. Up to GROUP tiles are worked on together: a warp's steps are chains of dependent
+// instructions, and several chains hide each other (three contexts of 131K to 262K
+// tokens: 212 us with 1, 171 with 2, 154 with 4, which leaves three slots, and with 6,
+// which leaves two; heads of 64: 93 with 4, 83 with 8); one by one at a unit's end (in
+// twos, too: 161, for the code's size).
+template <class T_, int G_, int NR_, int GROUP>
 struct CodesEngine {
   using T = T_;
-  static constexpr int G = G_, NR = NR_, KT = KT_, kW = W_;
+  static constexpr int G = G_, NR = NR_, KT = 16 * kWarps, kGroup = GROUP;
   static constexpr int DP = G == 1 ? 64 : (G == 2 ? 128 : 256);
-  static constexpr int kRows = 8 * NR, CH = KT / (16 * kW), NB = 1;
+  static constexpr int kRows = 8 * NR, NB = 1;
   static constexpr bool kHalf = sizeof(T) == 2;
   static constexpr int kParts = kHalf ? 1 : 3;  // parts of an operand
   static constexpr bool kCodes = true;
   static constexpr int kRowBytes = 32 * G, kMetaBytes = 4 * G, kMostSlots = 12;
   static constexpr uint32_t kTileBytes = KT * (kRowBytes + kMetaBytes);
-  static constexpr int kUnitCost = 3;
+  // tiles' worth of time of a unit's Q, join of the warps and results (10 contexts to
+  // 32,768 tokens, heads of 256: 41 us with 2, 35 with 6; 40 contexts, of 128: 31 with 3, 34 with 8)
+  static constexpr int kUnitCost = G > 2 ? 6 : 3;
   static constexpr int kSteps = 4 * G;  // products of 16 dimensions
   // Q as fragments in registers, or in shared memory where there are too many
   static constexpr bool kQInSmem = kSteps * NR * kParts > 32;
   static constexpr int kQBytes = kQInSmem ? kSteps * NR * kParts * 256 : 0;
-  static constexpr int kMl = kW * kRows;
-  static constexpr int kMergeBytes = kW * kRows * 64 * 4 + kQBytes;
-  static_assert(CH >= 1 && CH * 16 * kW == KT, "token groups");
+  static constexpr int kMl = kWarps * kRows;
+  static constexpr int kMergeCols = NR == 1 ? 32 : 64;  // columns joined at a time
+  static constexpr int kMergeBytes = kWarps * kRows * kMergeCols * 4 + kQBytes;
 
   uint32_t qf[kQInSmem ? 1 : kParts * NR * kSteps][2];
   uint32_t qs;           // shared copy of the fragments
-  float qsum[G][NR][2];  // sums of a group's x, of this thread's columns (query rows 8 nt + 2 c and + 1)
+  // of this thread's columns (query rows 8 nt + 2 c and + 1): sums of a group's x, and
+  // what its products with the magnitudes of K's operand add up to, negative
+  float qsum[G][NR][2], lift[G][NR][2];
   float o[4 * G][NR][4];
   float bias[G][NR][2];  // this thread's share of the offsets' sums
-  float x[CH][NR][4];    // scores, then numerators: tokens r and r + 8, two columns each
-  uint32_t seen[CH];     // of an edge tile: bit 4 nt + i of x visible
+  float x[GROUP][NR][4]; // scores, then numerators: tokens r and r + 8, two columns each
+  uint32_t seen[GROUP];  // of an edge tile: bit 4 nt + i of x visible
   float m[NR][2], thr[NR][2], l[NR][2];
   float cs[NR][2];       // scale log2(e), times the power of two that the row's x was divided by
   // f16: the numerators' products are kept divided by a power of two: 1 / it, and the
-  // scale from which on it has to grow (below 0: any)
-  float v_inv, v_most;
+  // bits of the scale from which on it has to grow (0: any)
+  float v_inv;
+  uint32_t v_limit;
   uint32_t magic;        // kMagic
   int pos[NR][2];        // -1: no row
   int lo_pos, hi_pos;    // of the unit's rows
   bool edge;             // the tile holds a token seen by some but not all of the rows
 
   __device__ __forceinline__ void place(float* buf) {
-    qs = su32(buf) + kW * kRows * 64 * 4;
+    qs = su32(buf) + kWarps * kRows * kMergeCols * 4;
     magic = in_register(kMagic<kHalf>);
   }
   __device__ __forceinline__ const uint32_t* fragment(int part, int nt, int step, uint32_t* tmp) const {
@@ -226,7 +241,7 @@ struct CodesEngine {
       }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        float sum = 0.f;
+        float sum = 0.f, up = 0.f;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           // a product takes pairs (i, i + 4) of eight dimensions
@@ -236,14 +251,21 @@ struct CodesEngine {
           sum += ((u[0] + u[1]) + (u[2] + u[3])) + ((u[4] + u[5]) + (u[6] + u[7]));
           uint32_t pair[4][kParts];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) split_pair<kParts>(u[i], u[i + 4], pair[i]);
+          for (int i = 0; i < 4; ++i) {
+            const float d = kHalf && (i & 1) ? 0.0625f : 1.f;  // (K's codes are 16-fold there)
+            split_pair<kParts>(u[i] * d, u[i + 4] * d, pair[i]);
+            if constexpr (kHalf) {
+              const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&pair[i][0]));
+              up -= 1024.f * z.x + 1024.f * z.y;
+            }
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int part = 0; part < kParts; ++part) {
               const int at = (part * NR + nt) * kSteps + (g * 2 + w) * 2 + h;
               if constexpr (kQInSmem) {
-                if (at % kW == warp)
+                if (at % kWarps == warp)
                   asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(qs + at * 256 + lane * 8), "r"(pair[2 * h][part]),
                                "r"(pair[2 * h + 1][part])
                                : "memory");
@@ -255,9 +277,12 @@ struct CodesEngine {
         }
         sum += __shfl_xor_sync(~0u, sum, 1);
         sum += __shfl_xor_sync(~0u, sum, 2);
+        up += __shfl_xor_sync(~0u, up, 1);
+        up += __shfl_xor_sync(~0u, up, 2);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           qsum[g][nt][e] = __shfl_sync(~0u, sum, 8 * cc + 4 * e);
+          lift[g][nt][e] = __shfl_sync(~0u, up, 8 * cc + 4 * e);
           bias[g][nt][e] = 0.f;
         }
       }
@@ -275,18 +300,35 @@ struct CodesEngine {
         for (int i = 0; i < 4; ++i) o[t][nt][i] = 0.f;
     }
     v_inv = 1.f;
-    v_most = -1.f;
-    if constexpr (kQInSmem) sync_compute<kW>();
+    v_limit = 0u;
+    if constexpr (kQInSmem) sync_compute();
   }
 
-  __device__ __forceinline__ void scores(const AttnArgs& a, const Cursor& c, const Tile& kt) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, cc = lane & 3;
+  // n tiles of K and V, from the cursor's on
+  __device__ __forceinline__ void tiles(const AttnArgs& a, const Cursor& c, uint32_t base, int n) {
     const int tile0 = c.sp.tile(c.t) * KT;
-    edge = tile0 + KT - 1 > lo_pos || (a.window > 0 && hi_pos - tile0 >= a.window);
+    if (GROUP > 1 && n == GROUP) {
+      scores<GROUP>(a, tile0, base, 0);
+      values<GROUP>(base, 0);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        scores<1>(a, tile0 + i * KT, base, i);
+        values<1>(base, i);
+      }
+    }
+  }
+
+  // CH tiles, the first of them the slot's i0-th
+  template <int CH>
+  __device__ __forceinline__ void scores(const AttnArgs& a, int tile0, uint32_t base, int i0) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, cc = lane & 3;
+    edge = tile0 + CH * KT - 1 > lo_pos || (a.window > 0 && hi_pos - tile0 >= a.window);
+    const uint32_t key0 = (i0 * kWarps + warp) * 16 + r;
+    const uint32_t at0 = base + key0 * kRowBytes + 8 * cc, meta0 = base + GROUP * KT * kRowBytes + key0 * kMetaBytes;
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
-      const int key = (ch * kW + warp) * 16 + r;
-      const uint32_t at = kt.base + key * kRowBytes + 8 * cc, meta = kt.base + KT * kRowBytes + key * kMetaBytes;
+      const uint32_t at = at0 + ch * KT * kRowBytes, meta = meta0 + ch * KT * kMetaBytes;
 #pragma unroll
       for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
@@ -297,7 +339,12 @@ struct CodesEngine {
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const uint2 w0 = lds64(at + 32 * g), w1 = lds64(at + 8 * kRowBytes + 32 * g);
+        // f16: codes of q, lifted; f32: of q - 8
         float acc[NR][4];
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[nt][i] = lift[g][nt][i & 1];
 #pragma unroll
         for (int w = 0; w < 2; ++w)
 #pragma unroll
@@ -307,17 +354,19 @@ struct CodesEngine {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t c = i & 1 ? c1 : c0;
-              k[i] = centred<kHalf>(c, 2 * h + (i >> 1), magic);
+              k[i] = kHalf ? raised(c, 2 * h + (i >> 1), magic) : centred<kHalf>(c, 2 * h + (i >> 1), magic);
             }
 #pragma unroll
             for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
               for (int part = 0; part < kParts; ++part) {
                 uint32_t tmp[2];
-                mma_codes<kHalf>(acc[nt], k, fragment(part, nt, (g * 2 + w) * 2 + h, tmp), w == 0 && h == 0 && part == 0);
+                mma_codes<kHalf>(acc[nt], k, fragment(part, nt, (g * 2 + w) * 2 + h, tmp), acc[nt]);
               }
           }
-        const float s0 = scale_of(m0[g]), b0 = offset_of(m0[g]), s1 = scale_of(m1[g]), b1 = offset_of(m1[g]);
+        const float s0 = scale_of(m0[g]), s1 = scale_of(m1[g]);
+        const float b0 = kHalf ? __uint_as_float(m0[g] & 0xFFFF0000u) : offset_of(m0[g]);
+        const float b1 = kHalf ? __uint_as_float(m1[g] & 0xFFFF0000u) : offset_of(m1[g]);
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
@@ -335,7 +384,7 @@ struct CodesEngine {
         for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int j = tile0 + (ch * kW + warp) * 16 + r + 8 * (i >> 1);
+            const int j = tile0 + (ch * kWarps + warp) * 16 + r + 8 * (i >> 1);
             const int back = pos[nt][i & 1] - j;
             const bool see = back >= 0 && (a.window == 0 || back < a.window || j < a.sinks);
             if (see)
@@ -399,36 +448,33 @@ struct CodesEngine {
       }
   }
 
-  __device__ __forceinline__ void values(const AttnArgs&, const Cursor&, const Tile& vt) {
+  template <int CH>
+  __device__ __forceinline__ void values(uint32_t base, int i0) {
     if (edge)
-      add_values<true>(vt);
+      add_values<CH, true>(base, i0);
     else
-      add_values<false>(vt);
+      add_values<CH, false>(base, i0);
   }
-  template <bool EDGE>
-  __device__ __forceinline__ void add_values(const Tile& vt) {
+  template <int CH, bool EDGE>
+  __device__ __forceinline__ void add_values(uint32_t base, int i0) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, cc = lane & 3;
+    const uint32_t v0 = base + GROUP * kTileBytes, key0 = (i0 * kWarps + warp) * 16;
+    const uint32_t at0 = v0 + (key0 + 2 * cc) * kRowBytes + 4 * r, meta0 = v0 + GROUP * KT * kRowBytes + (key0 + r) * kMetaBytes;
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
-      const int key0 = (ch * kW + warp) * 16;
-      const uint32_t meta = vt.base + KT * kRowBytes + (key0 + r) * kMetaBytes;
-      const uint32_t at = vt.base + (key0 + 2 * cc) * kRowBytes + 4 * r;
+      const uint32_t at = at0 + ch * KT * kRowBytes, meta = meta0 + ch * KT * kMetaBytes;
       uint32_t m0[G], m1[G];
       load_meta<G>(meta, m0);
       load_meta<G>(meta + 8 * kMetaBytes, m1);
-      if constexpr (kHalf) {
-        float top = -1.f;  // largest scale of this thread's tokens that a row sees
+      if constexpr (kHalf) {  // the largest scale, of what a row sees: the low halves as they are
+        const bool see0 = !EDGE || (seen[ch] & 0x33333333u), see1 = !EDGE || (seen[ch] & 0xCCCCCCCCu);
+        uint32_t most = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          bool see = true;
-          if (EDGE) see = seen[ch] & (h ? 0xCCCCCCCCu : 0x33333333u);
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            const float s = fabsf(scale_of(h ? m1[g] : m0[g]));
-            if (see && s < INFINITY) top = fmaxf(top, s);
-          }
+        for (int g = 0; g < G; ++g) {
+          most = __vmaxu2(most, see0 ? m0[g] : 0u);
+          most = __vmaxu2(most, see1 ? m1[g] : 0u);
         }
-        if (__any_sync(~0u, top > v_most)) widen(top);
+        if (__any_sync(~0u, (most << 16) >= v_limit)) widen(m0, m1, see0, see1);
       }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
@@ -464,12 +510,12 @@ struct CodesEngine {
 #pragma unroll
           for (int nt = 0; nt < NR; ++nt) {
             if constexpr (kParts == 1) {
-              mma_codes<kHalf>(o[4 * g + j][nt], v, p[nt][0]);
+              mma_codes<kHalf>(o[4 * g + j][nt], v, p[nt][0], o[4 * g + j][nt]);
             } else {
               // f32: a chunk's products are added up on their own and then to the sum in one rounding
-              float t[4];
+              float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-              for (int i = 0; i < kParts; ++i) mma_codes<kHalf>(t, v, p[nt][kParts - 1 - i], i == 0);
+              for (int i = 0; i < kParts; ++i) mma_codes<kHalf>(t, v, p[nt][kParts - 1 - i], t);
 #pragma unroll
               for (int i = 0; i < 4; ++i) o[4 * g + j][nt][i] += t[i];
             }
@@ -479,13 +525,22 @@ struct CodesEngine {
     }
   }
 
-  // A larger scale than before: products are kept divided by its power of two, until one is 64 times as large.
-  __device__ __forceinline__ void widen(float top) {
-    const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(fmaxf(top, 0.f)));
+  // Products are kept divided by the power of two of the first scale, until one is 64 times as large. (A negative
+  // scale, or one that is infinite or NaN, comes here too, and changes nothing by itself.)
+  __device__ __forceinline__ void widen(const uint32_t* m0, const uint32_t* m1, bool see0, bool see1) {
+    float top = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const float s0 = fabsf(scale_of(m0[g])), s1 = fabsf(scale_of(m1[g]));
+      if (see0 && s0 < INFINITY) top = fmaxf(top, s0);
+      if (see1 && s1 < INFINITY) top = fmaxf(top, s1);
+    }
+    const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(top));
+    if (most < v_limit || !__any_sync(~0u, see0 || see1)) return;
     const int e = max(static_cast<int>(most >> 23) - 127, -100);
     const float inv = exp2f(static_cast<float>(-e)), f = inv / v_inv;
     v_inv = inv;
-    v_most = exp2f(static_cast<float>(min(e + 6, 127)));
+    v_limit = __float_as_uint(exp2f(static_cast<float>(min(e + 6, 127))));
 #pragma unroll
     for (int t = 0; t < 4 * G; ++t)
 #pragma unroll
@@ -514,42 +569,51 @@ struct CodesEngine {
     const int rows = c.rows;
     const float unit = kHalf ? 1.f / v_inv : 1.f;
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) bias[g][nt][e] = over_tokens(bias[g][nt][e]);
+    // a thread's columns of a group: 8 r .. 8 r + 7, in two quads
+#pragma unroll
+    for (int col0 = 0; col0 < 64 * G; col0 += kMergeCols) {
+      const int g = col0 / 64;
 #pragma unroll
       for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float b = over_tokens(bias[g][nt][e]);
-          float* at = buf + (warp * kRows + 8 * nt + 2 * cc + e) * 64;
+          const float b = bias[g][nt][e];
+          float* at = buf + (warp * kRows + 8 * nt + 2 * cc + e) * kMergeCols;
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float4*>(at + ((8 * r + 4 * h) ^ (cc << 3))) =
-                make_float4(fmaf(o[4 * g][nt][2 * h + e], unit, b), fmaf(o[4 * g + 1][nt][2 * h + e], unit, b),
-                            fmaf(o[4 * g + 2][nt][2 * h + e], unit, b), fmaf(o[4 * g + 3][nt][2 * h + e], unit, b));
+            if (kMergeCols == 64 || (r >> 2) == (col0 & 32) / 32)
+              *reinterpret_cast<float4*>(at + (((8 * r + 4 * h) & (kMergeCols - 1)) ^ (cc << 3))) =
+                  make_float4(fmaf(o[4 * g][nt][2 * h + e], unit, b), fmaf(o[4 * g + 1][nt][2 * h + e], unit, b),
+                              fmaf(o[4 * g + 2][nt][2 * h + e], unit, b), fmaf(o[4 * g + 3][nt][2 * h + e], unit, b));
         }
-      sync_compute<kW>();
-      for (int e = threadIdx.x; e < rows * 16; e += 32 * kW) {
-        const int row = e >> 4, col = (e & 15) * 4;
+      sync_compute();
+      for (int e = threadIdx.x; e < rows * (kMergeCols / 4); e += kCompute) {
+        const int row = e / (kMergeCols / 4), col = e % (kMergeCols / 4) * 4;
         float M = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < kW; ++k) M = fmaxf(M, ml[k * kRows + row].x);
+        for (int k = 0; k < kWarps; ++k) M = fmaxf(M, ml[k * kRows + row].x);
         const float Mu = M == -INFINITY ? 0.f : M;
         float L = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < kW; ++k) {
+        for (int k = 0; k < kWarps; ++k) {
           const float2 t = ml[k * kRows + row];
           const float f = ex2(t.x - Mu);
           L += f * t.y;
-          const float4 u = *reinterpret_cast<const float4*>(buf + (k * kRows + row) * 64 + (col ^ (((row >> 1) & 3) << 3)));
+          const float4 u = *reinterpret_cast<const float4*>(buf + (k * kRows + row) * kMergeCols + (col ^ (((row >> 1) & 3) << 3)));
           v.x += f * u.x;
           v.y += f * u.y;
           v.z += f * u.z;
           v.w += f * u.w;
         }
-        store(row, 64 * g + col, v, M, L);
+        store(row, col0 + col, v, M, L);
       }
-      sync_compute<kW>();
+      sync_compute();
     }
   }
 };

@@ -15,12 +15,12 @@ cudaError_t chunks(const AttnArgs& a, cudaStream_t st) {
 template <class T>
 cudaError_t prefill_of(const AttnArgs& a, cudaStream_t st) {
   if constexpr (sizeof(T) == 4) {
-    if (a.D == 64) return chunks<CodesEngine<T, 1, 2, 256, 8>>(a, st);
-    if (a.D == 128) return chunks<CodesEngine<T, 2, 2, 256, 8>>(a, st);
+    if (a.D == 64) return chunks<CodesEngine<T, 1, 2, 2>>(a, st);
+    if (a.D == 128) return chunks<CodesEngine<T, 2, 2, 2>>(a, st);
   }
   switch (a.D / 64) {
-    case 3: return chunks<CodesEngine<T, 3, 2, 128, 8>>(a, st);
-    default: return chunks<CodesEngine<T, 4, 2, 128, 8>>(a, st);
+    case 3: return chunks<CodesEngine<T, 3, 2, 1>>(a, st);
+    default: return chunks<CodesEngine<T, 4, 2, 1>>(a, st);
   }
 }
 

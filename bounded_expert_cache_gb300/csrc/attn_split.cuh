@@ -17,14 +17,12 @@ namespace {
 
 using namespace tc;
 
-constexpr int kWarps = 8;  // computing warps of the engines of values (E::kW); the first warp of a further warpgroup copies
+constexpr int kWarps = 8;  // computing warps; the first warp of a third warpgroup copies
 constexpr int kCompute = 32 * kWarps;
+constexpr int kThreads = kCompute + 128;
 
 // barrier of the computing warps
-template <int W = kWarps>
-__device__ __forceinline__ void sync_compute() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");
-}
+__device__ __forceinline__ void sync_compute() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
   tma4d(dst, m, bar, x, y, 0, z);
 }
@@ -74,6 +72,14 @@ struct Cursor {
   __device__ __forceinline__ int token(const AttnArgs& a, int r) const { return tok0 + (hq0 + r) / a.g; }
   __device__ __forceinline__ int head(const AttnArgs& a, int r) const { return h * a.g + (hq0 + r) % a.g; }
 };
+
+// Tiles from the cursor's on that go together: neighbours, of this run.
+template <int GROUP>
+__device__ __forceinline__ int group_of(const Cursor& c) {
+  if (GROUP == 1) return 1;
+  const int n = min(GROUP, c.t1 - c.t);
+  return c.t < c.sp.n0 ? min(n, c.sp.n0 - c.t) : n;
+}
 
 template <int KT>
 __device__ __forceinline__ void open_seq(const AttnArgs& a, Cursor& c) {
@@ -138,7 +144,6 @@ __device__ __forceinline__ void write_out(const AttnArgs& a, const Cursor& c, in
 
 // Block-wide inclusive scan of one int64 per thread; returns the thread's
 // exclusive prefix and the total.
-template <int THREADS>
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t x = v;
@@ -151,7 +156,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t* 
   __syncthreads();
   int64_t base = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) base += tmp[w];
     all += tmp[w];
   }
@@ -160,24 +165,24 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t* 
   return base + x - v;
 }
 
-// The ring takes what the merge buffer leaves of 220 KB, at most E::kMostSlots tiles.
+// The ring takes what the merge buffer leaves of 220 KB (224 of codes), at most E::kMostSlots slots.
 template <class E>
 struct Ring {
-  static constexpr int kFit = (220 * 1024 - E::kMergeBytes) / static_cast<int>(E::kTileBytes);
+  // a slot is a tile of K or of V; of codes, which are few bytes, up to E::kGroup of both
+  static constexpr int kSlot = static_cast<int>(E::kTileBytes) * (E::kCodes ? 2 * E::kGroup : 1);
+  static constexpr int kFit = ((E::kCodes ? 224 : 220) * 1024 - E::kMergeBytes) / kSlot;
   static constexpr int kSlots = kFit > E::kMostSlots ? E::kMostSlots : kFit;
-  static constexpr int kSmem = kSlots * static_cast<int>(E::kTileBytes) + E::kMergeBytes;
+  static constexpr int kSmem = kSlots * kSlot + E::kMergeBytes;
 };
 
 // SPLIT: runs of the line of tiles (decode). Otherwise one unit a CTA (chunks).
-template <class E>
-constexpr int kThreadsOf = 32 * E::kW + 128;
 template <class E, bool SPLIT>
-__global__ void __launch_bounds__(kThreadsOf<E>, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, AttnArgs a,
                 int boxes) {
   constexpr int NS = Ring<E>::kSlots;
-  static_assert(NS >= 3, "ring");
-  constexpr int KT = E::KT, R = E::kRows, W = E::kW, kThreads = kThreadsOf<E>;
+  static_assert(NS >= (E::kCodes ? 2 : 3), "ring");
+  constexpr int KT = E::KT, R = E::kRows;
   extern __shared__ __align__(1024) unsigned char sm[];
   __shared__ uint64_t b_full[NS], b_empty[NS];
   __shared__ int64_t s_scan[kThreads / 32];
@@ -195,7 +200,8 @@ __global__ void __launch_bounds__(kThreadsOf<E>, 1)
   } else if (blockIdx.x == 0 && threadIdx.x == kThreads - 1) {
     check_chunks(a);
   }
-  float* merge = reinterpret_cast<float*>(sm + NS * E::kTileBytes);
+  constexpr uint32_t kSlotBytes = Ring<E>::kSlot;
+  float* merge = reinterpret_cast<float*>(sm + NS * kSlotBytes);
   const int rt_n = a.row_tiles;
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -204,7 +210,7 @@ __global__ void __launch_bounds__(kThreadsOf<E>, 1)
     s_found[0] = -1;
     for (int i = 0; i < NS; ++i) {
       mbar_init(su32(&b_full[i]), 1);
-      mbar_init(su32(&b_empty[i]), W);
+      mbar_init(su32(&b_empty[i]), kWarps);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -224,7 +230,7 @@ __global__ void __launch_bounds__(kThreadsOf<E>, 1)
     for (int b0 = 0; b0 < a.n; b0 += kThreads) {
       mine = line_of(b0 + threadIdx.x);
       int64_t t;
-      ex = block_scan<kThreads>(mine, s_scan, &t);
+      ex = block_scan(mine, s_scan, &t);
       all += t;
     }
     total = all;
@@ -236,7 +242,7 @@ __global__ void __launch_bounds__(kThreadsOf<E>, 1)
       int64_t t = total;
       if (a.n > kThreads) {
         mine = line_of(b0 + threadIdx.x);
-        ex = base + block_scan<kThreads>(mine, s_scan, &t);
+        ex = base + block_scan(mine, s_scan, &t);
       }
       if (run0 >= ex && run0 < ex + mine) {
         s_found[0] = b0 + threadIdx.x;
@@ -264,7 +270,7 @@ __global__ void __launch_bounds__(kThreadsOf<E>, 1)
       int64_t mine = 0, t;
       if (b0 + static_cast<int>(threadIdx.x) < a.n)
         mine = (static_cast<int64_t>(chunk_rows(a, b0 + threadIdx.x)) * a.g + R - 1) / R;
-      const int64_t ex = base + block_scan<kThreads>(mine, s_scan, &t);
+      const int64_t ex = base + block_scan(mine, s_scan, &t);
       if (want >= ex && want < ex + mine) {
         s_found[0] = b0 + threadIdx.x;
         s_found[1] = want - ex;
@@ -285,60 +291,75 @@ __global__ void __launch_bounds__(kThreadsOf<E>, 1)
   const int shift = min(a.page_shift, 31 - __clz(KT));  // log2 of a box's tokens
 
   // Registers: the block is launched with 384 x 168; the computing warpgroups
-  // take 216 a thread, the third keeps 72 (256 x 216 + 128 x 72 = 384 x 168). With
-  // sixteen computing warps: 640 x 96 become 512 x 112 and 128 x 32.
-  static_assert(W == 8 || W == 16, "registers");
-  if (warp >= W) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W == 8 ? 72 : 32));
-    if (warp > W) return;
+  // take 216 a thread, the third keeps 72 (256 x 216 + 128 x 72 = 384 x 168).
+  if (warp >= kWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp > kWarps) return;
     // ---------------- copies: lane i brings page i of the tile; pages that no
     // row sees are left out
-    const int per = KT >> shift;
     RingPos rp;
-    uint32_t n = 0;  // tiles issued
+    uint32_t n = 0, done = 0;  // slots filled, tiles of K and V in them
     const uint32_t most = a.copies;
     bool ok = true;
-    while (ok && n < most) {
-      const int tok = cp.sp.tile(cp.t) * KT + (lane << shift);
-      bool need = lane < per && tok < cp.sp.end && (tok < a.sinks || tok + (1 << shift) > cp.sp.low);
-      int page = 0;
-      if (need) {
-        page = __ldg(a.table + static_cast<int64_t>(cp.s.id) * a.max_pages + (tok >> a.page_shift));
-        if (page < 0 || page >= a.n_pages) {
-          atomicOr(a.err, MOE_DEVERR_BADIDX);
-          need = false;
-        }
-      }
+    while (ok && done < most) {
+      // a lane's pages: every 32nd of the tiles'
+      constexpr int kEach = (E::kGroup * KT / 16 + 31) / 32;
+      const int tiles = group_of<E::kGroup>(cp);
       const uint32_t box_bytes = (E::kTileBytes / KT) << shift;
-      const uint32_t bytes = __popc(__ballot_sync(~0u, need)) * box_bytes;
-      const int y = tok & ((1 << a.page_shift) - 1), z = page * a.Hkv + cp.h;
+      int page[kEach], y[kEach];  // -1: none
+      uint32_t bytes = 0;
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
+      for (int x = 0; x < kEach; ++x) {
+        const int box = lane + 32 * x, tok = cp.sp.tile(cp.t) * KT + (box << shift);
+        y[x] = tok & ((1 << a.page_shift) - 1);
+        page[x] = -1;
+        if (box < (tiles * KT) >> shift && tok < cp.sp.end && (tok < a.sinks || tok + (1 << shift) > cp.sp.low)) {
+          page[x] = __ldg(a.table + static_cast<int64_t>(cp.s.id) * a.max_pages + (tok >> a.page_shift));
+          if (page[x] < 0 || page[x] >= a.n_pages) {
+            atomicOr(a.err, MOE_DEVERR_BADIDX);
+            page[x] = -1;
+          }
+        }
+        bytes += __popc(__ballot_sync(~0u, page[x] >= 0)) * box_bytes;
+      }
+#pragma unroll
+      for (int kv = 0; kv < (E::kCodes ? 1 : 2); ++kv) {
         const uint32_t full = su32(&b_full[rp.s]);
         if (n >= NS && !mbar_wait(su32(&b_empty[rp.s]), rp.ph ^ 1u, &s_abort, a.err, a.wait_cycles)) ok = false;
         ok = __all_sync(~0u, ok);
         if (!ok) break;
-        if (lane == 0) mbar_expect_tx(full, bytes);  // without pages the barrier completes by this arrival
+        if (lane == 0) mbar_expect_tx(full, E::kCodes ? 2 * bytes : bytes);  // without pages the barrier completes by this arrival
         __syncwarp();
-        if (need && E::kCodes) {
-          // a head's codes of a page, and behind them its scales and offsets
-          constexpr uint32_t kCode = E::kRowBytes, kMeta = E::kTileBytes / KT - kCode;
-          const char* src = static_cast<const char*>(kv ? a.v : a.k) + ((static_cast<int64_t>(z) * (kCode + kMeta)) << a.page_shift);
-          const uint32_t dst = ring + rp.s * E::kTileBytes;
-          bulk_copy(dst + ((lane * kCode) << shift), src + y * kCode, kCode << shift, full);
-          bulk_copy(dst + KT * kCode + ((lane * kMeta) << shift), src + (static_cast<int64_t>(kCode) << a.page_shift) + y * kMeta,
-                    kMeta << shift, full);
-        } else if (need) {
-          const uint32_t dst = ring + rp.s * E::kTileBytes + lane * box_bytes;
-          for (int x = 0; x < boxes; ++x)
-            tma_page(dst + x * (128u << shift), kv ? &map_v : &map_k, full, x * (128 / static_cast<int>(sizeof(typename E::T))),
-                     y, z);
+#pragma unroll
+        for (int b = 0; b < kEach; ++b) {
+          if (page[b] < 0) continue;
+          const int box = lane + 32 * b, z = page[b] * a.Hkv + cp.h;
+          if constexpr (E::kCodes) {
+            // a head's codes of a page, and behind them its scales and offsets
+            constexpr uint32_t kCode = E::kRowBytes, kMeta = E::kTileBytes / KT - kCode;
+            const int64_t block = (static_cast<int64_t>(z) * (kCode + kMeta)) << a.page_shift;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const char* src = static_cast<const char*>(x ? a.v : a.k) + block;
+              const uint32_t dst = ring + rp.s * kSlotBytes + x * (kSlotBytes / 2);
+              bulk_copy(dst + ((box * kCode) << shift), src + y[b] * kCode, kCode << shift, full);
+              bulk_copy(dst + E::kGroup * KT * kCode + ((box * kMeta) << shift),
+                        src + (static_cast<int64_t>(kCode) << a.page_shift) + y[b] * kMeta, kMeta << shift, full);
+            }
+          } else {
+            const uint32_t dst = ring + rp.s * kSlotBytes + box * box_bytes;
+            for (int x = 0; x < boxes; ++x)
+              tma_page(dst + x * (128u << shift), kv ? &map_v : &map_k, full, x * (128 / static_cast<int>(sizeof(typename E::T))),
+                       y[b], z);
+          }
         }
         __syncwarp();
         ++n;
         rp.next(NS);
       }
-      if (++cp.t < cp.t1) continue;
+      done += E::kCodes ? tiles : 2;
+      cp.t += tiles;
+      if (cp.t < cp.t1) continue;
       if (!cp.more()) break;
       next_unit<KT, R>(a, cp);
     }
@@ -350,7 +371,7 @@ __global__ void __launch_bounds__(kThreadsOf<E>, 1)
   }
 
   // ---------------- computing warps
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(W == 8 ? 216 : 112));
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
   E eng;
   eng.place(merge);
   RingPos rp;
@@ -358,7 +379,7 @@ __global__ void __launch_bounds__(kThreadsOf<E>, 1)
   tile.shift = shift;
   auto wait_tile = [&]() {
     mbar_wait(su32(&b_full[rp.s]), rp.ph, &s_abort, a.err, a.wait_cycles);
-    tile.base = ring + rp.s * E::kTileBytes;
+    tile.base = ring + rp.s * kSlotBytes;
   };
   auto free_tile = [&]() {
     __syncwarp();
@@ -368,13 +389,22 @@ __global__ void __launch_bounds__(kThreadsOf<E>, 1)
   while (true) {
     // ---- one unit's share of the run
     eng.begin(a, cp);
-    for (; cp.t < cp.t1; ++cp.t) {
-      wait_tile();
-      eng.scores(a, cp, tile);
-      free_tile();
-      wait_tile();
-      eng.values(a, cp, tile);
-      free_tile();
+    if constexpr (E::kCodes) {
+      for (int tiles; cp.t < cp.t1; cp.t += tiles) {
+        tiles = group_of<E::kGroup>(cp);
+        wait_tile();
+        eng.tiles(a, cp, tile.base, tiles);
+        free_tile();
+      }
+    } else {
+      for (; cp.t < cp.t1; ++cp.t) {
+        wait_tile();
+        eng.scores(a, cp, tile);
+        free_tile();
+        wait_tile();
+        eng.values(a, cp, tile);
+        free_tile();
+      }
     }
     if (cp.t1 - cp.t0 == cp.per) {
       eng.end(a, cp, merge, s_ml, [&](int r, int col, float4 v, float, float L) {
@@ -493,7 +523,7 @@ cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
   constexpr int smem = Ring<E>::kSmem;
   e = cudaFuncSetAttribute(attn_kernel<E, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attn_kernel<E, SPLIT><<<grid, kThreadsOf<E>, smem, st>>>(mk, mv, a, boxes);
+  attn_kernel<E, SPLIT><<<grid, kThreads, smem, st>>>(mk, mv, a, boxes);
   return cudaGetLastError();
 }
 
