@@ -15,15 +15,25 @@
 // takes 2^-a from a table and the rest from its power series.
 //
 // One cluster of CTAs a row. Each holds a slice of the row in shared memory, so the
-// logits are read once. The end of the prefix is found by histograms (tokens, weight)
-// over 1,024 bins: first of d; then, within the bin that holds the end, of the place
-// in the order, (logit, index) as one number, ten bits a round, until the end is
-// decided: mostly one round. Bins that cannot hold it are left out: with top-k those
-// behind the k-th largest of the threads' own maxima; with top-p tokens of less than
-// (1 - top_p) / V of the weight, which all together are no more than what is cut off.
+// logits are read once. With neither top-k nor top-p two passes follow: the weights'
+// sums of every warp's tokens, and the one warp's in which the token is. Else the end of
+// the prefix is looked for first:
+// - Bins of d, 1,024 of them, bound it. With top-k, by the threads' own largest logits:
+//   the k-th largest of them is no larger than the k-th of all. With top-p, by a
+//   histogram (tokens, weight) over the bins; tokens of less than (1 - top_p) / V of the
+//   weight, which all together are no more than what is cut off, are left out of it.
+// - If that leaves few tokens, as it mostly does, they go to the first CTA, and the
+//   others are done.
+// - Histograms follow, over the bins and then, within the bin that holds the end, over
+//   the place in the order, (logit, index) as one number, ten bits a round, until the
+//   end is decided: mostly one round. The first CTA does that by itself, if the bin's
+//   tokens fit into its list.
 //
-// What bounds it: few rows the passes' and cluster barriers' latency; many the issue
-// of the weights' arithmetic (some 40 instructions a token where all weights count).
+// What bounds it: few rows the latency of the passes and cluster barriers; many the
+// issue of the weights' arithmetic (some 40 instructions a token where all weights count;
+// two fp32 an instruction did not make it shorter). 131,072 fp32 logits: 20.8 us a row
+// with top-k and top-p, 36 with top-p alone; 64 such rows 37 us with neither, 48 with
+// top-k, 75 with settings of all kinds, 95 with top-p alone. Their reading takes 5.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -37,7 +47,7 @@ namespace moe {
 namespace {
 
 constexpr int kSampleThreads = 512, kSampleWarps = kSampleThreads / 32;
-constexpr int kBins = 1024, kMostCtas = 8;
+constexpr int kBins = 1024, kMostCtas = 16, kList = 2048;
 constexpr int kFraction = 43;  // weights are whole numbers of 2^-43
 constexpr float kReach = 44.f;  // weights from here on are none
 constexpr float kBinsPer = kBins / kReach;
@@ -47,8 +57,12 @@ constexpr int kIndexBits = 20;
 struct PowerTable {
   uint32_t p[257];
 };
+struct Power {  // the same, and as fp32
+  uint32_t whole;
+  float rounded;
+};
 
-struct Hist {
+struct alignas(16) Hist {
   uint32_t count[kBins];
   unsigned long long weight[kBins];
 };
@@ -61,20 +75,23 @@ struct Search {
   unsigned int n_before, bin_n;           // and their number
   int done;              // 1: the end is decided: bin and hi; 2: there is none, all are kept
   unsigned long long sum;     // then: the weight kept
-  unsigned int kept;          // and the number
+  unsigned int kept;          // and the number; before: of tokens up to and with the bin
 };
 struct SampleShared {
   Hist first, next;
-  uint32_t maxima[kBins];
+  alignas(16) uint32_t maxima[kBins];
+  unsigned long long list[kList];
   unsigned long long chunk[kMostCtas * kSampleWarps];
-  unsigned long long best[kMostCtas], sum[kMostCtas];
+  unsigned long long sum[kMostCtas];
   unsigned long long warp64[kSampleWarps];
   unsigned int warp32[kSampleWarps];
   unsigned long long found64;
+  uint32_t top[kMostCtas];
   int found;
+  unsigned int listed[4], index;  // tokens listed by each gathering
   Search search;
   float c_hi, c_lo;
-  uint32_t power[257];
+  Power power[257];
 };
 
 __device__ __forceinline__ uint32_t order_key(float z) {
@@ -84,41 +101,51 @@ __device__ __forceinline__ uint32_t order_key(float z) {
 __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 // place in the order: falling logits, ties by index
 __device__ __forceinline__ unsigned long long place(float z, int i) {
-  return static_cast<unsigned long long>(~order_key(z)) << kIndexBits | static_cast<unsigned int>(i);
+  return static_cast<unsigned long long>(~order_key(z + 0.f)) << kIndexBits | static_cast<unsigned int>(i);  // (-0 is 0)
 }
+__device__ __forceinline__ float logit_of(unsigned long long place) { return of_key(~static_cast<uint32_t>(place >> kIndexBits)); }
 
 // Differences of logits are halved, which loses nothing and does not overflow; c is 2 log2(e) / T.
 struct Row {
   float top, half, c_hi, c_lo;
-  const uint32_t* power;
+  const Power* power;
   // bin of d; kBins: no weight. Does not fall as z falls.
   __device__ __forceinline__ int bin(float z) const {
     if (z == top) return 0;
     const float d = fmaf(z, -0.5f, half) * c_hi;
     return d < kReach ? min(static_cast<int>(d * kBinsPer), kBins - 1) : kBins;
   }
-  // weight of a token with bin(z) < kBins
+  // weight of a token
   __device__ __forceinline__ unsigned long long weight(float z) const {
     if (z == top) return 1ull << kFraction;
     // (top - z) / 2, and the rest of its rounding
     const float y = 0.5f * z, d0 = half - y, yy = half - d0, rest = (half - (d0 + yy)) + (yy - y);
     const float p = d0 * c_hi;
+    if (!(p < kReach)) return 0ull;
     const float e = fmaf(d0, c_hi, -p) + (d0 * c_lo + rest * c_hi);
     constexpr float kWhole = 12582912.f;        // 1.5 * 2^23: adding it rounds to a whole number
     constexpr float kPart = 49152.f;            // 1.5 * 2^15: to a multiple of 2^-8
     const float n = p + kWhole, f = p - (n - kWhole);
     const float a = f + kPart, r = (f - (a - kPart)) + e;
-    const uint32_t t = power[__float_as_int(a) - 0x47400000 + 128];  // (0x47400000: kPart)
+    const Power t = power[__float_as_int(a) - 0x47400000 + 128];  // (0x47400000: kPart)
     constexpr float kLn2 = 0.693147181f;
     const float x = r * -kLn2;  // 2^-r = e^x, |x| < 2^-9
     const float q = x * fmaf(x, fmaf(x, 1.f / 6.f, 0.5f), 1.f);
-    const float add = static_cast<float>(t) * q + kWhole;  // below 2^22
-    const uint32_t w = t + (__float_as_uint(add) - 0x4B400000u);
+    const float add = t.rounded * q + kWhole;  // below 2^22
+    const uint32_t w = t.whole + (__float_as_uint(add) - 0x4B400000u);
     const int by = __float_as_int(n) - 0x4B400000;
     return (static_cast<unsigned long long>(w) << (kFraction - 31)) >> by;
   }
 };
 
+// Adds to 64 bits in shared memory by 32-bit atomics, which are native there; the sum
+// of several is whole when all are done.
+__device__ __forceinline__ void add_shared(unsigned long long* at, unsigned long long w) {
+  uint32_t* half = reinterpret_cast<uint32_t*>(at);
+  const uint32_t low = static_cast<uint32_t>(w), old = atomicAdd(half, low);
+  const uint32_t high = static_cast<uint32_t>(w >> 32) + (old + low < old);
+  if (high) atomicAdd(half + 1, high);
+}
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 #pragma unroll
   for (int x = 16; x; x >>= 1) v += __shfl_xor_sync(~0u, v, x);
@@ -135,10 +162,11 @@ __device__ __forceinline__ T block_scan_incl(T v, T* tmp) {
   }
   if (lane == 31) tmp[warp] = v;
   __syncthreads();
-  T below = 0;
-  for (int w = 0; w < warp; ++w) below += tmp[w];
+  T below = lane < warp ? tmp[lane & (kSampleWarps - 1)] : static_cast<T>(0);
+#pragma unroll
+  for (int d = kSampleWarps / 2; d; d >>= 1) below += __shfl_xor_sync(~0u, below, d);
   __syncthreads();
-  return v + below;
+  return v + __shfl_sync(~0u, below, 0);
 }
 
 struct SampleArgs {
@@ -153,10 +181,10 @@ struct SampleArgs {
   int staged;  // of them in shared memory
 };
 
-__device__ __forceinline__ float clean(float z) { return z != z ? -INFINITY : z + 0.f; }  // NaN: never; -0 is 0
+// (NaN stays, and is none of the largest, of the bins or of the weights)
 template <class T>
-__device__ __forceinline__ float logit(const SampleArgs& a, int row, int i) {
-  return clean(static_cast<float>(__ldg(static_cast<const T*>(a.z) + row * a.ld + i)));
+__device__ __forceinline__ T raw_logit(const SampleArgs& a, int row, int i) {
+  return __ldg(static_cast<const T*>(a.z) + row * a.ld + i);
 }
 
 // u times s, rounded down; u in [0, 1)
@@ -166,11 +194,11 @@ __device__ __forceinline__ unsigned long long share_of(float u, unsigned long lo
 }
 
 template <class T>
-__global__ void __launch_bounds__(kSampleThreads)
+__global__ void __launch_bounds__(kSampleThreads, 2)
     sample_kernel(const __grid_constant__ SampleArgs a, const __grid_constant__ PowerTable table) {
   extern __shared__ __align__(16) unsigned char sm_raw[];
   SampleShared& sh = *reinterpret_cast<SampleShared*>(sm_raw);
-  float* const held = reinterpret_cast<float*>(sm_raw + sizeof(SampleShared));
+  T* const held = reinterpret_cast<T*>(sm_raw + sizeof(SampleShared));
   auto cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int row = blockIdx.x / C;
@@ -184,69 +212,100 @@ __global__ void __launch_bounds__(kSampleThreads)
   const float min_p = a.by.min_ps ? a.by.min_ps[row] : a.by.min_p;
   const float u = a.u[row];
   const bool k_on = top_k > 0 && top_k < a.V, p_on = top_p < 1.f;
+  const bool first_wins = !(temperature > 0.f) || top_k == 1;
 
-  for (int i = tid; i < kBins; i += kSampleThreads) {
-    sh.first.count[i] = sh.next.count[i] = sh.maxima[i] = 0u;
-    sh.first.weight[i] = sh.next.weight[i] = 0ull;
-  }
-  for (int i = tid; i < 257; i += kSampleThreads) sh.power[i] = table.p[i];
+  if (k_on || p_on)
+    for (int i = tid; i < kBins; i += kSampleThreads) {
+      sh.first.count[i] = sh.next.count[i] = sh.maxima[i] = 0u;
+      sh.first.weight[i] = sh.next.weight[i] = 0ull;
+    }
+  for (int i = tid; i < 257; i += kSampleThreads) sh.power[i] = Power{table.p[i], static_cast<float>(table.p[i])};
   if (tid == 0) {
     const double c = 2.8853900817779268148 / static_cast<double>(temperature);
     sh.c_hi = static_cast<float>(c);
     sh.c_lo = isfinite(sh.c_hi) ? static_cast<float>(c - static_cast<double>(sh.c_hi)) : 0.f;
+    for (int i = 0; i < 4; ++i) sh.listed[i] = 0u;
+    sh.index = ~0u;
   }
 
-  // ---- the slice, and the first in the order
+  // ---- the slice, and the largest logit
   float mine = -INFINITY;
-  int mine_i = 0;
-#pragma unroll 8
-  for (int j = lane; j < n_mine; j += 32) {
-    const int i = slice0 + w0 + j;
-    const float z = logit<T>(a, row, i);
-    if (w0 + j < a.staged) held[w0 + j] = z;
-    if (z > mine) {
-      mine = z;
-      mine_i = i;
-    }
-  }
   {
-    unsigned long long b = place(mine, mine == -INFINITY ? (1 << kIndexBits) - 1 : mine_i);
+    int j = lane;
+    for (; j + 7 * 32 < n_mine; j += 8 * 32) {  // eight loads in flight
+      T z[8];
 #pragma unroll
-    for (int x = 16; x; x >>= 1) b = min(b, __shfl_xor_sync(~0u, b, x));
-    if (lane == 0) sh.warp64[warp] = b;
+      for (int x = 0; x < 8; ++x) z[x] = raw_logit<T>(a, row, slice0 + w0 + j + 32 * x);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        if (w0 + j + 32 * x < a.staged) held[w0 + j + 32 * x] = z[x];
+        mine = fmaxf(mine, static_cast<float>(z[x]));
+      }
+    }
+    for (; j < n_mine; j += 32) {
+      const T z = raw_logit<T>(a, row, slice0 + w0 + j);
+      if (w0 + j < a.staged) held[w0 + j] = z;
+      mine = fmaxf(mine, static_cast<float>(z));
+    }
+    uint32_t k = __reduce_max_sync(~0u, order_key(mine));
+    if (lane == 0) sh.warp32[warp] = k;
     __syncthreads();
     if (warp == 0) {
-      b = sh.warp64[lane & (kSampleWarps - 1)];
-#pragma unroll
-      for (int x = 8; x; x >>= 1) b = min(b, __shfl_xor_sync(~0u, b, x));
-      if (lane < C) *cluster.map_shared_rank(&sh.best[rank], lane) = b;
+      k = __reduce_max_sync(~0u, lane < kSampleWarps ? sh.warp32[lane] : 0u);
+      if (lane < C) *cluster.map_shared_rank(&sh.top[rank], lane) = k;
     }
   }
   cluster.sync();
-  unsigned long long best = sh.best[0];
-  for (int i = 1; i < C; ++i) best = min(best, sh.best[i]);
+  uint32_t top_key = sh.top[0];
+  for (int i = 1; i < C; ++i) top_key = max(top_key, sh.top[i]);
   Row r;
-  r.top = of_key(~static_cast<uint32_t>(best >> kIndexBits));
+  r.top = of_key(top_key) + 0.f;
   r.half = 0.5f * r.top;
   r.c_hi = sh.c_hi;
   r.c_lo = sh.c_lo;
   r.power = sh.power;
-  // nothing to choose from, or nothing to choose
-  if (r.top == -INFINITY || !(temperature > 0.f) || top_k == 1) {
+  if (r.top == -INFINITY) {  // nothing to choose from
     if (rank == 0 && tid == 0) {
-      const bool none = r.top == -INFINITY;
-      a.token[row] = none ? -1 : static_cast<int32_t>(best & ((1u << kIndexBits) - 1));
-      if (a.prob) a.prob[row] = none ? 0.f : 1.f;
+      a.token[row] = -1;
+      if (a.prob) a.prob[row] = 0.f;
     }
     return;  // (every CTA's stores to the others were before the barrier)
   }
-  auto each = [&](auto&& f) {  // f(logit, index) of this warp's tokens, a lane every 32nd
+  bool solo = false;  // the first CTA alone, with the tokens of its list
+  int lists = 0;      // gatherings so far
+  // f(logit, index) of this warp's tokens, a lane every 32nd
+  auto each = [&](auto&& f) {
+    if (solo) {
+      for (unsigned int j = tid; j < sh.listed[lists - 1]; j += kSampleThreads) f(logit_of(sh.list[j]), static_cast<int>(sh.list[j] & ((1u << kIndexBits) - 1)));
+      return;
+    }
 #pragma unroll 4
     for (int j = lane; j < n_mine; j += 32) {
       const int i = slice0 + w0 + j;
-      f(w0 + j < a.staged ? held[w0 + j] : logit<T>(a, row, i), i);
+      f(static_cast<float>(w0 + j < a.staged ? held[w0 + j] : raw_logit<T>(a, row, i)), i);
     }
   };
+  SampleShared& lead = *cluster.map_shared_rank(&sh, 0);
+  auto sync = [&]() {
+    if (solo)
+      __syncthreads();
+    else
+      cluster.sync();
+  };
+  if (first_wins) {  // nothing to choose: the first of the largest
+    unsigned int at = ~0u;
+    each([&](float z, int i) {
+      if (z == r.top) at = min(at, static_cast<unsigned int>(i));
+    });
+    at = __reduce_min_sync(~0u, at);
+    if (lane == 0 && at != ~0u) atomicMin(&lead.index, at);
+    cluster.sync();
+    if (rank == 0 && tid == 0) {
+      a.token[row] = static_cast<int32_t>(sh.index);
+      if (a.prob) a.prob[row] = 1.f;
+    }
+    return;
+  }
   auto share_sum = [&](unsigned long long v) {  // over the cluster
     v = warp_sum(v);
     if (lane == 0) sh.warp64[warp] = v;
@@ -260,9 +319,34 @@ __global__ void __launch_bounds__(kSampleThreads)
     for (int i = 0; i < C; ++i) v += sh.sum[i];
     return v;
   };
-  SampleShared& lead = *cluster.map_shared_rank(&sh, 0);
   auto tell = [&](auto* field, auto v) {  // every CTA, by the first one's first threads
     if (tid < C) *cluster.map_shared_rank(field, tid) = v;
+  };
+  // The tokens of bins low .. most into the first CTA's list. Whether they all fitted.
+  auto gather = [&](int low, int most) -> bool {
+    auto value = [&](int j) {
+      return j < n_mine ? static_cast<float>(w0 + j < a.staged ? held[w0 + j] : raw_logit<T>(a, row, slice0 + w0 + j)) : -INFINITY;
+    };
+    unsigned int n = 0;
+#pragma unroll 4
+    for (int j0 = 0; j0 < n_mine; j0 += 32) {
+      const int b = r.bin(value(j0 + lane));
+      n += __popc(__ballot_sync(~0u, b >= low && b <= most));
+    }
+    unsigned int at = 0;
+    if (n > 0 && lane < C) at = atomicAdd(&cluster.map_shared_rank(&sh, lane)->listed[lists], n);  // (every CTA counts along)
+    at = __shfl_sync(~0u, at, 0);
+    if (n > 0 && at + n <= kList)
+      for (int j0 = 0; j0 < n_mine; j0 += 32) {
+        const float z = value(j0 + lane);
+        const int b = r.bin(z);
+        const bool in = b >= low && b <= most;
+        const unsigned int all = __ballot_sync(~0u, in);
+        if (in) lead.list[at + __popc(all & ((1u << lane) - 1u))] = place(z, slice0 + w0 + j0 + lane);
+        at += __popc(all);
+      }
+    cluster.sync();
+    return sh.listed[lists++] <= kList;
   };
 
   int end_bin = kBins - 1;                   // kept: bin <= end_bin and place <= end
@@ -273,10 +357,15 @@ __global__ void __launch_bounds__(kSampleThreads)
     unsigned long long sum = 0;  // all weight, where top-p needs it
     if (k_on) {
       const int b = mine == -INFINITY ? kBins : r.bin(mine);
-      if (b < kBins) atomicAdd(&lead.maxima[b], 1u);
+      if (b < kBins) atomicAdd(&sh.maxima[b], 1u);
       cluster.sync();
       if (rank == 0) {
-        const uint32_t n0 = sh.maxima[2 * tid], n1 = sh.maxima[2 * tid + 1];
+        uint32_t n0 = 0, n1 = 0;
+        for (int x = 0; x < C; ++x) {
+          const uint2 n = *reinterpret_cast<const uint2*>(&cluster.map_shared_rank(&sh, x)->maxima[2 * tid]);
+          n0 += n.x;
+          n1 += n.y;
+        }
         const uint32_t upto = block_scan_incl(n0 + n1, sh.warp32);
         if (tid == 0) sh.found = kBins - 1;
         __syncthreads();
@@ -289,11 +378,13 @@ __global__ void __launch_bounds__(kSampleThreads)
       }
       cluster.sync();
       most = sh.found;
+      if (gather(0, most)) {
+        if (rank > 0) return;
+        solo = true;
+      }
     } else {
       unsigned long long v = 0;
-      each([&](float z, int) {
-        if (r.bin(z) < kBins) v += r.weight(z);
-      });
+      each([&](float z, int) { v += r.weight(z); });
       sum = share_sum(v);
       const float d = log2f(static_cast<float>(a.V)) + static_cast<float>(kFraction) - log2f((1.f - fmaxf(top_p, 0.f)) * static_cast<float>(sum));
       most = static_cast<int>(fminf(fmaxf(d * kBinsPer, 0.f) + 2.f, kBins - 1.f));
@@ -303,20 +394,28 @@ __global__ void __launch_bounds__(kSampleThreads)
       const int b = r.bin(z);
       if (b <= most) {
         atomicAdd(&sh.first.count[b], 1u);
-        atomicAdd(&sh.first.weight[b], r.weight(z));
+        add_shared(&sh.first.weight[b], r.weight(z));
       }
     });
-    auto merge = [&](Hist& h, Hist& to) {  // into the first CTA's
-      __syncthreads();
-      if (rank > 0)
-        for (int i = tid; i < kBins; i += kSampleThreads)
-          if (h.count[i]) {
-            atomicAdd(&to.count[i], h.count[i]);
-            atomicAdd(&to.weight[i], h.weight[i]);
-          }
-      cluster.sync();
+    // The first CTA reads the others' histograms (adding theirs to its own by atomics
+    // took longer than all the rest: 46 us of one row's top-p); they leave them until
+    // after the next barrier.
+    auto merge = [&](Hist& h) {
+      sync();
+      if (rank == 0 && !solo) {
+        uint2 n = *reinterpret_cast<const uint2*>(&h.count[2 * tid]);
+        ulonglong2 w = *reinterpret_cast<const ulonglong2*>(&h.weight[2 * tid]);
+        for (int x = 1; x < C; ++x) {
+          const Hist& o = *cluster.map_shared_rank(&h, x);
+          const uint2 on = *reinterpret_cast<const uint2*>(&o.count[2 * tid]);
+          const ulonglong2 ow = *reinterpret_cast<const ulonglong2*>(&o.weight[2 * tid]);
+          n.x += on.x, n.y += on.y, w.x += ow.x, w.y += ow.y;
+        }
+        *reinterpret_cast<uint2*>(&h.count[2 * tid]) = n;
+        *reinterpret_cast<ulonglong2*>(&h.weight[2 * tid]) = w;
+      }
     };
-    merge(sh.first, lead.first);
+    merge(sh.first);
     // ---- one search after the other: by number, then by weight
     bool cut_k = false;
 #pragma unroll 1
@@ -324,6 +423,7 @@ __global__ void __launch_bounds__(kSampleThreads)
       if (by_weight ? !p_on : !k_on) continue;
       // round 0 is over bins of d, later ones over places
       unsigned long long goal = 0;  // the end is where the number or weight reaches it
+      bool alone = false;           // the first CTA looks for the end, with the tokens of its bin
 #pragma unroll 1
       for (int round = 0;; ++round) {
         if (rank == 0) {
@@ -392,36 +492,55 @@ __global__ void __launch_bounds__(kSampleThreads)
             q.lo = 0;
             q.hi = ~0ull;
             q.done = 2;
+            q.kept = ~0u;
             sh.search = q;
           }
           if (tid == kSampleThreads - 1) sh.found64 = s;  // all weight (round 0)
           __syncthreads();
           if (sh.search.done == 2 && tid == 0) sh.search.sum = sh.found64;
-          for (int i = tid; i < kBins; i += kSampleThreads) {
-            sh.next.count[i] = 0u;
-            sh.next.weight[i] = 0ull;
-          }
           __syncthreads();
-          const Search q = sh.search;
-          if (tid > 0 && tid < C) *cluster.map_shared_rank(&sh.search, tid) = q;
-        } else {
-          for (int i = tid; i < kBins; i += kSampleThreads) {
-            sh.next.count[i] = 0u;
-            sh.next.weight[i] = 0ull;
+          if (!solo) {
+            const Search q = sh.search;
+            if (tid > 0 && tid < C) *cluster.map_shared_rank(&sh.search, tid) = q;
           }
         }
-        cluster.sync();
+        sync();
         const Search q = sh.search;
+        for (int i = tid; i < kBins; i += kSampleThreads) {
+          sh.next.count[i] = 0u;
+          sh.next.weight[i] = 0ull;
+        }
+        __syncthreads();
+        if (!solo && !k_on && q.kept <= kList) {  // few tokens up to the end's bin
+          if (gather(0, q.bin)) {
+            if (rank > 0) return;
+            solo = true;
+          }
+        }
         if (q.done) break;
+        if (!solo && round == 0 && q.kept - q.n_before <= kList && gather(q.bin, q.bin)) {
+          alone = true;
+          if (rank > 0) break;
+          solo = true;
+        }
         each([&](float z, int i) {
           if (r.bin(z) != q.bin) return;
           const unsigned long long at = place(z, i);
           if (at < q.lo || at > q.hi || (q.bin == end_bin && at > end)) return;
           const int d = static_cast<int>((at - q.lo) >> q.shift);
           atomicAdd(&sh.next.count[d], 1u);
-          atomicAdd(&sh.next.weight[d], r.weight(z));
+          add_shared(&sh.next.weight[d], r.weight(z));
         });
-        merge(sh.next, lead.next);
+        merge(sh.next);
+      }
+      if (alone) {
+        solo = false;
+        if (rank == 0) {
+          __syncthreads();
+          const Search q = sh.search;
+          if (tid > 0 && tid < C) *cluster.map_shared_rank(&sh.search, tid) = q;
+        }
+        cluster.sync();
       }
       const Search q = sh.search;
       if (q.done == 1) {
@@ -430,21 +549,86 @@ __global__ void __launch_bounds__(kSampleThreads)
       }
       cut_k = q.done == 1;
       if (!by_weight) sum = q.sum;
-      cluster.sync();  // the search is read before the next one's is written
+      sync();  // the search is read before the next one's is written
     }
   }
 
-  // ---- weights kept, by the cluster's warps in the order of the vocabulary
+  // ---- weights kept, in the order of the vocabulary
   const unsigned long long least =
       min_p > 0.f ? static_cast<unsigned long long>(ceil(fmin(static_cast<double>(min_p), 1.0) * static_cast<double>(1ull << kFraction))) : 0ull;
+  const bool cut = end != ~0ull;
   auto kept = [&](float z, int i) -> unsigned long long {
-    const int b = r.bin(z);
-    if (b > end_bin || (b == end_bin && place(z, i) > end)) return 0ull;
+    if (cut) {
+      const int b = r.bin(z);
+      if (b > end_bin || (b == end_bin && place(z, i) > end)) return 0ull;
+    }
     const unsigned long long w = r.weight(z);
     return w >= least ? w : 0ull;
   };
+  auto drawn = [&](int i, unsigned long long w, unsigned long long total) {
+    a.token[row] = i;
+    if (a.prob) a.prob[row] = static_cast<float>(static_cast<double>(w) / static_cast<double>(total));
+  };
+  auto goal_of = [&](unsigned long long total) {  // the first sum above it
+    return min(u < 1.f ? share_of(u, total, false) : ~0ull, total - 1);
+  };
+  if (solo) {
+    // by index: 1,024 stretches of the vocabulary, then the tokens of one of them
+    const int shift = max(0, 32 - __clz(a.V - 1) - 10);
+    for (int i = tid; i < kBins; i += kSampleThreads) sh.next.weight[i] = 0ull;
+    __syncthreads();
+    each([&](float z, int i) {
+      const unsigned long long w = kept(z, i);
+      if (w) add_shared(&sh.next.weight[i >> shift], w);
+    });
+    __syncthreads();
+    const unsigned long long s0 = sh.next.weight[2 * tid], s1 = sh.next.weight[2 * tid + 1];
+    const unsigned long long upto = block_scan_incl(s0 + s1, sh.warp64);
+    if (tid == kSampleThreads - 1) sh.found64 = upto;
+    __syncthreads();
+    const unsigned long long total = sh.found64, goal = goal_of(total);
+    __syncthreads();
+    if (goal < upto && goal >= upto - s0 - s1) {
+      const bool second = goal >= upto - s1;
+      sh.found = 2 * tid + second;
+      sh.found64 = goal - (second ? upto - s1 : upto - s0 - s1);
+    }
+    __syncthreads();
+    const int stretch = sh.found;
+    const unsigned long long rest = sh.found64;
+    // of the stretch's tokens, at most 1,024, the one up to which the weights exceed what is left
+    if (tid == 0) sh.index = 0u;
+    __syncthreads();
+    each([&](float z, int i) {
+      if (i >> shift != stretch) return;
+      const unsigned long long w = kept(z, i);
+      if (!w) return;
+      const unsigned int at = atomicAdd(&sh.index, 1u);
+      sh.first.count[at] = static_cast<uint32_t>(i);
+      sh.first.weight[at] = w;
+    });
+    __syncthreads();
+    const unsigned int n = sh.index;
+    for (unsigned int j = tid; j < n; j += kSampleThreads) {
+      const uint32_t i = sh.first.count[j];
+      const unsigned long long w = sh.first.weight[j];
+      unsigned long long before = 0;
+      for (unsigned int o = 0; o < n; ++o)
+        if (sh.first.count[o] < i) before += sh.first.weight[o];
+      if (before <= rest && rest < before + w) drawn(static_cast<int>(i), w, total);
+    }
+    return;
+  }
   unsigned long long v = 0;
-  each([&](float z, int i) { v += kept(z, i); });
+  if (cut)
+    each([&](float z, int i) { v += kept(z, i); });
+  else if (least)
+    each([&](float z, int) {
+      const unsigned long long w = r.weight(z);
+      v += w >= least ? w : 0ull;
+    });
+  else
+    each([&](float z, int) { v += r.weight(z); });
   v = warp_sum(v);
   if (lane < C) *cluster.map_shared_rank(&sh.chunk[rank * kSampleWarps + warp], lane) = v;
   cluster.sync();
@@ -456,7 +640,7 @@ __global__ void __launch_bounds__(kSampleThreads)
   }
   total = warp_sum(total);
   to_cta = warp_sum(to_cta);
-  const unsigned long long goal = min(u < 1.f ? share_of(u, total, false) : ~0ull, total - 1);  // the first sum above it
+  const unsigned long long goal = goal_of(total);
   unsigned long long at = to_cta;  // before chunk c of this CTA
   int c = 0;
   for (; c < kSampleWarps; ++c) {
@@ -471,7 +655,7 @@ __global__ void __launch_bounds__(kSampleThreads)
   auto weight_at = [&](int j) -> unsigned long long {
     const int i = slice0 + j;
     if (j >= p1 || i >= a.V) return 0ull;
-    return kept(j < a.staged ? held[j] : logit<T>(a, row, i), i);
+    return kept(static_cast<float>(j < a.staged ? held[j] : raw_logit<T>(a, row, i)), i);
   };
   v = 0;
   for (int j = p0 + lane; j < p1; j += 32) v += weight_at(j);
@@ -491,10 +675,7 @@ __global__ void __launch_bounds__(kSampleThreads)
     }
     const unsigned int above = __ballot_sync(~0u, at + x > goal);
     if (above) {
-      if (lane == __ffs(above) - 1) {
-        a.token[row] = slice0 + j0 + lane;
-        if (a.prob) a.prob[row] = static_cast<float>(static_cast<double>(w) / static_cast<double>(total));
-      }
+      if (lane == __ffs(above) - 1) drawn(slice0 + j0 + lane, w, total);
       return;
     }
     at += __shfl_sync(~0u, x, 31);
@@ -512,17 +693,21 @@ const PowerTable& powers() {
 
 template <class T>
 cudaError_t sample(SampleArgs a, int rows, int num_sms, cudaStream_t st) {
-  // CTAs a row: slices of 16,384 tokens at most, and smaller ones, down to 2,048,
-  // while there are SMs without a CTA
+  // CTAs a row: slices of 18,432 tokens at most, and smaller ones, down to 2,048,
+  // while there are SMs without a CTA; 16, above the portable size, for a few long rows
+  // alone (a row of 131,072 with top-k and top-p: 20.8 us against 24.9 with 8).
   int ctas = 1;
-  while (ctas < kMostCtas && (a.V > 16384 * ctas || (static_cast<int64_t>(rows) * ctas < num_sms && a.V >= 4096 * ctas))) ctas *= 2;
+  while (ctas < 8 && (a.V > 18432 * ctas || (static_cast<int64_t>(rows) * ctas < num_sms && a.V >= 4096 * ctas))) ctas *= 2;
+  if (ctas == 8 && rows * 32 <= num_sms && a.V >= 32768) ctas = kMostCtas;
   const int each = (a.V + ctas - 1) / ctas;
   a.slice = (each + kSampleThreads - 1) / kSampleThreads * kSampleThreads;
   constexpr int kMostSmem = 227 * 1024;
-  a.staged = std::min(a.slice, (kMostSmem - static_cast<int>(sizeof(SampleShared))) / 4);
-  const int smem = static_cast<int>(sizeof(SampleShared)) + a.staged * 4;
+  constexpr int kBytes = static_cast<int>(sizeof(T));
+  a.staged = std::min(a.slice, (kMostSmem - static_cast<int>(sizeof(SampleShared))) / kBytes);
+  const int smem = static_cast<int>(sizeof(SampleShared)) + a.staged * kBytes;
   cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
   if (e != cudaSuccess) return e;
+  if (ctas > 8 && (e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(rows) * ctas);
   cfg.blockDim = dim3(kSampleThreads);
