@@ -14,9 +14,14 @@
 // infinity, a NaN or a magnitude above 2^126 becomes NaN as a whole.
 //
 // What bounds them: one row the latency of its lookups (chunk, sequence, length,
-// table, page count: five dependent reads) and of one sine; prompts HBM. A row's
-// sines and cosines are formed once and shared by its heads; a thread owns both
-// halves of a pair, so that a result may overwrite its input.
+// table, page count: five dependent reads) and of one sine (rotary 2.3 us in a graph,
+// a write of one token 4.5); prompts HBM. A row's sines and cosines are formed once and
+// shared by its heads; a thread owns both halves of a pair, so that a result may
+// overwrite its input. 16,384 rows of 40 bf16 heads of 128: 59.7 us, 5.6 TB/s. Blocks
+// of 256 threads with 32 registers, eight on an SM: with 40 and the next item read
+// ahead it is 68. 7,591 rows of ragged prompts, 32 + 2 x 8 heads of 128 into 4-bit pages,
+// and these values read back: 64 us, of which q's heads (124 MB) take 18, near HBM's
+// rate; the codes, the values read back and the lookups are bound by instructions.
 #include <cuda_bf16.h>
 
 #include "kv_device.cuh"
@@ -26,48 +31,127 @@ namespace {
 
 constexpr int kRotThreads = 256, kMostRows = 4;
 
+// two fp32 an instruction
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// u c - v s and v c + u s, of values that lie side by side
+template <int N>
+__device__ __forceinline__ void turn(float* u, float* v, const float* c, const float* s) {
+#pragma unroll
+  for (int j = 0; j < N; j += 2) {
+    const F2 a = f2(u[j], u[j + 1]), b = f2(v[j], v[j + 1]), cc = f2(c[j], c[j + 1]), ss = f2(s[j], s[j + 1]);
+    const F2 bs = mul2(b, ss);
+    const float2 x = both(fma2(a, cc, bs ^ 0x8000000080000000ull)), y = both(fma2(b, cc, mul2(a, ss)));
+    u[j] = x.x;
+    u[j + 1] = x.y;
+    v[j] = y.x;
+    v[j + 1] = y.y;
+  }
+}
+
 template <class T>
 struct Vec {
   static constexpr int N = 16 / static_cast<int>(sizeof(T));
 };
-template <class T, int N>
-__device__ __forceinline__ void load(const T* p, float* v) {
+// 16 bytes of values, as they are in memory, and in fp32
+__device__ __forceinline__ uint4 load16(const void* p) { return *static_cast<const uint4*>(p); }
+template <class T>
+__device__ __forceinline__ void widen(uint4 u, float* v) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < N; i += Vec<T>::N) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (sizeof(T) == 4) {
-        v[i + j] = __uint_as_float(w[j]);
-      } else {
-        v[i + 2 * j] = __uint_as_float(w[j] << 16);
-        v[i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      }
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (sizeof(T) == 4) {
+      v[j] = __uint_as_float(w[j]);
+    } else {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
     }
   }
 }
-template <class T, int N>
-__device__ __forceinline__ void store(T* p, const float* v) {
+template <class T>
+__device__ __forceinline__ uint4 narrow(const float* v) {
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < N; i += Vec<T>::N) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (sizeof(T) == 4) {
-        w[j] = __float_as_uint(v[i + j]);
-      } else {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[i + 2 * j], v[i + 2 * j + 1]);
-        w[j] = *reinterpret_cast<const uint32_t*>(&b);
-      }
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (sizeof(T) == 4) {
+      w[j] = __float_as_uint(v[j]);
+    } else {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    *reinterpret_cast<uint4*>(p + i) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// eight values
+template <class T>
+__device__ __forceinline__ void load8(const T* p, float* v) {
+#pragma unroll
+  for (int i = 0; i < 8; i += Vec<T>::N) widen<T>(load16(p + i), v + i);
+}
+template <class T>
+__device__ __forceinline__ void store8(T* p, const float* v) {
+#pragma unroll
+  for (int i = 0; i < 8; i += Vec<T>::N) *reinterpret_cast<uint4*>(p + i) = narrow<T>(v + i);
 }
 template <class T>
 __device__ __forceinline__ float value(const T* p) {
   return static_cast<float>(*p);
 }
+
+// t / n for t <= kRotThreads: (t + 1/2) / n is at least 1 / 2n off a whole number
+__device__ __forceinline__ int quotient(int t, int n) { return static_cast<int>((t + 0.5f) * __frcp_rn(static_cast<float>(n))); }
+
+// Items (row, head, item of a head) dealt out to a block's threads in order.
+struct Walk {
+  int r, h, i;
+  int heads, per, dr, dh, di;
+  __device__ __forceinline__ Walk(int heads, int per) : heads(heads), per(per) {
+    const int u = quotient(threadIdx.x, per), d = quotient(kRotThreads, per);
+    r = quotient(u, heads);
+    h = u - r * heads;
+    i = threadIdx.x - u * per;
+    dr = quotient(d, heads);
+    dh = d - dr * heads;
+    di = kRotThreads - d * per;
+  }
+  __device__ __forceinline__ void next() {
+    i += di;
+    h += dh;
+    r += dr;
+    if (i >= per) {
+      i -= per;
+      ++h;
+    }
+    if (h >= heads) {
+      h -= heads;
+      ++r;
+    }
+  }
+};
 
 // magnitude times (cos, sin) of a position's angle
 __device__ __forceinline__ float2 turned(const Rotary& rot, int i, int pos) {
@@ -85,186 +169,244 @@ __host__ __device__ __forceinline__ int layout_of(int dim, int interleaved) {
   return interleaved ? kPairs : ((dim / 2) % Vec<T>::N ? kSingle : kHalves);
 }
 
-// Heads [h0, h1) of the block's rows from x to y, turned by cs. Rows that are not
-// ok are left as they are.
-template <class T, int LAYOUT>
-__device__ __forceinline__ void turn_heads(const T* x, int64_t ldx, T* y, int64_t ldy, int64_t row0, int rows, const int* ok,
-                                           int h0, int h1, int D, int dim, const float2* cs) {
-  constexpr int N = Vec<T>::N;
-  const int half = dim / 2, heads = h1 - h0;
-  const bool in_place = x == y && ldx == ldy;  // what is not turned is there
-  const int turned_items = LAYOUT == kHalves ? half / N : (LAYOUT == kPairs ? (dim + N - 1) / N : half);
-  const int rest = LAYOUT == kSingle ? D - dim : (LAYOUT == kPairs ? D / N - turned_items : (D - dim) / N);
-  const int per = turned_items + (in_place ? 0 : rest);
-  if (heads <= 0 || per == 0) return;
-  // (row, head, item) of this thread, and the way to its next one
-  int r = threadIdx.x / (heads * per), h = threadIdx.x / per % heads, i = threadIdx.x % per;
-  const int dr = kRotThreads / (heads * per), dh = kRotThreads / per % heads, di = kRotThreads % per;
-  while (r < rows) {
-    if (ok[r]) {
-      const int64_t at = static_cast<int64_t>(h0 + h) * D;
-      const T* from = x + (row0 + r) * ldx + at;
-      T* to = y + (row0 + r) * ldy + at;
-      const float2* t = cs + r * half;
-      if constexpr (LAYOUT == kHalves) {
-        if (i < turned_items) {
-          float a[N], b[N];
-          load<T, N>(from + i * N, a);
-          load<T, N>(from + half + i * N, b);
+// Heads from h0 on of the block's rows from x to y.
+template <class T>
+struct Heads {
+  static constexpr int N = Vec<T>::N;
+  const T* x;
+  T* y;
+  int64_t ldx, ldy;
+  int h0, D, half, layout, turned_items, heads;  // items of a head from turned_items on are copied
+  int items;
+
+  static __device__ __forceinline__ int turned_of(const Rotary& rot, int layout) {
+    return layout == kHalves ? rot.dim / 2 / N : (layout == kPairs ? (rot.dim + N - 1) / N : rot.dim / 2);
+  }
+  static __device__ __forceinline__ int items_of(const Rotary& rot, int layout, int D, bool in_place) {
+    const int t = turned_of(rot, layout);
+    if (in_place) return t;  // what is not turned is there
+    return t + (layout == kSingle ? D - rot.dim : (layout == kPairs ? D / N - t : (D - rot.dim) / N));
+  }
+  // the block's rows from x and y on
+  __device__ __forceinline__ Heads(const T* x, int64_t ldx, T* y, int64_t ldy, int h0, int heads, int D, const Rotary& rot)
+      : x(x), y(y), ldx(ldx), ldy(ldy), h0(h0), D(D), half(rot.dim / 2), layout(layout_of<T>(rot.dim, rot.interleaved)),
+        turned_items(turned_of(rot, layout)), heads(heads), items(items_of(rot, layout, D, x == y && ldx == ldy)) {}
+  template <int LAYOUT>
+  __device__ __forceinline__ void turn(const Walk& w, const float* cs) const {
+    const int column = (h0 + w.h) * D;
+    const T* from = x + w.r * ldx + column;
+    T* to = y + w.r * ldy + column;
+    if constexpr (LAYOUT == kHalves) {
+      if (w.i < turned_items) {
+        float u[N], v[N], c[N], s[N];
+        widen<T>(load16(from + w.i * N), u);
+        widen<T>(load16(from + half + w.i * N), v);
 #pragma unroll
-          for (int j = 0; j < N; ++j) {
-            const float2 w = t[i * N + j];
-            const float u = a[j] * w.x - b[j] * w.y;
-            b[j] = b[j] * w.x + a[j] * w.y;
-            a[j] = u;
-          }
-          store<T, N>(to + i * N, a);
-          store<T, N>(to + half + i * N, b);
-        } else {
-          const int e = dim + (i - turned_items) * N;
-          *reinterpret_cast<uint4*>(to + e) = *reinterpret_cast<const uint4*>(from + e);
+        for (int j = 0; j < N; j += 4) {
+          *reinterpret_cast<float4*>(c + j) = *reinterpret_cast<const float4*>(cs + w.i * N + j);
+          *reinterpret_cast<float4*>(s + j) = *reinterpret_cast<const float4*>(cs + half + w.i * N + j);
         }
-      } else if constexpr (LAYOUT == kPairs) {
-        float a[N];
-        load<T, N>(from + i * N, a);
-#pragma unroll
-        for (int j = 0; j < N / 2; ++j) {
-          const int p = i * (N / 2) + j;
-          if (p < half) {
-            const float2 w = t[p];
-            const float u = a[2 * j] * w.x - a[2 * j + 1] * w.y;
-            a[2 * j + 1] = a[2 * j + 1] * w.x + a[2 * j] * w.y;
-            a[2 * j] = u;
-          }
-        }
-        store<T, N>(to + i * N, a);
+        moe::turn<N>(u, v, c, s);
+        *reinterpret_cast<uint4*>(to + w.i * N) = narrow<T>(u);
+        *reinterpret_cast<uint4*>(to + half + w.i * N) = narrow<T>(v);
       } else {
-        if (i < half) {
-          const float a = value(from + i), b = value(from + half + i);
-          const float2 w = t[i];
-          to[i] = static_cast<T>(a * w.x - b * w.y);
-          to[half + i] = static_cast<T>(b * w.x + a * w.y);
-        } else {
-          to[half + i] = from[half + i];  // items past the pairs are the columns from dim on
+        *reinterpret_cast<uint4*>(to + (w.i + turned_items) * N) = load16(from + (w.i + turned_items) * N);
+      }
+    } else if constexpr (LAYOUT == kPairs) {
+      float v[N];
+      widen<T>(load16(from + w.i * N), v);
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        const int p = w.i * (N / 2) + j;
+        if (p < half) {
+          const float c = cs[p], s = cs[half + p], t = v[2 * j] * c - v[2 * j + 1] * s;
+          v[2 * j + 1] = v[2 * j + 1] * c + v[2 * j] * s;
+          v[2 * j] = t;
         }
       }
-    }
-    i += di;
-    h += dh;
-    r += dr;
-    if (i >= per) {
-      i -= per;
-      ++h;
-    }
-    if (h >= heads) {
-      h -= heads;
-      ++r;
+      *reinterpret_cast<uint4*>(to + w.i * N) = narrow<T>(v);
+    } else {
+      if (w.i < half) {
+        const float u = value(from + w.i), v = value(from + half + w.i), c = cs[w.i], s = cs[half + w.i];
+        to[w.i] = static_cast<T>(u * c - v * s);
+        to[half + w.i] = static_cast<T>(v * c + u * s);
+      } else {
+        to[half + w.i] = from[half + w.i];  // items past the pairs are the columns from dim on
+      }
     }
   }
-}
-template <class T>
-__device__ __forceinline__ void turn_heads(const T* x, int64_t ldx, T* y, int64_t ldy, int64_t row0, int rows, const int* ok,
-                                           int h0, int h1, int D, const Rotary& rot, const float2* cs) {
-  switch (layout_of<T>(rot.dim, rot.interleaved)) {
-    case kHalves: return turn_heads<T, kHalves>(x, ldx, y, ldy, row0, rows, ok, h0, h1, D, rot.dim, cs);
-    case kPairs: return turn_heads<T, kPairs>(x, ldx, y, ldy, row0, rows, ok, h0, h1, D, rot.dim, cs);
-    default: return turn_heads<T, kSingle>(x, ldx, y, ldy, row0, rows, ok, h0, h1, D, rot.dim, cs);
+  // Rows that are not ok are left as they are.
+  template <int LAYOUT>
+  __device__ __forceinline__ void turn(int rows, const int* ok, const float* cs) const {
+    for (Walk w(heads, items); w.r < rows; w.next())
+      if (ok[w.r]) turn<LAYOUT>(w, cs + w.r * 2 * half);
   }
-}
+  __device__ __forceinline__ void turn(int rows, const int* ok, const float* cs) const {
+    if (heads == 0) return;
+    switch (layout) {
+      case kHalves: return turn<kHalves>(rows, ok, cs);
+      case kPairs: return turn<kPairs>(rows, ok, cs);
+      default: return turn<kSingle>(rows, ok, cs);
+    }
+  }
+};
 
 // this block's share of `heads` heads
 __device__ __forceinline__ int2 share(int heads) {
   return make_int2(static_cast<int>(static_cast<int64_t>(heads) * blockIdx.y / gridDim.y),
                    static_cast<int>(static_cast<int64_t>(heads) * (blockIdx.y + 1) / gridDim.y));
 }
+// the rows' cosines, half of them a row, and sines
+__device__ __forceinline__ void angles(const Rotary& rot, const int* pos, int rows, float* cs) {
+  const int half = rot.dim / 2;
+  if (half == 0) return;
+  int r = quotient(threadIdx.x, half), i = threadIdx.x - r * half;
+  const int dr = quotient(kRotThreads, half), di = kRotThreads - dr * half;
+  while (r < rows) {
+    const float2 w = turned(rot, i, pos[r]);
+    cs[r * 2 * half + i] = w.x;
+    cs[r * 2 * half + half + i] = w.y;
+    i += di;
+    r += dr;
+    if (i >= half) {
+      i -= half;
+      ++r;
+    }
+  }
+}
 
 template <class T>
-__global__ void __launch_bounds__(kRotThreads)
+__global__ void __launch_bounds__(kRotThreads, 8)
     rotary_kernel(Rotary rot, const int32_t* __restrict__ pos, const T* x, int64_t ldx, T* y, int64_t ldy, int n_rows, int heads,
                   int D, int per_block) {
-  extern __shared__ float2 cs[];
-  __shared__ int ok[kMostRows];
+  extern __shared__ __align__(16) float cs[];
+  __shared__ int ok[kMostRows], s_pos[kMostRows];
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * per_block;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(per_block), n_rows - row0)), half = rot.dim / 2;
-  if (threadIdx.x < kMostRows) ok[threadIdx.x] = 1;
-  for (int e = threadIdx.x; e < rows * half; e += kRotThreads) cs[e] = turned(rot, e % half, __ldg(pos + row0 + e / half));
+  const int rows = static_cast<int>(min(static_cast<int64_t>(per_block), n_rows - row0));
+  if (threadIdx.x < rows) {
+    s_pos[threadIdx.x] = __ldg(pos + row0 + threadIdx.x);
+    ok[threadIdx.x] = 1;
+  }
+  __syncthreads();
+  angles(rot, s_pos, rows, cs);
   __syncthreads();
   const int2 hs = share(heads);
-  turn_heads<T>(x, ldx, y, ldy, row0, rows, ok, hs.x, hs.y, D, rot, cs);
+  Heads<T>(x + row0 * ldx, ldx, y + row0 * ldy, ldy, hs.x, hs.y - hs.x, D, rot).turn(rows, ok, cs);
 }
 
 // Values 8 o .. 8 o + 7 of a head, turned.
 template <class T>
-__device__ __forceinline__ void turned8(const T* from, int o, const Rotary& rot, const float2* t, float* v) {
-  load<T, 8>(from + 8 * o, v);
+__device__ __forceinline__ void turn8(const T* from, int o, const Rotary& rot, const float* cs, float* v) {
   const int half = rot.dim / 2;
   if (8 * o >= rot.dim) return;
-  if (rot.interleaved) {
+  if (half % 8 == 0 && !rot.interleaved) {
+    const bool first = 8 * o < half;
+    float u[8], c[8], s[8];
+    load8<T>(from + 8 * o + (first ? half : -half), u);
+    const float* at = cs + 8 * o - (first ? 0 : half);
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+      *reinterpret_cast<float4*>(c + j) = *reinterpret_cast<const float4*>(at + j);
+      *reinterpret_cast<float4*>(s + j) = *reinterpret_cast<const float4*>(at + half + j);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const F2 us = mul2(f2(u[j], u[j + 1]), f2(s[j], s[j + 1])) ^ (first ? 0x8000000080000000ull : 0ull);
+      const float2 x = both(fma2(f2(v[j], v[j + 1]), f2(c[j], c[j + 1]), us));
+      v[j] = x.x;
+      v[j + 1] = x.y;
+    }
+  } else if (rot.interleaved) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (4 * o + j >= half) break;
-      const float2 w = t[4 * o + j];
-      const float u = v[2 * j] * w.x - v[2 * j + 1] * w.y;
-      v[2 * j + 1] = v[2 * j + 1] * w.x + v[2 * j] * w.y;
+      const float c = cs[4 * o + j], s = cs[half + 4 * o + j], u = v[2 * j] * c - v[2 * j + 1] * s;
+      v[2 * j + 1] = v[2 * j + 1] * c + v[2 * j] * s;
       v[2 * j] = u;
     }
-  } else if (half % 8 == 0) {
-    const bool first = 8 * o < half;
-    float b[8];
-    load<T, 8>(from + 8 * o + (first ? half : -half), b);
-    const float2* w = t + 8 * o - (first ? 0 : half);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = first ? v[j] * w[j].x - b[j] * w[j].y : v[j] * w[j].x + b[j] * w[j].y;
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int e = 8 * o + j;
       if (e < half)
-        v[j] = v[j] * t[e].x - value(from + e + half) * t[e].y;
+        v[j] = v[j] * cs[e] - value(from + e + half) * cs[half + e];
       else if (e < rot.dim)
-        v[j] = v[j] * t[e - half].x + value(from + e - half) * t[e - half].y;
+        v[j] = v[j] * cs[e - half] + value(from + e - half) * cs[e];
     }
   }
 }
 
+// the lesser and the larger; NaN if either is
+__device__ __forceinline__ float least(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float most(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // The codes of eight values of a group that eight neighbouring lanes hold, and the
 // group's scale and offset as one word.
+// A code is d / s rounded to the nearest whole number, to the even one of two as near,
+// with d = v - b. A division for each takes more time (77 us against 68 in all for the
+// prompts above): n is rounded from d / s less 2^-20 of it, so it is the code or the whole number below, and the code
+// is above if d - n s is more than s / 2, or as much and n is odd. That remainder is
+// exact: it is a multiple of d's or s's last place, and s has eight bits.
 __device__ __forceinline__ uint32_t quantised(const float* v, uint32_t* meta) {
   const unsigned int lanes = 0xFFu << (threadIdx.x & 24);
-  constexpr float kMost = 0x1p126f;
+  constexpr float kMost = 0x1p126f, kWhole = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
   float lo = v[0], hi = v[0];
-  bool fine = true;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, v[i]);
-    hi = fmaxf(hi, v[i]);
-    fine &= fabsf(v[i]) <= kMost;
+  for (int i = 1; i < 8; ++i) {
+    lo = least(lo, v[i]);
+    hi = most(hi, v[i]);
   }
 #pragma unroll
   for (int x = 1; x < 8; x <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(lanes, lo, x));
-    hi = fmaxf(hi, __shfl_xor_sync(lanes, hi, x));
+    lo = least(lo, __shfl_xor_sync(lanes, lo, x));
+    hi = most(hi, __shfl_xor_sync(lanes, hi, x));
   }
-  fine = __all_sync(lanes, fine);
+  if (!(lo >= -kMost && hi <= kMost)) {
+    *meta = 0x7FC07FC0u;
+    return 0u;
+  }
   const __nv_bfloat16 b16 = __float2bfloat16_rn(lo);
   const float b = __bfloat162float(b16);
   const __nv_bfloat16 s16 = __float2bfloat16_rn(__fdiv_rn(hi - b, 15.f));
   const float s = __bfloat162float(s16);
+  const uint32_t offset = static_cast<uint32_t>(__bfloat16_as_ushort(b16)) << 16;
+  *meta = offset;
+  if (!(s > 0.f)) return 0u;
+  *meta = offset | __bfloat16_as_ushort(s16);
   uint32_t w = 0;
-  if (fine && s > 0.f) {
+  if (s < 0x1p-100f) {  // (1 / s may be infinite, and s be short of bits)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       w |= static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(v[i] - b, s)), 0.f), 15.f)) << (4 * i);
+    return w;
   }
-  *meta = fine ? static_cast<uint32_t>(__bfloat16_as_ushort(s > 0.f ? s16 : __float2bfloat16_rn(0.f))) |
-                     static_cast<uint32_t>(__bfloat16_as_ushort(b16)) << 16
-               : 0x7FC07FC0u;
-  return w;
+  const float inv = __frcp_rn(s) * (1.f - 0x1p-20f);
+  const int half = __float_as_int(0.5f * s);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 d = both(add2(f2(v[i], v[i + 1]), f2(-b, -b)));
+    const F2 dd = f2(fmaxf(d.x, 0.f), fmaxf(d.y, 0.f)), mm = fma2(dd, f2(inv, inv), f2(kWhole, kWhole));
+    const float2 m = both(mm), rest = both(fma2(add2(mm, f2(-kWhole, -kWhole)), f2(-s, -s), dd));
+    int n0 = __float_as_int(m.x), n1 = __float_as_int(m.y);
+    if (__float_as_int(rest.x) + (n0 & 1) > half) ++n0;  // (a negative rest is a negative integer)
+    if (__float_as_int(rest.y) + (n1 & 1) > half) ++n1;
+    w += static_cast<uint32_t>(n0) << (4 * i);  // n is 0x4B400000 and the code, at most 15
+    w += static_cast<uint32_t>(n1) << (4 * i + 4);
+  }
+  return w - 0x4B400000u * 0x11111111u;
 }
 
 struct WriteArgs {
   Kv kv;
-  Rotary rot;  // dim 0: k is stored as it is
+  Rotary rot;  // dim 0: there is no q, and k is stored as it is
   const void *q, *k, *v;
   void *q_out, *pk, *pv;  // pages of the layer
   int64_t ldq, ldqo, ldk, ldv;
@@ -273,11 +415,11 @@ struct WriteArgs {
   uint32_t number;
 };
 
-// One to four rows a block: a warp a row finds its place, then q's heads are
-// turned and k and v are stored, eight values a thread at a time.
+// A warp a row finds its place, then q's heads are turned and k and v are stored,
+// eight values a thread at a time: items of k's heads, then of v's.
 template <class T, bool CODES>
-__global__ void __launch_bounds__(kRotThreads) write_rotary_kernel(const WriteArgs a) {
-  extern __shared__ float2 cs[];
+__global__ void __launch_bounds__(kRotThreads, 8) write_rotary_kernel(const WriteArgs a) {
+  extern __shared__ __align__(16) float cs[];
   __shared__ int ok[kMostRows], s_pos[kMostRows], s_page[kMostRows];
   const Kv& kv = a.kv;
   const int row0 = blockIdx.x * a.per_block, rows = min(a.per_block, a.n_rows - row0), half = a.rot.dim / 2;
@@ -299,50 +441,47 @@ __global__ void __launch_bounds__(kRotThreads) write_rotary_kernel(const WriteAr
   }
   // (warps read the word of errors at different times, and a block goes one way)
   if (__syncthreads_or(stop)) return;
-  for (int e = threadIdx.x; e < rows * half; e += kRotThreads) {
-    const int r = e / half;
-    cs[e] = turned(a.rot, e - r * half, s_pos[r]);
-  }
+  angles(a.rot, s_pos, rows, cs);
   __syncthreads();
   if (a.q) {
     const int2 hs = share(a.Hq);
-    turn_heads<T>(static_cast<const T*>(a.q), a.ldq, static_cast<T*>(a.q_out), a.ldqo, row0, rows, ok, hs.x, hs.y, a.D, a.rot, cs);
+    Heads<T>(static_cast<const T*>(a.q) + row0 * a.ldq, a.ldq, static_cast<T*>(a.q_out) + row0 * a.ldqo, a.ldqo, hs.x, hs.y - hs.x,
+             a.D, a.rot)
+        .turn(rows, ok, cs);
   }
-  // k and v: items (row, k or v, head, octet); the octets of a group are neighbouring lanes'
   const int2 hs = share(a.H);
-  const int heads = hs.y - hs.x, octets = a.D / 8, per_row = 2 * heads * octets;
-  for (int e = threadIdx.x; e < rows * per_row; e += kRotThreads) {
-    int i = e;
-    const int r = i / per_row;
-    i -= r * per_row;
-    const int is_v = i >= heads * octets;
-    i -= is_v * heads * octets;
-    const int h = i / octets, o = i - h * octets;
-    if (!ok[r]) continue;  // (a group's lanes are of one row)
-    const T* from = static_cast<const T*>(is_v ? a.v : a.k) + static_cast<int64_t>(row0 + r) * (is_v ? a.ldv : a.ldk) +
-                    static_cast<int64_t>(hs.x + h) * a.D;
+  const int heads = hs.y - hs.x;
+  if (heads == 0) return;
+  for (Walk w(2 * heads, a.D / 8); w.r < rows; w.next()) {
+    if (!ok[w.r]) continue;  // (a group's lanes are of one row)
+    const bool is_v = w.h >= heads;
+    const T* from = static_cast<const T*>(is_v ? a.v : a.k) + (row0 + w.r) * (is_v ? a.ldv : a.ldk) +
+                    (hs.x + w.h - (is_v ? heads : 0)) * a.D;
     float v[8];
-    if (is_v)
-      load<T, 8>(from + 8 * o, v);
-    else
-      turned8<T>(from, o, a.rot, cs + r * half, v);
+    load8<T>(from + 8 * w.i, v);
+    if (!is_v) turn8<T>(from, w.i, a.rot, cs + w.r * 2 * half, v);
     char* pages = static_cast<char*>(is_v ? a.pv : a.pk);
-    const int64_t block = static_cast<int64_t>(s_page[r]) * a.H + hs.x + h;
-    const int place = s_pos[r] & (kv.page - 1);
+    const int64_t block = static_cast<int64_t>(s_page[w.r]) * a.H + hs.x + w.h - (is_v ? heads : 0);
+    const int place = s_pos[w.r] & (kv.page - 1);
     if constexpr (CODES) {
       uint32_t meta;
-      const uint32_t w = quantised(v, &meta);
+      const uint32_t codes = quantised(v, &meta);
       const int row_bytes = a.D / 2, meta_bytes = a.D / 16;
-      char* at = pages + ((block * (row_bytes + meta_bytes)) << kv.page_shift);
-      *reinterpret_cast<uint32_t*>(at + place * row_bytes + 4 * o) = w;
-      if ((o & 7) == 0)
-        *reinterpret_cast<uint32_t*>(at + (row_bytes << kv.page_shift) + place * meta_bytes + o / 2) = meta;
+      char* to = pages + ((block * (row_bytes + meta_bytes)) << kv.page_shift);
+      *reinterpret_cast<uint32_t*>(to + place * row_bytes + 4 * w.i) = codes;
+      if ((w.i & 7) == 0)
+        *reinterpret_cast<uint32_t*>(to + (row_bytes << kv.page_shift) + place * meta_bytes + w.i / 2) = meta;
     } else {
-      store<T, 8>(reinterpret_cast<T*>(pages) + ((block << kv.page_shift) + place) * a.D + 8 * o, v);
+      store8<T>(reinterpret_cast<T*>(pages) + ((block << kv.page_shift) + place) * a.D + 8 * w.i, v);
     }
   }
 }
 
+// 2^(23 - 4 j), and that and code j < 5 of w
+__device__ __forceinline__ float one_of(int j) { return __uint_as_float(0x4B000000u - (j << 25)); }
+__device__ __forceinline__ float code_in(uint32_t w, int j) {
+  return __uint_as_float((w & (15u << (4 * j))) | (0x4B000000u - (j << 25)));
+}
 // The newest tokens of sequences out of their pages, eight values a thread.
 template <class T, bool CODES>
 __global__ void __launch_bounds__(kRotThreads) read_kernel(const WriteArgs a) {
@@ -364,37 +503,46 @@ __global__ void __launch_bounds__(kRotThreads) read_kernel(const WriteArgs a) {
   }
   __syncthreads();
   const int2 hs = share(a.H);
-  const int heads = hs.y - hs.x, octets = a.D / 8, per_row = 2 * heads * octets;
-  for (int e = threadIdx.x; e < rows * per_row; e += kRotThreads) {
-    int i = e;
-    const int r = i / per_row;
-    i -= r * per_row;
-    const int is_v = i >= heads * octets;
-    i -= is_v * heads * octets;
-    const int h = i / octets, o = i - h * octets;
-    if (s_page[r] < 0) continue;
+  const int heads = hs.y - hs.x;
+  if (heads == 0) return;
+  for (Walk w(2 * heads, a.D / 8); w.r < rows; w.next()) {
+    if (s_page[w.r] < 0) continue;
+    const bool is_v = w.h >= heads;
+    const int h = hs.x + w.h - (is_v ? heads : 0);
     const char* pages = static_cast<const char*>(is_v ? a.pv : a.pk);
-    const int64_t block = static_cast<int64_t>(s_page[r]) * a.H + hs.x + h;
-    const int place = s_pos[r] & (kv.page - 1);
-    T* to = static_cast<T*>(const_cast<void*>(is_v ? a.v : a.k)) + static_cast<int64_t>(row0 + r) * (is_v ? a.ldv : a.ldk) +
-            static_cast<int64_t>(hs.x + h) * a.D + 8 * o;
-    float v[8];
+    const int64_t block = static_cast<int64_t>(s_page[w.r]) * a.H + h;
+    const int place = s_pos[w.r] & (kv.page - 1);
+    T* to = static_cast<T*>(const_cast<void*>(is_v ? a.v : a.k)) + (row0 + w.r) * (is_v ? a.ldv : a.ldk) + h * a.D + 8 * w.i;
     if constexpr (CODES) {
+      float v[8];
       const int row_bytes = a.D / 2, meta_bytes = a.D / 16;
-      const char* at = pages + ((block * (row_bytes + meta_bytes)) << kv.page_shift);
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(at + place * row_bytes + 4 * o);
-      const uint32_t m = *reinterpret_cast<const uint32_t*>(at + (row_bytes << kv.page_shift) + place * meta_bytes + o / 8 * 4);
+      const char* from = pages + ((block * (row_bytes + meta_bytes)) << kv.page_shift);
+      const uint32_t c = *reinterpret_cast<const uint32_t*>(from + place * row_bytes + 4 * w.i);
+      const uint32_t m = *reinterpret_cast<const uint32_t*>(from + (row_bytes << kv.page_shift) + place * meta_bytes + w.i / 8 * 4);
       const float s = __uint_as_float(m << 16), b = __uint_as_float(m & 0xFFFF0000u);
+      // a code in its place in the fraction of 2^(23 - 4 j) adds the code to it
+      const uint32_t c5 = c >> 20;
+      const F2 ss = f2(s, s), bb = f2(b, b);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = static_cast<float>((w >> (4 * j)) & 15u) * s + b;
+      for (int j = 0; j < 8; j += 2) {
+        const float2 u = make_float2(code_in(j < 5 ? c : c5, j < 5 ? j : j - 5), code_in(j < 4 ? c : c5, j < 4 ? j + 1 : j - 4));
+        const float2 o = make_float2(-one_of(j < 5 ? j : j - 5), -one_of(j < 4 ? j + 1 : j - 4));
+        const float2 x = both(fma2(add2(f2(u.x, u.y), f2(o.x, o.y)), ss, bb));
+        v[j] = x.x;
+        v[j + 1] = x.y;
+      }
+      store8<T>(to, v);
     } else {
-      load<T, 8>(reinterpret_cast<const T*>(pages) + ((block << kv.page_shift) + place) * a.D + 8 * o, v);
+      const T* from = reinterpret_cast<const T*>(pages) + ((block << kv.page_shift) + place) * a.D + 8 * w.i;
+#pragma unroll
+      for (int j = 0; j < 8; j += Vec<T>::N) *reinterpret_cast<uint4*>(to + j) = load16(from + j);
     }
-    store<T, 8>(to, v);
   }
 }
 
-// Rows a block and blocks a row: a row is cut by its heads while blocks are short
+// Rows a block and blocks a row: four rows share a block's latencies once there are
+// blocks enough (the prompts above: 76 us with two, 68 with eight, of which an SM gets
+// six or seven at once and no more), and a row is cut by its heads while blocks are short
 // of the SMs and have work for their threads.
 struct Shape {
   int per_block;
@@ -412,7 +560,7 @@ template <class T>
 cudaError_t rotary(const Rotary& rot, const int32_t* pos, const void* x, int64_t ldx, void* y, int64_t ldy, int32_t rows,
                    int32_t heads, int32_t D, int num_sms, cudaStream_t st) {
   const Shape s = shape_of(rows, heads, static_cast<int64_t>(heads) * D / Vec<T>::N, num_sms);
-  rotary_kernel<T><<<s.grid, kRotThreads, s.per_block * rot.dim / 2 * sizeof(float2), st>>>(
+  rotary_kernel<T><<<s.grid, kRotThreads, s.per_block * rot.dim * sizeof(float), st>>>(
       rot, pos, static_cast<const T*>(x), ldx, static_cast<T*>(y), ldy, rows, heads, D, s.per_block);
   return cudaGetLastError();
 }
@@ -459,7 +607,7 @@ cudaError_t launch_kv_write_rotary(const moe_kv_t& a, const KvLayout& l, int32_t
   w.number = next_write();
   const Shape s = shape_of(n_rows, std::max(n_heads, a.n_kv_heads), (n_heads + 2ll * a.n_kv_heads) * a.head_dim / 8, num_sms);
   w.per_block = s.per_block;
-  const size_t smem = s.per_block * rot.dim / 2 * sizeof(float2);
+  const size_t smem = s.per_block * rot.dim * sizeof(float);
   const bool codes = a.dtype & MOE_KV_I4, f32 = token_type(a) == MOE_F32;
   if (codes && f32)
     write_rotary_kernel<float, true><<<s.grid, kRotThreads, smem, st>>>(w);
