@@ -70,7 +70,7 @@ class KvT(C.Structure):
 
 
 class RotaryT(C.Structure):
-    _fields_ = [("turns", C.c_void_p), ("dim", C.c_int32), ("interleaved", C.c_int32), ("magnitude", C.c_float)]
+    _fields_ = [("turns", C.c_void_p), ("dim", C.c_int32), ("interleaved", C.c_int32), ("magnitude", C.c_double)]
 
 
 class SamplingT(C.Structure):

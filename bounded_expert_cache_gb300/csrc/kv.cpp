@@ -112,8 +112,9 @@ moe_status_t open_rotary(const char* call, const moe_rotary_t* rot, int32_t D, m
   if (reinterpret_cast<uintptr_t>(rot->turns) % 8) return fail(MOE_ERR_ARG, call, "turns is not 8-byte aligned");
   if (rot->dim < 2 || rot->dim % 2 || rot->dim > D) return fail(MOE_ERR_ARG, call, "the rotation's dim is not an even number in 2..head_dim");
   if (rot->interleaved != 0 && rot->interleaved != 1) return fail(MOE_ERR_ARG, call, "interleaved is neither 0 nor 1");
-  if (!std::isfinite(rot->magnitude)) return fail(MOE_ERR_ARG, call, "magnitude is not finite");
-  *r = moe::Rotary{rot->turns, rot->dim, rot->interleaved, rot->magnitude};
+  const float magnitude = static_cast<float>(rot->magnitude);
+  if (!std::isfinite(magnitude)) return fail(MOE_ERR_ARG, call, "magnitude is not finite in fp32");
+  *r = moe::Rotary{rot->turns, rot->dim, rot->interleaved, magnitude, static_cast<float>(rot->magnitude - magnitude)};
   return MOE_OK;
 }
 // Rows of heads that go from x to y.

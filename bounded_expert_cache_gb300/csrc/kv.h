@@ -95,7 +95,7 @@ cudaError_t launch_kv_write(const moe_kv_t& kv, const KvLayout& l, int32_t layer
 struct Rotary {
   const uint64_t* turns;  // [dim / 2] turns a position, times 2^64
   int32_t dim, interleaved;
-  float magnitude;
+  float magnitude, magnitude_rest;  // its sum
 };
 cudaError_t launch_rotary(const Rotary& rot, const int32_t* pos, const void* x, int32_t xt, int64_t ldx, void* y, int64_t ldy,
                           int32_t rows, int32_t heads, int32_t D, int num_sms, cudaStream_t st);

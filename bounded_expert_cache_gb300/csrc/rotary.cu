@@ -5,12 +5,18 @@
 // becomes (a c - b s, b c + a s) with c, s = magnitude times cos, sin of p f_i.
 // p f_i reaches 10^6 radians, of which fp32 would keep a sixteenth: the frequencies
 // are given in turns as 64-bit fractions, so that p times one wraps whole turns
-// away exactly, and what is left is rounded to fp32 once. Rotation is in fp32, one
-// rounding to the type of the result (none before 4-bit codes).
+// away exactly. What is left is the nearest 256th of a turn, whose cosine and sine
+// are in a table, and an angle b of at most 2 pi / 512: cos(a + b) = cos a + (cos a
+// (cos b - 1) - sin a sin b), where b's series need two terms and what is added is so
+// small that c and s are the fp32 next to the exact values but for one in thirty.
+// Products and sums are fp32, each rounded, and then the result is to its type (not
+// before 4-bit codes): with that and such c and s, codes are those of the same steps
+// done one by one, where a last bit's difference puts a few in a million on the other
+// side of a border between two codes. (sincospif and fused products: the same times.)
 //
 // Pages of 4-bit codes: eight threads hold a group of 64 values; with lo and hi its
-// least and largest, b = bf16(lo), s = bf16((hi - b) / 15), q = round((x - b) / s)
-// within 0..15 (0 where s is 0), divisions and rounding as in IEEE. A group with an
+// least and largest, b = bf16(lo), s = bf16((hi - b) (1 / 15)), q = round((x - b) / s)
+// within 0..15 (0 where s is 0), in fp32 as in IEEE. A group with an
 // infinity, a NaN or a magnitude above 2^126 becomes NaN as a whole.
 //
 // What bounds them: one row the latency of its lookups (chunk, sequence, length,
@@ -53,26 +59,10 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
+// u c - v s and v c + u s (one by one: packed products and sums become fused instructions, .rn or not)
+__device__ __forceinline__ float2 turn(float u, float v, float c, float s) {
+  return make_float2(__fsub_rn(__fmul_rn(u, c), __fmul_rn(v, s)), __fadd_rn(__fmul_rn(v, c), __fmul_rn(u, s)));
 }
-// u c - v s and v c + u s, of values that lie side by side
-template <int N>
-__device__ __forceinline__ void turn(float* u, float* v, const float* c, const float* s) {
-#pragma unroll
-  for (int j = 0; j < N; j += 2) {
-    const F2 a = f2(u[j], u[j + 1]), b = f2(v[j], v[j + 1]), cc = f2(c[j], c[j + 1]), ss = f2(s[j], s[j + 1]);
-    const F2 bs = mul2(b, ss);
-    const float2 x = both(fma2(a, cc, bs ^ 0x8000000080000000ull)), y = both(fma2(b, cc, mul2(a, ss)));
-    u[j] = x.x;
-    u[j + 1] = x.y;
-    v[j] = y.x;
-    v[j + 1] = y.y;
-  }
-}
-
 template <class T>
 struct Vec {
   static constexpr int N = 16 / static_cast<int>(sizeof(T));
@@ -153,12 +143,41 @@ struct Walk {
   }
 };
 
+// Cosines and sines of the 256ths of a turn, each as a sum of two fp32.
+struct TurnTable {
+  float cs[256][4];
+};
+constexpr TurnTable turn_table() {
+  TurnTable t{};
+  for (int j = 0; j < 256; ++j) {
+    const double x = (j < 128 ? j : j - 256) * (3.14159265358979323846 / 128);
+    double c = 0, s = 0, term = 1;  // the series of both
+    for (int k = 0; k < 40; k += 2) {
+      c += term;
+      term *= x / (k + 1);
+      s += term;
+      term *= -x / (k + 2);
+    }
+    t.cs[j][0] = static_cast<float>(c);
+    t.cs[j][1] = static_cast<float>(c - static_cast<float>(c));
+    t.cs[j][2] = static_cast<float>(s);
+    t.cs[j][3] = static_cast<float>(s - static_cast<float>(s));
+  }
+  return t;
+}
+alignas(16) __device__ const TurnTable kTurnTable = turn_table();
+
 // magnitude times (cos, sin) of a position's angle
-__device__ __forceinline__ float2 turned(const Rotary& rot, int i, int pos) {
-  const int64_t t = static_cast<int64_t>(__ldg(rot.turns + i) * static_cast<uint64_t>(static_cast<int64_t>(pos)));
-  float s, c;  // t / 2^63 half turns in [-1, 1)
-  sincospif(__ll2float_rn(t) * 0x1p-63f, &s, &c);
-  return make_float2(c * rot.magnitude, s * rot.magnitude);
+__device__ __forceinline__ float2 turned(const Rotary& rot, int i, int pos, const float4* table) {
+  const uint64_t t = __ldg(rot.turns + i) * static_cast<uint64_t>(static_cast<int64_t>(pos));
+  const uint64_t at = t + (1ull << 55);
+  const float4 a = table[at >> 56];
+  const float b = __ll2float_rn(static_cast<int64_t>(at & ((1ull << 56) - 1)) - (1ll << 55)) * 3.40612158e-19f;  // 2 pi / 2^64
+  const float bb = b * b, c1 = bb * fmaf(bb, 1.f / 24, -0.5f), sb = fmaf(b * bb, -1.f / 6, b);
+  const float dc = fmaf(a.x, c1, fmaf(-a.z, sb, a.y)), ds = fmaf(a.z, c1, fmaf(a.x, sb, a.w));
+  const float m = rot.magnitude, c = m * a.x, s = m * a.z;
+  return make_float2(c + fmaf(m, dc, fmaf(rot.magnitude_rest, a.x, fmaf(m, a.x, -c))),
+                     s + fmaf(m, ds, fmaf(rot.magnitude_rest, a.z, fmaf(m, a.z, -s))));
 }
 
 // How a head's values are dealt out: halves whose vectors match, neighbours, or
@@ -206,7 +225,12 @@ struct Heads {
           *reinterpret_cast<float4*>(c + j) = *reinterpret_cast<const float4*>(cs + w.i * N + j);
           *reinterpret_cast<float4*>(s + j) = *reinterpret_cast<const float4*>(cs + half + w.i * N + j);
         }
-        moe::turn<N>(u, v, c, s);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const float2 t = moe::turn(u[j], v[j], c[j], s[j]);
+          u[j] = t.x;
+          v[j] = t.y;
+        }
         *reinterpret_cast<uint4*>(to + w.i * N) = narrow<T>(u);
         *reinterpret_cast<uint4*>(to + half + w.i * N) = narrow<T>(v);
       } else {
@@ -219,17 +243,17 @@ struct Heads {
       for (int j = 0; j < N / 2; ++j) {
         const int p = w.i * (N / 2) + j;
         if (p < half) {
-          const float c = cs[p], s = cs[half + p], t = v[2 * j] * c - v[2 * j + 1] * s;
-          v[2 * j + 1] = v[2 * j + 1] * c + v[2 * j] * s;
-          v[2 * j] = t;
+          const float2 t = moe::turn(v[2 * j], v[2 * j + 1], cs[p], cs[half + p]);
+          v[2 * j] = t.x;
+          v[2 * j + 1] = t.y;
         }
       }
       *reinterpret_cast<uint4*>(to + w.i * N) = narrow<T>(v);
     } else {
       if (w.i < half) {
-        const float u = value(from + w.i), v = value(from + half + w.i), c = cs[w.i], s = cs[half + w.i];
-        to[w.i] = static_cast<T>(u * c - v * s);
-        to[half + w.i] = static_cast<T>(v * c + u * s);
+        const float2 t = moe::turn(value(from + w.i), value(from + half + w.i), cs[w.i], cs[half + w.i]);
+        to[w.i] = static_cast<T>(t.x);
+        to[half + w.i] = static_cast<T>(t.y);
       } else {
         to[half + w.i] = from[half + w.i];  // items past the pairs are the columns from dim on
       }
@@ -256,14 +280,19 @@ __device__ __forceinline__ int2 share(int heads) {
   return make_int2(static_cast<int>(static_cast<int64_t>(heads) * blockIdx.y / gridDim.y),
                    static_cast<int>(static_cast<int64_t>(heads) * (blockIdx.y + 1) / gridDim.y));
 }
+// The table into shared memory, while a row's place is looked for.
+__device__ __forceinline__ void load_table(float4* table) {
+  static_assert(kRotThreads == 256, "one entry a thread");
+  table[threadIdx.x] = __ldg(reinterpret_cast<const float4*>(kTurnTable.cs[threadIdx.x]));
+}
 // the rows' cosines, half of them a row, and sines
-__device__ __forceinline__ void angles(const Rotary& rot, const int* pos, int rows, float* cs) {
+__device__ __forceinline__ void angles(const Rotary& rot, const int* pos, int rows, const float4* table, float* cs) {
   const int half = rot.dim / 2;
   if (half == 0) return;
   int r = quotient(threadIdx.x, half), i = threadIdx.x - r * half;
   const int dr = quotient(kRotThreads, half), di = kRotThreads - dr * half;
   while (r < rows) {
-    const float2 w = turned(rot, i, pos[r]);
+    const float2 w = turned(rot, i, pos[r], table);
     cs[r * 2 * half + i] = w.x;
     cs[r * 2 * half + half + i] = w.y;
     i += di;
@@ -281,6 +310,8 @@ __global__ void __launch_bounds__(kRotThreads, 8)
                   int D, int per_block) {
   extern __shared__ __align__(16) float cs[];
   __shared__ int ok[kMostRows], s_pos[kMostRows];
+  __shared__ float4 table[256];
+  load_table(table);
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * per_block;
   const int rows = static_cast<int>(min(static_cast<int64_t>(per_block), n_rows - row0));
   if (threadIdx.x < rows) {
@@ -288,7 +319,7 @@ __global__ void __launch_bounds__(kRotThreads, 8)
     ok[threadIdx.x] = 1;
   }
   __syncthreads();
-  angles(rot, s_pos, rows, cs);
+  angles(rot, s_pos, rows, table, cs);
   __syncthreads();
   const int2 hs = share(heads);
   Heads<T>(x + row0 * ldx, ldx, y + row0 * ldy, ldy, hs.x, hs.y - hs.x, D, rot).turn(rows, ok, cs);
@@ -310,28 +341,23 @@ __device__ __forceinline__ void turn8(const T* from, int o, const Rotary& rot, c
       *reinterpret_cast<float4*>(s + j) = *reinterpret_cast<const float4*>(at + half + j);
     }
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const F2 us = mul2(f2(u[j], u[j + 1]), f2(s[j], s[j + 1])) ^ (first ? 0x8000000080000000ull : 0ull);
-      const float2 x = both(fma2(f2(v[j], v[j + 1]), f2(c[j], c[j + 1]), us));
-      v[j] = x.x;
-      v[j + 1] = x.y;
-    }
+    for (int j = 0; j < 8; ++j) v[j] = first ? turn(v[j], u[j], c[j], s[j]).x : turn(u[j], v[j], c[j], s[j]).y;
   } else if (rot.interleaved) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (4 * o + j >= half) break;
-      const float c = cs[4 * o + j], s = cs[half + 4 * o + j], u = v[2 * j] * c - v[2 * j + 1] * s;
-      v[2 * j + 1] = v[2 * j + 1] * c + v[2 * j] * s;
-      v[2 * j] = u;
+      const float2 t = turn(v[2 * j], v[2 * j + 1], cs[4 * o + j], cs[half + 4 * o + j]);
+      v[2 * j] = t.x;
+      v[2 * j + 1] = t.y;
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int e = 8 * o + j;
       if (e < half)
-        v[j] = v[j] * cs[e] - value(from + e + half) * cs[half + e];
+        v[j] = turn(v[j], value(from + e + half), cs[e], cs[half + e]).x;
       else if (e < rot.dim)
-        v[j] = v[j] * cs[e - half] + value(from + e - half) * cs[e];
+        v[j] = turn(value(from + e - half), v[j], cs[e - half], cs[e]).y;
     }
   }
 }
@@ -375,7 +401,7 @@ __device__ __forceinline__ uint32_t quantised(const float* v, uint32_t* meta) {
   }
   const __nv_bfloat16 b16 = __float2bfloat16_rn(lo);
   const float b = __bfloat162float(b16);
-  const __nv_bfloat16 s16 = __float2bfloat16_rn(__fdiv_rn(hi - b, 15.f));
+  const __nv_bfloat16 s16 = __float2bfloat16_rn((hi - b) * (1.f / 15.f));
   const float s = __bfloat162float(s16);
   const uint32_t offset = static_cast<uint32_t>(__bfloat16_as_ushort(b16)) << 16;
   *meta = offset;
@@ -421,6 +447,8 @@ template <class T, bool CODES>
 __global__ void __launch_bounds__(kRotThreads, 8) write_rotary_kernel(const WriteArgs a) {
   extern __shared__ __align__(16) float cs[];
   __shared__ int ok[kMostRows], s_pos[kMostRows], s_page[kMostRows];
+  __shared__ float4 table[256];
+  if (a.q) load_table(table);
   const Kv& kv = a.kv;
   const int row0 = blockIdx.x * a.per_block, rows = min(a.per_block, a.n_rows - row0), half = a.rot.dim / 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -441,7 +469,7 @@ __global__ void __launch_bounds__(kRotThreads, 8) write_rotary_kernel(const Writ
   }
   // (warps read the word of errors at different times, and a block goes one way)
   if (__syncthreads_or(stop)) return;
-  angles(a.rot, s_pos, rows, cs);
+  angles(a.rot, s_pos, rows, table, cs);
   __syncthreads();
   if (a.q) {
     const int2 hs = share(a.Hq);

@@ -27,10 +27,10 @@
  * in the split-plane layout of one expert matrix (MOE_I4_G64 of moecache.h): the
  * codes, then the bf16 pairs (s, b). k and v are then bytes,
  * [n_layers][n_pages][n_kv_heads][page_tokens * head_dim * 9 / 16], and a value is
- * s*q + b. Storing a group takes b = its least value and s = (its largest - b) / 15,
- * both rounded to bf16, and q = (x - b) / s rounded to the nearest integer, ties to
- * even, within 0..15 (0 where s is 0), in fp32. A group with an infinity, a NaN or a
- * magnitude above 2^126 becomes NaN as a whole.
+ * s*q + b. Storing a group takes b = its least value and s = (its largest - b) times
+ * fp32's 1/15, both rounded to bf16, and q = (x - b) / s rounded to the nearest integer,
+ * ties to even, within 0..15 (0 where s is 0), in fp32. A group with an infinity, a NaN
+ * or a magnitude above 2^126 becomes NaN as a whole.
  *
  * The cache's arrays and a call's tensors are on the current device.
  */
@@ -122,7 +122,7 @@ typedef struct {
   const uint64_t* turns;
   int32_t dim;         /* even, 2..head size */
   int32_t interleaved; /* 0: halves, 1: neighbours */
-  float magnitude;     /* 1 for a plain rotation */
+  double magnitude;    /* 1 for a plain rotation */
 } moe_rotary_t;
 
 /* Angles a position, in radians: angles[i] = base^(-2i/dim) (host, [dim / 2]), for
