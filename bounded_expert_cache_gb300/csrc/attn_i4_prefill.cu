@@ -1,6 +1,8 @@
 // Attention of prompt chunks over pages of 4-bit codes in f32 and of heads above 128:
 // row tiles of the engine of attn_i4.cuh, one a CTA. (bf16 heads of 64 and 128 run on
-// the 5th-generation tensor cores, attn_prefill.cu.)
+// the 5th-generation tensor cores, attn_prefill.cu.) Every CTA converts all tokens its 16
+// rows see, and that bounds it: 1,024 tokens at 32,768, 16 heads / 2, of 256, bf16:
+// 4.6 ms; 2,048 at 8,192, f32, 8 / 8, of 64: 0.36 ms.
 #include "attn_i4.cuh"
 
 namespace moe {

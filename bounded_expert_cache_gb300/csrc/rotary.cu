@@ -23,11 +23,12 @@
 // table, page count: five dependent reads) and of one sine (rotary 2.3 us in a graph,
 // a write of one token 4.5); prompts HBM. A row's sines and cosines are formed once and
 // shared by its heads; a thread owns both halves of a pair, so that a result may
-// overwrite its input. 16,384 rows of 40 bf16 heads of 128: 59.7 us, 5.6 TB/s. Blocks
-// of 256 threads with 32 registers, eight on an SM: with 40 and the next item read
-// ahead it is 68. 7,591 rows of ragged prompts, 32 + 2 x 8 heads of 128 into 4-bit pages,
-// and these values read back: 64 us, of which q's heads (124 MB) take 18, near HBM's
-// rate; the codes, the values read back and the lookups are bound by instructions.
+// overwrite its input. 16,384 rows of 40 bf16 heads of 128: 56 us, 5.9 TB/s, halves or
+// neighbours. Blocks of 256 threads with 32 registers, eight on an SM: with 40 registers
+// and the next item read ahead 68. 7,591 rows of ragged prompts, 32 + 2 x 8 heads of 128
+// into 4-bit pages, and these values read back: 65 us, of which q's heads (124 MB) take
+// 18, near HBM's rate; the codes, the values read back and the lookups are bound by
+// instructions.
 #include <cuda_bf16.h>
 
 #include "kv_device.cuh"
@@ -210,6 +211,22 @@ struct Heads {
   __device__ __forceinline__ Heads(const T* x, int64_t ldx, T* y, int64_t ldy, int h0, int heads, int D, const Rotary& rot)
       : x(x), y(y), ldx(ldx), ldy(ldy), h0(h0), D(D), half(rot.dim / 2), layout(layout_of<T>(rot.dim, rot.interleaved)),
         turned_items(turned_of(rot, layout)), heads(heads), items(items_of(rot, layout, D, x == y && ldx == ldy)) {}
+  __device__ __forceinline__ int64_t offset(const Walk& w, int64_t ld) const { return w.r * ld + (h0 + w.h) * D + w.i * N; }
+  // neighbours: 16 bytes
+  __device__ __forceinline__ void turn_pairs(uint4 u, const Walk& w, const float* cs) const {
+    float v[N];
+    widen<T>(u, v);
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+      const int p = w.i * (N / 2) + j;
+      if (p < half) {
+        const float2 t = moe::turn(v[2 * j], v[2 * j + 1], cs[p], cs[half + p]);
+        v[2 * j] = t.x;
+        v[2 * j + 1] = t.y;
+      }
+    }
+    *reinterpret_cast<uint4*>(y + offset(w, ldy)) = narrow<T>(v);
+  }
   template <int LAYOUT>
   __device__ __forceinline__ void turn(const Walk& w, const float* cs) const {
     const int column = (h0 + w.h) * D;
@@ -236,19 +253,6 @@ struct Heads {
       } else {
         *reinterpret_cast<uint4*>(to + (w.i + turned_items) * N) = load16(from + (w.i + turned_items) * N);
       }
-    } else if constexpr (LAYOUT == kPairs) {
-      float v[N];
-      widen<T>(load16(from + w.i * N), v);
-#pragma unroll
-      for (int j = 0; j < N / 2; ++j) {
-        const int p = w.i * (N / 2) + j;
-        if (p < half) {
-          const float2 t = moe::turn(v[2 * j], v[2 * j + 1], cs[p], cs[half + p]);
-          v[2 * j] = t.x;
-          v[2 * j + 1] = t.y;
-        }
-      }
-      *reinterpret_cast<uint4*>(to + w.i * N) = narrow<T>(v);
     } else {
       if (w.i < half) {
         const float2 t = moe::turn(value(from + w.i), value(from + half + w.i), cs[w.i], cs[half + w.i]);
@@ -262,8 +266,23 @@ struct Heads {
   // Rows that are not ok are left as they are.
   template <int LAYOUT>
   __device__ __forceinline__ void turn(int rows, const int* ok, const float* cs) const {
-    for (Walk w(heads, items); w.r < rows; w.next())
-      if (ok[w.r]) turn<LAYOUT>(w, cs + w.r * 2 * half);
+    if constexpr (LAYOUT == kPairs) {
+      // (two items' loads at once: 16 bytes a thread are too few in flight, 59.7 us of the above)
+      for (Walk w(heads, items); w.r < rows; w.next()) {
+        const Walk first = w;
+        const bool one = ok[w.r];
+        uint4 u, v;
+        if (one) u = load16(x + offset(w, ldx));
+        w.next();
+        const bool two = w.r < rows && ok[w.r];
+        if (two) v = load16(x + offset(w, ldx));
+        if (one) turn_pairs(u, first, cs + first.r * 2 * half);
+        if (two) turn_pairs(v, w, cs + w.r * 2 * half);
+      }
+    } else {
+      for (Walk w(heads, items); w.r < rows; w.next())
+        if (ok[w.r]) turn<LAYOUT>(w, cs + w.r * 2 * half);
+    }
   }
   __device__ __forceinline__ void turn(int rows, const int* ok, const float* cs) const {
     if (heads == 0) return;
