@@ -146,7 +146,8 @@ moe_status_t moe_rotary(const moe_rotary_t* rot, const int32_t* pos, const void*
  * position in its sequence, k_new into the pages (from fp32 if they hold codes) and
  * q [n_rows][n_heads][head_dim] into q_out, which may be q (with ldqo = ldq) and
  * must not overlap q, k_new or v_new otherwise. v_new is stored as it is. Rows that
- * moe_kv_write would ignore or leave out are left as they are in q_out. */
+ * moe_kv_write would ignore or leave out are left as they are in q_out. Each sequence
+ * is listed once (else a token may hold codes of one row and a scale of another). */
 moe_status_t moe_kv_write_rotary(const moe_kv_t* kv, int32_t layer, const moe_rotary_t* rot, const void* q, int64_t ldq,
                                  int32_t n_heads, void* q_out, int64_t ldqo, const void* k_new, int64_t ldk,
                                  const void* v_new, int64_t ldv, const int32_t* seqs, const int32_t* cu, int32_t n,
@@ -185,8 +186,11 @@ moe_status_t moe_kv_copy_pages(const moe_kv_t* kv, const int32_t* src, const int
  * does not reach it, infinities and NaN included. q and out: device
  * [rows][n_heads][head_dim] of the cache's dtype (without MOE_KV_I4), rows ldq and
  * ldo elements apart and 16-byte aligned. Scores, softmax statistics and sums are
- * fp32; for bf16 the softmax's numerators (over pages of codes: times a scale)
- * enter the value product as bf16.
+ * fp32; for bf16 the softmax's numerators enter the value product as bf16. Over pages
+ * of codes bf16 calls multiply f16: queries, and values or numerators times scales,
+ * over powers of two that rows and tiles share. So a value loses bits beside one 2^24
+ * times as large that a row of the same call and sequence sees, and counts as 0 beside
+ * one 2^34 times as large. (f32 calls have fp32's range.)
  *
  * moe_attn_decode: the newest n_q (1..8) tokens of each of n sequences; rows
  * i*n_q .. i*n_q+n_q-1 belong to seqs[i] (device int32 [n], n <= 65536), at
@@ -253,8 +257,8 @@ typedef struct {
 
 /* Draw one token of each row: the first, by index, up to which the kept weights
  * exceed u[row] times their sum. logits: device [rows][V] (zt MOE_F32 or MOE_BF16),
- * rows ld elements apart (0: one row for all), aligned to their type; 1 <= V <= 2^20. u: device [rows], in
- * [0, 1). token: device int32 [rows]; prob: device [rows], the token's share of the
+ * rows ld elements apart (0: one row for all), aligned to their type; 1 <= V <= 2^20.
+ * u: device [rows], in [0, 1). token: device int32 [rows]; prob: device [rows], the token's share of the
  * kept weight, or NULL. A NaN counts as -inf. Infinite logits share all the weight. A
  * row without a logit above -inf gets token -1 and probability 0. Weights are formed
  * to about 2^-31 of themselves, down to 2^-43 of the first, and added without
