@@ -18,22 +18,22 @@
 // logits are read once. With neither top-k nor top-p two passes follow: the weights'
 // sums of every warp's tokens, and the one warp's in which the token is. Else the end of
 // the prefix is looked for first:
-// - Bins of d, 1,024 of them, bound it. With top-k, by the threads' own largest logits:
-//   the k-th largest of them is no larger than the k-th of all. With top-p, by a
-//   histogram (tokens, weight) over the bins; tokens of less than (1 - top_p) / V of the
-//   weight, which all together are no more than what is cut off, are left out of it.
-// - If that leaves few tokens, as it mostly does, they go to the first CTA, and the
-//   others are done.
-// - Histograms follow, over the bins and then, within the bin that holds the end, over
-//   the place in the order, (logit, index) as one number, ten bits a round, until the
-//   end is decided: mostly one round. The first CTA does that by itself, if the bin's
-//   tokens fit into its list.
+// - With top-k, bins of d, 1,024 of them, bound it by the threads' own largest logits:
+//   the k-th largest of them is no larger than the k-th of all. If that leaves few
+//   tokens, as it mostly does, they go to the first CTA, and the others are done.
+// - Histograms (tokens, weight) follow, over the bins and then, within the bin that
+//   holds the end, over the place in the order, (logit, index) as one number, ten bits a
+//   round, until the end is decided: mostly one round. The first CTA does that by
+//   itself, if the bin's tokens, or all before its end, fit into its list. (Top-p's
+//   share is of the first histogram's total. A pass for the total alone, after which
+//   most tokens can be left out of the histogram, cost more: 64 rows 95 us, not 75.)
 //
 // What bounds it: few rows the latency of the passes and cluster barriers; many the
 // issue of the weights' arithmetic (some 40 instructions a token where all weights count;
-// two fp32 an instruction did not make it shorter). 131,072 fp32 logits: 20.8 us a row
-// with top-k and top-p, 36 with top-p alone; 64 such rows 37 us with neither, 48 with
-// top-k, 75 with settings of all kinds, 95 with top-p alone. Their reading takes 5.
+// two fp32 an instruction did not make it shorter) and the barriers. 131,072 fp32 logits:
+// 20.8 us a row with top-k and top-p, 32 with top-p alone; 64 such rows 37 us with
+// neither, 43 with top-k, 63 with settings of all kinds, 72 with top-p alone. Their
+// reading takes 5.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -88,7 +88,8 @@ struct SampleShared {
   unsigned long long found64;
   uint32_t top[kMostCtas];
   int found;
-  unsigned int listed[4], index;  // tokens listed by each gathering
+  unsigned int listed[4], index;  // tokens listed by each gathering: this CTA's, then the first one's all
+  unsigned int lists_of[4][kMostCtas];
   Search search;
   float c_hi, c_lo;
   Power power[257];
@@ -306,47 +307,46 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
     }
     return;
   }
-  auto share_sum = [&](unsigned long long v) {  // over the cluster
-    v = warp_sum(v);
-    if (lane == 0) sh.warp64[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-      v = warp_sum(lane < kSampleWarps ? sh.warp64[lane] : 0ull);
-      if (lane < C) *cluster.map_shared_rank(&sh.sum[rank], lane) = v;
-    }
-    cluster.sync();
-    v = 0;
-    for (int i = 0; i < C; ++i) v += sh.sum[i];
-    return v;
-  };
   auto tell = [&](auto* field, auto v) {  // every CTA, by the first one's first threads
     if (tid < C) *cluster.map_shared_rank(field, tid) = v;
   };
-  // The tokens of bins low .. most into the first CTA's list. Whether they all fitted.
+  // The tokens of bins low .. most into the first CTA's list, by way of each CTA's own.
+  // Whether they all fitted.
   auto gather = [&](int low, int most) -> bool {
     auto value = [&](int j) {
       return j < n_mine ? static_cast<float>(w0 + j < a.staged ? held[w0 + j] : raw_logit<T>(a, row, slice0 + w0 + j)) : -INFINITY;
     };
-    unsigned int n = 0;
+    unsigned int* const mine_n = &sh.listed[lists];
 #pragma unroll 4
     for (int j0 = 0; j0 < n_mine; j0 += 32) {
-      const int b = r.bin(value(j0 + lane));
-      n += __popc(__ballot_sync(~0u, b >= low && b <= most));
-    }
-    unsigned int at = 0;
-    if (n > 0 && lane < C) at = atomicAdd(&cluster.map_shared_rank(&sh, lane)->listed[lists], n);  // (every CTA counts along)
-    at = __shfl_sync(~0u, at, 0);
-    if (n > 0 && at + n <= kList)
-      for (int j0 = 0; j0 < n_mine; j0 += 32) {
-        const float z = value(j0 + lane);
-        const int b = r.bin(z);
-        const bool in = b >= low && b <= most;
-        const unsigned int all = __ballot_sync(~0u, in);
-        if (in) lead.list[at + __popc(all & ((1u << lane) - 1u))] = place(z, slice0 + w0 + j0 + lane);
-        at += __popc(all);
+      const float z = value(j0 + lane);
+      const int b = r.bin(z);
+      const bool in = b >= low && b <= most;
+      const unsigned int all = __ballot_sync(~0u, in);
+      if (all) {
+        unsigned int at = 0;
+        if (lane == 0) at = atomicAdd(mine_n, __popc(all));
+        at = __shfl_sync(~0u, at, 0) + __popc(all & ((1u << lane) - 1u));
+        if (in && at < kList) sh.list[at] = place(z, slice0 + w0 + j0 + lane);
       }
+    }
+    __syncthreads();
+    const unsigned int n = *mine_n;
+    if (tid < C) cluster.map_shared_rank(&sh, tid)->lists_of[lists][rank] = n;
     cluster.sync();
-    return sh.listed[lists++] <= kList;
+    unsigned int total = 0, before = 0;
+    for (int i = 0; i < C; ++i) {
+      const unsigned int m = sh.lists_of[lists][i];
+      if (i < rank) before += m;
+      total += m;
+    }
+    const bool fit = total <= kList;
+    if (fit && rank > 0)
+      for (unsigned int i = tid; i < n; i += kSampleThreads) lead.list[before + i] = sh.list[i];
+    if (fit && rank == 0 && tid == 0) *mine_n = total;
+    ++lists;
+    if (fit) cluster.sync();
+    return fit;
   };
 
   int end_bin = kBins - 1;                   // kept: bin <= end_bin and place <= end
@@ -382,12 +382,6 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
         if (rank > 0) return;
         solo = true;
       }
-    } else {
-      unsigned long long v = 0;
-      each([&](float z, int) { v += r.weight(z); });
-      sum = share_sum(v);
-      const float d = log2f(static_cast<float>(a.V)) + static_cast<float>(kFraction) - log2f((1.f - fmaxf(top_p, 0.f)) * static_cast<float>(sum));
-      most = static_cast<int>(fminf(fmaxf(d * kBinsPer, 0.f) + 2.f, kBins - 1.f));
     }
     // ---- tokens and weight by bins of d
     each([&](float z, int) {
@@ -449,6 +443,12 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
           const unsigned long long sb = round == 0 ? 0ull : sh.search.before;
           const uint32_t n = nb + block_scan_incl(n0 + n1, sh.warp32);
           const unsigned long long s = sb + block_scan_incl(s0 + s1, sh.warp64);
+          if (round == 0 && by_weight && !k_on) {
+            if (tid == kSampleThreads - 1) sh.found64 = s;
+            __syncthreads();
+            sum = sh.found64;
+            goal = max(share_of(top_p, sum, true), 1ull);
+          }
           if (tid == 0) sh.found = 0;
           __syncthreads();
           // the bin in which the goal is reached
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
           sh.next.weight[i] = 0ull;
         }
         __syncthreads();
-        if (!solo && !k_on && q.kept <= kList) {  // few tokens up to the end's bin
+        if (!solo && !k_on && round == 0 && q.kept <= kList) {  // few tokens up to the end's bin
           if (gather(0, q.bin)) {
             if (rank > 0) return;
             solo = true;

@@ -132,6 +132,21 @@ def test_sample_ties(bec, dtype, V, kind):
             assert torch.allclose(prob, torch.full_like(prob, 1.0 / k), rtol=2.0 ** -23, atol=0)
 
 
+@pytest.mark.parametrize("V", [5000, 60000])
+@pytest.mark.parametrize("steps", [3, 700, 200000])
+def test_sample_thousands_of_near_ties(bec, V, steps):
+    """Logits a few last bits apart: the end lies among thousands of tokens of one bin, and is looked for round by round."""
+    rng = np.random.default_rng(V + steps)
+    ulp = rng.integers(0, steps, (12, V))
+    z = torch.from_numpy((np.float32(1.0) + ulp.astype(np.float32) * np.float32(2.0 ** -23)).astype(np.float32)).cuda()
+    u = torch.from_numpy(rng.uniform(0, 1, 12).astype(np.float32)).cuda()
+    p = torch.tensor([0.001, 0.01, 0.03, 0.3, 0.5, 0.9, 0.99, 0.9999, 1.0, 0.02, 0.6, 0.5], device="cuda")
+    check(bec, z, u, top_p=p)
+    k = torch.tensor([0, 1, 2, 900, 2047, 2048, 2049, 4000, V - 1, V, 3000, 1000], device="cuda", dtype=torch.int32)
+    check(bec, z, u, top_k=k)
+    check(bec, z, u, 0.5, top_k=k, top_p=p)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("V", [70, 20000])
 def test_sample_infinities_and_nan(bec, dtype, V):
