@@ -20,7 +20,8 @@
 // the prefix is looked for first:
 // - With top-k, bins of d, 1,024 of them, bound it by the threads' own largest logits:
 //   the k-th largest of them is no larger than the k-th of all. If that leaves few
-//   tokens, as it mostly does, they go to the first CTA, and the others are done.
+//   tokens, as it mostly does, they go to the first CTA, and the others are done. Of a
+//   few hundred that CTA counts each one's place among them, and needs no search.
 // - Histograms (tokens, weight) follow, over the bins and then, within the bin that
 //   holds the end, over the place in the order, (logit, index) as one number, ten bits a
 //   round, until the end is decided: mostly one round. The first CTA does that by
@@ -31,9 +32,9 @@
 // What bounds it: few rows the latency of the passes and cluster barriers; many the
 // issue of the weights' arithmetic (some 40 instructions a token where all weights count;
 // two fp32 an instruction did not make it shorter) and the barriers. 131,072 fp32 logits:
-// 20.8 us a row with top-k and top-p, 32 with top-p alone; 64 such rows 37 us with
-// neither, 43 with top-k, 63 with settings of all kinds, 72 with top-p alone. Their
-// reading takes 5.
+// a row with top-k 50 and top-p 12.3 us in a captured graph, with top-p alone 30; 64 such
+// rows 37 us with neither, 35 with top-k 50, 62 with settings of all kinds, 72 with top-p
+// alone. Their reading takes 5.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -47,7 +48,7 @@ namespace moe {
 namespace {
 
 constexpr int kSampleThreads = 512, kSampleWarps = kSampleThreads / 32;
-constexpr int kBins = 1024, kMostCtas = 16, kList = 2048;
+constexpr int kBins = 1024, kMostCtas = 16, kList = 2048, kFew = 256;
 constexpr int kFraction = 43;  // weights are whole numbers of 2^-43
 constexpr float kReach = 44.f;  // weights from here on are none
 constexpr float kBinsPer = kBins / kReach;
@@ -80,7 +81,7 @@ struct Search {
 struct SampleShared {
   Hist first, next;
   alignas(16) uint32_t maxima[kBins];
-  unsigned long long list[kList];
+  alignas(16) unsigned long long list[kList];
   unsigned long long chunk[kMostCtas * kSampleWarps];
   unsigned long long sum[kMostCtas];
   unsigned long long warp64[kSampleWarps];
@@ -349,6 +350,58 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
     return fit;
   };
 
+  auto least_weight = [&]() {  // by min-p
+    return min_p > 0.f ? static_cast<unsigned long long>(ceil(fmin(static_cast<double>(min_p), 1.0) * static_cast<double>(1ull << kFraction))) : 0ull;
+  };
+  auto drawn = [&](int i, unsigned long long w, unsigned long long total) {
+    a.token[row] = i;
+    if (a.prob) a.prob[row] = static_cast<float>(static_cast<double>(w) / static_cast<double>(total));
+  };
+  auto goal_of = [&](unsigned long long total) {  // the first sum above it
+    return min(u < 1.f ? share_of(u, total, false) : ~0ull, total - 1);
+  };
+  // The rest, by the first CTA, of a short list of all tokens up to the end or more, one
+  // a thread: each counts the tokens before its own, in the order and by index. sum: all
+  // weight, where there is no top-k. (64 rows of 131,072 with top-k 50: 35 us, with the
+  // searches below 43; top-k 200, 42 and 45; 300, in lists of up to 512, 50 and 46.)
+  auto few = [&](unsigned long long sum) {
+    const int n = static_cast<int>(sh.listed[lists - 1]);
+    const unsigned long long mine = tid < n ? sh.list[tid] : ~0ull;
+    const uint32_t index = static_cast<uint32_t>(mine) & ((1u << kIndexBits) - 1);
+    if (tid < 8) sh.list[n + tid] = ~0ull;  // (before no token, in either way)
+    __syncthreads();
+    int at = 0, by_index = 0;
+    if (tid < n)
+      for (int j = 0; j < n; j += 8)
+#pragma unroll
+        for (int x = 0; x < 8; x += 2) {
+          const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&sh.list[j + x]);
+          at += (o.x < mine) + (o.y < mine);
+          by_index += ((static_cast<uint32_t>(o.x) & ((1u << kIndexBits) - 1)) < index) +
+                      ((static_cast<uint32_t>(o.y) & ((1u << kIndexBits) - 1)) < index);
+        }
+    const unsigned long long w = tid < n && !(k_on && at >= top_k) ? r.weight(logit_of(mine)) : 0ull;
+    if (tid < n) sh.first.weight[at] = w;
+    __syncthreads();
+    const unsigned long long v = tid < n ? sh.first.weight[tid] : 0ull, upto = block_scan_incl(v, sh.warp64);
+    if (tid < n) sh.first.weight[tid] = upto - v;
+    if (tid == kSampleThreads - 1) sh.found64 = upto;
+    __syncthreads();
+    if (k_on) sum = sh.found64;
+    const unsigned long long end = p_on ? max(share_of(top_p, sum, true), 1ull) : ~0ull;
+    const bool in = tid < n && w >= least_weight() && sh.first.weight[at] < end;
+    if (tid < n) {
+      sh.next.weight[by_index] = in ? w : 0ull;
+      sh.next.count[by_index] = index;
+    }
+    __syncthreads();
+    const unsigned long long x = tid < n ? sh.next.weight[tid] : 0ull, sums = block_scan_incl(x, sh.warp64);
+    if (tid == kSampleThreads - 1) sh.found64 = sums;
+    __syncthreads();
+    const unsigned long long total = sh.found64, goal = goal_of(total);
+    if (goal < sums && goal >= sums - x) drawn(static_cast<int>(sh.next.count[tid]), x, total);
+  };
+
   int end_bin = kBins - 1;                   // kept: bin <= end_bin and place <= end
   unsigned long long end = ~0ull;
   if (k_on || p_on) {
@@ -380,6 +433,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
       most = sh.found;
       if (gather(0, most)) {
         if (rank > 0) return;
+        if (sh.listed[lists - 1] <= kFew) return few(0);
         solo = true;
       }
     }
@@ -514,6 +568,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
         if (!solo && !k_on && round == 0 && q.kept <= kList) {  // few tokens up to the end's bin
           if (gather(0, q.bin)) {
             if (rank > 0) return;
+            if (sh.listed[lists - 1] <= kFew) return few(sum);
             solo = true;
           }
         }
@@ -554,8 +609,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
   }
 
   // ---- weights kept, in the order of the vocabulary
-  const unsigned long long least =
-      min_p > 0.f ? static_cast<unsigned long long>(ceil(fmin(static_cast<double>(min_p), 1.0) * static_cast<double>(1ull << kFraction))) : 0ull;
+  const unsigned long long least = least_weight();
   const bool cut = end != ~0ull;
   auto kept = [&](float z, int i) -> unsigned long long {
     if (cut) {
@@ -564,13 +618,6 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
     }
     const unsigned long long w = r.weight(z);
     return w >= least ? w : 0ull;
-  };
-  auto drawn = [&](int i, unsigned long long w, unsigned long long total) {
-    a.token[row] = i;
-    if (a.prob) a.prob[row] = static_cast<float>(static_cast<double>(w) / static_cast<double>(total));
-  };
-  auto goal_of = [&](unsigned long long total) {  // the first sum above it
-    return min(u < 1.f ? share_of(u, total, false) : ~0ull, total - 1);
   };
   if (solo) {
     // by index: 1,024 stretches of the vocabulary, then the tokens of one of them

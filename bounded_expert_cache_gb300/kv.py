@@ -385,6 +385,15 @@ def quant_linear(x: torch.Tensor, w: torch.Tensor, quant: int, n_out: int, bias:
     return y
 
 
+def _column(t: torch.Tensor, name: str, dtype: torch.dtype, rows: int, device: int) -> int:
+    """Address of one value a row."""
+    if t.dtype != dtype or t.shape != (rows,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {rows} entries")
+    if t.get_device() != device:
+        raise _elsewhere(t, name, device)
+    return t.data_ptr()
+
+
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=None, prob=None,
            stream=None):
     """Draw one token of each row of logits [rows, V] (float32 or bfloat16, rows may lie apart) with u [rows] in [0, 1).
@@ -395,29 +404,35 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     The token is the first, by index, up to which their weights exceed u times the sum.
     Returns (token int32 [rows], prob float32 [rows]), new ones if None.
     """
-    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    if logits.dim() != 2 or not logits.is_cuda:
         raise ValueError("logits must be a [rows, V] CUDA tensor with dense rows")
     zt = _dtype_id(logits.dtype)
     device = logits.get_device()
     rows, V = logits.shape
-
-    def column(t, name, dtype):
-        if t.dtype != dtype or t.dim() != 1 or t.shape[0] != rows or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {rows} entries")
-        if t.get_device() != device:
-            raise _elsewhere(t, name, device)
-        return t.data_ptr()
-
+    ld, one = logits.stride()
+    if one != 1 and V > 1:
+        raise ValueError("logits must be a [rows, V] CUDA tensor with dense rows")
     by = N.SamplingT()
-    for value, name, dtype in ((temperature, "temperature", torch.float32), (top_p, "top_p", torch.float32),
-                               (min_p, "min_p", torch.float32), (top_k, "top_k", torch.int32)):
-        if hasattr(value, "data_ptr"):
-            setattr(by, name + "s", column(value, name, dtype))
-        else:
-            setattr(by, name, min(max(int(value), 0), _MOST) if name == "top_k" else float(value))
+    if hasattr(temperature, "data_ptr"):
+        by.temperatures = _column(temperature, "temperature", torch.float32, rows, device)
+    else:
+        by.temperature = float(temperature)
+    if hasattr(top_k, "data_ptr"):
+        by.top_ks = _column(top_k, "top_k", torch.int32, rows, device)
+    else:
+        by.top_k = min(max(int(top_k), 0), _MOST)
+    if hasattr(top_p, "data_ptr"):
+        by.top_ps = _column(top_p, "top_p", torch.float32, rows, device)
+    else:
+        by.top_p = float(top_p)
+    if hasattr(min_p, "data_ptr"):
+        by.min_ps = _column(min_p, "min_p", torch.float32, rows, device)
+    else:
+        by.min_p = float(min_p)
+    at = _column(u, "u", torch.float32, rows, device)
     token = _new((rows,), torch.int32, logits.device, stream) if token is None else token
     prob = _new((rows,), torch.float32, logits.device, stream) if prob is None else prob
-    _run(device, lib.moe_sample, logits.data_ptr(), zt, logits.stride(0) if rows > 1 else V, rows, V,
-         column(u, "u", torch.float32), C.byref(by), column(token, "token", torch.int32), column(prob, "prob", torch.float32),
+    _run(device, lib.moe_sample, logits.data_ptr(), zt, ld if rows > 1 else V, rows, V, at, C.byref(by),
+         _column(token, "token", torch.int32, rows, device), _column(prob, "prob", torch.float32, rows, device),
          _raw_stream(device) if stream is None else stream.cuda_stream)
     return token, prob
