@@ -251,3 +251,11 @@ def test_sample_refusals(native, change, why):  # noqa: F811
 
 def test_sample_of_no_rows_is_no_work(native):  # noqa: F811
     assert native.lib.moe_sample(None, 0, 0, 0, 5, None, C.byref(native.SamplingT()), None, None, None) == 0
+
+
+@pytest.mark.parametrize("magnitude,fine", [(1e39, False), (-math.inf, False), (3e38, True), (-0.5, True)])
+def test_magnitude_must_be_finite_in_fp32(native, magnitude, fine):  # noqa: F811
+    rot = native.RotaryT(4096, 8, 0, magnitude)
+    st = native.lib.moe_rotary(C.byref(rot), None, None, 0, 0, 0, 1, 8, None, 0, None)
+    assert (st == 0) == fine
+    assert fine or b"magnitude" in native.lib.moe_last_error(None)
