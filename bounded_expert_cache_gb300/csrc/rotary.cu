@@ -26,7 +26,7 @@
 // overwrite its input. 16,384 rows of 40 bf16 heads of 128: 56 us, 5.9 TB/s, halves or
 // neighbours. Blocks of 256 threads with 32 registers, eight on an SM: with 40 registers
 // and the next item read ahead 68. 7,591 rows of ragged prompts, 32 + 2 x 8 heads of 128
-// into 4-bit pages, and these values read back: 65 us, of which q's heads (124 MB) take
+// into 4-bit pages, and these values read back: 64 us, of which q's heads (124 MB) take
 // 18, near HBM's rate; the codes, the values read back and the lookups are bound by
 // instructions.
 #include <cuda_bf16.h>
@@ -529,7 +529,25 @@ __device__ __forceinline__ float one_of(int j) { return __uint_as_float(0x4B0000
 __device__ __forceinline__ float code_in(uint32_t w, int j) {
   return __uint_as_float((w & (15u << (4 * j))) | (0x4B000000u - (j << 25)));
 }
-// The newest tokens of sequences out of their pages, eight values a thread.
+// the values of a word of codes
+template <class T>
+__device__ __forceinline__ void store_values(T* to, uint32_t c, float s, float b) {
+  float v[8];
+  // a code in its place in the fraction of 2^(23 - 4 j) adds the code to it
+  const uint32_t c5 = c >> 20;
+  const F2 ss = f2(s, s), bb = f2(b, b);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const int j0 = j < 5 ? j : j - 5, j1 = j < 4 ? j + 1 : j - 4;
+    const F2 u = f2(code_in(j < 5 ? c : c5, j0), code_in(j < 4 ? c : c5, j1));
+    const float2 x = both(fma2(add2(u, f2(-one_of(j0), -one_of(j1))), ss, bb));
+    v[j] = x.x;
+    v[j + 1] = x.y;
+  }
+  store8<T>(to, v);
+}
+// The newest tokens of sequences out of their pages, eight values a thread, or
+// sixteen codes (of the 64 us above two less than with eight).
 template <class T, bool CODES>
 __global__ void __launch_bounds__(kRotThreads) read_kernel(const WriteArgs a) {
   __shared__ int s_pos[kMostRows], s_page[kMostRows];
@@ -552,33 +570,23 @@ __global__ void __launch_bounds__(kRotThreads) read_kernel(const WriteArgs a) {
   const int2 hs = share(a.H);
   const int heads = hs.y - hs.x;
   if (heads == 0) return;
-  for (Walk w(2 * heads, a.D / 8); w.r < rows; w.next()) {
+  constexpr int kItem = CODES ? 16 : 8;  // values
+  for (Walk w(2 * heads, a.D / kItem); w.r < rows; w.next()) {
     if (s_page[w.r] < 0) continue;
     const bool is_v = w.h >= heads;
     const int h = hs.x + w.h - (is_v ? heads : 0);
     const char* pages = static_cast<const char*>(is_v ? a.pv : a.pk);
     const int64_t block = static_cast<int64_t>(s_page[w.r]) * a.H + h;
     const int place = s_pos[w.r] & (kv.page - 1);
-    T* to = static_cast<T*>(const_cast<void*>(is_v ? a.v : a.k)) + (row0 + w.r) * (is_v ? a.ldv : a.ldk) + h * a.D + 8 * w.i;
+    T* to = static_cast<T*>(const_cast<void*>(is_v ? a.v : a.k)) + (row0 + w.r) * (is_v ? a.ldv : a.ldk) + h * a.D + kItem * w.i;
     if constexpr (CODES) {
-      float v[8];
       const int row_bytes = a.D / 2, meta_bytes = a.D / 16;
       const char* from = pages + ((block * (row_bytes + meta_bytes)) << kv.page_shift);
-      const uint32_t c = *reinterpret_cast<const uint32_t*>(from + place * row_bytes + 4 * w.i);
-      const uint32_t m = *reinterpret_cast<const uint32_t*>(from + (row_bytes << kv.page_shift) + place * meta_bytes + w.i / 8 * 4);
+      const uint2 c = *reinterpret_cast<const uint2*>(from + place * row_bytes + 8 * w.i);
+      const uint32_t m = *reinterpret_cast<const uint32_t*>(from + (row_bytes << kv.page_shift) + place * meta_bytes + w.i / 4 * 4);
       const float s = __uint_as_float(m << 16), b = __uint_as_float(m & 0xFFFF0000u);
-      // a code in its place in the fraction of 2^(23 - 4 j) adds the code to it
-      const uint32_t c5 = c >> 20;
-      const F2 ss = f2(s, s), bb = f2(b, b);
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        const float2 u = make_float2(code_in(j < 5 ? c : c5, j < 5 ? j : j - 5), code_in(j < 4 ? c : c5, j < 4 ? j + 1 : j - 4));
-        const float2 o = make_float2(-one_of(j < 5 ? j : j - 5), -one_of(j < 4 ? j + 1 : j - 4));
-        const float2 x = both(fma2(add2(f2(u.x, u.y), f2(o.x, o.y)), ss, bb));
-        v[j] = x.x;
-        v[j + 1] = x.y;
-      }
-      store8<T>(to, v);
+      store_values<T>(to, c.x, s, b);
+      store_values<T>(to + 8, c.y, s, b);
     } else {
       const T* from = reinterpret_cast<const T*>(pages) + ((block << kv.page_shift) + place) * a.D + 8 * w.i;
 #pragma unroll
