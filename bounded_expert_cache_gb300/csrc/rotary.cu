@@ -14,7 +14,7 @@
 // done one by one, where a last bit's difference puts a few in a million on the other
 // side of a border between two codes. (sincospif and fused products: the same times.)
 //
-// Pages of 4-bit codes: eight threads hold a group of 64 values; with lo and hi its
+// Pages of 4-bit codes: four threads hold a group of 64 values; with lo and hi its
 // least and largest, b = bf16(lo), s = bf16((hi - b) (1 / 15)), q = round((x - b) / s)
 // within 0..15 (0 where s is 0), in fp32 as in IEEE. A group with an
 // infinity, a NaN or a magnitude above 2^126 becomes NaN as a whole.
@@ -26,7 +26,7 @@
 // overwrite its input. 16,384 rows of 40 bf16 heads of 128: 56 us, 5.9 TB/s, halves or
 // neighbours. Blocks of 256 threads with 32 registers, eight on an SM: with 40 registers
 // and the next item read ahead 68. 7,591 rows of ragged prompts, 32 + 2 x 8 heads of 128
-// into 4-bit pages, and these values read back: 64 us, of which q's heads (124 MB) take
+// into 4-bit pages, and these values read back: 60 us, of which q's heads (124 MB) take
 // 18, near HBM's rate; the codes, the values read back and the lookups are bound by
 // instructions.
 #include <cuda_bf16.h>
@@ -393,30 +393,30 @@ __device__ __forceinline__ float most(float a, float b) {
   return r;
 }
 
-// The codes of eight values of a group that eight neighbouring lanes hold, and the
+// The codes of sixteen values of a group that four neighbouring lanes hold, and the
 // group's scale and offset as one word.
 // A code is d / s rounded to the nearest whole number, to the even one of two as near,
 // with d = v - b. A division for each takes more time (77 us against 68 in all for the
 // prompts above): n is rounded from d / s less 2^-20 of it, so it is the code or the whole number below, and the code
 // is above if d - n s is more than s / 2, or as much and n is odd. That remainder is
 // exact: it is a multiple of d's or s's last place, and s has eight bits.
-__device__ __forceinline__ uint32_t quantised(const float* v, uint32_t* meta) {
-  const unsigned int lanes = 0xFFu << (threadIdx.x & 24);
+__device__ __forceinline__ uint2 quantised(const float* v, uint32_t* meta) {
+  const unsigned int lanes = 0xFu << (threadIdx.x & 28);
   constexpr float kMost = 0x1p126f, kWhole = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
   float lo = v[0], hi = v[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
+  for (int i = 1; i < 16; ++i) {
     lo = least(lo, v[i]);
     hi = most(hi, v[i]);
   }
 #pragma unroll
-  for (int x = 1; x < 8; x <<= 1) {
+  for (int x = 1; x < 4; x <<= 1) {
     lo = least(lo, __shfl_xor_sync(lanes, lo, x));
     hi = most(hi, __shfl_xor_sync(lanes, hi, x));
   }
   if (!(lo >= -kMost && hi <= kMost)) {
     *meta = 0x7FC07FC0u;
-    return 0u;
+    return make_uint2(0u, 0u);
   }
   const __nv_bfloat16 b16 = __float2bfloat16_rn(lo);
   const float b = __bfloat162float(b16);
@@ -424,29 +424,32 @@ __device__ __forceinline__ uint32_t quantised(const float* v, uint32_t* meta) {
   const float s = __bfloat162float(s16);
   const uint32_t offset = static_cast<uint32_t>(__bfloat16_as_ushort(b16)) << 16;
   *meta = offset;
-  if (!(s > 0.f)) return 0u;
+  if (!(s > 0.f)) return make_uint2(0u, 0u);
   *meta = offset | __bfloat16_as_ushort(s16);
-  uint32_t w = 0;
+  uint32_t w[2] = {0u, 0u};
   if (s < 0x1p-100f) {  // (1 / s may be infinite, and s be short of bits)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w |= static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(v[i] - b, s)), 0.f), 15.f)) << (4 * i);
-    return w;
+    for (int i = 0; i < 8; ++i) {
+      w[0] |= static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(v[i] - b, s)), 0.f), 15.f)) << (4 * i);
+      w[1] |= static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(v[8 + i] - b, s)), 0.f), 15.f)) << (4 * i);
+    }
+    return make_uint2(w[0], w[1]);
   }
   const float inv = __frcp_rn(s) * (1.f - 0x1p-20f);
   const int half = __float_as_int(0.5f * s);
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
+  for (int i = 0; i < 16; i += 2) {
     const float2 d = both(add2(f2(v[i], v[i + 1]), f2(-b, -b)));
     const F2 dd = f2(fmaxf(d.x, 0.f), fmaxf(d.y, 0.f)), mm = fma2(dd, f2(inv, inv), f2(kWhole, kWhole));
     const float2 m = both(mm), rest = both(fma2(add2(mm, f2(-kWhole, -kWhole)), f2(-s, -s), dd));
     int n0 = __float_as_int(m.x), n1 = __float_as_int(m.y);
     if (__float_as_int(rest.x) + (n0 & 1) > half) ++n0;  // (a negative rest is a negative integer)
     if (__float_as_int(rest.y) + (n1 & 1) > half) ++n1;
-    w += static_cast<uint32_t>(n0) << (4 * i);  // n is 0x4B400000 and the code, at most 15
-    w += static_cast<uint32_t>(n1) << (4 * i + 4);
+    w[i / 8] += static_cast<uint32_t>(n0) << (4 * (i & 7));  // n is 0x4B400000 and the code, at most 15
+    w[i / 8] += static_cast<uint32_t>(n1) << (4 * (i & 7) + 4);
   }
-  return w - 0x4B400000u * 0x11111111u;
+  constexpr uint32_t kRaised = 0x4B400000u * 0x11111111u;
+  return make_uint2(w[0] - kRaised, w[1] - kRaised);
 }
 
 struct WriteArgs {
@@ -461,9 +464,11 @@ struct WriteArgs {
 };
 
 // A warp a row finds its place, then q's heads are turned and k and v are stored,
-// eight values a thread at a time: items of k's heads, then of v's.
+// eight values a thread at a time, or for codes sixteen: items of k's heads, then of
+// v's. (Sixteen need 48 registers, five blocks on an SM: 60 us for the prompts above;
+// with six blocks 61, with eight 63, as with eight values.)
 template <class T, bool CODES>
-__global__ void __launch_bounds__(kRotThreads, 8) write_rotary_kernel(const WriteArgs a) {
+__global__ void __launch_bounds__(kRotThreads, CODES ? 5 : 8) write_rotary_kernel(const WriteArgs a) {
   extern __shared__ __align__(16) float cs[];
   __shared__ int ok[kMostRows], s_pos[kMostRows], s_page[kMostRows];
   __shared__ float4 table[256];
@@ -499,25 +504,30 @@ __global__ void __launch_bounds__(kRotThreads, 8) write_rotary_kernel(const Writ
   const int2 hs = share(a.H);
   const int heads = hs.y - hs.x;
   if (heads == 0) return;
-  for (Walk w(2 * heads, a.D / 8); w.r < rows; w.next()) {
+  constexpr int kItem = CODES ? 16 : 8;  // values
+  for (Walk w(2 * heads, a.D / kItem); w.r < rows; w.next()) {
     if (!ok[w.r]) continue;  // (a group's lanes are of one row)
     const bool is_v = w.h >= heads;
     const T* from = static_cast<const T*>(is_v ? a.v : a.k) + (row0 + w.r) * (is_v ? a.ldv : a.ldk) +
                     (hs.x + w.h - (is_v ? heads : 0)) * a.D;
-    float v[8];
-    load8<T>(from + 8 * w.i, v);
-    if (!is_v) turn8<T>(from, w.i, a.rot, cs + w.r * 2 * half, v);
+    float v[kItem];
+#pragma unroll
+    for (int j = 0; j < kItem / 8; ++j) {
+      const int octet = w.i * (kItem / 8) + j;
+      load8<T>(from + 8 * octet, v + 8 * j);
+      if (!is_v) turn8<T>(from, octet, a.rot, cs + w.r * 2 * half, v + 8 * j);
+    }
     char* pages = static_cast<char*>(is_v ? a.pv : a.pk);
     const int64_t block = static_cast<int64_t>(s_page[w.r]) * a.H + hs.x + w.h - (is_v ? heads : 0);
     const int place = s_pos[w.r] & (kv.page - 1);
     if constexpr (CODES) {
       uint32_t meta;
-      const uint32_t codes = quantised(v, &meta);
+      const uint2 codes = quantised(v, &meta);
       const int row_bytes = a.D / 2, meta_bytes = a.D / 16;
       char* to = pages + ((block * (row_bytes + meta_bytes)) << kv.page_shift);
-      *reinterpret_cast<uint32_t*>(to + place * row_bytes + 4 * w.i) = codes;
-      if ((w.i & 7) == 0)
-        *reinterpret_cast<uint32_t*>(to + (row_bytes << kv.page_shift) + place * meta_bytes + w.i / 2) = meta;
+      *reinterpret_cast<uint2*>(to + place * row_bytes + 8 * w.i) = codes;
+      if ((w.i & 3) == 0)
+        *reinterpret_cast<uint32_t*>(to + (row_bytes << kv.page_shift) + place * meta_bytes + w.i) = meta;
     } else {
       store8<T>(reinterpret_cast<T*>(pages) + ((block << kv.page_shift) + place) * a.D + 8 * w.i, v);
     }
@@ -547,7 +557,7 @@ __device__ __forceinline__ void store_values(T* to, uint32_t c, float s, float b
   store8<T>(to, v);
 }
 // The newest tokens of sequences out of their pages, eight values a thread, or
-// sixteen codes (of the 64 us above two less than with eight).
+// sixteen codes (of the 60 us above two less than with eight).
 template <class T, bool CODES>
 __global__ void __launch_bounds__(kRotThreads) read_kernel(const WriteArgs a) {
   __shared__ int s_pos[kMostRows], s_page[kMostRows];
