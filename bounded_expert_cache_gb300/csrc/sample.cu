@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
   SampleShared& sh = *reinterpret_cast<SampleShared*>(sm_raw);
   T* const held = reinterpret_cast<T*>(sm_raw + sizeof(SampleShared));
   auto cluster = cg::this_cluster();
+  cluster.barrier_arrive();  // that it runs, for the first access of another CTA to its shared memory
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int row = blockIdx.x / C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -251,6 +252,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
     }
     uint32_t k = __reduce_max_sync(~0u, order_key(mine));
     if (lane == 0) sh.warp32[warp] = k;
+    cluster.barrier_wait();  // every CTA of the cluster has started (one with an empty slice is here before others are)
     __syncthreads();
     if (warp == 0) {
       k = __reduce_max_sync(~0u, lane < kSampleWarps ? sh.warp32[lane] : 0u);
