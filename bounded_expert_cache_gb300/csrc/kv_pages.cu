@@ -139,7 +139,8 @@ __device__ __forceinline__ int count_free(const Kv& kv, Strip s, int lane) {
   for (int p0 = s.first; p0 < s.last; p0 += 32) c += p0 + lane < s.last && kv.ref[p0 + lane] == 0;
   return __reduce_add_sync(~0u, c);
 }
-// Give every CTA of the cluster every warp's count.
+// Give every CTA of the cluster every warp's count. (Each of them has to have started:
+// a barrier that a kernel arrives at first and waits for before its first call of this.)
 __device__ __forceinline__ void share_counts(cg::cluster_group& cluster, int* counts, int w, int lane, int c) {
   if (lane < kCtas) *cluster.map_shared_rank(counts + w, lane) = c;
   cluster.sync();
@@ -189,6 +190,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
   __shared__ int counts[kAllWarps];
   __shared__ uint32_t scan[kWarps];
   auto cluster = cg::this_cluster();
+  cluster.barrier_arrive();
   const int tid = threadIdx.x, rank = cluster.block_rank(), lane = tid & 31;
   const int w = rank * kWarps + (tid >> 5);
   for (int i = tid; i < kBitmapWords; i += kThreads) bits[i] = 0u;
@@ -218,6 +220,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
   room = __syncthreads_and(room);
   const Strip st = strip_of(kv.P, w);
   const int mine = count_free(kv, st, lane);
+  cluster.barrier_wait();
   share_counts(cluster, counts, w, lane, mine);  // also publishes shr and last
   // requests of every listed sequence
   int64_t wanted = 0;  // pages
@@ -359,11 +362,13 @@ __global__ void __launch_bounds__(256)
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) compact_kernel(Kv kv) {
   __shared__ int counts[kAllWarps], below[kAllWarps];
   auto cluster = cg::this_cluster();
+  cluster.barrier_arrive();
   const int tid = threadIdx.x, rank = cluster.block_rank(), lane = tid & 31;
   const int w = rank * kWarps + (tid >> 5);
   const bool stop = pending(kv);
   const Strip st = strip_of(kv.P, w);
   const int free_mine = count_free(kv, st, lane);
+  cluster.barrier_wait();
   share_counts(cluster, counts, w, lane, free_mine);
   const int2 pre = prefix_of(counts, w, lane);
   const int live = kv.P - pre.y;

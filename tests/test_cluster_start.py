@@ -26,7 +26,7 @@ def before_remote_accesses(source):
     return found
 
 
-@pytest.mark.parametrize("source,kernels", [("sample.cu", {"sample_kernel"})])
+@pytest.mark.parametrize("source,kernels", [("sample.cu", {"sample_kernel"}), ("kv_pages.cu", {"reserve_kernel", "compact_kernel"})])
 def test_a_cluster_has_started_before_its_shared_memory_is_accessed(source, kernels):
     found = before_remote_accesses(source)
     assert set(found) == kernels
