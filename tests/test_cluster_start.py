@@ -19,8 +19,8 @@ def before_remote_accesses(source):
                if "map_shared_rank" in m.group(2)]
     found = {}
     for body in kernels:
-        at = [m.start() for name in ["map_shared_rank"] + helpers for m in re.finditer(rf"\b{name}\(", body)
-              if not body[:m.start()].rstrip().endswith(("void", "bool", "int"))]
+        body = body.split("\n}\n")[0]
+        at = [m.start() for name in ["map_shared_rank"] + helpers for m in re.finditer(rf"\b{name}\(", body)]
         if at:
             found[re.search(r"\b(\w+_kernel)\(", body).group(1)] = body[:min(at)]
     return found
