@@ -498,11 +498,12 @@ __device__ __forceinline__ void fill_tiles(const AttnArgs& a, Walk w, Sh& sh, ui
   };
   RingPos kp, vp, rp;
   uint32_t n = 0;  // tiles filled
+  // The warps meet at barriers without a limit, so they leave together: one whose wait has
+  // failed does no more work, but comes to the next tile's meeting, where all learn of it.
   bool ok = true;
   auto wait = [&](uint64_t* b, uint32_t ph) {
     ok = ok && mbar_wait(su32(b), ph, abort_flag, a.err, a.wait_cycles);
     ok = __all_sync(~0u, ok);
-    return ok;
   };
   auto tell = [&](uint64_t* b) {
     __syncwarp();
@@ -514,7 +515,9 @@ __device__ __forceinline__ void fill_tiles(const AttnArgs& a, Walk w, Sh& sh, ui
     for (int j = 0; j < w.nt; ++j) {
       RingPos next = rp;
       next.next(C::kRS);
-      if (!wait(&sh.rf[rp.s], rp.ph) || !wait(&sh.rf[next.s], next.ph)) return;
+      wait(&sh.rf[rp.s], rp.ph);
+      wait(&sh.rf[next.s], next.ph);
+      if (any_of_fillers(!ok)) return;
       const uint32_t rk = raw + rp.s * C::kRaw, rv = raw + next.s * C::kRaw;
       const int tile0 = w.sp.tile(w.t0 + j) * kKT;
       // One thread a token looks at its scales and offsets.
@@ -568,17 +571,21 @@ __device__ __forceinline__ void fill_tiles(const AttnArgs& a, Walk w, Sh& sh, ui
         sh.powers[n & 7].k = exp2f(static_cast<float>(ke));
         sh.powers[n & 7].v = v_exp;
       }
-      if (n >= C::kKS && !wait(&sh.ke[kp.s], kp.ph ^ 1u)) return;
-      convert(rk, sk + kp.s * C::kTile, exp2f(static_cast<float>(-ke)));
-      fence_async_smem();
-      tell(&sh.kf[kp.s]);
-      tell(&sh.re[rp.s]);
+      if (n >= C::kKS) wait(&sh.ke[kp.s], kp.ph ^ 1u);
+      if (ok) {
+        convert(rk, sk + kp.s * C::kTile, exp2f(static_cast<float>(-ke)));
+        fence_async_smem();
+        tell(&sh.kf[kp.s]);
+        tell(&sh.re[rp.s]);
+      }
       kp.next(C::kKS);
-      if (n >= C::kVS && !wait(&sh.ve[vp.s], vp.ph ^ 1u)) return;
-      convert(rv, sv + vp.s * C::kTile, exp2f(static_cast<float>(-v_exp)));
-      fence_async_smem();
-      tell(&sh.vf[vp.s]);
-      tell(&sh.re[next.s]);
+      if (n >= C::kVS) wait(&sh.ve[vp.s], vp.ph ^ 1u);
+      if (ok) {
+        convert(rv, sv + vp.s * C::kTile, exp2f(static_cast<float>(-v_exp)));
+        fence_async_smem();
+        tell(&sh.vf[vp.s]);
+        tell(&sh.re[next.s]);
+      }
       vp.next(C::kVS);
       rp = next;
       rp.next(C::kRS);
