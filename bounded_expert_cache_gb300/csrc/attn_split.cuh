@@ -326,6 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kv = 0; kv < (E::kCodes ? 1 : 2); ++kv) {
         const uint32_t full = su32(&b_full[rp.s]);
         if (n >= NS && !mbar_wait(su32(&b_empty[rp.s]), rp.ph ^ 1u, &s_abort, a.err, a.wait_cycles)) ok = false;
+        // (computing warps whose wait has failed hand slots on whose copies may still be on their way)
+        if (*static_cast<volatile int*>(&s_abort)) ok = false;
         ok = __all_sync(~0u, ok);
         if (!ok) break;
         if (lane == 0) mbar_expect_tx(full, E::kCodes ? 2 * bytes : bytes);  // without pages the barrier completes by this arrival
