@@ -24,8 +24,8 @@ def run_out(bec, kv, call):
     kv.check_errors()
     ran_out = 0
     for cycles in (1, 100, 300, 500, 700, 1000, 1300, 1700, 2000, 2500, 3000, 4000, 6000, 9000, 15000, 40000):
-        for _ in range(3):
-            bec.KvCache.debug_attn_wait_timeout(cycles, 2 ** 31 - 1)
+        for copies in (2 ** 31 - 1, 7, 1, 0):
+            bec.KvCache.debug_attn_wait_timeout(cycles, copies)
             got = call()
             try:
                 kv.check_errors()
@@ -38,10 +38,9 @@ def run_out(bec, kv, call):
     kv.check_errors()
 
 
-def filled(bec, D, bits, g):
-    lens = [9000, 700, 70, 3000]
-    kv = bec.KvCache.empty(1, 1000, 2, 16, D, 4, 600, bits=bits)
-    seqs, cu = i32(range(4)), i32([0, 9000, 9700, 9770, 12770])
+def filled(bec, D, bits, g, lens):
+    kv = bec.KvCache.empty(1, sum(lens) // 16 + 4, 2, 16, D, 4, max(lens) // 16 + 1, bits=bits)
+    seqs, cu = i32(range(4)), i32([sum(lens[:i]) for i in range(5)])
     kv.reserve(seqs, i32(lens))
     x = torch.randn((sum(lens), 2, D), device="cuda", generator=g).to(BF16)
     kv.write(0, x, x.flip(0), seqs, cu)
@@ -53,7 +52,7 @@ def test_waits_of_a_few_cycles_in_prompt_chunks(bec, D, window):
     """Some warps' waits end in time and others' do not, of copies, of free slots, of scores. Warps that meet
     at a barrier have to come or leave together."""
     g = torch.Generator(device="cuda").manual_seed(D)
-    kv, seqs = filled(bec, D, 4, g)
+    kv, seqs = filled(bec, D, 4, g, [9000, 700, 70, 3000])
     ms = [300, 129, 70, 1500]
     q = torch.randn((sum(ms), 8, D), device="cuda", generator=g).to(BF16)
     qcu = i32([sum(ms[:i]) for i in range(5)])
@@ -66,6 +65,6 @@ def test_waits_of_a_few_cycles_in_decode(bec, D, bits, window):
     """Computing warps go on after a failed wait and free the slot: nothing may be copied into it while
     what they did not wait for is still on its way."""
     g = torch.Generator(device="cuda").manual_seed(D)
-    kv, seqs = filled(bec, D, bits, g)
+    kv, seqs = filled(bec, D, bits, g, [150000, 40000, 70, 3000])
     q = torch.randn((8, 8, D), device="cuda", generator=g).to(BF16)
     run_out(bec, kv, lambda: kv.attn_decode(0, q, seqs, 2, window=window))
