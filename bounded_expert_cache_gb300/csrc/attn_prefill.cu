@@ -222,13 +222,12 @@ struct Shared {
   uint32_t poison[8];  // ring over units: number + 1 of a unit with infinities or NaN taken out of V
   uint32_t tmem;
   int abort;
-  // codes: powers of two taken out of the last tiles of K (as the factor that makes
-  // up for it) and V (as exponent) and of the last units' Q, by their number
+  // codes: exponents of the powers of two taken out of the last tiles of K and V and of
+  // the last units' Q, by their number
   struct Powers {
-    float k;
-    int v;
+    int k, v;
   } powers[8];
-  float q_power[2][8];
+  int q_power[2][8];
   uint32_t fill_top[2][4];
 };
 template <int DP, bool APART, bool CODES>
@@ -375,6 +374,14 @@ constexpr float kHalfMost = 16384.f, kHalfLeast = 0x1p-8f;
 __device__ __forceinline__ int half_exponent(float top) {
   if (top == 0.f || (top <= kHalfMost && top >= kHalfLeast)) return 0;
   return max(-120, static_cast<int>(__float_as_uint(top) >> 23) - 127 - 10);  // (a denormal's is -137)
+}
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float two_to(int e) { return __int_as_float((e + 127) << 23); }
+// A score's factor, x times 2^e of Q's and K's exponents. In fp32's normal range: of 0 a hidden
+// score, -infinity, would become NaN, and of an infinity a score of 0. (Scores that small tell
+// no tokens apart either way.)
+__device__ __forceinline__ float score_factor(float x, int e) {
+  return fminf(fmaxf(x * two_to(e >> 1) * two_to(e - (e >> 1)), 0x1p-126f), 3.402823466e38f);
 }
 __device__ __forceinline__ bool finite_words(uint32_t m) { return !nonfinite2(m); }
 __device__ __forceinline__ bool any_of_fillers(bool x) {
@@ -568,7 +575,7 @@ __device__ __forceinline__ void fill_tiles(const AttnArgs& a, Walk w, Sh& sh, ui
       ve = max(ve, v_now);
       const int v_exp = ve == -1000 ? 0 : ve;
       if (t == 0) {
-        sh.powers[n & 7].k = exp2f(static_cast<float>(ke));
+        sh.powers[n & 7].k = ke;
         sh.powers[n & 7].v = v_exp;
       }
       if (n >= C::kKS) wait(&sh.ke[kp.s], kp.ph ^ 1u);
@@ -664,7 +671,7 @@ __device__ __forceinline__ void convert_q(const AttnArgs& a, Walk w, Sh& sh, uin
       top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
       e = half_exponent(top);
       if (e != 0) pass();
-      if (lane == 0) sh.q_power[t][unit & 7] = exp2f(static_cast<float>(e));
+      if (lane == 0) sh.q_power[t][unit & 7] = e;
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(su32(&sh.qr[t]));
@@ -1168,7 +1175,7 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
           int v_exp = 0;
           if constexpr (CODES) {
             const volatile Sh& vs = sh;
-            cj = a.scale_log2 * vs.q_power[t][unit & 7] * vs.powers[(tile_n + j) & 7].k;
+            cj = score_factor(a.scale_log2, vs.q_power[t][unit & 7] + vs.powers[(tile_n + j) & 7].k);
             v_exp = vs.powers[(tile_n + j) & 7].v;
           }
           tmem_wait_ld();

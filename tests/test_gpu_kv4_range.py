@@ -129,7 +129,7 @@ def check(pool, kind, q, ms, scale, window=0, sinks=0):
 def made(bec, lens, hkv, D, dtype, seed, k=1.0, v=1.0):
     """Random keys and values times k and v (numbers, or tensors of [n, D] for one sequence)."""
     g = gen(seed)
-    rand = lambda n, f: (torch.randn((n, hkv, D), device="cuda", generator=g) + 0.3) * (f if not torch.is_tensor(f) else f[:, None])  # noqa: E731
+    rand = lambda n, f: (torch.randn((n, hkv, D), device="cuda", generator=g) + 0.3) * (f if not torch.is_tensor(f) else f[:, None, None])  # noqa: E731
     keys, values = [rand(n, k) for n in lens], [rand(n, v) for n in lens]
     return Pool(bec, keys, values, dtype)
 
@@ -148,7 +148,7 @@ def chunks(kind, lens):
 
 # ---------------------------------------------------------------- scores beyond fp32's smallest
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("kind,D", CALLS)
+@pytest.mark.parametrize("kind,D", [c for c in CALLS if c[0] == "prefill" and c[1] <= 128])
 @pytest.mark.parametrize("q,k,scale", [(2.0 ** -70, 2.0 ** -70, 0.1), (2.0 ** -110, 2.0 ** -20, 1e-30), (2.0 ** -115, 1.0, 1e-37)])
 def test_scores_that_are_nothing_weigh_evenly(bec, dtype, kind, D, q, k, scale):
     lens = [300, 40]
