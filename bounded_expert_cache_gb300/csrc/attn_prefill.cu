@@ -222,12 +222,14 @@ struct Shared {
   uint32_t poison[8];  // ring over units: number + 1 of a unit with infinities or NaN taken out of V
   uint32_t tmem;
   int abort;
-  // codes: exponents of the powers of two taken out of the last tiles of K and V and of
-  // the last units' Q, by their number
+  // codes: exponents of the powers of two taken out of the last tiles of K and V, by the
+  // tile's number, and out of Q, by the number of units in which the row tile had rows. (By
+  // the number of all units its warp could pass by many that have rows in the other row tile
+  // alone and take the place of a power that is still to be read.)
   struct Powers {
     int k, v;
   } powers[8];
-  int q_power[2][8];
+  int q_power[2][4];
   uint32_t fill_top[2][4];
 };
 template <int DP, bool APART, bool CODES>
@@ -610,17 +612,14 @@ __device__ __forceinline__ void convert_q(const AttnArgs& a, Walk w, Sh& sh, uin
   constexpr int kPieces = DP / 8, kRowsPer = 32 / kPieces, kBatch = 4;
   const int lane = threadIdx.x & 31, p = lane % kPieces;
   volatile int* abort_flag = &sh.abort;
-  uint32_t qe_ph = 0;
-  bool ok = true, q_used = false;
-  for (uint32_t unit = 0; ok; ++unit) {
+  uint32_t mine = 0;  // units in which this row tile had rows
+  while (true) {
     if (t * kQT < w.rows) {
-      if (q_used) {
-        ok = mbar_wait(su32(&sh.qe[t]), qe_ph, abort_flag, a.err, a.wait_cycles);
+      if (mine > 0) {
+        bool ok = mbar_wait(su32(&sh.qe[t]), (mine - 1) & 1u, abort_flag, a.err, a.wait_cycles);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
-        qe_ph ^= 1u;
       }
-      q_used = true;
       const int rows = w.rows - t * kQT;
       int e = 0;
       float top;
@@ -671,7 +670,9 @@ __device__ __forceinline__ void convert_q(const AttnArgs& a, Walk w, Sh& sh, uin
       top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
       e = half_exponent(top);
       if (e != 0) pass();
-      if (lane == 0) sh.q_power[t][unit & 7] = e;
+      // (the scores of the unit before are formed, so those of the one before that have been read, and their power with them)
+      if (lane == 0) sh.q_power[t][mine & 3] = e;
+      ++mine;
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(su32(&sh.qr[t]));
@@ -1127,7 +1128,7 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
     // (codes: maxima are in units of log2, as a score's unit differs from tile to tile)
     const float c = CODES ? 1.f : a.scale_log2, raise = kRaise / c;
     uint32_t s_ph = 0, o_ph = 0, p_n = 0;  // p_n: numerators written (kApart)
-    uint32_t tile_n = 0;                   // tiles before this unit's
+    uint32_t tile_n = 0, mine = 0;         // tiles before this unit's, and units in which this row tile had rows
     bool ok = true;
     for (uint32_t unit = 0; ok; ++unit) {
       if (t * kQT < w.rows) {
@@ -1175,7 +1176,7 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
           int v_exp = 0;
           if constexpr (CODES) {
             const volatile Sh& vs = sh;
-            cj = score_factor(a.scale_log2, vs.q_power[t][unit & 7] + vs.powers[(tile_n + j) & 7].k);
+            cj = score_factor(a.scale_log2, vs.q_power[t][mine & 3] + vs.powers[(tile_n + j) & 7].k);
             v_exp = vs.powers[(tile_n + j) & 7].v;
           }
           tmem_wait_ld();
@@ -1401,6 +1402,7 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
         }
         // the next unit's products overwrite O only after this read
         fence_before();
+        ++mine;
       }
       tile_n += w.nt;
       if (!w.more()) break;

@@ -156,3 +156,38 @@ def test_scores_that_are_nothing_weigh_evenly(bec, dtype, kind, D, q, k, scale):
     ms = chunks(kind, lens)
     check(pool, kind, queries(sum(ms), 4, D, dtype, 2, q), ms, scale)
     check(pool, kind, queries(sum(ms), 4, D, dtype, 2, q), ms, scale, window=30, sinks=3)
+
+
+# ---------------------------------------------------------------- units of many kinds in one call
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lone", [7, 15])
+def test_chunks_of_one_and_two_row_tiles_whose_queries_differ(bec, D, lone):
+    """Chunks of 200 rows between `lone` of 100: the second row tile has work in every eighth unit of a block or so."""
+    n_seqs = 152 * 4 * (lone + 1)
+    two = [b % (lone + 1) == 0 for b in range(n_seqs)]
+    ms = [200 if t else 100 for t in two]
+    g = gen(16)
+    T = sum(ms)
+    k, v = (torch.randn((T, 1, D), device="cuda", generator=g) for _ in range(2))
+    kv = bec.KvCache.empty(1, sum(-(-m // PAGE) for m in ms), 1, PAGE, D, n_seqs, 16, bits=4)
+    seqs = i32(range(n_seqs))
+    for s in range(0, n_seqs, 8000):
+        kv.reserve(seqs[s:s + 8000].contiguous(), i32(ms[s:s + 8000]))
+    cu = torch.tensor([0] + ms).cumsum(0).int().cuda()
+    kv.write(0, k.bfloat16(), v.bfloat16(), seqs, cu)
+    kv.check_errors()
+    # a chunk's queries are 2^16, 2^18 or 2^20 times the usual ones, in turn
+    size = torch.tensor([2.0 ** (16 + 2 * ((b // (lone + 1)) % 3)) for b in range(n_seqs)]).repeat_interleave(torch.tensor(ms)).cuda()
+    x = torch.randn((T, 1, D), device="cuda", generator=g)
+    scale = D ** -0.5 * 2.0 ** -18
+    q = (x * size[:, None, None]).bfloat16()
+    got = kv.attn_prefill(0, q, seqs, cu, scale=scale)
+    kv.check_errors()
+    # the same rows of chunks of 200 alone
+    alone = torch.tensor([b for b in range(n_seqs) if two[b]])
+    rows = torch.cat([torch.arange(int(cu[b]), int(cu[b + 1])) for b in alone]).cuda()
+    want = kv.attn_prefill(0, q[rows].contiguous(), alone.int().cuda(), i32(range(0, 200 * len(alone) + 1, 200)), scale=scale)
+    kv.check_errors()
+    a, b = got[rows].float(), want.float()
+    # (how the work is cut may move a sum's last bit, and so a result by one step of bf16)
+    assert ((a - b).abs() <= 2 * U8 * b.abs() + 1e-4 * b.abs().max()).all(), (a - b).abs().max().item()
