@@ -223,13 +223,13 @@ struct Shared {
   uint32_t tmem;
   int abort;
   // codes: exponents of the powers of two taken out of the last tiles of K and V, by the
-  // tile's number, and out of Q, by the number of units in which the row tile had rows. (By
-  // the number of all units its warp could pass by many that have rows in the other row tile
-  // alone and take the place of a power that is still to be read.)
+  // tile's number, and out of Q's rows, by the number of units in which the row tile had rows.
+  // (By the number of all units its warp could pass by many that have rows in the other row
+  // tile alone and take the place of powers that are still to be read.)
   struct Powers {
     int k, v;
   } powers[8];
-  int q_power[2][4];
+  int8_t q_power[2][2][kQT];
   uint32_t fill_top[2][4];
 };
 template <int DP, bool APART, bool CODES>
@@ -350,10 +350,10 @@ __device__ __noinline__ void zero_nonfinite(uint32_t rows) {
 // ---- pages of 4-bit codes. A tile's values s q + b become f16, whose 11 bits keep
 // what 8 of bf16 would not (keys rounded to bf16 put 0.25% of noise on every
 // numerator: 3.4e-3 of the results' norm instead of 2.0e-3); Q and the numerators are
-// f16 with them. f16's range is made up for by powers of two: a tile of K whose
-// largest value is above 2^14 or below 2^-8, and a row tile of Q likewise, is divided by
-// one that makes it about 2^10, and its scores multiplied by it; V by the largest power
-// that its unit has come across, and O is kept in that unit. (Values that are then below
+// f16 with them. f16's range is made up for by powers of two: a row of Q is divided by one
+// that makes its largest value about 2^13, a tile of K whose largest value is above 2^14 or
+// below 2^-8 by one that makes it about 2^10, and its scores are multiplied by both; V by the
+// largest power that its unit has come across, and O is kept in that unit. (Values that are then below
 // 2^-24, or 2^-34 of the largest, are lost.) Of the eight values of
 // a word, nibbles i and i + 4 come out as a pair, so that columns lie in the order 0 4
 // 1 5 2 6 3 7: Q is laid out the same, and results are put back as they are read.
@@ -377,6 +377,9 @@ __device__ __forceinline__ int half_exponent(float top) {
   if (top == 0.f || (top <= kHalfMost && top >= kHalfLeast)) return 0;
   return max(-120, static_cast<int>(__float_as_uint(top) >> 23) - 127 - 10);  // (a denormal's is -137)
 }
+// The power of two that a row of Q with this largest value (bits of a bf16) is divided by: about
+// 2^13 is left, so that what f16 holds as it is reaches down to 2^-27 of it.
+__device__ __forceinline__ int row_exponent(uint32_t top) { return max(-112, static_cast<int>(top >> 7) - 127 - 13); }
 // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float two_to(int e) { return __int_as_float((e + 127) << 23); }
 // A score's factor, x times 2^e of Q's and K's exponents. In fp32's normal range: of 0 a hidden
@@ -605,11 +608,13 @@ __device__ __forceinline__ void fill_tiles(const AttnArgs& a, Walk w, Sh& sh, ui
   }
 }
 
-// A warp brings in Q of row tile t of every unit, as f16 in the columns' order.
+// A warp brings in Q of row tile t of every unit, as f16 in the columns' order, each row over
+// its own power of two. Short loops here, too (24 ragged prompts of up to 4,000 tokens, heads of
+// 128: 769 us; unrolled four times, four rows a turn 822; rows by way of registers 893).
 template <int DP, class Sh>
 __device__ __forceinline__ void convert_q(const AttnArgs& a, Walk w, Sh& sh, uint32_t sq, int t) {
   using C = typename Sh::C;
-  constexpr int kPieces = DP / 8, kRowsPer = 32 / kPieces, kBatch = 4;
+  constexpr int kPieces = DP / 8, kRowsPer = 32 / kPieces, kBatch = 2;
   const int lane = threadIdx.x & 31, p = lane % kPieces;
   volatile int* abort_flag = &sh.abort;
   uint32_t mine = 0;  // units in which this row tile had rows
@@ -621,57 +626,71 @@ __device__ __forceinline__ void convert_q(const AttnArgs& a, Walk w, Sh& sh, uin
         if (!ok) break;
       }
       const int rows = w.rows - t * kQT;
-      int e = 0;
-      float top;
-      auto pass = [&]() {
-        const float f = exp2f(static_cast<float>(-e));
-        const int64_t rg = static_cast<int64_t>(w.rt) * kUnitRows + t * kQT + lane / kPieces;
-        const int i = static_cast<int>(quotient(rg, a.g));
-        int hq = static_cast<int>(rg - static_cast<int64_t>(i) * a.g);
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(w.s.row0) + i) * a.ldq +
-                                   static_cast<int64_t>(w.h * a.g + hq) * a.D + p * 8;
-        const int64_t step = kRowsPer * a.D, wrap = a.ldq - static_cast<int64_t>(a.g) * a.D;
-        const uint32_t dst = sq + (p >> 3) * C::kHalf;
-        top = 0.f;
+      const int64_t rg = static_cast<int64_t>(w.rt) * kUnitRows + t * kQT + lane / kPieces;
+      const int i = static_cast<int>(quotient(rg, a.g));
+      int hq = static_cast<int>(rg - static_cast<int64_t>(i) * a.g);
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(w.s.row0) + i) * a.ldq +
+                                 static_cast<int64_t>(w.h * a.g + hq) * a.D + p * 8;
+      const int64_t step = kRowsPer * a.D, wrap = a.ldq - static_cast<int64_t>(a.g) * a.D;
+      const uint32_t dst = sq + (p >> 3) * C::kHalf;
+      auto at = [&](int r) { return dst + r * 128u + (((p & 7) ^ (r & 7)) << 4); };
 #pragma unroll 1
-        for (int r0 = lane / kPieces; r0 < kQT; r0 += kRowsPer * kBatch) {
-          uint4 u[kBatch];
-#pragma unroll
-          for (int x = 0; x < kBatch; ++x) {
-            u[x] = make_uint4(0u, 0u, 0u, 0u);
-            if (r0 + x * kRowsPer < rows) u[x] = __ldg(reinterpret_cast<const uint4*>(src));
-            src += step;  // the next row's head, or the next token's first ones
-            hq += kRowsPer;
-            while (hq >= a.g) {
-              hq -= a.g;
-              src += wrap;
-            }
-          }
-#pragma unroll
-          for (int x = 0; x < kBatch; ++x) {
-            const int r = r0 + x * kRowsPer;
-            const uint32_t ws[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
-            float v[8];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              v[2 * y] = __uint_as_float(ws[y] << 16) * f;
-              v[2 * y + 1] = __uint_as_float(ws[y] & 0xFFFF0000u) * f;
-            }
-#pragma unroll
-            for (int y = 0; y < 8; ++y)
-              if (fabsf(v[y]) < INFINITY) top = fmaxf(top, fabsf(v[y]));
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + r * 128u + (((p & 7) ^ (r & 7)) << 4)),
-                         "r"(pack_f16(v[0], v[4])), "r"(pack_f16(v[1], v[5])), "r"(pack_f16(v[2], v[6])), "r"(pack_f16(v[3], v[7]))
-                         : "memory");
-          }
+      for (int r = lane / kPieces; r < kQT; r += kRowsPer) {  // rows past the end are zero
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(r)), "l"(r < rows ? src : a.q), "r"(r < rows ? 16 : 0)
+                     : "memory");
+        src += step;  // the next row's head, or the next token's first ones
+        hq += kRowsPer;
+        while (hq >= a.g) {
+          hq -= a.g;
+          src += wrap;
         }
-      };
-      pass();
-      top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
-      e = half_exponent(top);
-      if (e != 0) pass();
-      // (the scores of the unit before are formed, so those of the one before that have been read, and their power with them)
-      if (lane == 0) sh.q_power[t][mine & 3] = e;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      // in place: a lane's pieces are those that it has copied. (The scores of the unit before
+      // are formed, so those of the one before that have been read, and their powers with them.)
+      int8_t* power = sh.q_power[t][mine & 1];
+#pragma unroll 1
+      for (int r0 = lane / kPieces; r0 < kQT; r0 += kRowsPer * kBatch) {
+        uint4 u[kBatch];
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x)
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(u[x].x), "=r"(u[x].y), "=r"(u[x].z), "=r"(u[x].w)
+                       : "r"(at(r0 + x * kRowsPer))
+                       : "memory");
+        // the rows' largest magnitudes, as bf16 bits, of two rows in a word. (With an infinity or
+        // NaN in a row no score of it is finite, whatever the power.)
+        uint32_t top[kBatch / 2];
+#pragma unroll
+        for (int x = 0; x < kBatch; x += 2) {
+          auto most = [](uint4 q) {
+            constexpr uint32_t kMagnitude = 0x7FFF7FFFu;
+            return __vmaxu2(__vmaxu2(q.x & kMagnitude, q.y & kMagnitude), __vmaxu2(q.z & kMagnitude, q.w & kMagnitude));
+          };
+          const uint32_t m0 = most(u[x]), m1 = most(u[x + 1]);
+          top[x / 2] = __vmaxu2(__byte_perm(m0, m1, 0x5410), __byte_perm(m0, m1, 0x7632));
+        }
+#pragma unroll
+        for (int d = 1; d < kPieces; d <<= 1)
+#pragma unroll
+          for (int x = 0; x < kBatch / 2; ++x) top[x] = __vmaxu2(top[x], __shfl_xor_sync(~0u, top[x], d));
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          const int r = r0 + x * kRowsPer, e = row_exponent(x & 1 ? top[x / 2] >> 16 : top[x / 2] & 0xFFFFu);
+          const float f = two_to(-e);
+          const uint32_t ws[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
+          float v[8];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            v[2 * y] = __uint_as_float(ws[y] << 16) * f;
+            v[2 * y + 1] = __uint_as_float(ws[y] & 0xFFFF0000u) * f;
+          }
+          if (p == 0) power[r] = static_cast<int8_t>(e);
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at(r)), "r"(pack_f16(v[0], v[4])), "r"(pack_f16(v[1], v[5])),
+                       "r"(pack_f16(v[2], v[6])), "r"(pack_f16(v[3], v[7]))
+                       : "memory");
+        }
+      }
       ++mine;
       fence_async_smem();
       __syncwarp();
@@ -1176,7 +1195,7 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
           int v_exp = 0;
           if constexpr (CODES) {
             const volatile Sh& vs = sh;
-            cj = score_factor(a.scale_log2, vs.q_power[t][mine & 3] + vs.powers[(tile_n + j) & 7].k);
+            cj = score_factor(a.scale_log2, vs.q_power[t][mine & 1][r] + vs.powers[(tile_n + j) & 7].k);
             v_exp = vs.powers[(tile_n + j) & 7].v;
           }
           tmem_wait_ld();

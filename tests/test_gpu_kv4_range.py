@@ -158,6 +158,20 @@ def test_scores_that_are_nothing_weigh_evenly(bec, dtype, kind, D, q, k, scale):
     check(pool, kind, queries(sum(ms), 4, D, dtype, 2, q), ms, scale, window=30, sinks=3)
 
 
+# ---------------------------------------------------------------- queries' and keys' columns, and rows, of different magnitudes
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind,D", CALLS)
+def test_rows_of_queries_of_different_magnitudes(bec, dtype, kind, D):
+    """Some rows' queries are 2^-22 of their neighbours' and see keys that the others do not tell apart."""
+    lens = [300, 40]
+    pool = made(bec, lens, 2, D, dtype, 7, k=2.0 ** 20)
+    ms = chunks(kind, lens)
+    q = queries(sum(ms), 8, D, F32, 8, 2.0 ** -20)
+    q[1::2] = 0
+    q[1::2, :, 0] = 4.0
+    check(pool, kind, q.to(dtype), ms, D ** -0.5)
+
+
 # ---------------------------------------------------------------- units of many kinds in one call
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("lone", [7, 15])
