@@ -230,7 +230,7 @@ struct Shared {
     int k, v;
   } powers[8];
   int8_t q_power[2][2][kQT];
-  uint32_t fill_top[2][4];
+  alignas(16) uint32_t fill_top[2][2][4];  // of a tile's K and V, by its number: the converting warps' largest values
 };
 template <int DP, bool APART, bool CODES>
 constexpr int kSmem = Cfg<DP, APART, CODES>::kTiles + static_cast<int>(sizeof(Shared<DP, APART, CODES>));
@@ -350,12 +350,13 @@ __device__ __noinline__ void zero_nonfinite(uint32_t rows) {
 // ---- pages of 4-bit codes. A tile's values s q + b become f16, whose 11 bits keep
 // what 8 of bf16 would not (keys rounded to bf16 put 0.25% of noise on every
 // numerator: 3.4e-3 of the results' norm instead of 2.0e-3); Q and the numerators are
-// f16 with them. f16's range is made up for by powers of two: a row of Q is divided by one
-// that makes its largest value about 2^13, a tile of K whose largest value is above 2^14 or
-// below 2^-8 by one that makes it about 2^10, and its scores are multiplied by both; V by the
-// largest power that its unit has come across, and O is kept in that unit. (Values that are then below
-// 2^-24, or 2^-34 of the largest, are lost.) Of the eight values of
-// a word, nibbles i and i + 4 come out as a pair, so that columns lie in the order 0 4
+// f16 with them. f16's range is made up for by powers of two: a row of Q and a tile of K are
+// divided by one that makes their largest value about 2^13, and the scores are multiplied by
+// both. A unit's V is divided by one that makes its first tile's largest value about 2^11, and
+// by a larger one from a tile on whose values would pass 2^15; O is kept in that unit. So a
+// value (and the scale that it is formed with, a fifteenth of it or so) keeps its bits down to
+// 2^-24 of the largest one beside it and is more than nothing down to 2^-34. Of the eight values of a
+// word, nibbles i and i + 4 come out as a pair, so that columns lie in the order 0 4
 // 1 5 2 6 3 7: Q is laid out the same, and results are put back as they are read.
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -371,15 +372,10 @@ __device__ __forceinline__ void in_order(float* o, float f) {
     for (int y = 0; y < 8; ++y) o[x + y] = t[y];
   }
 }
-constexpr float kHalfMost = 16384.f, kHalfLeast = 0x1p-8f;
-// the power of two that a tile with this largest value is divided by
-__device__ __forceinline__ int half_exponent(float top) {
-  if (top == 0.f || (top <= kHalfMost && top >= kHalfLeast)) return 0;
-  return max(-120, static_cast<int>(__float_as_uint(top) >> 23) - 127 - 10);  // (a denormal's is -137)
-}
-// The power of two that a row of Q with this largest value (bits of a bf16) is divided by: about
-// 2^13 is left, so that what f16 holds as it is reaches down to 2^-27 of it.
-__device__ __forceinline__ int row_exponent(uint32_t top) { return max(-112, static_cast<int>(top >> 7) - 127 - 13); }
+// The exponent of what values are divided by: their largest one's, a float's upper nine bits, less
+// what is left to it. (From -112 on all that fp32 holds as it is, 2^-126 and up, f16 does too.)
+__device__ __forceinline__ int exponent_of(uint32_t top, int left) { return max(-112, static_cast<int>(top) - 127 - left); }
+constexpr int kLeftQk = 13, kLeftV = 11, kRoomV = 3;
 // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float two_to(int e) { return __int_as_float((e + 127) << 23); }
 // A score's factor, x times 2^e of Q's and K's exponents. In fp32's normal range: of 0 a hidden
@@ -529,63 +525,54 @@ __device__ __forceinline__ void fill_tiles(const AttnArgs& a, Walk w, Sh& sh, ui
       next.next(C::kRS);
       wait(&sh.rf[rp.s], rp.ph);
       wait(&sh.rf[next.s], next.ph);
-      if (any_of_fillers(!ok)) return;
       const uint32_t rk = raw + rp.s * C::kRaw, rv = raw + next.s * C::kRaw;
-      const int tile0 = w.sp.tile(w.t0 + j) * kKT;
-      // One thread a token looks at its scales and offsets.
-      const int tok = tile0 + t;
-      const bool seen = tok < w.sp.end && (tok < a.sinks || tok >= w.sp.low), mixed = mixed_tile(a, tile0, lo_pos, hi_pos);
-      float top[2] = {0.f, 0.f};
-      bool changed = false;
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const uint32_t at = (kv ? rv : rk) + kKT * C::kCodeRow + t * C::kMetaRow + 4 * g;
-          uint32_t m;
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(m) : "r"(at));
-          const float s = __uint_as_float(m << 16), b = __uint_as_float(m & 0xFFFF0000u);
-          const bool fine = finite_words(m);
-          // Tokens that no row sees become zeros. So do values that are infinite or NaN
-          // in a tile with tokens that only some rows see; the rows that see them learn
-          // of it at the unit's end.
-          if (!seen || (kv && mixed && !fine)) {
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(0) : "memory");
-            changed = true;
-            if (seen) *const_cast<volatile uint32_t*>(&sh.poison[unit & 7]) = unit + 1;
-          } else if (fine) {
-            top[kv] = fmaxf(top[kv], fminf(fmaxf(fabsf(b), fabsf(fmaf(15.f, s, b))), 3.3e38f));
-          }
-        }
-      }
-      if (changed) fence_async_smem();  // these writes, before the slot's next copy
-      // the tile's powers of two, the same in every thread; a look at each thread's own token settles most
-      int ke = 0, v_now = 0;
-      if (any_of_fillers(top[0] > kHalfMost || top[0] < kHalfLeast || top[1] > kHalfMost || top[1] < kHalfLeast)) {
+      if (ok) {
+        // One thread a token looks at its scales and offsets.
+        const int tile0 = w.sp.tile(w.t0 + j) * kKT, tok = tile0 + t;
+        const bool seen = tok < w.sp.end && (tok < a.sinks || tok >= w.sp.low), mixed = mixed_tile(a, tile0, lo_pos, hi_pos);
+        bool changed = false;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(top[kv]));
-          if (lane == 0) sh.fill_top[kv][t >> 5] = most;
+          float top = 0.f;
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const uint32_t at = (kv ? rv : rk) + kKT * C::kCodeRow + t * C::kMetaRow + 4 * g;
+            uint32_t m;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(m) : "r"(at));
+            const float s = __uint_as_float(m << 16), b = __uint_as_float(m & 0xFFFF0000u);
+            const bool fine = finite_words(m);
+            // Tokens that no row sees become zeros. So do values that are infinite or NaN
+            // in a tile with tokens that only some rows see; the rows that see them learn
+            // of it at the unit's end.
+            if (!seen || (kv && mixed && !fine)) {
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(0) : "memory");
+              changed = true;
+              if (seen) *const_cast<volatile uint32_t*>(&sh.poison[unit & 7]) = unit + 1;
+            } else if (fine) {
+              top = fmaxf(top, fminf(fmaxf(fabsf(b), fabsf(fmaf(15.f, s, b))), 3.3e38f));
+            }
+          }
+          const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(top));
+          if (lane == 0) sh.fill_top[n & 1][kv][t >> 5] = most;
         }
-        asm volatile("bar.sync 2, 128;" ::: "memory");
-        const volatile Sh& all = sh;
-        auto most = [&](int x) {
-          return __uint_as_float(max(max(all.fill_top[x][0], all.fill_top[x][1]), max(all.fill_top[x][2], all.fill_top[x][3])));
-        };
-        ke = half_exponent(most(0));
-        v_now = half_exponent(most(1));
-        if (most(1) == 0.f) v_now = ve;  // (nothing to hold)
-        asm volatile("bar.sync 2, 128;" ::: "memory");
+        if (changed) fence_async_smem();  // these writes, before the slot's next copy
       }
-      ve = max(ve, v_now);
-      const int v_exp = ve == -1000 ? 0 : ve;
+      if (any_of_fillers(!ok)) return;
+      // the tile's powers of two, the same in every thread. (The next tile's maxima have places of
+      // their own, and the next but one's are written after the next meeting.)
+      auto exponent = [&](int kv, int left) {
+        const uint4 m = *reinterpret_cast<const uint4*>(sh.fill_top[n & 1][kv]);
+        return exponent_of(max(max(m.x, m.y), max(m.z, m.w)) >> 23, left);
+      };
+      const int ke = exponent(0, kLeftQk), v_now = exponent(1, kLeftV);
+      if (v_now > ve + kRoomV) ve = v_now;
       if (t == 0) {
         sh.powers[n & 7].k = ke;
-        sh.powers[n & 7].v = v_exp;
+        sh.powers[n & 7].v = ve;
       }
       if (n >= C::kKS) wait(&sh.ke[kp.s], kp.ph ^ 1u);
       if (ok) {
-        convert(rk, sk + kp.s * C::kTile, exp2f(static_cast<float>(-ke)));
+        convert(rk, sk + kp.s * C::kTile, two_to(-ke));
         fence_async_smem();
         tell(&sh.kf[kp.s]);
         tell(&sh.re[rp.s]);
@@ -593,7 +580,7 @@ __device__ __forceinline__ void fill_tiles(const AttnArgs& a, Walk w, Sh& sh, ui
       kp.next(C::kKS);
       if (n >= C::kVS) wait(&sh.ve[vp.s], vp.ph ^ 1u);
       if (ok) {
-        convert(rv, sv + vp.s * C::kTile, exp2f(static_cast<float>(-v_exp)));
+        convert(rv, sv + vp.s * C::kTile, two_to(-ve));
         fence_async_smem();
         tell(&sh.vf[vp.s]);
         tell(&sh.re[next.s]);
@@ -676,7 +663,7 @@ __device__ __forceinline__ void convert_q(const AttnArgs& a, Walk w, Sh& sh, uin
           for (int x = 0; x < kBatch / 2; ++x) top[x] = __vmaxu2(top[x], __shfl_xor_sync(~0u, top[x], d));
 #pragma unroll
         for (int x = 0; x < kBatch; ++x) {
-          const int r = r0 + x * kRowsPer, e = row_exponent(x & 1 ? top[x / 2] >> 16 : top[x / 2] & 0xFFFFu);
+          const int r = r0 + x * kRowsPer, e = exponent_of(x & 1 ? top[x / 2] >> 23 : (top[x / 2] & 0xFFFFu) >> 7, kLeftQk);
           const float f = two_to(-e);
           const uint32_t ws[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
           float v[8];
@@ -1334,7 +1321,7 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
         float* part = a.part + ((2 * static_cast<int64_t>(blockIdx.x) + (run0 > w.tiles0() ? 0 : 1)) * 2 + t) * C::kPart;
         if (!whole) *reinterpret_cast<float2*>(part + r * 4) = make_float2(m, l);
         const float inv = 1.f / l;  // no weight at all on what is seen: 0/0
-        const float unit_of_o = CODES ? exp2f(static_cast<float>(o_exp)) : 1.f;
+        const float unit_of_o = CODES ? two_to(o_exp) : 1.f;
 #pragma unroll 1
         for (int x = 0; x < DP; x += 32) {
           float o[32];

@@ -158,7 +158,35 @@ def test_scores_that_are_nothing_weigh_evenly(bec, dtype, kind, D, q, k, scale):
     check(pool, kind, queries(sum(ms), 4, D, dtype, 2, q), ms, scale, window=30, sinks=3)
 
 
+# ---------------------------------------------------------------- magnitudes
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind,D", CALLS)
+@pytest.mark.parametrize("q,k,v", [(16, -12, -70), (-70, 16, 16), (-12, -70, 60), (16, -90, -100), (60, -70, -12), (0, 0, 0)])
+def test_queries_keys_and_values_of_any_magnitude(bec, dtype, kind, D, q, k, v):
+    lens = [300, 40]
+    pool = made(bec, lens, 2, D, dtype, 3, k=2.0 ** k, v=2.0 ** v)
+    ms = chunks(kind, lens)
+    check(pool, kind, queries(sum(ms), 8, D, dtype, 4, 2.0 ** q), ms, D ** -0.5 * 2.0 ** -(q + k))
+
+
 # ---------------------------------------------------------------- queries' and keys' columns, and rows, of different magnitudes
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind,D", [("prefill", 128)])
+def test_columns_of_queries_and_keys_that_make_up_for_each_other(bec, dtype, kind, D):
+    lens = [300, 40]
+    pool = made(bec, lens, 2, D, dtype, 5)
+    g = gen(5)
+    keys = [torch.randn((n, 2, D), device="cuda", generator=g) for n in lens]
+    values = [torch.randn((n, 2, D), device="cuda", generator=g) for n in lens]
+    for x in keys:
+        x[..., 64:] *= 2.0 ** -20
+    pool = Pool(bec, keys, values, dtype)
+    ms = chunks(kind, lens)
+    q = queries(sum(ms), 8, D, F32, 6)
+    q[..., :64] *= 2.0 ** -20
+    check(pool, kind, q.to(dtype), ms, 2.0 ** 20 * D ** -0.5)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("kind,D", CALLS)
 def test_rows_of_queries_of_different_magnitudes(bec, dtype, kind, D):
@@ -170,6 +198,43 @@ def test_rows_of_queries_of_different_magnitudes(bec, dtype, kind, D):
     q[1::2] = 0
     q[1::2, :, 0] = 4.0
     check(pool, kind, q.to(dtype), ms, D ** -0.5)
+
+
+# ---------------------------------------------------------------- values
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind,D", [("prefill", 128)])
+def test_groups_of_values_2_20_apart(bec, dtype, kind, D):
+    lens = [300, 40]
+    g = gen(9)
+    keys = [torch.randn((n, 2, D), device="cuda", generator=g) for n in lens]
+    values = [torch.randn((n, 2, D), device="cuda", generator=g) + 0.3 for n in lens]
+    for x in values:
+        x[..., 64:] *= 2.0 ** -20
+    pool = Pool(bec, keys, values, dtype)
+    ms = chunks(kind, lens)
+    check(pool, kind, queries(sum(ms), 8, D, dtype, 10), ms, D ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind,D", CALLS)
+@pytest.mark.parametrize("exponents,window", [((0, 10, 20), 0), ((20, 10, 0), 100), ((0, 20, 5), 100), ((-60, -70, -50), 0), ((0, 3, 6, 1, 9), 0)])
+def test_values_whose_size_changes_from_tile_to_tile(bec, dtype, kind, D, exponents, window):
+    n = 128 * len(exponents)
+    f = torch.tensor([2.0 ** e for e in exponents], device="cuda").repeat_interleave(128)
+    pool = made(bec, [n], 2, D, dtype, 11, v=f)
+    ms = [8 if kind == "decode" else n]
+    check(pool, kind, queries(ms[0], 4, D, dtype, 12), ms, D ** -0.5, window, 2 if window else 0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind,D", CALLS)
+@pytest.mark.parametrize("what", ["keys", "values"])
+def test_tiles_of_zeros_and_of_small_keys(bec, dtype, kind, D, what):
+    n = 384
+    f = torch.tensor([0.0, 1.0, 2.0 ** -14] if what == "keys" else [0.0, 2.0 ** -30, 0.0], device="cuda").repeat_interleave(128)
+    pool = made(bec, [n], 2, D, dtype, 13, **{"k" if what == "keys" else "v": f})
+    ms = [8 if kind == "decode" else n]
+    check(pool, kind, queries(ms[0], 4, D, dtype, 14), ms, D ** -0.5)
 
 
 # ---------------------------------------------------------------- units of many kinds in one call
