@@ -237,6 +237,24 @@ def test_tiles_of_zeros_and_of_small_keys(bec, dtype, kind, D, what):
     check(pool, kind, queries(ms[0], 4, D, dtype, 14), ms, D ** -0.5)
 
 
+# ---------------------------------------------------------------- weights
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind,D", [("prefill", 64), ("prefill", 128)])
+@pytest.mark.parametrize("bits", [20, 24, 27])
+@pytest.mark.parametrize("at", [0, 1000, 2047])
+def test_many_tokens_far_below_the_largest(bec, dtype, kind, D, bits, at):
+    """One token outweighs each of the others by 2^bits, and its values are zeros. Heads enough for one block to see it all."""
+    n, hkv = 2048, 152
+    keys = torch.zeros((n, hkv, D), device="cuda")
+    keys[at, :, 0::64] = 15.0  # (exact in codes)
+    values = torch.rand((n, hkv, D), device="cuda", generator=gen(15)) + 0.5
+    values[at] = 0.0
+    pool = Pool(bec, [keys], [values], dtype)
+    q = torch.zeros((2, hkv, D), dtype=dtype, device="cuda")
+    q[..., 0] = 1.0
+    check(pool, kind, q, [2], bits * 0.6931471805599453 / 15.0)
+
+
 # ---------------------------------------------------------------- units of many kinds in one call
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("lone", [7, 15])
