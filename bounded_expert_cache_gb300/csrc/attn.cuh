@@ -30,6 +30,14 @@ __device__ __forceinline__ uint32_t in_register(uint32_t c) {
   asm volatile("mov.u32 %0, %1;" : "=r"(r) : "r"(c));
   return r;
 }
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float two_to(int e) { return __int_as_float((e + 127) << 23); }
+// A score's factor, x times 2^e of what Q and K were divided by. In fp32's normal range: of 0 a hidden
+// score, -infinity, would become NaN, and of an infinity a score of 0. (Scores that small tell
+// no tokens apart either way.)
+__device__ __forceinline__ float score_factor(float x, int e) {
+  return fminf(fmaxf(x * two_to(e >> 1) * two_to(e - (e >> 1)), 0x1p-126f), 3.402823466e38f);
+}
 // Either half of a bf16 pair is an infinity or a NaN.
 __device__ __forceinline__ bool nonfinite2(uint32_t v) {
   return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;

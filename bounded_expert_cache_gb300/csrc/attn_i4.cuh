@@ -235,8 +235,8 @@ struct CodesEngine {
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
         if (top > 16384.f || (top < 0x1p-8f && top > 0.f)) {
           const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 137, -120);  // about 2^10 is left
-          f = exp2f(static_cast<float>(-e));
-          c_row *= exp2f(static_cast<float>(e));
+          f = two_to(-e);
+          c_row = score_factor(a.scale_log2, e);
         }
       }
 #pragma unroll

@@ -381,14 +381,6 @@ __device__ __forceinline__ void in_order(float* o, float f) {
 // what is left to it. (From -112 on all that fp32 holds as it is, 2^-126 and up, f16 does too.)
 __device__ __forceinline__ int exponent_of(uint32_t top, int left) { return max(-112, static_cast<int>(top) - 127 - left); }
 constexpr int kLeftQk = 13, kLeftV = 11, kRoomV = 3;
-// 2^e, -126 <= e <= 127
-__device__ __forceinline__ float two_to(int e) { return __int_as_float((e + 127) << 23); }
-// A score's factor, x times 2^e of Q's and K's exponents. In fp32's normal range: of 0 a hidden
-// score, -infinity, would become NaN, and of an infinity a score of 0. (Scores that small tell
-// no tokens apart either way.)
-__device__ __forceinline__ float score_factor(float x, int e) {
-  return fminf(fmaxf(x * two_to(e >> 1) * two_to(e - (e >> 1)), 0x1p-126f), 3.402823466e38f);
-}
 __device__ __forceinline__ bool finite_words(uint32_t m) { return !nonfinite2(m); }
 __device__ __forceinline__ bool any_of_fillers(bool x) {
   uint32_t r;
