@@ -233,11 +233,9 @@ struct CodesEngine {
       if constexpr (kHalf) {
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        if (top > 16384.f || (top < 0x1p-8f && top > 0.f)) {
-          const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 137, -120);  // about 2^10 is left
-          f = two_to(-e);
-          c_row = score_factor(a.scale_log2, e);
-        }
+        const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -116);  // about 2^14 is left
+        f = two_to(-e);
+        c_row = score_factor(a.scale_log2, e);
       }
 #pragma unroll
       for (int g = 0; g < G; ++g) {

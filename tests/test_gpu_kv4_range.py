@@ -171,7 +171,7 @@ def test_queries_keys_and_values_of_any_magnitude(bec, dtype, kind, D, q, k, v):
 
 # ---------------------------------------------------------------- queries' and keys' columns, and rows, of different magnitudes
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("kind,D", [("prefill", 128)])
+@pytest.mark.parametrize("kind,D", [c for c in CALLS if c[1] > 64])
 def test_columns_of_queries_and_keys_that_make_up_for_each_other(bec, dtype, kind, D):
     lens = [300, 40]
     pool = made(bec, lens, 2, D, dtype, 5)
