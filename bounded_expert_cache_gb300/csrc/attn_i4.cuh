@@ -142,6 +142,10 @@ struct CodesEngine {
   static constexpr int kRows = 8 * NR, NB = 1;
   static constexpr bool kHalf = sizeof(T) == 2;
   static constexpr int kParts = kHalf ? 1 : 3;  // parts of an operand
+  // f16: numerators stay below 2^3 and scales below 4 of their unit, so that their products may be
+  // kept 2^10 times as large
+  static constexpr float kRaise = kHalf ? 3.f : 8.f;
+  static constexpr int kRoom = 2, kLift = 10;
   static constexpr bool kCodes = true;
   static constexpr int kRowBytes = 32 * G, kMetaBytes = 4 * G, kMostSlots = 12;
   static constexpr uint32_t kTileBytes = KT * (kRowBytes + kMetaBytes);
@@ -392,7 +396,7 @@ struct CodesEngine {
           }
       }
     }
-    // m is raised only when a score passes it by 2^8: numerators up to there lose nothing
+    // m is raised only when a score passes it by kRaise: numerators up to there lose nothing
     float mx[NR][2];
     bool up = false;
 #pragma unroll
@@ -419,7 +423,7 @@ struct CodesEngine {
           if (v > thr[nt][e]) {
             f[e] = ex2((m[nt][e] - v) * cs[nt][e]);  // 0 for the first maximum
             m[nt][e] = v;
-            thr[nt][e] = v + 8.f / cs[nt][e];
+            thr[nt][e] = v + kRaise / cs[nt][e];
           }
           l[nt][e] *= f[e];
 #pragma unroll
@@ -523,7 +527,7 @@ struct CodesEngine {
     }
   }
 
-  // Products are kept divided by the power of two of the first scale, until one is 64 times as large. (A negative
+  // Products are kept divided by the power of two of the first scale, until one is 4 times as large. (A negative
   // scale, or one that is infinite or NaN, comes here too, and changes nothing by itself.)
   __device__ __forceinline__ void widen(const uint32_t* m0, const uint32_t* m1, bool see0, bool see1) {
     float top = 0.f;
@@ -535,10 +539,10 @@ struct CodesEngine {
     }
     const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(top));
     if (most < v_limit || !__any_sync(~0u, see0 || see1)) return;
-    const int e = max(static_cast<int>(most >> 23) - 127, -100);
-    const float inv = exp2f(static_cast<float>(-e)), f = inv / v_inv;
+    const int e = max(static_cast<int>(most >> 23) - 127, -116);
+    const float inv = two_to(kLift - e), f = inv / v_inv;
     v_inv = inv;
-    v_limit = __float_as_uint(exp2f(static_cast<float>(min(e + 6, 127))));
+    v_limit = __float_as_uint(two_to(min(e + kRoom, 127)));
 #pragma unroll
     for (int t = 0; t < 4 * G; ++t)
 #pragma unroll

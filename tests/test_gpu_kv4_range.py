@@ -202,7 +202,7 @@ def test_rows_of_queries_of_different_magnitudes(bec, dtype, kind, D):
 
 # ---------------------------------------------------------------- values
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("kind,D", [("prefill", 128)])
+@pytest.mark.parametrize("kind,D", [c for c in CALLS if c[1] > 64])
 def test_groups_of_values_2_20_apart(bec, dtype, kind, D):
     lens = [300, 40]
     g = gen(9)
@@ -239,7 +239,7 @@ def test_tiles_of_zeros_and_of_small_keys(bec, dtype, kind, D, what):
 
 # ---------------------------------------------------------------- weights
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("kind,D", [("prefill", 64), ("prefill", 128)])
+@pytest.mark.parametrize("kind,D", CALLS)
 @pytest.mark.parametrize("bits", [20, 24, 27])
 @pytest.mark.parametrize("at", [0, 1000, 2047])
 def test_many_tokens_far_below_the_largest(bec, dtype, kind, D, bits, at):
