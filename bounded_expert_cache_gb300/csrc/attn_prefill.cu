@@ -224,7 +224,7 @@ struct Shared {
   uint64_t qr[2], qe[2], sr[2], sc[2], pa[2], pb[2], pv[2], of[2], drain;
   int64_t scan[C::kThreads / 32];
   Walk walk;
-  uint32_t poison[8];  // ring over units: number + 1 of a unit with infinities or NaN taken out of V
+  uint32_t poison[8];  // ring over units: number + 1 of the last one with infinities or NaN taken out of V
   uint32_t tmem;
   int abort;
   // codes: exponents of the powers of two taken out of the last tiles of K and V, by the
@@ -1268,7 +1268,10 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
         fence_after();
         const int hq = w.h * a.g + static_cast<int>(rg - static_cast<int64_t>(qi) * a.g);
         const int64_t row = static_cast<int64_t>(w.s.row0) + qi;
-        const bool poisoned = *const_cast<volatile uint32_t*>(&sh.poison[unit & 7]) == unit + 1;
+        // (A later number has taken the place of this unit's, if it had one: then there is
+        // nothing to find at worst.)
+        const bool poisoned =
+            __any_sync(~0u, static_cast<int>(*const_cast<volatile uint32_t*>(&sh.poison[unit & 7]) - (unit + 1)) >= 0);
         // codes: the groups of 64 columns that a visible token's scale or offset makes NaN
         const uint32_t lost = CODES && poisoned ? lost_groups<DP>(a, w, pos) : 0u;
         if (!CODES && poisoned) {

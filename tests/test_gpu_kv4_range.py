@@ -288,3 +288,35 @@ def test_chunks_of_one_and_two_row_tiles_whose_queries_differ(bec, D, lone):
     a, b = got[rows].float(), want.float()
     # (how the work is cut may move a sum's last bit, and so a result by one step of bf16)
     assert ((a - b).abs() <= 2 * U8 * b.abs() + 1e-4 * b.abs().max()).all(), (a - b).abs().max().item()
+
+
+@pytest.mark.parametrize("bits", [4, 0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_nan_of_many_short_units(bec, bits, D):
+    """Units of one and two row tiles, each with a NaN among its values that its last rows see: those and no others are NaN."""
+    lone, hkv = 7, 2
+    n_seqs = 152 * 3 * (lone + 1)
+    ms = [200 if b % (lone + 1) == 0 else 40 for b in range(n_seqs)]
+    T = sum(ms)
+    g = gen(17)
+    k, v = (torch.randn((T, hkv, D), device="cuda", generator=g).bfloat16() for _ in range(2))
+    cu = torch.tensor([0] + ms).cumsum(0)
+    # token 3/4 through each chunk; in every third none
+    bad = torch.tensor([int(cu[b]) + ms[b] * 3 // 4 for b in range(n_seqs) if b % 3])
+    v[bad.cuda()] = float("nan")
+    kv = bec.KvCache.empty(1, sum(-(-m // PAGE) for m in ms), hkv, PAGE, D, n_seqs, 16, bits=bits)
+    seqs = i32(range(n_seqs))
+    kv.reserve(seqs, i32(ms))
+    cu = cu.int().cuda()
+    kv.write(0, k, v, seqs, cu)
+    q = torch.randn((T, hkv, D), device="cuda", generator=g).bfloat16()
+    want = torch.zeros(T, dtype=torch.bool)
+    first = cu.tolist()
+    for b in range(n_seqs):
+        if b % 3:
+            want[first[b] + ms[b] * 3 // 4:first[b + 1]] = True
+    for _ in range(10):
+        out = kv.attn_prefill(0, q, seqs, cu)
+        assert torch.equal(torch.isnan(out).all(-1).all(-1).cpu(), want)
+        assert torch.equal(torch.isnan(out).any(-1).any(-1).cpu(), want)
+    kv.check_errors()
