@@ -57,6 +57,7 @@
 #include <cuda_fp16.h>
 
 #include "attn.cuh"
+#include "packed.cuh"
 #include "pdl.cuh"
 #include "prefill.h"
 #include "tc.cuh"
@@ -122,11 +123,6 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t lbo) {
   d |= static_cast<uint64_t>(2) << 61;
   return d;
 }
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-               "r"(bytes), "r"(bar)
-               : "memory");
-}
 __device__ __forceinline__ void tma3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
@@ -173,28 +169,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// two fp32 lanes an instruction
-__device__ __forceinline__ unsigned long long pack2(float a, float b) {
-  unsigned long long v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-  return v;
-}
-__device__ __forceinline__ float2 unpack2(unsigned long long v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
-  unsigned long long r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // A CTA's walk along the line: units (sequence, row tile, cache head) in order,
 // of each the tiles [t0, t0 + nt) that fall into the run. On the line a unit is
 // `cost` positions and then one per tile.
@@ -1229,19 +1203,19 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
             }
           }
           const float mc = (m == -INFINITY ? 0.f : m * c) - (CODES ? kLiftCodes : 0.f);
-          const unsigned long long c2 = pack2(cj, cj), m2 = pack2(-mc, -mc);
-          unsigned long long l0 = 0ull, l1 = 0ull;
+          const F2 c2 = f2(cj, cj), m2 = f2(-mc, -mc);
+          F2 l0 = 0ull, l1 = 0ull;
 #pragma unroll
           for (int x = 0; x < 128; x += 32) {
             uint32_t p[16];
 #pragma unroll
             for (int y = 0; y < 32; y += 4) {
-              const float2 u = unpack2(fma2(pack2(s[x + y], s[x + y + 1]), c2, m2));
-              const float2 v = unpack2(fma2(pack2(s[x + y + 2], s[x + y + 3]), c2, m2));
+              const float2 u = both(fma2(f2(s[x + y], s[x + y + 1]), c2, m2));
+              const float2 v = both(fma2(f2(s[x + y + 2], s[x + y + 3]), c2, m2));
               const float e0 = ex2(u.x), e1 = ex2(u.y), e2 = ex2(v.x), e3 = ex2(v.y);
               // the sum takes the numerators before their rounding to bf16
-              l0 = add2(l0, pack2(e0, e1));
-              l1 = add2(l1, pack2(e2, e3));
+              l0 = add2(l0, f2(e0, e1));
+              l1 = add2(l1, f2(e2, e3));
               p[y / 2] = CODES ? pack_f16(e0, e1) : pack_bf16(e0, e1);
               p[y / 2 + 1] = CODES ? pack_f16(e2, e3) : pack_bf16(e2, e3);
             }
@@ -1257,7 +1231,7 @@ __global__ void __launch_bounds__(Cfg<DP, APART, CODES>::kThreads, 1)
           fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(su32(&sh.pb[t]));
-          const float2 la = unpack2(add2(l0, l1));
+          const float2 la = both(add2(l0, l1));
           l += la.x + la.y;
         }
         if (!ok) break;

@@ -26,11 +26,6 @@ __device__ __forceinline__ void sync_compute() { asm volatile("bar.sync 1, 256;"
 __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
   tma4d(dst, m, bar, x, y, 0, z);
 }
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-               "r"(bytes), "r"(bar)
-               : "memory");
-}
 // A CTA's walk along the line: units in order, of each the tiles [t0, t1) that
 // fall into the run. On the line a unit is `cost` positions, for its Q and its
 // results, and then one per tile.
