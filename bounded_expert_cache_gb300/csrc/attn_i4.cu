@@ -2,10 +2,12 @@
 // attn_split.cuh with the engine of attn_i4.cuh.
 //
 // Measured: three contexts of 131,072 to 262,143 tokens, 8 heads of 128, 4 rows each:
-// 154 us, 4.4 TB/s of 0.5625 bytes a value (bf16 pages: 354); copies alone take 112, and
-// with all pages in L2 the call still 152: the integer pipe (half its cycles busy with
-// masks and shifts) and the chains of each warp bound it. 40 contexts of 1 to 32,768
-// tokens, 2 heads of 128: 33 us. One of 777: 12 us (9.5 in a captured graph).
+// 156 us, 4.4 TB/s of 0.5625 bytes a value (bf16 pages: 354); copies alone take 112, and
+// with all pages in L2 the call still 152. What bounds it are the chains of dependent
+// instructions with two computing warps a scheduler (issue slots 46% used) and the masks on
+// the integer pipe (41% of its cycles). 40 contexts of 1 to 32,768 tokens, 2 heads of 128,
+// one new token: 27 us (bf16 pages: 35; bytes take 6), four: 56: a unit's Q and join, and
+// the second launch. One of 777: 12 us (9.7 in a captured graph).
 #include "attn_i4.cuh"
 
 namespace moe {

@@ -9,12 +9,15 @@
 // The matrix instructions multiply codes, q - 8, which are exact in f16 and in bf16.
 // Scales and offsets are applied in fp32 to the scores of a group, and to the numerators
 // before they become an operand; the offsets' sums stay in fp32. bf16 calls multiply f16:
-// x exactly, p s rounded to f16 once (error against 64 bits 1.7e-3 of the norm, nearly all
+// x as it is, p s rounded to f16 once (error against 64 bits 1.7e-3 of the norm, nearly all
 // of it the result's own rounding to bf16; with p s in bf16 2.4e-3). f16's range is made
-// up for by powers of two: a row's x is divided by one if its largest is above 2^14 or
-// below 2^-8, and p s by that of the largest scale come across. (What is then below 2^-24
-// is lost: a 2^-30th of the row's largest x, and of a value with the largest scale.) f32
-// calls multiply x and p s as three bf16 that add up to them.
+// up for by powers of two. A row's x is divided by one that makes its largest about 2^14:
+// with the factor of 16 below, x loses no bits down to 2^-24 of that. p s is divided by that
+// of a unit's first scale, or of a later one 4 times as large, and kept 2^10 times as large
+// (p is below 2^3): it loses no bits down to 2^-24 of a token that has both the row's largest
+// weight and the largest scale, and is more than nothing down to 2^-34. (Scores are in x's
+// unit, up to 2^14 times as large as they are: scales from 2^100 on may take them beyond
+// fp32.) f32 calls multiply x and p s as three bf16 that add up to them.
 // V's codes are centred because the rounding of p s is multiplied by them: of q itself
 // it would carry 2.5 times the noise. K's are not, for f16: their operand keeps the
 // magnitude of 1024 that unpacking gives them (and the factor of 16 of every other

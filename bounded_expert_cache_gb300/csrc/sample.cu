@@ -29,12 +29,15 @@
 //   share is of the first histogram's total. A pass for the total alone, after which
 //   most tokens can be left out of the histogram, cost more: 64 rows 95 us, not 75.)
 //
-// What bounds it: few rows the latency of the passes and cluster barriers; many the
-// issue of the weights' arithmetic (some 40 instructions a token where all weights count;
-// two fp32 an instruction did not make it shorter) and the barriers. 131,072 fp32 logits:
-// a row with top-k 50 and top-p 12.3 us in a captured graph, with top-p alone 30; 64 such
-// rows 37 us with neither, 35 with top-k 50, 62 with settings of all kinds, 72 with top-p
-// alone. Their reading takes 5.
+// What bounds it: few rows the latency of the passes and cluster barriers; many that a CTA
+// loads, finds the maximum, forms weights and looks for the token in turn, with cluster
+// barriers between, and two CTAs on an SM hardly hide that for each other (64 rows with
+// neither cut: half the issue slots used, HBM a tenth; the weights' arithmetic alone, some 40
+// instructions a token, would take 8 to 9 us), in 1.7 waves of clusters, so two. Top-p adds
+// three atomics in shared memory for every token with weight. 131,072 fp32 logits: a row with
+// top-k 50 and top-p 12.6 us in a captured graph, with top-p alone 28; 64 such rows 37 us
+// with neither, 35 with top-k 50, 62 with settings of all kinds, with top-p alone 72 to 100,
+// by how many tokens share a bin. Their reading takes 5.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 

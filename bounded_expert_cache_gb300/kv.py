@@ -97,7 +97,8 @@ class Rotary:
     Pairs are halves of those columns, or with ``interleaved`` neighbours. Frequency i
     is base^(-2i/dim) radians a position; for long contexts it is divided by ``factor``:
     every one with context 0, else those of at most turns[0] turns within ``context``
-    tokens, less and less up to those of turns[1] turns, which stay. ``angles``
+    tokens, less and less up to those of turns[1] turns, which stay: linearly in the turns
+    (a rule that is linear in i instead needs ``angles``). ``angles``
     gives the dim / 2 frequencies themselves instead. Results are scaled by ``magnitude``.
     """
 

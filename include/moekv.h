@@ -128,7 +128,9 @@ typedef struct {
 /* Angles a position, in radians: angles[i] = base^(-2i/dim) (host, [dim / 2]), for
  * long contexts divided by factor: all of them with context = 0; else those that
  * make at most turns_low turns within `context` tokens, while those of at least
- * turns_high turns stay and the ones between are interpolated by their turns.
+ * turns_high turns stay and the ones between are interpolated linearly in their
+ * turns. (A rule that interpolates in the frequency's index gives other angles between
+ * the two: hand those to moe_rotary_turns.)
  * moe_rotary_turns: angles (host, any finite ones) as fractions of a turn times
  * 2^64 (host, [n]). Host only, no CUDA call. */
 moe_status_t moe_rotary_angles(int32_t dim, double base, double factor, int32_t context, double turns_low,
@@ -187,10 +189,16 @@ moe_status_t moe_kv_copy_pages(const moe_kv_t* kv, const int32_t* src, const int
  * [rows][n_heads][head_dim] of the cache's dtype (without MOE_KV_I4), rows ldq and
  * ldo elements apart and 16-byte aligned. Scores, softmax statistics and sums are
  * fp32; for bf16 the softmax's numerators enter the value product as bf16. Over pages
- * of codes bf16 calls multiply f16: queries, and values or numerators times scales,
- * over powers of two that rows and tiles share. So a value loses bits beside one 2^24
- * times as large that a row of the same call and sequence sees, and counts as 0 beside
- * one 2^34 times as large. (f32 calls have fp32's range.)
+ * of codes bf16 calls multiply f16 over powers of two. Of two that go by one power the
+ * smaller loses bits when the other is 2^24 times as large, and counts as 0 when it is
+ * 2^34 times as large. One power have
+ *   a query's values;
+ *   prompt chunks of heads of 64 and 128: the keys of 128 tokens and a cache head, the
+ *     values that the rows of a chunk see, and a row's weights (of the softmax);
+ *   decode, and chunks of larger heads: a row's weights times the groups' scales that
+ *     the sequence's rows see (the groups' offsets are summed in fp32). Scores are held
+ *     up to 2^14 times as large as they are: keys from 2^100 on may overflow.
+ * (f32 calls have fp32's range.)
  *
  * moe_attn_decode: the newest n_q (1..8) tokens of each of n sequences; rows
  * i*n_q .. i*n_q+n_q-1 belong to seqs[i] (device int32 [n], n <= 65536), at

@@ -161,7 +161,7 @@ def test_scores_that_are_nothing_weigh_evenly(bec, dtype, kind, D, q, k, scale):
 # ---------------------------------------------------------------- magnitudes
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("kind,D", CALLS)
-@pytest.mark.parametrize("q,k,v", [(16, -12, -70), (-70, 16, 16), (-12, -70, 60), (16, -90, -100), (60, -70, -12), (0, 0, 0)])
+@pytest.mark.parametrize("q,k,v", [(16, -12, -70), (-70, 16, 16), (-12, -70, 60), (16, -90, -100), (60, -70, -12), (-60, 95, 100), (0, 0, 0)])
 def test_queries_keys_and_values_of_any_magnitude(bec, dtype, kind, D, q, k, v):
     lens = [300, 40]
     pool = made(bec, lens, 2, D, dtype, 3, k=2.0 ** k, v=2.0 ** v)
